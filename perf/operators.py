@@ -347,13 +347,13 @@ def _own(s):
     case = s["case"]
     plan, gemm = _plan()
     if case["op"] == "product":
-        _done(plan.run_fp8(s["A"], s["SA"], s["B"], s["SB"], s["D"], act=gemm.GEMM_ACT_SILU if case["act"] == "silu" else gemm.GEMM_ACT_NONE))
+        _done(plan.run_scaled(s["A"], s["SA"], s["B"], s["SB"], s["D"], act=gemm.GEMM_ACT_SILU if case["act"] == "silu" else gemm.GEMM_ACT_NONE))
         return s["D"]
     if case["op"] == "quantize":
-        _done(plan.quantize_fp8(s["X"], s["Q"], s["SQ"], s.get("QT"), s.get("SQT"), block_rows=case["rows"]))
+        _done(plan.quantize(s["X"], s["Q"], s["SQ"], s.get("QT"), s.get("SQT"), block_rows=case["rows"]))
         return {n: s[n] for n in ("Q", "SQ", "QT", "SQT") if n in s}
     if case["op"] == "experts":
-        call = plan.run_fp8_grouped if case["form"] == "rows" else plan.run_fp8_grouped_k
+        call = plan.run_grouped if case["form"] == "rows" else plan.run_grouped_k
         _done(call(s["A"], s["SA"], s["B"], s["SB"], s["D"], s["starts"], s["counts"]))
         return s["D"]
     if case["op"] == "route":
