@@ -368,7 +368,7 @@ def _own(s):
         return {n: s[n] for n in names}
     _done(plan.combine(s["Y"], s["pos"], s["weights"], s["out"]))
     if case["grad"]:
-        _done(plan.combine_backward(s["dout"], s["Y"], s["rowmap"], s["weights"], s["dY"], s["dweights"]))
+        _done(plan.combine_backward(s["dout"], s["Y"], s["pos"], s["weights"], s["dY"], s["dweights"], rowmap=s["rowmap"]))
     return {n: s[n] for n in ("out", "dY", "dweights") if n in s}
 
 
