@@ -36,8 +36,14 @@ SOURCES = [
     "gemm_tc_tf32_bn128.cu",
     "gemm_tc_tf32_bn256.cu",
     "noalloc.cu",
+    "ops.cpp",
+    "scaled_tile.cu",
+    "scaled_sliced.cu",
+    "quantize.cu",
+    "route.cu",
+    "combine.cu",
 ]
-HEADERS = ["ptx.cuh", "kernels.h", "gemm_tc.cuh"]
+HEADERS = ["ptx.cuh", "kernels.h", "plan.h", "gemm_tc.cuh", "scaled.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

@@ -1,0 +1,202 @@
+// combine.cu -- the experts' rows back into tokens, and its gradients:
+//
+//   out[t] = sum_j w[t,j] Y[pos[t,j]]
+//   dY[pos[t,j]] = w[t,j] dout[t]        dw[t,j] = <dout[t], Y[pos[t,j]]>
+//
+// Every row of Y belongs to one choice of one token, so the gradient of Y has one term
+// and needs no atomics.  What bounds both is memory: each row of Y is read once (and of dY
+// written once), each row of out or dout once.  16-byte loads, all k rows' of a piece in flight together.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "kernels.h"
+
+namespace dg {
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kPiece = 8;   // consecutive columns of a thread
+constexpr int kChoices = 8;  // choices of a token whose loads are in flight together
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else if constexpr (std::is_same<T, __half>::value) return __half2float(v);
+  else return __bfloat162float(v);
+}
+template <typename T>
+__device__ __forceinline__ T from_f(float v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else if constexpr (std::is_same<T, __half>::value) return __float2half_rn(v);
+  else return __float2bfloat16_rn(v);
+}
+
+template <typename T>
+struct alignas(16) Piece {
+  T v[kPiece];
+};
+
+// Columns [0, n) of a piece at p; whole pieces as 16-byte loads where rows allow it.
+template <typename T>
+__device__ __forceinline__ void load_piece(Piece<T>& o, const T* p, int n, bool vec) {
+  if (vec && n == kPiece) {
+    o = *reinterpret_cast<const Piece<T>*>(p);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kPiece; ++i) o.v[i] = i < n ? p[i] : from_f<T>(0.f);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_piece(const Piece<T>& o, T* p, int n, bool vec) {
+  if (vec && n == kPiece) {
+    *reinterpret_cast<Piece<T>*>(p) = o;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kPiece; ++i)
+    if (i < n) p[i] = o.v[i];
+}
+
+__device__ __forceinline__ int row_of(const CombineArgs& a, int64_t slot) {
+  if (!DG_IN(a.dbg, a.pos + slot, 4, DBG_COMBINE)) return -1;
+  const int r = __ldg(a.pos + slot);
+  return r < a.rows ? r : -1;  // negative: the choice has no row
+}
+
+// One thread a piece of a token's row.
+template <typename TY, typename TO>
+__global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
+  wait_prior_grid();
+  const int t = int(blockIdx.x), col = int(blockIdx.y * blockDim.x + threadIdx.x) * kPiece;
+  if (col >= a.cols) return;
+  const int n = min(kPiece, a.cols - col);
+  const TY* const y = static_cast<const TY*>(a.y) + col;
+  float sum[kPiece];
+#pragma unroll
+  for (int i = 0; i < kPiece; ++i) sum[i] = 0.f;
+  for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+    Piece<TY> p[kChoices];
+    float w[kChoices];
+#pragma unroll
+    for (int j = 0; j < kChoices; ++j) {
+      const int64_t slot = int64_t(t) * a.k + j0 + j;
+      const int r = j0 + j < a.k ? row_of(a, slot) : -1;
+      const TY* const src = y + int64_t(max(r, 0)) * a.ldy;
+      w[j] = r >= 0 && DG_IN(a.dbg, a.weights + slot, 4, DBG_COMBINE) ? __ldg(a.weights + slot) : 0.f;
+      load_piece(p[j], src, r >= 0 && DG_IN(a.dbg, src, n * int(sizeof(TY)), DBG_COMBINE) ? n : 0, a.vec);
+    }
+#pragma unroll
+    for (int j = 0; j < kChoices; ++j)
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) sum[i] = fmaf(w[j], to_f(p[j].v[i]), sum[i]);
+  }
+  Piece<TO> o;
+#pragma unroll
+  for (int i = 0; i < kPiece; ++i) o.v[i] = from_f<TO>(sum[i]);
+  TO* const dst = static_cast<TO*>(a.out) + int64_t(t) * a.ldo + col;
+  if (DG_IN(a.dbg, dst, n * int(sizeof(TO)), DBG_COMBINE)) store_piece(o, dst, n, a.vec);
+}
+
+// Gradients: one warp a token (dout read once, its choices' rows side by side);
+// the warps after the tokens' clear the rows that hold no slot.
+template <typename TY, typename TO>
+__global__ void __launch_bounds__(256) combine_backward_kernel(const CombineArgs a) {
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  if (warp >= a.tokens) {
+    const int64_t r = warp - a.tokens;
+    if (!a.rowmap || r >= a.rows || !DG_IN(a.dbg, a.rowmap + r, 4, DBG_COMBINE) || __ldg(a.rowmap + r) >= 0) return;
+    Piece<TY> zero;
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) zero.v[i] = from_f<TY>(0.f);
+    TY* const dst = static_cast<TY*>(a.dy) + r * a.lddy;
+    for (int col = lane * kPiece; col < a.cols; col += 32 * kPiece) {
+      const int n = min(kPiece, a.cols - col);
+      if (DG_IN(a.dbg, dst + col, n * int(sizeof(TY)), DBG_COMBINE)) store_piece(zero, dst + col, n, a.vec);
+    }
+    return;
+  }
+  const TO* const dout = static_cast<const TO*>(a.out) + warp * a.ldo;
+  for (int j0 = 0; j0 < a.k; j0 += kChoices) {
+    int row[kChoices];
+    float w[kChoices], dot[kChoices];
+#pragma unroll
+    for (int j = 0; j < kChoices; ++j) {
+      const int64_t slot = warp * a.k + j0 + j;
+      row[j] = j0 + j < a.k ? row_of(a, slot) : -1;
+      w[j] = row[j] >= 0 && DG_IN(a.dbg, a.weights + slot, 4, DBG_COMBINE) ? __ldg(a.weights + slot) : 0.f;
+      dot[j] = 0.f;
+    }
+    for (int col = lane * kPiece; col < a.cols; col += 32 * kPiece) {
+      const int n = min(kPiece, a.cols - col);
+      Piece<TO> g;
+      load_piece(g, dout + col, DG_IN(a.dbg, dout + col, n * int(sizeof(TO)), DBG_COMBINE) ? n : 0, a.vec);
+      Piece<TY> y[kChoices];
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j) {
+        const TY* const src = static_cast<const TY*>(a.y) + int64_t(max(row[j], 0)) * a.ldy + col;
+        load_piece(y[j], src, row[j] >= 0 && DG_IN(a.dbg, src, n * int(sizeof(TY)), DBG_COMBINE) ? n : 0, a.vec);
+      }
+#pragma unroll
+      for (int j = 0; j < kChoices; ++j) {
+        if (row[j] < 0) continue;
+        Piece<TY> d;
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) {
+          const float f = to_f(g.v[i]);
+          dot[j] = fmaf(f, to_f(y[j].v[i]), dot[j]);
+          d.v[i] = from_f<TY>(w[j] * f);
+        }
+        TY* const dst = static_cast<TY*>(a.dy) + int64_t(row[j]) * a.lddy + col;
+        if (DG_IN(a.dbg, dst, n * int(sizeof(TY)), DBG_COMBINE)) store_piece(d, dst, n, a.vec);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kChoices; ++j) {
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) dot[j] += __shfl_xor_sync(kAll, dot[j], s);
+      const int64_t slot = warp * a.k + j0 + j;
+      if (lane == 0 && j0 + j < a.k && DG_IN(a.dbg, a.dweights + slot, 4, DBG_COMBINE)) a.dweights[slot] = dot[j];
+    }
+  }
+}
+
+template <typename TY, typename TO>
+cudaError_t launch(const CombineArgs& a, bool backward, cudaStream_t s) {
+  if (backward) {
+    const int64_t warps = int64_t(a.tokens) + (a.rowmap ? a.rows : 0);
+    return launch_k(combine_backward_kernel<TY, TO>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0, s, a.pdl, a);
+  }
+  const int pieces = (a.cols + kPiece - 1) / kPiece;
+  const int threads = pieces >= 256 ? 256 : (pieces + 31) / 32 * 32;
+  return launch_k(combine_kernel<TY, TO>, dim3(unsigned(a.tokens), unsigned((pieces + threads - 1) / threads)),
+                  dim3(unsigned(threads)), 0, s, a.pdl, a);
+}
+
+template <typename TY>
+cudaError_t launch_y(const CombineArgs& a, bool backward, cudaStream_t s) {
+  switch (a.o_kind) {
+    case OUT_F32: return launch<TY, float>(a, backward, s);
+    case OUT_BF16: return launch<TY, __nv_bfloat16>(a, backward, s);
+    default: return launch<TY, __half>(a, backward, s);
+  }
+}
+
+cudaError_t launch_any(const CombineArgs& a, bool backward, cudaStream_t s) {
+  switch (a.y_kind) {
+    case OUT_F32: return launch_y<float>(a, backward, s);
+    case OUT_BF16: return launch_y<__nv_bfloat16>(a, backward, s);
+    default: return launch_y<__half>(a, backward, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t s) { return launch_any(a, false, s); }
+cudaError_t launch_combine_backward(const CombineArgs& a, cudaStream_t s) { return launch_any(a, true, s); }
+
+}  // namespace dg

@@ -34,11 +34,15 @@ enum DbgSite : int {
   DBG_REDUCE = 4,     // tile reduction kernel
   DBG_GEMV = 5,       // GEMV kernels: matrix, vector, output, partials, counters
   DBG_SCALE = 6,      // the K == 0 / alpha == 0 kernel
-  DBG_TRANSPOSE = 7   // the TF32 operand transpose
+  DBG_TRANSPOSE = 7,  // the TF32 operand transpose
+  DBG_SCALED = 8,     // 8-bit products: plain loads and stores of D
+  DBG_QUANTIZE = 9,   // the quantiser
+  DBG_ROUTE = 10,     // routing, its map and its gradient
+  DBG_COMBINE = 11    // the weighted sum of rows and its gradients
 };
 constexpr int DBG_SITE_SHIFT = 16;
 constexpr int DBG_FLAG = 1 << 30;
-constexpr int kDbgSpans = 6;
+constexpr int kDbgSpans = 8;
 struct DbgSpans {
   uint64_t lo[kDbgSpans], hi[kDbgSpans];  // [lo, hi) byte ranges; unused entries have lo == hi
   int* err;                               // the plan's error word
@@ -60,7 +64,8 @@ enum WaitCode : int {
   WAIT_SELFTEST = 64,
   WAIT_EPI_EXCHANGE = 128,  // K pair: the peer CTA's partial sums or its free buffers
   WAIT_SPLIT_PEERS = 256,   // split-K reduced in the GEMM kernel: the tile's other K slices
-  WAIT_SPLIT_LOAD = 512     // ... or the bulk loads of the published slices
+  WAIT_SPLIT_LOAD = 512,    // ... or the bulk loads of the published slices
+  WAIT_SLICES = 1024        // 8-bit products: the partial sums of a tile's other K slices
 };
 
 // Variants of the tensor-core kernel.
@@ -302,5 +307,161 @@ cudaError_t launch_gemv_generic(const GemvArgs& g, cudaStream_t s, int sms, int*
 
 // One CTA waits on a barrier that nothing arrives on; gives up after timeout_ns.
 cudaError_t launch_watchdog_selftest(int* err, uint64_t timeout_ns, cudaStream_t s);
+
+// ------------------------------------------------ 8-bit block-scaled products
+
+// How the rows of a product are grouped.
+enum ScGroup : int {
+  SC_DENSE = 0,  // one product
+  SC_ROWS = 1,   // group e: rows starts[e] .. starts[e] + counts[e] of A and D, its own B
+  SC_K = 2       // group e: those columns (along K) of A and B, its own D
+};
+
+constexpr int SC_BK = 128;           // K values per ring stage: one 128-byte swizzle row, one scale
+constexpr int SC_MAX_GROUPS = 1024;  // groups whose tile counts fit the kernels' table
+
+struct ScParams {
+  int M, N;        // rows of A and of B (of one group's B)
+  int group;       // ScGroup
+  int groups;
+  const int* starts;  // device: multiples of 128
+  const int* counts;
+  int cap;            // rows (SC_ROWS: of A and D) or K values (SC_K) that starts / counts may reach
+  int m_blocks, n_blocks;  // tiles (SC_ROWS: m_blocks is per group, in the kernel)
+  int k_blocks;       // of one product (SC_K: of cap)
+  int raster;         // output-tile rows per rasterisation group
+  int units;          // tiles (SC_ROWS: counted in the kernel)
+  // 512-byte scale tiles (128 rows x 4 k-blocks): tile of row block r, k-blocks
+  // 4g .. 4g+3 is number r * sa_cols + g; group e's B scales start at e * sb_group
+  int sa_cols, sb_cols, sb_group;
+  int out_kind;
+  int n_tma;          // columns [0, n_tma) of D go through TMA (a 16-byte multiple per row)
+  void* d;
+  int64_t ldd, d_group;  // elements between rows, between groups' D (SC_K)
+  float alpha, beta, slope;
+  int act;
+  uint32_t idesc;     // tcgen05 instruction descriptor, scale ids zero
+  int bn;             // sliced kernel: rows of A per tile at most (32, 64, 96 or 128; a call with several tiles of rows: 128)
+  int stages;         // sliced kernel: ring depth
+  int slices;         // sliced kernel: CTAs of a cluster, each with kb_per_slice k-blocks of the tile
+  int kb_per_slice;
+  int* err;
+  uint64_t timeout_ns;
+  int pdl;
+  DG_DEBUG_FIELD
+};
+
+struct ScMaps {
+  CUtensorMap a, b, d, sa, sb;
+};
+
+// Tile kernel: `pair` = 256 x 256 tiles on a cluster of two CTAs, else 128 x 128
+// tiles; maps: a (box 128 values x 128 rows), b (box 128 values x 128 rows),
+// d (box 128 bytes x 32 rows), sa and sb (box one scale tile).
+cudaError_t launch_scaled_tile(bool pair, const ScMaps& m, const ScParams& p, int grid, cudaStream_t s);
+int scaled_tile_clusters();  // pairs that can be resident at once
+int scaled_tile_stages(bool pair);
+// Sliced kernel: tiles of 128 rows of B x bn rows of A; maps: a (box 128 values x
+// 32 rows), b (box 128 values x 128 rows).  idesc: N zero.
+cudaError_t launch_scaled_sliced(const ScMaps& m, const ScParams& p, int grid, cudaStream_t s);
+int scaled_sliced_smem(int bn, int stages);
+
+// Rows of `cols` bytes (groups x rows of them, `ld` bytes apart, groups `group` bytes apart) copied
+// to rows of `ld_out` bytes, a multiple of 16: makes a code matrix whose rows the TMA cannot address one
+// that it can.  With counts, groups that have none are left out.
+struct RepackArgs {
+  const uint8_t* in;
+  int64_t ld, group;
+  int cols, rows, groups;
+  const int* counts;
+  uint8_t* out;
+  int64_t ld_out;
+  int pdl;
+  DG_DEBUG_FIELD
+};
+cudaError_t launch_repack(const RepackArgs& a, cudaStream_t s);
+
+// --------------------------------------------------------------- quantiser
+
+struct QuantArgs {
+  const void* x;
+  int64_t ldx;
+  int x_kind;  // OutKind of X
+  int rows, cols;  // of the result; row r is row rowmap[r] / map_div of X (no map: row r)
+  int rows_padded, cols_padded;  // to whole scale tiles (multiples of 128)
+  const int* rowmap;  // a negative entry, or one past src_rows: no row
+  int map_div, src_rows;
+  int block_rows;  // 1 or 128
+  int e5m2;
+  int vec;         // rows of X allow four values a load
+  uint8_t *q, *sq, *qt, *sqt;  // q / sq or qt / sqt may be null
+  int64_t ldq, ldqt;
+  int q_groups, qt_groups;  // groups of four blocks along the rows of q / of qt
+  int pdl;
+  DG_DEBUG_FIELD
+};
+cudaError_t launch_quantize(const QuantArgs& a, cudaStream_t s);
+
+// ----------------------------------------------------------------- routing
+
+struct RouteArgs {
+  int tokens, experts;
+  const void* logits;
+  int64_t ldl;
+  int kind;  // OutKind of the logits
+  const float* bias;
+  int sigmoid, top_k, groups, top_groups, group_top, renormalize;
+  float scale;
+  float* weights;    // tokens x top_k
+  int* indices;      // tokens x top_k
+  // gradient
+  const float* dweights;
+  void* dlogits;
+  int64_t lddl;
+  int pdl;
+  DG_DEBUG_FIELD
+};
+constexpr int ROUTE_MAX_EXPERTS = 1024;
+constexpr int ROUTE_MAX_K = 32;
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
+cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t s);
+
+struct RouteMapArgs {
+  const int* indices;
+  int slots;  // tokens x top_k
+  int experts;
+  int* starts;
+  int* counts;
+  int* pos;
+  int* rowmap;
+  int rows;  // length of rowmap
+  int pdl;
+  DG_DEBUG_FIELD
+};
+cudaError_t launch_route_map(const RouteMapArgs& a, cudaStream_t s);
+
+// ----------------------------------------------------------------- combine
+
+struct CombineArgs {
+  int tokens, k, cols, rows;  // rows of Y
+  const void* y;
+  int64_t ldy;
+  int y_kind;
+  const int* pos;
+  const float* weights;
+  void* out;  // forward: sums; backward: their gradient (read)
+  int64_t ldo;
+  int o_kind;
+  // backward
+  const int* rowmap;
+  void* dy;
+  int64_t lddy;
+  float* dweights;
+  int vec;  // every row allows eight values a load
+  int pdl;
+  DG_DEBUG_FIELD
+};
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t s);
+cudaError_t launch_combine_backward(const CombineArgs& a, cudaStream_t s);
 
 }  // namespace dg

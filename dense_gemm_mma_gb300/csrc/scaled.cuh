@@ -1,0 +1,171 @@
+// scaled.cuh -- what the two 8-bit block-scaled product kernels share.
+//
+// D[m, n] = act(alpha * sum_k a[m,k] b[n,k] 2^(ea[m,k/128] + eb[n,k/128]) + beta * D[m, n])
+//
+// a and b are E4M3 or E5M2, K contiguous; ea and eb are power-of-two scales, one
+// E8M0 byte for each row and block of 128 along K.  The tensor core applies them:
+// tcgen05.mma.kind::mxf8f6f4 multiplies each 32 products of a row pair by two E8M0
+// scales before they enter the fp32 accumulator in tensor memory, so a block of 128
+// is four MMAs (K = 32) that name the same scale byte, and no partial sum ever leaves
+// the accumulator to be scaled.  A power-of-two scale costs nothing in precision: it
+// moves the block's exponents and leaves its fractions alone.
+//
+// The scales come as 512-byte tiles (128 rows x 4 blocks; include/gemm.h), which is
+// the image tcgen05.cp lays into tensor memory: one copy per 128 rows serves four
+// k-blocks, whose MMAs pick byte (k-block mod 4) of each 32-bit word.
+#pragma once
+
+#include <atomic>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace dg {
+
+__device__ __forceinline__ uint32_t sc_pack2(float a, float b, int kind) {
+  if (kind == OUT_BF16) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float sc_load1(const void* p, int kind) {
+  if (kind == OUT_F32) return *static_cast<const float*>(p);
+  if (kind == OUT_BF16) return __bfloat162float(*static_cast<const __nv_bfloat16*>(p));
+  return __half2float(*static_cast<const __half*>(p));
+}
+
+__device__ __forceinline__ void sc_store1(void* p, float v, int kind) {
+  if (kind == OUT_F32)
+    *static_cast<float*>(p) = v;
+  else if (kind == OUT_BF16)
+    *static_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(v);
+  else
+    *static_cast<__half*>(p) = __float2half_rn(v);
+}
+
+// One output tile of a call.
+struct ScUnit {
+  int row0, row_end;  // first row of A (and D) of the tile; end of the rows that exist
+  int n0;             // first column
+  int zb, zd;         // group whose B / D this is
+  int kb0, kb1;       // k-blocks
+};
+
+// A group's rows (or K values) as the kernels take them: a start that is no
+// multiple of 128 or lies outside [0, cap) means an empty group, a count that
+// reaches past cap is cut there, so that no device value leads out of a buffer.
+__device__ __forceinline__ void sc_segment(const ScParams& p, int e, int* start, int* count) {
+  const int s = __ldg(p.starts + e), c = __ldg(p.counts + e);
+  const bool ok = s >= 0 && s < p.cap && (s & 127) == 0 && c > 0;
+  *start = ok ? s : 0;
+  *count = ok ? min(c, p.cap - s) : 0;
+}
+
+// SC_ROWS: table[e] = tiles of the groups before e, table[groups] = all tiles.
+// Executed by one warp.
+__device__ __forceinline__ void sc_tile_table(const ScParams& p, int tile_rows, int* table) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int e0 = 0; e0 < p.groups; e0 += 32) {
+    const int e = e0 + lane;
+    int tiles = 0;
+    if (e < p.groups) {
+      int start, count;
+      sc_segment(p, e, &start, &count);
+      tiles = (count + tile_rows - 1) / tile_rows * p.n_blocks;
+    }
+    int sum = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    if (e < p.groups) table[e] = carry + sum - tiles;
+    carry += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (lane == 0) table[p.groups] = carry;
+}
+
+// Unit u -> tile.  `cursor` (SC_ROWS) is the group of the caller's last unit:
+// units are visited in ascending order, so the search for u's group goes on there.
+__device__ __forceinline__ ScUnit sc_unit(const ScParams& p, int u, int tile_rows, int tile_cols, const int* table,
+                                          int* cursor) {
+  ScUnit x;
+  int mb, nb;
+  x.zb = x.zd = 0;
+  x.kb0 = 0;
+  x.kb1 = p.k_blocks;
+  if (p.group == SC_ROWS) {
+    int e = *cursor;
+    while (e + 1 < p.groups && u >= table[e + 1]) ++e;
+    *cursor = e;
+    int start, count;
+    sc_segment(p, e, &start, &count);
+    tile_coords(u - table[e], (count + tile_rows - 1) / tile_rows, p.n_blocks, p.raster, &mb, &nb);
+    x.row0 = start + mb * tile_rows;
+    x.row_end = start + count;
+    x.zb = e;
+  } else {
+    int t = u;
+    if (p.group == SC_K) {
+      const int per = p.m_blocks * p.n_blocks;
+      const int e = u / per;
+      t = u - e * per;
+      int start, count;
+      sc_segment(p, e, &start, &count);
+      x.kb0 = start / SC_BK;
+      x.kb1 = (start + count + SC_BK - 1) / SC_BK;
+      x.zd = e;
+    }
+    tile_coords(t, p.m_blocks, p.n_blocks, p.raster, &mb, &nb);
+    x.row0 = mb * tile_rows;
+    x.row_end = p.M;
+  }
+  x.n0 = nb * tile_cols;
+  return x;
+}
+
+// The MMA warp's cursor through the sets of scale columns in tensor memory.  Set
+// g mod 4 holds the scales of the g-th copied group of k-blocks (`it` counts this
+// CTA's k-blocks from 0).  The MMAs of group g - 4 must have completed before their
+// set is written again.  Full barrier `it` already says that k-blocks up to it -
+// stages have: only short groups (a K range that starts or ends inside a group of
+// four) leave anything to wait for, on the empty barrier of that group's last stage.
+struct ScSets {
+  int s1 = -1000000, s2 = -1000000, s3 = -1000000;  // first k-blocks of the last three groups
+  uint32_t next = 0;
+  // Last k-block that used the set about to be written (group g - 4: group g - 3 starts after it).
+  __device__ __forceinline__ int last_user() const { return s3 - 1; }
+  __device__ __forceinline__ uint32_t take(int it) {
+    s3 = s2;
+    s2 = s1;
+    s1 = it;
+    return (next++) & 3u;
+  }
+};
+
+// v <- act(v), every run-time choice outside the unrolled loops.
+template <int N>
+__device__ __forceinline__ void sc_act(float (&v)[N], int act, float slope) {
+  if (act == 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? v[i] * slope : v[i];
+  } else if (act == 2) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
+  } else if (act == 3) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = apply_act(v[i], 3, 0.f);
+  } else if (act == 4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = apply_act(v[i], 4, 0.f);
+  }
+}
+
+}  // namespace dg

@@ -28,15 +28,18 @@ GEMM_ERR_DEBUG_CHECK = 8
 # bits of the plan's error word (gemm_plan_last_error_bits)
 DBG_FLAG = 1 << 30
 DBG_SITES = {0: "tma", 1: "epilogue_store", 2: "epilogue_load", 3: "split_in_kernel", 4: "tile_reduce",
-             5: "gemv", 6: "scale", 7: "transpose"}
+             5: "gemv", 6: "scale", 7: "transpose", 8: "scaled", 9: "quantize", 10: "route", 11: "combine"}
 
 GEMM_OP_N, GEMM_OP_T = 0, 1
 GEMM_TYPE_BF16, GEMM_TYPE_F16, GEMM_TYPE_F32, GEMM_TYPE_TF32 = 0, 1, 2, 3
+GEMM_TYPE_E4M3, GEMM_TYPE_E5M2 = 4, 5
+GEMM_SCORE_SOFTMAX, GEMM_SCORE_SIGMOID = 0, 1
 GEMM_BF16_F32, GEMM_BF16_BF16, GEMM_F16_F32, GEMM_F16_F16, GEMM_TF32_F32 = 0, 1, 2, 3, 4
 GEMM_ACT_NONE, GEMM_ACT_LEAKY_RELU, GEMM_ACT_RELU, GEMM_ACT_GELU, GEMM_ACT_SILU = 0, 1, 2, 3, 4
 
 PATH_NAMES = {0: "none", 1: "tc", 2: "tc_splitk", 3: "gemv_rowdot", 4: "gemv_colstream",
-              5: "gemv_generic", 6: "scale", 7: "tc_splitk_cluster", 8: "tc_tail_split"}
+              5: "gemv_generic", 6: "scale", 7: "tc_splitk_cluster", 8: "tc_tail_split",
+              9: "scaled", 10: "scaled_sliced"}
 
 DTYPES = {("bf16", "f32"): GEMM_BF16_F32, ("bf16", "bf16"): GEMM_BF16_BF16,
           ("f16", "f32"): GEMM_F16_F32, ("f16", "f16"): GEMM_F16_F16, ("tf32", "f32"): GEMM_TF32_F32}
@@ -44,6 +47,12 @@ DTYPES = {("bf16", "f32"): GEMM_BF16_F32, ("bf16", "bf16"): GEMM_BF16_BF16,
 
 class gemm_epilogue_t(ctypes.Structure):
     _fields_ = [("act", ctypes.c_int32), ("slope", ctypes.c_float)]
+
+
+class gemm_route_t(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("top_k", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class gemm_config_info_t(ctypes.Structure):
@@ -99,6 +108,24 @@ _SIGNATURES = {
     "gemm_plan_tuned_count": (_I32, [_VP, ctypes.POINTER(_I64)]),
     "gemm_plan_last_error_bits": (_I32, [_VP, ctypes.POINTER(_I64)]),
     "gemm_debug_build": (ctypes.c_int, []),
+    "gemm_scale_bytes": (_I64, [_I64, _I64]),
+    "gemm_quantize": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _I64, _I64, _I32, _I32, _VP, _I64, _VP, _VP,
+                             _I64, _VP, _VP]),
+    "gemm_run_scaled": (_I32, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, _I32, _VP, _I64, _VP, _I32, _VP, _I64, _I32,
+                               _F, _F, gemm_epilogue_t, _VP]),
+    "gemm_check_scaled": (_I32, [_I64, _I64, _I64, _VP, _I64, _VP, _I32, _VP, _I64, _VP, _I32, _VP, _I64, _I32,
+                                 _F, _F, gemm_epilogue_t]),
+    "gemm_run_grouped": (_I32, [_VP, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _I64, _VP, _I32, _VP, _I64, _I64, _VP,
+                                _I32, _VP, _I64, _I32, _F, _F, gemm_epilogue_t, _VP]),
+    "gemm_run_grouped_k": (_I32, [_VP, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _I64, _VP, _I32, _VP, _I64, _VP, _I32,
+                                  _VP, _I64, _I64, _I32, _F, _F, gemm_epilogue_t, _VP]),
+    "gemm_route": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, gemm_route_t, _VP, _VP, _VP]),
+    "gemm_route_backward": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, gemm_route_t, _VP, _VP, _VP, _I64, _VP]),
+    "gemm_route_rows": (_I64, [_I64, _I64, _I64]),
+    "gemm_route_map": (_I32, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _I64, _VP]),
+    "gemm_combine": (_I32, [_VP, _I64, _I64, _I64, _I64, _VP, _I64, _I32, _VP, _VP, _VP, _I64, _I32, _VP]),
+    "gemm_combine_backward": (_I32, [_VP, _I64, _I64, _I64, _I64, _VP, _I64, _I32, _VP, _I64, _I32, _VP, _VP, _VP,
+                                     _VP, _I64, _VP, _VP]),
 }
 
 
@@ -237,7 +264,132 @@ def gemm_plan_tuned_count(plan) -> int:
     return n.value
 
 
+def gemm_scale_bytes(rows, cols) -> int:
+    return load().gemm_scale_bytes(rows, cols)
+
+
+def gemm_quantize(plan, rows, cols, X, ldx, x_type, rowmap, map_div, src_rows, q_type, block_rows, Q, ldq, SQ, QT,
+                  ldqt, SQT, stream=None) -> int:
+    return load().gemm_quantize(plan, rows, cols, X, ldx, x_type, rowmap, map_div, src_rows, q_type, block_rows, Q,
+                                ldq, SQ, QT, ldqt, SQT, stream)
+
+
+def gemm_run_scaled(plan, M, N, K, A, lda, SA, a_type, B, ldb, SB, b_type, D, ldd, d_type, alpha, beta,
+                    act=GEMM_ACT_NONE, slope=0.0, stream=None) -> int:
+    return load().gemm_run_scaled(plan, M, N, K, A, lda, SA, a_type, B, ldb, SB, b_type, D, ldd, d_type, alpha, beta,
+                                  gemm_epilogue_t(act, slope), stream)
+
+
+def gemm_check_scaled(M, N, K, A, lda, SA, a_type, B, ldb, SB, b_type, D, ldd, d_type, alpha, beta,
+                      act=GEMM_ACT_NONE, slope=0.0) -> int:
+    return load().gemm_check_scaled(M, N, K, A, lda, SA, a_type, B, ldb, SB, b_type, D, ldd, d_type, alpha, beta,
+                                    gemm_epilogue_t(act, slope))
+
+
+def gemm_run_grouped(plan, groups, rows, N, K, starts, counts, A, lda, SA, a_type, B, ldb, b_group, SB, b_type, D,
+                     ldd, d_type, alpha, beta, act=GEMM_ACT_NONE, slope=0.0, stream=None) -> int:
+    return load().gemm_run_grouped(plan, groups, rows, N, K, starts, counts, A, lda, SA, a_type, B, ldb, b_group, SB,
+                                   b_type, D, ldd, d_type, alpha, beta, gemm_epilogue_t(act, slope), stream)
+
+
+def gemm_run_grouped_k(plan, groups, M, N, rows, starts, counts, A, lda, SA, a_type, B, ldb, SB, b_type, D, ldd,
+                       d_group, d_type, alpha, beta, act=GEMM_ACT_NONE, slope=0.0, stream=None) -> int:
+    return load().gemm_run_grouped_k(plan, groups, M, N, rows, starts, counts, A, lda, SA, a_type, B, ldb, SB, b_type,
+                                     D, ldd, d_group, d_type, alpha, beta, gemm_epilogue_t(act, slope), stream)
+
+
+def gemm_route(plan, tokens, experts, logits, ldl, l_type, bias, route, weights, indices, stream=None) -> int:
+    return load().gemm_route(plan, tokens, experts, logits, ldl, l_type, bias, route, weights, indices, stream)
+
+
+def gemm_route_backward(plan, tokens, experts, logits, ldl, l_type, route, indices, dweights, dlogits, lddl,
+                        stream=None) -> int:
+    return load().gemm_route_backward(plan, tokens, experts, logits, ldl, l_type, route, indices, dweights, dlogits,
+                                      lddl, stream)
+
+
+def gemm_route_rows(tokens, top_k, experts) -> int:
+    return load().gemm_route_rows(tokens, top_k, experts)
+
+
+def gemm_route_map(plan, tokens, top_k, experts, indices, starts, counts, pos, rowmap, rows, stream=None) -> int:
+    return load().gemm_route_map(plan, tokens, top_k, experts, indices, starts, counts, pos, rowmap, rows, stream)
+
+
+def gemm_combine(plan, tokens, top_k, cols, rows, Y, ldy, y_type, pos, weights, out, ldo, out_type,
+                 stream=None) -> int:
+    return load().gemm_combine(plan, tokens, top_k, cols, rows, Y, ldy, y_type, pos, weights, out, ldo, out_type,
+                               stream)
+
+
+def gemm_combine_backward(plan, tokens, top_k, cols, rows, dout, ldo, out_type, Y, ldy, y_type, pos, weights, rowmap,
+                          dY, lddy, dweights, stream=None) -> int:
+    return load().gemm_combine_backward(plan, tokens, top_k, cols, rows, dout, ldo, out_type, Y, ldy, y_type, pos,
+                                        weights, rowmap, dY, lddy, dweights, stream)
+
+
 # ------------------------------------------------------------------ torch helpers
+
+_types: dict = {}
+
+
+def _type_of(t) -> int:
+    """gemm_type_t of a tensor."""
+    if not _types:
+        import torch
+        _types.update({torch.bfloat16: GEMM_TYPE_BF16, torch.float16: GEMM_TYPE_F16, torch.float32: GEMM_TYPE_F32,
+                       torch.float8_e4m3fn: GEMM_TYPE_E4M3, torch.float8_e5m2: GEMM_TYPE_E5M2})
+    try:
+        return _types[t.dtype]
+    except KeyError:
+        raise ValueError(f"no gemm_type_t for {t.dtype}") from None
+
+
+def _scales(t, rows: int, cols: int, groups: int = 1) -> int:
+    """Pointer of the packed scale bytes of `groups` rows x cols matrices."""
+    need = groups * gemm_scale_bytes(rows, cols)
+    if t.element_size() != 1 or not t.is_contiguous() or t.numel() < need:
+        raise ValueError(f"scales are {need} contiguous bytes")
+    return t.data_ptr()
+
+
+def _ints(t, n: int) -> int:
+    import torch
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"expected {n} contiguous int32")
+    return t.data_ptr()
+
+
+def _floats(t, n: int) -> int:
+    import torch
+    if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"expected {n} contiguous float32")
+    return t.data_ptr()
+
+
+def _matrices(t):
+    """(pointer, ld, elements between matrices) of a 3-D stack of matrices with contiguous rows."""
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError("expected a 3-D stack of matrices with contiguous rows")
+    ld = max(t.stride(1), t.shape[2], 1)
+    return t.data_ptr(), ld, max(t.stride(0), ld * t.shape[1])
+
+
+def pack_scales(scales):
+    """Packed scale bytes (include/gemm.h) of a rows x blocks uint8 tensor of E8M0 bytes,
+    e.g. a checkpoint's power-of-two scales.  A 128 x 128 block's scale is repeated in its 128 rows."""
+    import torch
+    rows, blocks = scales.shape
+    r, c = max(-(-rows // 128), 1) * 128, max(-(-blocks // 4), 1) * 4
+    full = torch.zeros((r, c), dtype=torch.uint8, device=scales.device)
+    full[:rows, :blocks] = scales
+    return full.view(r // 128, 4, 32, c // 4, 4).permute(0, 3, 2, 1, 4).reshape(-1)
+
+
+def unpack_scales(packed, rows: int, cols: int):
+    """The rows x ceil(cols / 128) scale bytes of a packed rows x cols matrix."""
+    r, c = max(-(-rows // 128), 1) * 128, max(-(-cols // 512), 1) * 4
+    return packed[:r * c].view(r // 128, c // 4, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(r, c)[:rows, :-(-cols // 128)]
 
 def _operand(t, trans: bool):
     """(pointer, ld) of a stored 2-D operand whose rows are contiguous."""
@@ -290,3 +442,143 @@ class Plan:
 
     def poll_error(self, stream=None) -> int:
         return gemm_plan_poll_error(self.handle, stream)
+
+    # ------------------------------------------- block-scaled 8-bit products
+
+    def _stream(self, t, stream):
+        if stream is not None:
+            return stream
+        import torch
+        return torch.cuda.current_stream(t.device).cuda_stream
+
+    def quantize(self, X, Q=None, SQ=None, QT=None, SQT=None, *, block_rows=1, rowmap=None, map_div=1,
+                 stream=None) -> int:
+        """X (rows x cols) -> 8-bit Q and scales SQ, and/or its transpose QT and scales SQT
+        (float8_e4m3fn or float8_e5m2; scales gemm_scale_bytes uint8).  With rowmap (int32) row r
+        of the result is X's row rowmap[r] // map_div (negative: none)."""
+        x, ldx = _operand(X, False)
+        src_rows, cols = X.shape
+        rows = src_rows if rowmap is None else rowmap.numel()
+        q = sq = qt = sqt = None
+        ldq = ldqt = 0
+        if Q is not None:
+            q, ldq = _operand(Q, False)
+            sq = _scales(SQ, rows, cols)
+            if Q.shape != (rows, cols):
+                raise ValueError("Q is rows x cols")
+        if QT is not None:
+            qt, ldqt = _operand(QT, False)
+            sqt = _scales(SQT, cols, rows)
+            if QT.shape != (cols, rows) or (Q is not None and Q.dtype != QT.dtype):
+                raise ValueError("QT is cols x rows, of Q's type")
+        kind = Q if Q is not None else QT
+        if kind is None:
+            raise ValueError("neither Q nor QT")
+        return gemm_quantize(self.handle, rows, cols, x, ldx, _type_of(X), None if rowmap is None else _ints(rowmap, rows),
+                             map_div, src_rows, _type_of(kind), block_rows, q, ldq, sq, qt, ldqt, sqt,
+                             self._stream(X, stream))
+
+    def run_scaled(self, A, SA, B, SB, D, *, alpha=1.0, beta=0.0, act=GEMM_ACT_NONE, slope=0.0, stream=None) -> int:
+        """D <- act(alpha * A @ B^T + beta * D) on 8-bit A (M x K), B (N x K) with packed scales SA, SB."""
+        a, lda = _operand(A, False)
+        b, ldb = _operand(B, False)
+        d, ldd = _operand(D, False)
+        M, K = A.shape
+        N = B.shape[0]
+        if B.shape[1] != K or D.shape != (M, N):
+            raise ValueError("A is M x K, B is N x K and D is M x N")
+        return gemm_run_scaled(self.handle, M, N, K, a, lda, _scales(SA, M, K), _type_of(A), b, ldb, _scales(SB, N, K),
+                               _type_of(B), d, ldd, _type_of(D), alpha, beta, act, slope, self._stream(D, stream))
+
+    def run_grouped(self, A, SA, B, SB, D, starts, counts, *, alpha=1.0, beta=0.0, act=GEMM_ACT_NONE, slope=0.0,
+                    stream=None) -> int:
+        """Rows starts[e] .. starts[e] + counts[e] of A (rows x K) times B[e]^T (B groups x N x K, SB
+        the groups' packed scales one after another) into the same rows of D (rows x N)."""
+        a, lda = _operand(A, False)
+        b, ldb, b_group = _matrices(B)
+        d, ldd = _operand(D, False)
+        rows, K = A.shape
+        groups, N = B.shape[:2]
+        if B.shape[2] != K or D.shape != (rows, N):
+            raise ValueError("A is rows x K, B is groups x N x K and D is rows x N")
+        return gemm_run_grouped(self.handle, groups, rows, N, K, _ints(starts, groups), _ints(counts, groups), a, lda,
+                                _scales(SA, rows, K), _type_of(A), b, ldb, b_group, _scales(SB, N, K, groups),
+                                _type_of(B), d, ldd, _type_of(D), alpha, beta, act, slope, self._stream(D, stream))
+
+    def run_grouped_k(self, A, SA, B, SB, D, starts, counts, *, alpha=1.0, beta=0.0, act=GEMM_ACT_NONE, slope=0.0,
+                      stream=None) -> int:
+        """D[e] <- act(alpha * A_e @ B_e^T + beta * D[e]), A_e and B_e columns starts[e] .. starts[e] + counts[e]
+        of A (M x rows) and B (N x rows); D groups x M x N."""
+        a, lda = _operand(A, False)
+        b, ldb = _operand(B, False)
+        d, ldd, d_group = _matrices(D)
+        M, rows = A.shape
+        N = B.shape[0]
+        groups = D.shape[0]
+        if B.shape[1] != rows or D.shape[1:] != (M, N):
+            raise ValueError("A is M x rows, B is N x rows and D is groups x M x N")
+        return gemm_run_grouped_k(self.handle, groups, M, N, rows, _ints(starts, groups), _ints(counts, groups), a, lda,
+                                  _scales(SA, M, rows), _type_of(A), b, ldb, _scales(SB, N, rows), _type_of(B), d, ldd,
+                                  d_group, _type_of(D), alpha, beta, act, slope, self._stream(D, stream))
+
+    # ----------------------------------------------------------- experts
+
+    def route(self, logits, weights, indices, *, bias=None, score=GEMM_SCORE_SOFTMAX, groups=1, top_groups=1,
+              group_top=1, renormalize=False, scale=1.0, stream=None) -> int:
+        """logits (tokens x experts) -> each token's chosen experts (indices, tokens x top_k int32)
+        and their weights (tokens x top_k float32)."""
+        x, ldl = _operand(logits, False)
+        tokens, experts = logits.shape
+        if weights.shape != indices.shape or weights.dim() != 2 or weights.shape[0] != tokens:
+            raise ValueError("weights and indices are tokens x top_k")
+        k = weights.shape[1]
+        return gemm_route(self.handle, tokens, experts, x, ldl, _type_of(logits),
+                          None if bias is None else _floats(bias, experts),
+                          gemm_route_t(score, k, groups, top_groups, group_top, int(renormalize), scale),
+                          _floats(weights, tokens * k), _ints(indices, tokens * k), self._stream(logits, stream))
+
+    def route_backward(self, logits, indices, dweights, dlogits, *, score=GEMM_SCORE_SOFTMAX, renormalize=False,
+                       scale=1.0, stream=None) -> int:
+        """The gradient of the logits (dlogits) from the weights' (dweights) and the choice (indices)."""
+        x, ldl = _operand(logits, False)
+        d, lddl = _operand(dlogits, False)
+        tokens, experts = logits.shape
+        if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or indices.shape != dweights.shape:
+            raise ValueError("dlogits is like logits, dweights like indices")
+        k = indices.shape[1]
+        return gemm_route_backward(self.handle, tokens, experts, x, ldl, _type_of(logits),
+                                   gemm_route_t(score, k, 1, 1, 1, int(renormalize), scale), _ints(indices, tokens * k),
+                                   _floats(dweights, tokens * k), d, lddl, self._stream(logits, stream))
+
+    def route_map(self, indices, experts, starts, counts, pos, rowmap, *, stream=None) -> int:
+        """The order of the slots of indices (tokens x top_k) by expert; rowmap has gemm_route_rows entries."""
+        tokens, k = indices.shape
+        return gemm_route_map(self.handle, tokens, k, experts, _ints(indices, tokens * k), _ints(starts, experts),
+                              _ints(counts, experts), _ints(pos, tokens * k), _ints(rowmap, 0), rowmap.numel(),
+                              self._stream(indices, stream))
+
+    def combine(self, Y, pos, weights, out, *, stream=None) -> int:
+        """out[t] <- sum_j weights[t, j] * Y[pos[t, j]]."""
+        y, ldy = _operand(Y, False)
+        o, ldo = _operand(out, False)
+        tokens, k = pos.shape
+        rows, cols = Y.shape
+        if out.shape != (tokens, cols):
+            raise ValueError("out is tokens x cols")
+        return gemm_combine(self.handle, tokens, k, cols, rows, y, ldy, _type_of(Y), _ints(pos, tokens * k),
+                            _floats(weights, tokens * k), o, ldo, _type_of(out), self._stream(out, stream))
+
+    def combine_backward(self, dout, Y, pos, weights, dY, dweights, *, rowmap=None, stream=None) -> int:
+        """dY[pos[t, j]] <- weights[t, j] * dout[t], dweights[t, j] <- <dout[t], Y[pos[t, j]]>; with rowmap the
+        rows of dY that hold no slot are cleared."""
+        y, ldy = _operand(Y, False)
+        g, ldo = _operand(dout, False)
+        d, lddy = _operand(dY, False)
+        tokens, k = pos.shape
+        rows, cols = Y.shape
+        if dout.shape != (tokens, cols) or dY.shape != Y.shape or dY.dtype != Y.dtype:
+            raise ValueError("dout is tokens x cols, dY like Y")
+        return gemm_combine_backward(self.handle, tokens, k, cols, rows, g, ldo, _type_of(dout), y, ldy, _type_of(Y),
+                                     _ints(pos, tokens * k), _floats(weights, tokens * k),
+                                     None if rowmap is None else _ints(rowmap, rows), d, lddy,
+                                     _floats(dweights, tokens * k), self._stream(Y, stream))

@@ -124,9 +124,12 @@ typedef enum {
   GEMM_PATH_TC_SPLITK_CLUSTER = 7, /* tcgen05 GEMM, K in two halves on a cluster of two CTAs
                                   whose partial sums are added on chip: one launch, no
                                   workspace (the reduction of section 2.3 done in place) */
-  GEMM_PATH_TC_TAIL_SPLIT = 8  /* tcgen05 GEMM: whole tiles for the full waves; only the
+  GEMM_PATH_TC_TAIL_SPLIT = 8, /* tcgen05 GEMM: whole tiles for the full waves; only the
                                   tiles of the last, partly filled wave are split along K
                                   (section 3.2's tail wave), + reduction of those tiles  */
+  GEMM_PATH_SCALED = 9,        /* 8-bit block-scaled product, whole output tiles         */
+  GEMM_PATH_SCALED_SLICED = 10 /* 8-bit block-scaled product with few rows or few tiles: */
+                               /* K slices on a cluster of CTAs, added on chip           */
 } gemm_path_t;
 
 /* Plan decisions and the tile/wave quantization they imply ("Matrix
@@ -230,7 +233,9 @@ const char* gemm_status_string(gemm_status_t status);
 
 /* Element types of gemm_run_ex's matrices. */
 typedef enum { GEMM_TYPE_BF16 = 0, GEMM_TYPE_F16 = 1, GEMM_TYPE_F32 = 2,
-               GEMM_TYPE_TF32 = 3 /* operands only (ab_type): fp32 words read as TF32 */ } gemm_type_t;
+               GEMM_TYPE_TF32 = 3, /* operands only (ab_type): fp32 words read as TF32 */
+               GEMM_TYPE_E4M3 = 4, /* 8-bit, 4 exponent and 3 fraction bits, no infinity, largest 448   */
+               GEMM_TYPE_E5M2 = 5  /* 8-bit, 5 and 2, largest 57344; both: block-scaled products only */ } gemm_type_t;
 
 /* D <- act(alpha * op(A) @ op(B) + beta * C) with a separate output D: the
  * gemm_run operation where the C that beta scales is read from one matrix and
@@ -277,7 +282,8 @@ gemm_status_t gemm_plan_poll_error(gemm_plan_t plan, void* stream);
  * starting at a negative coordinate), 1 an epilogue store, 2 an epilogue load
  * of the C that beta scales, 3 the in-kernel split-K reduction, 4 the tile
  * reduction kernel, 5 a GEMV kernel, 6 the K == 0 / alpha == 0 kernel, 7 the
- * TF32 operand transpose.  GEMM_ERR_INVALID_ARG on NULL. */
+ * TF32 operand transpose, 8 an 8-bit product's load or store of D, 9 the
+ * quantiser, 10 routing, 11 the weighted sum.  GEMM_ERR_INVALID_ARG on NULL. */
 gemm_status_t gemm_plan_last_error_bits(gemm_plan_t plan, int64_t* bits);
 
 /* 1 in the debug build of the library (libdgemm_gb300_debug.so, compiled
@@ -397,6 +403,175 @@ gemm_status_t gemm_gemv_noalloc(int64_t M, int64_t N, int64_t K,
                                 void* C, int64_t ldc, float alpha, float beta,
                                 gemm_dtype_t dtype, gemm_op_t transA, gemm_op_t transB,
                                 gemm_epilogue_t epilogue, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit products with a scale for each block of 128, and what goes round them:
+ * the quantiser, the experts' products, routing and the weighted sum.
+ *
+ * A block-scaled matrix of R rows and K columns is two buffers:
+ *   codes   R x K bytes, row-major, rows `ld` bytes apart: GEMM_TYPE_E4M3 or GEMM_TYPE_E5M2
+ *   scales  one E8M0 byte b (the scale 2^(b - 127)) for each row and block of 128
+ *           columns, packed: the matrix is cut into tiles of 128 rows and
+ *           four blocks (512 columns); tile (r / 128, k / 512) is 512 bytes at
+ *           512 * ((r / 128) * ceil(K / 512) + k / 512), and in it row r, block
+ *           c = k / 128 is byte (r % 32) * 16 + (r % 128) / 32 * 4 + c % 4.
+ *           gemm_scale_bytes(R, K) bytes in all; bytes of rows and blocks past the matrix
+ *           are 0 as gemm_quantize writes them and must not be 255 (255 is NaN).
+ * Element (r, k) stands for code * scale.  A 128 x 128 block's scale is the same
+ * byte in its 128 rows.
+ *
+ * The calls below are asynchronous on `stream` (a cudaStream_t), ordered like
+ * gemm_run's, may be captured into a CUDA graph and keep nothing
+ * between calls.  Row counts that depend on the data (counts, starts, pos, rowmap) are
+ * read on the device: no call waits for them.  Errors are those of gemm_run: argument
+ * problems come back before anything is launched.  Results are deterministic.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of the packed scales of a rows x cols matrix (a multiple of 512, at least 512);
+ * -1 if a size is negative or past 2^31 - 1. */
+int64_t gemm_scale_bytes(int64_t rows, int64_t cols);
+
+/* Quantise X (GEMM_TYPE_BF16, F16 or F32; row r of the result is row r of X, rows
+ * ldx elements apart) to codes and scales:
+ *   block_rows = 1    a scale for each row and block of 128 columns
+ *   block_rows = 128  a scale for each 128 x 128 block (weights)
+ *   Q, SQ    the matrix as it stands (rows x cols, ldq bytes between rows); both or neither
+ *   QT, SQT  the transposed matrix (cols x rows, ldqt), its blocks along rows: an operand
+ *            of a gradient product; both or neither, and one of the pairs at least
+ * A scale is the least power of two, 2^-127 at least, with which the block's largest
+ * finite magnitude stays within the type's largest value; a code is the value over
+ * the scale, rounded to nearest, ties to even.  Infinities and NaN become NaN codes and
+ * do not count for the scale.  A block of zeros has the scale byte 0.
+ * rowmap (device, `rows` int32; NULL: none): row r of the result is row rowmap[r] /
+ * map_div of X, which has src_rows rows; where rowmap[r] is negative or leads past
+ * X there is no row: the row of Q is left as it is, its scales are 0, and the column of
+ * QT is zero.  With gemm_route_map's rowmap and map_div = top_k this orders tokens by expert.
+ * Q, SQ, QT, SQT 16-byte aligned, ldq and ldqt multiples of 16, X and rowmap
+ * aligned to their elements; no result may share a byte with an input or another result.
+ * rows up to 8,388,096. */
+gemm_status_t gemm_quantize(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx,
+                            gemm_type_t x_type, const int32_t* rowmap, int64_t map_div, int64_t src_rows,
+                            gemm_type_t q_type, int32_t block_rows, void* Q, int64_t ldq, void* SQ, void* QT,
+                            int64_t ldqt, void* SQT, void* stream);
+
+/* D <- act(alpha * A @ B^T + beta * D) with block-scaled A (M x K, scales SA) and B
+ * (N x K, scales SB), D M x N of GEMM_TYPE_BF16, F16 or F32.  The tensor core applies
+ * the scales and accumulates in fp32; alpha, beta and act are applied in fp32 before the one
+ * rounding to D's type.  A and B may be of different 8-bit types.
+ *   forward            Y  = X  @ W^T      A = X  (tokens x in),   B = W   (out x in)
+ *   input gradient     dX = dY @ W        A = dY (tokens x out),  B = W^T (in x out)
+ *   weight gradient    dW = dY^T @ X      A = dY^T (out x tokens), B = X^T (in x tokens)
+ * (W^T, dY^T and X^T are gemm_quantize's QT.)
+ * M, N, K >= 0 and < 2^31; K == 0 gives D <- act(beta * D) without reading A or B; with
+ * beta == 0, D is not read.  SA, SB and D 16-byte aligned; lda and ldb >= K.  A
+ * matrix of codes that is 16-byte aligned with rows a multiple of 16 bytes apart is read where it is; another is copied
+ * into plan workspace first (a launch more and the matrix read and written once more; the workspace grows
+ * as gemm_run's does).  ldd elements between rows of D, a multiple of 16 bytes, >= N.  No byte of D may lie in A,
+ * B or their scales.  D's columns past N are not written.
+ * GEMM_SCALED_KERNEL=tile|pair|sliced and GEMM_SCALED_SLICES=n in the environment
+ * (read at every call) override the choice of kernel. */
+gemm_status_t gemm_run_scaled(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                              const void* SA, gemm_type_t a_type, const void* B, int64_t ldb, const void* SB,
+                              gemm_type_t b_type, void* D, int64_t ldd, gemm_type_t d_type, float alpha,
+                              float beta, gemm_epilogue_t epilogue, void* stream);
+
+/* The argument checks of gemm_run_scaled without a plan or a device. */
+gemm_status_t gemm_check_scaled(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA,
+                                gemm_type_t a_type, const void* B, int64_t ldb, const void* SB, gemm_type_t b_type,
+                                const void* D, int64_t ldd, gemm_type_t d_type, float alpha, float beta,
+                                gemm_epilogue_t epilogue);
+
+/* Experts' products: for each group e, rows starts[e] .. starts[e] + counts[e] of A
+ * (rows x K) times B_e^T (B_e N x K, b_group bytes after B_(e-1); its scales
+ * gemm_scale_bytes(N, K) after the last group's) into the same rows of D (rows x N), as
+ * gemm_run_scaled.  starts and counts (device, `groups` int32 each) are gemm_route_map's:
+ * starts are multiples of 128, so that a group's rows begin a scale tile.  A group whose start is no
+ * multiple of 128 or outside [0, rows) counts as empty, a count past the end of A is cut there.  Rows of D that are
+ * in no group are left as they are.  What A holds in rows between groups does not matter.
+ * groups <= 1024; B is read where it is if b_group is a multiple of 16 too, else the groups that have rows
+ * are copied. */
+gemm_status_t gemm_run_grouped(gemm_plan_t plan, int64_t groups, int64_t rows, int64_t N, int64_t K,
+                               const int32_t* starts, const int32_t* counts, const void* A, int64_t lda,
+                               const void* SA, gemm_type_t a_type, const void* B, int64_t ldb, int64_t b_group,
+                               const void* SB, gemm_type_t b_type, void* D, int64_t ldd, gemm_type_t d_type,
+                               float alpha, float beta, gemm_epilogue_t epilogue, void* stream);
+
+/* Experts' weight gradients: for each group e, columns starts[e] .. starts[e] + counts[e] of A
+ * (M x rows) times the same columns of B (N x rows), summed over them, into D_e
+ * (M x N, d_group elements after D_(e-1)): D_e <- act(alpha * A_e @ B_e^T + beta * D_e).
+ * A and B are gemm_quantize's QT of rows in gemm_route_map's order; the columns from a group's end to
+ * the next multiple of 128 are read and must be zero, as gemm_quantize leaves them.  An
+ * empty group gives D_e <- act(beta * D_e). */
+gemm_status_t gemm_run_grouped_k(gemm_plan_t plan, int64_t groups, int64_t M, int64_t N, int64_t rows,
+                                 const int32_t* starts, const int32_t* counts, const void* A, int64_t lda,
+                                 const void* SA, gemm_type_t a_type, const void* B, int64_t ldb, const void* SB,
+                                 gemm_type_t b_type, void* D, int64_t ldd, int64_t d_group, gemm_type_t d_type,
+                                 float alpha, float beta, gemm_epilogue_t epilogue, void* stream);
+
+typedef enum { GEMM_SCORE_SOFTMAX = 0, GEMM_SCORE_SIGMOID = 1 } gemm_score_t;
+
+/* How tokens choose experts. */
+typedef struct {
+  int32_t score;       /* gemm_score_t: softmax over all experts, or each expert's sigmoid      */
+  int32_t top_k;       /* experts a token goes to, 1 .. 32                                      */
+  int32_t groups;      /* equal groups of consecutive experts, 1 .. 32                          */
+  int32_t top_groups;  /* groups a token chooses from                                           */
+  int32_t group_top;   /* a group ranks by its best key (1) or its two best keys' sum (2)       */
+  int32_t renormalize; /* != 0: weights are scores over the sum of the chosen ones              */
+  float scale;         /* factor of the weights                                                 */
+} gemm_route_t;
+
+/* Route tokens: logits (tokens x experts, GEMM_TYPE_F32, BF16 or F16, rows ldl
+ * elements apart) -> the top_k experts of each token in descending order of their keys
+ * (indices) and their weights (both tokens x top_k, contiguous).
+ * Scores s are computed in fp32.  The key is s + bias (bias: device, `experts`
+ * floats, for balance: it takes part in the choice, not in the weights), or without a
+ * bias and with group_top = 1 the logit itself, whose order is the same.  Equal keys: the lowest index first, of
+ * groups too.  A logit of minus infinity or NaN masks its expert: its score is 0 and its
+ * key below every other of its group choice; where fewer than top_k experts are left, masked ones of
+ * the chosen groups follow in order of index, with weight 0.  Experts of other groups are never chosen.
+ * Renormalising a sum of 0 gives weights 0.
+ * experts <= 1024, a multiple of groups, and top_k <= experts of top_groups groups. */
+gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
+                         gemm_type_t l_type, const float* bias, gemm_route_t route, float* weights, int32_t* indices,
+                         void* stream);
+
+/* Gradient of gemm_route: dlogits (tokens x experts, of the logits' type, every entry written)
+ * from dweights (tokens x top_k) and the choice it made (indices; one outside [0,
+ * experts) takes no part).  The choice itself has no gradient.  Of `route`, score, top_k,
+ * renormalize and scale are used. */
+gemm_status_t gemm_route_backward(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
+                                  gemm_type_t l_type, gemm_route_t route, const int32_t* indices,
+                                  const float* dweights, void* dlogits, int64_t lddl, void* stream);
+
+/* Rows that gemm_route_map's order may take: tokens * top_k, and up to 127 empty rows for each expert
+ * that has one, rounded up to 128; -1 if a size is out of range. */
+int64_t gemm_route_rows(int64_t tokens, int64_t top_k, int64_t experts);
+
+/* The order of the slots (slot = token * top_k + choice) by expert: expert e's slots, in their
+ * own order, take rows starts[e] .. starts[e] + counts[e], starts[e] the next multiple of 128
+ * after the experts before.  pos[slot] is the slot's row (-1 where its index is outside [0, experts)),
+ * rowmap[row] the row's slot (-1: none), for `rows` rows, gemm_route_rows(...) at least. */
+gemm_status_t gemm_route_map(gemm_plan_t plan, int64_t tokens, int64_t top_k, int64_t experts, const int32_t* indices,
+                             int32_t* starts, int32_t* counts, int32_t* pos, int32_t* rowmap, int64_t rows,
+                             void* stream);
+
+/* out[t] <- sum over j of weights[t, j] * Y[pos[t, j]], in fp32 with one rounding: the experts' rows
+ * (Y rows x cols) back into tokens (out tokens x cols).  A pos that is negative or >= rows adds
+ * nothing.  Y and out are of any of GEMM_TYPE_F32, BF16, F16 and need only their element's alignment (rows
+ * on 16-byte boundaries are faster); out may not share a byte with Y. */
+gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top_k, int64_t cols, int64_t rows, const void* Y,
+                           int64_t ldy, gemm_type_t y_type, const int32_t* pos, const float* weights, void* out,
+                           int64_t ldo, gemm_type_t out_type, void* stream);
+
+/* Gradients of gemm_combine from dout (tokens x cols, out_type): dY[pos[t, j]] <-
+ * weights[t, j] * dout[t] (dY of Y's type) and dweights[t, j] <- <dout[t], Y[pos[t, j]]> (0
+ * where pos leads nowhere).  pos must name no row twice, as gemm_route_map's does not.  With rowmap (`rows`
+ * int32; NULL: none) the rows of dY that hold no slot are set to zero; other rows are left as they are. */
+gemm_status_t gemm_combine_backward(gemm_plan_t plan, int64_t tokens, int64_t top_k, int64_t cols, int64_t rows,
+                                    const void* dout, int64_t ldo, gemm_type_t out_type, const void* Y, int64_t ldy,
+                                    gemm_type_t y_type, const int32_t* pos, const float* weights,
+                                    const int32_t* rowmap, void* dY, int64_t lddy, float* dweights, void* stream);
 
 #ifdef __cplusplus
 }
