@@ -18,7 +18,6 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kPiece = 8;   // consecutive columns of a thread
-constexpr int kChoices = 8;  // choices of a token whose loads are in flight together
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v) {
@@ -38,26 +37,30 @@ struct alignas(16) Piece {
   T v[kPiece];
 };
 
-// Columns [0, n) of a piece at p; whole pieces as 16-byte loads where rows allow it.
-template <typename T>
-__device__ __forceinline__ void load_piece(Piece<T>& o, const T* p, int n, bool vec) {
-  if (vec && n == kPiece) {
-    o = *reinterpret_cast<const Piece<T>*>(p);
-    return;
-  }
+// Columns [0, n) of a piece, the rest zero.  VEC (rows on 16-byte boundaries, whole pieces):
+// one predicated load per 16 bytes, no branch, so that the pieces of all rows are in flight together.
+template <bool VEC, typename T>
+__device__ __forceinline__ void load_piece(Piece<T>& o, const T* p, int n) {
 #pragma unroll
-  for (int i = 0; i < kPiece; ++i) o.v[i] = i < n ? p[i] : from_f<T>(0.f);
+  for (int i = 0; i < kPiece; ++i) o.v[i] = from_f<T>(0.f);
+  if constexpr (VEC) {
+    if (n > 0) o = *reinterpret_cast<const Piece<T>*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i)
+      if (i < n) o.v[i] = p[i];
+  }
 }
 
-template <typename T>
-__device__ __forceinline__ void store_piece(const Piece<T>& o, T* p, int n, bool vec) {
-  if (vec && n == kPiece) {
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_piece(const Piece<T>& o, T* p, int n) {
+  if constexpr (VEC) {
     *reinterpret_cast<Piece<T>*>(p) = o;
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < kPiece; ++i)
-    if (i < n) p[i] = o.v[i];
+    for (int i = 0; i < kPiece; ++i)
+      if (i < n) p[i] = o.v[i];
+  }
 }
 
 __device__ __forceinline__ int row_of(const CombineArgs& a, int64_t slot) {
@@ -67,7 +70,7 @@ __device__ __forceinline__ int row_of(const CombineArgs& a, int64_t slot) {
 }
 
 // One thread a piece of a token's row.
-template <typename TY, typename TO>
+template <typename TY, typename TO, bool VEC, int KC>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
   wait_prior_grid();
   const int t = int(blockIdx.x), col = int(blockIdx.y * blockDim.x + threadIdx.x) * kPiece;
@@ -77,19 +80,19 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
   float sum[kPiece];
 #pragma unroll
   for (int i = 0; i < kPiece; ++i) sum[i] = 0.f;
-  for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-    Piece<TY> p[kChoices];
-    float w[kChoices];
+  for (int j0 = 0; j0 < a.k; j0 += KC) {
+    Piece<TY> p[KC];
+    float w[KC];
 #pragma unroll
-    for (int j = 0; j < kChoices; ++j) {
+    for (int j = 0; j < KC; ++j) {
       const int64_t slot = int64_t(t) * a.k + j0 + j;
       const int r = j0 + j < a.k ? row_of(a, slot) : -1;
       const TY* const src = y + int64_t(max(r, 0)) * a.ldy;
       w[j] = r >= 0 && DG_IN(a.dbg, a.weights + slot, 4, DBG_COMBINE) ? __ldg(a.weights + slot) : 0.f;
-      load_piece(p[j], src, r >= 0 && DG_IN(a.dbg, src, n * int(sizeof(TY)), DBG_COMBINE) ? n : 0, a.vec);
+      load_piece<VEC>(p[j], src, r >= 0 && DG_IN(a.dbg, src, n * int(sizeof(TY)), DBG_COMBINE) ? n : 0);
     }
 #pragma unroll
-    for (int j = 0; j < kChoices; ++j)
+    for (int j = 0; j < KC; ++j)
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) sum[i] = fmaf(w[j], to_f(p[j].v[i]), sum[i]);
   }
@@ -97,12 +100,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
 #pragma unroll
   for (int i = 0; i < kPiece; ++i) o.v[i] = from_f<TO>(sum[i]);
   TO* const dst = static_cast<TO*>(a.out) + int64_t(t) * a.ldo + col;
-  if (DG_IN(a.dbg, dst, n * int(sizeof(TO)), DBG_COMBINE)) store_piece(o, dst, n, a.vec);
+  if (DG_IN(a.dbg, dst, n * int(sizeof(TO)), DBG_COMBINE)) store_piece<VEC>(o, dst, n);
 }
 
 // Gradients: one warp a token (dout read once, its choices' rows side by side);
 // the warps after the tokens' clear the rows that hold no slot.
-template <typename TY, typename TO>
+template <typename TY, typename TO, bool VEC, int KC>
 __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineArgs a) {
   wait_prior_grid();
   const int lane = threadIdx.x & 31;
@@ -116,16 +119,16 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineArgs
     TY* const dst = static_cast<TY*>(a.dy) + r * a.lddy;
     for (int col = lane * kPiece; col < a.cols; col += 32 * kPiece) {
       const int n = min(kPiece, a.cols - col);
-      if (DG_IN(a.dbg, dst + col, n * int(sizeof(TY)), DBG_COMBINE)) store_piece(zero, dst + col, n, a.vec);
+      if (DG_IN(a.dbg, dst + col, n * int(sizeof(TY)), DBG_COMBINE)) store_piece<VEC>(zero, dst + col, n);
     }
     return;
   }
   const TO* const dout = static_cast<const TO*>(a.out) + warp * a.ldo;
-  for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-    int row[kChoices];
-    float w[kChoices], dot[kChoices];
+  for (int j0 = 0; j0 < a.k; j0 += KC) {
+    int row[KC];
+    float w[KC], dot[KC];
 #pragma unroll
-    for (int j = 0; j < kChoices; ++j) {
+    for (int j = 0; j < KC; ++j) {
       const int64_t slot = warp * a.k + j0 + j;
       row[j] = j0 + j < a.k ? row_of(a, slot) : -1;
       w[j] = row[j] >= 0 && DG_IN(a.dbg, a.weights + slot, 4, DBG_COMBINE) ? __ldg(a.weights + slot) : 0.f;
@@ -134,15 +137,15 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineArgs
     for (int col = lane * kPiece; col < a.cols; col += 32 * kPiece) {
       const int n = min(kPiece, a.cols - col);
       Piece<TO> g;
-      load_piece(g, dout + col, DG_IN(a.dbg, dout + col, n * int(sizeof(TO)), DBG_COMBINE) ? n : 0, a.vec);
-      Piece<TY> y[kChoices];
+      load_piece<VEC>(g, dout + col, DG_IN(a.dbg, dout + col, n * int(sizeof(TO)), DBG_COMBINE) ? n : 0);
+      Piece<TY> y[KC];
 #pragma unroll
-      for (int j = 0; j < kChoices; ++j) {
+      for (int j = 0; j < KC; ++j) {
         const TY* const src = static_cast<const TY*>(a.y) + int64_t(max(row[j], 0)) * a.ldy + col;
-        load_piece(y[j], src, row[j] >= 0 && DG_IN(a.dbg, src, n * int(sizeof(TY)), DBG_COMBINE) ? n : 0, a.vec);
+        load_piece<VEC>(y[j], src, row[j] >= 0 && DG_IN(a.dbg, src, n * int(sizeof(TY)), DBG_COMBINE) ? n : 0);
       }
 #pragma unroll
-      for (int j = 0; j < kChoices; ++j) {
+      for (int j = 0; j < KC; ++j) {
         if (row[j] < 0) continue;
         Piece<TY> d;
 #pragma unroll
@@ -152,11 +155,11 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineArgs
           d.v[i] = from_f<TY>(w[j] * f);
         }
         TY* const dst = static_cast<TY*>(a.dy) + int64_t(row[j]) * a.lddy + col;
-        if (DG_IN(a.dbg, dst, n * int(sizeof(TY)), DBG_COMBINE)) store_piece(d, dst, n, a.vec);
+        if (DG_IN(a.dbg, dst, n * int(sizeof(TY)), DBG_COMBINE)) store_piece<VEC>(d, dst, n);
       }
     }
 #pragma unroll
-    for (int j = 0; j < kChoices; ++j) {
+    for (int j = 0; j < KC; ++j) {
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) dot[j] += __shfl_xor_sync(kAll, dot[j], s);
       const int64_t slot = warp * a.k + j0 + j;
@@ -165,24 +168,33 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineArgs
   }
 }
 
-template <typename TY, typename TO>
+template <typename TY, typename TO, bool VEC, int KC>
 cudaError_t launch(const CombineArgs& a, bool backward, cudaStream_t s) {
   if (backward) {
     const int64_t warps = int64_t(a.tokens) + (a.rowmap ? a.rows : 0);
-    return launch_k(combine_backward_kernel<TY, TO>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0, s, a.pdl, a);
+    return launch_k(combine_backward_kernel<TY, TO, VEC, KC>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0, s, a.pdl, a);
   }
   const int pieces = (a.cols + kPiece - 1) / kPiece;
   const int threads = pieces >= 256 ? 256 : (pieces + 31) / 32 * 32;
-  return launch_k(combine_kernel<TY, TO>, dim3(unsigned(a.tokens), unsigned((pieces + threads - 1) / threads)),
+  return launch_k(combine_kernel<TY, TO, VEC, KC>, dim3(unsigned(a.tokens), unsigned((pieces + threads - 1) / threads)),
                   dim3(unsigned(threads)), 0, s, a.pdl, a);
+}
+
+// KC, the choices of a token that are in flight together: its k rounded up, eight at most.
+template <typename TY, typename TO>
+cudaError_t launch_k_of(const CombineArgs& a, bool backward, cudaStream_t s) {
+  if (!a.vec) return launch<TY, TO, false, 4>(a, backward, s);
+  if (a.k <= 2) return launch<TY, TO, true, 2>(a, backward, s);
+  if (a.k <= 4) return launch<TY, TO, true, 4>(a, backward, s);
+  return launch<TY, TO, true, 8>(a, backward, s);
 }
 
 template <typename TY>
 cudaError_t launch_y(const CombineArgs& a, bool backward, cudaStream_t s) {
   switch (a.o_kind) {
-    case OUT_F32: return launch<TY, float>(a, backward, s);
-    case OUT_BF16: return launch<TY, __nv_bfloat16>(a, backward, s);
-    default: return launch<TY, __half>(a, backward, s);
+    case OUT_F32: return launch_k_of<TY, float>(a, backward, s);
+    case OUT_BF16: return launch_k_of<TY, __nv_bfloat16>(a, backward, s);
+    default: return launch_k_of<TY, __half>(a, backward, s);
   }
 }
 

@@ -435,6 +435,7 @@ struct RouteMapArgs {
   int* pos;
   int* rowmap;
   int rows;  // length of rowmap
+  int wide;  // rowmap on a 16-byte boundary
   int pdl;
   DG_DEBUG_FIELD
 };
@@ -457,7 +458,7 @@ struct CombineArgs {
   void* dy;
   int64_t lddy;
   float* dweights;
-  int vec;  // every row allows eight values a load
+  int vec;  // whole pieces of eight columns on 16-byte boundaries in every row
   int pdl;
   DG_DEBUG_FIELD
 };

@@ -601,6 +601,7 @@ gemm_status_t gemm_route_map(gemm_plan_t plan, int64_t tokens, int64_t top_k, in
   a.pos = pos;
   a.rowmap = rowmap;
   a.rows = int(rows);
+  a.wide = aligned(rowmap, 16);
   a.pdl = plan->pdl;
 #ifdef DG_DEBUG
   a.dbg = Spans(plan->err).bytes(indices, tokens * top_k * 4).bytes(starts, experts * 4).bytes(counts, experts * 4)
@@ -631,7 +632,7 @@ gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top_k, int6
   a.out = out;
   a.ldo = ldo;
   a.o_kind = type_kind(out_type);
-  a.vec = rows_wide(Y, ldy, ye) && rows_wide(out, ldo, oe);
+  a.vec = cols % 8 == 0 && rows_wide(Y, ldy, ye) && rows_wide(out, ldo, oe);
   a.pdl = plan->pdl;
 #ifdef DG_DEBUG
   a.dbg = Spans(plan->err).matrix(Y, rows, cols, ldy, ye).bytes(pos, tokens * top_k * 4).bytes(weights, tokens * top_k * 4)
@@ -674,7 +675,7 @@ gemm_status_t gemm_combine_backward(gemm_plan_t plan, int64_t tokens, int64_t to
   a.dy = dY;
   a.lddy = lddy;
   a.dweights = dweights;
-  a.vec = rows_wide(Y, ldy, ye) && rows_wide(dout, ldo, oe) && rows_wide(dY, lddy, ye);
+  a.vec = cols % 8 == 0 && rows_wide(Y, ldy, ye) && rows_wide(dout, ldo, oe) && rows_wide(dY, lddy, ye);
   a.pdl = plan->pdl;
 #ifdef DG_DEBUG
   a.dbg = Spans(plan->err).matrix(dout, tokens, cols, ldo, oe).matrix(Y, rows, cols, ldy, ye).bytes(pos, tokens * top_k * 4)

@@ -16,6 +16,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 
 namespace dg {
@@ -23,39 +25,76 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 
+// Four consecutive values of a row as they are loaded.
 template <typename T>
-__device__ __forceinline__ float to_f(T v);
+struct Four;
 template <>
-__device__ __forceinline__ float to_f(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-
-// Four consecutive values of a row, the first n of which exist (the rest are 0).
+struct Four<float> {
+  uint4 w;
+  __device__ __forceinline__ void clear() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const float* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void put(int i, float v) { (&w.x)[i] = __float_as_uint(v); }
+  __device__ __forceinline__ float at(int i) const { return __uint_as_float(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w); }
+};
+// 16-bit types: a magnitude's bits are ordered like the number, two to a register.
 template <typename T>
-__device__ __forceinline__ void load4(float (&v)[4], const T* p, int n, bool vec) {
-  if (vec && n >= 4) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 q = *reinterpret_cast<const float4*>(p);
-      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-    } else {
-      const uint2 q = *reinterpret_cast<const uint2*>(p);
-      alignas(8) T h[4];
-      *reinterpret_cast<uint2*>(h) = q;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = to_f(h[i]);
-    }
-    return;
+struct Four {
+  uint2 w;
+  __device__ __forceinline__ void clear() { w = make_uint2(0, 0); }
+  __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void put(int i, T v) {
+    const uint32_t b = *reinterpret_cast<const uint16_t*>(&v);
+    uint32_t& r = i < 2 ? w.x : w.y;
+    r = i & 1 ? (r & 0xffffu) | b << 16 : (r & 0xffff0000u) | b;
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = i < n ? to_f(p[i]) : 0.f;
-}
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t r = i < 2 ? w.x : w.y;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(i & 1 ? r & 0xffff0000u : r << 16);
+    const uint16_t h = uint16_t(i & 1 ? r >> 16 : r);
+    return __half2float(*reinterpret_cast<const __half*>(&h));
+  }
+};
+
+// Largest magnitudes: of a row's four values, and column by column of several rows; as
+// fp32 bits at the end.  Infinities and NaN come out as bits of at least kInf.
+constexpr uint32_t kInf = 0x7f800000u;
+
+template <typename T>
+struct Peak {  // 16-bit types: columns 0-1 and 2-3 of a lane
+  uint32_t a = 0, b = 0;
+  __device__ __forceinline__ void take(const Four<T>& f) {
+    a = __vmaxu2(a, f.w.x & 0x7fff7fffu);
+    b = __vmaxu2(b, f.w.y & 0x7fff7fffu);
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t h) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) return h << 16;
+    const uint16_t u = uint16_t(h);
+    return __float_as_uint(__half2float(*reinterpret_cast<const __half*>(&u)));
+  }
+  __device__ __forceinline__ uint32_t column(int j) const {
+    const uint32_t r = j < 2 ? a : b;
+    return bits(j & 1 ? r >> 16 : r & 0xffffu);
+  }
+  __device__ __forceinline__ uint32_t row() const {
+    const uint32_t m = __vmaxu2(a, b);
+    return bits(max(m >> 16, m & 0xffffu));
+  }
+};
+template <>
+struct Peak<float> {
+  uint32_t m[4] = {0, 0, 0, 0};
+  __device__ __forceinline__ void take(const Four<float>& f) {
+    m[0] = max(m[0], f.w.x & 0x7fffffffu), m[1] = max(m[1], f.w.y & 0x7fffffffu);
+    m[2] = max(m[2], f.w.z & 0x7fffffffu), m[3] = max(m[3], f.w.w & 0x7fffffffu);
+  }
+  __device__ __forceinline__ uint32_t column(int j) const { return m[j]; }
+  __device__ __forceinline__ uint32_t row() const { return max(max(m[0], m[1]), max(m[2], m[3])); }
+};
 
 // |v|'s bits, 0 for infinities and NaN.
-__device__ __forceinline__ uint32_t magnitude(float v) {
+__device__ __forceinline__ uint32_t finite_bits(float v) {
   const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
-  return b < 0x7f800000u ? b : 0u;
+  return b < kInf ? b : 0u;
 }
 
 // Scale byte (e + 127) of a block whose largest magnitude has the bits m.
@@ -67,13 +106,21 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t m) {
 
 __device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// Codes of v * inv; what is not finite becomes NaN (the conversion would saturate infinities).
-template <bool E5M2>
+// Codes of two values times inv.  NaN converts to NaN; infinities would saturate, so that
+// where a tile holds any (CAREFUL) they are made NaN first.
+template <bool E5M2, bool CAREFUL>
 __device__ __forceinline__ uint32_t codes2(float a, float b, float inv) {
-  const float nan = __uint_as_float(0x7fc00000u);
-  a = fabsf(a) < __uint_as_float(0x7f800000u) ? a * inv : nan;
-  b = fabsf(b) < __uint_as_float(0x7f800000u) ? b * inv : nan;
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, E5M2 ? __NV_E5M2 : __NV_E4M3);
+  if constexpr (CAREFUL) {
+    const float nan = __uint_as_float(0x7fc00000u);
+    if (!(fabsf(a) < __uint_as_float(kInf))) a = nan;
+    if (!(fabsf(b) < __uint_as_float(kInf))) b = nan;
+  }
+  return __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, E5M2 ? __NV_E5M2 : __NV_E4M3);
+}
+
+template <bool E5M2, bool CAREFUL>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
+  return codes2<E5M2, CAREFUL>(a, b, inv) | codes2<E5M2, CAREFUL>(c, d, inv) << 16;
 }
 
 // Byte of row r, block c in the packed scales of a matrix with `groups` groups of four blocks.
@@ -90,54 +137,77 @@ __device__ __forceinline__ int source_row(const QuantArgs& a, int r) {
   return row < a.src_rows ? row : -1;
 }
 
+// n rows' groups of four columns, from `col` on: whole groups as one load each (VEC: rows
+// allow it) without a branch between them, so that all are in flight together; then the
+// columns of a group that reaches past the matrix, one by one.
+template <typename T, bool VEC, int N>
+__device__ __forceinline__ void load_rows(Four<T> (&f)[N], const QuantArgs& a, const int (&src)[N], int col) {
+  const T* const x = static_cast<const T*>(a.x) + col;
+  const int n = min(4, a.cols - col);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    f[i].clear();
+    const T* const p = x + int64_t(src[i]) * a.ldx;
+    if (VEC && n == 4 && src[i] >= 0 && DG_IN(a.dbg, p, 4 * int(sizeof(T)), DBG_QUANTIZE)) f[i].load(p);
+  }
+  if (n > 0 && (!VEC || n < 4)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const T* const p = x + int64_t(src[i]) * a.ldx;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (src[i] >= 0 && j < n && DG_IN(a.dbg, p + j, int(sizeof(T)), DBG_QUANTIZE)) f[i].put(j, p[j]);
+    }
+  }
+}
+
+__device__ __forceinline__ void store4(const QuantArgs& a, uint8_t* dst, uint32_t c, int n) {
+  if (n <= 0 || !DG_IN(a.dbg, dst, n < 4 ? n : 4, DBG_QUANTIZE)) return;
+  if (n >= 4)
+    *reinterpret_cast<uint32_t*>(dst) = c;
+  else
+    for (int t = 0; t < n; ++t) dst[t] = uint8_t(c >> (8 * t));
+}
+
 // One orientation, a scale for each row's block: a warp takes kRows rows of 512
 // columns (one word of scale bytes each), all its loads in flight together.
 constexpr int kRows = 2;
 
-template <typename T, bool E5M2>
+template <typename T, bool E5M2, bool VEC>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
   wait_prior_grid();
   const int lane = threadIdx.x & 31;
-  const int64_t warp = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int groups = a.q_groups;
+  const uint32_t warp = uint32_t((uint64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5);
+  const uint32_t groups = uint32_t(a.q_groups);
   const int r0 = int(warp / groups) * kRows;
   const int g = int(warp % groups);
   if (r0 >= a.rows_padded) return;
-  const T* const x = static_cast<const T*>(a.x);
-  float v[kRows][4][4];
+  Four<T> f[4][kRows];
   int src[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) src[i] = source_row(a, r0 + i);
 #pragma unroll
-  for (int i = 0; i < kRows; ++i)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int col = g * 512 + b * 128 + 4 * lane;
-      const T* const p = x + int64_t(src[i]) * a.ldx + col;
-      const int n = src[i] >= 0 ? min(4, a.cols - col) : 0;
-      load4(v[i][b], p, n > 0 && DG_IN(a.dbg, p, n * int(sizeof(T)), DBG_QUANTIZE) ? n : 0, a.vec);
-    }
+  for (int b = 0; b < 4; ++b) load_rows<T, VEC>(f[b], a, src, g * 512 + b * 128 + 4 * lane);
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     uint32_t word = 0;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      float(&w)[4] = v[i][b];
-      const uint32_t m = __reduce_max_sync(
-          kAll, max(max(magnitude(w[0]), magnitude(w[1])), max(magnitude(w[2]), magnitude(w[3]))));
+      const Four<T>& v = f[b][i];
+      Peak<T> peak;
+      peak.take(v);
+      uint32_t m = __reduce_max_sync(kAll, peak.row());
+      const bool careful = m >= kInf;
+      if (careful)
+        m = __reduce_max_sync(kAll, max(max(finite_bits(v.at(0)), finite_bits(v.at(1))),
+                                        max(finite_bits(v.at(2)), finite_bits(v.at(3)))));
       const uint32_t byte = scale_byte<E5M2>(m);
       word |= byte << (8 * b);
       const int col = g * 512 + b * 128 + 4 * lane;
-      const int n = src[i] >= 0 ? min(4, a.cols - col) : 0;
-      if (n <= 0) continue;
       const float inv = inverse_scale(byte);
-      const uint32_t c = codes2<E5M2>(w[0], w[1], inv) | codes2<E5M2>(w[2], w[3], inv) << 16;
-      uint8_t* const dst = a.q + int64_t(r0 + i) * a.ldq + col;
-      if (!DG_IN(a.dbg, dst, n, DBG_QUANTIZE)) continue;
-      if (n == 4)
-        *reinterpret_cast<uint32_t*>(dst) = c;
-      else
-        for (int t = 0; t < n; ++t) dst[t] = uint8_t(c >> (8 * t));
+      const uint32_t c = careful ? codes4<E5M2, true>(v.at(0), v.at(1), v.at(2), v.at(3), inv)
+                                 : codes4<E5M2, false>(v.at(0), v.at(1), v.at(2), v.at(3), inv);
+      if (src[i] >= 0) store4(a, a.q + int64_t(r0 + i) * a.ldq + col, c, a.cols - col);
     }
     uint8_t* const s = a.sq + scale_at(r0 + i, int64_t(g) * 4, groups);
     if (lane == 0 && DG_IN(a.dbg, s, 4, DBG_QUANTIZE)) *reinterpret_cast<uint32_t*>(s) = word;
@@ -145,34 +215,43 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
 }
 
 // Both orientations (or 128 x 128 scales): a CTA takes one 128 x 128 tile, 16 rows a
-// warp and 4 columns a lane, held in registers.  Row maxima are warp reductions;
-// column maxima meet in shared memory.  A thread's 16 rows of a column are 16 consecutive
-// bytes of the transposed matrix: they are turned round in a swizzled shared-memory tile
-// and leave as 128-byte rows.
-template <typename T, bool E5M2>
-__global__ void __launch_bounds__(256) quantize_tile_kernel(const QuantArgs a) {
+// warp and 4 columns a lane, held in registers.  Row maxima are warp reductions, each
+// row's scale worked out by one lane; column maxima meet in shared memory.  A thread's 16
+// rows of a column are 16 consecutive bytes of the transposed matrix: they are turned
+// round in a swizzled shared-memory tile and leave as 128-byte rows.
+template <typename T, bool E5M2, bool VEC>
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quantize_tile_kernel(const QuantArgs a) {
   __shared__ uint32_t col_max[8][128];
   __shared__ uint4 turn[128 * 8];  // [column][16-byte piece of rows ^ (column / 4 % 8)]
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cb = blockIdx.x, rb = blockIdx.y;  // past the matrix: only scale bytes, zero
   const int row0 = rb * 128 + warp * 16, col = cb * 128 + 4 * lane;
-  const T* const x = static_cast<const T*>(a.x);
-  float v[16][4];
-  uint32_t live = 0;  // rows that are read
+  Four<T> v[16];
+  uint32_t live = 0;  // rows that exist
+  {
+    int src[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int src = source_row(a, row0 + i);
-    const int n = src >= 0 ? min(4, a.cols - col) : 0;
-    const T* const p = x + int64_t(src) * a.ldx + col;
-    load4(v[i], p, n > 0 && DG_IN(a.dbg, p, n * int(sizeof(T)), DBG_QUANTIZE) ? n : 0, a.vec);
-    live |= uint32_t(src >= 0) << i;
+    for (int i = 0; i < 16; ++i) {
+      src[i] = source_row(a, row0 + i);
+      live |= uint32_t(src[i] >= 0) << i;
+    }
+    load_rows<T, VEC>(v, a, src, col);
   }
-  uint32_t cm[4] = {0, 0, 0, 0};
+  Peak<T> peak;
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < 16; ++i) peak.take(v[i]);
+  uint32_t cm[4] = {peak.column(0), peak.column(1), peak.column(2), peak.column(3)};
+  // infinities or NaN anywhere in the tile: maxima over what is finite, careful conversions
+  const bool careful = __syncthreads_or(max(max(cm[0], cm[1]), max(cm[2], cm[3])) >= kInf);
+  if (careful) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) cm[j] = max(cm[j], magnitude(v[i][j]));
+    for (int j = 0; j < 4; ++j) {
+      cm[j] = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) cm[j] = max(cm[j], finite_bits(v[i].at(j)));
+    }
+  }
   *reinterpret_cast<uint4*>(&col_max[warp][4 * lane]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
   __syncthreads();
 #pragma unroll
@@ -183,24 +262,29 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const QuantArgs a) {
   uint32_t tile = 0;  // scale byte of the whole tile
   if (a.block_rows > 1) tile = scale_byte<E5M2>(__reduce_max_sync(kAll, max(max(cm[0], cm[1]), max(cm[2], cm[3]))));
   if (a.q) {
-    uint32_t mine = 0;
+    uint32_t mine = 0;  // lane i: scale byte of row i
+    if (a.block_rows == 1) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        Peak<T> row;
+        row.take(v[i]);
+        uint32_t m = row.row();
+        if (careful)
+          m = max(max(finite_bits(v[i].at(0)), finite_bits(v[i].at(1))), max(finite_bits(v[i].at(2)), finite_bits(v[i].at(3))));
+        m = __reduce_max_sync(kAll, m);
+        if (lane == i) mine = m;
+      }
+      mine = scale_byte<E5M2>(mine);
+    } else {
+      mine = tile;
+    }
+    const float inv_mine = inverse_scale(mine);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      uint32_t byte = tile;
-      if (a.block_rows == 1)
-        byte = scale_byte<E5M2>(__reduce_max_sync(
-            kAll, max(max(magnitude(v[i][0]), magnitude(v[i][1])), max(magnitude(v[i][2]), magnitude(v[i][3])))));
-      if (lane == i) mine = byte;
-      const int n = (live >> i) & 1 ? min(4, a.cols - col) : 0;
-      if (n <= 0) continue;
-      const float inv = inverse_scale(byte);
-      const uint32_t c = codes2<E5M2>(v[i][0], v[i][1], inv) | codes2<E5M2>(v[i][2], v[i][3], inv) << 16;
-      uint8_t* const dst = a.q + int64_t(row0 + i) * a.ldq + col;
-      if (!DG_IN(a.dbg, dst, n, DBG_QUANTIZE)) continue;
-      if (n == 4)
-        *reinterpret_cast<uint32_t*>(dst) = c;
-      else
-        for (int t = 0; t < n; ++t) dst[t] = uint8_t(c >> (8 * t));
+      const float inv = __shfl_sync(kAll, inv_mine, i);
+      const uint32_t c = careful ? codes4<E5M2, true>(v[i].at(0), v[i].at(1), v[i].at(2), v[i].at(3), inv)
+                                 : codes4<E5M2, false>(v[i].at(0), v[i].at(1), v[i].at(2), v[i].at(3), inv);
+      if ((live >> i) & 1u) store4(a, a.q + int64_t(row0 + i) * a.ldq + col, c, a.cols - col);
     }
     if (lane < 16 && row0 < a.rows_padded) {
       uint8_t* const s = a.sq + scale_at(row0 + lane, cb, a.q_groups);
@@ -210,14 +294,14 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const QuantArgs a) {
   if (a.qt) {
     uint32_t bytes[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) bytes[j] = a.block_rows == 1 ? scale_byte<E5M2>(cm[j]) : tile;
-#pragma unroll
     for (int j = 0; j < 4; ++j) {
+      bytes[j] = a.block_rows == 1 ? scale_byte<E5M2>(cm[j]) : tile;
       const float inv = inverse_scale(bytes[j]);
       uint32_t w[4];
 #pragma unroll
       for (int h = 0; h < 4; ++h)
-        w[h] = codes2<E5M2>(v[4 * h][j], v[4 * h + 1][j], inv) | codes2<E5M2>(v[4 * h + 2][j], v[4 * h + 3][j], inv) << 16;
+        w[h] = careful ? codes4<E5M2, true>(v[4 * h].at(j), v[4 * h + 1].at(j), v[4 * h + 2].at(j), v[4 * h + 3].at(j), inv)
+                       : codes4<E5M2, false>(v[4 * h].at(j), v[4 * h + 1].at(j), v[4 * h + 2].at(j), v[4 * h + 3].at(j), inv);
       turn[(4 * lane + j) * 8 + (warp ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
     }
     if (warp == 0) {
@@ -251,22 +335,23 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(const QuantArgs a) {
   }
 }
 
-template <typename T, bool E5M2>
+template <typename T, bool E5M2, bool VEC>
 cudaError_t launch(const QuantArgs& a, cudaStream_t s) {
   if (!a.qt && a.block_rows == 1) {
     const int64_t warps = int64_t(a.rows_padded / kRows) * a.q_groups;
-    return launch_k(quantize_rows_kernel<T, E5M2>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0, s, a.pdl, a);
+    return launch_k(quantize_rows_kernel<T, E5M2, VEC>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0, s, a.pdl, a);
   }
   // blocks past the matrix write the zero bytes that pad the scales to whole words
   const int col_blocks = a.q ? a.q_groups * 4 : (a.cols + 127) / 128;
   const int row_blocks = a.qt ? a.qt_groups * 4 : (a.rows + 127) / 128;
-  return launch_k(quantize_tile_kernel<T, E5M2>, dim3(unsigned(col_blocks), unsigned(row_blocks)), dim3(256), 0, s,
+  return launch_k(quantize_tile_kernel<T, E5M2, VEC>, dim3(unsigned(col_blocks), unsigned(row_blocks)), dim3(256), 0, s,
                   a.pdl, a);
 }
 
 template <typename T>
 cudaError_t launch_type(const QuantArgs& a, cudaStream_t s) {
-  return a.e5m2 ? launch<T, true>(a, s) : launch<T, false>(a, s);
+  if (a.vec) return a.e5m2 ? launch<T, true, true>(a, s) : launch<T, false, true>(a, s);
+  return a.e5m2 ? launch<T, true, false>(a, s) : launch<T, false, false>(a, s);
 }
 
 // One thread 16 bytes of a row, loaded in pieces that the rows' alignment allows (T).

@@ -52,64 +52,80 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The scores of a token from its logits (NaN read as minus infinity).  A masked
+// What turns a token's logits (NaN read as minus infinity) into scores.  A masked
 // expert (minus infinity) scores 0; a row with nothing else scores 0 throughout.
-template <int P>
-__device__ __forceinline__ void scores(const RouteArgs& a, const float (&x)[P], float (&s)[P]) {
-  if (a.sigmoid) {
+struct Scorer {
+  int sigmoid;
+  float top, sum;  // softmax: largest logit, sum of exp(x - top)
+  template <int P>
+  __device__ __forceinline__ Scorer(const RouteArgs& a, const float (&x)[P]) : sigmoid(a.sigmoid), top(kNegInf), sum(0.f) {
+    if (sigmoid) return;
 #pragma unroll
-    for (int i = 0; i < P; ++i) s[i] = __fdiv_rn(1.f, __fadd_rn(1.f, expf(-x[i])));
-    return;
+    for (int i = 0; i < P; ++i) top = fmaxf(top, x[i]);
+    top = key_value(__reduce_max_sync(kAll, order_key(top)));
+#pragma unroll
+    for (int i = 0; i < P; ++i) sum = __fadd_rn(sum, power(x[i]));
+    sum = warp_sum(sum);
   }
-  float top = kNegInf;
-#pragma unroll
-  for (int i = 0; i < P; ++i) top = fmaxf(top, x[i]);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    s[i] = x[i] == kNegInf ? 0.f : x[i] == top ? 1.f : expf(__fsub_rn(x[i], top));
-    sum = __fadd_rn(sum, s[i]);
+  __device__ __forceinline__ float power(float x) const {  // softmax's numerator
+    return x == kNegInf ? 0.f : x == top ? 1.f : expf(__fsub_rn(x, top));
   }
-  sum = warp_sum(sum);
-  if (sum > 0.f)
-#pragma unroll
-    for (int i = 0; i < P; ++i) s[i] = __fdiv_rn(s[i], sum);
+  __device__ __forceinline__ float score(float x) const {
+    if (sigmoid) return __fdiv_rn(1.f, __fadd_rn(1.f, expf(-x)));
+    return sum > 0.f ? __fdiv_rn(power(x), sum) : 0.f;
+  }
+};
+
+// Logit e of token t, NaN and what is not there as minus infinity.
+__device__ __forceinline__ float logit(const RouteArgs& a, int t, int e) {
+  if (e < 0 || e >= a.experts) return kNegInf;
+  const int64_t at = int64_t(t) * a.ldl + e;
+  if (!DG_IN(a.dbg, static_cast<const char*>(a.logits) + at * (a.kind == OUT_F32 ? 4 : 2), a.kind == OUT_F32 ? 4 : 2,
+             DBG_ROUTE))
+    return kNegInf;
+  const float f = load_logit(a.logits, a.kind, at);
+  return f == f ? f : kNegInf;
 }
 
 template <int P>
 __device__ __forceinline__ void load_logits(const RouteArgs& a, int t, int lane, float (&x)[P]) {
-  [[maybe_unused]] const int es = a.kind == OUT_F32 ? 4 : 2;
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int e = 32 * i + lane;
-    x[i] = kNegInf;
-    if (e >= a.experts) continue;
-    const int64_t at = int64_t(t) * a.ldl + e;
-    if (!DG_IN(a.dbg, static_cast<const char*>(a.logits) + at * es, es, DBG_ROUTE)) continue;
-    const float f = load_logit(a.logits, a.kind, at);
-    x[i] = f == f ? f : kNegInf;
-  }
+  for (int i = 0; i < P; ++i) x[i] = logit(a, t, 32 * i + lane);
 }
 
-// Largest key of the warp and the lowest expert that has it; the expert's key becomes kNone.
+// Sorts a lane's keys, largest first (an odd-even network of P rounds); ex[i] is the expert of
+// key[i].  Equal keys keep the lower expert first: only a strictly larger key moves up.
 template <int P>
-__device__ __forceinline__ uint32_t take_best(uint32_t (&key)[P], int lane, int* expert) {
-  uint32_t best = key[0];
+__device__ __forceinline__ void sort_lane(uint32_t (&key)[P], int (&ex)[P]) {
 #pragma unroll
-  for (int i = 1; i < P; ++i) best = max(best, key[i]);
-  best = __reduce_max_sync(kAll, best);
-  uint32_t at = 0xffffffffu;
+  for (int round = 0; round < P; ++round)
 #pragma unroll
-  for (int i = P - 1; i >= 0; --i)
-    if (key[i] == best) at = uint32_t(32 * i + lane);
-  at = __reduce_min_sync(kAll, at);
+    for (int i = round & 1; i + 1 < P; i += 2) {
+      const bool up = key[i + 1] > key[i];
+      const uint32_t k0 = key[i], k1 = key[i + 1];
+      const int e0 = ex[i], e1 = ex[i + 1];
+      key[i] = up ? k1 : k0, key[i + 1] = up ? k0 : k1;
+      ex[i] = up ? e1 : e0, ex[i + 1] = up ? e0 : e1;
+    }
+}
+
+// The warp's best expert, whose lane then moves on to its next one: the largest key, and
+// among equal ones the lowest expert (lanes that have it are compared only if there are several).
+template <int P>
+__device__ __forceinline__ int take_best(uint32_t (&key)[P], int (&ex)[P], int lane) {
+  const uint32_t best = __reduce_max_sync(kAll, key[0]);
+  const uint32_t who = __ballot_sync(kAll, key[0] == best);
+  int expert;
+  if (who & (who - 1))
+    expert = int(__reduce_min_sync(kAll, key[0] == best ? uint32_t(ex[0]) : 0xffffffffu));
+  else
+    expert = __shfl_sync(kAll, ex[0], __ffs(who) - 1);
+  if (lane == (expert & 31)) {
 #pragma unroll
-  for (int i = 0; i < P; ++i)
-    if (at == uint32_t(32 * i + lane)) key[i] = kNone;
-  *expert = int(at);
-  return best;
+    for (int i = 0; i + 1 < P; ++i) key[i] = key[i + 1], ex[i] = ex[i + 1];
+    key[P - 1] = kNone;
+  }
+  return expert;
 }
 
 // Two largest keys among the experts of group g.
@@ -137,17 +153,19 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
   const int lane = threadIdx.x & 31;
   const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (t >= a.tokens) return;
-  float x[P], s[P];
+  float x[P];
   load_logits(a, t, lane, x);
-  scores(a, x, s);
+  const Scorer scorer(a, x);
   uint32_t key[P];
   const bool by_logit = a.bias == nullptr && a.group_top == 1;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int e = 32 * i + lane;
-    float k = by_logit ? x[i] : s[i];
-    if (e < a.experts && a.bias && DG_IN(a.dbg, a.bias + e, 4, DBG_ROUTE)) k = __fadd_rn(k, __ldg(a.bias + e));
-    if (x[i] == kNegInf) k = kNegInf;  // masked, whatever its bias
+    float k = x[i];
+    if (!by_logit && k != kNegInf) {  // a masked expert stays minus infinity, whatever its bias
+      k = scorer.score(k);
+      if (e < a.experts && a.bias && DG_IN(a.dbg, a.bias + e, 4, DBG_ROUTE)) k = __fadd_rn(k, __ldg(a.bias + e));
+    }
     key[i] = e < a.experts ? order_key(k) : kNone;
   }
   if (a.groups > 1) {
@@ -176,21 +194,18 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
       if (e < a.experts && !((chosen >> (e / per)) & 1u)) key[i] = kOutside;
     }
   }
-  int expert = 0;     // lane j: choice j
-  float score = 0.f;
-  for (int j = 0; j < a.top_k; ++j) {
-    int e;
-    take_best(key, lane, &e);
-    float v = 0.f;
+  int ex[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (e == 32 * i + lane) v = s[i];
-    v = __shfl_sync(kAll, v, e & 31);
-    if (lane == j) {
-      expert = e;
-      score = v;
-    }
+  for (int i = 0; i < P; ++i) ex[i] = 32 * i + lane;
+  sort_lane(key, ex);
+  int expert = -1;  // lane j: choice j
+  for (int j = 0; j < a.top_k; ++j) {
+    const int e = take_best(key, ex, lane);
+    if (lane == j) expert = e;
   }
+  // the chosen ones' scores, from their logits again (a few loads that hit L1)
+  const float mine = logit(a, t, expert);
+  float score = mine == kNegInf ? 0.f : scorer.score(mine);
   if (a.renormalize) {
     float sum = 0.f;
     for (int j = 0; j < a.top_k; ++j) sum = __fadd_rn(sum, __shfl_sync(kAll, score, j));
@@ -213,26 +228,19 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
   const int lane = threadIdx.x & 31;
   const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (t >= a.tokens) return;
-  float x[P], s[P], ds[P];
+  float x[P], ds[P];
   load_logits(a, t, lane, x);
-  scores(a, x, s);
+  const Scorer scorer(a, x);
   int expert = -1;  // lane j: choice j; an index outside the experts takes no part
-  float dw = 0.f, sj = 0.f;
+  float dw = 0.f;
   if (lane < a.top_k) {
     const int64_t at = int64_t(t) * a.top_k + lane;
     if (DG_IN(a.dbg, a.indices + at, 4, DBG_ROUTE)) expert = a.indices[at];
     if (DG_IN(a.dbg, a.dweights + at, 4, DBG_ROUTE)) dw = a.dweights[at];
     if (expert < 0 || expert >= a.experts) expert = -1, dw = 0.f;
   }
-  for (int j = 0; j < a.top_k; ++j) {
-    const int e = __shfl_sync(kAll, expert, j);
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (e == 32 * i + lane) v = s[i];
-    v = __shfl_sync(kAll, v, e & 31);
-    if (lane == j && e >= 0) sj = v;
-  }
+  const float chosen = logit(a, t, expert);
+  const float sj = chosen == kNegInf ? 0.f : scorer.score(chosen);
   float dsj = a.scale * dw;
   if (a.renormalize) {
     const float sum = warp_sum(sj);
@@ -250,11 +258,18 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
       if (e == 32 * i + lane) ds[i] += d;
   }
   const int es = a.kind == OUT_F32 ? 4 : 2;
+  const float over = scorer.sum > 0.f ? 1.f / scorer.sum : 0.f;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int e = 32 * i + lane;
     if (e >= a.experts) continue;
-    const float d = a.sigmoid ? s[i] * (1.f - s[i]) * ds[i] : s[i] * (ds[i] - through);
+    float d = 0.f;
+    if (!a.sigmoid) {
+      d = scorer.power(x[i]) * over * (ds[i] - through);
+    } else if (ds[i] != 0.f) {  // (experts that were not chosen)
+      const float s = scorer.score(x[i]);
+      d = s * (1.f - s) * ds[i];
+    }
     char* const dst = static_cast<char*>(a.dlogits) + (int64_t(t) * a.lddl + e) * es;
     if (!DG_IN(a.dbg, dst, es, DBG_ROUTE)) continue;
     if (a.kind == OUT_F32)
@@ -283,9 +298,10 @@ cudaError_t by_experts(int experts, F f) {
 // its CTA's.  A warp counts its slots by expert (lanes with the same expert find each
 // other with match, one of them adds), CTAs read each other's totals through
 // distributed shared memory, and a second walk over the slots hands out rows:
-// start of the expert + slots of earlier CTAs, warps and lanes.  No atomics: the
-// order is the slots' own.
+// start of the expert + slots of earlier CTAs, warps and lanes (the place within the warp is
+// kept in pos between the walks).  No atomics: the order is the slots' own.
 constexpr int kMapThreads = 1024;
+constexpr int kAhead = 8;  // loads of a warp's slots that are in flight together
 
 // ints: four tables over the experts (this CTA's slots, all slots, slots of earlier
 // CTAs, first row), then a count for each warp and expert
@@ -303,13 +319,22 @@ __global__ void __launch_bounds__(kMapThreads) route_map_kernel(const RouteMapAr
   int* const before = all + E;
   int* const start = before + E;     // E + 1: [E] is the end of the last expert's rows
   int* const count = start + E + 1;  // [warps][E]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = int(blockDim.x);
-  for (int i = threadIdx.x; i < E * warps; i += threads) count[i] = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < E * warps; i += kMapThreads) count[i] = 0;
+  // every row holds no slot, until its slot says otherwise (after the barriers below)
+  for (int r = 4 * (rank * kMapThreads + int(threadIdx.x)); r < a.rows; r += 4 * ctas * kMapThreads) {
+    const int n = min(4, a.rows - r);
+    if (!DG_IN(a.dbg, a.rowmap + r, 4 * n, DBG_ROUTE)) continue;
+    if (n == 4 && a.wide)
+      *reinterpret_cast<int4*>(a.rowmap + r) = make_int4(-1, -1, -1, -1);
+    else
+      for (int i = 0; i < n; ++i) a.rowmap[r + i] = -1;
+  }
   __syncthreads();
-  // this warp's run of slots: a multiple of 32
+  // this warp's run of slots: a multiple of 32 (warps past `warps` have none)
   const int runs = ctas * warps;
   const int run = ((a.slots + runs - 1) / runs + 31) & ~31;
-  const int64_t first = int64_t(rank * warps + warp) * run;
+  const int64_t first = warp < warps ? int64_t(rank * warps + warp) * run : a.slots;
   const int64_t last = min(int64_t(a.slots), first + run);
   int* const mine = count + warp * E;
   auto expert_of = [&](int64_t slot) {
@@ -317,14 +342,25 @@ __global__ void __launch_bounds__(kMapThreads) route_map_kernel(const RouteMapAr
     const int e = __ldg(a.indices + slot);
     return e >= 0 && e < E ? e : -1;
   };
-  for (int64_t s = first; s < last; s += 32) {
-    const int e = expert_of(s + lane);
-    const uint32_t same = __match_any_sync(kAll, e);
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
+  // first walk: a slot's place among its warp's slots of its expert, kept in pos
+  for (int64_t s = first; s < last; s += 32 * kAhead) {
+    int e[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) e[i] = expert_of(s + 32 * i + lane);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t slot = s + 32 * i + lane;
+      const uint32_t same = __match_any_sync(kAll, e[i]);
+      const int earlier = e[i] >= 0 ? mine[e[i]] : 0;
+      __syncwarp();
+      if (e[i] >= 0 && lane == __ffs(same) - 1) mine[e[i]] = earlier + __popc(same);
+      __syncwarp();
+      if (slot < last && DG_IN(a.dbg, a.pos + slot, 4, DBG_ROUTE))
+        a.pos[slot] = earlier + __popc(same & ((1u << lane) - 1u));
+    }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += threads) {  // counts -> slots of earlier warps
+  for (int e = threadIdx.x; e < E; e += kMapThreads) {  // counts -> slots of earlier warps
     int sum = 0;
     for (int w = 0; w < warps; ++w) {
       const int n = count[w * E + e];
@@ -337,7 +373,7 @@ __global__ void __launch_bounds__(kMapThreads) route_map_kernel(const RouteMapAr
     cluster.sync();
   else
     __syncthreads();
-  for (int e = threadIdx.x; e < E; e += threads) {
+  for (int e = threadIdx.x; e < E; e += kMapThreads) {
     int earlier = 0, sum = 0;
     for (int c = 0; c < ctas; ++c) {
       const int n = ctas > 1 ? *cluster.map_shared_rank(total + e, c) : total[e];
@@ -366,28 +402,17 @@ __global__ void __launch_bounds__(kMapThreads) route_map_kernel(const RouteMapAr
       }
       carry += __shfl_sync(kAll, sum, 31);
     }
-    if (lane == 0) start[E] = carry;
   }
   __syncthreads();
-  // rows that hold no slot: the ends of the experts' last 128s, and what follows the last expert
-  auto no_slot = [&](int row) {
-    if (row < a.rows && DG_IN(a.dbg, a.rowmap + row, 4, DBG_ROUTE)) a.rowmap[row] = -1;
-  };
-  for (int e = rank * warps + warp; e < E; e += runs)
-    for (int r = start[e] + all[e] + lane; r < start[e + 1]; r += 32) no_slot(r);
-  for (int r = start[E] + rank * threads + int(threadIdx.x); r < a.rows; r += ctas * threads) no_slot(r);
-  // rows of this warp's slots, in their order
-  for (int64_t s = first; s < last; s += 32) {
-    const int64_t slot = s + lane;
-    const int e = expert_of(slot);
-    const uint32_t same = __match_any_sync(kAll, e);
-    int row = -1;
-    if (e >= 0) row = start[e] + before[e] + mine[e] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
-    if (slot < last) {
-      if (DG_IN(a.dbg, a.pos + slot, 4, DBG_ROUTE)) a.pos[slot] = row;
+  // second walk: rows of this warp's slots
+  for (int64_t s = first; s < last; s += 32 * kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t slot = s + 32 * i + lane;
+      const int e = expert_of(slot);
+      if (slot >= last || !DG_IN(a.dbg, a.pos + slot, 4, DBG_ROUTE)) continue;
+      const int row = e >= 0 ? start[e] + before[e] + mine[e] + a.pos[slot] : -1;
+      a.pos[slot] = row;
       if (row >= 0 && row < a.rows && DG_IN(a.dbg, a.rowmap + row, 4, DBG_ROUTE)) a.rowmap[row] = int(slot);
     }
   }
@@ -426,7 +451,7 @@ cudaError_t launch_route_map(const RouteMapArgs& a, cudaStream_t s) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
-  cfg.blockDim = dim3(unsigned(warps * 32));
+  cfg.blockDim = dim3(kMapThreads);
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

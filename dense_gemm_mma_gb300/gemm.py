@@ -330,7 +330,9 @@ def gemm_combine_backward(plan, tokens, top_k, cols, rows, dout, ldo, out_type, 
 
 # ------------------------------------------------------------------ torch helpers
 
-_types: dict = {}
+_types: dict = {}  # torch dtype -> gemm_type_t, filled at the first tensor
+_array_types: dict = {}
+_PLAIN = gemm_epilogue_t(GEMM_ACT_NONE, 0.0)
 
 
 def _type_of(t) -> int:
@@ -345,34 +347,50 @@ def _type_of(t) -> int:
         raise ValueError(f"no gemm_type_t for {t.dtype}") from None
 
 
+def _matrix(t):
+    """(pointer, rows, columns, ld) of a 2-D tensor whose rows are contiguous.  (These helpers run in
+    front of every launch, and small launches wait for them: one look at each property.)"""
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError("expected a 2-D tensor with contiguous rows")
+    return t.data_ptr(), rows, cols, ld if ld >= cols and ld > 0 else max(cols, 1)
+
+
+def _matrices(t):
+    """(pointer, matrices, rows, columns, ld, elements between matrices) of a 3-D stack of matrices
+    whose rows are contiguous."""
+    n, rows, cols = t.shape
+    group, ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError("expected a 3-D stack of matrices with contiguous rows")
+    ld = max(ld, cols, 1)
+    return t.data_ptr(), n, rows, cols, ld, max(group, ld * rows)
+
+
 def _scales(t, rows: int, cols: int, groups: int = 1) -> int:
     """Pointer of the packed scale bytes of `groups` rows x cols matrices."""
-    need = groups * gemm_scale_bytes(rows, cols)
-    if t.element_size() != 1 or not t.is_contiguous() or t.numel() < need:
+    need = groups * 512 * (-(-rows // 128) or 1) * (-(-cols // 512) or 1)  # gemm_scale_bytes
+    if t.element_size() != 1 or t.numel() < need or not t.is_contiguous():
         raise ValueError(f"scales are {need} contiguous bytes")
     return t.data_ptr()
 
 
-def _ints(t, n: int) -> int:
-    import torch
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"expected {n} contiguous int32")
+def _array(t, n: int, dtype: str) -> int:
+    """Pointer of at least n contiguous values ("int32" or "float32")."""
+    if t.dtype is not _array_types.get(dtype):
+        if not _array_types:
+            import torch
+            _array_types.update(int32=torch.int32, float32=torch.float32)
+            return _array(t, n, dtype)
+        raise ValueError(f"expected {dtype}")
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"expected {n} contiguous {dtype}")
     return t.data_ptr()
 
 
-def _floats(t, n: int) -> int:
-    import torch
-    if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"expected {n} contiguous float32")
-    return t.data_ptr()
-
-
-def _matrices(t):
-    """(pointer, ld, elements between matrices) of a 3-D stack of matrices with contiguous rows."""
-    if t.dim() != 3 or t.stride(2) != 1:
-        raise ValueError("expected a 3-D stack of matrices with contiguous rows")
-    ld = max(t.stride(1), t.shape[2], 1)
-    return t.data_ptr(), ld, max(t.stride(0), ld * t.shape[1])
+def _epilogue(act, slope):
+    return _PLAIN if act == GEMM_ACT_NONE else gemm_epilogue_t(act, slope)
 
 
 def pack_scales(scales):
@@ -403,6 +421,8 @@ class Plan:
 
     def __init__(self, device: int = 0):
         self.handle = gemm_plan_create(device)
+        self.device = device
+        self._current = None  # reads torch's current stream
 
     def close(self):
         if self.handle:
@@ -445,81 +465,79 @@ class Plan:
 
     # ------------------------------------------- block-scaled 8-bit products
 
-    def _stream(self, t, stream):
+    def _stream(self, stream):
+        """The given stream, or torch's current one on the plan's device."""
         if stream is not None:
             return stream
-        import torch
-        return torch.cuda.current_stream(t.device).cuda_stream
+        if self._current is None:
+            import torch
+            self._current = torch._C._cuda_getCurrentRawStream
+        return self._current(self.device)
 
     def quantize(self, X, Q=None, SQ=None, QT=None, SQT=None, *, block_rows=1, rowmap=None, map_div=1,
                  stream=None) -> int:
         """X (rows x cols) -> 8-bit Q and scales SQ, and/or its transpose QT and scales SQT
         (float8_e4m3fn or float8_e5m2; scales gemm_scale_bytes uint8).  With rowmap (int32) row r
         of the result is X's row rowmap[r] // map_div (negative: none)."""
-        x, ldx = _operand(X, False)
-        src_rows, cols = X.shape
+        x, src_rows, cols, ldx = _matrix(X)
         rows = src_rows if rowmap is None else rowmap.numel()
         q = sq = qt = sqt = None
         ldq = ldqt = 0
         if Q is not None:
-            q, ldq = _operand(Q, False)
+            q, r, c, ldq = _matrix(Q)
             sq = _scales(SQ, rows, cols)
-            if Q.shape != (rows, cols):
+            if (r, c) != (rows, cols):
                 raise ValueError("Q is rows x cols")
         if QT is not None:
-            qt, ldqt = _operand(QT, False)
+            qt, c, r, ldqt = _matrix(QT)
             sqt = _scales(SQT, cols, rows)
-            if QT.shape != (cols, rows) or (Q is not None and Q.dtype != QT.dtype):
+            if (r, c) != (rows, cols) or (Q is not None and Q.dtype != QT.dtype):
                 raise ValueError("QT is cols x rows, of Q's type")
         kind = Q if Q is not None else QT
         if kind is None:
             raise ValueError("neither Q nor QT")
-        return gemm_quantize(self.handle, rows, cols, x, ldx, _type_of(X), None if rowmap is None else _ints(rowmap, rows),
-                             map_div, src_rows, _type_of(kind), block_rows, q, ldq, sq, qt, ldqt, sqt,
-                             self._stream(X, stream))
+        return load().gemm_quantize(self.handle, rows, cols, x, ldx, _type_of(X),
+                                    None if rowmap is None else _array(rowmap, rows, "int32"), map_div, src_rows,
+                                    _type_of(kind), block_rows, q, ldq, sq, qt, ldqt, sqt, self._stream(stream))
 
     def run_scaled(self, A, SA, B, SB, D, *, alpha=1.0, beta=0.0, act=GEMM_ACT_NONE, slope=0.0, stream=None) -> int:
         """D <- act(alpha * A @ B^T + beta * D) on 8-bit A (M x K), B (N x K) with packed scales SA, SB."""
-        a, lda = _operand(A, False)
-        b, ldb = _operand(B, False)
-        d, ldd = _operand(D, False)
-        M, K = A.shape
-        N = B.shape[0]
-        if B.shape[1] != K or D.shape != (M, N):
+        a, M, K, lda = _matrix(A)
+        b, N, Kb, ldb = _matrix(B)
+        d, Md, Nd, ldd = _matrix(D)
+        if Kb != K or Md != M or Nd != N:
             raise ValueError("A is M x K, B is N x K and D is M x N")
-        return gemm_run_scaled(self.handle, M, N, K, a, lda, _scales(SA, M, K), _type_of(A), b, ldb, _scales(SB, N, K),
-                               _type_of(B), d, ldd, _type_of(D), alpha, beta, act, slope, self._stream(D, stream))
+        return load().gemm_run_scaled(self.handle, M, N, K, a, lda, _scales(SA, M, K), _type_of(A), b, ldb,
+                                      _scales(SB, N, K), _type_of(B), d, ldd, _type_of(D), alpha, beta,
+                                      _epilogue(act, slope), self._stream(stream))
 
     def run_grouped(self, A, SA, B, SB, D, starts, counts, *, alpha=1.0, beta=0.0, act=GEMM_ACT_NONE, slope=0.0,
                     stream=None) -> int:
         """Rows starts[e] .. starts[e] + counts[e] of A (rows x K) times B[e]^T (B groups x N x K, SB
         the groups' packed scales one after another) into the same rows of D (rows x N)."""
-        a, lda = _operand(A, False)
-        b, ldb, b_group = _matrices(B)
-        d, ldd = _operand(D, False)
-        rows, K = A.shape
-        groups, N = B.shape[:2]
-        if B.shape[2] != K or D.shape != (rows, N):
+        a, rows, K, lda = _matrix(A)
+        b, groups, N, Kb, ldb, b_group = _matrices(B)
+        d, rows_d, Nd, ldd = _matrix(D)
+        if Kb != K or rows_d != rows or Nd != N:
             raise ValueError("A is rows x K, B is groups x N x K and D is rows x N")
-        return gemm_run_grouped(self.handle, groups, rows, N, K, _ints(starts, groups), _ints(counts, groups), a, lda,
-                                _scales(SA, rows, K), _type_of(A), b, ldb, b_group, _scales(SB, N, K, groups),
-                                _type_of(B), d, ldd, _type_of(D), alpha, beta, act, slope, self._stream(D, stream))
+        return load().gemm_run_grouped(self.handle, groups, rows, N, K, _array(starts, groups, "int32"),
+                                       _array(counts, groups, "int32"), a, lda, _scales(SA, rows, K), _type_of(A), b,
+                                       ldb, b_group, _scales(SB, N, K, groups), _type_of(B), d, ldd, _type_of(D), alpha,
+                                       beta, _epilogue(act, slope), self._stream(stream))
 
     def run_grouped_k(self, A, SA, B, SB, D, starts, counts, *, alpha=1.0, beta=0.0, act=GEMM_ACT_NONE, slope=0.0,
                       stream=None) -> int:
         """D[e] <- act(alpha * A_e @ B_e^T + beta * D[e]), A_e and B_e columns starts[e] .. starts[e] + counts[e]
         of A (M x rows) and B (N x rows); D groups x M x N."""
-        a, lda = _operand(A, False)
-        b, ldb = _operand(B, False)
-        d, ldd, d_group = _matrices(D)
-        M, rows = A.shape
-        N = B.shape[0]
-        groups = D.shape[0]
-        if B.shape[1] != rows or D.shape[1:] != (M, N):
+        a, M, rows, lda = _matrix(A)
+        b, N, rows_b, ldb = _matrix(B)
+        d, groups, Md, Nd, ldd, d_group = _matrices(D)
+        if rows_b != rows or Md != M or Nd != N:
             raise ValueError("A is M x rows, B is N x rows and D is groups x M x N")
-        return gemm_run_grouped_k(self.handle, groups, M, N, rows, _ints(starts, groups), _ints(counts, groups), a, lda,
-                                  _scales(SA, M, rows), _type_of(A), b, ldb, _scales(SB, N, rows), _type_of(B), d, ldd,
-                                  d_group, _type_of(D), alpha, beta, act, slope, self._stream(D, stream))
+        return load().gemm_run_grouped_k(self.handle, groups, M, N, rows, _array(starts, groups, "int32"),
+                                         _array(counts, groups, "int32"), a, lda, _scales(SA, M, rows), _type_of(A), b,
+                                         ldb, _scales(SB, N, rows), _type_of(B), d, ldd, d_group, _type_of(D), alpha,
+                                         beta, _epilogue(act, slope), self._stream(stream))
 
     # ----------------------------------------------------------- experts
 
@@ -527,58 +545,57 @@ class Plan:
               group_top=1, renormalize=False, scale=1.0, stream=None) -> int:
         """logits (tokens x experts) -> each token's chosen experts (indices, tokens x top_k int32)
         and their weights (tokens x top_k float32)."""
-        x, ldl = _operand(logits, False)
-        tokens, experts = logits.shape
-        if weights.shape != indices.shape or weights.dim() != 2 or weights.shape[0] != tokens:
+        x, tokens, experts, ldl = _matrix(logits)
+        n, k = weights.shape
+        if n != tokens or indices.shape != weights.shape:
             raise ValueError("weights and indices are tokens x top_k")
-        k = weights.shape[1]
-        return gemm_route(self.handle, tokens, experts, x, ldl, _type_of(logits),
-                          None if bias is None else _floats(bias, experts),
-                          gemm_route_t(score, k, groups, top_groups, group_top, int(renormalize), scale),
-                          _floats(weights, tokens * k), _ints(indices, tokens * k), self._stream(logits, stream))
+        return load().gemm_route(self.handle, tokens, experts, x, ldl, _type_of(logits),
+                                 None if bias is None else _array(bias, experts, "float32"),
+                                 gemm_route_t(score, k, groups, top_groups, group_top, int(renormalize), scale),
+                                 _array(weights, tokens * k, "float32"), _array(indices, tokens * k, "int32"),
+                                 self._stream(stream))
 
     def route_backward(self, logits, indices, dweights, dlogits, *, score=GEMM_SCORE_SOFTMAX, renormalize=False,
                        scale=1.0, stream=None) -> int:
         """The gradient of the logits (dlogits) from the weights' (dweights) and the choice (indices)."""
-        x, ldl = _operand(logits, False)
-        d, lddl = _operand(dlogits, False)
-        tokens, experts = logits.shape
-        if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or indices.shape != dweights.shape:
+        x, tokens, experts, ldl = _matrix(logits)
+        d, nt, ne, lddl = _matrix(dlogits)
+        n, k = indices.shape
+        if (nt, ne) != (tokens, experts) or n != tokens or dlogits.dtype != logits.dtype or indices.shape != dweights.shape:
             raise ValueError("dlogits is like logits, dweights like indices")
-        k = indices.shape[1]
-        return gemm_route_backward(self.handle, tokens, experts, x, ldl, _type_of(logits),
-                                   gemm_route_t(score, k, 1, 1, 1, int(renormalize), scale), _ints(indices, tokens * k),
-                                   _floats(dweights, tokens * k), d, lddl, self._stream(logits, stream))
+        return load().gemm_route_backward(self.handle, tokens, experts, x, ldl, _type_of(logits),
+                                          gemm_route_t(score, k, 1, 1, 1, int(renormalize), scale),
+                                          _array(indices, tokens * k, "int32"), _array(dweights, tokens * k, "float32"), d,
+                                          lddl, self._stream(stream))
 
     def route_map(self, indices, experts, starts, counts, pos, rowmap, *, stream=None) -> int:
         """The order of the slots of indices (tokens x top_k) by expert; rowmap has gemm_route_rows entries."""
         tokens, k = indices.shape
-        return gemm_route_map(self.handle, tokens, k, experts, _ints(indices, tokens * k), _ints(starts, experts),
-                              _ints(counts, experts), _ints(pos, tokens * k), _ints(rowmap, 0), rowmap.numel(),
-                              self._stream(indices, stream))
+        return load().gemm_route_map(self.handle, tokens, k, experts, _array(indices, tokens * k, "int32"),
+                                     _array(starts, experts, "int32"), _array(counts, experts, "int32"),
+                                     _array(pos, tokens * k, "int32"), _array(rowmap, 0, "int32"), rowmap.numel(),
+                                     self._stream(stream))
 
     def combine(self, Y, pos, weights, out, *, stream=None) -> int:
         """out[t] <- sum_j weights[t, j] * Y[pos[t, j]]."""
-        y, ldy = _operand(Y, False)
-        o, ldo = _operand(out, False)
+        y, rows, cols, ldy = _matrix(Y)
+        o, nt, nc, ldo = _matrix(out)
         tokens, k = pos.shape
-        rows, cols = Y.shape
-        if out.shape != (tokens, cols):
+        if nt != tokens or nc != cols:
             raise ValueError("out is tokens x cols")
-        return gemm_combine(self.handle, tokens, k, cols, rows, y, ldy, _type_of(Y), _ints(pos, tokens * k),
-                            _floats(weights, tokens * k), o, ldo, _type_of(out), self._stream(out, stream))
+        return load().gemm_combine(self.handle, tokens, k, cols, rows, y, ldy, _type_of(Y), _array(pos, tokens * k, "int32"),
+                                   _array(weights, tokens * k, "float32"), o, ldo, _type_of(out), self._stream(stream))
 
     def combine_backward(self, dout, Y, pos, weights, dY, dweights, *, rowmap=None, stream=None) -> int:
         """dY[pos[t, j]] <- weights[t, j] * dout[t], dweights[t, j] <- <dout[t], Y[pos[t, j]]>; with rowmap the
         rows of dY that hold no slot are cleared."""
-        y, ldy = _operand(Y, False)
-        g, ldo = _operand(dout, False)
-        d, lddy = _operand(dY, False)
+        y, rows, cols, ldy = _matrix(Y)
+        g, nt, nc, ldo = _matrix(dout)
+        d, nr, ncd, lddy = _matrix(dY)
         tokens, k = pos.shape
-        rows, cols = Y.shape
-        if dout.shape != (tokens, cols) or dY.shape != Y.shape or dY.dtype != Y.dtype:
+        if (nt, nc) != (tokens, cols) or (nr, ncd) != (rows, cols) or dY.dtype != Y.dtype:
             raise ValueError("dout is tokens x cols, dY like Y")
-        return gemm_combine_backward(self.handle, tokens, k, cols, rows, g, ldo, _type_of(dout), y, ldy, _type_of(Y),
-                                     _ints(pos, tokens * k), _floats(weights, tokens * k),
-                                     None if rowmap is None else _ints(rowmap, rows), d, lddy,
-                                     _floats(dweights, tokens * k), self._stream(Y, stream))
+        return load().gemm_combine_backward(self.handle, tokens, k, cols, rows, g, ldo, _type_of(dout), y, ldy, _type_of(Y),
+                                            _array(pos, tokens * k, "int32"), _array(weights, tokens * k, "float32"),
+                                            None if rowmap is None else _array(rowmap, rows, "int32"), d, lddy,
+                                            _array(dweights, tokens * k, "float32"), self._stream(stream))
