@@ -418,6 +418,7 @@ struct RouteArgs {
   const float* dweights;
   void* dlogits;
   int64_t lddl;
+  int wide, wide_out;  // rows of the logits, of dlogits on 16-byte boundaries
   int pdl;
   DG_DEBUG_FIELD
 };
@@ -436,10 +437,13 @@ struct RouteMapArgs {
   int* rowmap;
   int rows;  // length of rowmap
   int wide;  // rowmap on a 16-byte boundary
+  int* block_counts;  // route_map_workspace bytes
+  int run, warps;     // slots of a CTA, warps that share them (set by the launcher)
   int pdl;
   DG_DEBUG_FIELD
 };
-cudaError_t launch_route_map(const RouteMapArgs& a, cudaStream_t s);
+size_t route_map_workspace(int64_t slots, int64_t experts);
+cudaError_t launch_route_map(RouteMapArgs a, cudaStream_t s);
 
 // ----------------------------------------------------------------- combine
 

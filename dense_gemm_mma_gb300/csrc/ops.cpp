@@ -350,6 +350,9 @@ gemm_status_t checked_run(gemm_plan_t plan, const Product& x, void* stream) {
   return st != GEMM_OK ? st : run_product(plan, x, static_cast<cudaStream_t>(stream));
 }
 
+// Rows of `ld` elements of es bytes from p allow 16-byte accesses where columns do.
+bool rows_wide(const void* p, int64_t ld, int64_t es) { return aligned(p, 16) && (ld * es) % 16 == 0; }
+
 gemm_status_t check_route(int64_t tokens, int64_t experts, const void* logits, int64_t ldl, gemm_type_t type,
                           const gemm_route_t& r) {
   if (tokens < 0 || experts < 1 || !is_float_type(type)) return GEMM_ERR_INVALID_ARG;
@@ -380,6 +383,7 @@ RouteArgs route_args(gemm_plan_t plan, int64_t tokens, int64_t experts, const vo
   a.group_top = r.group_top;
   a.renormalize = r.renormalize;
   a.scale = r.scale;
+  a.wide = rows_wide(logits, ldl, type_bytes(type));
   a.pdl = plan->pdl;
   return a;
 }
@@ -400,9 +404,6 @@ gemm_status_t check_combine(int64_t tokens, int64_t top_k, int64_t cols, int64_t
     return GEMM_ERR_ALIGNMENT;
   return GEMM_OK;
 }
-
-// Rows of `ld` elements of es bytes from p allow 16-byte accesses at multiples of eight columns.
-bool rows_wide(const void* p, int64_t ld, int64_t es) { return aligned(p, 16) && (ld * es) % 16 == 0; }
 
 }  // namespace
 
@@ -567,6 +568,7 @@ gemm_status_t gemm_route_backward(gemm_plan_t plan, int64_t tokens, int64_t expe
   a.dweights = dweights;
   a.dlogits = dlogits;
   a.lddl = lddl;
+  a.wide_out = rows_wide(dlogits, lddl, type_bytes(l_type));
 #ifdef DG_DEBUG
   a.dbg = Spans(plan->err).matrix(logits, tokens, experts, ldl, type_bytes(l_type)).bytes(indices, tokens * route.top_k * 4)
               .bytes(dweights, tokens * route.top_k * 4).out_matrix(dlogits, tokens, experts, lddl, type_bytes(l_type)).s;
@@ -592,6 +594,11 @@ gemm_status_t gemm_route_map(gemm_plan_t plan, int64_t tokens, int64_t top_k, in
   if (!aligned(indices, 4) || !aligned(starts, 4) || !aligned(counts, 4) || !aligned(pos, 4) || !aligned(rowmap, 4))
     return GEMM_ERR_ALIGNMENT;
   DeviceGuard guard(plan->device);
+  const size_t ws = route_map_workspace(tokens * top_k, experts);
+  if (ws > 0) {
+    const gemm_status_t st = ensure_ws(plan, ws, static_cast<cudaStream_t>(stream));
+    if (st != GEMM_OK) return st;
+  }
   RouteMapArgs a{};
   a.indices = indices;
   a.slots = int(tokens * top_k);
@@ -602,10 +609,11 @@ gemm_status_t gemm_route_map(gemm_plan_t plan, int64_t tokens, int64_t top_k, in
   a.rowmap = rowmap;
   a.rows = int(rows);
   a.wide = aligned(rowmap, 16);
+  a.block_counts = static_cast<int*>(plan->ws);
   a.pdl = plan->pdl;
 #ifdef DG_DEBUG
   a.dbg = Spans(plan->err).bytes(indices, tokens * top_k * 4).bytes(starts, experts * 4).bytes(counts, experts * 4)
-              .bytes(pos, tokens * top_k * 4).out_matrix(rowmap, 1, rows, 0, 4).s;
+              .bytes(pos, tokens * top_k * 4).bytes(plan->ws, int64_t(ws)).out_matrix(rowmap, 1, rows, 0, 4).s;
 #endif
   return launched(launch_route_map(a, static_cast<cudaStream_t>(stream)));
 }

@@ -61,10 +61,16 @@ constexpr uint32_t kInf = 0x7f800000u;
 
 template <typename T>
 struct Peak {  // 16-bit types: columns 0-1 and 2-3 of a lane
+  using Pair = typename std::conditional<std::is_same<T, __nv_bfloat16>::value, __nv_bfloat162, __half2>::type;
   uint32_t a = 0, b = 0;
+  // (NaN wins and stays: its bits are past kInf)
+  static __device__ __forceinline__ uint32_t most(uint32_t x, uint32_t y) {
+    const Pair m = __hmax2_nan(*reinterpret_cast<const Pair*>(&x), *reinterpret_cast<const Pair*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
   __device__ __forceinline__ void take(const Four<T>& f) {
-    a = __vmaxu2(a, f.w.x & 0x7fff7fffu);
-    b = __vmaxu2(b, f.w.y & 0x7fff7fffu);
+    a = most(a, f.w.x & 0x7fff7fffu);
+    b = most(b, f.w.y & 0x7fff7fffu);
   }
   static __device__ __forceinline__ uint32_t bits(uint32_t h) {
     if constexpr (std::is_same<T, __nv_bfloat16>::value) return h << 16;
@@ -76,7 +82,7 @@ struct Peak {  // 16-bit types: columns 0-1 and 2-3 of a lane
     return bits(j & 1 ? r >> 16 : r & 0xffffu);
   }
   __device__ __forceinline__ uint32_t row() const {
-    const uint32_t m = __vmaxu2(a, b);
+    const uint32_t m = most(a, b);
     return bits(max(m >> 16, m & 0xffffu));
   }
 };
@@ -214,25 +220,42 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
   }
 }
 
-// Both orientations (or 128 x 128 scales): a CTA takes one 128 x 128 tile, 16 rows a
+// Both orientations (or 128 x 128 scales): a CTA takes one 128 x 128 tile, kTileRows rows a
 // warp and 4 columns a lane, held in registers.  Row maxima are warp reductions, each
-// row's scale worked out by one lane; column maxima meet in shared memory.  A thread's 16
-// rows of a column are 16 consecutive bytes of the transposed matrix: they are turned
-// round in a swizzled shared-memory tile and leave as 128-byte rows.
+// row's scale worked out by one lane; column maxima meet in shared memory.  A thread's 8
+// rows of a column are 8 consecutive bytes of the transposed matrix: they are turned
+// round in a swizzled shared-memory tile and leave as 128-byte rows.  (16 rows a warp
+// spilled at three CTAs an SM and left too few warps at two: 47.0 us for 8192 x 4096 bf16.)
+constexpr int kTileRows = 8;
+constexpr int kTileWarps = 128 / kTileRows;
+
+// kTileRows rows' codes (lane i: inverse scale of row i), then the columns' of a lane.
+template <bool E5M2, bool CAREFUL, typename T>
+__device__ __forceinline__ void row_codes(uint32_t (&c)[kTileRows], const Four<T> (&v)[kTileRows], float inv_mine) {
+#pragma unroll
+  for (int i = 0; i < kTileRows; ++i)
+    c[i] = codes4<E5M2, CAREFUL>(v[i].at(0), v[i].at(1), v[i].at(2), v[i].at(3), __shfl_sync(kAll, inv_mine, i));
+}
+template <bool E5M2, bool CAREFUL, typename T>
+__device__ __forceinline__ uint2 column_codes(const Four<T> (&v)[kTileRows], int j, float inv) {
+  return make_uint2(codes4<E5M2, CAREFUL>(v[0].at(j), v[1].at(j), v[2].at(j), v[3].at(j), inv),
+                    codes4<E5M2, CAREFUL>(v[4].at(j), v[5].at(j), v[6].at(j), v[7].at(j), inv));
+}
+
 template <typename T, bool E5M2, bool VEC>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quantize_tile_kernel(const QuantArgs a) {
-  __shared__ uint32_t col_max[8][128];
-  __shared__ uint4 turn[128 * 8];  // [column][16-byte piece of rows ^ (column / 4 % 8)]
+__global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 1 : 2) quantize_tile_kernel(const QuantArgs a) {
+  __shared__ uint32_t col_max[kTileWarps][128];
+  __shared__ uint4 turn[128 * 8];  // [column][8-byte piece of rows ^ (column / 4 % 16)]
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cb = blockIdx.x, rb = blockIdx.y;  // past the matrix: only scale bytes, zero
-  const int row0 = rb * 128 + warp * 16, col = cb * 128 + 4 * lane;
-  Four<T> v[16];
+  const int row0 = rb * 128 + warp * kTileRows, col = cb * 128 + 4 * lane;
+  Four<T> v[kTileRows];
   uint32_t live = 0;  // rows that exist
   {
-    int src[16];
+    int src[kTileRows];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kTileRows; ++i) {
       src[i] = source_row(a, row0 + i);
       live |= uint32_t(src[i] >= 0) << i;
     }
@@ -240,7 +263,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quantize_tile_ker
   }
   Peak<T> peak;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) peak.take(v[i]);
+  for (int i = 0; i < kTileRows; ++i) peak.take(v[i]);
   uint32_t cm[4] = {peak.column(0), peak.column(1), peak.column(2), peak.column(3)};
   // infinities or NaN anywhere in the tile: maxima over what is finite, careful conversions
   const bool careful = __syncthreads_or(max(max(cm[0], cm[1]), max(cm[2], cm[3])) >= kInf);
@@ -249,23 +272,23 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quantize_tile_ker
     for (int j = 0; j < 4; ++j) {
       cm[j] = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) cm[j] = max(cm[j], finite_bits(v[i].at(j)));
+      for (int i = 0; i < kTileRows; ++i) cm[j] = max(cm[j], finite_bits(v[i].at(j)));
     }
   }
   *reinterpret_cast<uint4*>(&col_max[warp][4 * lane]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
+  for (int w = 0; w < kTileWarps; ++w) {
     const uint4 o = *reinterpret_cast<const uint4*>(&col_max[w][4 * lane]);
     cm[0] = max(cm[0], o.x), cm[1] = max(cm[1], o.y), cm[2] = max(cm[2], o.z), cm[3] = max(cm[3], o.w);
   }
   uint32_t tile = 0;  // scale byte of the whole tile
   if (a.block_rows > 1) tile = scale_byte<E5M2>(__reduce_max_sync(kAll, max(max(cm[0], cm[1]), max(cm[2], cm[3]))));
   if (a.q) {
-    uint32_t mine = 0;  // lane i: scale byte of row i
+    uint32_t mine = tile;  // lane i: scale byte of row i
     if (a.block_rows == 1) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < kTileRows; ++i) {
         Peak<T> row;
         row.take(v[i]);
         uint32_t m = row.row();
@@ -275,18 +298,26 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quantize_tile_ker
         if (lane == i) mine = m;
       }
       mine = scale_byte<E5M2>(mine);
-    } else {
-      mine = tile;
     }
-    const float inv_mine = inverse_scale(mine);
+    uint32_t c[kTileRows];
+    if (careful)
+      row_codes<E5M2, true>(c, v, inverse_scale(mine));
+    else
+      row_codes<E5M2, false>(c, v, inverse_scale(mine));
+    uint8_t* const dst = a.q + int64_t(row0) * a.ldq + col;
+    if (col + 4 <= a.cols) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float inv = __shfl_sync(kAll, inv_mine, i);
-      const uint32_t c = careful ? codes4<E5M2, true>(v[i].at(0), v[i].at(1), v[i].at(2), v[i].at(3), inv)
-                                 : codes4<E5M2, false>(v[i].at(0), v[i].at(1), v[i].at(2), v[i].at(3), inv);
-      if ((live >> i) & 1u) store4(a, a.q + int64_t(row0 + i) * a.ldq + col, c, a.cols - col);
+      for (int i = 0; i < kTileRows; ++i)
+        if (((live >> i) & 1u) && DG_IN(a.dbg, dst + i * a.ldq, 4, DBG_QUANTIZE))
+          *reinterpret_cast<uint32_t*>(dst + i * a.ldq) = c[i];
+    } else if (col < a.cols) {
+      for (int j = 0; j < a.cols - col; ++j)
+#pragma unroll
+        for (int i = 0; i < kTileRows; ++i)
+          if (((live >> i) & 1u) && DG_IN(a.dbg, dst + i * a.ldq + j, 1, DBG_QUANTIZE))
+            dst[i * a.ldq + j] = uint8_t(c[i] >> (8 * j));
     }
-    if (lane < 16 && row0 < a.rows_padded) {
+    if (lane < kTileRows && row0 < a.rows_padded) {
       uint8_t* const s = a.sq + scale_at(row0 + lane, cb, a.q_groups);
       if (DG_IN(a.dbg, s, 1, DBG_QUANTIZE)) *s = uint8_t(row0 + lane < a.rows || a.block_rows == 1 ? mine : 0u);
     }
@@ -297,12 +328,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quantize_tile_ker
     for (int j = 0; j < 4; ++j) {
       bytes[j] = a.block_rows == 1 ? scale_byte<E5M2>(cm[j]) : tile;
       const float inv = inverse_scale(bytes[j]);
-      uint32_t w[4];
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
-        w[h] = careful ? codes4<E5M2, true>(v[4 * h].at(j), v[4 * h + 1].at(j), v[4 * h + 2].at(j), v[4 * h + 3].at(j), inv)
-                       : codes4<E5M2, false>(v[4 * h].at(j), v[4 * h + 1].at(j), v[4 * h + 2].at(j), v[4 * h + 3].at(j), inv);
-      turn[(4 * lane + j) * 8 + (warp ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<uint2*>(turn)[(4 * lane + j) * 16 + (warp ^ (lane & 15))] =
+          careful ? column_codes<E5M2, true>(v, j, inv) : column_codes<E5M2, false>(v, j, inv);
     }
     if (warp == 0) {
 #pragma unroll
@@ -315,11 +342,13 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) quantize_tile_ker
     }
     __syncthreads();
 #pragma unroll
-    for (int pass = 0; pass < 4; ++pass) {
-      const int c = pass * 32 + int(threadIdx.x >> 3), piece = threadIdx.x & 7;
+    for (int pass = 0; pass < 128 * 8 / (32 * kTileWarps); ++pass) {
+      const int c = pass * 4 * kTileWarps + int(threadIdx.x >> 3), piece = threadIdx.x & 7;  // 16 bytes: two pieces of 8
       const int r = rb * 128 + piece * 16;
       if (cb * 128 + c >= a.cols || r >= a.rows) continue;
-      const uint4 w = turn[c * 8 + (piece ^ ((c >> 2) & 7))];
+      const int f = (c >> 2) & 15;
+      uint4 w = turn[c * 8 + (piece ^ (f >> 1))];
+      if (f & 1) w = make_uint4(w.z, w.w, w.x, w.y);
       uint8_t* const dst = a.qt + int64_t(cb * 128 + c) * a.ldqt + r;
       const int n = min(16, a.rows - r);
       if (!DG_IN(a.dbg, dst, n, DBG_QUANTIZE)) continue;
@@ -344,8 +373,8 @@ cudaError_t launch(const QuantArgs& a, cudaStream_t s) {
   // blocks past the matrix write the zero bytes that pad the scales to whole words
   const int col_blocks = a.q ? a.q_groups * 4 : (a.cols + 127) / 128;
   const int row_blocks = a.qt ? a.qt_groups * 4 : (a.rows + 127) / 128;
-  return launch_k(quantize_tile_kernel<T, E5M2, VEC>, dim3(unsigned(col_blocks), unsigned(row_blocks)), dim3(256), 0, s,
-                  a.pdl, a);
+  return launch_k(quantize_tile_kernel<T, E5M2, VEC>, dim3(unsigned(col_blocks), unsigned(row_blocks)),
+                  dim3(32 * kTileWarps), 0, s, a.pdl, a);
 }
 
 template <typename T>

@@ -6,12 +6,13 @@
 // that counts (no bias, groups ranked by their best), else s_i + bias_i.  Weights of the chosen: s_i, over their
 // sum if renormalised, times `scale`.
 //
-// What bounds it is latency, then reading the logits: one warp a token, its experts in
-// registers (expert 32 i + lane in register i), each choice two warp reductions on
-// order-preserving integer keys (largest key, then the lowest index that has it).
-// Sums and products are written with the rounding intrinsics, so that no compiler
-// contraction moves a key by a bit: the choice depends on it.
-#include <cooperative_groups.h>
+// What bounds it is latency for few tokens, then issuing instructions (reading the
+// logits is a few microseconds at most): one warp a token, a run of consecutive experts per
+// lane in registers, sorted by order-preserving integer keys.  A choice is then one warp
+// maximum over the lanes' first keys: the lowest lane that has it holds the lowest expert that has it, and
+// moves on to its next.  Scores are worked out only where something needs them.
+// Sums and products that make a key are written with the rounding intrinsics, so that no
+// compiler contraction moves it by a bit: the choice depends on it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -40,11 +41,23 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-__device__ __forceinline__ float load_logit(const void* p, int kind, int64_t i) {
-  if (kind == OUT_F32) return static_cast<const float*>(p)[i];
-  if (kind == OUT_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
+__device__ __forceinline__ float half_at(uint32_t pair, int i, int kind) {
+  if (kind == OUT_BF16) return __uint_as_float(i & 1 ? pair & 0xffff0000u : pair << 16);
+  const uint16_t h = uint16_t(i & 1 ? pair >> 16 : pair);
+  return __half2float(*reinterpret_cast<const __half*>(&h));
 }
+
+__device__ __forceinline__ uint32_t half_pair(float a, float b, int kind) {
+  if (kind == OUT_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// NaN read as minus infinity.
+__device__ __forceinline__ float masked(float f) { return f == f ? f : kNegInf; }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -52,8 +65,49 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// What turns a token's logits (NaN read as minus infinity) into scores.  A masked
-// expert (minus infinity) scores 0; a row with nothing else scores 0 throughout.
+// Logit e of token t; what is not there is minus infinity.
+__device__ __forceinline__ float logit(const RouteArgs& a, int t, int e) {
+  if (e < 0 || e >= a.experts) return kNegInf;
+  const int es = a.kind == OUT_F32 ? 4 : 2;
+  const char* const p = static_cast<const char*>(a.logits) + (int64_t(t) * a.ldl + e) * es;
+  if (!DG_IN(a.dbg, p, es, DBG_ROUTE)) return kNegInf;
+  if (es == 4) return masked(*reinterpret_cast<const float*>(p));
+  return masked(half_at(*reinterpret_cast<const uint16_t*>(p), 0, a.kind));
+}
+
+// A lane's experts: lane * run .. lane * run + run, run <= P.  Whole runs of a row on
+// 16-byte boundaries (`wide`) are loaded 8 or 16 bytes at a time.
+template <int P>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int t, int first, int run, bool wide, float (&x)[P]) {
+  if constexpr (P >= 4) {
+    if (wide && run == P && first + P <= a.experts) {
+      const int es = a.kind == OUT_F32 ? 4 : 2;
+      const char* const p = static_cast<const char*>(a.logits) + (int64_t(t) * a.ldl + first) * es;
+      if (DG_IN(a.dbg, p, P * es, DBG_ROUTE)) {
+        if (a.kind == OUT_F32) {
+#pragma unroll
+          for (int i = 0; i < P; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
+            x[i] = masked(v.x), x[i + 1] = masked(v.y), x[i + 2] = masked(v.z), x[i + 3] = masked(v.w);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < P; i += 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p + 2 * i);
+            x[i] = masked(half_at(v.x, 0, a.kind)), x[i + 1] = masked(half_at(v.x, 1, a.kind));
+            x[i + 2] = masked(half_at(v.y, 0, a.kind)), x[i + 3] = masked(half_at(v.y, 1, a.kind));
+          }
+        }
+        return;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) x[i] = i < run ? logit(a, t, first + i) : kNegInf;
+}
+
+// What turns a token's logits into scores.  A masked expert (minus infinity) scores 0;
+// a row with nothing else scores 0 throughout.
 struct Scorer {
   int sigmoid;
   float top, sum;  // softmax: largest logit, sum of exp(x - top)
@@ -76,23 +130,6 @@ struct Scorer {
   }
 };
 
-// Logit e of token t, NaN and what is not there as minus infinity.
-__device__ __forceinline__ float logit(const RouteArgs& a, int t, int e) {
-  if (e < 0 || e >= a.experts) return kNegInf;
-  const int64_t at = int64_t(t) * a.ldl + e;
-  if (!DG_IN(a.dbg, static_cast<const char*>(a.logits) + at * (a.kind == OUT_F32 ? 4 : 2), a.kind == OUT_F32 ? 4 : 2,
-             DBG_ROUTE))
-    return kNegInf;
-  const float f = load_logit(a.logits, a.kind, at);
-  return f == f ? f : kNegInf;
-}
-
-template <int P>
-__device__ __forceinline__ void load_logits(const RouteArgs& a, int t, int lane, float (&x)[P]) {
-#pragma unroll
-  for (int i = 0; i < P; ++i) x[i] = logit(a, t, 32 * i + lane);
-}
-
 // Sorts a lane's keys, largest first (an odd-even network of P rounds); ex[i] is the expert of
 // key[i].  Equal keys keep the lower expert first: only a strictly larger key moves up.
 template <int P>
@@ -109,18 +146,13 @@ __device__ __forceinline__ void sort_lane(uint32_t (&key)[P], int (&ex)[P]) {
     }
 }
 
-// The warp's best expert, whose lane then moves on to its next one: the largest key, and
-// among equal ones the lowest expert (lanes that have it are compared only if there are several).
+// The warp's best expert; its lane moves on to its next one.
 template <int P>
 __device__ __forceinline__ int take_best(uint32_t (&key)[P], int (&ex)[P], int lane) {
   const uint32_t best = __reduce_max_sync(kAll, key[0]);
-  const uint32_t who = __ballot_sync(kAll, key[0] == best);
-  int expert;
-  if (who & (who - 1))
-    expert = int(__reduce_min_sync(kAll, key[0] == best ? uint32_t(ex[0]) : 0xffffffffu));
-  else
-    expert = __shfl_sync(kAll, ex[0], __ffs(who) - 1);
-  if (lane == (expert & 31)) {
+  const int owner = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
+  const int expert = __shfl_sync(kAll, ex[0], owner);
+  if (lane == owner) {
 #pragma unroll
     for (int i = 0; i + 1 < P; ++i) key[i] = key[i + 1], ex[i] = ex[i + 1];
     key[P - 1] = kNone;
@@ -128,23 +160,21 @@ __device__ __forceinline__ int take_best(uint32_t (&key)[P], int (&ex)[P], int l
   return expert;
 }
 
-// Two largest keys among the experts of group g.
-template <int P>
-__device__ __forceinline__ void group_best(const uint32_t (&key)[P], int lane, int per, int g, uint32_t* first,
-                                           uint32_t* second) {
-  uint32_t b1 = kNone, b2 = kNone;  // of this lane
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int e = 32 * i + lane;
-    if (e >= g * per && e < (g + 1) * per) {
-      b2 = max(b2, min(b1, key[i]));
-      b1 = max(b1, key[i]);
-    }
+__device__ __forceinline__ uint32_t group_key(const RouteArgs& a, uint32_t best, uint32_t second) {
+  return a.group_top == 2 && second != kNone ? order_key(__fadd_rn(key_value(best), key_value(second))) : best;
+}
+
+// The top_groups groups of the largest keys, ties to the lower group: bit g of the result.
+// Group g's key is `mine` in lane g * every, and kNone elsewhere.
+__device__ __forceinline__ uint32_t choose_groups(const RouteArgs& a, uint32_t mine, int every, int lane) {
+  uint32_t chosen = 0;
+  for (int i = 0; i < a.top_groups; ++i) {
+    const uint32_t best = __reduce_max_sync(kAll, mine);
+    const int owner = __ffs(__ballot_sync(kAll, mine == best)) - 1;
+    chosen |= 1u << (owner / every);
+    if (lane == owner) mine = kNone;
   }
-  *first = __reduce_max_sync(kAll, b1);
-  const uint32_t owner = __ballot_sync(kAll, b1 == *first);
-  // the best may be there more than once: only one lane gives its own up
-  *second = __reduce_max_sync(kAll, lane == __ffs(owner) - 1 ? b2 : b1);
+  return chosen;
 }
 
 template <int P>
@@ -153,51 +183,65 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
   const int lane = threadIdx.x & 31;
   const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (t >= a.tokens) return;
+  const int run = (a.experts + 31) / 32, first = lane * run;
   float x[P];
-  load_logits(a, t, lane, x);
+  load_logits(a, t, first, run, a.wide, x);
   const Scorer scorer(a, x);
   uint32_t key[P];
+  int ex[P];
   const bool by_logit = a.bias == nullptr && a.group_top == 1;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int e = 32 * i + lane;
+    const int e = first + i;
+    const bool there = i < run && e < a.experts;
     float k = x[i];
     if (!by_logit && k != kNegInf) {  // a masked expert stays minus infinity, whatever its bias
       k = scorer.score(k);
-      if (e < a.experts && a.bias && DG_IN(a.dbg, a.bias + e, 4, DBG_ROUTE)) k = __fadd_rn(k, __ldg(a.bias + e));
+      if (there && a.bias && DG_IN(a.dbg, a.bias + e, 4, DBG_ROUTE)) k = __fadd_rn(k, __ldg(a.bias + e));
     }
-    key[i] = e < a.experts ? order_key(k) : kNone;
+    key[i] = there ? order_key(k) : kNone;
+    ex[i] = e;
   }
-  if (a.groups > 1) {
-    // Lane g holds group g's key; lanes are ranked, ties to the lower group.
+  // Groups that are whole lanes (a power of two of them, every lane full): their best keys
+  // meet in a few exchanges.  Others: one pair of warp maxima each.
+  const bool by_lanes = a.experts % 32 == 0 && 32 % a.groups == 0;
+  if (a.groups > 1 && !by_lanes) {
     const int per = a.experts / a.groups;
     uint32_t mine = kNone;
     for (int g = 0; g < a.groups; ++g) {
-      uint32_t b1, b2;
-      group_best(key, lane, per, g, &b1, &b2);
-      uint32_t k = b1;
-      if (a.group_top == 2 && b2 != kNone) k = order_key(__fadd_rn(key_value(b1), key_value(b2)));
-      if (lane == g) mine = k;
-    }
-    uint32_t chosen = 0;  // bit g: group g is in
-    for (int i = 0; i < a.top_groups; ++i) {
-      const uint32_t best = __reduce_max_sync(kAll, mine);
-      const uint32_t who = __ballot_sync(kAll, mine == best && lane < a.groups && !((chosen >> lane) & 1u));
-      const int g = __ffs(who) - 1;
-      if (g < 0) break;
-      chosen |= 1u << g;
-      if (lane == g) mine = kNone;
-    }
+      uint32_t b1 = kNone, b2 = kNone;  // of this lane
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int e = 32 * i + lane;
-      if (e < a.experts && !((chosen >> (e / per)) & 1u)) key[i] = kOutside;
+      for (int i = 0; i < P; ++i)
+        if (ex[i] >= g * per && ex[i] < (g + 1) * per) {
+          b2 = max(b2, min(b1, key[i]));
+          b1 = max(b1, key[i]);
+        }
+      const uint32_t best = __reduce_max_sync(kAll, b1);
+      // the best may be there more than once: only one lane gives its own up
+      const int owner = __ffs(__ballot_sync(kAll, b1 == best)) - 1;
+      const uint32_t second = __reduce_max_sync(kAll, lane == owner ? b2 : b1);
+      if (lane == g) mine = group_key(a, best, second);
     }
+    const uint32_t chosen = choose_groups(a, mine, 1, lane);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (key[i] != kNone && !((chosen >> (ex[i] / per)) & 1u)) key[i] = kOutside;
   }
-  int ex[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) ex[i] = 32 * i + lane;
   sort_lane(key, ex);
+  if (a.groups > 1 && by_lanes) {
+    const int every = 32 / a.groups;
+    uint32_t b1 = key[0], b2 = kNone;
+    if constexpr (P > 1) b2 = key[1];
+    for (int d = 1; d < every; d <<= 1) {
+      const uint32_t o1 = __shfl_xor_sync(kAll, b1, d), o2 = __shfl_xor_sync(kAll, b2, d);
+      b2 = max(min(b1, o1), max(b2, o2));
+      b1 = max(b1, o1);
+    }
+    const uint32_t chosen = choose_groups(a, lane % every == 0 ? group_key(a, b1, b2) : kNone, every, lane);
+    if (!((chosen >> (lane / every)) & 1u))
+#pragma unroll
+      for (int i = 0; i < P; ++i) key[i] = min(key[i], kOutside);
+  }
   int expert = -1;  // lane j: choice j
   for (int j = 0; j < a.top_k; ++j) {
     const int e = take_best(key, ex, lane);
@@ -207,8 +251,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
   const float mine = logit(a, t, expert);
   float score = mine == kNegInf ? 0.f : scorer.score(mine);
   if (a.renormalize) {
-    float sum = 0.f;
-    for (int j = 0; j < a.top_k; ++j) sum = __fadd_rn(sum, __shfl_sync(kAll, score, j));
+    const float sum = warp_sum(score);
     score = sum > 0.f ? __fdiv_rn(score, sum) : 0.f;
   }
   if (lane < a.top_k) {
@@ -228,8 +271,9 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
   const int lane = threadIdx.x & 31;
   const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (t >= a.tokens) return;
+  const int run = (a.experts + 31) / 32, first = lane * run;
   float x[P], ds[P];
-  load_logits(a, t, lane, x);
+  load_logits(a, t, first, run, a.wide, x);
   const Scorer scorer(a, x);
   int expert = -1;  // lane j: choice j; an index outside the experts takes no part
   float dw = 0.f;
@@ -247,37 +291,49 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
     const float dot = warp_sum(dw * sj);
     dsj = sum > 0.f && expert >= 0 ? a.scale * (dw - dot / sum) / sum : 0.f;
   }
-  const float through = warp_sum(dsj * sj);
+  const float through = a.sigmoid ? 0.f : warp_sum(dsj * sj);
 #pragma unroll
   for (int i = 0; i < P; ++i) ds[i] = 0.f;
   for (int j = 0; j < a.top_k; ++j) {
-    const int e = __shfl_sync(kAll, expert, j);
+    const int at = __shfl_sync(kAll, expert, j) - first;
     const float d = __shfl_sync(kAll, dsj, j);
 #pragma unroll
     for (int i = 0; i < P; ++i)
-      if (e == 32 * i + lane) ds[i] += d;
+      if (at == i && i < run) ds[i] += d;
   }
-  const int es = a.kind == OUT_F32 ? 4 : 2;
   const float over = scorer.sum > 0.f ? 1.f / scorer.sum : 0.f;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int e = 32 * i + lane;
-    if (e >= a.experts) continue;
-    float d = 0.f;
     if (!a.sigmoid) {
-      d = scorer.power(x[i]) * over * (ds[i] - through);
-    } else if (ds[i] != 0.f) {  // (experts that were not chosen)
+      ds[i] = scorer.power(x[i]) * over * (ds[i] - through);
+    } else if (ds[i] != 0.f) {  // (0 for experts that were not chosen)
       const float s = scorer.score(x[i]);
-      d = s * (1.f - s) * ds[i];
+      ds[i] = s * (1.f - s) * ds[i];
     }
-    char* const dst = static_cast<char*>(a.dlogits) + (int64_t(t) * a.lddl + e) * es;
-    if (!DG_IN(a.dbg, dst, es, DBG_ROUTE)) continue;
-    if (a.kind == OUT_F32)
-      *reinterpret_cast<float*>(dst) = d;
-    else if (a.kind == OUT_BF16)
-      *reinterpret_cast<__nv_bfloat16*>(dst) = __float2bfloat16_rn(d);
+  }
+  const int es = a.kind == OUT_F32 ? 4 : 2;
+  char* const dst = static_cast<char*>(a.dlogits) + (int64_t(t) * a.lddl + first) * es;
+  if constexpr (P >= 4) {
+    if (a.wide_out && run == P && first + P <= a.experts) {
+      if (!DG_IN(a.dbg, dst, P * es, DBG_ROUTE)) return;
+#pragma unroll
+      for (int i = 0; i < P; i += 4) {
+        if (a.kind == OUT_F32)
+          *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(ds[i], ds[i + 1], ds[i + 2], ds[i + 3]);
+        else
+          *reinterpret_cast<uint2*>(dst + 2 * i) =
+              make_uint2(half_pair(ds[i], ds[i + 1], a.kind), half_pair(ds[i + 2], ds[i + 3], a.kind));
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    if (i >= run || first + i >= a.experts || !DG_IN(a.dbg, dst + i * es, es, DBG_ROUTE)) continue;
+    if (es == 4)
+      *reinterpret_cast<float*>(dst + 4 * i) = ds[i];
     else
-      *reinterpret_cast<__half*>(dst) = __float2half_rn(d);
+      *reinterpret_cast<uint16_t*>(dst + 2 * i) = uint16_t(half_pair(ds[i], 0.f, a.kind));
   }
 }
 
@@ -293,60 +349,61 @@ cudaError_t by_experts(int experts, F f) {
 
 // ------------------------------------------------------------------- order
 //
-// A stable counting sort of the slots (token * top_k + choice) by expert, in one launch:
-// a cluster of up to eight CTAs, each with a run of the slots, each warp with a run of
-// its CTA's.  A warp counts its slots by expert (lanes with the same expert find each
-// other with match, one of them adds), CTAs read each other's totals through
-// distributed shared memory, and a second walk over the slots hands out rows:
-// start of the expert + slots of earlier CTAs, warps and lanes (the place within the warp is
-// kept in pos between the walks).  No atomics: the order is the slots' own.
+// A stable counting sort of the slots (token * top_k + choice) by expert.  Each CTA has a run of
+// the slots, each warp a run of its CTA's: a first walk counts them by expert
+// (lanes with the same expert find each other with match, one of them adds) and keeps each
+// slot's place among its CTA's slots of its expert in pos; a second walk turns places into rows: first row of
+// the expert + slots of earlier CTAs + place.  No atomics: the order is the slots' own.
+//   up to kMapRun slots: one launch, one CTA
+//   more: two launches, the CTAs' counts in between in plan workspace; every CTA
+//         of the second sums up the counts of those before it (and of all) by itself.
+// One launch on a cluster of eight CTAs took 36 us for 131072 slots of 128 experts, two launches of 64 CTAs 9 us.
 constexpr int kMapThreads = 1024;
-constexpr int kAhead = 8;  // loads of a warp's slots that are in flight together
+constexpr int kMapWarps = kMapThreads / 32;
+constexpr int kAhead = 4;  // loads of a warp's slots that are in flight together
 
-// ints: four tables over the experts (this CTA's slots, all slots, slots of earlier
-// CTAs, first row), then a count for each warp and expert
-__host__ __device__ constexpr int map_ints(int experts, int warps) { return experts * (4 + warps) + 1; }
+struct MapRun {  // a warp's slots [first, last), `first` a multiple of 32 from the CTA's start
+  int64_t first, last;
+};
 
-__global__ void __launch_bounds__(kMapThreads) route_map_kernel(const RouteMapArgs a, int ctas, int warps) {
-  namespace cg = cooperative_groups;
-  extern __shared__ int map_shared[];
-  wait_prior_grid();
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = ctas > 1 ? int(cluster.block_rank()) : 0;
-  const int E = a.experts;
-  int* const total = map_shared;
-  int* const all = total + E;
-  int* const before = all + E;
-  int* const start = before + E;     // E + 1: [E] is the end of the last expert's rows
-  int* const count = start + E + 1;  // [warps][E]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < E * warps; i += kMapThreads) count[i] = 0;
-  // every row holds no slot, until its slot says otherwise (after the barriers below)
-  for (int r = 4 * (rank * kMapThreads + int(threadIdx.x)); r < a.rows; r += 4 * ctas * kMapThreads) {
-    const int n = min(4, a.rows - r);
+__device__ __forceinline__ MapRun map_run(const RouteMapArgs& a, int block, int warp) {
+  const int64_t from = int64_t(block) * a.run, to = min(int64_t(a.slots), from + a.run);
+  const int per = a.run / a.warps;  // a multiple of 32
+  MapRun r;
+  r.first = warp < a.warps ? min(to, from + int64_t(warp) * per) : to;
+  r.last = warp < a.warps ? min(to, r.first + per) : to;
+  return r;
+}
+
+__device__ __forceinline__ int expert_of(const RouteMapArgs& a, int64_t slot, int64_t last) {
+  if (slot >= last || !DG_IN(a.dbg, a.indices + slot, 4, DBG_ROUTE)) return -1;
+  const int e = __ldg(a.indices + slot);
+  return e >= 0 && e < a.experts ? e : -1;
+}
+
+// Every row holds no slot, until its slot says otherwise.
+__device__ __forceinline__ void map_clear_rows(const RouteMapArgs& a, int block, int blocks) {
+  for (int64_t r = 4 * (int64_t(block) * kMapThreads + threadIdx.x); r < a.rows; r += 4 * int64_t(blocks) * kMapThreads) {
+    const int n = int(min(int64_t(4), a.rows - r));
     if (!DG_IN(a.dbg, a.rowmap + r, 4 * n, DBG_ROUTE)) continue;
     if (n == 4 && a.wide)
       *reinterpret_cast<int4*>(a.rowmap + r) = make_int4(-1, -1, -1, -1);
     else
       for (int i = 0; i < n; ++i) a.rowmap[r + i] = -1;
   }
+}
+
+// First walk of a CTA.  count: [warps][experts]; afterwards count[w][e] is the number of slots of e in
+// warps before w, total[e] in the CTA.  A slot's place among its warp's is in pos.
+__device__ __forceinline__ void map_count(const RouteMapArgs& a, const MapRun& r, int* count, int* total) {
+  const int E = a.experts, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < E * a.warps; i += kMapThreads) count[i] = 0;
   __syncthreads();
-  // this warp's run of slots: a multiple of 32 (warps past `warps` have none)
-  const int runs = ctas * warps;
-  const int run = ((a.slots + runs - 1) / runs + 31) & ~31;
-  const int64_t first = warp < warps ? int64_t(rank * warps + warp) * run : a.slots;
-  const int64_t last = min(int64_t(a.slots), first + run);
   int* const mine = count + warp * E;
-  auto expert_of = [&](int64_t slot) {
-    if (slot >= last || !DG_IN(a.dbg, a.indices + slot, 4, DBG_ROUTE)) return -1;
-    const int e = __ldg(a.indices + slot);
-    return e >= 0 && e < E ? e : -1;
-  };
-  // first walk: a slot's place among its warp's slots of its expert, kept in pos
-  for (int64_t s = first; s < last; s += 32 * kAhead) {
+  for (int64_t s = r.first; s < r.last; s += 32 * kAhead) {
     int e[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) e[i] = expert_of(s + 32 * i + lane);
+    for (int i = 0; i < kAhead; ++i) e[i] = expert_of(a, s + 32 * i + lane, r.last);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int64_t slot = s + 32 * i + lane;
@@ -355,68 +412,144 @@ __global__ void __launch_bounds__(kMapThreads) route_map_kernel(const RouteMapAr
       __syncwarp();
       if (e[i] >= 0 && lane == __ffs(same) - 1) mine[e[i]] = earlier + __popc(same);
       __syncwarp();
-      if (slot < last && DG_IN(a.dbg, a.pos + slot, 4, DBG_ROUTE))
+      if (slot < r.last && DG_IN(a.dbg, a.pos + slot, 4, DBG_ROUTE))
         a.pos[slot] = earlier + __popc(same & ((1u << lane) - 1u));
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kMapThreads) {  // counts -> slots of earlier warps
+  for (int e = threadIdx.x; e < E; e += kMapThreads) {
     int sum = 0;
-    for (int w = 0; w < warps; ++w) {
+    for (int w = 0; w < a.warps; ++w) {
       const int n = count[w * E + e];
       count[w * E + e] = sum;
       sum += n;
     }
     total[e] = sum;
   }
-  if (ctas > 1)
-    cluster.sync();
-  else
-    __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kMapThreads) {
-    int earlier = 0, sum = 0;
-    for (int c = 0; c < ctas; ++c) {
-      const int n = ctas > 1 ? *cluster.map_shared_rank(total + e, c) : total[e];
-      if (c < rank) earlier += n;
-      sum += n;
-    }
-    before[e] = earlier;
-    all[e] = sum;
-  }
-  __syncthreads();
-  if (warp == 0) {  // first rows: whole 128s of the experts before
-    int carry = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      const int n = e < E ? (all[e] + 127) & ~127 : 0;
-      int sum = n;
+}
+
+// all[e] -> start[e], the first row of expert e: whole 128s of the experts before (experts <=
+// kMapThreads: one a thread).  Block `writer` writes starts and counts.
+__device__ __forceinline__ void map_starts(const RouteMapArgs& a, const int* all, int* start, int* warp_sums, bool writer) {
+  const int e = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = e < a.experts ? (all[e] + 127) & ~127 : 0;
+  int sum = n;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(kAll, sum, d);
-        if (lane >= d) sum += o;
-      }
-      if (e < E) {
-        start[e] = carry + sum - n;
-        if (rank == 0 && DG_IN(a.dbg, a.starts + e, 4, DBG_ROUTE)) a.starts[e] = carry + sum - n;
-        if (rank == 0 && DG_IN(a.dbg, a.counts + e, 4, DBG_ROUTE)) a.counts[e] = all[e];
-      }
-      carry += __shfl_sync(kAll, sum, 31);
-    }
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(kAll, sum, d);
+    if (lane >= d) sum += o;
   }
+  if (lane == 31) warp_sums[warp] = sum;
   __syncthreads();
-  // second walk: rows of this warp's slots
-  for (int64_t s = first; s < last; s += 32 * kAhead) {
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += warp_sums[w];
+  if (e < a.experts) {
+    start[e] = before + sum - n;
+    if (writer && DG_IN(a.dbg, a.starts + e, 4, DBG_ROUTE)) a.starts[e] = start[e];
+    if (writer && DG_IN(a.dbg, a.counts + e, 4, DBG_ROUTE)) a.counts[e] = all[e];
+  }
+}
+
+// Second walk: row of a slot = offset[expert] + place.
+template <typename F>
+__device__ __forceinline__ void map_place(const RouteMapArgs& a, const MapRun& r, F offset) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t s = r.first; s < r.last; s += 32 * kAhead) {
+    int e[kAhead], place[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int64_t slot = s + 32 * i + lane;
-      const int e = expert_of(slot);
-      if (slot >= last || !DG_IN(a.dbg, a.pos + slot, 4, DBG_ROUTE)) continue;
-      const int row = e >= 0 ? start[e] + before[e] + mine[e] + a.pos[slot] : -1;
+      e[i] = expert_of(a, slot, r.last);
+      place[i] = slot < r.last && DG_IN(a.dbg, a.pos + slot, 4, DBG_ROUTE) ? a.pos[slot] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t slot = s + 32 * i + lane;
+      if (slot >= r.last || !DG_IN(a.dbg, a.pos + slot, 4, DBG_ROUTE)) continue;
+      const int row = e[i] >= 0 ? offset(e[i]) + place[i] : -1;
       a.pos[slot] = row;
       if (row >= 0 && row < a.rows && DG_IN(a.dbg, a.rowmap + row, 4, DBG_ROUTE)) a.rowmap[row] = int(slot);
     }
   }
-  if (ctas > 1) cluster.sync();  // no CTA leaves while another may still read its totals
+}
+
+// ints of shared memory: totals, first rows and warp sums, then [warps][experts]
+__host__ __device__ constexpr int map_ints(int experts, int warps) { return experts * (2 + warps) + 32; }
+
+__global__ void __launch_bounds__(kMapThreads) route_map_kernel(const RouteMapArgs a) {
+  extern __shared__ int map_shared[];
+  int* const total = map_shared;
+  int* const start = total + a.experts;
+  int* const warp_sums = start + a.experts;
+  int* const count = warp_sums + 32;
+  const int warp = threadIdx.x >> 5;
+  wait_prior_grid();
+  map_clear_rows(a, 0, 1);
+  const MapRun r = map_run(a, 0, warp);
+  map_count(a, r, count, total);
+  __syncthreads();
+  map_starts(a, total, start, warp_sums, true);
+  __syncthreads();
+  const int* const mine = count + warp * a.experts;
+  map_place(a, r, [&](int e) { return start[e] + mine[e]; });
+}
+
+// Two launches.  block_counts: [blocks][experts].
+__global__ void __launch_bounds__(kMapThreads) route_map_count_kernel(const RouteMapArgs a) {
+  extern __shared__ int map_shared[];
+  int* const total = map_shared;
+  int* const count = total + a.experts;
+  const int block = int(blockIdx.x), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_prior_grid();
+  map_clear_rows(a, block, int(gridDim.x));
+  const MapRun r = map_run(a, block, warp);
+  map_count(a, r, count, total);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kMapThreads) {
+    int* const c = a.block_counts + int64_t(block) * a.experts + e;
+    if (DG_IN(a.dbg, c, 4, DBG_ROUTE)) *c = total[e];
+  }
+  // places among the CTA's slots
+  const int* const mine = count + warp * a.experts;
+  for (int64_t slot = r.first + lane; slot < r.last; slot += 32) {
+    const int e = expert_of(a, slot, r.last);
+    if (e >= 0 && DG_IN(a.dbg, a.pos + slot, 4, DBG_ROUTE)) a.pos[slot] += mine[e];
+  }
+}
+
+__global__ void __launch_bounds__(kMapThreads) route_map_place_kernel(const RouteMapArgs a) {
+  extern __shared__ int map_shared[];
+  const int E = a.experts, blocks = int(gridDim.x), block = int(blockIdx.x), warp = threadIdx.x >> 5;
+  int* const all = map_shared;
+  int* const before = all + E;
+  int* const start = before + E;
+  int* const warp_sums = start + E;
+  wait_prior_grid();
+  for (int e = threadIdx.x; e < E; e += kMapThreads) all[e] = before[e] = 0;
+  __syncthreads();
+  // counts of all CTAs and of those before this one: 8 CTAs' counts of an expert a thread
+  // (whole numbers: the order of the additions does not matter)
+  const int parts = (blocks + 7) / 8;
+  for (int i = threadIdx.x; i < parts * E; i += kMapThreads) {
+    const int e = i % E, b0 = i / E * 8;
+    int n[8], sum = 0, earlier = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int* const c = a.block_counts + int64_t(b0 + j) * E + e;
+      n[j] = b0 + j < blocks && DG_IN(a.dbg, c, 4, DBG_ROUTE) ? __ldcg(c) : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sum += n[j];
+      if (b0 + j < block) earlier += n[j];
+    }
+    if (sum) atomicAdd(all + e, sum);
+    if (earlier) atomicAdd(before + e, earlier);
+  }
+  __syncthreads();
+  map_starts(a, all, start, warp_sums, block == 0);
+  __syncthreads();
+  map_place(a, map_run(a, block, warp), [&](int e) { return start[e] + before[e]; });
 }
 
 }  // namespace
@@ -434,41 +567,42 @@ cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t s) {
   });
 }
 
-cudaError_t launch_route_map(const RouteMapArgs& a, cudaStream_t s) {
-  // 4096 slots a CTA, up to the portable cluster size
-  const int ctas = std::max(1, std::min(8, (a.slots + 4095) / 4096));
-  const int warps = std::max(1, std::min(kMapThreads / 32, (a.slots / ctas + 31) / 32));
-  const int smem = map_ints(a.experts, warps) * 4;
-  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
+constexpr int kMapRun = 2048;     // slots of a CTA, where there are not more than kMapBlocks of them
+constexpr int kMapBlocks = 128;
+
+static int map_blocks(int64_t slots) {
+  return int(std::min<int64_t>(kMapBlocks, std::max<int64_t>(1, (slots + kMapRun - 1) / kMapRun)));
+}
+
+size_t route_map_workspace(int64_t slots, int64_t experts) {
+  const int blocks = map_blocks(slots);
+  return blocks > 1 ? size_t(blocks) * size_t(experts) * 4 : 0;
+}
+
+cudaError_t launch_route_map(RouteMapArgs a, cudaStream_t s) {
+  const int blocks = map_blocks(a.slots);
+  const int per_block = (a.slots + blocks - 1) / blocks;
+  a.warps = std::max(1, std::min(kMapWarps, (per_block + 31) / 32));
+  const int per_warp = ((per_block + a.warps - 1) / a.warps + 31) & ~31;
+  a.run = per_warp * a.warps;
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limits are set
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (bit == 0 || (ready.load(std::memory_order_acquire) & bit) == 0) {
-    const cudaError_t err = cudaFuncSetAttribute(route_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 map_ints(ROUTE_MAX_EXPERTS, kMapThreads / 32) * 4);
+    const int most = map_ints(ROUTE_MAX_EXPERTS, kMapWarps) * 4;
+    cudaError_t err = cudaFuncSetAttribute(route_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (err == cudaSuccess)
+      err = cudaFuncSetAttribute(route_map_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (err != cudaSuccess) return err;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(ctas));
-  cfg.blockDim = dim3(kMapThreads);
-  cfg.dynamicSmemBytes = size_t(smem);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  attr[n].id = cudaLaunchAttributeClusterDimension;
-  attr[n].val.clusterDim.x = unsigned(ctas);
-  attr[n].val.clusterDim.y = 1;
-  attr[n].val.clusterDim.z = 1;
-  ++n;
-  if (a.pdl) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, route_map_kernel, a, ctas, warps);
+  const size_t smem = size_t(map_ints(a.experts, a.warps)) * 4;
+  if (blocks == 1) return launch_k(route_map_kernel, dim3(1), dim3(kMapThreads), smem, s, a.pdl, a);
+  const cudaError_t err = launch_k(route_map_count_kernel, dim3(unsigned(blocks)), dim3(kMapThreads), smem, s, a.pdl, a);
+  if (err != cudaSuccess) return err;
+  return launch_k(route_map_place_kernel, dim3(unsigned(blocks)), dim3(kMapThreads), size_t(3 * a.experts + 32) * 4, s,
+                  a.pdl, a);
 }
 
 }  // namespace dg
