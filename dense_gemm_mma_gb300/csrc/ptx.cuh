@@ -472,27 +472,6 @@ static __device__ __noinline__ bool wait_bar_slow_cluster(uint32_t bar, uint32_t
 
 // ------------------------------------------- 3-D copies, block-scaled MMAs
 
-// 3-D tiled load global -> shared (x innermost, z outermost), counted in bytes
-// on `bar` of this CTA.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t x,
-                                            int32_t y, int32_t z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-// As above, counted on a barrier of either CTA of a pair (cluster address).
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar_cluster,
-                                                 int32_t x, int32_t y, int32_t z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
 // 3-D tiled store shared -> global (out-of-range parts of the box are clipped).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int32_t x, int32_t y, int32_t z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -501,43 +480,103 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src,
                : "memory");
 }
 
+// The forms below are called by a whole warp, converged, with warp-uniform operands
+// (so that they stay in uniform registers), and issued by the one thread whose `one` is
+// not 0, the same one every time: tcgen05.commit tracks what its own thread issued.
+
+// Descriptors as two words: the high one is the same for every operand of a layout, the low one
+// holds the address, in 16-byte units.
+constexpr uint32_t kDescSw128Hi = (1024u >> 4) | 1u << 14 | SMEM_SW128 << 29;  // K-major rows of 128 bytes
+constexpr uint32_t kDescScaleHi = (128u >> 4) | 1u << 14;  // no swizzling, groups of 8 lines 128 bytes apart
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | 1u << 16; }
+
 // Copy a 512-byte tile of scale bytes (32 lines of 16 bytes in shared memory)
 // into tensor memory: line i becomes lane i (and lanes i + 32, 64, 96), its four
 // 32-bit words four columns from `taddr`.  Completes before an MMA that this
 // thread issues later reads it; tc_commit tracks it like an MMA.
 template <bool PAIR>
-__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t sdesc) {
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint32_t lo, uint32_t one) {
+#define DG_COPY_SCALES(GROUP)                                                  \
+  asm volatile(                                                                \
+      "{\n\t.reg .pred q;\n\t.reg .b64 d;\n\t"                                   \
+      "setp.ne.b32 q, %3, 0;\n\tmov.b64 d, {%1, %2};\n\t"                      \
+      "@q tcgen05.cp.cta_group::" GROUP ".32x128b.warpx4 [%0], d;\n\t}" ::"r"(  \
+          taddr),                                                              \
+      "r"(lo), "r"(kDescScaleHi), "r"(one)                                     \
+      : "memory")
   if constexpr (PAIR)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+    DG_COPY_SCALES("2");
   else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+    DG_COPY_SCALES("1");
+#undef DG_COPY_SCALES
 }
-
-// Descriptor of such a tile: no swizzling, groups of 8 lines 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) { return smem_desc_sw128(saddr, 16, 128, 0); }
 
 // D (+)= (A * 2^(sa-127)) (B * 2^(sb-127)) over K = 32 8-bit values, fp32
 // accumulator; the scale bytes of A's and B's rows are in tensor memory, the
 // byte of each 32-bit word that is meant in the descriptor's scale ids.
 template <bool PAIR>
-__device__ __forceinline__ void tc_mma_scaled(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                              uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_scaled(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc,
+                                              uint32_t sfa, uint32_t sfb, uint32_t accumulate, uint32_t one) {
+#define DG_MMA_SCALED(GROUP)                                                                         \
+  asm volatile(                                                                                      \
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"                                                   \
+      "setp.ne.b32 p, %7, 0;\n\tsetp.ne.b32 q, %8, 0;\n\t"                                           \
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"                                             \
+      "@q tcgen05.mma.cta_group::" GROUP                                                             \
+      ".kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %4, [%5], [%6], p;\n\t}" ::"r"(d_tmem),  \
+      "r"(alo), "r"(blo), "r"(kDescSw128Hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(one) \
+      : "memory")
+  if constexpr (PAIR)
+    DG_MMA_SCALED("2");
+  else
+    DG_MMA_SCALED("1");
+#undef DG_MMA_SCALED
+}
+
+// Arrive on `bar` (a pair: at this offset in both CTAs) once every tcgen05
+// operation that thread has issued so far has completed.
+template <bool PAIR>
+__device__ __forceinline__ void tc_commit_one(uint32_t bar, uint32_t one) {
   if constexpr (PAIR)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-            d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\tsetp.ne.b32 q, %1, 0;\n\tmov.b16 m, 3;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+            bar),
+        "r"(one)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-            d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(one)
         : "memory");
+}
+
+// 3-D tiled load global -> shared (x innermost, z outermost), counted in bytes on `bar`: of
+// this CTA, or for a pair of either CTA (cluster address).
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_one(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t x, int32_t y,
+                                             int32_t z, uint32_t one) {
+#define DG_LOAD_ONE(GROUP)                                                                                  \
+  asm volatile(                                                                                             \
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"                                                     \
+      "@q cp.async.bulk.tensor.3d" GROUP ".shared::cluster.global.mbarrier::complete_tx::bytes"             \
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),                                                    \
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(one)                        \
+      : "memory")
+  if constexpr (PAIR)
+    DG_LOAD_ONE(".cta_group::2");
+  else
+    DG_LOAD_ONE("");
+#undef DG_LOAD_ONE
+}
+
+__device__ __forceinline__ void mbar_expect_one(uint32_t bar, uint32_t bytes, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(one)
+      : "memory");
 }
 
 // 16-byte load from the shared memory of a CTA of this cluster (cluster address).

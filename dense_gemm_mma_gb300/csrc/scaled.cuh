@@ -150,8 +150,18 @@ struct ScSets {
   }
 };
 
-// v <- act(v), every run-time choice outside the unrolled loops.
-template <int N>
+// Index of the warp, known to be the same in all its lanes.
+__device__ __forceinline__ int sc_warp() { return __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0); }
+
+// A whole warp's wait (bounded): true in every lane, or false in every lane.  `ready`: the
+// barrier has been seen complete already.
+__device__ __forceinline__ bool sc_wait(bool ready, uint32_t bar, uint32_t parity, const Watch& w, int code) {
+  if (__all_sync(0xffffffffu, ready)) return true;
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, w, code));
+}
+
+// v <- act(v), every run-time choice outside the unrolled loops; GELU and SiLU only if ALL.
+template <bool ALL, int N>
 __device__ __forceinline__ void sc_act(float (&v)[N], int act, float slope) {
   if (act == 1) {
 #pragma unroll
@@ -159,12 +169,14 @@ __device__ __forceinline__ void sc_act(float (&v)[N], int act, float slope) {
   } else if (act == 2) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
-  } else if (act == 3) {
+  } else if constexpr (ALL) {
+    if (act == 3) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = apply_act(v[i], 3, 0.f);
-  } else if (act == 4) {
+      for (int i = 0; i < N; ++i) v[i] = apply_act(v[i], 3, 0.f);
+    } else if (act == 4) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = apply_act(v[i], 4, 0.f);
+      for (int i = 0; i < N; ++i) v[i] = apply_act(v[i], 4, 0.f);
+    }
   }
 }
 

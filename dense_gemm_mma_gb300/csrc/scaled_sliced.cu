@@ -13,7 +13,7 @@
 // all CTAs through distributed shared memory, in slice order, so the result has
 // the same bits every time and no workspace or second launch is needed.
 //
-//  - warp 0, one lane: TMA producer; warp 1, one lane: MMA issuer (two accumulators,
+//  - warp 0: TMA producer; warp 1: MMA issuer (two accumulators,
 //    so a tile's MMAs overlap the previous one's epilogue);
 //  - warps 2-5: accumulator lanes -> partial tile [32 rows of A][128 rows of B] in shared
 //    memory, then whole rows of it, 512 bytes a warp, to D; 32 rows of A at a time.
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const sbase = smem_raw + (base - raw);
-  const int warp = threadIdx.x >> 5;
+  const int warp = sc_warp();
   const int lane = threadIdx.x & 31;
   const uint32_t full0 = base + off_bar(bn, S), empty0 = full0 + 8 * kMaxStages;
   const uint32_t tfull0 = empty0 + 8 * kMaxStages, tempty0 = tfull0 + 16, drain_bar = tempty0 + 16;
@@ -110,106 +110,103 @@ __global__ void __launch_bounds__(kThreads)
   // 32-row pieces of A in a tile
   auto pieces_of = [&](const ScUnit& x) { return (min(bn, x.row_end - x.row0) + 31) / 32; };
 
+  const uint32_t one = lane == 0;  // the lane that issues
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0, issued = 0, cursor = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int u = unit0; u < units && ok; u += step) {
-        const ScUnit x = unit_of(u, &cursor);
-        const int pieces = pieces_of(x);
-        for (int kb = x.kb0; kb < x.kb1; ++kb) {
-          if (!wait_bar(empty0 + 8 * stage, phase ^ 1u, w, WAIT_PRODUCER_EMPTY)) {
-            ok = false;
-            break;
-          }
-          const bool scales = kb == x.kb0 || (kb & 3) == 0;
-          const uint32_t fb = full0 + 8 * stage;
-          mbar_arrive_expect_tx(fb, uint32_t(kWeights + pieces * kRowsA + (scales ? kScales : 0)));
-          auto load = [&](uint32_t dst, const CUtensorMap* m, int cx, int cy, int cz, int esize) {
-            if (DG_TMA(p.dbg, cx, cy, esize, false)) tma_load_3d(dst, m, fb, cx, cy, cz);
-          };
-          const uint32_t st = base + uint32_t(stage * stage_bytes(bn));
-          load(st, &maps.b, kb * SC_BK, x.n0, x.zb, 1);
-          for (int j = 0; j < pieces; ++j) load(st + kWeights + j * kRowsA, &maps.a, kb * SC_BK, x.row0 + 32 * j, 0, 1);
-          if (scales) {
-            const uint32_t sf = base + uint32_t(off_scales(bn, S) + stage * kScales);
-            load(sf, &maps.sb, 0, x.zb * p.sb_group + (x.n0 / 128) * p.sb_cols + kb / 4, 0, 4);
-            load(sf + 512, &maps.sa, 0, (x.row0 / 128) * p.sa_cols + kb / 4, 0, 4);
-          }
-          ++issued;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
+    int stage = 0, issued = 0, cursor = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = unit0; u < units && ok; u += step) {
+      const ScUnit x = unit_of(u, &cursor);
+      const int pieces = pieces_of(x);
+      const int sb_row = x.zb * p.sb_group + (x.n0 / 128) * p.sb_cols, sa_row = (x.row0 / 128) * p.sa_cols;
+      for (int kb = x.kb0; kb < x.kb1; ++kb) {
+        const uint32_t eb = empty0 + 8 * stage, fb = full0 + 8 * stage;
+        if (!sc_wait(mbar_try_wait(eb, phase ^ 1u), eb, phase ^ 1u, w, WAIT_PRODUCER_EMPTY)) {
+          ok = false;
+          break;
+        }
+        const bool scales = kb == x.kb0 || (kb & 3) == 0;
+        mbar_expect_one(fb, uint32_t(kWeights + pieces * kRowsA + (scales ? kScales : 0)), one);
+        auto load = [&](uint32_t dst, const CUtensorMap* m, int cx, int cy, int cz, int esize) {
+          if (DG_TMA(p.dbg, cx, cy, esize, false)) tma_load_one<false>(dst, m, fb, cx, cy, cz, one);
+        };
+        const uint32_t st = base + uint32_t(stage * stage_bytes(bn));
+        load(st, &maps.b, kb * SC_BK, x.n0, x.zb, 1);
+        for (int j = 0; j < pieces; ++j) load(st + kWeights + j * kRowsA, &maps.a, kb * SC_BK, x.row0 + 32 * j, 0, 1);
+        if (scales) {
+          const uint32_t sf = base + uint32_t(off_scales(bn, S) + stage * kScales);
+          load(sf, &maps.sb, 0, sb_row + kb / 4, 0, 4);
+          load(sf + 512, &maps.sa, 0, sa_row + kb / 4, 0, 4);
+        }
+        ++issued;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) {
-        // Let the loads already in flight land before the CTA can exit.
-        for (int s = 0; s < S; ++s) {
-          const int n_s = issued > s ? (issued - s + S - 1) / S : 0;
-          if (n_s > 0) wait_bar(full0 + 8 * s, (uint32_t)((n_s - 1) & 1), w, 0);
-        }
+    }
+    if (!ok && lane == 0) {
+      // Let the loads already in flight land before the CTA can exit.
+      for (int s = 0; s < S; ++s) {
+        const int n_s = issued > s ? (issued - s + S - 1) / S : 0;
+        if (n_s > 0) wait_bar(full0 + 8 * s, (uint32_t)((n_s - 1) & 1), w, 0);
       }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      int stage = 0, it = 0, cursor = 0, tiles = 0;
-      uint32_t phase = 0;
-      uint32_t set_col = 0;
-      ScSets sets;
-      bool ok = true;
-      for (int u = unit0; u < units && ok; u += step) {
-        const ScUnit x = unit_of(u, &cursor);
-        if (x.kb0 >= x.kb1) continue;  // no K at all
-        const int acc = tiles & 1;
-        if (tiles > 1 && !wait_bar(tempty0 + 8 * acc, ((tiles - 2) >> 1) & 1, w, WAIT_MMA_TMEM_EMPTY)) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + uint32_t(acc * bn);
-        const uint32_t mma_n = uint32_t(pieces_of(x)) * 32;
-        for (int kb = x.kb0; kb < x.kb1; ++kb) {
-          if (!wait_bar(full0 + 8 * stage, phase, w, WAIT_MMA_FULL)) {
+    int stage = 0, it = 0, cursor = 0, tiles = 0;
+    uint32_t phase = 0;
+    uint32_t set_col = 0;
+    ScSets sets;
+    bool ok = true;
+    for (int u = unit0; u < units && ok; u += step) {
+      const ScUnit x = unit_of(u, &cursor);
+      if (x.kb0 >= x.kb1) continue;  // no K at all
+      const int acc = tiles & 1;
+      if (tiles > 1 && !sc_wait(false, tempty0 + 8 * acc, ((tiles - 2) >> 1) & 1, w, WAIT_MMA_TMEM_EMPTY)) break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + uint32_t(acc * bn);
+      const uint32_t mma_n = uint32_t(pieces_of(x)) * 32;
+      for (int kb = x.kb0; kb < x.kb1; ++kb) {
+        if (!sc_wait(false, full0 + 8 * stage, phase, w, WAIT_MMA_FULL)) {
+          ok = false;
+          break;
+        }
+        if (kb == x.kb0 || (kb & 3) == 0) {
+          const int old = sets.last_user();
+          if (old >= 0 && old > it - S &&
+              !sc_wait(false, empty0 + 8 * (old % S), uint32_t(old / S) & 1u, w, WAIT_MMA_FULL)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          if (kb == x.kb0 || (kb & 3) == 0) {
-            const int old = sets.last_user();
-            if (old >= 0 && old > it - S &&
-                !wait_bar(empty0 + 8 * (old % S), uint32_t(old / S) & 1u, w, WAIT_MMA_FULL)) {
-              ok = false;
-              break;
-            }
-            set_col = tmem_base + uint32_t(2 * bn) + 8 * sets.take(it);
-            const uint32_t sf = base + uint32_t(off_scales(bn, S) + stage * kScales);
-            tc_copy_scales<false>(set_col, scale_desc(sf));
-            tc_copy_scales<false>(set_col + 4, scale_desc(sf + 512));
-          }
-          const uint32_t id = uint32_t(kb & 3);
-          const uint32_t idesc = p.idesc | (mma_n >> 3 << 17) | (id << 4) | (id << 29);
-          const uint32_t st = base + uint32_t(stage * stage_bytes(bn));
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_scaled<false>(d_tmem, smem_desc_sw128(st + 32 * kk, 16, 1024),
-                                 smem_desc_sw128(st + kWeights + 32 * kk, 16, 1024), idesc, set_col, set_col + 4,
-                                 kb > x.kb0 || kk > 0);
-          tc_commit(empty0 + 8 * stage);  // stage free once these MMAs finish
-          ++it;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          set_col = tmem_base + uint32_t(2 * bn) + 8 * sets.take(it);
+          const uint32_t sf = desc_lo(base + uint32_t(off_scales(bn, S) + stage * kScales));
+          tc_copy_scales<false>(set_col, sf, one);
+          tc_copy_scales<false>(set_col + 4, sf + (512 >> 4), one);
         }
-        if (!ok) break;
-        tc_commit(tfull0 + 8 * acc);
-        ++tiles;
+        const uint32_t id = uint32_t(kb & 3);
+        const uint32_t idesc = p.idesc | (mma_n >> 3 << 17) | (id << 4) | (id << 29);
+        const uint32_t lo = desc_lo(base + uint32_t(stage * stage_bytes(bn)));
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_scaled<false>(d_tmem, lo + (32 >> 4) * kk, lo + (kWeights >> 4) + (32 >> 4) * kk, idesc, set_col,
+                               set_col + 4, kb > x.kb0 || kk > 0, one);
+        tc_commit_one<false>(empty0 + 8 * stage, one);  // stage free once these MMAs finish
+        ++it;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      // Every MMA issued by this thread completes before tensor memory is freed.
-      tc_commit(drain_bar);
-      wait_bar(drain_bar, 0, w, WAIT_DRAIN);
+      if (!ok) break;
+      tc_commit_one<false>(tfull0 + 8 * acc, one);
+      ++tiles;
     }
+    // Every MMA issued by this warp completes before tensor memory is freed.
+    tc_commit_one<false>(drain_bar, one);
+    sc_wait(false, drain_bar, 0, w, WAIT_DRAIN);
   } else {
     // ------------------------------------------------------------ epilogue
     const int e = warp - 2;
@@ -287,7 +284,7 @@ __global__ void __launch_bounds__(kThreads)
             v[i] *= p.alpha;
             if (p.beta != 0.f && i < n) v[i] = fmaf(p.beta, sc_load1(dst + i * es, p.out_kind), v[i]);
           }
-          sc_act(v, p.act, p.slope);
+          sc_act<true>(v, p.act, p.slope);
           if (whole && es == 4)
             *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
           else if (whole)

@@ -2,12 +2,15 @@
 // persistent, warp-specialised tcgen05 kernel for calls with enough tiles to
 // fill the GPU (formula and scales: scaled.cuh).
 //
-//  - warp 0, one lane: TMA producer.  A ring stage is one k-block: 128 rows of A
+//  - warp 0: TMA producer.  A ring stage is one k-block: 128 rows of A
 //    and of B (a pair: half of the tile's columns per CTA) by 128 bytes of K, and,
 //    with the first k-block of a group of four, the scale tiles of that group.
-//  - warp 1, one lane: MMA issuer.  Copies a group's scale tiles into one of four
-//    sets of tensor-memory columns and issues four K = 32 MMAs per k-block.
-//  - warps 2-5: epilogue, 32 accumulator lanes (rows) each, through a swizzled
+//  - warp 1: MMA issuer.  Copies a group's scale tiles into one of four
+//    sets of tensor-memory columns and issues four K = 32 MMAs per k-block.  Both warps run
+//    converged and have one lane issue: with the loop inside a one-lane branch its operands
+//    went through vector registers, and a k-block took ~450 cycles and 75 more for each MMA to
+//    issue, of which the tensor core needs 512 in all.
+//  - warps 2-9: epilogue, 32 accumulator lanes (rows) for two of them, through a swizzled
 //    shared-memory box and a TMA store; rows of a box that do not all exist (the
 //    last rows of a group) are stored by the threads, so rows between groups
 //    are never written.
@@ -18,14 +21,17 @@
 // of tensor memory and leave none for the scales, so they overlap by 64: columns
 // 0-255 and 192-447, scales from 448.  The epilogue drains the shared columns of
 // a tile first and only then lets the next tile's MMAs begin.
+#include <type_traits>
+
 #include "scaled.cuh"
 
 namespace dg {
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;     // two for each quarter of the accumulator's lanes
+constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kBox = 32 * 128;  // one 32-row x 128-byte epilogue box
+constexpr int kBufs = 1;        // boxes of a warp
 
 template <bool PAIR>
 struct Cfg {
@@ -37,7 +43,7 @@ struct Cfg {
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + STAGES * OPERAND;
   static constexpr int OFF_STG = OFF_B + STAGES * OPERAND;
-  static constexpr int OFF_S = OFF_STG + kEpiWarps * 2 * kBox;
+  static constexpr int OFF_S = OFF_STG + kEpiWarps * kBufs * kBox;
   static constexpr int OFF_BAR = OFF_S + STAGES * SCALES;
   // full[S], empty[S], tmem_full[2], tmem_empty[2], drain
   static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 5) * 8;
@@ -51,11 +57,15 @@ struct Cfg {
   static_assert(ACC1 + BN <= SF0 && SF0 + 64 <= TMEM_COLS, "tensor memory budget");
 };
 
+// Epilogue variants, compiled separately: what a tile's loop does not need would cost it
+// the instruction cache.  Plain: beta == 0; identity, LeakyReLU or ReLU.
+enum : int { EPI_PLAIN = 0, EPI_ANY = 1 };
+
 // v <- alpha * v + beta * D for the columns [col, col + 32) of a row.
 __device__ __forceinline__ void blend(float (&v)[32], const ScParams& p, const uint8_t* row, int col, bool live) {
   const int es = p.out_kind == OUT_F32 ? 4 : 2;
 #pragma unroll
-  for (int j = 0; j < 32; j += 16 / 4) {
+  for (int j = 0; j < 32; j += 4) {
     float c[4] = {0.f, 0.f, 0.f, 0.f};
     if (live && col + j < p.N) {
       const uint8_t* const src = row + int64_t(col + j) * es;
@@ -76,14 +86,15 @@ __device__ __forceinline__ void blend(float (&v)[32], const ScParams& p, const u
   }
 }
 
+template <int V>
 __device__ __forceinline__ void finish(float (&v)[32], const ScParams& p, const uint8_t* row, int col, bool live) {
-  if (p.beta != 0.f) {
+  if (V == EPI_ANY && p.beta != 0.f) {
     blend(v, p, row, col, live);
   } else {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= p.alpha;
   }
-  sc_act(v, p.act, p.slope);
+  sc_act<V == EPI_ANY>(v, p.act, p.slope);
 }
 
 template <bool PAIR>
@@ -97,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const sbase = smem_raw + (base - raw);
-  const int warp = threadIdx.x >> 5;
+  const int warp = sc_warp();
   const int lane = threadIdx.x & 31;
   const uint32_t full0 = base + C::OFF_BAR, empty0 = full0 + 8 * S;
   const uint32_t tfull0 = empty0 + 8 * S, tempty0 = tfull0 + 16, drain_bar = tempty0 + 16;
@@ -146,69 +157,67 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int unit0 = PAIR ? int(blockIdx.x) / 2 : int(blockIdx.x);
   const int step = PAIR ? int(gridDim.x) / 2 : int(gridDim.x);
   const Watch w{abort_flag, p.err, p.timeout_ns};
-  auto wait = [&](uint32_t bar, uint32_t parity, int code) {
+  // Bounded wait on a barrier that the peer CTA's threads arrive on.
+  auto wait_peers = [&](uint32_t bar, uint32_t parity, int code) {
     if constexpr (PAIR) return wait_bar_cluster(bar, parity, w, code);
     return wait_bar(bar, parity, w, code);
   };
+  const uint32_t one = lane == 0;  // the lane that issues
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0, issued = 0, cursor = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int u = unit0; u < units && ok; u += step) {
-        const ScUnit x = sc_unit(p, u, C::TILE_M, C::BN, table, &cursor);
-        const int m0 = x.row0 + int(rank) * 128, n0 = x.n0 + int(rank) * (PAIR ? 128 : 0);
-        for (int kb = x.kb0; kb < x.kb1; ++kb) {
-          if (!wait(empty0 + 8 * stage, phase ^ 1u, WAIT_PRODUCER_EMPTY)) {
-            ok = false;
-            break;
-          }
-          const bool scales = kb == x.kb0 || (kb & 3) == 0;
-          const uint32_t fb = full0 + 8 * stage;
-          const uint32_t fbc = PAIR ? mapa_shared(fb, 0) : fb;
-          if (leader) mbar_arrive_expect_tx(fb, (PAIR ? 2 : 1) * (2 * C::OPERAND + (scales ? C::SCALES : 0)));
-          auto load = [&](uint32_t dst, const CUtensorMap* m, int cx, int cy, int cz, int esize) {
-            if (!DG_TMA(p.dbg, cx, cy, esize, false)) return;  // (its barrier never completes)
-            if constexpr (PAIR)
-              tma_load_3d_pair(dst, m, fbc, cx, cy, cz);
-            else
-              tma_load_3d(dst, m, fb, cx, cy, cz);
-          };
-          load(base + C::OFF_A + stage * C::OPERAND, &maps.a, kb * SC_BK, m0, 0, 1);
-          load(base + C::OFF_B + stage * C::OPERAND, &maps.b, kb * SC_BK, n0, x.zb, 1);
-          if (scales) {
-            // (row blocks past the matrix read another tile or zero: their rows are not stored)
-            const uint32_t sf = base + C::OFF_S + stage * C::SCALES;
-            load(sf, &maps.sa, 0, (m0 / 128) * p.sa_cols + kb / 4, 0, 4);
+    int stage = 0, issued = 0, cursor = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = unit0; u < units && ok; u += step) {
+      const ScUnit x = sc_unit(p, u, C::TILE_M, C::BN, table, &cursor);
+      const int m0 = x.row0 + int(rank) * 128, n0 = x.n0 + int(rank) * (PAIR ? 128 : 0);
+      const int sa_row = (m0 / 128) * p.sa_cols, sb_row = x.zb * p.sb_group + (x.n0 / 128) * p.sb_cols;
+      for (int kb = x.kb0; kb < x.kb1; ++kb) {
+        const uint32_t eb = empty0 + 8 * stage, fb = full0 + 8 * stage;
+        if (!sc_wait(mbar_try_wait(eb, phase ^ 1u), eb, phase ^ 1u, w, WAIT_PRODUCER_EMPTY)) {
+          ok = false;
+          break;
+        }
+        const bool scales = kb == x.kb0 || (kb & 3) == 0;
+        const uint32_t fbc = PAIR ? mapa_shared(fb, 0) : fb;
+        mbar_expect_one(fb, uint32_t(PAIR ? 2 : 1) * (2 * C::OPERAND + (scales ? C::SCALES : 0)), one & uint32_t(leader));
+        auto load = [&](uint32_t dst, const CUtensorMap* m, int cx, int cy, int cz, int esize) {
+          if (!DG_TMA(p.dbg, cx, cy, esize, false)) return;  // (its barrier never completes)
+          tma_load_one<PAIR>(dst, m, fbc, cx, cy, cz, one);
+        };
+        load(base + C::OFF_A + stage * C::OPERAND, &maps.a, kb * SC_BK, m0, 0, 1);
+        load(base + C::OFF_B + stage * C::OPERAND, &maps.b, kb * SC_BK, n0, x.zb, 1);
+        if (scales) {
+          // (row blocks past the matrix read another tile or zero: their rows are not stored)
+          const uint32_t sf = base + C::OFF_S + stage * C::SCALES;
+          load(sf, &maps.sa, 0, sa_row + kb / 4, 0, 4);
 #pragma unroll
-            for (int j = 0; j < C::BN / 128; ++j)
-              load(sf + 512 * (1 + j), &maps.sb, 0, x.zb * p.sb_group + (x.n0 / 128 + j) * p.sb_cols + kb / 4, 0, 4);
-          }
-          ++issued;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          for (int j = 0; j < C::BN / 128; ++j) load(sf + 512 * (1 + j), &maps.sb, 0, sb_row + j * p.sb_cols + kb / 4, 0, 4);
+        }
+        ++issued;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) {
-        // Let the loads already in flight land before the CTA can exit.
-        for (int s = 0; s < S; ++s) {
-          const int n_s = issued > s ? (issued - s + S - 1) / S : 0;
-          if (n_s > 0 && leader) wait(full0 + 8 * s, (uint32_t)((n_s - 1) & 1), 0);
-        }
+    }
+    if (!ok && lane == 0) {
+      // Let the loads already in flight land before the CTA can exit.
+      for (int s = 0; s < S; ++s) {
+        const int n_s = issued > s ? (issued - s + S - 1) / S : 0;
+        if (n_s > 0 && leader) wait_bar(full0 + 8 * s, (uint32_t)((n_s - 1) & 1), w, 0);
       }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0 && leader) {
+    if (leader) {
       int stage = 0, it = 0, cursor = 0, tiles = 0;
       uint32_t phase = 0;
       uint32_t set_col = 0;
       ScSets sets;
       bool ok = true;
+      bool ready = false;  // the next stage's loads have been seen to have landed
       for (int u = unit0; u < units && ok; u += step) {
         const ScUnit x = sc_unit(p, u, C::TILE_M, C::BN, table, &cursor);
         if (x.kb0 >= x.kb1) continue;  // an empty group: the epilogue writes it without an accumulator
@@ -217,183 +226,204 @@ __global__ void __launch_bounds__(kThreads, 1)
         // drained (and with them the whole tile before it).  Separate ones: this
         // accumulator's last tile has.
         if (C::OVERLAP > 0) {
-          if (tiles > 0 && !wait(tempty0 + 8 * (acc ^ 1), ((tiles - 1) >> 1) & 1, WAIT_MMA_TMEM_EMPTY)) break;
+          if (tiles > 0 && !__all_sync(0xffffffffu, wait_peers(tempty0 + 8 * (acc ^ 1), ((tiles - 1) >> 1) & 1,
+                                                               WAIT_MMA_TMEM_EMPTY)))
+            break;
         } else {
-          if (tiles > 1 && !wait(tempty0 + 8 * acc, ((tiles - 2) >> 1) & 1, WAIT_MMA_TMEM_EMPTY)) break;
+          if (tiles > 1 &&
+              !__all_sync(0xffffffffu, wait_peers(tempty0 + 8 * acc, ((tiles - 2) >> 1) & 1, WAIT_MMA_TMEM_EMPTY)))
+            break;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + uint32_t(acc ? C::ACC1 : 0);
         for (int kb = x.kb0; kb < x.kb1; ++kb) {
-          if (!wait(full0 + 8 * stage, phase, WAIT_MMA_FULL)) {
+          if (!sc_wait(ready, full0 + 8 * stage, phase, w, WAIT_MMA_FULL)) {
             ok = false;
             break;
           }
-          tc_fence_after();
+          const int next_stage = stage + 1 == S ? 0 : stage + 1;
+          const uint32_t next_phase = phase ^ uint32_t(stage + 1 == S);
+          ready = mbar_try_wait(full0 + 8 * next_stage, next_phase);
           if (kb == x.kb0 || (kb & 3) == 0) {
             const int old = sets.last_user();
-            if (old >= 0 && old > it - S && !wait(empty0 + 8 * (old % S), uint32_t(old / S) & 1u, WAIT_MMA_FULL)) {
+            if (old >= 0 && old > it - S &&
+                !sc_wait(false, empty0 + 8 * (old % S), uint32_t(old / S) & 1u, w, WAIT_MMA_FULL)) {
               ok = false;
               break;
             }
             set_col = tmem_base + C::SF0 + 16 * sets.take(it);
-            const uint32_t sf = base + C::OFF_S + stage * C::SCALES;
+            const uint32_t sf = desc_lo(base + C::OFF_S + stage * C::SCALES);
 #pragma unroll
-            for (int j = 0; j < 1 + C::BN / 128; ++j) tc_copy_scales<PAIR>(set_col + 4 * j, scale_desc(sf + 512 * j));
+            for (int j = 0; j < 1 + C::BN / 128; ++j) tc_copy_scales<PAIR>(set_col + 4 * j, sf + (512 >> 4) * j, one);
           }
           const uint32_t id = uint32_t(kb & 3);
           const uint32_t idesc = p.idesc | (id << 4) | (id << 29);
-          const uint32_t sa = base + C::OFF_A + stage * C::OPERAND, sb = base + C::OFF_B + stage * C::OPERAND;
+          const uint32_t alo = desc_lo(base + C::OFF_A + stage * C::OPERAND);
+          const uint32_t blo = desc_lo(base + C::OFF_B + stage * C::OPERAND);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_scaled<PAIR>(d_tmem, smem_desc_sw128(sa + 32 * kk, 16, 1024), smem_desc_sw128(sb + 32 * kk, 16, 1024),
-                                idesc, set_col, set_col + 4, kb > x.kb0 || kk > 0);
-          // stage free (in both CTAs of a pair) once these MMAs finish
-          if constexpr (PAIR)
-            tc_commit_pair_multicast(empty0 + 8 * stage, 0x3);
-          else
-            tc_commit(empty0 + 8 * stage);
+            tc_mma_scaled<PAIR>(d_tmem, alo + (32 >> 4) * kk, blo + (32 >> 4) * kk, idesc, set_col, set_col + 4,
+                                kb > x.kb0 || kk > 0, one);
+          tc_commit_one<PAIR>(empty0 + 8 * stage, one);  // stage free (in both CTAs of a pair) once these MMAs finish
           ++it;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          stage = next_stage;
+          phase = next_phase;
         }
         if (!ok) break;
-        if constexpr (PAIR)
-          tc_commit_pair_multicast(tfull0 + 8 * acc, 0x3);
-        else
-          tc_commit(tfull0 + 8 * acc);
+        tc_commit_one<PAIR>(tfull0 + 8 * acc, one);
         ++tiles;
       }
-      // Every MMA issued by this thread completes before tensor memory is freed.
-      if constexpr (PAIR)
-        tc_commit_pair_multicast(drain_bar, 0x1);
-      else
-        tc_commit(drain_bar);
-      wait(drain_bar, 0, WAIT_DRAIN);
+      // Every MMA issued by this warp completes before tensor memory is freed.
+      if (one) {
+        if constexpr (PAIR)
+          tc_commit_pair_multicast(drain_bar, 0x1);
+        else
+          tc_commit(drain_bar);
+      }
+      __syncwarp();
+      sc_wait(false, drain_bar, 0, w, WAIT_DRAIN);
     }
   } else {
     // ------------------------------------------------------------ epilogue
     const int e = warp - 2;
-    const int q = warp & 3;  // tensor-memory lane quarter this warp may read
-    const uint32_t stg0 = base + C::OFF_STG + e * 2 * kBox;
-    uint8_t* const stg_p0 = sbase + C::OFF_STG + e * 2 * kBox;
+    const int q = warp & 3;       // tensor-memory lane quarter this warp may read
+    const int half = e >> 2;      // which of the quarter's warps: chunks half, half + 2, ...
+    constexpr int kHalves = kEpiWarps / 4;
+    const uint32_t stg0 = base + C::OFF_STG + e * kBufs * kBox;
+    uint8_t* const stg_p0 = sbase + C::OFF_STG + e * kBufs * kBox;
     const int es = p.out_kind == OUT_F32 ? 4 : 2;
     const int cw = 128 / es;  // columns per 128-byte box row
     const int chunks = C::BN / cw;
     const int shared_chunks = C::OVERLAP / cw;
     const int sw = lane & 7;  // 128-byte swizzle: 16-byte chunk j of row r lives at j ^ (r % 8)
     int cursor = 0, tiles = 0, sbuf = 0;
-    for (int u = unit0; u < units; u += step) {
-      const ScUnit x = sc_unit(p, u, C::TILE_M, C::BN, table, &cursor);
-      const bool empty = x.kb0 >= x.kb1;
-      const int acc = tiles & 1;
-      if (!empty) {
-        if (!__all_sync(0xffffffffu, wait(tfull0 + 8 * acc, (tiles >> 1) & 1, WAIT_EPI_TMEM_FULL))) break;
-        tc_fence_after();
-        ++tiles;
-      }
-      auto release = [&]() {  // this warp's reads that the next MMAs wait for are complete
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (PAIR)
-            mbar_arrive_cluster(mapa_shared(tempty0 + 8 * acc, 0));
-          else
-            mbar_arrive(tempty0 + 8 * acc);
-        }
-        __syncwarp();
-      };
-      const int y0 = x.row0 + int(rank) * 128 + 32 * q;
-      const int live = min(32, x.row_end - y0);  // rows of the box that exist
-      if (live <= 0) {
-        if (!empty) release();
-        continue;
-      }
-      const bool mine = lane < live;
-      // past the last row of a product the TMA clips; past a group's it must not write
-      const bool by_tma = p.group != SC_ROWS || live == 32;
-      const uint32_t t_row =
-          tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc ? C::ACC1 : 0);
-      uint8_t* const d_row = static_cast<uint8_t*>(p.d) + (int64_t(x.zd) * p.d_group + int64_t(y0 + lane) * p.ldd) * es;
-      // the shared columns first: the last ones of accumulator 0, the first ones of accumulator 1
-      const int first = acc == 0 ? chunks - shared_chunks : 0;
-      for (int i = 0; i < chunks; ++i) {
-        const int c = shared_chunks == 0 ? i : (i + first) % chunks;
-        const int x0 = x.n0 + c * cw;
-        const uint32_t stg = stg0 + sbuf * kBox;
-        uint8_t* const row_p = stg_p0 + sbuf * kBox + lane * 128;
-        uint32_t r0[32], r1[32];
+    auto tiles_loop = [&](auto variant) {
+      constexpr int V = decltype(variant)::value;
+      for (int u = unit0; u < units; u += step) {
+        const ScUnit x = sc_unit(p, u, C::TILE_M, C::BN, table, &cursor);
+        const bool empty = x.kb0 >= x.kb1;
+        const int acc = tiles & 1;
         if (!empty) {
-          tmem_ld_32x32b_x32(t_row + c * cw, r0);
-          if (es == 2) tmem_ld_32x32b_x32(t_row + c * cw + 32, r1);
-          tmem_ld_wait(r0);
-          if (es == 2) tmem_ld_wait(r1);
-          if (i + 1 == (shared_chunks == 0 ? chunks : shared_chunks)) release();
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) r0[k] = r1[k] = 0u;
+          if (!__all_sync(0xffffffffu, wait_peers(tfull0 + 8 * acc, (tiles >> 1) & 1, WAIT_EPI_TMEM_FULL))) break;
+          tc_fence_after();
+          ++tiles;
         }
-        if (x0 >= p.N) continue;
-        if (lane == 0) bulk_wait_read<1>();  // the store that last used this buffer has read it
-        __syncwarp();
-        float v[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r0[k]);
-        finish(v, p, d_row, x0, mine);
-        if (es == 4) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float4*>(row_p + ((j ^ sw) << 4)) =
-                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == 1) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r1[k]);
-              finish(v, p, d_row, x0 + 32, mine);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(row_p + (((4 * h + j) ^ sw) << 4)) =
-                  make_uint4(sc_pack2(v[8 * j], v[8 * j + 1], p.out_kind), sc_pack2(v[8 * j + 2], v[8 * j + 3], p.out_kind),
-                             sc_pack2(v[8 * j + 4], v[8 * j + 5], p.out_kind), sc_pack2(v[8 * j + 6], v[8 * j + 7], p.out_kind));
-          }
-        }
-        if (mine) {
-          // by the threads: rows of a box that is not whole, in 16-byte pieces up to
-          // n_tma, and the columns past the last whole piece of a row
-          if (!by_tma) {
-            const int per = 16 / es;
-#pragma unroll 1
-            for (int j = 0; j < 8 && x0 + (j + 1) * per <= p.n_tma; ++j) {
-              uint8_t* const dst = d_row + int64_t(x0 + j * per) * es;
-              if (DG_IN(p.dbg, dst, 16, DBG_SCALED))
-                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(row_p + ((j ^ sw) << 4));
-            }
-          }
-          for (int col = max(x0, p.n_tma); col < min(x0 + cw, p.N); ++col) {
-            const int b = (col - x0) * es;
-            const uint8_t* const src = row_p + (((b >> 4) ^ sw) << 4) + (b & 15);
-            uint8_t* const dst = d_row + int64_t(col) * es;
-            if (!DG_IN(p.dbg, dst, es, DBG_SCALED)) continue;
-            if (es == 4)
-              *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
+        auto release = [&]() {  // this warp's reads that the next MMAs wait for are complete
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR)
+              mbar_arrive_cluster(mapa_shared(tempty0 + 8 * acc, 0));
             else
-              *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
+              mbar_arrive(tempty0 + 8 * acc);
           }
+          __syncwarp();
+        };
+        const int y0 = x.row0 + int(rank) * 128 + 32 * q;
+        const int live = min(32, x.row_end - y0);  // rows of the box that exist
+        if (live <= 0) {
+          if (!empty) release();
+          continue;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (by_tma && x0 < p.n_tma && DG_TMA(p.dbg, x0, y0, es, true)) tma_store_3d(&maps.d, stg, x0, y0, x.zd);
-          bulk_commit();  // one group per chunk (possibly empty) keeps the buffer accounting exact
+        const bool mine = lane < live;
+        // past the last row of a product the TMA clips; past a group's it must not write
+        const bool by_tma = p.group != SC_ROWS || live == 32;
+        const uint32_t t_row =
+            tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc ? C::ACC1 : 0);
+        uint8_t* const d_row = static_cast<uint8_t*>(p.d) + (int64_t(x.zd) * p.d_group + int64_t(y0 + lane) * p.ldd) * es;
+        // the shared columns first: the last ones of accumulator 0, the first ones of accumulator 1
+        const int first = acc == 0 ? chunks - shared_chunks : 0;
+        // after which of its chunks this warp has read what the next MMAs wait for
+        const int release_after = shared_chunks == 0 ? chunks - kHalves + half : half + (shared_chunks - 1 - half) / kHalves * kHalves;
+        bool released = empty;
+        if (!released && shared_chunks > 0 && half >= shared_chunks) {
+          release();
+          released = true;
         }
-        __syncwarp();  // whole again before the next tcgen05.ld
-        sbuf ^= 1;
+        for (int i = half; i < chunks; i += kHalves) {
+          const int c = shared_chunks == 0 ? i : (i + first) % chunks;
+          const int x0 = x.n0 + c * cw;
+          uint32_t r0[32], r1[32];
+          if (!empty) {
+            tmem_ld_32x32b_x32(t_row + c * cw, r0);
+            if (es == 2) tmem_ld_32x32b_x32(t_row + c * cw + 32, r1);
+            tmem_ld_wait(r0);
+            if (es == 2) tmem_ld_wait(r1);
+            if (!released && i == release_after) {
+              release();
+              released = true;
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) r0[k] = r1[k] = 0u;
+          }
+          if (x0 >= p.N) continue;
+          const uint32_t stg = stg0 + sbuf * kBox;
+          uint8_t* const row_p = stg_p0 + sbuf * kBox + lane * 128;
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r0[k]);
+          finish<V>(v, p, d_row, x0, mine);
+          if (lane == 0) bulk_wait_read<kBufs - 1>();  // the store that last used this box has read it
+          __syncwarp();
+          if (es == 4) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(row_p + ((j ^ sw) << 4)) =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h == 1) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r1[k]);
+                finish<V>(v, p, d_row, x0 + 32, mine);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(row_p + (((4 * h + j) ^ sw) << 4)) = make_uint4(
+                    sc_pack2(v[8 * j], v[8 * j + 1], p.out_kind), sc_pack2(v[8 * j + 2], v[8 * j + 3], p.out_kind),
+                    sc_pack2(v[8 * j + 4], v[8 * j + 5], p.out_kind), sc_pack2(v[8 * j + 6], v[8 * j + 7], p.out_kind));
+            }
+          }
+          if (mine) {
+            // by the threads: rows of a box that is not whole, in 16-byte pieces up to
+            // n_tma, and the columns past the last whole piece of a row
+            if (!by_tma) {
+              const int per = 16 / es;
+#pragma unroll 1
+              for (int j = 0; j < 8 && x0 + (j + 1) * per <= p.n_tma; ++j) {
+                uint8_t* const dst = d_row + int64_t(x0 + j * per) * es;
+                if (DG_IN(p.dbg, dst, 16, DBG_SCALED))
+                  *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(row_p + ((j ^ sw) << 4));
+              }
+            }
+            for (int col = max(x0, p.n_tma); col < min(x0 + cw, p.N); ++col) {
+              const int b = (col - x0) * es;
+              const uint8_t* const src = row_p + (((b >> 4) ^ sw) << 4) + (b & 15);
+              uint8_t* const dst = d_row + int64_t(col) * es;
+              if (!DG_IN(p.dbg, dst, es, DBG_SCALED)) continue;
+              if (es == 4)
+                *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
+              else
+                *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (by_tma && x0 < p.n_tma && DG_TMA(p.dbg, x0, y0, es, true)) tma_store_3d(&maps.d, stg, x0, y0, x.zd);
+            bulk_commit();  // one group per chunk (possibly empty) keeps the buffer accounting exact
+          }
+          __syncwarp();  // whole again before the next tcgen05.ld
+          if (++sbuf == kBufs) sbuf = 0;
+        }
       }
-    }
+    };
+    if (p.beta == 0.f && p.act <= 2)
+      tiles_loop(std::integral_constant<int, EPI_PLAIN>{});
+    else
+      tiles_loop(std::integral_constant<int, EPI_ANY>{});
     // The stores must have read the staging buffers before the CTA exits; the
     // grid's completion covers their writes to global memory.
     if (lane == 0) bulk_wait_read<0>();
