@@ -526,7 +526,7 @@ gemm_status_t gemm_quantize(gemm_plan_t plan, int64_t rows, int64_t cols, const 
 #ifdef DG_DEBUG
   a.dbg = Spans(plan->err).matrix(X, xr, cols, ldx, es).matrix(Q, Q ? rows : 0, cols, ldq, 1)
               .bytes(SQ, gemm_scale_bytes(rows, cols)).out_matrix(QT, QT ? cols : 0, rows, ldqt, 1)
-              .bytes(SQT, gemm_scale_bytes(cols, rows)).s;
+              .bytes(SQT, gemm_scale_bytes(cols, rows)).bytes(rowmap, rowmap ? rows * 4 : 0).s;
 #endif
   return launched(launch_quantize(a, static_cast<cudaStream_t>(stream)));
 }

@@ -134,13 +134,24 @@ __device__ __forceinline__ int64_t scale_at(int64_t r, int64_t c, int64_t groups
   return ((r >> 7) * groups + (c >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (c & 3);
 }
 
-__device__ __forceinline__ int source_row(const QuantArgs& a, int r) {
-  if (r >= a.rows) return -1;
-  if (!a.rowmap) return r;
-  const int s = __ldg(a.rowmap + r);
-  if (s < 0) return -1;
-  const int row = s / a.map_div;
-  return row < a.src_rows ? row : -1;
+// Rows of X that rows r0 .. r0 + N of the result come from, -1 for none.
+template <int N>
+__device__ __forceinline__ void source_rows(const QuantArgs& a, int r0, int (&src)[N]) {
+  if (!a.rowmap) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) src[i] = r0 + i < a.rows ? r0 + i : -1;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    src[i] = -1;
+    if (r0 + i < a.rows && DG_IN(a.dbg, a.rowmap + r0 + i, 4, DBG_QUANTIZE)) src[i] = __ldg(a.rowmap + r0 + i);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (src[i] >= 0) src[i] /= a.map_div;
+    if (src[i] >= a.src_rows) src[i] = -1;
+  }
 }
 
 // n rows' groups of four columns, from `col` on: whole groups as one load each (VEC: rows
@@ -190,8 +201,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
   if (r0 >= a.rows_padded) return;
   Four<T> f[4][kRows];
   int src[kRows];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) src[i] = source_row(a, r0 + i);
+  source_rows(a, r0, src);
 #pragma unroll
   for (int b = 0; b < 4; ++b) load_rows<T, VEC>(f[b], a, src, g * 512 + b * 128 + 4 * lane);
 #pragma unroll
@@ -220,31 +230,73 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
   }
 }
 
-// Both orientations (or 128 x 128 scales): a CTA takes one 128 x 128 tile, kTileRows rows a
+// Both orientations (or 128 x 128 scales): a CTA takes 128 x 128 tiles, kTileRows rows a
 // warp and 4 columns a lane, held in registers.  Row maxima are warp reductions, each
-// row's scale worked out by one lane; column maxima meet in shared memory.  A thread's 8
-// rows of a column are 8 consecutive bytes of the transposed matrix: they are turned
-// round in a swizzled shared-memory tile and leave as 128-byte rows.  (16 rows a warp
-// spilled at three CTAs an SM and left too few warps at two: 47.0 us for 8192 x 4096 bf16.)
+// row's scale worked out by one lane; column maxima meet in shared memory, each column's
+// scale worked out by one thread.  A thread's 8 rows of a column are 8 consecutive bytes of the
+// transposed matrix: they are turned round in a swizzled shared-memory tile and leave as
+// 128-byte rows.
+// Many CTAs one after another overlap loading, converting and storing better than two that
+// go from tile to tile with the next one's loads under way: 36.5 against 47.3 us for
+// 8192 x 4096 bf16, both ways.  (16 rows a warp, which spilled: 47.0.)
 constexpr int kTileRows = 8;
 constexpr int kTileWarps = 128 / kTileRows;
 
-// kTileRows rows' codes (lane i: inverse scale of row i), then the columns' of a lane.
-template <bool E5M2, bool CAREFUL, typename T>
-__device__ __forceinline__ void row_codes(uint32_t (&c)[kTileRows], const Four<T> (&v)[kTileRows], float inv_mine) {
+// Lane that works out row i's scale, and the row of a lane (kTileRows: none).
+__device__ __forceinline__ int lane_of_row(int i) { return (i >> 1) * 8 + (i & 1); }
+__device__ __forceinline__ int row_of_lane(int lane) { return (lane & 7) < 2 ? (lane >> 3) * 2 + (lane & 1) : kTileRows; }
+
+// Largest magnitudes of the 8 rows, each in the lane of its row: two rows to a register, and
+// lanes halve the rows they hold as they exchange (6 exchanges; one reduction a row would
+// be 8 and as many selections more).  32-bit values: a reduction a row.
+template <typename T>
+__device__ __forceinline__ uint32_t row_maxima(const Four<T> (&v)[kTileRows], int lane) {
+  if constexpr (sizeof(T) == 4) {
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kTileRows; ++i) {
+      Peak<T> row;
+      row.take(v[i]);
+      const uint32_t m = __reduce_max_sync(kAll, row.row());
+      if (lane == lane_of_row(i)) mine = m;
+    }
+    return mine;
+  } else {
+    uint32_t k[4];  // rows 2i and 2i + 1
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = Peak<T>::most(v[2 * i].w.x & 0x7fff7fffu, v[2 * i].w.y & 0x7fff7fffu);
+      const uint32_t b = Peak<T>::most(v[2 * i + 1].w.x & 0x7fff7fffu, v[2 * i + 1].w.y & 0x7fff7fffu);
+      k[i] = Peak<T>::most(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+    }
+    const bool high = lane & 16, mid = lane & 8;
+    const uint32_t o0 = __shfl_xor_sync(kAll, high ? k[0] : k[2], 16), o1 = __shfl_xor_sync(kAll, high ? k[1] : k[3], 16);
+    const uint32_t k0 = Peak<T>::most(high ? k[2] : k[0], o0), k1 = Peak<T>::most(high ? k[3] : k[1], o1);
+    uint32_t m = Peak<T>::most(mid ? k1 : k0, __shfl_xor_sync(kAll, mid ? k0 : k1, 8));
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) m = Peak<T>::most(m, __shfl_xor_sync(kAll, m, d));
+    return Peak<T>::bits(lane & 1 ? m >> 16 : m & 0xffffu);
+  }
+}
+
+// kTileRows rows' codes (inverse scales: in the rows' lanes), then the columns' of a lane.
+template <bool E5M2, bool CAREFUL>
+__device__ __forceinline__ void row_codes(uint32_t (&c)[kTileRows], const float (&f)[kTileRows][4], float inv_mine) {
 #pragma unroll
   for (int i = 0; i < kTileRows; ++i)
-    c[i] = codes4<E5M2, CAREFUL>(v[i].at(0), v[i].at(1), v[i].at(2), v[i].at(3), __shfl_sync(kAll, inv_mine, i));
+    c[i] = codes4<E5M2, CAREFUL>(f[i][0], f[i][1], f[i][2], f[i][3], __shfl_sync(kAll, inv_mine, lane_of_row(i)));
 }
-template <bool E5M2, bool CAREFUL, typename T>
-__device__ __forceinline__ uint2 column_codes(const Four<T> (&v)[kTileRows], int j, float inv) {
-  return make_uint2(codes4<E5M2, CAREFUL>(v[0].at(j), v[1].at(j), v[2].at(j), v[3].at(j), inv),
-                    codes4<E5M2, CAREFUL>(v[4].at(j), v[5].at(j), v[6].at(j), v[7].at(j), inv));
+template <bool E5M2, bool CAREFUL>
+__device__ __forceinline__ uint2 column_codes(const float (&f)[kTileRows][4], int j, float inv) {
+  return make_uint2(codes4<E5M2, CAREFUL>(f[0][j], f[1][j], f[2][j], f[3][j], inv),
+                    codes4<E5M2, CAREFUL>(f[4][j], f[5][j], f[6][j], f[7][j], inv));
 }
 
 template <typename T, bool E5M2, bool VEC>
 __global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 1 : 2) quantize_tile_kernel(const QuantArgs a) {
-  __shared__ uint32_t col_max[kTileWarps][128];
+  alignas(16) __shared__ uint32_t col_max[kTileWarps][128];
+  alignas(16) __shared__ float col_inv[128];  // inverse scales of the columns
+  __shared__ uint32_t tile_max[4];
   __shared__ uint4 turn[128 * 8];  // [column][8-byte piece of rows ^ (column / 4 % 16)]
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -254,62 +306,87 @@ __global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 1 : 2) quant
   uint32_t live = 0;  // rows that exist
   {
     int src[kTileRows];
+    source_rows(a, row0, src);
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-      src[i] = source_row(a, row0 + i);
-      live |= uint32_t(src[i] >= 0) << i;
-    }
+    for (int i = 0; i < kTileRows; ++i) live |= uint32_t(src[i] >= 0) << i;
     load_rows<T, VEC>(v, a, src, col);
   }
-  Peak<T> peak;
+  bool careful = false;  // infinities or NaN: maxima over what is finite, careful conversions
+  if (a.qt || a.block_rows > 1) {
+    Peak<T> peak;
 #pragma unroll
-  for (int i = 0; i < kTileRows; ++i) peak.take(v[i]);
-  uint32_t cm[4] = {peak.column(0), peak.column(1), peak.column(2), peak.column(3)};
-  // infinities or NaN anywhere in the tile: maxima over what is finite, careful conversions
-  const bool careful = __syncthreads_or(max(max(cm[0], cm[1]), max(cm[2], cm[3])) >= kInf);
-  if (careful) {
+    for (int i = 0; i < kTileRows; ++i) peak.take(v[i]);
+    uint32_t cm[4] = {peak.column(0), peak.column(1), peak.column(2), peak.column(3)};
+    const bool wild = max(max(cm[0], cm[1]), max(cm[2], cm[3])) >= kInf;
+    if (wild) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      cm[j] = 0;
+      for (int j = 0; j < 4; ++j) {
+        cm[j] = 0;
 #pragma unroll
-      for (int i = 0; i < kTileRows; ++i) cm[j] = max(cm[j], finite_bits(v[i].at(j)));
+        for (int i = 0; i < kTileRows; ++i) cm[j] = max(cm[j], finite_bits(v[i].at(j)));
+      }
     }
-  }
-  *reinterpret_cast<uint4*>(&col_max[warp][4 * lane]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
-  __syncthreads();
+    *reinterpret_cast<uint4*>(&col_max[warp][4 * lane]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+    careful = __syncthreads_or(wild);
+    // one thread a column: its scale, its scale byte
+    if (threadIdx.x < 128) {
+      uint32_t m = 0;
 #pragma unroll
-  for (int w = 0; w < kTileWarps; ++w) {
-    const uint4 o = *reinterpret_cast<const uint4*>(&col_max[w][4 * lane]);
-    cm[0] = max(cm[0], o.x), cm[1] = max(cm[1], o.y), cm[2] = max(cm[2], o.z), cm[3] = max(cm[3], o.w);
-  }
-  uint32_t tile = 0;  // scale byte of the whole tile
-  if (a.block_rows > 1) tile = scale_byte<E5M2>(__reduce_max_sync(kAll, max(max(cm[0], cm[1]), max(cm[2], cm[3]))));
-  if (a.q) {
-    uint32_t mine = tile;  // lane i: scale byte of row i
-    if (a.block_rows == 1) {
-#pragma unroll
-      for (int i = 0; i < kTileRows; ++i) {
-        Peak<T> row;
-        row.take(v[i]);
-        uint32_t m = row.row();
-        if (careful)
-          m = max(max(finite_bits(v[i].at(0)), finite_bits(v[i].at(1))), max(finite_bits(v[i].at(2)), finite_bits(v[i].at(3))));
+      for (int w = 0; w < kTileWarps; ++w) m = max(m, col_max[w][threadIdx.x]);
+      if (a.block_rows > 1) {  // one scale for the tile
         m = __reduce_max_sync(kAll, m);
-        if (lane == i) mine = m;
+        if (lane == 0) tile_max[warp] = m;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        m = max(max(tile_max[0], tile_max[1]), max(tile_max[2], tile_max[3]));
+      }
+      const uint32_t byte = scale_byte<E5M2>(m);
+      col_inv[threadIdx.x] = inverse_scale(byte);
+      const int c = cb * 128 + int(threadIdx.x);
+      if (a.qt && c < a.cols_padded) {
+        uint8_t* const s = a.sqt + scale_at(c, rb, a.qt_groups);
+        if (DG_IN(a.dbg, s, 1, DBG_QUANTIZE)) *s = uint8_t(c < a.cols ? byte : 0u);
+      }
+      if (a.block_rows > 1 && threadIdx.x == 0) tile_max[0] = byte;
+    }
+    __syncthreads();
+  }
+  const uint32_t tile_scale = a.block_rows > 1 ? tile_max[0] : 0u;
+  const uint32_t peaks = a.q && a.block_rows == 1 ? row_maxima(v, lane) : 0u;
+  float f[kTileRows][4];
+#pragma unroll
+  for (int i = 0; i < kTileRows; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[i][j] = v[i].at(j);
+  if (a.q) {
+    uint32_t mine = tile_scale;  // scale byte of the lane's row
+    const int my_row = row0 + row_of_lane(lane);
+    bool careful_rows = careful;
+    if (a.block_rows == 1) {
+      mine = peaks;
+      careful_rows = __any_sync(kAll, mine >= kInf);
+      if (careful_rows) {
+#pragma unroll
+        for (int i = 0; i < kTileRows; ++i) {
+          const uint32_t m = __reduce_max_sync(kAll, max(max(finite_bits(f[i][0]), finite_bits(f[i][1])),
+                                                         max(finite_bits(f[i][2]), finite_bits(f[i][3]))));
+          if (lane == lane_of_row(i)) mine = m;
+        }
       }
       mine = scale_byte<E5M2>(mine);
+    } else if (my_row >= a.rows) {
+      mine = 0;
     }
+    const float inv = a.block_rows == 1 ? inverse_scale(mine) : col_inv[0];
     uint32_t c[kTileRows];
-    if (careful)
-      row_codes<E5M2, true>(c, v, inverse_scale(mine));
+    if (careful_rows)
+      row_codes<E5M2, true>(c, f, inv);
     else
-      row_codes<E5M2, false>(c, v, inverse_scale(mine));
-    uint8_t* const dst = a.q + int64_t(row0) * a.ldq + col;
+      row_codes<E5M2, false>(c, f, inv);
+    uint8_t* dst = a.q + int64_t(row0) * a.ldq + col;
     if (col + 4 <= a.cols) {
 #pragma unroll
-      for (int i = 0; i < kTileRows; ++i)
-        if (((live >> i) & 1u) && DG_IN(a.dbg, dst + i * a.ldq, 4, DBG_QUANTIZE))
-          *reinterpret_cast<uint32_t*>(dst + i * a.ldq) = c[i];
+      for (int i = 0; i < kTileRows; ++i, dst += a.ldq)
+        if (((live >> i) & 1u) && DG_IN(a.dbg, dst, 4, DBG_QUANTIZE)) *reinterpret_cast<uint32_t*>(dst) = c[i];
     } else if (col < a.cols) {
       for (int j = 0; j < a.cols - col; ++j)
 #pragma unroll
@@ -317,28 +394,18 @@ __global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 1 : 2) quant
           if (((live >> i) & 1u) && DG_IN(a.dbg, dst + i * a.ldq + j, 1, DBG_QUANTIZE))
             dst[i * a.ldq + j] = uint8_t(c[i] >> (8 * j));
     }
-    if (lane < kTileRows && row0 < a.rows_padded) {
-      uint8_t* const s = a.sq + scale_at(row0 + lane, cb, a.q_groups);
-      if (DG_IN(a.dbg, s, 1, DBG_QUANTIZE)) *s = uint8_t(row0 + lane < a.rows || a.block_rows == 1 ? mine : 0u);
+    if (row_of_lane(lane) < kTileRows && row0 < a.rows_padded) {
+      uint8_t* const s = a.sq + scale_at(my_row, cb, a.q_groups);
+      if (DG_IN(a.dbg, s, 1, DBG_QUANTIZE)) *s = uint8_t(mine);
     }
   }
   if (a.qt) {
-    uint32_t bytes[4];
+    const float4 inv = *reinterpret_cast<const float4*>(&col_inv[4 * lane]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      bytes[j] = a.block_rows == 1 ? scale_byte<E5M2>(cm[j]) : tile;
-      const float inv = inverse_scale(bytes[j]);
+      const float by = j == 0 ? inv.x : j == 1 ? inv.y : j == 2 ? inv.z : inv.w;
       reinterpret_cast<uint2*>(turn)[(4 * lane + j) * 16 + (warp ^ (lane & 15))] =
-          careful ? column_codes<E5M2, true>(v, j, inv) : column_codes<E5M2, false>(v, j, inv);
-    }
-    if (warp == 0) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (col + j < a.cols_padded) {
-          uint8_t* const s = a.sqt + scale_at(col + j, rb, a.qt_groups);
-          if (DG_IN(a.dbg, s, 1, DBG_QUANTIZE)) *s = uint8_t(col + j < a.cols || a.block_rows == 1 ? bytes[j] : 0u);
-        }
-      }
+          careful ? column_codes<E5M2, true>(f, j, by) : column_codes<E5M2, false>(f, j, by);
     }
     __syncthreads();
 #pragma unroll
