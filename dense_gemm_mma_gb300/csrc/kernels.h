@@ -343,6 +343,7 @@ struct ScParams {
   uint32_t idesc;     // tcgen05 instruction descriptor, scale ids zero
   int bn;             // sliced kernel: rows of A per tile at most (32, 64, 96 or 128; a call with several tiles of rows: 128)
   int stages;         // sliced kernel: ring depth
+  int part_rows;      // sliced kernel: rows of A in the partial tile (32, or bn)
   int slices;         // sliced kernel: CTAs of a cluster, each with kb_per_slice k-blocks of the tile
   int kb_per_slice;
   int* err;
@@ -364,7 +365,8 @@ int scaled_tile_stages(bool pair);
 // Sliced kernel: tiles of 128 rows of B x bn rows of A; maps: a (box 128 values x
 // 32 rows), b (box 128 values x 128 rows).  idesc: N zero.
 cudaError_t launch_scaled_sliced(const ScMaps& m, const ScParams& p, int grid, cudaStream_t s);
-int scaled_sliced_smem(int bn, int stages);
+int scaled_sliced_smem(int bn, int stages, int part_rows);
+int scaled_sliced_clusters(int slices);  // clusters of that many CTAs that can be resident at once, a CTA an SM
 
 // Rows of `cols` bytes (groups x rows of them, `ld` bytes apart, groups `group` bytes apart) copied
 // to rows of `ld_out` bytes, a multiple of 16: makes a code matrix whose rows the TMA cannot address one

@@ -119,30 +119,42 @@ enum ScKernel { SC_TILE, SC_PAIR, SC_SLICED };
 
 struct ScPick {
   ScKernel kernel = SC_TILE;
-  int bn = 128, slices = 1, stages = 0;
+  int bn = 128, slices = 1, stages = 0, part_rows = 32;
   int per_sm = 1;  // CTAs an SM holds at once
 };
 
-// Ring stages of the sliced kernel when an SM holds `per_sm` CTAs.
-int sliced_stages(int bn, int per_sm) {
+void set_sliced(ScPick* c, int slices, int per_sm) {
+  c->slices = slices;
+  c->per_sm = per_sm;
+  c->part_rows = slices > 1 ? c->bn : 32;
   const int room = per_sm == 1 ? kSmemMax : (kSmemMax + 1024) / per_sm - 1024;
-  int st = 8;
-  while (st > 2 && scaled_sliced_smem(bn, st) > room) --st;
-  return st;
+  c->stages = 8;
+  while (c->stages > 2 && scaled_sliced_smem(c->bn, c->stages, c->part_rows) > room) --c->stages;
 }
 
-// `rows` rows of A at most in a group's tiles, `tiles` tiles.
-ScPick pick_sliced(int64_t rows, int64_t tiles, int64_t k_blocks, int sms) {
+// Clusters of 1 .. 8 CTAs that the device holds at once (16 tiles in 8 slices, 128 CTAs,
+// took two waves: a cluster lies within one group of SMs).
+struct Residency {
+  int clusters[9];
+  explicit Residency(int sms) {
+    clusters[0] = 0;
+    clusters[1] = sms;
+    for (int s = 2; s <= 8; ++s) clusters[s] = scaled_sliced_clusters(s);
+  }
+};
+
+// `rows` rows of A at most in a tile, `tiles` tiles.  K is cut into as many slices as leave
+// every cluster resident at once, a CTA an SM (4096 x 4096, one row: 6.2 us in 4 slices,
+// 128 CTAs, against 7.9 in 5).  A slice may be empty: its CTA still takes its share of the rows that
+// the slices add up (33 x 1024 x 512, four k-blocks: 5.3 us in 8 slices, 6.4 in 2).
+ScPick pick_sliced(int64_t rows, int64_t tiles, int sms) {
+  static const Residency fits(sms);
   ScPick c;
   c.kernel = SC_SLICED;
   c.bn = int(std::min<int64_t>(128, round_up(rows, 32)));
-  // K slices until every SM has a CTA, each with two k-blocks at least
-  int64_t s = std::min<int64_t>({8, ceil_div(sms, std::max<int64_t>(tiles, 1)), std::max<int64_t>(1, k_blocks / 2)});
-  s = std::max<int64_t>(s, 1);
-  s = std::max<int64_t>(1, ceil_div(k_blocks, ceil_div(std::max<int64_t>(k_blocks, 1), s)));  // no empty slice
-  c.slices = int(s);
-  c.per_sm = tiles * s > sms && c.bn == 32 ? 2 : 1;
-  c.stages = sliced_stages(c.bn, c.per_sm);
+  int s = 8;
+  while (s > 1 && fits.clusters[s] < tiles) --s;
+  set_sliced(&c, s, 1);
   return c;
 }
 
@@ -150,35 +162,39 @@ ScPick pick_sliced(int64_t rows, int64_t tiles, int64_t k_blocks, int sms) {
 // the device; its rows are estimated from the capacity, which holds up to 127 empty rows a
 // group).  GEMM_SCALED_KERNEL=tile|pair|sliced and GEMM_SCALED_SLICES=n override it.
 ScPick pick(const Product& x, int sms) {
-  const int64_t kb = ceil_div(x.K, SC_BK), nb = ceil_div(x.N, 128);
+  const int64_t kb = ceil_div(x.K, SC_BK), nb = ceil_div(x.N, 128), mb = ceil_div(x.M, 128);
   ScPick c;
   if (x.group == SC_ROWS) {
     const int64_t per = std::max<int64_t>(1, x.M / x.groups - 127);
     const int64_t active = std::max<int64_t>(1, std::min(x.groups, x.M / 128));
     if (per <= 128)
-      c = pick_sliced(128, active * nb, kb, sms);
+      c = pick_sliced(128, active * nb, sms);
     else
       c.kernel = SC_PAIR;
+  } else if (x.group == SC_K) {
+    c.kernel = x.groups * mb * nb > sms ? SC_PAIR : SC_TILE;
   } else {
-    const int64_t mb = ceil_div(x.M, 128);
-    if (x.group == SC_DENSE && (x.M <= 128 || mb * nb < sms))
-      c = pick_sliced(x.M, mb * nb, kb, sms);
-    else
-      c.kernel = x.groups * ceil_div(x.M, 256) * ceil_div(x.N, 256) * 2 >= sms ? SC_PAIR : SC_TILE;
+    // 128 x 128 tiles on one CTA each while they fill one wave at most (200 x 6912 x 2048: 10.6
+    // us, pairs 12.3), 256 x 256 on pairs beyond (400 x 8192 x 8192: 27 us, 37 on single CTAs).
+    // Fewer tiles: K slices, if what they save of the K loop (0.22 us a k-block) pays for adding up
+    // the slices' rows (0.07 us a row and CTA).  735 x 6489: 800 rows 14.1 us in 3
+    // slices, 19.4 whole; 128 x 6912 x 2048: 11.8 in 2 slices, 10.5 whole.
+    c.kernel = mb * nb > sms ? SC_PAIR : SC_TILE;
+    if (mb * nb <= sms) {
+      const ScPick sl = pick_sliced(x.M, mb * nb, sms);
+      const double rows = double(std::min<int64_t>(x.M, 128)), s = sl.slices;
+      if (x.M <= 64 || 0.07 * rows / s < 0.22 * double(kb) * (1 - 1 / s)) c = sl;
+    }
   }
   if (const char* f = std::getenv("GEMM_SCALED_KERNEL")) {
     if (!std::strcmp(f, "tile")) c.kernel = SC_TILE;
     if (!std::strcmp(f, "pair")) c.kernel = SC_PAIR;
     if (!std::strcmp(f, "sliced") && x.group != SC_K && c.kernel != SC_SLICED)
-      c = pick_sliced(x.group == SC_ROWS ? 128 : x.M, ceil_div(x.M, 128) * nb, kb, sms);
+      c = pick_sliced(x.group == SC_ROWS ? 128 : x.M, mb * nb, sms);
   }
   if (c.kernel == SC_SLICED) {
     const int s = env_int("GEMM_SCALED_SLICES", 0);
-    if (s >= 1 && s <= 8) {
-      c.slices = s;
-      c.per_sm = 1;
-      c.stages = sliced_stages(c.bn, 1);
-    }
+    if (s >= 1 && s <= 8) set_sliced(&c, s, 1);
   }
   return c;
 }
@@ -266,6 +282,7 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   p.slope = x.epi.slope;
   p.bn = c.bn;
   p.stages = c.stages;
+  p.part_rows = c.part_rows;
   p.slices = c.slices;
   p.kb_per_slice = int(ceil_div(p.k_blocks, c.slices));
   p.err = plan->err;

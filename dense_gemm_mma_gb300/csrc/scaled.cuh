@@ -153,11 +153,26 @@ struct ScSets {
 // Index of the warp, known to be the same in all its lanes.
 __device__ __forceinline__ int sc_warp() { return __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0); }
 
-// A whole warp's wait (bounded): true in every lane, or false in every lane.  `ready`: the
-// barrier has been seen complete already.
-__device__ __forceinline__ bool sc_wait(bool ready, uint32_t bar, uint32_t parity, const Watch& w, int code) {
-  if (__all_sync(0xffffffffu, ready)) return true;
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, w, code));
+// A whole warp's bounded wait: true in every lane, or false in every lane, which then
+// leave their loop (the limit ran out, or another role of the CTA gave up).  CLUSTER:
+// threads of the peer CTA arrive on the barrier.  The loop is spelled out here: a call on the slow
+// path would make every value of the caller's loop leave the uniform registers.
+template <bool CLUSTER>
+__device__ __forceinline__ bool sc_wait(uint32_t bar, uint32_t parity, const Watch& w, int code) {
+  uint64_t t0 = 0;
+  while (true) {
+    const bool done = CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, done)) return true;
+    const uint64_t t = global_timer_ns();
+    if (t0 == 0) t0 = t;
+    const bool late = t - t0 > w.limit_ns;
+    if (__any_sync(0xffffffffu, late)) {
+      *w.abort = 1;
+      if ((threadIdx.x & 31) == 0) atomicOr(w.err, code);
+      return false;
+    }
+    if (__any_sync(0xffffffffu, *w.abort != 0)) return false;
+  }
 }
 
 // v <- act(v), every run-time choice outside the unrolled loops; GELU and SiLU only if ALL.

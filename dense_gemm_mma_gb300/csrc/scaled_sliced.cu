@@ -15,8 +15,12 @@
 //
 //  - warp 0: TMA producer; warp 1: MMA issuer (two accumulators,
 //    so a tile's MMAs overlap the previous one's epilogue);
-//  - warps 2-5: accumulator lanes -> partial tile [32 rows of A][128 rows of B] in shared
-//    memory, then whole rows of it, 512 bytes a warp, to D; 32 rows of A at a time.
+//  - warps 2-5: accumulator lanes -> partial tile [rows of A][128 rows of B] in shared
+//    memory, then whole rows of it, 512 bytes a warp, to D.  The partial tile holds all rows of a
+//    tile where its CTAs meet (an exchange takes ~1.5 us whatever its size), 32 at a time where a CTA
+//    has K to itself and the room serves the ring better.
+#include <type_traits>
+
 #include "scaled.cuh"
 
 namespace dg {
@@ -29,16 +33,15 @@ constexpr int kMaxSlices = 8;
 constexpr int kWeights = 128 * SC_BK;  // bytes of B per stage
 constexpr int kScales = 1024;          // scale tiles of B's 128 rows and of the block of A's rows
 constexpr int kRowsA = 32 * SC_BK;     // bytes of a load of A: 32 rows
-constexpr int kPart = 32 * 128 * 4;    // partial tile: 32 rows of A
 
 __host__ __device__ constexpr int stage_bytes(int bn) { return kWeights + bn * SC_BK; }
 // ring (every operand tile is 1024-byte aligned), scales, partial tile, barriers, table
 __host__ __device__ constexpr int off_scales(int bn, int stages) { return stages * stage_bytes(bn); }
 __host__ __device__ constexpr int off_part(int bn, int stages) { return off_scales(bn, stages) + stages * kScales; }
-__host__ __device__ constexpr int off_bar(int bn, int stages) { return off_part(bn, stages) + kPart; }
+__host__ __device__ constexpr int off_bar(int bn, int stages, int part) { return off_part(bn, stages) + part * 128 * 4; }
 constexpr int kBarBytes = (2 * kMaxStages + 2 + 2 + 1 + 2) * 8;  // full, empty, tmem_full, tmem_empty, drain, part_full, part_free
-__host__ __device__ constexpr int off_misc(int bn, int stages) { return off_bar(bn, stages) + kBarBytes; }
-__host__ __device__ constexpr int off_table(int bn, int stages) { return off_misc(bn, stages) + 16; }
+__host__ __device__ constexpr int off_misc(int bn, int stages, int part) { return off_bar(bn, stages, part) + kBarBytes; }
+__host__ __device__ constexpr int off_table(int bn, int stages, int part) { return off_misc(bn, stages, part) + 16; }
 
 // Tensor-memory columns: two accumulators of bn, then four sets of 8 scale columns
 // (B's rows, A's rows).
@@ -46,6 +49,10 @@ __host__ __device__ constexpr uint32_t tmem_cols(int bn) {
   return 2 * bn + 32 <= 128 ? 128u : 2 * bn + 32 <= 256 ? 256u : 512u;
 }
 
+// ALL: GELU and SiLU as well.  A kernel of their own: inlined into every variant of the rows'
+// loop they fill the instruction cache, and as a call they slowed the other warps' loops (one row,
+// 8192 x 8192: 11.6 us, 14.7 with the call).
+template <bool ALL>
 __global__ void __launch_bounds__(kThreads)
     scaled_sliced_kernel(const __grid_constant__ ScMaps maps, const __grid_constant__ ScParams p) {
   const int bn = p.bn, S = p.stages, slices = p.slices;
@@ -56,12 +63,12 @@ __global__ void __launch_bounds__(kThreads)
   uint8_t* const sbase = smem_raw + (base - raw);
   const int warp = sc_warp();
   const int lane = threadIdx.x & 31;
-  const uint32_t full0 = base + off_bar(bn, S), empty0 = full0 + 8 * kMaxStages;
+  const uint32_t full0 = base + off_bar(bn, S, p.part_rows), empty0 = full0 + 8 * kMaxStages;
   const uint32_t tfull0 = empty0 + 8 * kMaxStages, tempty0 = tfull0 + 16, drain_bar = tempty0 + 16;
   const uint32_t part_full = drain_bar + 8, part_free = part_full + 8;
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sbase + off_misc(bn, S));
-  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sbase + off_misc(bn, S) + 4);
-  int* const table = reinterpret_cast<int*>(sbase + off_table(bn, S));
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sbase + off_misc(bn, S, p.part_rows));
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sbase + off_misc(bn, S, p.part_rows) + 4);
+  int* const table = reinterpret_cast<int*>(sbase + off_table(bn, S, p.part_rows));
   const uint32_t cols = tmem_cols(bn);
 
   if (threadIdx.x == 0) {
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(kThreads)
       const int sb_row = x.zb * p.sb_group + (x.n0 / 128) * p.sb_cols, sa_row = (x.row0 / 128) * p.sa_cols;
       for (int kb = x.kb0; kb < x.kb1; ++kb) {
         const uint32_t eb = empty0 + 8 * stage, fb = full0 + 8 * stage;
-        if (!sc_wait(mbar_try_wait(eb, phase ^ 1u), eb, phase ^ 1u, w, WAIT_PRODUCER_EMPTY)) {
+        if (!sc_wait<false>(eb, phase ^ 1u, w, WAIT_PRODUCER_EMPTY)) {
           ok = false;
           break;
         }
@@ -147,11 +154,11 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
     }
-    if (!ok && lane == 0) {
+    if (!ok) {
       // Let the loads already in flight land before the CTA can exit.
       for (int s = 0; s < S; ++s) {
         const int n_s = issued > s ? (issued - s + S - 1) / S : 0;
-        if (n_s > 0) wait_bar(full0 + 8 * s, (uint32_t)((n_s - 1) & 1), w, 0);
+        if (n_s > 0) sc_wait<false>(full0 + 8 * s, (uint32_t)((n_s - 1) & 1), w, 0);
       }
     }
   } else if (warp == 1) {
@@ -165,19 +172,19 @@ __global__ void __launch_bounds__(kThreads)
       const ScUnit x = unit_of(u, &cursor);
       if (x.kb0 >= x.kb1) continue;  // no K at all
       const int acc = tiles & 1;
-      if (tiles > 1 && !sc_wait(false, tempty0 + 8 * acc, ((tiles - 2) >> 1) & 1, w, WAIT_MMA_TMEM_EMPTY)) break;
+      if (tiles > 1 && !sc_wait<false>(tempty0 + 8 * acc, ((tiles - 2) >> 1) & 1, w, WAIT_MMA_TMEM_EMPTY)) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + uint32_t(acc * bn);
       const uint32_t mma_n = uint32_t(pieces_of(x)) * 32;
       for (int kb = x.kb0; kb < x.kb1; ++kb) {
-        if (!sc_wait(false, full0 + 8 * stage, phase, w, WAIT_MMA_FULL)) {
+        if (!sc_wait<false>(full0 + 8 * stage, phase, w, WAIT_MMA_FULL)) {
           ok = false;
           break;
         }
         if (kb == x.kb0 || (kb & 3) == 0) {
           const int old = sets.last_user();
           if (old >= 0 && old > it - S &&
-              !sc_wait(false, empty0 + 8 * (old % S), uint32_t(old / S) & 1u, w, WAIT_MMA_FULL)) {
+              !sc_wait<false>(empty0 + 8 * (old % S), uint32_t(old / S) & 1u, w, WAIT_MMA_FULL)) {
             ok = false;
             break;
           }
@@ -206,7 +213,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     // Every MMA issued by this warp completes before tensor memory is freed.
     tc_commit_one<false>(drain_bar, one);
-    sc_wait(false, drain_bar, 0, w, WAIT_DRAIN);
+    sc_wait<false>(drain_bar, 0, w, WAIT_DRAIN);
   } else {
     // ------------------------------------------------------------ epilogue
     const int e = warp - 2;
@@ -229,69 +236,92 @@ __global__ void __launch_bounds__(kThreads)
       const bool empty = x.kb0 >= x.kb1;
       const int acc = tiles & 1;
       if (!empty) {
-        if (!__all_sync(0xffffffffu, wait_bar(tfull0 + 8 * acc, (tiles >> 1) & 1, w, WAIT_EPI_TMEM_FULL))) break;
+        if (!sc_wait<false>(tfull0 + 8 * acc, (tiles >> 1) & 1, w, WAIT_EPI_TMEM_FULL)) break;
         tc_fence_after();
         ++tiles;
       }
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc * bn);
-      const int pieces = pieces_of(x);
-      for (int c = 0; c < pieces; ++c, ++done) {
-        uint32_t r[32];
-        if (!empty) {
-          tmem_ld_32x32b_x32(t_row + 32 * c, r);
-          tmem_ld_wait(r);
-          if (c + 1 == pieces) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tempty0 + 8 * acc);
-            __syncwarp();
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = 0u;
-        }
-        // the partials of the 32 rows before these have been read by every CTA
-        if (done > 0 && !__all_sync(0xffffffffu, wait_bar_cluster(part_free, (done - 1) & 1, w, WAIT_SLICES))) {
+      const int pieces = pieces_of(x), round = p.part_rows / 32;
+      for (int c0 = 0; c0 < pieces; c0 += round, ++done) {
+        // the partials of the round before this one have been read by every CTA
+        if (done > 0 && !sc_wait<true>(part_free, (done - 1) & 1, w, WAIT_SLICES)) {
           ok = false;
           break;
         }
+        const int c1 = min(pieces, c0 + round);
+        for (int c = c0; c < c1; ++c) {
+          uint32_t r[32];
+          if (!empty) {
+            tmem_ld_32x32b_x32(t_row + 32 * c, r);
+            tmem_ld_wait(r);
+          } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) part[j * 128 + 32 * q + lane] = __uint_as_float(r[j]);
+            for (int j = 0; j < 32; ++j) r[j] = 0u;
+          }
+          float* const at = part + (c - c0) * 32 * 128 + 32 * q + lane;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) at[j * 128] = __uint_as_float(r[j]);
+        }
+        if (!empty && c1 == pieces) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty0 + 8 * acc);
+        }
         arrive_all(part_full);
-        if (!__all_sync(0xffffffffu, wait_bar_cluster(part_full, done & 1, w, WAIT_SLICES))) {
+        if (!sc_wait<true>(part_full, done & 1, w, WAIT_SLICES)) {
           ok = false;
           break;
         }
-        const int live = min(32, x.row_end - x.row0 - 32 * c);
+        const int live = min(p.part_rows, x.row_end - x.row0 - 32 * c0);
         const int col = x.n0 + 4 * lane;
-        for (int t = int(rank) + slices * e; t < live; t += slices * kEpiWarps) {
-          float v[4] = {0.f, 0.f, 0.f, 0.f};
-          const uint32_t at = part_addr + uint32_t(t * 128 + 4 * lane) * 4u;
-          float4 f[kMaxSlices];
+        const int n = min(4, p.N - col);
+        // this warp's rows, several at a time: as many loads in flight whatever the slices
+        auto finish_rows = [&](auto rows_c, auto slices_c) {
+          constexpr int R = decltype(rows_c)::value, MS = decltype(slices_c)::value;
+          for (int t0 = int(rank) + slices * e; t0 < live; t0 += slices * kEpiWarps * R) {
+            float4 f[R][MS];
 #pragma unroll
-          for (int s = 0; s < kMaxSlices; ++s)
-            if (s < slices) f[s] = ld_cluster_f4(mapa_shared(at, uint32_t(s)));
+            for (int i = 0; i < R; ++i) {
+              const int t = t0 + i * slices * kEpiWarps;
+              const uint32_t at = part_addr + uint32_t(t * 128 + 4 * lane) * 4u;
 #pragma unroll
-          for (int s = 0; s < kMaxSlices; ++s)
-            if (s < slices) v[0] += f[s].x, v[1] += f[s].y, v[2] += f[s].z, v[3] += f[s].w;
-          const int n = min(4, p.N - col);
-          if (n <= 0) continue;
-          uint8_t* const dst = static_cast<uint8_t*>(p.d) + (int64_t(x.row0 + 32 * c + t) * p.ldd + col) * es;
-          if (!DG_IN(p.dbg, dst, n * es, DBG_SCALED)) continue;
-          const bool whole = wide && n == 4;
+              for (int s = 0; s < MS; ++s)
+                if (s < slices && t < live) f[i][s] = MS == 1 ? ld_shared_f4(at) : ld_cluster_f4(mapa_shared(at, uint32_t(s)));
+            }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i] *= p.alpha;
-            if (p.beta != 0.f && i < n) v[i] = fmaf(p.beta, sc_load1(dst + i * es, p.out_kind), v[i]);
+            for (int i = 0; i < R; ++i) {
+              const int t = t0 + i * slices * kEpiWarps;
+              if (t >= live || n <= 0) continue;
+              float v[4] = {f[i][0].x, f[i][0].y, f[i][0].z, f[i][0].w};
+#pragma unroll
+              for (int s = 1; s < MS; ++s)
+                if (s < slices) v[0] += f[i][s].x, v[1] += f[i][s].y, v[2] += f[i][s].z, v[3] += f[i][s].w;
+              uint8_t* const dst = static_cast<uint8_t*>(p.d) + (int64_t(x.row0 + 32 * c0 + t) * p.ldd + col) * es;
+              if (!DG_IN(p.dbg, dst, n * es, DBG_SCALED)) continue;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                v[j] *= p.alpha;
+                if (p.beta != 0.f && j < n) v[j] = fmaf(p.beta, sc_load1(dst + j * es, p.out_kind), v[j]);
+              }
+              sc_act<ALL>(v, p.act, p.slope);
+              if (wide && n == 4 && es == 4)
+                *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+              else if (wide && n == 4)
+                *reinterpret_cast<uint2*>(dst) =
+                    make_uint2(sc_pack2(v[0], v[1], p.out_kind), sc_pack2(v[2], v[3], p.out_kind));
+              else
+                for (int j = 0; j < n; ++j) sc_store1(dst + j * es, v[j], p.out_kind);
+            }
           }
-          sc_act<true>(v, p.act, p.slope);
-          if (whole && es == 4)
-            *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-          else if (whole)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(sc_pack2(v[0], v[1], p.out_kind), sc_pack2(v[2], v[3], p.out_kind));
-          else
-            for (int i = 0; i < n; ++i) sc_store1(dst + i * es, v[i], p.out_kind);
-        }
+        };
+        if (slices == 1)
+          finish_rows(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+        else if (slices <= 2)
+          finish_rows(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+        else if (slices <= 4)
+          finish_rows(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+        else
+          finish_rows(std::integral_constant<int, 1>{}, std::integral_constant<int, kMaxSlices>{});
         arrive_all(part_free);
       }
     }
@@ -312,25 +342,60 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-int scaled_sliced_smem(int bn, int stages) {
-  return off_table(bn, stages) + (SC_MAX_GROUPS + 1) * 4 + 1024;  // + slack for 1024-B alignment
+int scaled_sliced_smem(int bn, int stages, int part_rows) {
+  return off_table(bn, stages, part_rows) + (SC_MAX_GROUPS + 1) * 4 + 1024;  // + slack for 1024-B alignment
 }
 
-cudaError_t launch_scaled_sliced(const ScMaps& m, const ScParams& p, int grid, cudaStream_t s) {
-  auto kern = scaled_sliced_kernel;
+namespace {
+cudaError_t set_limits() {
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (bit == 0 || (ready.load(std::memory_order_acquire) & bit) == 0) {
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    cudaError_t err =
+        cudaFuncSetAttribute(scaled_sliced_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    if (err == cudaSuccess)
+      err = cudaFuncSetAttribute(scaled_sliced_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
     if (err != cudaSuccess) return err;
     ready.fetch_or(bit, std::memory_order_release);
   }
+  return cudaSuccess;
+}
+}  // namespace
+
+int scaled_sliced_clusters(int slices) {
+  if (set_limits() != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(slices));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 160 * 1024;  // one CTA an SM
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(slices);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, scaled_sliced_kernel<true>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+cudaError_t launch_scaled_sliced(const ScMaps& m, const ScParams& p, int grid, cudaStream_t s) {
+  auto kern = p.act >= 3 ? scaled_sliced_kernel<true> : scaled_sliced_kernel<false>;
+  const cudaError_t err = set_limits();
+  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = size_t(scaled_sliced_smem(p.bn, p.stages));
+  cfg.dynamicSmemBytes = size_t(scaled_sliced_smem(p.bn, p.stages, p.part_rows));
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int n = 0;

@@ -157,11 +157,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int unit0 = PAIR ? int(blockIdx.x) / 2 : int(blockIdx.x);
   const int step = PAIR ? int(gridDim.x) / 2 : int(gridDim.x);
   const Watch w{abort_flag, p.err, p.timeout_ns};
-  // Bounded wait on a barrier that the peer CTA's threads arrive on.
-  auto wait_peers = [&](uint32_t bar, uint32_t parity, int code) {
-    if constexpr (PAIR) return wait_bar_cluster(bar, parity, w, code);
-    return wait_bar(bar, parity, w, code);
-  };
   const uint32_t one = lane == 0;  // the lane that issues
 
   if (warp == 0) {
@@ -175,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int sa_row = (m0 / 128) * p.sa_cols, sb_row = x.zb * p.sb_group + (x.n0 / 128) * p.sb_cols;
       for (int kb = x.kb0; kb < x.kb1; ++kb) {
         const uint32_t eb = empty0 + 8 * stage, fb = full0 + 8 * stage;
-        if (!sc_wait(mbar_try_wait(eb, phase ^ 1u), eb, phase ^ 1u, w, WAIT_PRODUCER_EMPTY)) {
+        if (!sc_wait<false>(eb, phase ^ 1u, w, WAIT_PRODUCER_EMPTY)) {
           ok = false;
           break;
         }
@@ -202,11 +197,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!ok && lane == 0) {
+    if (!ok && leader) {
       // Let the loads already in flight land before the CTA can exit.
       for (int s = 0; s < S; ++s) {
         const int n_s = issued > s ? (issued - s + S - 1) / S : 0;
-        if (n_s > 0 && leader) wait_bar(full0 + 8 * s, (uint32_t)((n_s - 1) & 1), w, 0);
+        if (n_s > 0) sc_wait<false>(full0 + 8 * s, (uint32_t)((n_s - 1) & 1), w, 0);
       }
     }
   } else if (warp == 1) {
@@ -226,18 +221,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // drained (and with them the whole tile before it).  Separate ones: this
         // accumulator's last tile has.
         if (C::OVERLAP > 0) {
-          if (tiles > 0 && !__all_sync(0xffffffffu, wait_peers(tempty0 + 8 * (acc ^ 1), ((tiles - 1) >> 1) & 1,
-                                                               WAIT_MMA_TMEM_EMPTY)))
-            break;
+          if (tiles > 0 && !sc_wait<PAIR>(tempty0 + 8 * (acc ^ 1), ((tiles - 1) >> 1) & 1, w, WAIT_MMA_TMEM_EMPTY)) break;
         } else {
-          if (tiles > 1 &&
-              !__all_sync(0xffffffffu, wait_peers(tempty0 + 8 * acc, ((tiles - 2) >> 1) & 1, WAIT_MMA_TMEM_EMPTY)))
-            break;
+          if (tiles > 1 && !sc_wait<PAIR>(tempty0 + 8 * acc, ((tiles - 2) >> 1) & 1, w, WAIT_MMA_TMEM_EMPTY)) break;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + uint32_t(acc ? C::ACC1 : 0);
         for (int kb = x.kb0; kb < x.kb1; ++kb) {
-          if (!sc_wait(ready, full0 + 8 * stage, phase, w, WAIT_MMA_FULL)) {
+          if (!__all_sync(0xffffffffu, ready) && !sc_wait<false>(full0 + 8 * stage, phase, w, WAIT_MMA_FULL)) {
             ok = false;
             break;
           }
@@ -247,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kb == x.kb0 || (kb & 3) == 0) {
             const int old = sets.last_user();
             if (old >= 0 && old > it - S &&
-                !sc_wait(false, empty0 + 8 * (old % S), uint32_t(old / S) & 1u, w, WAIT_MMA_FULL)) {
+                !sc_wait<false>(empty0 + 8 * (old % S), uint32_t(old / S) & 1u, w, WAIT_MMA_FULL)) {
               ok = false;
               break;
             }
@@ -281,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit(drain_bar);
       }
       __syncwarp();
-      sc_wait(false, drain_bar, 0, w, WAIT_DRAIN);
+      sc_wait<false>(drain_bar, 0, w, WAIT_DRAIN);
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -304,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool empty = x.kb0 >= x.kb1;
         const int acc = tiles & 1;
         if (!empty) {
-          if (!__all_sync(0xffffffffu, wait_peers(tfull0 + 8 * acc, (tiles >> 1) & 1, WAIT_EPI_TMEM_FULL))) break;
+          if (!sc_wait<false>(tfull0 + 8 * acc, (tiles >> 1) & 1, w, WAIT_EPI_TMEM_FULL)) break;
           tc_fence_after();
           ++tiles;
         }
