@@ -176,6 +176,10 @@ cudaError_t launch_gemm_tc(int bn, int mode, const CUtensorMap& a, const CUtenso
 // are visible.  In a kernel launched normally it returns at once.
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets a dependent grid be scheduled once every CTA of this one has called it (or exited): its
+// launch and prologue overlap this grid's tail.
+__device__ __forceinline__ void allow_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Debug-build checks (see DbgSite): true when the access may go ahead.
 #ifdef DG_DEBUG
 __device__ __forceinline__ bool dbg_in(const DbgSpans& d, const void* ptr, int64_t bytes, int site) {
@@ -343,7 +347,7 @@ struct ScParams {
   uint32_t idesc;     // tcgen05 instruction descriptor, scale ids zero
   int bn;             // sliced kernel: rows of A per tile at most (32, 64, 96 or 128; a call with several tiles of rows: 128)
   int stages;         // sliced kernel: ring depth
-  int part_rows;      // sliced kernel: rows of A in the partial tile (32, or bn)
+  int part_rows;      // sliced kernel: rows of A in the partial tile (bn; one slice: 32)
   int slices;         // sliced kernel: CTAs of a cluster, each with kb_per_slice k-blocks of the tile
   int kb_per_slice;
   int* err;

@@ -158,6 +158,9 @@ ScPick pick_sliced(int64_t rows, int64_t tiles, int sms) {
   return c;
 }
 
+// Rows of a group up to which the sliced kernel is faster than 128 x 128 tiles.
+constexpr int64_t kFewRows = 48;
+
 // Which kernel a product takes, by sizes alone (the counts of a grouped call are on
 // the device; its rows are estimated from the capacity, which holds up to 127 empty rows a
 // group).  GEMM_SCALED_KERNEL=tile|pair|sliced and GEMM_SCALED_SLICES=n override it.
@@ -167,12 +170,12 @@ ScPick pick(const Product& x, int sms) {
   if (x.group == SC_ROWS) {
     const int64_t per = std::max<int64_t>(1, x.M / x.groups - 127);
     const int64_t active = std::max<int64_t>(1, std::min(x.groups, x.M / 128));
-    if (per <= 128)
+    if (per <= kFewRows)
       c = pick_sliced(128, active * nb, sms);
     else
-      c.kernel = SC_PAIR;
+      c.kernel = per < 256 ? SC_TILE : SC_PAIR;
   } else if (x.group == SC_K) {
-    c.kernel = x.groups * mb * nb > sms ? SC_PAIR : SC_TILE;
+    c.kernel = x.K / x.groups < 512 ? SC_TILE : SC_PAIR;
   } else {
     // 128 x 128 tiles on one CTA each while they fill one wave at most (200 x 6912 x 2048: 10.6
     // us, pairs 12.3), 256 x 256 on pairs beyond (400 x 8192 x 8192: 27 us, 37 on single CTAs).

@@ -148,8 +148,9 @@ __device__ __forceinline__ void sort_lane(uint32_t (&key)[P], int (&ex)[P]) {
 
 // The warp's best expert; its lane moves on to its next one.
 template <int P>
-__device__ __forceinline__ int take_best(uint32_t (&key)[P], int (&ex)[P], int lane) {
+__device__ __forceinline__ int take_best(uint32_t (&key)[P], int (&ex)[P], int lane, uint32_t* value) {
   const uint32_t best = __reduce_max_sync(kAll, key[0]);
+  *value = best;
   const int owner = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
   const int expert = __shfl_sync(kAll, ex[0], owner);
   if (lane == owner) {
@@ -181,7 +182,7 @@ template <int P>
 __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
   wait_prior_grid();
   const int lane = threadIdx.x & 31;
-  const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int t = int(blockIdx.x * 4 + (threadIdx.x >> 5));
   if (t >= a.tokens) return;
   const int run = (a.experts + 31) / 32, first = lane * run;
   float x[P];
@@ -243,12 +244,15 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
       for (int i = 0; i < P; ++i) key[i] = min(key[i], kOutside);
   }
   int expert = -1;  // lane j: choice j
+  uint32_t best = kNone;
   for (int j = 0; j < a.top_k; ++j) {
-    const int e = take_best(key, ex, lane);
-    if (lane == j) expert = e;
+    uint32_t k;
+    const int e = take_best(key, ex, lane, &k);
+    if (lane == j) expert = e, best = k;
   }
-  // the chosen ones' scores, from their logits again (a few loads that hit L1)
-  const float mine = logit(a, t, expert);
+  // the chosen ones' scores, from the key where it is the logit, else from the logits again
+  // (a few loads that hit L1)
+  const float mine = !by_logit ? logit(a, t, expert) : expert >= 0 ? key_value(best) : kNegInf;
   float score = mine == kNegInf ? 0.f : scorer.score(mine);
   if (a.renormalize) {
     const float sum = warp_sum(score);
@@ -269,7 +273,7 @@ template <int P>
 __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) {
   wait_prior_grid();
   const int lane = threadIdx.x & 31;
-  const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int t = int(blockIdx.x * 4 + (threadIdx.x >> 5));
   if (t >= a.tokens) return;
   const int run = (a.experts + 31) / 32, first = lane * run;
   float x[P], ds[P];

@@ -16,9 +16,9 @@
 //  - warp 0: TMA producer; warp 1: MMA issuer (two accumulators,
 //    so a tile's MMAs overlap the previous one's epilogue);
 //  - warps 2-5: accumulator lanes -> partial tile [rows of A][128 rows of B] in shared
-//    memory, then whole rows of it, 512 bytes a warp, to D.  The partial tile holds all rows of a
-//    tile where its CTAs meet (an exchange takes ~1.5 us whatever its size), 32 at a time where a CTA
-//    has K to itself and the room serves the ring better.
+//    memory, then whole rows of it, 512 bytes a warp, to D.  All rows of a tile in one exchange: it
+//    takes ~1.5 us whatever its size.  Where a CTA has K to itself nothing is exchanged: each warp turns
+//    its 32 columns of D round in 4 KB of its own, 32 rows at a time, and the ring has the room.
 #include <type_traits>
 
 #include "scaled.cuh"
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads)
     tmem_relinquish();
   }
   wait_prior_grid();
-  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) allow_next_grid();
   if (warp == 2 && p.group == SC_ROWS) sc_tile_table(p, bn, table);
   tc_fence_before();
   if (slices > 1)
@@ -230,8 +230,7 @@ __global__ void __launch_bounds__(kThreads)
       if (lane < slices) mbar_arrive_cluster(mapa_shared(bar, uint32_t(lane)));
       __syncwarp();
     };
-    bool ok = true;
-    for (int u = unit0; u < units && ok; u += step) {
+    for (int u = unit0; u < units; u += step) {
       const ScUnit x = unit_of(u, &cursor);
       const bool empty = x.kb0 >= x.kb1;
       const int acc = tiles & 1;
@@ -241,89 +240,104 @@ __global__ void __launch_bounds__(kThreads)
         ++tiles;
       }
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc * bn);
-      const int pieces = pieces_of(x), round = p.part_rows / 32;
-      for (int c0 = 0; c0 < pieces; c0 += round, ++done) {
-        // the partials of the round before this one have been read by every CTA
-        if (done > 0 && !sc_wait<true>(part_free, (done - 1) & 1, w, WAIT_SLICES)) {
-          ok = false;
-          break;
-        }
-        const int c1 = min(pieces, c0 + round);
-        for (int c = c0; c < c1; ++c) {
-          uint32_t r[32];
-          if (!empty) {
-            tmem_ld_32x32b_x32(t_row + 32 * c, r);
-            tmem_ld_wait(r);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = 0u;
-          }
-          float* const at = part + (c - c0) * 32 * 128 + 32 * q + lane;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) at[j * 128] = __uint_as_float(r[j]);
-        }
-        if (!empty && c1 == pieces) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(tempty0 + 8 * acc);
-        }
-        arrive_all(part_full);
-        if (!sc_wait<true>(part_full, done & 1, w, WAIT_SLICES)) {
-          ok = false;
-          break;
-        }
-        const int live = min(p.part_rows, x.row_end - x.row0 - 32 * c0);
-        const int col = x.n0 + 4 * lane;
+      const int pieces = pieces_of(x);
+      // v[0 .. n) of row `row`, columns from `col` on, to D
+      auto store = [&](float (&v)[4], int row, int col) {
         const int n = min(4, p.N - col);
-        // this warp's rows, several at a time: as many loads in flight whatever the slices
-        auto finish_rows = [&](auto rows_c, auto slices_c) {
-          constexpr int R = decltype(rows_c)::value, MS = decltype(slices_c)::value;
-          for (int t0 = int(rank) + slices * e; t0 < live; t0 += slices * kEpiWarps * R) {
-            float4 f[R][MS];
+        if (n <= 0) return;
+        uint8_t* const dst = static_cast<uint8_t*>(p.d) + (int64_t(row) * p.ldd + col) * es;
+        if (!DG_IN(p.dbg, dst, n * es, DBG_SCALED)) return;
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-              const int t = t0 + i * slices * kEpiWarps;
-              const uint32_t at = part_addr + uint32_t(t * 128 + 4 * lane) * 4u;
-#pragma unroll
-              for (int s = 0; s < MS; ++s)
-                if (s < slices && t < live) f[i][s] = MS == 1 ? ld_shared_f4(at) : ld_cluster_f4(mapa_shared(at, uint32_t(s)));
-            }
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-              const int t = t0 + i * slices * kEpiWarps;
-              if (t >= live || n <= 0) continue;
-              float v[4] = {f[i][0].x, f[i][0].y, f[i][0].z, f[i][0].w};
-#pragma unroll
-              for (int s = 1; s < MS; ++s)
-                if (s < slices) v[0] += f[i][s].x, v[1] += f[i][s].y, v[2] += f[i][s].z, v[3] += f[i][s].w;
-              uint8_t* const dst = static_cast<uint8_t*>(p.d) + (int64_t(x.row0 + 32 * c0 + t) * p.ldd + col) * es;
-              if (!DG_IN(p.dbg, dst, n * es, DBG_SCALED)) continue;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                v[j] *= p.alpha;
-                if (p.beta != 0.f && j < n) v[j] = fmaf(p.beta, sc_load1(dst + j * es, p.out_kind), v[j]);
-              }
-              sc_act<ALL>(v, p.act, p.slope);
-              if (wide && n == 4 && es == 4)
-                *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-              else if (wide && n == 4)
-                *reinterpret_cast<uint2*>(dst) =
-                    make_uint2(sc_pack2(v[0], v[1], p.out_kind), sc_pack2(v[2], v[3], p.out_kind));
-              else
-                for (int j = 0; j < n; ++j) sc_store1(dst + j * es, v[j], p.out_kind);
-            }
-          }
-        };
-        if (slices == 1)
-          finish_rows(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-        else if (slices <= 2)
-          finish_rows(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-        else if (slices <= 4)
-          finish_rows(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+        for (int j = 0; j < 4; ++j) {
+          v[j] *= p.alpha;
+          if (p.beta != 0.f && j < n) v[j] = fmaf(p.beta, sc_load1(dst + j * es, p.out_kind), v[j]);
+        }
+        sc_act<ALL>(v, p.act, p.slope);
+        if (wide && n == 4 && es == 4)
+          *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+        else if (wide && n == 4)
+          *reinterpret_cast<uint2*>(dst) = make_uint2(sc_pack2(v[0], v[1], p.out_kind), sc_pack2(v[2], v[3], p.out_kind));
         else
-          finish_rows(std::integral_constant<int, 1>{}, std::integral_constant<int, kMaxSlices>{});
-        arrive_all(part_free);
+          for (int j = 0; j < n; ++j) sc_store1(dst + j * es, v[j], p.out_kind);
+      };
+      // 32 rows of A of this warp's lanes, as a column of [row][stride] floats
+      auto drain = [&](int c, float* at, int stride) {
+        uint32_t r[32];
+        if (!empty) {
+          tmem_ld_32x32b_x32(t_row + 32 * c, r);
+          tmem_ld_wait(r);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) at[j * stride] = __uint_as_float(r[j]);
+      };
+      auto release = [&]() {
+        if (empty) return;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty0 + 8 * acc);
+      };
+      if (slices == 1) {
+        float* const own = part + e * 32 * 32;
+        for (int c = 0; c < pieces; ++c) {
+          __syncwarp();  // the rows before these have been read
+          drain(c, own + lane, 32);
+          __syncwarp();
+          if (c + 1 == pieces) release();
+          const int live = min(32, x.row_end - x.row0 - 32 * c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // four rows at a time, eight lanes each
+            const int t = 4 * i + lane / 8;
+            const float4 f = *reinterpret_cast<const float4*>(own + t * 32 + 4 * (lane & 7));
+            float v[4] = {f.x, f.y, f.z, f.w};
+            if (t < live) store(v, x.row0 + 32 * c + t, x.n0 + 32 * q + 4 * (lane & 7));
+          }
+        }
+        continue;
       }
+      // the partials of the tile before this one have been read by every CTA
+      if (done > 0 && !sc_wait<true>(part_free, (done - 1) & 1, w, WAIT_SLICES)) break;
+      for (int c = 0; c < pieces; ++c) drain(c, part + c * 32 * 128 + 32 * q + lane, 128);
+      release();
+      arrive_all(part_full);
+      if (!sc_wait<true>(part_full, done & 1, w, WAIT_SLICES)) break;
+      ++done;
+      const int live = min(bn, x.row_end - x.row0);
+      const int col = x.n0 + 4 * lane;
+      // this warp's rows, several at a time: as many loads in flight whatever the slices
+      auto finish_rows = [&](auto rows_c, auto slices_c) {
+        constexpr int R = decltype(rows_c)::value, MS = decltype(slices_c)::value;
+        for (int t0 = int(rank) + slices * e; t0 < live; t0 += slices * kEpiWarps * R) {
+          float4 f[R][MS];
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const int t = t0 + i * slices * kEpiWarps;
+            const uint32_t at = part_addr + uint32_t(t * 128 + 4 * lane) * 4u;
+#pragma unroll
+            for (int s = 0; s < MS; ++s)
+              if (s < slices && t < live) f[i][s] = ld_cluster_f4(mapa_shared(at, uint32_t(s)));
+          }
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const int t = t0 + i * slices * kEpiWarps;
+            if (t >= live) continue;
+            float v[4] = {f[i][0].x, f[i][0].y, f[i][0].z, f[i][0].w};
+#pragma unroll
+            for (int s = 1; s < MS; ++s)
+              if (s < slices) v[0] += f[i][s].x, v[1] += f[i][s].y, v[2] += f[i][s].z, v[3] += f[i][s].w;
+            store(v, x.row0 + t, col);
+          }
+        }
+      };
+      if (slices <= 2)
+        finish_rows(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+      else if (slices <= 4)
+        finish_rows(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+      else
+        finish_rows(std::integral_constant<int, 1>{}, std::integral_constant<int, kMaxSlices>{});
+      arrive_all(part_free);
     }
   }
 

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   wait_prior_grid();
-  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) allow_next_grid();
   if (warp == 2 && p.group == SC_ROWS) sc_tile_table(p, C::TILE_M, table);
   tc_fence_before();
   if constexpr (PAIR)
