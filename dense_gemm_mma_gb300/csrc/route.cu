@@ -30,12 +30,14 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // Keys of experts that are not there or taken, and of experts outside the chosen groups; every float's key is larger.
 constexpr uint32_t kNone = 0, kOutside = 1;
 
-// A float's order as an unsigned integer; NaN as minus infinity, -0 as 0.
-__device__ __forceinline__ uint32_t order_key(float f) {
-  f = f == f ? f + 0.f : kNegInf;
-  const uint32_t b = __float_as_uint(f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+// A number's order as an unsigned integer, -0 as 0 (positive: the sign bit set; negative: all bits flipped).
+__device__ __forceinline__ uint32_t number_key(float f) {
+  const uint32_t b = __float_as_uint(f + 0.f);
+  return b ^ (uint32_t(int(b) >> 31) | 0x80000000u);
 }
+
+// The same for any float: NaN as minus infinity.
+__device__ __forceinline__ uint32_t order_key(float f) { return number_key(f == f ? f : kNegInf); }
 
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
@@ -107,18 +109,23 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, int t, int first
 }
 
 // What turns a token's logits into scores.  A masked expert (minus infinity) scores 0;
-// a row with nothing else scores 0 throughout.
+// a row with nothing else scores 0 throughout; of logits of plus infinity each takes an equal share.
 struct Scorer {
   int sigmoid;
   float top, sum;  // softmax: largest logit, sum of exp(x - top)
+  // `best`: the key of the lane's largest logit
   template <int P>
-  __device__ __forceinline__ Scorer(const RouteArgs& a, const float (&x)[P]) : sigmoid(a.sigmoid), top(kNegInf), sum(0.f) {
+  __device__ __forceinline__ Scorer(const RouteArgs& a, const float (&x)[P], uint32_t best)
+      : sigmoid(a.sigmoid), top(kNegInf), sum(0.f) {
     if (sigmoid) return;
+    top = key_value(__reduce_max_sync(kAll, best));
+    if (fabsf(top) < -kNegInf) {  // exp(-inf) is 0 and exp(0) is 1: nothing to look out for
 #pragma unroll
-    for (int i = 0; i < P; ++i) top = fmaxf(top, x[i]);
-    top = key_value(__reduce_max_sync(kAll, order_key(top)));
+      for (int i = 0; i < P; ++i) sum = __fadd_rn(sum, expf(__fsub_rn(x[i], top)));
+    } else {
 #pragma unroll
-    for (int i = 0; i < P; ++i) sum = __fadd_rn(sum, power(x[i]));
+      for (int i = 0; i < P; ++i) sum = __fadd_rn(sum, power(x[i]));
+    }
     sum = warp_sum(sum);
   }
   __device__ __forceinline__ float power(float x) const {  // softmax's numerator
@@ -187,21 +194,30 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
   const int run = (a.experts + 31) / 32, first = lane * run;
   float x[P];
   load_logits(a, t, first, run, a.wide, x);
-  const Scorer scorer(a, x);
   uint32_t key[P];
   int ex[P];
-  const bool by_logit = a.bias == nullptr && a.group_top == 1;
+  uint32_t lane_best = 0;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int e = first + i;
-    const bool there = i < run && e < a.experts;
-    float k = x[i];
-    if (!by_logit && k != kNegInf) {  // a masked expert stays minus infinity, whatever its bias
-      k = scorer.score(k);
-      if (there && a.bias && DG_IN(a.dbg, a.bias + e, 4, DBG_ROUTE)) k = __fadd_rn(k, __ldg(a.bias + e));
+    key[i] = number_key(x[i]);
+    ex[i] = first + i;
+    lane_best = max(lane_best, key[i]);
+  }
+  const Scorer scorer(a, x, lane_best);
+  const bool by_logit = a.bias == nullptr && a.group_top == 1;
+  if (!by_logit) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (x[i] == kNegInf) continue;  // a masked expert stays minus infinity, whatever its bias
+      float k = scorer.score(x[i]);
+      if (a.bias && DG_IN(a.dbg, a.bias + ex[i], 4, DBG_ROUTE)) k = __fadd_rn(k, __ldg(a.bias + ex[i]));
+      key[i] = order_key(k);
     }
-    key[i] = there ? order_key(k) : kNone;
-    ex[i] = e;
+  }
+  if (run * 32 != a.experts || run != P) {  // what is not there
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (i >= run || ex[i] >= a.experts) key[i] = kNone;
   }
   // Groups that are whole lanes (a power of two of them, every lane full): their best keys
   // meet in a few exchanges.  Others: one pair of warp maxima each.
@@ -278,7 +294,10 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
   const int run = (a.experts + 31) / 32, first = lane * run;
   float x[P], ds[P];
   load_logits(a, t, first, run, a.wide, x);
-  const Scorer scorer(a, x);
+  float lane_best = kNegInf;
+#pragma unroll
+  for (int i = 0; i < P; ++i) lane_best = fmaxf(lane_best, x[i]);
+  const Scorer scorer(a, x, number_key(lane_best));
   int expert = -1;  // lane j: choice j; an index outside the experts takes no part
   float dw = 0.f;
   if (lane < a.top_k) {
@@ -296,21 +315,43 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
     dsj = sum > 0.f && expert >= 0 ? a.scale * (dw - dot / sum) / sum : 0.f;
   }
   const float through = a.sigmoid ? 0.f : warp_sum(dsj * sj);
+  // dsj from lane j to the lane of its expert: through shared memory, or one after another
+  // where two choices name the same expert (their sum then has an order)
+  __shared__ float moved[4][32 * P];
+  float* const mine = moved[threadIdx.x >> 5] + lane * P;
+  const uint32_t same = __match_any_sync(kAll, expert >= 0 ? expert : -1 - lane);
+  if (__any_sync(kAll, (same & (same - 1)) != 0)) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) ds[i] = 0.f;
-  for (int j = 0; j < a.top_k; ++j) {
-    const int at = __shfl_sync(kAll, expert, j) - first;
-    const float d = __shfl_sync(kAll, dsj, j);
+    for (int i = 0; i < P; ++i) ds[i] = 0.f;
+    for (int j = 0; j < a.top_k; ++j) {
+      const int at = __shfl_sync(kAll, expert, j) - first;
+      const float d = __shfl_sync(kAll, dsj, j);
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (at == i && i < run) ds[i] += d;
+      for (int i = 0; i < P; ++i)
+        if (at == i && i < run) ds[i] += d;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) mine[i] = 0.f;
+    __syncwarp();
+    if (expert >= 0) moved[threadIdx.x >> 5][expert / run * P + expert % run] = dsj;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < P; ++i) ds[i] = mine[i];
   }
-  const float over = scorer.sum > 0.f ? 1.f / scorer.sum : 0.f;
+  if (!a.sigmoid) {
+    const float over = scorer.sum > 0.f ? 1.f / scorer.sum : 0.f;
+    if (fabsf(scorer.top) < -kNegInf) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    if (!a.sigmoid) {
-      ds[i] = scorer.power(x[i]) * over * (ds[i] - through);
-    } else if (ds[i] != 0.f) {  // (0 for experts that were not chosen)
+      for (int i = 0; i < P; ++i) ds[i] = expf(x[i] - scorer.top) * over * (ds[i] - through);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) ds[i] = scorer.power(x[i]) * over * (ds[i] - through);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (ds[i] == 0.f) continue;  // (experts that were not chosen)
       const float s = scorer.score(x[i]);
       ds[i] = s * (1.f - s) * ds[i];
     }
