@@ -120,16 +120,13 @@ enum ScKernel { SC_TILE, SC_PAIR, SC_SLICED };
 struct ScPick {
   ScKernel kernel = SC_TILE;
   int bn = 128, slices = 1, stages = 0, part_rows = 32;
-  int per_sm = 1;  // CTAs an SM holds at once
 };
 
-void set_sliced(ScPick* c, int slices, int per_sm) {
+void set_sliced(ScPick* c, int slices) {
   c->slices = slices;
-  c->per_sm = per_sm;
   c->part_rows = slices > 1 ? c->bn : 32;
-  const int room = per_sm == 1 ? kSmemMax : (kSmemMax + 1024) / per_sm - 1024;
   c->stages = 8;
-  while (c->stages > 2 && scaled_sliced_smem(c->bn, c->stages, c->part_rows) > room) --c->stages;
+  while (c->stages > 2 && scaled_sliced_smem(c->bn, c->stages, c->part_rows) > kSmemMax) --c->stages;
 }
 
 // Clusters of 1 .. 8 CTAs that the device holds at once (16 tiles in 8 slices, 128 CTAs,
@@ -154,7 +151,7 @@ ScPick pick_sliced(int64_t rows, int64_t tiles, int sms) {
   c.bn = int(std::min<int64_t>(128, round_up(rows, 32)));
   int s = 8;
   while (s > 1 && fits.clusters[s] < tiles) --s;
-  set_sliced(&c, s, 1);
+  set_sliced(&c, s);
   return c;
 }
 
@@ -197,7 +194,7 @@ ScPick pick(const Product& x, int sms) {
   }
   if (c.kernel == SC_SLICED) {
     const int s = env_int("GEMM_SCALED_SLICES", 0);
-    if (s >= 1 && s <= 8) set_sliced(&c, s, 1);
+    if (s >= 1 && s <= 8) set_sliced(&c, s);
   }
   return c;
 }
@@ -212,7 +209,7 @@ size_t repack_bytes(const void* p, int64_t ld, int64_t groups, int64_t group, in
 // Copy such a matrix into `out` (plan workspace) and make the product read it there.
 gemm_status_t repack(gemm_plan* plan, const void** p, int64_t* ld, int64_t groups, int64_t* group, int64_t rows, int64_t K,
                      const int32_t* counts, void* out, cudaStream_t s) {
-  if (K > int64_t(65535) * 4096) return GEMM_ERR_UNSUPPORTED;  // (the copy's grid)
+  if (rows * ceil_div(K, 16) > int64_t(0xffffffff)) return GEMM_ERR_UNSUPPORTED;  // (the copy counts in 32 bits)
   RepackArgs a{};
   a.in = static_cast<const uint8_t*>(*p);
   a.ld = *ld;
@@ -312,7 +309,7 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
     if (clusters <= 0) return GEMM_ERR_UNSUPPORTED;
     grid = int(2 * std::min<int64_t>(bound, clusters));
   } else if (sliced) {
-    const int64_t resident = std::max<int64_t>(1, int64_t(plan->sms) * c.per_sm / c.slices);
+    const int64_t resident = std::max<int64_t>(1, plan->sms / c.slices);
     grid = int(c.slices * (x.group == SC_ROWS ? std::min(bound, resident) : bound));
   } else {
     grid = int(std::min<int64_t>(bound, plan->sms));
