@@ -40,6 +40,14 @@ __device__ __forceinline__ float sc_load1(const void* p, int kind) {
   return __half2float(*static_cast<const __half*>(p));
 }
 
+// Two neighbouring 16-bit values of a word.
+__device__ __forceinline__ float2 sc_unpack2(uint32_t w, int kind) {
+  if (kind == OUT_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  __half2 h;
+  memcpy(&h, &w, 4);
+  return __half22float2(h);
+}
+
 __device__ __forceinline__ void sc_store1(void* p, float v, int kind) {
   if (kind == OUT_F32)
     *static_cast<float*>(p) = v;
@@ -175,8 +183,17 @@ __device__ __forceinline__ bool sc_wait(uint32_t bar, uint32_t parity, const Wat
   }
 }
 
-// v <- act(v), every run-time choice outside the unrolled loops; GELU and SiLU only if ALL.
-template <bool ALL, int N>
+// Which activations a compiled epilogue holds: what a call does not need costs it the instruction
+// cache, so that the tile kernel's loops are compiled apart.
+enum : int { ACT_SIMPLE = 0, ACT_GELU = 1, ACT_SILU = 2, ACT_ALL = 3 };  // identity, LeakyReLU and ReLU in every one
+
+// x / (1 + exp(-x)) with the fast division (2 units in the last place; 0 where exp(-x) is past 2^126, of
+// which the quotient is below 2^-119): the exact one is a call for some operands, and with it in
+// the loop a 2711 x 3104 x 5376 product with SiLU took 64.7 us, without an activation 32.3.
+__device__ __forceinline__ float sc_silu(float x) { return __fdividef(x, 1.f + expf(-x)); }
+
+// v <- act(v), every run-time choice outside the unrolled loops.
+template <int A, int N>
 __device__ __forceinline__ void sc_act(float (&v)[N], int act, float slope) {
   if (act == 1) {
 #pragma unroll
@@ -184,13 +201,17 @@ __device__ __forceinline__ void sc_act(float (&v)[N], int act, float slope) {
   } else if (act == 2) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
-  } else if constexpr (ALL) {
+  }
+  if constexpr ((A & ACT_GELU) != 0) {
     if (act == 3) {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] = apply_act(v[i], 3, 0.f);
-    } else if (act == 4) {
+    }
+  }
+  if constexpr ((A & ACT_SILU) != 0) {
+    if (act == 4) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = apply_act(v[i], 4, 0.f);
+      for (int i = 0; i < N; ++i) v[i] = sc_silu(v[i]);
     }
   }
 }

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads)
           v[j] *= p.alpha;
           if (p.beta != 0.f && j < n) v[j] = fmaf(p.beta, sc_load1(dst + j * es, p.out_kind), v[j]);
         }
-        sc_act<ALL>(v, p.act, p.slope);
+        sc_act<ALL ? ACT_ALL : ACT_SIMPLE>(v, p.act, p.slope);
         if (wide && n == 4 && es == 4)
           *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
         else if (wide && n == 4)
