@@ -236,9 +236,11 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
 // scale worked out by one thread.  A thread's 8 rows of a column are 8 consecutive bytes of the
 // transposed matrix: they are turned round in a swizzled shared-memory tile and leave as
 // 128-byte rows.
-// Many CTAs one after another overlap loading, converting and storing better than two that
-// go from tile to tile with the next one's loads under way: 36.5 against 47.3 us for
-// 8192 x 4096 bf16, both ways.  (16 rows a warp, which spilled: 47.0.)
+// Many CTAs one after another overlap loading, converting and storing better than a few that
+// go from tile to tile with the next one's loads under way (8192 x 4096 bf16, both ways, two CTAs an SM:
+// 36.5 against 47.3 us).  Values stay in the input's type until a conversion needs them, so
+// that 40 registers do and three CTAs share an SM: 30.5 us, 4.4 TB/s; 32-bit input two: 40.7
+// us (one: 54.8).
 constexpr int kTileRows = 8;
 constexpr int kTileWarps = 128 / kTileRows;
 
@@ -279,21 +281,27 @@ __device__ __forceinline__ uint32_t row_maxima(const Four<T> (&v)[kTileRows], in
   }
 }
 
-// kTileRows rows' codes (inverse scales: in the rows' lanes), then the columns' of a lane.
-template <bool E5M2, bool CAREFUL>
-__device__ __forceinline__ void row_codes(uint32_t (&c)[kTileRows], const float (&f)[kTileRows][4], float inv_mine) {
+// kTileRows rows' codes to q (inverse scales: in the rows' lanes).
+template <bool E5M2, bool CAREFUL, typename T>
+__device__ __forceinline__ void row_codes(const QuantArgs& a, const Four<T> (&v)[kTileRows], float inv_mine, uint32_t live,
+                                          uint8_t* dst, int n) {
 #pragma unroll
-  for (int i = 0; i < kTileRows; ++i)
-    c[i] = codes4<E5M2, CAREFUL>(f[i][0], f[i][1], f[i][2], f[i][3], __shfl_sync(kAll, inv_mine, lane_of_row(i)));
+  for (int i = 0; i < kTileRows; ++i, dst += a.ldq) {
+    const uint32_t c = codes4<E5M2, CAREFUL>(v[i].at(0), v[i].at(1), v[i].at(2), v[i].at(3),
+                                             __shfl_sync(kAll, inv_mine, lane_of_row(i)));
+    if ((live >> i) & 1u) store4(a, dst, c, n);
+  }
 }
-template <bool E5M2, bool CAREFUL>
-__device__ __forceinline__ uint2 column_codes(const float (&f)[kTileRows][4], int j, float inv) {
-  return make_uint2(codes4<E5M2, CAREFUL>(f[0][j], f[1][j], f[2][j], f[3][j], inv),
-                    codes4<E5M2, CAREFUL>(f[4][j], f[5][j], f[6][j], f[7][j], inv));
+
+// Codes of a lane's column j.
+template <bool E5M2, bool CAREFUL, typename T>
+__device__ __forceinline__ uint2 column_codes(const Four<T> (&v)[kTileRows], int j, float inv) {
+  return make_uint2(codes4<E5M2, CAREFUL>(v[0].at(j), v[1].at(j), v[2].at(j), v[3].at(j), inv),
+                    codes4<E5M2, CAREFUL>(v[4].at(j), v[5].at(j), v[6].at(j), v[7].at(j), inv));
 }
 
 template <typename T, bool E5M2, bool VEC>
-__global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 1 : 2) quantize_tile_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 2 : 3) quantize_tile_kernel(const QuantArgs a) {
   alignas(16) __shared__ uint32_t col_max[kTileWarps][128];
   alignas(16) __shared__ float col_inv[128];  // inverse scales of the columns
   __shared__ uint32_t tile_max[4];
@@ -352,11 +360,6 @@ __global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 1 : 2) quant
   }
   const uint32_t tile_scale = a.block_rows > 1 ? tile_max[0] : 0u;
   const uint32_t peaks = a.q && a.block_rows == 1 ? row_maxima(v, lane) : 0u;
-  float f[kTileRows][4];
-#pragma unroll
-  for (int i = 0; i < kTileRows; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[i][j] = v[i].at(j);
   if (a.q) {
     uint32_t mine = tile_scale;  // scale byte of the lane's row
     const int my_row = row0 + row_of_lane(lane);
@@ -367,8 +370,8 @@ __global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 1 : 2) quant
       if (careful_rows) {
 #pragma unroll
         for (int i = 0; i < kTileRows; ++i) {
-          const uint32_t m = __reduce_max_sync(kAll, max(max(finite_bits(f[i][0]), finite_bits(f[i][1])),
-                                                         max(finite_bits(f[i][2]), finite_bits(f[i][3]))));
+          const uint32_t m = __reduce_max_sync(kAll, max(max(finite_bits(v[i].at(0)), finite_bits(v[i].at(1))),
+                                                         max(finite_bits(v[i].at(2)), finite_bits(v[i].at(3)))));
           if (lane == lane_of_row(i)) mine = m;
         }
       }
@@ -377,23 +380,11 @@ __global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 1 : 2) quant
       mine = 0;
     }
     const float inv = a.block_rows == 1 ? inverse_scale(mine) : col_inv[0];
-    uint32_t c[kTileRows];
+    uint8_t* const dst = a.q + int64_t(row0) * a.ldq + col;
     if (careful_rows)
-      row_codes<E5M2, true>(c, f, inv);
+      row_codes<E5M2, true>(a, v, inv, live, dst, a.cols - col);
     else
-      row_codes<E5M2, false>(c, f, inv);
-    uint8_t* dst = a.q + int64_t(row0) * a.ldq + col;
-    if (col + 4 <= a.cols) {
-#pragma unroll
-      for (int i = 0; i < kTileRows; ++i, dst += a.ldq)
-        if (((live >> i) & 1u) && DG_IN(a.dbg, dst, 4, DBG_QUANTIZE)) *reinterpret_cast<uint32_t*>(dst) = c[i];
-    } else if (col < a.cols) {
-      for (int j = 0; j < a.cols - col; ++j)
-#pragma unroll
-        for (int i = 0; i < kTileRows; ++i)
-          if (((live >> i) & 1u) && DG_IN(a.dbg, dst + i * a.ldq + j, 1, DBG_QUANTIZE))
-            dst[i * a.ldq + j] = uint8_t(c[i] >> (8 * j));
-    }
+      row_codes<E5M2, false>(a, v, inv, live, dst, a.cols - col);
     if (row_of_lane(lane) < kTileRows && row0 < a.rows_padded) {
       uint8_t* const s = a.sq + scale_at(my_row, cb, a.q_groups);
       if (DG_IN(a.dbg, s, 1, DBG_QUANTIZE)) *s = uint8_t(mine);
@@ -405,7 +396,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 1 : 2) quant
     for (int j = 0; j < 4; ++j) {
       const float by = j == 0 ? inv.x : j == 1 ? inv.y : j == 2 ? inv.z : inv.w;
       reinterpret_cast<uint2*>(turn)[(4 * lane + j) * 16 + (warp ^ (lane & 15))] =
-          careful ? column_codes<E5M2, true>(f, j, by) : column_codes<E5M2, false>(f, j, by);
+          careful ? column_codes<E5M2, true>(v, j, by) : column_codes<E5M2, false>(v, j, by);
     }
     __syncthreads();
 #pragma unroll
