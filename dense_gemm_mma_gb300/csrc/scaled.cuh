@@ -57,6 +57,9 @@ __device__ __forceinline__ void sc_store1(void* p, float v, int kind) {
     *static_cast<__half*>(p) = __float2half_rn(v);
 }
 
+// Index of the warp, known to be the same in all its lanes.
+__device__ __forceinline__ int sc_warp() { return __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0); }
+
 // One output tile of a call.
 struct ScUnit {
   int row0, row_end;  // first row of A (and D) of the tile; end of the rows that exist
@@ -75,9 +78,20 @@ __device__ __forceinline__ void sc_segment(const ScParams& p, int e, int* start,
   *count = ok ? min(c, p.cap - s) : 0;
 }
 
+// From the copy in shared memory, if the kernel has one.
+__device__ __forceinline__ void sc_segment_of(const ScParams& p, const int2* seg, int e, int* start, int* count) {
+  if (seg) {
+    const int2 s = seg[e];
+    *start = s.x;
+    *count = s.y;
+  } else {
+    sc_segment(p, e, start, count);
+  }
+}
+
 // SC_ROWS: table[e] = tiles of the groups before e, table[groups] = all tiles.
-// Executed by one warp.
-__device__ __forceinline__ void sc_tile_table(const ScParams& p, int tile_rows, int* table) {
+// Executed by one warp.  seg: the groups' segments in shared memory, or null.
+__device__ __forceinline__ void sc_tile_table(const ScParams& p, int tile_rows, const int2* seg, int* table) {
   const int lane = threadIdx.x & 31;
   int carry = 0;
   for (int e0 = 0; e0 < p.groups; e0 += 32) {
@@ -85,7 +99,7 @@ __device__ __forceinline__ void sc_tile_table(const ScParams& p, int tile_rows, 
     int tiles = 0;
     if (e < p.groups) {
       int start, count;
-      sc_segment(p, e, &start, &count);
+      sc_segment_of(p, seg, e, &start, &count);
       tiles = (count + tile_rows - 1) / tile_rows * p.n_blocks;
     }
     int sum = tiles;
@@ -102,8 +116,8 @@ __device__ __forceinline__ void sc_tile_table(const ScParams& p, int tile_rows, 
 
 // Unit u -> tile.  `cursor` (SC_ROWS) is the group of the caller's last unit:
 // units are visited in ascending order, so the search for u's group goes on there.
-__device__ __forceinline__ ScUnit sc_unit(const ScParams& p, int u, int tile_rows, int tile_cols, const int* table,
-                                          int* cursor) {
+__device__ __forceinline__ ScUnit sc_unit(const ScParams& p, int u, int tile_rows, int tile_cols, const int2* seg,
+                                          const int* table, int* cursor) {
   ScUnit x;
   int mb, nb;
   x.zb = x.zd = 0;
@@ -114,7 +128,7 @@ __device__ __forceinline__ ScUnit sc_unit(const ScParams& p, int u, int tile_row
     while (e + 1 < p.groups && u >= table[e + 1]) ++e;
     *cursor = e;
     int start, count;
-    sc_segment(p, e, &start, &count);
+    sc_segment_of(p, seg, e, &start, &count);
     tile_coords(u - table[e], (count + tile_rows - 1) / tile_rows, p.n_blocks, p.raster, &mb, &nb);
     x.row0 = start + mb * tile_rows;
     x.row_end = start + count;
@@ -126,7 +140,7 @@ __device__ __forceinline__ ScUnit sc_unit(const ScParams& p, int u, int tile_row
       const int e = u / per;
       t = u - e * per;
       int start, count;
-      sc_segment(p, e, &start, &count);
+      sc_segment_of(p, seg, e, &start, &count);
       x.kb0 = start / SC_BK;
       x.kb1 = (start + count + SC_BK - 1) / SC_BK;
       x.zd = e;
@@ -158,18 +172,19 @@ struct ScSets {
   }
 };
 
-// Index of the warp, known to be the same in all its lanes.
-__device__ __forceinline__ int sc_warp() { return __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0); }
-
 // A whole warp's bounded wait: true in every lane, or false in every lane, which then
-// leave their loop (the limit ran out, or another role of the CTA gave up).  CLUSTER:
-// threads of the peer CTA arrive on the barrier.  The loop is spelled out here: a call on the slow
+// leave their loop (the limit ran out, or another role of the CTA gave up).  SC_CLUSTER:
+// threads of other CTAs arrive on the barrier, and the wait orders memory after what they wrote;
+// SC_RELAXED: they do, and it orders nothing.  The loop is spelled out here: a call on the slow
 // path would make every value of the caller's loop leave the uniform registers.
-template <bool CLUSTER>
+enum : int { SC_OWN, SC_CLUSTER, SC_RELAXED };
+template <int FROM>
 __device__ __forceinline__ bool sc_wait(uint32_t bar, uint32_t parity, const Watch& w, int code) {
   uint64_t t0 = 0;
   while (true) {
-    const bool done = CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+    const bool done = FROM == SC_CLUSTER   ? mbar_try_wait_cluster(bar, parity)
+                      : FROM == SC_RELAXED ? mbar_try_wait_cluster_relaxed(bar, parity)
+                                           : mbar_try_wait(bar, parity);
     if (__all_sync(0xffffffffu, done)) return true;
     const uint64_t t = global_timer_ns();
     if (t0 == 0) t0 = t;

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   wait_prior_grid();
   if (threadIdx.x == 0) allow_next_grid();
-  if (warp == 2 && p.group == SC_ROWS) sc_tile_table(p, bn, table);
+  if (warp == 2 && p.group == SC_ROWS) sc_tile_table(p, bn, nullptr, table);
   tc_fence_before();
   if (slices > 1)
     cluster_sync();  // every CTA's barriers exist before another arrives on them
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads)
   const int step = int(gridDim.x) / slices;
   const Watch w{abort_flag, p.err, p.timeout_ns};
   auto unit_of = [&](int u, int* cursor) {
-    ScUnit x = sc_unit(p, u, bn, 128, table, cursor);
+    ScUnit x = sc_unit(p, u, bn, 128, nullptr, table, cursor);
     x.kb0 = int(rank) * p.kb_per_slice;
     x.kb1 = min(p.k_blocks, x.kb0 + p.kb_per_slice);
     return x;
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads)
       const int sb_row = x.zb * p.sb_group + (x.n0 / 128) * p.sb_cols, sa_row = (x.row0 / 128) * p.sa_cols;
       for (int kb = x.kb0; kb < x.kb1; ++kb) {
         const uint32_t eb = empty0 + 8 * stage, fb = full0 + 8 * stage;
-        if (!sc_wait<false>(eb, phase ^ 1u, w, WAIT_PRODUCER_EMPTY)) {
+        if (!sc_wait<SC_OWN>(eb, phase ^ 1u, w, WAIT_PRODUCER_EMPTY)) {
           ok = false;
           break;
         }
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads)
       // Let the loads already in flight land before the CTA can exit.
       for (int s = 0; s < S; ++s) {
         const int n_s = issued > s ? (issued - s + S - 1) / S : 0;
-        if (n_s > 0) sc_wait<false>(full0 + 8 * s, (uint32_t)((n_s - 1) & 1), w, 0);
+        if (n_s > 0) sc_wait<SC_OWN>(full0 + 8 * s, (uint32_t)((n_s - 1) & 1), w, 0);
       }
     }
   } else if (warp == 1) {
@@ -172,19 +172,19 @@ __global__ void __launch_bounds__(kThreads)
       const ScUnit x = unit_of(u, &cursor);
       if (x.kb0 >= x.kb1) continue;  // no K at all
       const int acc = tiles & 1;
-      if (tiles > 1 && !sc_wait<false>(tempty0 + 8 * acc, ((tiles - 2) >> 1) & 1, w, WAIT_MMA_TMEM_EMPTY)) break;
+      if (tiles > 1 && !sc_wait<SC_OWN>(tempty0 + 8 * acc, ((tiles - 2) >> 1) & 1, w, WAIT_MMA_TMEM_EMPTY)) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + uint32_t(acc * bn);
       const uint32_t mma_n = uint32_t(pieces_of(x)) * 32;
       for (int kb = x.kb0; kb < x.kb1; ++kb) {
-        if (!sc_wait<false>(full0 + 8 * stage, phase, w, WAIT_MMA_FULL)) {
+        if (!sc_wait<SC_OWN>(full0 + 8 * stage, phase, w, WAIT_MMA_FULL)) {
           ok = false;
           break;
         }
         if (kb == x.kb0 || (kb & 3) == 0) {
           const int old = sets.last_user();
           if (old >= 0 && old > it - S &&
-              !sc_wait<false>(empty0 + 8 * (old % S), uint32_t(old / S) & 1u, w, WAIT_MMA_FULL)) {
+              !sc_wait<SC_OWN>(empty0 + 8 * (old % S), uint32_t(old / S) & 1u, w, WAIT_MMA_FULL)) {
             ok = false;
             break;
           }
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     // Every MMA issued by this warp completes before tensor memory is freed.
     tc_commit_one<false>(drain_bar, one);
-    sc_wait<false>(drain_bar, 0, w, WAIT_DRAIN);
+    sc_wait<SC_OWN>(drain_bar, 0, w, WAIT_DRAIN);
   } else {
     // ------------------------------------------------------------ epilogue
     const int e = warp - 2;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads)
       const bool empty = x.kb0 >= x.kb1;
       const int acc = tiles & 1;
       if (!empty) {
-        if (!sc_wait<false>(tfull0 + 8 * acc, (tiles >> 1) & 1, w, WAIT_EPI_TMEM_FULL)) break;
+        if (!sc_wait<SC_OWN>(tfull0 + 8 * acc, (tiles >> 1) & 1, w, WAIT_EPI_TMEM_FULL)) break;
         tc_fence_after();
         ++tiles;
       }
@@ -298,11 +298,11 @@ __global__ void __launch_bounds__(kThreads)
         continue;
       }
       // the partials of the tile before this one have been read by every CTA
-      if (done > 0 && !sc_wait<true>(part_free, (done - 1) & 1, w, WAIT_SLICES)) break;
+      if (done > 0 && !sc_wait<SC_CLUSTER>(part_free, (done - 1) & 1, w, WAIT_SLICES)) break;
       for (int c = 0; c < pieces; ++c) drain(c, part + c * 32 * 128 + 32 * q + lane, 128);
       release();
       arrive_all(part_full);
-      if (!sc_wait<true>(part_full, done & 1, w, WAIT_SLICES)) break;
+      if (!sc_wait<SC_CLUSTER>(part_full, done & 1, w, WAIT_SLICES)) break;
       ++done;
       const int live = min(bn, x.row_end - x.row0);
       const int col = x.n0 + 4 * lane;
