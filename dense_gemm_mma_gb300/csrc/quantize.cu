@@ -11,7 +11,8 @@
 //
 // What bounds it is memory: each value is read once, and written once per
 // orientation.  Maxima are taken on the magnitudes' bits (ordered like the numbers),
-// one warp reduction per row and block.
+// one warp reduction per row and block.  8192 x 4096 bf16: one orientation 19.5 us (5.2 TB/s), both 30.6
+// us (4.4 TB/s; the columns' scales need the whole tile before the first transposed code).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

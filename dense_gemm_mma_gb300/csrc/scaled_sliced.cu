@@ -19,6 +19,9 @@
 //    memory, then whole rows of it, 512 bytes a warp, to D.  All rows of a tile in one exchange: it
 //    takes ~1.5 us whatever its size.  Where a CTA has K to itself nothing is exchanged: each warp turns
 //    its 32 columns of D round in 4 KB of its own, 32 rows at a time, and the ring has the room.
+//
+// Measured: one row, 4096 x 4096: 6.4 us (the 17 MB come from L2 in repeated calls); 48 tokens to 4 of 64
+// experts of 2048 x 2048: 34.7 us, 7.2 TB/s of the weights of ~60 experts.
 #include <type_traits>
 
 #include "scaled.cuh"

@@ -21,6 +21,11 @@
 // of tensor memory and leave none for the scales, so they overlap by 64: columns
 // 0-255 and 192-447, scales from 448.  The epilogue drains the shared columns of
 // a tile first and only then lets the next tile's MMAs begin.
+//
+// What bounds it: 8192^3 into bf16 340 to 360 us, 3.1 to 3.2 PFLOP/s, at the power limit (287 us, 3.8
+// PFLOP/s, with operands whose bits change little).  Short K: what goes through L2.  16 weight gradients of 2048 x 2048 over
+// 1,024 rows each read 537 MB of tiles and write 268 MB in 78.7 us, and take 61 if nothing is written; a load
+// takes 4,000 to 5,000 cycles while the tile before is written, of which the ring covers 2,600.
 #include <type_traits>
 
 #include "scaled.cuh"
