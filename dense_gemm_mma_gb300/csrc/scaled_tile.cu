@@ -22,9 +22,9 @@
 // 0-255 and 192-447, scales from 448.  The epilogue drains the shared columns of
 // a tile first and only then lets the next tile's MMAs begin.
 //
-// What bounds it: 8192^3 into bf16 340 to 360 us, 3.1 to 3.2 PFLOP/s, at the power limit (287 us, 3.8
+// What bounds it: 8192^3 into bf16 330 to 360 us, 3.1 to 3.3 PFLOP/s, at the power limit (287 us, 3.8
 // PFLOP/s, with operands whose bits change little).  Short K: what goes through L2.  16 weight gradients of 2048 x 2048 over
-// 1,024 rows each read 537 MB of tiles and write 268 MB in 78.7 us, and take 61 if nothing is written; a load
+// 1,024 rows each read 537 MB of tiles and write 268 MB in 76 us, and take 61 if nothing is written; a load
 // takes 4,000 to 5,000 cycles while the tile before is written, of which the ring covers 2,600.
 #include <type_traits>
 
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_prior_grid();
   if (threadIdx.x == 0) allow_next_grid();
   // The groups' segments: a unit's own read from global memory queued behind the operand loads in
-  // flight, 2,000 to 5,000 cycles before every tile (K groups of 1,024, 16 x 2048 x 2048: 86 us, now 78.7).
+  // flight, 2,000 to 5,000 cycles before every tile (K groups of 1,024, 16 x 2048 x 2048: 86 us, with the copy and the release below 78.7).
   if (p.group != SC_DENSE) {
     for (int e = threadIdx.x; e < p.groups; e += kThreads) {
       int start, count;
@@ -319,6 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cw = 128 / es;  // columns per 128-byte box row
     const int chunks = C::BN / cw;
     const int shared_chunks = C::OVERLAP / cw;
+    constexpr int kSteps = C::BN / 32 / kHalves;  // 32-column steps of a warp
+    static_assert(kSteps % 2 == 0, "steps go in pairs");
+    const int per = cw / 32;  // steps to a chunk
     const int sw = lane & 7;  // 128-byte swizzle: 16-byte chunk j of row r lives at j ^ (r % 8)
     int cursor = 0, tiles = 0;
     auto tiles_loop = [&](auto beta_c, auto act_c) {
@@ -333,7 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           ++tiles;
         }
-        auto release = [&]() {  // this warp's reads that the next MMAs wait for are complete
+        // This warp's reads that the next MMAs wait for are complete.  To the leader of a pair without
+        // ordering memory: there is none to order, and it took 1,100 to 3,300 cycles.
+        auto release = [&]() {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -358,38 +363,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* const d_row = static_cast<uint8_t*>(p.d) + (int64_t(x.zd) * p.d_group + int64_t(y0 + lane) * p.ldd) * es;
         // the shared columns first: the last ones of accumulator 0, the first ones of accumulator 1
         const int first = acc == 0 ? chunks - shared_chunks : 0;
-        // after which of its chunks this warp has read what the next MMAs wait for
-        const int release_after = shared_chunks == 0 ? chunks - kHalves + half : half + (shared_chunks - 1 - half) / kHalves * kHalves;
-        bool released = empty;
-        if (!released && shared_chunks > 0 && half >= shared_chunks) {
-          release();
-          released = true;
-        }
-        for (int i = half; i < chunks; i += kHalves) {
-          const int c = shared_chunks == 0 ? i : (i + first) % chunks;
-          const int x0 = x.n0 + c * cw;
-          uint32_t r0[32], r1[32];
-          if (!empty) {
-            tmem_ld_32x32b_x32(t_row + c * cw, r0);
-            if (es == 2) tmem_ld_32x32b_x32(t_row + c * cw + 32, r1);
-            tmem_ld_wait(r0);
-            if (es == 2) tmem_ld_wait(r1);
-            if (!released && i == release_after) {
-              release();
-              released = true;
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) r0[k] = r1[k] = 0u;
-          }
-          if (x0 >= p.N) continue;
+        // Steps of 32 columns, two to a chunk of 16-bit results: step s is columns 32 * (s % per) of
+        // this warp's chunk s / per.  After step last_shared it has read what the next MMAs wait for (-1: it
+        // has none of it).
+        auto chunk_of = [&](int s) { return (half + s / per * kHalves + first) & (chunks - 1); };
+        const int last_shared = shared_chunks == 0 ? kSteps - 1 : (shared_chunks - half + kHalves - 1) / kHalves * per - 1;
+        if (!empty && last_shared < 0) release();
+        // Where the arithmetic is short each step is loaded while the one before is converted (a
+        // prompt through 32 experts 215 -> 208 us, weight gradients of 16 experts 78.6 -> 76.2).  Those steps are unrolled,
+        // so that no copy of registers that a load still writes is needed on the way; GELU four times over no longer fits
+        // the instruction cache (2711 x 3104 x 5376: 44 us, 56 unrolled).
+        uint32_t ra[32], rb[32];
+        auto load = [&](uint32_t (&r)[32], int s) { tmem_ld_32x32b_x32(t_row + chunk_of(s) * cw + 32 * (s % per), r); };
+        auto loaded = [&](uint32_t (&r)[32], int s) {
+          tmem_ld_wait(r);
+          if (s == last_shared) release();
+        };
+        auto process = [&](const uint32_t (&r)[32], int s, bool opens, bool closes) {
+          const int h = s % per;
+          const int x0 = x.n0 + chunk_of(s) * cw;
+          if (x0 >= p.N) return;
           uint8_t* const row_p = stg_p0 + lane * 128;
           float v[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r0[k]);
-          finish<BETA, A>(v, p, d_row, x0, mine);
-          if (lane == 0) bulk_wait_read<0>();  // the store that last used this box has read it
-          __syncwarp();
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+          finish<BETA, A>(v, p, d_row, x0 + 32 * h, mine);
+          if (opens) {
+            if (lane == 0) bulk_wait_read<0>();  // the store that last used this box has read it
+            __syncwarp();
+          }
           if (es == 4) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -397,27 +399,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (h == 1) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r1[k]);
-                finish<BETA, A>(v, p, d_row, x0 + 32, mine);
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4*>(row_p + (((4 * h + j) ^ sw) << 4)) = make_uint4(
-                    sc_pack2(v[8 * j], v[8 * j + 1], p.out_kind), sc_pack2(v[8 * j + 2], v[8 * j + 3], p.out_kind),
-                    sc_pack2(v[8 * j + 4], v[8 * j + 5], p.out_kind), sc_pack2(v[8 * j + 6], v[8 * j + 7], p.out_kind));
-            }
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(row_p + (((4 * h + j) ^ sw) << 4)) = make_uint4(
+                  sc_pack2(v[8 * j], v[8 * j + 1], p.out_kind), sc_pack2(v[8 * j + 2], v[8 * j + 3], p.out_kind),
+                  sc_pack2(v[8 * j + 4], v[8 * j + 5], p.out_kind), sc_pack2(v[8 * j + 6], v[8 * j + 7], p.out_kind));
           }
+          if (!closes) return;
           if (mine) {
             // by the threads: rows of a box that is not whole, in 16-byte pieces up to
             // n_tma, and the columns past the last whole piece of a row
             if (!by_tma) {
-              const int per = 16 / es;
+              const int piece = 16 / es;
 #pragma unroll 1
-              for (int j = 0; j < 8 && x0 + (j + 1) * per <= p.n_tma; ++j) {
-                uint8_t* const dst = d_row + int64_t(x0 + j * per) * es;
+              for (int j = 0; j < 8 && x0 + (j + 1) * piece <= p.n_tma; ++j) {
+                uint8_t* const dst = d_row + int64_t(x0 + j * piece) * es;
                 if (DG_IN(p.dbg, dst, 16, DBG_SCALED))
                   *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(row_p + ((j ^ sw) << 4));
               }
@@ -440,6 +435,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             bulk_commit();  // one group per chunk (possibly empty) keeps the buffer accounting exact
           }
           __syncwarp();  // whole again before the next tcgen05.ld
+        };
+        if (BETA || (A & ACT_GELU) != 0 || empty) {
+#pragma unroll 1
+          for (int s = 0; s < kSteps; ++s) {
+            if (!empty) {
+              load(ra, s);
+              loaded(ra, s);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) ra[k] = 0u;
+            }
+            process(ra, s, s % per == 0, s % per == per - 1);
+          }
+          continue;
+        }
+        load(ra, 0);
+#pragma unroll
+        for (int s = 0; s < kSteps; s += 2) {
+          loaded(ra, s);
+          load(rb, s + 1);
+          process(ra, s, true, es == 4);
+          loaded(rb, s + 1);
+          if (s + 2 < kSteps) load(ra, s + 2);
+          process(rb, s + 1, es == 4, true);
         }
       }
     };
