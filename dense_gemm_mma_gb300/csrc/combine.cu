@@ -6,10 +6,12 @@
 // Every row of Y belongs to one choice of one token, so the gradient of Y has one term
 // and needs no atomics.  What bounds both is memory: each row of Y is read once (and of dY
 // written once), each row of out or dout once.  16-byte loads, all k rows' of a piece in flight together.
-// Measured, 8192 tokens of 4 rows of 2048 bf16: sum and gradients 79.8 us, 5.9 TB/s.
+// Measured, 8192 tokens of 4 rows of 2048 bf16: sum and gradients 79.6 us, 5.9 TB/s; of 1026 (4-byte loads) 73 us,
+// of 1027 (by element; 2000 tokens) 16.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cstring>
 #include <type_traits>
 
 #include "kernels.h"
@@ -18,7 +20,7 @@ namespace dg {
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kPiece = 8;   // consecutive columns of a thread
+constexpr int kPiece = 8;   // columns of a thread
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v) {
@@ -38,29 +40,52 @@ struct alignas(16) Piece {
   T v[kPiece];
 };
 
-// Columns [0, n) of a piece, the rest zero.  VEC (rows on 16-byte boundaries, whole pieces):
-// one predicated load per 16 bytes, no branch, so that the pieces of all rows are in flight together.
-template <bool VEC, typename T>
-__device__ __forceinline__ void load_piece(Piece<T>& o, const T* p, int n) {
+// A warp takes 256 columns of a row at a time, a thread a piece of them.  WIDE, the bytes of a load:
+//   16  eight neighbouring columns, rows on 16-byte boundaries, whole pieces: loads without a branch, so that the
+//       pieces of all rows are in flight together
+//   4   eight neighbouring columns, rows on 4-byte boundaries: a whole piece in words, the last one of a row by element
+//   0   every 32nd column, so that a load of the warp is one run of memory
+template <int WIDE>
+struct Units {
+  static constexpr int COLS = WIDE ? kPiece : 1;  // neighbouring columns of a thread
+  static constexpr int STEP = WIDE ? 1 : 32;      // columns between values of a piece
+  // Columns from a thread's first to its last, `left` in the row.
+  static __device__ __forceinline__ int span(int left) { return min(left, (kPiece - 1) * STEP + 1); }
+};
+
+// A thread's piece, its first column at p, `left` columns from there to the end of the row; what does
+// not exist is zero.
+template <int WIDE, typename T>
+__device__ __forceinline__ void load_piece(Piece<T>& o, const T* p, int left) {
 #pragma unroll
   for (int i = 0; i < kPiece; ++i) o.v[i] = from_f<T>(0.f);
-  if constexpr (VEC) {
-    if (n > 0) o = *reinterpret_cast<const Piece<T>*>(p);
+  if constexpr (WIDE == 16) {
+    if (left > 0) o = *reinterpret_cast<const Piece<T>*>(p);
+  } else if (WIDE == 4 && left >= kPiece) {
+    uint32_t w[sizeof(Piece<T>) / 4];
+#pragma unroll
+    for (int i = 0; i < int(sizeof(w) / 4); ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    memcpy(&o, w, sizeof(w));
   } else {
 #pragma unroll
     for (int i = 0; i < kPiece; ++i)
-      if (i < n) o.v[i] = p[i];
+      if (i * Units<WIDE>::STEP < left) o.v[i] = p[i * Units<WIDE>::STEP];
   }
 }
 
-template <bool VEC, typename T>
-__device__ __forceinline__ void store_piece(const Piece<T>& o, T* p, int n) {
-  if constexpr (VEC) {
-    *reinterpret_cast<Piece<T>*>(p) = o;
+template <int WIDE, typename T>
+__device__ __forceinline__ void store_piece(const Piece<T>& o, T* p, int left) {
+  if constexpr (WIDE == 16) {
+    if (left > 0) *reinterpret_cast<Piece<T>*>(p) = o;
+  } else if (WIDE == 4 && left >= kPiece) {
+    uint32_t w[sizeof(Piece<T>) / 4];
+    memcpy(w, &o, sizeof(w));
+#pragma unroll
+    for (int i = 0; i < int(sizeof(w) / 4); ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
   } else {
 #pragma unroll
     for (int i = 0; i < kPiece; ++i)
-      if (i < n) p[i] = o.v[i];
+      if (i * Units<WIDE>::STEP < left) p[i * Units<WIDE>::STEP] = o.v[i];
   }
 }
 
@@ -71,12 +96,15 @@ __device__ __forceinline__ int row_of(const CombineArgs& a, int64_t slot) {
 }
 
 // One thread a piece of a token's row.
-template <typename TY, typename TO, bool VEC, int KC>
+template <typename TY, typename TO, int WIDE, int KC>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
   wait_prior_grid();
-  const int t = int(blockIdx.x), col = int(blockIdx.y * blockDim.x + threadIdx.x) * kPiece;
-  if (col >= a.cols) return;
-  const int n = min(kPiece, a.cols - col);
+  using U = Units<WIDE>;
+  const int t = int(blockIdx.x), first = int(blockIdx.y * blockDim.x + threadIdx.x);
+  const int col = first / 32 * (32 * kPiece) + first % 32 * U::COLS;
+  const int left = a.cols - col;
+  if (left <= 0) return;
+  const int n = U::span(left);
   const TY* const y = static_cast<const TY*>(a.y) + col;
   float sum[kPiece];
 #pragma unroll
@@ -90,7 +118,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
       const int r = j0 + j < a.k ? row_of(a, slot) : -1;
       const TY* const src = y + int64_t(max(r, 0)) * a.ldy;
       w[j] = r >= 0 && DG_IN(a.dbg, a.weights + slot, 4, DBG_COMBINE) ? __ldg(a.weights + slot) : 0.f;
-      load_piece<VEC>(p[j], src, r >= 0 && DG_IN(a.dbg, src, n * int(sizeof(TY)), DBG_COMBINE) ? n : 0);
+      load_piece<WIDE>(p[j], src, r >= 0 && DG_IN(a.dbg, src, n * int(sizeof(TY)), DBG_COMBINE) ? left : 0);
     }
 #pragma unroll
     for (int j = 0; j < KC; ++j)
@@ -101,26 +129,31 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
 #pragma unroll
   for (int i = 0; i < kPiece; ++i) o.v[i] = from_f<TO>(sum[i]);
   TO* const dst = static_cast<TO*>(a.out) + int64_t(t) * a.ldo + col;
-  if (DG_IN(a.dbg, dst, n * int(sizeof(TO)), DBG_COMBINE)) store_piece<VEC>(o, dst, n);
+  if (DG_IN(a.dbg, dst, n * int(sizeof(TO)), DBG_COMBINE)) store_piece<WIDE>(o, dst, left);
 }
 
-// Gradients: one warp a token (dout read once, its choices' rows side by side);
-// the warps after the tokens' clear the rows that hold no slot.
-template <typename TY, typename TO, bool VEC, int KC>
+// Gradients: WARPS warps a token (dout read once, its choices' rows side by side), each every
+// WARPS-th 256 columns, their products added up in the warps' order; the warps after the
+// tokens' clear the rows that hold no slot.
+template <typename TY, typename TO, int WIDE, int KC, int WARPS>
 __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineArgs a) {
+  using U = Units<WIDE>;
+  __shared__ float part[WARPS > 1 ? WARPS : 1][KC];
   wait_prior_grid();
   const int lane = threadIdx.x & 31;
-  const int64_t warp = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int share = WARPS > 1 ? int(threadIdx.x >> 5) : 0;  // this warp's part of the token's columns
+  const int64_t index = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int64_t warp = index / WARPS;  // (a whole CTA's warps have a token, or none has)
   if (warp >= a.tokens) {
-    const int64_t r = warp - a.tokens;
+    const int64_t r = index - int64_t(a.tokens) * WARPS;
     if (!a.rowmap || r >= a.rows || !DG_IN(a.dbg, a.rowmap + r, 4, DBG_COMBINE) || __ldg(a.rowmap + r) >= 0) return;
     Piece<TY> zero;
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) zero.v[i] = from_f<TY>(0.f);
     TY* const dst = static_cast<TY*>(a.dy) + r * a.lddy;
-    for (int col = lane * kPiece; col < a.cols; col += 32 * kPiece) {
-      const int n = min(kPiece, a.cols - col);
-      if (DG_IN(a.dbg, dst + col, n * int(sizeof(TY)), DBG_COMBINE)) store_piece<VEC>(zero, dst + col, n);
+    for (int col = lane * U::COLS; col < a.cols; col += 32 * kPiece) {
+      const int left = a.cols - col;
+      if (DG_IN(a.dbg, dst + col, U::span(left) * int(sizeof(TY)), DBG_COMBINE)) store_piece<WIDE>(zero, dst + col, left);
     }
     return;
   }
@@ -135,15 +168,15 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineArgs
       w[j] = row[j] >= 0 && DG_IN(a.dbg, a.weights + slot, 4, DBG_COMBINE) ? __ldg(a.weights + slot) : 0.f;
       dot[j] = 0.f;
     }
-    for (int col = lane * kPiece; col < a.cols; col += 32 * kPiece) {
-      const int n = min(kPiece, a.cols - col);
+    for (int col = share * (32 * kPiece) + lane * U::COLS; col < a.cols; col += WARPS * 32 * kPiece) {
+      const int left = a.cols - col, n = U::span(left);
       Piece<TO> g;
-      load_piece<VEC>(g, dout + col, DG_IN(a.dbg, dout + col, n * int(sizeof(TO)), DBG_COMBINE) ? n : 0);
+      load_piece<WIDE>(g, dout + col, DG_IN(a.dbg, dout + col, n * int(sizeof(TO)), DBG_COMBINE) ? left : 0);
       Piece<TY> y[KC];
 #pragma unroll
       for (int j = 0; j < KC; ++j) {
         const TY* const src = static_cast<const TY*>(a.y) + int64_t(max(row[j], 0)) * a.ldy + col;
-        load_piece<VEC>(y[j], src, row[j] >= 0 && DG_IN(a.dbg, src, n * int(sizeof(TY)), DBG_COMBINE) ? n : 0);
+        load_piece<WIDE>(y[j], src, row[j] >= 0 && DG_IN(a.dbg, src, n * int(sizeof(TY)), DBG_COMBINE) ? left : 0);
       }
 #pragma unroll
       for (int j = 0; j < KC; ++j) {
@@ -156,38 +189,63 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineArgs
           d.v[i] = from_f<TY>(w[j] * f);
         }
         TY* const dst = static_cast<TY*>(a.dy) + int64_t(row[j]) * a.lddy + col;
-        if (DG_IN(a.dbg, dst, n * int(sizeof(TY)), DBG_COMBINE)) store_piece<VEC>(d, dst, n);
+        if (DG_IN(a.dbg, dst, n * int(sizeof(TY)), DBG_COMBINE)) store_piece<WIDE>(d, dst, left);
       }
     }
 #pragma unroll
     for (int j = 0; j < KC; ++j) {
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) dot[j] += __shfl_xor_sync(kAll, dot[j], s);
+    }
+    if constexpr (WARPS > 1) {
+      if (j0 > 0) __syncthreads();  // the sums of the choices before have been read
+#pragma unroll
+      for (int j = 0; j < KC; ++j)
+        if (lane == 0) part[share][j] = dot[j];
+      __syncthreads();
+      if (share > 0) continue;
+#pragma unroll
+      for (int j = 0; j < KC; ++j) {
+        dot[j] = 0.f;
+        for (int w = 0; w < WARPS; ++w) dot[j] += part[w][j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < KC; ++j) {
       const int64_t slot = warp * a.k + j0 + j;
       if (lane == 0 && j0 + j < a.k && DG_IN(a.dbg, a.dweights + slot, 4, DBG_COMBINE)) a.dweights[slot] = dot[j];
     }
   }
 }
 
-template <typename TY, typename TO, bool VEC, int KC>
+// Tokens up to which the gradients take eight warps a token.  16-byte loads, 4 rows of 2048 bf16 a
+// token: 20 tokens 3.7 us (one warp 7.1), 256 tokens 5.6 (7.4), 512 tokens 7.6 (7.4).  Narrower loads keep one warp busy for
+// longer: 300 tokens of 7 rows of 1116, 6.9 us (one warp 15.1).
+constexpr int few_tokens(int wide) { return wide == 16 ? 256 : 1024; }
+
+template <typename TY, typename TO, int WIDE, int KC>
 cudaError_t launch(const CombineArgs& a, bool backward, cudaStream_t s) {
-  if (backward) {
-    const int64_t warps = int64_t(a.tokens) + (a.rowmap ? a.rows : 0);
-    return launch_k(combine_backward_kernel<TY, TO, VEC, KC>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0, s, a.pdl, a);
-  }
   const int pieces = (a.cols + kPiece - 1) / kPiece;
+  if (backward) {
+    const bool few = a.tokens <= few_tokens(WIDE) && pieces > 32;
+    const int64_t warps = int64_t(a.tokens) * (few ? 8 : 1) + (a.rowmap ? a.rows : 0);
+    const dim3 grid(unsigned((warps + 7) / 8));
+    if (few) return launch_k(combine_backward_kernel<TY, TO, WIDE, 8, 8>, grid, dim3(256), 0, s, a.pdl, a);
+    return launch_k(combine_backward_kernel<TY, TO, WIDE, KC, 1>, grid, dim3(256), 0, s, a.pdl, a);
+  }
   const int threads = pieces >= 256 ? 256 : (pieces + 31) / 32 * 32;
-  return launch_k(combine_kernel<TY, TO, VEC, KC>, dim3(unsigned(a.tokens), unsigned((pieces + threads - 1) / threads)),
+  return launch_k(combine_kernel<TY, TO, WIDE, KC>, dim3(unsigned(a.tokens), unsigned((pieces + threads - 1) / threads)),
                   dim3(unsigned(threads)), 0, s, a.pdl, a);
 }
 
 // KC, the choices of a token that are in flight together: its k rounded up, eight at most.
 template <typename TY, typename TO>
 cudaError_t launch_k_of(const CombineArgs& a, bool backward, cudaStream_t s) {
-  if (!a.vec) return launch<TY, TO, false, 4>(a, backward, s);
-  if (a.k <= 2) return launch<TY, TO, true, 2>(a, backward, s);
-  if (a.k <= 4) return launch<TY, TO, true, 4>(a, backward, s);
-  return launch<TY, TO, true, 8>(a, backward, s);
+  if (a.wide == 0) return launch<TY, TO, 0, 4>(a, backward, s);
+  if (a.wide == 4) return launch<TY, TO, 4, 4>(a, backward, s);
+  if (a.k <= 2) return launch<TY, TO, 16, 2>(a, backward, s);
+  if (a.k <= 4) return launch<TY, TO, 16, 4>(a, backward, s);
+  return launch<TY, TO, 16, 8>(a, backward, s);
 }
 
 template <typename TY>

@@ -468,7 +468,7 @@ struct CombineArgs {
   void* dy;
   int64_t lddy;
   float* dweights;
-  int vec;  // whole pieces of eight columns on 16-byte boundaries in every row
+  int wide;  // bytes of a load: 16 (whole pieces of eight columns on 16-byte boundaries in every row), 4, or 0: by element
   int pdl;
   DG_DEBUG_FIELD
 };

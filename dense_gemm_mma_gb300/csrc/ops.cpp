@@ -10,6 +10,8 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
+#include <utility>
 
 #include "plan.h"
 
@@ -370,6 +372,14 @@ gemm_status_t checked_run(gemm_plan_t plan, const Product& x, void* stream) {
 // Rows of `ld` elements of es bytes from p allow 16-byte accesses where columns do.
 bool rows_wide(const void* p, int64_t ld, int64_t es) { return aligned(p, 16) && (ld * es) % 16 == 0; }
 
+// Bytes of the weighted sum's loads and stores, given each matrix's address and bytes between rows.
+int access_bytes(int64_t cols, std::initializer_list<std::pair<const void*, int64_t>> rows) {
+  int wide = cols % 8 == 0 ? 16 : 4;
+  for (const auto& m : rows)
+    while (wide && (!aligned(m.first, size_t(wide)) || m.second % wide)) wide = wide == 16 ? 4 : 0;
+  return wide;
+}
+
 gemm_status_t check_route(int64_t tokens, int64_t experts, const void* logits, int64_t ldl, gemm_type_t type,
                           const gemm_route_t& r) {
   if (tokens < 0 || experts < 1 || !is_float_type(type)) return GEMM_ERR_INVALID_ARG;
@@ -657,7 +667,7 @@ gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top_k, int6
   a.out = out;
   a.ldo = ldo;
   a.o_kind = type_kind(out_type);
-  a.vec = cols % 8 == 0 && rows_wide(Y, ldy, ye) && rows_wide(out, ldo, oe);
+  a.wide = access_bytes(cols, {{Y, ldy * ye}, {out, ldo * oe}});
   a.pdl = plan->pdl;
 #ifdef DG_DEBUG
   a.dbg = Spans(plan->err).matrix(Y, rows, cols, ldy, ye).bytes(pos, tokens * top_k * 4).bytes(weights, tokens * top_k * 4)
@@ -700,7 +710,7 @@ gemm_status_t gemm_combine_backward(gemm_plan_t plan, int64_t tokens, int64_t to
   a.dy = dY;
   a.lddy = lddy;
   a.dweights = dweights;
-  a.vec = cols % 8 == 0 && rows_wide(Y, ldy, ye) && rows_wide(dout, ldo, oe) && rows_wide(dY, lddy, ye);
+  a.wide = access_bytes(cols, {{Y, ldy * ye}, {dout, ldo * oe}, {dY, lddy * ye}});
   a.pdl = plan->pdl;
 #ifdef DG_DEBUG
   a.dbg = Spans(plan->err).matrix(dout, tokens, cols, ldo, oe).matrix(Y, rows, cols, ldy, ye).bytes(pos, tokens * top_k * 4)

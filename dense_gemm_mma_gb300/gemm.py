@@ -409,6 +409,7 @@ def unpack_scales(packed, rows: int, cols: int):
     r, c = max(-(-rows // 128), 1) * 128, max(-(-cols // 512), 1) * 4
     return packed[:r * c].view(r // 128, c // 4, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(r, c)[:rows, :-(-cols // 128)]
 
+
 def _operand(t, trans: bool):
     """(pointer, ld) of a stored 2-D operand whose rows are contiguous."""
     if t.dim() != 2 or t.stride(1) != 1:

@@ -167,7 +167,8 @@ def test_route_map(plan, g, T, k, E):
             np.testing.assert_array_equal(got.cpu().numpy(), want)
 
 
-COMBINES = [(1, 1, 1, 3), (1, 8, 64, 2048), (5, 3, 4, 517), (33, 9, 16, 40), (200, 4, 8, 1024), (20, 17, 32, 264)]
+COMBINES = [(1, 1, 1, 3), (1, 8, 64, 2048), (5, 3, 4, 517), (33, 9, 16, 40), (200, 4, 8, 1024), (20, 17, 32, 264),
+            (24, 9, 8, 700), (300, 2, 4, 600), (1100, 2, 4, 262)]
 
 
 def combine_case(rng, g, T, k, E, N, y, o, pad):
