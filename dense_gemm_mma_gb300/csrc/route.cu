@@ -313,8 +313,10 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
   float dsj = a.scale * dw;
   if (a.renormalize) {
     const float sum = warp_sum(sj);
-    const float dot = warp_sum(dw * sj);
-    dsj = sum > 0.f && expert >= 0 ? a.scale * (dw - dot / sum) / sum : 0.f;
+    // by the weights, not the scores: a token whose one score is its sum has a weight of exactly
+    // 1, and a gradient of exactly 0
+    const float dot = warp_sum(sum > 0.f ? dw * (sj / sum) : 0.f);
+    dsj = sum > 0.f && expert >= 0 ? a.scale * (dw - dot) / sum : 0.f;
   }
   const float through = a.sigmoid ? 0.f : warp_sum(dsj * sj);
   // dsj from lane j to the lane of its expert: through shared memory, or one after another

@@ -123,6 +123,27 @@ def test_route_gradient(plan, g, T, E, k, how, score):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [8, 100, 256])
+def test_route_gradient_of_constant_weights(plan, g, score, E):
+    """A renormalised weight that is 1 whatever the logits (one choice, or one that is not masked) has no gradient, exactly."""
+    import torch
+    rng = np.random.default_rng(E)
+    T = 152
+    kind = g.GEMM_SCORE_SIGMOID if score == "sigmoid" else g.GEMM_SCORE_SOFTMAX
+    for k in (1, 3):
+        x = torch.from_numpy(grid_logits(rng, T, E)).float().cuda()
+        if k > 1:
+            keep = torch.from_numpy(rng.integers(0, E, T)).cuda()
+            x[torch.arange(E, device="cuda") != keep[:, None]] = -float("inf")
+        w, i = torch.empty((T, k), device="cuda"), torch.empty((T, k), dtype=torch.int32, device="cuda")
+        assert plan.route(x, w, i, score=kind, renormalize=True) == 0
+        assert torch.equal(w[:, 0], torch.ones_like(w[:, 0]))
+        dw, dx = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda(), torch.full((T, E), 9.0, device="cuda")
+        assert plan.route_backward(x, i, dw, dx, score=kind, renormalize=True) == 0
+        assert (dx == 0).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renormalize", [False, True])
 def test_route_gradient_against_differences(plan, g, score, renormalize):
     """The kernel's gradient along random directions against central differences of the 64-bit
