@@ -291,13 +291,13 @@ def test_refusals(plan, g):
         assert call(**bad) == g.GEMM_ERR_UNSUPPORTED, bad
     assert call(logits=p + 2) == g.GEMM_ERR_ALIGNMENT
     m = lambda **c: g.gemm_route_map(*{**dict(plan=plan.handle, tokens=4, top_k=2, experts=8, indices=p, starts=p + 1024,  # noqa: E731
-                                              counts=p + 2048, pos=p + 3072, rowmap=p + 4096, rows=1152), **c}.values())
+                                              counts=p + 2048, pos=p + 3200, rowmap=p + 4096, rows=1152), **c}.values())
     assert m(tokens=1, rows=256) == g.GEMM_OK
     for bad in ({"rows": 1023}, {"indices": None}, {"starts": None}, {"pos": None}, {"rowmap": None}, {"top_k": 0}):
         assert m(**bad) == g.GEMM_ERR_INVALID_ARG, bad
     assert m(experts=2000) == g.GEMM_ERR_UNSUPPORTED
     c = lambda **k: g.gemm_combine(*{**dict(plan=plan.handle, tokens=2, top_k=1, cols=8, rows=4, Y=p, ldy=8, y_type=2, pos=p + 1024,  # noqa: E731
-                                            weights=p + 2048, out=p + 3072, ldo=8, out_type=2), **k}.values())
+                                            weights=p + 2048, out=p + 3200, ldo=8, out_type=2), **k}.values())
     assert c() == g.GEMM_OK and c(tokens=0) == g.GEMM_OK
     for bad in ({"ldy": 7}, {"Y": None}, {"pos": None}, {"out": p + 16}, {"top_k": 0}, {"y_type": 5}):
         assert c(**bad) == g.GEMM_ERR_INVALID_ARG, bad
