@@ -11,8 +11,8 @@
 //
 // What bounds it is memory: each value is read once, and written once per
 // orientation.  Maxima are taken on the magnitudes' bits (ordered like the numbers),
-// one warp reduction per row and block.  8192 x 4096 bf16: one orientation 19.5 us (5.2 TB/s), both 30.6
-// us (4.4 TB/s; the columns' scales need the whole tile before the first transposed code).
+// one warp reduction per row and block.  8192 x 4096 bf16: one orientation 19.5 us (5.2 TB/s), both 30.0
+// us (4.5 TB/s; the columns' scales need the whole tile before the first transposed code).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -135,24 +135,24 @@ __device__ __forceinline__ int64_t scale_at(int64_t r, int64_t c, int64_t groups
   return ((r >> 7) * groups + (c >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (c & 3);
 }
 
-// Rows of X that rows r0 .. r0 + N of the result come from, -1 for none.
+// Row of X that row r of the result comes from, -1 for none.
+__device__ __forceinline__ int source_row(const QuantArgs& a, int r) {
+  if (r >= a.rows) return -1;
+  if (!a.rowmap) return r;
+  if (!DG_IN(a.dbg, a.rowmap + r, 4, DBG_QUANTIZE)) return -1;
+  int src = __ldg(a.rowmap + r);
+  if (src >= 0) src /= a.map_div;
+  return src < a.src_rows ? src : -1;
+}
+
+// The same of rows r0 .. r0 + N, each looked up by one lane; by a whole warp.  (Every lane looking all of
+// them up: 4096 tokens to 4 of 32 experts, 2048 bf16, both ways: 43.3 us, so 34.6.)
 template <int N>
 __device__ __forceinline__ void source_rows(const QuantArgs& a, int r0, int (&src)[N]) {
-  if (!a.rowmap) {
+  const int lane = threadIdx.x & 31;
+  const int mine = lane < N ? source_row(a, r0 + lane) : -1;
 #pragma unroll
-    for (int i = 0; i < N; ++i) src[i] = r0 + i < a.rows ? r0 + i : -1;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    src[i] = -1;
-    if (r0 + i < a.rows && DG_IN(a.dbg, a.rowmap + r0 + i, 4, DBG_QUANTIZE)) src[i] = __ldg(a.rowmap + r0 + i);
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (src[i] >= 0) src[i] /= a.map_div;
-    if (src[i] >= a.src_rows) src[i] = -1;
-  }
+  for (int i = 0; i < N; ++i) src[i] = __shfl_sync(kAll, mine, i);
 }
 
 // n rows' groups of four columns, from `col` on: whole groups as one load each (VEC: rows
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
 // Many CTAs one after another overlap loading, converting and storing better than a few that
 // go from tile to tile with the next one's loads under way (8192 x 4096 bf16, both ways, two CTAs an SM:
 // 36.5 against 47.3 us).  Values stay in the input's type until a conversion needs them, so
-// that 40 registers do and three CTAs share an SM: 30.5 us, 4.4 TB/s; 32-bit input two: 40.7
+// that 40 registers do and three CTAs share an SM: 30.0 us, 4.5 TB/s; 32-bit input two: 40.7
 // us (one: 54.8).
 constexpr int kTileRows = 8;
 constexpr int kTileWarps = 128 / kTileRows;
