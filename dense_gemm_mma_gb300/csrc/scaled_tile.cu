@@ -371,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!empty && last_shared < 0) release();
         // Where the arithmetic is short each step is loaded while the one before is converted (a
         // prompt through 32 experts 215 -> 208 us, weight gradients of 16 experts 78.6 -> 76.2).  Those steps are unrolled,
-        // so that no copy of registers that a load still writes is needed on the way; GELU four times over no longer fits
-        // the instruction cache (2711 x 3104 x 5376: 44 us, 56 unrolled).
+        // so that no copy of registers that a load still writes is needed on the way; GELU or SiLU four times over no longer
+        // fits the instruction cache (2711 x 3104 x 5376, GELU: 44 us, 56 unrolled; 8192 x 8192 x 1024, SiLU: 71 and 84).
         uint32_t ra[32], rb[32];
         auto load = [&](uint32_t (&r)[32], int s) { tmem_ld_32x32b_x32(t_row + chunk_of(s) * cw + 32 * (s % per), r); };
         auto loaded = [&](uint32_t (&r)[32], int s) {
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();  // whole again before the next tcgen05.ld
         };
-        if (BETA || (A & ACT_GELU) != 0 || empty) {
+        if (BETA || A != ACT_SIMPLE || empty) {
 #pragma unroll 1
           for (int s = 0; s < kSteps; ++s) {
             if (!empty) {
