@@ -305,7 +305,7 @@ template <typename T, bool E5M2, bool VEC>
 __global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 2 : 3) quantize_tile_kernel(const QuantArgs a) {
   alignas(16) __shared__ uint32_t col_max[kTileWarps][128];
   alignas(16) __shared__ float col_inv[128];  // inverse scales of the columns
-  __shared__ uint32_t tile_max[4];
+  __shared__ uint32_t tile_max[4], tile_byte;  // 128 x 128 scales: largest magnitudes of four stripes, the scale byte
   __shared__ uint4 turn[128 * 8];  // [column][8-byte piece of rows ^ (column / 4 % 16)]
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -355,11 +355,12 @@ __global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 2 : 3) quant
         uint8_t* const s = a.sqt + scale_at(c, rb, a.qt_groups);
         if (DG_IN(a.dbg, s, 1, DBG_QUANTIZE)) *s = uint8_t(c < a.cols ? byte : 0u);
       }
-      if (a.block_rows > 1 && threadIdx.x == 0) tile_max[0] = byte;
+      // (not into tile_max: a slower warp may still be reading it)
+      if (a.block_rows > 1 && threadIdx.x == 0) tile_byte = byte;
     }
     __syncthreads();
   }
-  const uint32_t tile_scale = a.block_rows > 1 ? tile_max[0] : 0u;
+  const uint32_t tile_scale = a.block_rows > 1 ? tile_byte : 0u;
   const uint32_t peaks = a.q && a.block_rows == 1 ? row_maxima(v, lane) : 0u;
   if (a.q) {
     uint32_t mine = tile_scale;  // scale byte of the lane's row

@@ -162,6 +162,38 @@ def test_quantize_through_a_row_map(plan, g):
             np.testing.assert_array_equal(st.cpu().numpy(), ref.pack(byte, rows))
 
 
+@pytest.mark.parametrize("name,fmt", [("bf16", "e4m3"), ("f32", "e5m2")])
+def test_quantize_square_scales_with_every_sm_full(plan, g, name, fmt):
+    """128 x 128 scales of both orientations while several CTAs share an SM and their warps are held up: a
+    tile's largest value lies in its first 32 columns, so that a warp of the other columns that took the scale
+    from anything but the whole tile would choose a smaller one.  The same bits every time."""
+    import torch
+    rng = np.random.default_rng(12)
+    R, K = 3000, 2500
+    x = rng.standard_normal((R, K))
+    for b in range(0, K, 128):
+        x[rng.integers(0, 128) % min(128, R):: 128, b + rng.integers(0, min(32, K - b))] = 1000.0 * (1 + b)
+    _, xd = rows_of(R, K, name)
+    xd.copy_(torch.from_numpy(x))
+    want, byte = ref.quantize(xd.double().cpu().numpy(), fmt, 128)
+    want_t, byte_t = ref.quantize(xd.double().cpu().numpy().T, fmt, 128)
+    first = None
+    for _ in range(8):
+        _, q = rows_of(R, K, fmt)
+        _, qt = rows_of(K, R, fmt)
+        sq = torch.full((g.gemm_scale_bytes(R, K),), 0xEE, dtype=torch.uint8, device="cuda")
+        st = torch.full((g.gemm_scale_bytes(K, R),), 0xEE, dtype=torch.uint8, device="cuda")
+        assert plan.quantize(xd, q, sq, qt, st, block_rows=128) == 0
+        got = [v.view(torch.uint8).contiguous().cpu() for v in (q, sq, qt, st)]
+        if first is None:
+            first = got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+    np.testing.assert_array_equal(ref.decode(first[0].numpy(), fmt), want)
+    np.testing.assert_array_equal(first[1].numpy(), ref.pack(byte, K))
+    np.testing.assert_array_equal(ref.decode(first[2].numpy(), fmt), want_t)
+    np.testing.assert_array_equal(first[3].numpy(), ref.pack(byte_t, R))
+
+
 def test_quantize_refusals(plan, g):
     import torch
     x = torch.zeros((8, 64), device="cuda", dtype=torch.bfloat16)
