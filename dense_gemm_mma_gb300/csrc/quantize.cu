@@ -378,8 +378,8 @@ __global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 4 ? 2 : 3) quant
         }
       }
       mine = scale_byte<E5M2>(mine);
-    } else if (my_row >= a.rows) {
-      mine = 0;
+    } else if (((live >> row_of_lane(lane)) & 1u) == 0u) {
+      mine = 0;  // no such row, or a map that gives it no source
     }
     const float inv = a.block_rows == 1 ? inverse_scale(mine) : col_inv[0];
     uint8_t* const dst = a.q + int64_t(row0) * a.ldq + col;

@@ -194,6 +194,37 @@ def test_quantize_square_scales_with_every_sm_full(plan, g, name, fmt):
     np.testing.assert_array_equal(first[3].numpy(), ref.pack(byte_t, R))
 
 
+@pytest.mark.parametrize("both", [False, True])
+def test_square_scales_through_a_row_map(plan, g, both):
+    """With 128 x 128 scales too, a row without a source has scale bytes of 0, and its codes are left; it
+    takes no part in its block's scale, and its column of the transposed matrix is zero."""
+    import torch
+    rng = np.random.default_rng(13)
+    T, k, K, rows = 90, 2, 300, 500
+    x = values(rng, T, K, "bf16")
+    rowmap = np.full(rows, -1)
+    rowmap[rng.permutation(rows - 200)[:T * k]] = np.arange(T * k)  # (the last tile has no row at all)
+    rowmap[rows - 1] = T * k  # past X
+    src = np.where((rowmap >= 0) & (rowmap < T * k), rowmap // k, -1)
+    moved = np.where((src >= 0)[:, None], x.double().numpy()[src], 0.0)
+    _, q = rows_of(rows, K, "e4m3", fill=0xA5)
+    sq = torch.full((g.gemm_scale_bytes(rows, K),), 0xEE, dtype=torch.uint8, device="cuda")
+    _, qt = rows_of(K, rows, "e4m3", fill=0xA5)
+    st = torch.full((g.gemm_scale_bytes(K, rows),), 0xEE, dtype=torch.uint8, device="cuda")
+    assert plan.quantize(x.cuda(), q, sq, *((qt, st) if both else ()), map_div=k, block_rows=128,
+                         rowmap=torch.from_numpy(rowmap.astype(np.int32)).cuda()) == 0
+    want, byte = ref.quantize(moved, "e4m3", 128)
+    got = ref.decode(q.view(torch.uint8).cpu().numpy(), "e4m3")
+    np.testing.assert_array_equal(got[src >= 0], want[src >= 0])
+    assert (q.view(torch.uint8)[torch.from_numpy(src < 0).cuda()] == 0xA5).all()
+    byte[src < 0] = 0
+    np.testing.assert_array_equal(sq.cpu().numpy(), ref.pack(byte, K))
+    if both:
+        want, byte = ref.quantize(moved.T, "e4m3", 128)
+        np.testing.assert_array_equal(ref.decode(qt.view(torch.uint8).cpu().numpy(), "e4m3"), want)
+        np.testing.assert_array_equal(st.cpu().numpy(), ref.pack(byte, rows))
+
+
 def test_quantize_refusals(plan, g):
     import torch
     x = torch.zeros((8, 64), device="cuda", dtype=torch.bfloat16)
