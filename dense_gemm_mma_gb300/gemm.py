@@ -354,7 +354,11 @@ def _matrix(t):
     ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError("expected a 2-D tensor with contiguous rows")
-    return t.data_ptr(), rows, cols, ld if ld >= cols and ld > 0 else max(cols, 1)
+    if ld < cols or ld <= 0:  # only a row that is alone (or empty) has no use for its stride
+        if rows > 1 and cols > 0:
+            raise ValueError("rows share memory (an expanded tensor?): expected each on its own")
+        ld = max(cols, 1)
+    return t.data_ptr(), rows, cols, ld
 
 
 def _matrices(t):
