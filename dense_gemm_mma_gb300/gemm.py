@@ -368,8 +368,16 @@ def _matrices(t):
     group, ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError("expected a 3-D stack of matrices with contiguous rows")
-    ld = max(ld, cols, 1)
-    return t.data_ptr(), n, rows, cols, ld, max(group, ld * rows)
+    some = n > 0 and rows > 0 and cols > 0
+    if ld < cols or ld <= 0:
+        if rows > 1 and some:
+            raise ValueError("rows share memory (an expanded tensor?): expected each on its own")
+        ld = max(cols, 1)
+    if group < (rows - 1) * ld + cols:  # only a matrix that is alone (or empty) has no use for its stride
+        if n > 1 and some:
+            raise ValueError("the stack's matrices share memory or interleave: expected one after another")
+        group = ld * rows
+    return t.data_ptr(), n, rows, cols, ld, group
 
 
 def _scales(t, rows: int, cols: int, groups: int = 1) -> int:

@@ -72,3 +72,30 @@ def test_expanded_arguments_never_reach_a_kernel(plan):
         with pytest.raises(ValueError):
             call()
             pytest.fail("call %d" % n)
+
+
+def test_strides_of_a_stack():
+    t = torch.zeros((3, 5, 8))
+    close = torch.zeros(64).as_strided((3, 2, 6), (14, 8, 1))  # a matrix begins right after the one before ends
+    for view, ld, group in ((t, 8, 40), (t[:, :2], 8, 40), (t[:, :, :3], 8, 40), (t[::2], 8, 80), (t[:1], 8, 40), (close, 8, 14),
+                            (t.transpose(0, 1)[:1], 40, 120), (torch.zeros((2, 0, 8)), 8, 8), (torch.zeros((4, 1, 8)), 8, 8),
+                            (torch.zeros((5, 8)).expand(1, 5, 8), 8, 40), (torch.zeros((4, 6)).unsqueeze(1)[:, :, :1], 6, 6)):
+        p, n, rows, cols, *strides = g._matrices(view)
+        assert (p, n, rows, cols) == (view.data_ptr(), *view.shape) and strides == [ld, group], (view.shape, strides)
+
+
+def test_stacks_whose_matrices_share_or_interleave_are_refused(plan):
+    E, N, K, rows = 4, 32, 128, 512
+    A, SA, i = codes(rows, K), scales(rows, K), torch.zeros(E, dtype=torch.int32)
+    D = torch.zeros((rows, N))
+    stacks = lambda n, r, c, zero: (  # noqa: E731
+        zero(r, n, c).transpose(0, 1), zero(r, c).expand(n, r, c), zero(n, 1, c).expand(n, r, c), zero(n * r * c + 1).as_strided((n, r, c), (r * c - 1, c, 1)))
+    for B in stacks(E, N, K, codes):
+        with pytest.raises(ValueError):
+            g._matrices(B)
+        with pytest.raises(ValueError):
+            plan.run_grouped(A, SA, B, scales(N, K, E), D, i, i)
+    QT, ST = codes(N, rows), scales(N, rows)
+    for out in stacks(E, N, N, lambda *shape: torch.zeros(shape)):
+        with pytest.raises(ValueError):
+            plan.run_grouped_k(QT, ST, QT, ST, out, i, i)
