@@ -426,6 +426,8 @@ def _operand(t, trans: bool):
     """(pointer, ld) of a stored 2-D operand whose rows are contiguous."""
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError("operands must be 2-D with contiguous rows")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError("rows share memory (an expanded tensor?): expected each on its own")
     return t.data_ptr(), max(t.stride(0), t.shape[1], 1)
 
 

@@ -99,3 +99,15 @@ def test_stacks_whose_matrices_share_or_interleave_are_refused(plan):
     for out in stacks(E, N, N, lambda *shape: torch.zeros(shape)):
         with pytest.raises(ValueError):
             plan.run_grouped_k(QT, ST, QT, ST, out, i, i)
+
+
+def test_expanded_operands_of_the_dense_product_are_refused(plan):
+    bf16 = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16)  # noqa: E731
+    whole = (bf16(16, 64), bf16(64, 32), bf16(16, 32))
+    for at, t in enumerate(whole):
+        bad = list(whole)
+        bad[at] = bf16(t.shape[1]).expand(*t.shape)
+        with pytest.raises(ValueError):
+            plan.run(*bad)
+    assert g._operand(bf16(64).expand(1, 64), False)[1] == 64
+    assert g._operand(whole[0][::2, :5], False)[1] == 128
