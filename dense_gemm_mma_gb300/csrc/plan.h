@@ -194,6 +194,7 @@ inline bool overlaps(Region x, Region y) {
   const uint64_t xe = x.base + uint64_t(x.rows - 1) * uint64_t(x.pitch) + uint64_t(x.width);
   const uint64_t ye = y.base + uint64_t(y.rows - 1) * uint64_t(y.pitch) + uint64_t(y.width);
   if (xe <= y.base || ye <= x.base) return false;  // disjoint spans
+  if (x.rows == 1 && y.rows == 1) return true;  // (whose pitches mean nothing, and may be 0)
   if (x.rows == 1) x.pitch = y.pitch;  // a single row fits any pitch
   if (y.rows == 1) y.pitch = x.pitch;
   if (x.pitch == y.pitch) {

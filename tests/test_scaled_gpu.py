@@ -244,6 +244,23 @@ def test_quantize_refusals(plan, g):
         plan.quantize(x, q, s[:100])
 
 
+def test_quantize_refuses_runs_of_bytes_that_meet(plan, g):
+    """Scales over scales, over the map or over a single row: runs of bytes without a pitch."""
+    import torch
+    x = torch.zeros((1, 64), device="cuda", dtype=torch.bfloat16)
+    q = torch.zeros(64, device="cuda", dtype=torch.uint8)
+    qt = torch.zeros(64 * 16, device="cuda", dtype=torch.uint8)
+    s = torch.zeros(4096, device="cuda", dtype=torch.uint8)
+    base, rowmap = s.data_ptr(), s.data_ptr() + 2048
+    call = lambda **c: g.gemm_quantize(*{**dict(  # noqa: E731
+        plan=plan.handle, rows=1, cols=64, X=x.data_ptr(), ldx=64, x_type=0, rowmap=rowmap, map_div=1, src_rows=1, q_type=4,
+        block_rows=1, Q=q.data_ptr(), ldq=64, SQ=base, QT=qt.data_ptr(), ldqt=16, SQT=base + 512), **c}.values())
+    assert call() == g.GEMM_OK
+    for bad in ({"SQT": base}, {"SQT": base + 496}, {"SQ": rowmap - 496}, {"SQT": rowmap}, {"SQ": q.data_ptr()}, {"Q": base + 480},
+                {"SQ": x.data_ptr()}):
+        assert call(**bad) == g.GEMM_ERR_INVALID_ARG, bad
+
+
 # ------------------------------------------------------------------- products
 
 KERNELS = [None, "tile", "pair", "sliced"]

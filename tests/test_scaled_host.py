@@ -62,6 +62,19 @@ def test_invalid(change):
     assert check(**change) == g.GEMM_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("change", [
+    {"D": 0x200000}, {"D": 0x200000 + 496}, {"D": 0x200000 - 16}, {"D": 0x400000}, {"D": 0x400000 + 496, "N": 8, "ldd": 8},
+    {"D": 0x100000 + 192}, {"N": 1, "D": 0x400000 + 496}, {"N": 1, "D": 0x300000 + 192}, {"N": 1, "D": 0x100000}])
+def test_one_row_over_an_operand(change):
+    """One row of D against one run of bytes (scales, one row of an operand): neither has a pitch that means anything."""
+    assert check(M=1, **change) == g.GEMM_ERR_INVALID_ARG
+
+
+def test_one_row_beside_the_operands():
+    for d in (0x200000 - 192, 0x200000 + 512, 0x400000 - 192, 0x400000 + 512, 0x100000 + 208):
+        assert check(M=1, D=d) == g.GEMM_OK
+
+
 @pytest.mark.parametrize("change", [{"SA": 0x200004}, {"SB": 0x400008}, {"D": 0x500008}, {"ldd": 100}])
 def test_misaligned(change):
     assert check(**change) == g.GEMM_ERR_ALIGNMENT
