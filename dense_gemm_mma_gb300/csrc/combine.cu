@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(const CombineArgs
     for (int j = 0; j < KC; ++j) {
       const int64_t slot = warp * a.k + j0 + j;
       row[j] = j0 + j < a.k ? row_of(a, slot) : -1;
-      w[j] = row[j] >= 0 && DG_IN(a.dbg, a.weights + slot, 4, DBG_COMBINE) ? __ldg(a.weights + slot) : 0.f;
+      // (a plain load: dweights may be the same array)
+      w[j] = row[j] >= 0 && DG_IN(a.dbg, a.weights + slot, 4, DBG_COMBINE) ? a.weights[slot] : 0.f;
       dot[j] = 0.f;
     }
     for (int col = share * (32 * kPiece) + lane * U::COLS; col < a.cols; col += WARPS * 32 * kPiece) {

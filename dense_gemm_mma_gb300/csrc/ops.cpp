@@ -98,9 +98,11 @@ gemm_status_t check_product(const Product& x) {
   if (x.group != SC_DENSE && (!x.starts || !x.counts)) return GEMM_ERR_INVALID_ARG;
   if (!x.D) return GEMM_ERR_INVALID_ARG;
   const int64_t es = type_bytes(x.d_type);
+  const Region d = group_region(x.D, by_k ? x.groups : 1, x.M, x.N, x.ldd, x.d_group, es);
+  if (x.group != SC_DENSE && (overlaps(d, region(x.starts, 1, x.groups * 4, 0, 1)) || overlaps(d, region(x.counts, 1, x.groups * 4, 0, 1))))
+    return GEMM_ERR_INVALID_ARG;
   if (x.K > 0) {
     if (!x.A || !x.B || !x.SA || !x.SB) return GEMM_ERR_INVALID_ARG;
-    const Region d = group_region(x.D, by_k ? x.groups : 1, x.M, x.N, x.ldd, x.d_group, es);
     const int64_t nb = rows ? x.groups : 1;
     if (overlaps(d, region(x.A, x.M, x.K, x.lda, 1)) ||
         overlaps(d, group_region(x.B, nb, x.N, x.K, x.ldb, x.b_group, 1)) ||
@@ -383,6 +385,20 @@ int access_bytes(int64_t cols, std::initializer_list<std::pair<const void*, int6
   return wide;
 }
 
+// A run of n bytes.
+Region run_of(const void* p, int64_t n) { return region(p, p ? 1 : 0, n, 0, 1); }
+
+// Does a result share a byte with an input or with another result?
+bool results_meet(std::initializer_list<Region> results, std::initializer_list<Region> inputs) {
+  for (const Region* r = results.begin(); r != results.end(); ++r) {
+    for (const Region& i : inputs)
+      if (overlaps(*r, i)) return true;
+    for (const Region* o = results.begin(); o != r; ++o)
+      if (overlaps(*r, *o)) return true;
+  }
+  return false;
+}
+
 gemm_status_t check_route(int64_t tokens, int64_t experts, const void* logits, int64_t ldl, gemm_type_t type,
                           const gemm_route_t& r) {
   if (tokens < 0 || experts < 1 || !is_float_type(type)) return GEMM_ERR_INVALID_ARG;
@@ -520,15 +536,10 @@ gemm_status_t gemm_quantize(gemm_plan_t plan, int64_t rows, int64_t cols, const 
       !aligned(SQT, 16) || (Q && ldq % 16) || (QT && ldqt % 16))
     return GEMM_ERR_ALIGNMENT;
   // no result may share a byte with X, the map or another result
-  const Region in[2] = {region(X, xr, cols, ldx, es), region(rowmap, rowmap ? 1 : 0, rows * 4, 0, 1)};
-  const Region out[4] = {region(Q, Q ? rows : 0, cols, ldq, 1), region(SQ, SQ ? 1 : 0, gemm_scale_bytes(rows, cols), 0, 1),
-                         region(QT, QT ? cols : 0, rows, ldqt, 1),
-                         region(SQT, SQT ? 1 : 0, gemm_scale_bytes(cols, rows), 0, 1)};
-  for (int i = 0; i < 4; ++i) {
-    if (overlaps(out[i], in[0]) || overlaps(out[i], in[1])) return GEMM_ERR_INVALID_ARG;
-    for (int j = 0; j < i; ++j)
-      if (overlaps(out[i], out[j])) return GEMM_ERR_INVALID_ARG;
-  }
+  if (results_meet({region(Q, Q ? rows : 0, cols, ldq, 1), run_of(SQ, gemm_scale_bytes(rows, cols)),
+                    region(QT, QT ? cols : 0, rows, ldqt, 1), run_of(SQT, gemm_scale_bytes(cols, rows))},
+                   {region(X, xr, cols, ldx, es), run_of(rowmap, rows * 4)}))
+    return GEMM_ERR_INVALID_ARG;
   DeviceGuard guard(plan->device);
   QuantArgs a{};
   a.x = X;
@@ -569,6 +580,10 @@ gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, cons
   if (st != GEMM_OK || tokens == 0) return st;
   if (!weights || !indices) return GEMM_ERR_INVALID_ARG;
   if (!aligned(weights, 4) || !aligned(indices, 4) || !aligned(bias, 4)) return GEMM_ERR_ALIGNMENT;
+  const int64_t slots = tokens * route.top_k;
+  if (results_meet({run_of(weights, slots * 4), run_of(indices, slots * 4)},
+                   {region(logits, tokens, experts, ldl, type_bytes(l_type)), run_of(bias, experts * 4)}))
+    return GEMM_ERR_INVALID_ARG;
   DeviceGuard guard(plan->device);
   RouteArgs a = route_args(plan, tokens, experts, logits, ldl, l_type, route);
   a.bias = bias;
@@ -592,6 +607,12 @@ gemm_status_t gemm_route_backward(gemm_plan_t plan, int64_t tokens, int64_t expe
   if (!indices || !dweights || !dlogits) return GEMM_ERR_INVALID_ARG;
   if (!aligned(dweights, 4) || !aligned(indices, 4) || !aligned(dlogits, size_t(type_bytes(l_type))))
     return GEMM_ERR_ALIGNMENT;
+  // (a token's logits are read before its gradients are written: these may be the logits' own place)
+  const int64_t es = type_bytes(l_type), slots = tokens * route.top_k;
+  const bool in_place = dlogits == logits && lddl == ldl;
+  if (results_meet({region(dlogits, tokens, experts, lddl, es)},
+                   {region(logits, in_place ? 0 : tokens, experts, ldl, es), run_of(indices, slots * 4), run_of(dweights, slots * 4)}))
+    return GEMM_ERR_INVALID_ARG;
   DeviceGuard guard(plan->device);
   RouteArgs a = route_args(plan, tokens, experts, logits, ldl, l_type, route);
   a.indices = const_cast<int32_t*>(indices);
@@ -623,15 +644,19 @@ gemm_status_t gemm_route_map(gemm_plan_t plan, int64_t tokens, int64_t top_k, in
   if ((tokens > 0 && (!indices || !pos)) || (rows > 0 && !rowmap)) return GEMM_ERR_INVALID_ARG;
   if (!aligned(indices, 4) || !aligned(starts, 4) || !aligned(counts, 4) || !aligned(pos, 4) || !aligned(rowmap, 4))
     return GEMM_ERR_ALIGNMENT;
+  const int64_t slots = tokens * top_k;
+  if (results_meet({run_of(starts, experts * 4), run_of(counts, experts * 4), run_of(pos, slots * 4), run_of(rowmap, rows * 4)},
+                   {run_of(indices, slots * 4)}))
+    return GEMM_ERR_INVALID_ARG;
   DeviceGuard guard(plan->device);
-  const size_t ws = route_map_workspace(tokens * top_k, experts);
+  const size_t ws = route_map_workspace(slots, experts);
   if (ws > 0) {
     const gemm_status_t st = ensure_ws(plan, ws, static_cast<cudaStream_t>(stream));
     if (st != GEMM_OK) return st;
   }
   RouteMapArgs a{};
   a.indices = indices;
-  a.slots = int(tokens * top_k);
+  a.slots = int(slots);
   a.experts = int(experts);
   a.starts = starts;
   a.counts = counts;
@@ -655,7 +680,10 @@ gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top_k, int6
   const gemm_status_t st = check_combine(tokens, top_k, cols, rows, Y, ldy, y_type, pos, weights, out, ldo, out_type);
   if (st != GEMM_OK || tokens == 0 || cols == 0) return st;
   const int64_t ye = type_bytes(y_type), oe = type_bytes(out_type);
-  if (overlaps(region(out, tokens, cols, ldo, oe), region(Y, rows, cols, ldy, ye))) return GEMM_ERR_INVALID_ARG;
+  const int64_t slots = tokens * top_k;
+  if (results_meet({region(out, tokens, cols, ldo, oe)},
+                   {region(Y, rows, cols, ldy, ye), run_of(pos, slots * 4), run_of(weights, slots * 4)}))
+    return GEMM_ERR_INVALID_ARG;
   DeviceGuard guard(plan->device);
   CombineArgs a{};
   a.tokens = int(tokens);
@@ -692,8 +720,13 @@ gemm_status_t gemm_combine_backward(gemm_plan_t plan, int64_t tokens, int64_t to
   if (cols == 0 && (!pos || !weights)) return GEMM_ERR_INVALID_ARG;
   const int64_t ye = type_bytes(y_type), oe = type_bytes(out_type);
   if (!aligned(dY, size_t(ye)) || !aligned(dweights, 4) || !aligned(rowmap, 4)) return GEMM_ERR_ALIGNMENT;
-  const Region d = region(dY, rows, cols, lddy, ye);
-  if (overlaps(d, region(Y, rows, cols, ldy, ye)) || overlaps(d, region(dout, tokens, cols, ldo, oe)))
+  // (a token's weights are read before their gradients are written: these may be the weights' own place)
+  const int64_t slots = tokens * top_k;
+  if (results_meet({region(dY, rows, cols, lddy, ye), run_of(dweights, slots * 4)},
+                   {region(Y, rows, cols, ldy, ye), region(dout, tokens, cols, ldo, oe), run_of(pos, slots * 4),
+                    run_of(rowmap, rows * 4)}) ||
+      overlaps(region(dY, rows, cols, lddy, ye), run_of(weights, slots * 4)) ||
+      (dweights != weights && overlaps(run_of(dweights, slots * 4), run_of(weights, slots * 4))))
     return GEMM_ERR_INVALID_ARG;
   DeviceGuard guard(plan->device);
   CombineArgs a{};

@@ -488,8 +488,8 @@ gemm_status_t gemm_check_scaled(int64_t M, int64_t N, int64_t K, const void* A, 
  * gemm_scale_bytes(N, K) after the last group's) into the same rows of D (rows x N), as
  * gemm_run_scaled.  starts and counts (device, `groups` int32 each) are gemm_route_map's:
  * starts are multiples of 128, so that a group's rows begin a scale tile.  A group whose start is no
- * multiple of 128 or outside [0, rows) counts as empty, a count past the end of A is cut there.  Rows of D that are
- * in no group are left as they are.  What A holds in rows between groups does not matter.
+ * multiple of 128 or outside [0, rows) counts as empty, a count past the end of A is cut there.  D may share no byte
+ * with starts or counts either.  Rows of D that are in no group are left as they are.  What A holds in rows between groups does not matter.
  * groups <= 1024; B is read where it is if b_group is a multiple of 16 too, else the groups that have rows
  * are copied. */
 gemm_status_t gemm_run_grouped(gemm_plan_t plan, int64_t groups, int64_t rows, int64_t N, int64_t K,
@@ -533,6 +533,7 @@ typedef struct {
  * key below every other of its group choice; where fewer than top_k experts are left, masked ones of
  * the chosen groups follow in order of index, with weight 0.  Experts of other groups are never chosen.
  * Renormalising a sum of 0 gives weights 0.
+ * weights and indices may share no byte with each other, the logits or the bias.
  * experts <= 1024, a multiple of groups, and top_k <= experts of top_groups groups. */
 gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
                          gemm_type_t l_type, const float* bias, gemm_route_t route, float* weights, int32_t* indices,
@@ -541,7 +542,8 @@ gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, cons
 /* Gradient of gemm_route: dlogits (tokens x experts, of the logits' type, every entry written)
  * from dweights (tokens x top_k) and the choice it made (indices; one outside [0,
  * experts) takes no part).  The choice itself has no gradient.  Of `route`, score, top_k,
- * renormalize and scale are used. */
+ * renormalize and scale are used.  dlogits may be the logits themselves (the same
+ * address and stride), and may share no byte with an input otherwise. */
 gemm_status_t gemm_route_backward(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
                                   gemm_type_t l_type, gemm_route_t route, const int32_t* indices,
                                   const float* dweights, void* dlogits, int64_t lddl, void* stream);
@@ -553,7 +555,8 @@ int64_t gemm_route_rows(int64_t tokens, int64_t top_k, int64_t experts);
 /* The order of the slots (slot = token * top_k + choice) by expert: expert e's slots, in their
  * own order, take rows starts[e] .. starts[e] + counts[e], starts[e] the next multiple of 128
  * after the experts before.  pos[slot] is the slot's row (-1 where its index is outside [0, experts)),
- * rowmap[row] the row's slot (-1: none), for `rows` rows, gemm_route_rows(...) at least. */
+ * rowmap[row] the row's slot (-1: none), for `rows` rows, gemm_route_rows(...) at least.
+ * starts, counts, pos and rowmap may share no byte with each other or with indices. */
 gemm_status_t gemm_route_map(gemm_plan_t plan, int64_t tokens, int64_t top_k, int64_t experts, const int32_t* indices,
                              int32_t* starts, int32_t* counts, int32_t* pos, int32_t* rowmap, int64_t rows,
                              void* stream);
@@ -561,7 +564,7 @@ gemm_status_t gemm_route_map(gemm_plan_t plan, int64_t tokens, int64_t top_k, in
 /* out[t] <- sum over j of weights[t, j] * Y[pos[t, j]], in fp32 with one rounding: the experts' rows
  * (Y rows x cols) back into tokens (out tokens x cols).  A pos that is negative or >= rows adds
  * nothing.  Y and out are of any of GEMM_TYPE_F32, BF16, F16 and need only their element's alignment (rows
- * on 16-byte boundaries are faster); out may not share a byte with Y. */
+ * on 16-byte boundaries are faster); out may not share a byte with Y, pos or weights. */
 gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top_k, int64_t cols, int64_t rows, const void* Y,
                            int64_t ldy, gemm_type_t y_type, const int32_t* pos, const float* weights, void* out,
                            int64_t ldo, gemm_type_t out_type, void* stream);
@@ -569,7 +572,9 @@ gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top_k, int6
 /* Gradients of gemm_combine from dout (tokens x cols, out_type): dY[pos[t, j]] <-
  * weights[t, j] * dout[t] (dY of Y's type) and dweights[t, j] <- <dout[t], Y[pos[t, j]]> (0
  * where pos leads nowhere).  pos must name no row twice, as gemm_route_map's does not.  With rowmap (`rows`
- * int32; NULL: none) the rows of dY that hold no slot are set to zero; other rows are left as they are. */
+ * int32; NULL: none) the rows of dY that hold no slot are set to zero; other rows are left as they are.
+ * dweights may be the weights themselves (the same address); dY and dweights may share no byte with each
+ * other or an input otherwise. */
 gemm_status_t gemm_combine_backward(gemm_plan_t plan, int64_t tokens, int64_t top_k, int64_t cols, int64_t rows,
                                     const void* dout, int64_t ldo, gemm_type_t out_type, const void* Y, int64_t ldy,
                                     gemm_type_t y_type, const int32_t* pos, const float* weights,

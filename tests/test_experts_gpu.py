@@ -304,3 +304,79 @@ def test_refusals(plan, g):
     assert c(out=p + 3074) == g.GEMM_ERR_ALIGNMENT
     with pytest.raises(ValueError):
         plan.combine(t.view(64, 64), torch.zeros((4, 2), dtype=torch.int64, device="cuda"), t[:8].view(4, 2), t.view(64, 64)[:4])
+
+
+def test_results_may_not_share_bytes(plan, g):
+    """A result over an input or over another result is refused before anything is launched: most would be read
+    after they were written."""
+    import torch
+    t = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    p = t.data_ptr()
+    T, E, k = 8, 16, 2
+    r = g.gemm_route_t(0, k, 1, 1, 1, 0, 1.0)
+    # logits 8 x 16 f32 in rows of 20: 624 bytes from p
+    route = lambda **c: g.gemm_route(*{**dict(plan=plan.handle, tokens=T, experts=E, logits=p, ldl=20, l_type=2, bias=p + 1024,  # noqa: E731
+                                              route=r, weights=p + 2048, indices=p + 4096), **c}.values())
+    assert route() == 0 and route(weights=p + 624) == 0 and route(indices=p + 2048 + 64) == 0 and route(bias=None) == 0
+    for bad in ({"weights": p}, {"weights": p + 620}, {"indices": p + 560}, {"indices": p + 2048 + 60}, {"weights": p + 1024 + 60},
+                {"indices": p + 1024 - 60}):
+        assert route(**bad) == g.GEMM_ERR_INVALID_ARG, bad
+    back = lambda **c: g.gemm_route_backward(*{**dict(plan=plan.handle, tokens=T, experts=E, logits=p, ldl=20, l_type=2, route=r,  # noqa: E731
+                                                      indices=p + 4096, dweights=p + 2048, dlogits=p + 8192, lddl=20), **c}.values())
+    assert back() == 0 and back(dlogits=p) == 0 and back(dlogits=p + 640, lddl=16) == 0
+    for bad in ({"dlogits": p, "lddl": 16}, {"dlogits": p + 4}, {"dlogits": p + 4096 - 64, "lddl": 16}, {"dlogits": p + 2048}):
+        assert back(**bad) == g.GEMM_ERR_INVALID_ARG, bad
+    t.zero_()
+    rows = g.gemm_route_rows(T, k, E)
+    order = lambda **c: g.gemm_route_map(*{**dict(plan=plan.handle, tokens=T, top_k=k, experts=E, indices=p, starts=p + 1024,  # noqa: E731
+                                                  counts=p + 2048, pos=p + 3072, rowmap=p + 4096, rows=rows), **c}.values())
+    assert order() == 0
+    for bad in ({"pos": p}, {"pos": p + 60}, {"starts": p + 2048 + 60}, {"counts": p + 3072 - 60}, {"rowmap": p + 4}, {"pos": p + 4096 + 4 * rows - 4}):
+        assert order(**bad) == g.GEMM_ERR_INVALID_ARG, bad
+    t.zero_()
+    summed = lambda **c: g.gemm_combine(*{**dict(plan=plan.handle, tokens=T, top_k=k, cols=E, rows=32, Y=p, ldy=16, y_type=2,  # noqa: E731
+                                                 pos=p + 4096, weights=p + 5120, out=p + 8192, ldo=16, out_type=2), **c}.values())
+    assert summed() == 0
+    for bad in ({"out": p + 1024}, {"out": p + 4096 + 60}, {"out": p + 5120 - 480}):
+        assert summed(**bad) == g.GEMM_ERR_INVALID_ARG, bad
+    grads = lambda **c: g.gemm_combine_backward(*{**dict(  # noqa: E731
+        plan=plan.handle, tokens=T, top_k=k, cols=E, rows=32, dout=p + 8192, ldo=16, out_type=2, Y=p, ldy=16, y_type=2, pos=p + 4096,
+        weights=p + 5120, rowmap=p + 6144, dY=p + 16384, lddy=16, dweights=p + 7168), **c}.values())
+    assert grads() == 0 and grads(dweights=p + 5120) == 0 and grads(rowmap=None) == 0
+    for bad in ({"dY": p}, {"dY": p + 8192 + 256}, {"dY": p + 4096 + 60}, {"dY": p + 5120 + 60}, {"dY": p + 6144}, {"dweights": p + 16384 + 64},
+                {"dweights": p + 5120 + 4}, {"dweights": p + 4096}, {"dweights": p + 6144 + 124}, {"dweights": p + 2044}, {"dweights": p + 8192}):
+        assert grads(**bad) == g.GEMM_ERR_INVALID_ARG, bad
+    c = lambda **k: g.gemm_run_grouped(*{**dict(  # noqa: E731
+        plan=plan.handle, groups=2, rows=256, N=32, K=64, starts=p + 40960, counts=p + 41984, A=p + 49152, lda=64, SA=p, a_type=4,
+        B=p + 45056, ldb=64, b_group=2048, SB=p + 1024, b_type=4, D=p + 4096, ldd=32, d_type=2, alpha=1.0, beta=0.0), **k}.values())
+    assert c() == 0 and c(starts=p + 4096 + 256 * 128) == 0
+    for bad in ({"starts": p + 4096 + 64}, {"counts": p + 4096 + 256 * 128 - 4}):
+        assert c(**bad) == g.GEMM_ERR_INVALID_ARG, bad
+    assert plan.poll_error() == 0
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("E", [8, 60, 128])
+def test_gradients_in_place(plan, g, name, E):
+    """dlogits over the logits, dweights over the weights: the same bits as in places of their own."""
+    import torch
+    rng = np.random.default_rng(E)
+    T, k = 70, 4
+    for score, renormalize in (("softmax", False), ("sigmoid", True), ("softmax", True)):
+        x, _, i = run_route(plan, g, grid_logits(rng, T, E), k, name, score=score)
+        i[3, 1] = i[3, 0]  # two choices of one expert
+        how = dict(score=g.GEMM_SCORE_SIGMOID if score == "sigmoid" else g.GEMM_SCORE_SOFTMAX, renormalize=renormalize)
+        xd = torch.from_numpy(x).cuda().to(dtype(name))
+        i, dw, dx = torch.from_numpy(i).cuda(), torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda(), torch.empty_like(xd)
+        assert plan.route_backward(xd, i, dw, dx, **how) == 0
+        assert plan.route_backward(xd, i, dw, xd, **how) == 0
+        assert torch.equal(xd, dx)
+    for T, k, N in ((20, 4, 512), (20, 19, 512), (1500, 3, 256), (30, 5, 90)):
+        pos, rowmap, Y, w, pd, rd = combine_case(rng, g, T, k, E, N, name, name, 0)
+        _, dout = rows_of(T, N, name)
+        dout.copy_(torch.from_numpy(rng.standard_normal((T, N))))
+        dY, dw, dY2 = torch.zeros_like(Y), torch.empty_like(w), torch.zeros_like(Y)
+        assert plan.combine_backward(dout, Y, pd, w, dY, dw, rowmap=rd) == 0
+        assert plan.combine_backward(dout, Y, pd, w, dY2, w, rowmap=rd) == 0
+        assert torch.equal(dY, dY2) and torch.equal(dw, w)
+    assert plan.poll_error() == 0
