@@ -947,6 +947,7 @@ gemm_status_t gemm_plan_destroy(gemm_plan_t plan) {
   if (plan->ws) cudaFree(plan->ws);
   if (plan->tws) cudaFree(plan->tws);
   if (plan->counters) cudaFree(plan->counters);
+  for (void* p : plan->kept) cudaFree(p);
   if (plan->err) cudaFree(plan->err);
   delete plan;
   return GEMM_OK;
@@ -1060,7 +1061,7 @@ gemm_status_t run_all(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, const v
     const size_t a_bytes = copy_a ? size_t(M) * size_t(lda_t) * 4 : 0;
     const size_t b_bytes = copy_b ? size_t(N) * size_t(ldb_t) * 4 : 0;
     const size_t a_off = 0, b_off = (a_bytes + 255) & ~size_t(255);
-    r = ensure_buffer(&plan->tws, &plan->tws_bytes, b_off + b_bytes, s);
+    r = ensure_tws(plan, b_off + b_bytes, s);
     const void* A2 = A;
     const void* B2 = B;
     int64_t lda2 = lda, ldb2 = ldb;

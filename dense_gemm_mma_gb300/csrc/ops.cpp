@@ -252,7 +252,7 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   const size_t a_copy = repack_bytes(x.A, x.lda, 1, 0, x.M, x.K);
   const size_t b_copy = repack_bytes(x.B, x.ldb, b_groups, x.b_group, x.N, x.K);
   if (a_copy + b_copy > 0) {
-    gemm_status_t st = ensure_buffer(&plan->tws, &plan->tws_bytes, a_copy + b_copy, s);
+    gemm_status_t st = ensure_tws(plan, a_copy + b_copy, s);
     int64_t none = 0;
     if (st == GEMM_OK && a_copy) st = repack(plan, &x.A, &x.lda, 1, &none, x.M, x.K, nullptr, plan->tws, s);
     if (st == GEMM_OK && b_copy)

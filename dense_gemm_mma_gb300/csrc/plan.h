@@ -13,6 +13,7 @@
 #include <cstdlib>
 #include <mutex>
 #include <unordered_map>
+#include <vector>
 
 #include "kernels.h"
 
@@ -77,10 +78,14 @@ struct gemm_plan {
   int sms = 0;
   int* err = nullptr;  // device word, OR of wait codes (and, debug build, failed-check sites)
   int64_t last_err_bits = 0;  // the word the last gemm_plan_poll_error read
-  void* ws = nullptr;  // workspace (split-K partials, GEMV partials)
+  void* ws = nullptr;  // workspace (split-K partials, GEMV partials, counts of the slots' order)
   size_t ws_bytes = 0;
+  // Whether a captured graph holds the buffer's address: it then lives as long as the plan, in `kept`
+  // once a larger one has taken its place.
+  bool ws_in_graph = false, tws_in_graph = false, counters_in_graph = false;
+  std::vector<void*> kept;
   unsigned* counters = nullptr;  // GEMV per-panel arrival counters: zero between calls
-  void* tws = nullptr;  // K-major copies of TF32 operands stored M/N-major
+  void* tws = nullptr;  // K-major copies of TF32 operands stored M/N-major, copies of unaligned codes
   size_t tws_bytes = 0;
   size_t counter_count = 0;
   uint64_t watchdog_ns = 2000000000ull;
@@ -238,45 +243,87 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // ------------------------------------------------------------- workspace
 
-// Grow a plan buffer to at least `bytes` (1 MiB steps, stream-ordered,
-// zero-filled).
-inline gemm_status_t ensure_buffer(void** buf, size_t* have, size_t bytes, cudaStream_t s) {
-  if (bytes <= *have) return GEMM_OK;
-  size_t nb = std::max<size_t>(bytes, size_t(1) << 20);
-  nb = (nb + (size_t(1) << 20) - 1) & ~((size_t(1) << 20) - 1);
-  if (*buf) cudaFreeAsync(*buf, s);
+// Is `s` being captured?  (A query that fails, as for the legacy stream during another's capture, means no.)
+inline bool capturing(cudaStream_t s) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &status) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return status != cudaStreamCaptureStatusNone;
+}
+
+// `bytes` of zeroed device memory allocated at once, not as a node of the graph that the calling thread
+// is capturing: such memory would exist in that graph's launches only.
+inline cudaError_t alloc_outside_capture(void** out, size_t bytes) {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // this thread may allocate meanwhile
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return e;
+  cudaStream_t side = nullptr;
+  e = cudaMalloc(out, bytes);
+  if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking);
+  if (e == cudaSuccess) e = cudaMemsetAsync(*out, 0, bytes, side);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(side);
+  if (side) cudaStreamDestroy(side);
+  if (e != cudaSuccess && *out) {
+    cudaFree(*out);
+    *out = nullptr;
+  }
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  return e;
+}
+
+// Make a plan buffer at least `bytes` long (multiples of `step`, zero-filled; stream-ordered on `s`, except in a
+// capture).  What a captured graph works on is never freed or moved under it: a buffer that was used
+// in a capture stays with the plan when it is replaced.
+inline gemm_status_t ensure_buffer(gemm_plan* plan, void** buf, size_t* have, bool* in_graph, size_t bytes, size_t step,
+                                   cudaStream_t s) {
+  const bool graph = capturing(s);
+  if (bytes <= *have) {
+    *in_graph |= graph;
+    return GEMM_OK;
+  }
+  const size_t nb = (bytes + step - 1) / step * step;
+  if (*buf && (graph || *in_graph)) {
+    try {
+      plan->kept.push_back(*buf);
+    } catch (...) {
+      return GEMM_ERR_OUT_OF_MEMORY;
+    }
+  } else if (*buf) {
+    cudaFreeAsync(*buf, s);
+  }
   *buf = nullptr;
   *have = 0;
-  if (cudaMallocAsync(buf, nb, s) != cudaSuccess) {
+  *in_graph = graph;
+  if ((graph ? alloc_outside_capture(buf, nb) : cudaMallocAsync(buf, nb, s)) != cudaSuccess) {
     cudaGetLastError();
     *buf = nullptr;
     return GEMM_ERR_OUT_OF_MEMORY;
   }
-  if (cudaMemsetAsync(*buf, 0, nb, s) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (!graph && cudaMemsetAsync(*buf, 0, nb, s) != cudaSuccess) return GEMM_ERR_CUDA;
   *have = nb;
   return GEMM_OK;
 }
 
 inline gemm_status_t ensure_ws(gemm_plan* plan, size_t bytes, cudaStream_t s) {
-  return ensure_buffer(&plan->ws, &plan->ws_bytes, bytes, s);
+  return ensure_buffer(plan, &plan->ws, &plan->ws_bytes, &plan->ws_in_graph, bytes, size_t(1) << 20, s);
+}
+
+inline gemm_status_t ensure_tws(gemm_plan* plan, size_t bytes, cudaStream_t s) {
+  return ensure_buffer(plan, &plan->tws, &plan->tws_bytes, &plan->tws_in_graph, bytes, size_t(1) << 20, s);
 }
 
 // The counters are zeroed once when allocated; every kernel that uses one
 // leaves it at zero again.
 inline gemm_status_t ensure_counters(gemm_plan* plan, size_t count, cudaStream_t s) {
-  if (count <= plan->counter_count) return GEMM_OK;
-  size_t nc = std::max<size_t>(count, 4096);
-  if (plan->counters) cudaFreeAsync(plan->counters, s);
-  plan->counters = nullptr;
-  plan->counter_count = 0;
-  if (cudaMallocAsync(reinterpret_cast<void**>(&plan->counters), nc * sizeof(unsigned), s) != cudaSuccess) {
-    cudaGetLastError();
-    plan->counters = nullptr;
-    return GEMM_ERR_OUT_OF_MEMORY;
-  }
-  if (cudaMemsetAsync(plan->counters, 0, nc * sizeof(unsigned), s) != cudaSuccess) return GEMM_ERR_CUDA;
-  plan->counter_count = nc;
-  return GEMM_OK;
+  void* buf = plan->counters;
+  size_t bytes = plan->counter_count * sizeof(unsigned);
+  const gemm_status_t st = ensure_buffer(plan, &buf, &bytes, &plan->counters_in_graph, count * sizeof(unsigned),
+                                         4096 * sizeof(unsigned), s);
+  plan->counters = static_cast<unsigned*>(buf);
+  plan->counter_count = bytes / sizeof(unsigned);
+  return st;
 }
 
 struct DeviceGuard {

@@ -176,8 +176,11 @@ gemm_status_t gemm_plan_create(gemm_plan_t* plan, int device);
 
 /* C <- act(alpha * op(A) @ op(B) + beta * C), enqueued on `stream` (a
  * cudaStream_t; NULL means the legacy default stream).  Calls may be captured
- * into a CUDA graph; a call whose shape, pointers and flags the plan has seen
- * before (same workspace size) adds only kernel launches to the capture.  See the top of this
+ * into a CUDA graph and add only kernel launches to it: workspace that a captured
+ * call has to add is allocated at once, outside the graph (the host waits for that; a call of the
+ * same sizes before the capture avoids it), and what a captured call uses stays where it is
+ * until gemm_plan_destroy, so that a graph may be replayed after later calls have grown
+ * the workspace.  Replays are subject to the rule on streams at the top like calls.  See the top of this
  * file for the layout of A, B and C; all three are device pointers.
  *
  * Dispatch: M == 0 or N == 0 launches nothing; K == 0 or alpha == 0 gives
@@ -421,8 +424,9 @@ gemm_status_t gemm_gemv_noalloc(int64_t M, int64_t N, int64_t K,
  * byte in its 128 rows.
  *
  * The calls below are asynchronous on `stream` (a cudaStream_t), ordered like
- * gemm_run's, may be captured into a CUDA graph and keep nothing
- * between calls.  Row counts that depend on the data (counts, starts, pos, rowmap) are
+ * gemm_run's, may be captured into a CUDA graph as gemm_run may, and keep no result
+ * between calls.  Two of them use plan workspace, which grows as gemm_run's does: gemm_route_map for more than 2,048
+ * slots, and products of codes that have to be copied first.  Row counts that depend on the data (counts, starts, pos, rowmap) are
  * read on the device: no call waits for them.  Errors are those of gemm_run: argument
  * problems come back before anything is launched.  Results are deterministic.
  * ------------------------------------------------------------------------ */
