@@ -283,9 +283,12 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
   }
 }
 
-// With S = the chosen scores' sum, w_j = scale s_j / S (or scale s_j):
-//   ds_j = scale (dw_j - sum_i dw_i s_i / S) / S   (or scale dw_j)
-//   dx_i = s_i (ds_i - sum_j ds_j s_j) (softmax), s_i (1 - s_i) ds_i (sigmoid).
+// Without renormalising w_j = scale s_j, and with g_j = scale dw_j s_j
+//   dx_i = g_i - s_i sum_j g_j (softmax), g_i (1 - s_i) (sigmoid)
+// where g_i is 0 for experts that were not chosen.  With it w_j = scale s_j / S, S the chosen scores' sum, and
+//   g_j = scale (s_j / S) (dw_j - sum_i dw_i s_i / S)
+// whose sum is 0 whatever dw: softmax's second term goes.  Written by the quotients s_j / S, which are at most 1, so
+// that nothing overflows however small the chosen scores are ((dw_j - ...) / S does from S ~ 1e-38).
 // The scores are computed again from the logits: reading them costs what reading kept scores would.
 template <int P>
 __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) {
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
   const int t = int(blockIdx.x * 4 + (threadIdx.x >> 5));
   if (t >= a.tokens) return;
   const int run = (a.experts + 31) / 32, first = lane * run;
-  float x[P], ds[P];
+  float x[P], dx[P];
   load_logits(a, t, first, run, a.wide, x);
   float lane_best = kNegInf;
 #pragma unroll
@@ -310,54 +313,55 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
   }
   const float chosen = logit(a, t, expert);
   const float sj = chosen == kNegInf ? 0.f : scorer.score(chosen);
-  float dsj = a.scale * dw;
+  float gj = a.scale * dw * sj;
+  float through = 0.f;
   if (a.renormalize) {
     const float sum = warp_sum(sj);
-    // by the weights, not the scores: a token whose one score is its sum has a weight of exactly
-    // 1, and a gradient of exactly 0
-    const float dot = warp_sum(sum > 0.f ? dw * (sj / sum) : 0.f);
-    dsj = sum > 0.f && expert >= 0 ? a.scale * (dw - dot) / sum : 0.f;
+    // a token whose one score is its sum has a weight of exactly 1, and a gradient of exactly 0
+    const float w = sum > 0.f ? sj / sum : 0.f;
+    const float dot = warp_sum(dw * w);
+    gj = a.scale * w * (dw - dot);
+  } else if (!a.sigmoid) {
+    through = warp_sum(gj);
   }
-  const float through = a.sigmoid ? 0.f : warp_sum(dsj * sj);
-  // dsj from lane j to the lane of its expert: through shared memory, or one after another
+  // gj from lane j to the lane of its expert: through shared memory, or one after another
   // where two choices name the same expert (their sum then has an order)
   __shared__ float moved[4][32 * P];
   float* const mine = moved[threadIdx.x >> 5] + lane * P;
   const uint32_t same = __match_any_sync(kAll, expert >= 0 ? expert : -1 - lane);
   if (__any_sync(kAll, (same & (same - 1)) != 0)) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) ds[i] = 0.f;
+    for (int i = 0; i < P; ++i) dx[i] = 0.f;
     for (int j = 0; j < a.top_k; ++j) {
       const int at = __shfl_sync(kAll, expert, j) - first;
-      const float d = __shfl_sync(kAll, dsj, j);
+      const float d = __shfl_sync(kAll, gj, j);
 #pragma unroll
       for (int i = 0; i < P; ++i)
-        if (at == i && i < run) ds[i] += d;
+        if (at == i && i < run) dx[i] += d;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < P; ++i) mine[i] = 0.f;
     __syncwarp();
-    if (expert >= 0) moved[threadIdx.x >> 5][expert / run * P + expert % run] = dsj;
+    if (expert >= 0) moved[threadIdx.x >> 5][expert / run * P + expert % run] = gj;
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < P; ++i) ds[i] = mine[i];
+    for (int i = 0; i < P; ++i) dx[i] = mine[i];
   }
-  if (!a.sigmoid) {
+  if (a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (dx[i] == 0.f) continue;  // (experts that were not chosen)
+      dx[i] *= 1.f - scorer.score(x[i]);
+    }
+  } else if (through != 0.f) {
     const float over = scorer.sum > 0.f ? 1.f / scorer.sum : 0.f;
     if (fabsf(scorer.top) < -kNegInf) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) ds[i] = expf(x[i] - scorer.top) * over * (ds[i] - through);
+      for (int i = 0; i < P; ++i) dx[i] -= expf(x[i] - scorer.top) * over * through;
     } else {
 #pragma unroll
-      for (int i = 0; i < P; ++i) ds[i] = scorer.power(x[i]) * over * (ds[i] - through);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      if (ds[i] == 0.f) continue;  // (experts that were not chosen)
-      const float s = scorer.score(x[i]);
-      ds[i] = s * (1.f - s) * ds[i];
+      for (int i = 0; i < P; ++i) dx[i] -= scorer.power(x[i]) * over * through;
     }
   }
   const int es = a.kind == OUT_F32 ? 4 : 2;
@@ -368,10 +372,10 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
 #pragma unroll
       for (int i = 0; i < P; i += 4) {
         if (a.kind == OUT_F32)
-          *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(ds[i], ds[i + 1], ds[i + 2], ds[i + 3]);
+          *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(dx[i], dx[i + 1], dx[i + 2], dx[i + 3]);
         else
           *reinterpret_cast<uint2*>(dst + 2 * i) =
-              make_uint2(half_pair(ds[i], ds[i + 1], a.kind), half_pair(ds[i + 2], ds[i + 3], a.kind));
+              make_uint2(half_pair(dx[i], dx[i + 1], a.kind), half_pair(dx[i + 2], dx[i + 3], a.kind));
       }
       return;
     }
@@ -380,9 +384,9 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
   for (int i = 0; i < P; ++i) {
     if (i >= run || first + i >= a.experts || !DG_IN(a.dbg, dst + i * es, es, DBG_ROUTE)) continue;
     if (es == 4)
-      *reinterpret_cast<float*>(dst + 4 * i) = ds[i];
+      *reinterpret_cast<float*>(dst + 4 * i) = dx[i];
     else
-      *reinterpret_cast<uint16_t*>(dst + 2 * i) = uint16_t(half_pair(ds[i], 0.f, a.kind));
+      *reinterpret_cast<uint16_t*>(dst + 2 * i) = uint16_t(half_pair(dx[i], 0.f, a.kind));
   }
 }
 

@@ -380,3 +380,31 @@ def test_gradients_in_place(plan, g, name, E):
         assert plan.combine_backward(dout, Y, pd, w, dY2, w, rowmap=rd) == 0
         assert torch.equal(dY, dY2) and torch.equal(dw, w)
     assert plan.poll_error() == 0
+
+
+@pytest.mark.parametrize("E", [8, 100, 256])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_gradient_of_tiny_scores(plan, g, score, E):
+    """Renormalised weights of experts whose scores are near fp32's least numbers (a bias or the groups chose
+    them): their sum's reciprocal overflows, the gradient does not.  Tolerance: a score s in that range is off by 2^-150
+    and a quotient of sums of k by k + 1 times that over the least chosen score, besides the 2^-16 of the others; a gradient is at most
+    the weights' sum of |dw| times 2."""
+    import torch
+    rng = np.random.default_rng(E + 1)
+    T, k = 40, 4
+    x = rng.uniform(-95.0, -86.0, (T, E)) if score == "softmax" else rng.uniform(-88.5, -87.0, (T, E))
+    i = np.argsort(rng.random((T, E - 1)), 1)[:, :k] + 1
+    if score == "softmax":
+        x[:, 0] = 0.0  # the score that is not tiny, which nobody chose
+    x = x.astype(np.float32)
+    dw = (rng.standard_normal((T, k)) * 100).astype(np.float32)
+    dx = torch.full((T, E), 9.0, device="cuda")
+    assert plan.route_backward(torch.from_numpy(x).cuda(), torch.from_numpy(i.astype(np.int32)).cuda(), torch.from_numpy(dw).cuda(), dx,
+                               score=g.GEMM_SCORE_SIGMOID if score == "sigmoid" else g.GEMM_SCORE_SOFTMAX, renormalize=True, scale=1.5) == 0
+    want = ref.route_backward(x, i, dw, score, renormalize=True, scale=1.5)
+    _, _, s = ref.route(x, 1, score)
+    least = np.take_along_axis(s, i, 1).min(1, keepdims=True)
+    got = dx.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= (2.0 ** -16 + (k + 1) * 2.0 ** -149 / least) * 2 * 1.5 * np.abs(dw).sum(1, keepdims=True)).all()
+    assert (np.abs(want).max(1) > 1).mean() > 0.8  # (of the oracle alone: most rows have a gradient worth the name)
