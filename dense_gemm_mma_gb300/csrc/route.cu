@@ -313,15 +313,15 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
   }
   const float chosen = logit(a, t, expert);
   const float sj = chosen == kNegInf ? 0.f : scorer.score(chosen);
-  float gj = a.scale * dw * sj;
-  float through = 0.f;
+  float gj = sj, through = 0.f;
   if (a.renormalize) {
     const float sum = warp_sum(sj);
     // a token whose one score is its sum has a weight of exactly 1, and a gradient of exactly 0
     const float w = sum > 0.f ? sj / sum : 0.f;
     const float dot = warp_sum(dw * w);
     gj = a.scale * w * (dw - dot);
-  } else if (!a.sigmoid) {
+  } else {
+    gj *= a.scale * dw;
     through = warp_sum(gj);
   }
   // gj from lane j to the lane of its expert: through shared memory, or one after another
@@ -348,20 +348,22 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
 #pragma unroll
     for (int i = 0; i < P; ++i) dx[i] = mine[i];
   }
-  if (a.sigmoid) {
+  if (!a.sigmoid) {
+    // (also where weights are renormalised and `through` is 0: a branch round it took two registers more than
+    // the 32 with which 16 CTAs share an SM)
+    const float by = scorer.sum > 0.f ? through / scorer.sum : 0.f;
+    if (fabsf(scorer.top) < -kNegInf) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) dx[i] -= expf(x[i] - scorer.top) * by;
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) dx[i] -= scorer.power(x[i]) * by;
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       if (dx[i] == 0.f) continue;  // (experts that were not chosen)
       dx[i] *= 1.f - scorer.score(x[i]);
-    }
-  } else if (through != 0.f) {
-    const float over = scorer.sum > 0.f ? 1.f / scorer.sum : 0.f;
-    if (fabsf(scorer.top) < -kNegInf) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) dx[i] -= expf(x[i] - scorer.top) * over * through;
-    } else {
-#pragma unroll
-      for (int i = 0; i < P; ++i) dx[i] -= scorer.power(x[i]) * over * through;
     }
   }
   const int es = a.kind == OUT_F32 ? 4 : 2;
