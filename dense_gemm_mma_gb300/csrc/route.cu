@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteArgs a) {
 }
 
 // Without renormalising w_j = scale s_j, and with g_j = scale dw_j s_j
-//   dx_i = g_i - s_i sum_j g_j (softmax), g_i (1 - s_i) (sigmoid)
-// where g_i is 0 for experts that were not chosen.  With it w_j = scale s_j / S, S the chosen scores' sum, and
+//   dx_i = g_i - s_i sum_j g_j (softmax), g_i (1 - s_i) = g_i / (1 + exp(x_i)) (sigmoid)
+// where g_i is 0 for experts that were not chosen (the difference 1 - s_i of a rounded s_i would be 1% off at x_i = 12).  With it w_j = scale s_j / S, S the chosen scores' sum, and
 //   g_j = scale (s_j / S) (dw_j - sum_i dw_i s_i / S)
 // whose sum is 0 whatever dw: softmax's second term goes.  Written by the quotients s_j / S, which are at most 1, so
 // that nothing overflows however small the chosen scores are ((dw_j - ...) / S does from S ~ 1e-38).
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       if (dx[i] == 0.f) continue;  // (experts that were not chosen)
-      dx[i] *= 1.f - scorer.score(x[i]);
+      dx[i] = __fdiv_rn(dx[i], __fadd_rn(1.f, expf(x[i])));
     }
   }
   const int es = a.kind == OUT_F32 ? 4 : 2;

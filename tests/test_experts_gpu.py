@@ -408,3 +408,29 @@ def test_route_gradient_of_tiny_scores(plan, g, score, E):
     assert np.isfinite(got).all()
     assert (np.abs(got - want) <= (2.0 ** -16 + (k + 1) * 2.0 ** -149 / least) * 2 * 1.5 * np.abs(dw).sum(1, keepdims=True)).all()
     assert (np.abs(want).max(1) > 1).mean() > 0.8  # (of the oracle alone: most rows have a gradient worth the name)
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_route_gradient_of_sure_sigmoids(plan, g, renormalize):
+    """Sigmoid scores near 1, whose gradient is s (1 - s): 1 - s keeps the precision of exp(-x) where s has none left.  Tolerance:
+    test_route_gradient's, with that factor in the terms."""
+    import torch
+    rng = np.random.default_rng(21)
+    T, E, k = 64, 40, 6
+    x = rng.uniform(-2.0, 20.0, (T, E)).astype(np.float32)
+    i = np.argsort(rng.random((T, E)), 1)[:, :k]
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    dx = torch.empty((T, E), device="cuda")
+    assert plan.route_backward(torch.from_numpy(x).cuda(), torch.from_numpy(i.astype(np.int32)).cuda(), torch.from_numpy(dw).cuda(), dx,
+                               score=g.GEMM_SCORE_SIGMOID, renormalize=renormalize) == 0
+    x64 = x.astype(np.float64)
+    s, rest = 1 / (1 + np.exp(-x64)), 1 / (1 + np.exp(x64))
+    sj = np.take_along_axis(s, i, 1)
+    w = sj / sj.sum(1, keepdims=True) if renormalize else sj
+    d = dw - (dw * w).sum(1, keepdims=True) if renormalize else dw
+    want, terms = np.zeros((T, E)), np.zeros((T, E))
+    np.put_along_axis(want, i, w * d, 1)
+    np.put_along_axis(terms, i, w * (np.abs(dw).sum(1, keepdims=True) if renormalize else np.abs(dw)) * 2, 1)
+    got = dx.double().cpu().numpy()
+    assert (np.abs(got - want * rest) <= 2.0 ** -16 * terms * rest).all()
+    assert rest[got != 0].min() < 1e-7
