@@ -434,3 +434,26 @@ def test_route_gradient_of_sure_sigmoids(plan, g, renormalize):
     got = dx.double().cpu().numpy()
     assert (np.abs(got - want * rest) <= 2.0 ** -16 * terms * rest).all()
     assert rest[got != 0].min() < 1e-7
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(1, 8, 2), (33, 60, 6), (7, 1024, 32), (70, 128, 8)])
+def test_route_gradient_f16(plan, g, score, T, E, k):
+    """Logits and their gradient in f16: test_route_gradient's tolerance and f16's least step."""
+    import torch
+    rng = np.random.default_rng(T * E + k + 1)
+    for renormalize in (False, True):
+        x, _, i = run_route(plan, g, grid_logits(rng, T, E), k, "f16", score=score, renormalize=renormalize)
+        dw = rng.standard_normal((T, k)).astype(np.float32)
+        xd = torch.full((T, E + 3), 3.0, device="cuda", dtype=torch.float16)
+        xd[:, :E] = torch.from_numpy(x)
+        dx = torch.full((T, E + 5), 9.0, device="cuda", dtype=torch.float16)
+        assert plan.route_backward(xd[:, :E], torch.from_numpy(i).cuda(), torch.from_numpy(dw).cuda(), dx[:, :E],
+                                   score=g.GEMM_SCORE_SIGMOID if score == "sigmoid" else g.GEMM_SCORE_SOFTMAX, renormalize=renormalize) == 0
+        want = ref.route_backward(x, i, dw, score, renormalize)
+        _, _, s = ref.route(x, 1, score)
+        total = np.take_along_axis(s, i.astype(np.int64), 1).sum(1, keepdims=True) if renormalize else 1.0
+        terms = s * np.abs(dw).sum(1, keepdims=True) * 2 / total
+        got = dx[:, :E].double().cpu().numpy()
+        assert (np.abs(got - want) <= 2.0 ** -16 * terms + ROUND["f16"] * np.abs(want) + 2.0 ** -25).all()
+        assert (dx[:, E:] == 9).all()
