@@ -323,6 +323,7 @@ enum ScGroup : int {
 
 constexpr int SC_BK = 128;           // K values per ring stage: one 128-byte swizzle row, one scale
 constexpr int SC_MAX_GROUPS = 1024;  // groups whose tile counts fit the kernels' table
+constexpr int SC_MAX_TILES = 1 << 30;  // output tiles of a call
 
 struct ScParams {
   int M, N;        // rows of A and of B (of one group's B)

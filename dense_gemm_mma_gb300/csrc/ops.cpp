@@ -307,7 +307,7 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   const int64_t bound = x.group == SC_ROWS  // SC_ROWS: whole tiles and one partial tile for each group at most
                             ? (ceil_div(x.M, tile_m) + std::min<int64_t>(x.groups, ceil_div(x.M, 128))) * p.n_blocks
                             : int64_t(p.m_blocks) * p.n_blocks * (x.group == SC_K ? x.groups : 1);
-  if (bound > kMaxDim) return GEMM_ERR_UNSUPPORTED;
+  if (bound > SC_MAX_TILES) return GEMM_ERR_UNSUPPORTED;
   p.units = int(bound);
   if (x.group == SC_ROWS) p.raster = 4;
   int grid;

@@ -89,29 +89,36 @@ __device__ __forceinline__ void sc_segment_of(const ScParams& p, const int2* seg
   }
 }
 
-// SC_ROWS: table[e] = tiles of the groups before e, table[groups] = all tiles.
+// Tile rows of a group.
+__device__ __forceinline__ int sc_tile_rows(int count, int tile_rows) {
+  return int((uint32_t(count) + uint32_t(tile_rows) - 1) / uint32_t(tile_rows));
+}
+
+// SC_ROWS: table[e] = tiles of the groups before e, table[groups] = all tiles; SC_MAX_TILES where there
+// would be more (one group has no more, so that only groups that share rows, which a caller's starts
+// should not make, get there; tiles past it are left out, and no sum wraps).
 // Executed by one warp.  seg: the groups' segments in shared memory, or null.
 __device__ __forceinline__ void sc_tile_table(const ScParams& p, int tile_rows, const int2* seg, int* table) {
   const int lane = threadIdx.x & 31;
   int carry = 0;
   for (int e0 = 0; e0 < p.groups; e0 += 32) {
     const int e = e0 + lane;
-    int tiles = 0;
+    int sum = 0;
     if (e < p.groups) {
       int start, count;
       sc_segment_of(p, seg, e, &start, &count);
-      tiles = (count + tile_rows - 1) / tile_rows * p.n_blocks;
+      sum = sc_tile_rows(count, tile_rows) * p.n_blocks;
     }
-    int sum = tiles;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += o;
+      if (lane >= d) sum = min(sum, SC_MAX_TILES - o) + o;
     }
-    if (e < p.groups) table[e] = carry + sum - tiles;
-    carry += __shfl_sync(0xffffffffu, sum, 31);
+    sum = min(sum, SC_MAX_TILES - carry) + carry;
+    if (e < p.groups) table[e + 1] = sum;
+    carry = __shfl_sync(0xffffffffu, sum, 31);
   }
-  if (lane == 0) table[p.groups] = carry;
+  if (lane == 0) table[0] = 0;
 }
 
 // Unit u -> tile.  `cursor` (SC_ROWS) is the group of the caller's last unit:
@@ -129,7 +136,7 @@ __device__ __forceinline__ ScUnit sc_unit(const ScParams& p, int u, int tile_row
     *cursor = e;
     int start, count;
     sc_segment_of(p, seg, e, &start, &count);
-    tile_coords(u - table[e], (count + tile_rows - 1) / tile_rows, p.n_blocks, p.raster, &mb, &nb);
+    tile_coords(u - table[e], sc_tile_rows(count, tile_rows), p.n_blocks, p.raster, &mb, &nb);
     x.row0 = start + mb * tile_rows;
     x.row_end = start + count;
     x.zb = e;
@@ -142,7 +149,7 @@ __device__ __forceinline__ ScUnit sc_unit(const ScParams& p, int u, int tile_row
       int start, count;
       sc_segment_of(p, seg, e, &start, &count);
       x.kb0 = start / SC_BK;
-      x.kb1 = (start + count + SC_BK - 1) / SC_BK;
+      x.kb1 = start / SC_BK + sc_tile_rows(count, SC_BK);  // (a start is a multiple of 128)
       x.zd = e;
     }
     tile_coords(t, p.m_blocks, p.n_blocks, p.raster, &mb, &nb);

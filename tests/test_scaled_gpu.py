@@ -453,6 +453,27 @@ def test_grouped_takes_no_row_outside(plan, g):
     assert plan.poll_error() == 0
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_groups_that_share_rows(plan, monkeypatch, kernel):
+    """Segments over one another: as many tiles in all as they add up to, every one inside the matrices (the groups have
+    equal B, so that it does not matter whose result stays)."""
+    import torch
+    if kernel:
+        monkeypatch.setenv("GEMM_SCALED_KERNEL", kernel)
+    rng = np.random.default_rng(14)
+    rows, N, K, E = 400, 260, 200, 70
+    A, SA, a = operand(rng, rows, K, "e4m3", spread=1)
+    B, SB, b = operand(rng, N, K, "e4m3", spread=1)
+    B = torch.stack([B.view(torch.uint8)] * E).view(torch.float8_e4m3fn)
+    starts = torch.zeros(E, dtype=torch.int32, device="cuda")
+    counts = torch.full((E,), rows, dtype=torch.int32, device="cuda")
+    starts[1::3], counts[2::5] = 128, 0
+    _, D = rows_of(rows, N, "f32", fill=0x7F)
+    assert plan.run_grouped(A, SA, B, torch.cat([SB] * E), D, starts, counts) == 0
+    near(D, *expect(a, b), "f32")
+    assert plan.poll_error() == 0
+
+
 @pytest.mark.parametrize("kernel", [None, "tile", "pair"])
 @pytest.mark.parametrize("counts", COUNTS, ids=lambda c: "e%d" % len(c))
 def test_grouped_k(plan, g, monkeypatch, kernel, counts):
