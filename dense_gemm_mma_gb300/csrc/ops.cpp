@@ -54,6 +54,9 @@ bool map3(CUtensorMap* m, CUtensorMapDataType t, int64_t esize, const void* ptr,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A run of n bytes.
+Region run_of(const void* p, int64_t n) { return region(p, p ? 1 : 0, n, 0, 1); }
+
 // A product as its callers give it.
 struct Product {
   int group = SC_DENSE;
@@ -77,11 +80,15 @@ struct Product {
   bool nothing() const { return M == 0 || N == 0 || groups == 0; }
 };
 
-// Rows of a matrix of `groups` groups: one region where the groups follow each other,
-// else the bytes from the first to the last.
-Region group_region(const void* p, int64_t groups, int64_t rows, int64_t cols, int64_t ld, int64_t group, int64_t es) {
-  if (groups <= 1 || group == rows * ld) return region(p, std::max<int64_t>(groups, 1) * rows, cols, ld, es);
-  return region(p, 1, (groups - 1) * group + (rows - 1) * ld + cols, 0, es);
+// Do `groups` matrices, `group` elements from one to the next, share a byte with y?  What lies between
+// them is not theirs.
+bool groups_meet(const void* p, int64_t groups, int64_t rows, int64_t cols, int64_t ld, int64_t group, int64_t es,
+                 const Region& y) {
+  if (groups <= 1 || group == rows * ld) return overlaps(region(p, std::max<int64_t>(groups, 1) * rows, cols, ld, es), y);
+  if (!overlaps(region(p, 1, (groups - 1) * group + (rows - 1) * ld + cols, 0, es), y)) return false;
+  for (int64_t e = 0; e < groups; ++e)
+    if (overlaps(region(static_cast<const char*>(p) + e * group * es, rows, cols, ld, es), y)) return true;
+  return false;
 }
 
 gemm_status_t check_product(const Product& x) {
@@ -98,16 +105,18 @@ gemm_status_t check_product(const Product& x) {
   if (x.group != SC_DENSE && (!x.starts || !x.counts)) return GEMM_ERR_INVALID_ARG;
   if (!x.D) return GEMM_ERR_INVALID_ARG;
   const int64_t es = type_bytes(x.d_type);
-  const Region d = group_region(x.D, by_k ? x.groups : 1, x.M, x.N, x.ldd, x.d_group, es);
-  if (x.group != SC_DENSE && (overlaps(d, region(x.starts, 1, x.groups * 4, 0, 1)) || overlaps(d, region(x.counts, 1, x.groups * 4, 0, 1))))
+  const auto d_meets = [&](const Region& y) {
+    return groups_meet(x.D, by_k ? x.groups : 1, x.M, x.N, x.ldd, x.d_group, es, y);
+  };
+  if (x.group != SC_DENSE && (d_meets(run_of(x.starts, x.groups * 4)) || d_meets(run_of(x.counts, x.groups * 4))))
     return GEMM_ERR_INVALID_ARG;
   if (x.K > 0) {
     if (!x.A || !x.B || !x.SA || !x.SB) return GEMM_ERR_INVALID_ARG;
     const int64_t nb = rows ? x.groups : 1;
-    if (overlaps(d, region(x.A, x.M, x.K, x.lda, 1)) ||
-        overlaps(d, group_region(x.B, nb, x.N, x.K, x.ldb, x.b_group, 1)) ||
-        overlaps(d, region(x.SA, 1, scale_tiles(x.M, x.K) * 512, 0, 1)) ||
-        overlaps(d, region(x.SB, 1, nb * scale_tiles(x.N, x.K) * 512, 0, 1)))
+    if (d_meets(region(x.A, x.M, x.K, x.lda, 1)) || d_meets(run_of(x.SA, scale_tiles(x.M, x.K) * 512)) ||
+        d_meets(run_of(x.SB, nb * scale_tiles(x.N, x.K) * 512)) ||
+        (rows ? groups_meet(x.B, nb, x.N, x.K, x.ldb, x.b_group, 1, region(x.D, x.M, x.N, x.ldd, es))
+              : d_meets(region(x.B, x.N, x.K, x.ldb, 1))))
       return GEMM_ERR_INVALID_ARG;
     if (!aligned(x.SA, 16) || !aligned(x.SB, 16)) return GEMM_ERR_ALIGNMENT;
     if (scale_tiles(x.M, x.K) > kMaxDim || nb * scale_tiles(x.N, x.K) > kMaxDim) return GEMM_ERR_UNSUPPORTED;
@@ -384,9 +393,6 @@ int access_bytes(int64_t cols, std::initializer_list<std::pair<const void*, int6
     while (wide && (!aligned(m.first, size_t(wide)) || m.second % wide)) wide = wide == 16 ? 4 : 0;
   return wide;
 }
-
-// A run of n bytes.
-Region run_of(const void* p, int64_t n) { return region(p, p ? 1 : 0, n, 0, 1); }
 
 // Does a result share a byte with an input or with another result?
 bool results_meet(std::initializer_list<Region> results, std::initializer_list<Region> inputs) {

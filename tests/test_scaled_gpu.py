@@ -506,6 +506,45 @@ def test_grouped_k(plan, g, monkeypatch, kernel, counts):
     assert plan.poll_error() == 0
 
 
+def test_results_between_the_groups(plan, g):
+    """What lies between the matrices of a stack is not theirs: D in the gap between two B, A between two D."""
+    import torch
+    rng = np.random.default_rng(15)
+    rows, N, K = 128, 32, 64
+    A, SA, a = operand(rng, rows, K, "e4m3", spread=1)
+    (B0, SB0, b0), (B1, SB1, b1) = (operand(rng, N, K, "e4m3", spread=1) for _ in range(2))
+    d_bytes, b_bytes = rows * N * 4, N * K
+    buf = torch.zeros(2 * b_bytes + d_bytes, dtype=torch.uint8, device="cuda")
+    buf[:b_bytes], buf[b_bytes + d_bytes:] = B0.view(torch.uint8).reshape(-1), B1.view(torch.uint8).reshape(-1)
+    D = buf[b_bytes:b_bytes + d_bytes].view(torch.float32).view(rows, N)
+    SB = torch.cat([SB0, SB1])
+    starts, counts = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.tensor([0, 100], dtype=torch.int32, device="cuda")
+    call = lambda **c: g.gemm_run_grouped(*{**dict(  # noqa: E731
+        plan=plan.handle, groups=2, rows=rows, N=N, K=K, starts=starts.data_ptr(), counts=counts.data_ptr(), A=A.data_ptr(), lda=A.stride(0),
+        SA=SA.data_ptr(), a_type=4, B=buf.data_ptr(), ldb=K, b_group=b_bytes + d_bytes, SB=SB.data_ptr(), b_type=4, D=D.data_ptr(), ldd=N,
+        d_type=2, alpha=1.0, beta=0.0, act=0, slope=0.0, stream=torch.cuda.current_stream().cuda_stream), **c}.values())
+    assert call() == g.GEMM_OK
+    near(D[:100], *expect(a[:100], b1), "f32")
+    assert (D[100:] == 0).all()
+    assert call(D=D.data_ptr() - 16) == call(D=D.data_ptr() + 16) == g.GEMM_ERR_INVALID_ARG
+    # columns of A and B times each other into two D with A's codes between them
+    QA, SQ, qa = operand(rng, N, rows, "e4m3", spread=1)
+    QA.view(torch.uint8)[:, 100:] = 0
+    qa[:, 100:] = 0
+    one = N * N * 4
+    buf = torch.zeros(2 * one + N * rows, dtype=torch.uint8, device="cuda")
+    buf[one:one + N * rows] = QA.view(torch.uint8).reshape(-1)
+    call = lambda **c: g.gemm_run_grouped_k(*{**dict(  # noqa: E731
+        plan=plan.handle, groups=2, M=N, N=N, rows=rows, starts=starts.data_ptr(), counts=counts.data_ptr(), A=buf.data_ptr() + one, lda=rows,
+        SA=SQ.data_ptr(), a_type=4, B=QA.data_ptr(), ldb=QA.stride(0), SB=SQ.data_ptr(), b_type=4, D=buf.data_ptr(), ldd=N,
+        d_group=(one + N * rows) // 4, d_type=2, alpha=1.0, beta=0.0, act=0, slope=0.0, stream=torch.cuda.current_stream().cuda_stream), **c}.values())
+    assert call() == g.GEMM_OK
+    near(buf[one + N * rows:].view(torch.float32).view(N, N), *expect(qa, qa), "f32")
+    assert (buf[:one] == 0).all()  # an empty group
+    assert call(A=buf.data_ptr() + one - 16) == call(A=buf.data_ptr() + one + 16) == g.GEMM_ERR_INVALID_ARG
+    assert plan.poll_error() == 0
+
+
 def test_grouped_refusals(plan, g):
     import torch
     A = torch.zeros((256, 64), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
