@@ -5,9 +5,12 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <cstdarg>
 #include <cstdint>
+#include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <initializer_list>
@@ -40,6 +43,48 @@ gemm_status_t launched(cudaError_t e) {
   return GEMM_ERR_CUDA;
 }
 
+const char* type_name(gemm_type_t t) {
+  static const char* kName[] = {"bf16", "f16", "f32", "tf32", "e4m3", "e5m2"};
+  return int(t) >= 0 && int(t) < 6 ? kName[int(t)] : "?";
+}
+
+// A call under GEMM_NVTX (a range named after it, closed on every return) and GEMM_LOG (one line when it
+// has succeeded).
+class CallScope {
+ public:
+  CallScope(const gemm_plan* plan, const char* format, ...) __attribute__((format(printf, 3, 4)))
+      : log_(plan->log), nvtx_(plan->nvtx) {
+    if (!log_ && !nvtx_) return;
+    va_list args;
+    va_start(args, format);
+    std::vsnprintf(text_, sizeof text_, format, args);
+    va_end(args);
+    if (nvtx_) nvtxRangePushA(text_);
+  }
+  CallScope(const CallScope&) = delete;
+  CallScope& operator=(const CallScope&) = delete;
+  ~CallScope() {
+    if (nvtx_) nvtxRangePop();
+  }
+  gemm_status_t done(gemm_status_t st, const gemm_config_info_t* c = nullptr) const {
+    if (!log_ || st != GEMM_OK || (c && c->path == GEMM_PATH_NONE)) return st;
+    if (c)
+      std::fprintf(stderr,
+                   "gemm_log %s -> %s tile %dx%d cta/tile %d split %d stages %d grid %d sms %d tiles %lld launches %d "
+                   "workspace %lld B\n",
+                   text_, c->path == GEMM_PATH_SCALED_SLICED ? "scaled_sliced" : "scaled",
+                   c->tile_m, c->tile_n, c->cta_per_tile, c->splitk, c->stages, c->grid, c->sms, (long long)c->tiles, c->launches,
+                   (long long)c->workspace_bytes);
+    else
+      std::fprintf(stderr, "gemm_log %s\n", text_);
+    return st;
+  }
+
+ private:
+  const bool log_, nvtx_;
+  char text_[160];
+};
+
 // 3-D row-major tensor (inner contiguous, ld elements between rows, group elements
 // between groups); boxes of box_inner x box_rows x 1.  Out-of-range reads give zero.
 bool map3(CUtensorMap* m, CUtensorMapDataType t, int64_t esize, const void* ptr, int64_t inner, int64_t rows, int64_t groups,
@@ -59,6 +104,7 @@ Region run_of(const void* p, int64_t n) { return region(p, p ? 1 : 0, n, 0, 1); 
 
 // A product as its callers give it.
 struct Product {
+  const char* name = "gemm_run_scaled";
   int group = SC_DENSE;
   int64_t groups = 1;
   int64_t M = 0, N = 0, K = 0;  // SC_ROWS: M = rows of A and D; SC_K: K = columns of A and B
@@ -380,7 +426,10 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
 gemm_status_t checked_run(gemm_plan_t plan, const Product& x, void* stream) {
   if (!plan) return GEMM_ERR_INVALID_ARG;
   const gemm_status_t st = check_product(x);
-  return st != GEMM_OK ? st : run_product(plan, x, static_cast<cudaStream_t>(stream));
+  if (st != GEMM_OK) return st;
+  const CallScope call(plan, "%s %lldx%lldx%lld groups %lld %s %s->%s", x.name, (long long)x.M, (long long)x.N, (long long)x.K,
+                       (long long)x.groups, type_name(x.a_type), type_name(x.b_type), type_name(x.d_type));
+  return call.done(run_product(plan, x, static_cast<cudaStream_t>(stream)), &plan->last);
 }
 
 // Rows of `ld` elements of es bytes from p allow 16-byte accesses where columns do.
@@ -497,6 +546,7 @@ gemm_status_t gemm_run_grouped(gemm_plan_t plan, int64_t groups, int64_t rows, i
                                const void* SB, gemm_type_t b_type, void* D, int64_t ldd, gemm_type_t d_type,
                                float alpha, float beta, gemm_epilogue_t epilogue, void* stream) {
   Product x;
+  x.name = "gemm_run_grouped";
   x.group = SC_ROWS, x.groups = groups, x.M = rows, x.N = N, x.K = K;
   x.starts = starts, x.counts = counts;
   x.A = A, x.lda = lda, x.SA = SA, x.a_type = a_type;
@@ -512,6 +562,7 @@ gemm_status_t gemm_run_grouped_k(gemm_plan_t plan, int64_t groups, int64_t M, in
                                  gemm_type_t b_type, void* D, int64_t ldd, int64_t d_group, gemm_type_t d_type,
                                  float alpha, float beta, gemm_epilogue_t epilogue, void* stream) {
   Product x;
+  x.name = "gemm_run_grouped_k";
   x.group = SC_K, x.groups = groups, x.M = M, x.N = N, x.K = rows;
   x.starts = starts, x.counts = counts;
   x.A = A, x.lda = lda, x.SA = SA, x.a_type = a_type;
@@ -546,6 +597,9 @@ gemm_status_t gemm_quantize(gemm_plan_t plan, int64_t rows, int64_t cols, const 
                     region(QT, QT ? cols : 0, rows, ldqt, 1), run_of(SQT, gemm_scale_bytes(cols, rows))},
                    {region(X, xr, cols, ldx, es), run_of(rowmap, rows * 4)}))
     return GEMM_ERR_INVALID_ARG;
+  const CallScope call(plan, "gemm_quantize %lldx%lld %s->%s block %dx128%s%s%s", (long long)rows, (long long)cols,
+                       type_name(x_type), type_name(q_type),
+                       int(block_rows), Q ? " Q" : "", QT ? " QT" : "", rowmap ? " by map" : "");
   DeviceGuard guard(plan->device);
   QuantArgs a{};
   a.x = X;
@@ -575,7 +629,7 @@ gemm_status_t gemm_quantize(gemm_plan_t plan, int64_t rows, int64_t cols, const 
               .bytes(SQ, gemm_scale_bytes(rows, cols)).out_matrix(QT, QT ? cols : 0, rows, ldqt, 1)
               .bytes(SQT, gemm_scale_bytes(cols, rows)).bytes(rowmap, rowmap ? rows * 4 : 0).s;
 #endif
-  return launched(launch_quantize(a, static_cast<cudaStream_t>(stream)));
+  return call.done(launched(launch_quantize(a, static_cast<cudaStream_t>(stream))));
 }
 
 gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
@@ -590,6 +644,10 @@ gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, cons
   if (results_meet({run_of(weights, slots * 4), run_of(indices, slots * 4)},
                    {region(logits, tokens, experts, ldl, type_bytes(l_type)), run_of(bias, experts * 4)}))
     return GEMM_ERR_INVALID_ARG;
+  const CallScope call(plan, "gemm_route %lldx%lld %s %s top %d groups %d of %d%s%s", (long long)tokens,
+                       (long long)experts, type_name(l_type),
+                       route.score == GEMM_SCORE_SIGMOID ? "sigmoid" : "softmax", int(route.top_k), int(route.top_groups),
+                       int(route.groups), bias ? " bias" : "", route.renormalize ? " renormalized" : "");
   DeviceGuard guard(plan->device);
   RouteArgs a = route_args(plan, tokens, experts, logits, ldl, l_type, route);
   a.bias = bias;
@@ -599,7 +657,7 @@ gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, cons
   a.dbg = Spans(plan->err).matrix(logits, tokens, experts, ldl, type_bytes(l_type)).bytes(bias, bias ? experts * 4 : 0)
               .bytes(weights, tokens * route.top_k * 4).out_matrix(indices, 1, tokens * route.top_k, 0, 4).s;
 #endif
-  return launched(launch_route(a, static_cast<cudaStream_t>(stream)));
+  return call.done(launched(launch_route(a, static_cast<cudaStream_t>(stream))));
 }
 
 gemm_status_t gemm_route_backward(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
@@ -619,6 +677,10 @@ gemm_status_t gemm_route_backward(gemm_plan_t plan, int64_t tokens, int64_t expe
   if (results_meet({region(dlogits, tokens, experts, lddl, es)},
                    {region(logits, in_place ? 0 : tokens, experts, ldl, es), run_of(indices, slots * 4), run_of(dweights, slots * 4)}))
     return GEMM_ERR_INVALID_ARG;
+  const CallScope call(plan, "gemm_route_backward %lldx%lld %s %s top %d%s", (long long)tokens, (long long)experts,
+                       type_name(l_type),
+                       route.score == GEMM_SCORE_SIGMOID ? "sigmoid" : "softmax", int(route.top_k),
+                       route.renormalize ? " renormalized" : "");
   DeviceGuard guard(plan->device);
   RouteArgs a = route_args(plan, tokens, experts, logits, ldl, l_type, route);
   a.indices = const_cast<int32_t*>(indices);
@@ -630,7 +692,7 @@ gemm_status_t gemm_route_backward(gemm_plan_t plan, int64_t tokens, int64_t expe
   a.dbg = Spans(plan->err).matrix(logits, tokens, experts, ldl, type_bytes(l_type)).bytes(indices, tokens * route.top_k * 4)
               .bytes(dweights, tokens * route.top_k * 4).out_matrix(dlogits, tokens, experts, lddl, type_bytes(l_type)).s;
 #endif
-  return launched(launch_route_backward(a, static_cast<cudaStream_t>(stream)));
+  return call.done(launched(launch_route_backward(a, static_cast<cudaStream_t>(stream))));
 }
 
 int64_t gemm_route_rows(int64_t tokens, int64_t top_k, int64_t experts) {
@@ -654,6 +716,8 @@ gemm_status_t gemm_route_map(gemm_plan_t plan, int64_t tokens, int64_t top_k, in
   if (results_meet({run_of(starts, experts * 4), run_of(counts, experts * 4), run_of(pos, slots * 4), run_of(rowmap, rows * 4)},
                    {run_of(indices, slots * 4)}))
     return GEMM_ERR_INVALID_ARG;
+  const CallScope call(plan, "gemm_route_map %lldx%lld experts %lld rows %lld", (long long)tokens, (long long)top_k,
+                       (long long)experts, (long long)rows);
   DeviceGuard guard(plan->device);
   const size_t ws = route_map_workspace(slots, experts);
   if (ws > 0) {
@@ -676,7 +740,7 @@ gemm_status_t gemm_route_map(gemm_plan_t plan, int64_t tokens, int64_t top_k, in
   a.dbg = Spans(plan->err).bytes(indices, tokens * top_k * 4).bytes(starts, experts * 4).bytes(counts, experts * 4)
               .bytes(pos, tokens * top_k * 4).bytes(plan->ws, int64_t(ws)).out_matrix(rowmap, 1, rows, 0, 4).s;
 #endif
-  return launched(launch_route_map(a, static_cast<cudaStream_t>(stream)));
+  return call.done(launched(launch_route_map(a, static_cast<cudaStream_t>(stream))));
 }
 
 gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top_k, int64_t cols, int64_t rows, const void* Y,
@@ -690,6 +754,9 @@ gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top_k, int6
   if (results_meet({region(out, tokens, cols, ldo, oe)},
                    {region(Y, rows, cols, ldy, ye), run_of(pos, slots * 4), run_of(weights, slots * 4)}))
     return GEMM_ERR_INVALID_ARG;
+  const CallScope call(plan, "gemm_combine %lldx%lldx%lld rows %lld %s->%s", (long long)tokens, (long long)top_k,
+                       (long long)cols, (long long)rows,
+                       type_name(y_type), type_name(out_type));
   DeviceGuard guard(plan->device);
   CombineArgs a{};
   a.tokens = int(tokens);
@@ -710,7 +777,7 @@ gemm_status_t gemm_combine(gemm_plan_t plan, int64_t tokens, int64_t top_k, int6
   a.dbg = Spans(plan->err).matrix(Y, rows, cols, ldy, ye).bytes(pos, tokens * top_k * 4).bytes(weights, tokens * top_k * 4)
               .out_matrix(out, tokens, cols, ldo, oe).s;
 #endif
-  return launched(launch_combine(a, static_cast<cudaStream_t>(stream)));
+  return call.done(launched(launch_combine(a, static_cast<cudaStream_t>(stream))));
 }
 
 gemm_status_t gemm_combine_backward(gemm_plan_t plan, int64_t tokens, int64_t top_k, int64_t cols, int64_t rows,
@@ -734,6 +801,9 @@ gemm_status_t gemm_combine_backward(gemm_plan_t plan, int64_t tokens, int64_t to
       overlaps(region(dY, rows, cols, lddy, ye), run_of(weights, slots * 4)) ||
       (dweights != weights && overlaps(run_of(dweights, slots * 4), run_of(weights, slots * 4))))
     return GEMM_ERR_INVALID_ARG;
+  const CallScope call(plan, "gemm_combine_backward %lldx%lldx%lld rows %lld %s->%s%s", (long long)tokens,
+                       (long long)top_k, (long long)cols,
+                       (long long)rows, type_name(out_type), type_name(y_type), rowmap ? " by map" : "");
   DeviceGuard guard(plan->device);
   CombineArgs a{};
   a.tokens = int(tokens);
@@ -759,7 +829,7 @@ gemm_status_t gemm_combine_backward(gemm_plan_t plan, int64_t tokens, int64_t to
               .bytes(weights, tokens * top_k * 4).bytes(rowmap, rowmap ? rows * 4 : 0).bytes(dweights, tokens * top_k * 4)
               .out_matrix(dY, rows, cols, lddy, ye).s;
 #endif
-  return launched(launch_combine_backward(a, static_cast<cudaStream_t>(stream)));
+  return call.done(launched(launch_combine_backward(a, static_cast<cudaStream_t>(stream))));
 }
 
 }  // extern "C"
