@@ -284,7 +284,7 @@ gemm_status_t repack(gemm_plan* plan, const void** p, int64_t* ld, int64_t group
   a.ld_out = round_up(K, 16);
   a.pdl = plan->pdl;
 #ifdef DG_DEBUG
-  a.dbg = Spans(plan->err).bytes(*p, (groups - 1) * *group + (rows - 1) * *ld + K)
+  a.dbg = Spans(plan->err).input(*p, (groups - 1) * *group + (rows - 1) * *ld + K).bytes(counts, groups * 4)
               .bytes(out, groups * rows * a.ld_out).s;
 #endif
   *p = out;
@@ -403,7 +403,8 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   }
   if (!ok) return GEMM_ERR_CUDA;
 #ifdef DG_DEBUG
-  p.dbg = Spans(plan->err).out_matrix(x.D, 1, x.group == SC_K ? (x.groups - 1) * x.d_group + (x.M - 1) * x.ldd + x.N
+  p.dbg = Spans(plan->err).input(x.starts, x.starts ? x.groups * 4 : 0).input(x.counts, x.counts ? x.groups * 4 : 0)
+              .out_matrix(x.D, 1, x.group == SC_K ? (x.groups - 1) * x.d_group + (x.M - 1) * x.ldd + x.N
                                                              : (x.M - 1) * x.ldd + x.N, 0, es).s;
 #endif
   info.path = sliced ? GEMM_PATH_SCALED_SLICED : GEMM_PATH_SCALED;

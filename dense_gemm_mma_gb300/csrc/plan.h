@@ -146,6 +146,7 @@ inline Region region(const void* p, int64_t rows, int64_t cols, int64_t ld, int6
 // GEMM_DEBUG_SHRINK=n (read by the debug build only, for its tests) makes the
 // output's range n bytes shorter, so that the checks of the last output
 // elements fail while every access stays inside the caller's buffer.
+// GEMM_DEBUG_SHRINK_INPUT does the same for the inputs that say so below.
 struct Spans {
   dg::DbgSpans s{};
   int n = 0;
@@ -172,6 +173,14 @@ struct Spans {
     const int at = n;
     matrix(p, rows, cols, ld, esize);
     return shrink(at);
+  }
+  // an input that a copy or the groups' kernels read, `len` bytes: its range less GEMM_DEBUG_SHRINK_INPUT bytes
+  Spans& input(const void* p, int64_t len) {
+    static const int64_t cut = [] {
+      const char* v = std::getenv("GEMM_DEBUG_SHRINK_INPUT");
+      return v ? std::max<int64_t>(0, std::atoll(v)) : int64_t(0);
+    }();
+    return bytes(p, len - std::min(cut, len));
   }
   Spans& out_vector(const void* p, int64_t count, int64_t inc, int64_t esize) {
     const int at = n;

@@ -451,7 +451,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) repack_kernel(const RepackArgs a, uint32_t pieces) {
   wait_prior_grid();
   const int z = int(blockIdx.z);
-  if (a.counts && __ldg(a.counts + z) <= 0) return;
+  if (a.counts && (!DG_IN(a.dbg, a.counts + z, 4, DBG_QUANTIZE) || __ldg(a.counts + z) <= 0)) return;
   const uint8_t* const in = a.in + z * a.group;
   uint8_t* const out = a.out + int64_t(z) * a.rows * a.ld_out;
   alignas(16) T v[kItems][16 / sizeof(T)];
@@ -467,10 +467,9 @@ __global__ void __launch_bounds__(256) repack_kernel(const RepackArgs a, uint32_
 #pragma unroll
     for (int j = 0; j < int(16 / sizeof(T)); ++j) {
       v[i][j] = 0;
-      if (int(j * sizeof(T)) < n[i] && DG_IN(a.dbg, in + from[i] + j * sizeof(T), 1, DBG_QUANTIZE)) {
-        // (the last one of a row may reach past it: those byte by byte, below)
-        if (int((j + 1) * sizeof(T)) <= n[i]) v[i][j] = __ldg(reinterpret_cast<const T*>(in + from[i]) + j);
-      }
+      // (the last one of a row may reach past it: those byte by byte, below)
+      if (int((j + 1) * sizeof(T)) <= n[i] && DG_IN(a.dbg, in + from[i] + j * sizeof(T), int(sizeof(T)), DBG_QUANTIZE))
+        v[i][j] = __ldg(reinterpret_cast<const T*>(in + from[i]) + j);
     }
   }
 #pragma unroll
@@ -478,7 +477,8 @@ __global__ void __launch_bounds__(256) repack_kernel(const RepackArgs a, uint32_
     if (n[i] <= 0 || !DG_IN(a.dbg, out + to[i], 16, DBG_QUANTIZE)) continue;
     const int whole = n[i] / int(sizeof(T)) * int(sizeof(T));
     *reinterpret_cast<uint4*>(out + to[i]) = *reinterpret_cast<const uint4*>(&v[i][0]);
-    for (int b = whole; b < n[i]; ++b) out[to[i] + b] = __ldg(in + from[i] + b);
+    for (int b = whole; b < n[i]; ++b)
+      if (DG_IN(a.dbg, in + from[i] + b, 1, DBG_QUANTIZE)) out[to[i] + b] = __ldg(in + from[i] + b);
   }
 }
 

@@ -72,6 +72,8 @@ struct ScUnit {
 // multiple of 128 or lies outside [0, cap) means an empty group, a count that
 // reaches past cap is cut there, so that no device value leads out of a buffer.
 __device__ __forceinline__ void sc_segment(const ScParams& p, int e, int* start, int* count) {
+  *start = *count = 0;
+  if (!DG_IN(p.dbg, p.starts + e, 4, DBG_SCALED) || !DG_IN(p.dbg, p.counts + e, 4, DBG_SCALED)) return;
   const int s = __ldg(p.starts + e), c = __ldg(p.counts + e);
   const bool ok = s >= 0 && s < p.cap && (s & 127) == 0 && c > 0;
   *start = ok ? s : 0;

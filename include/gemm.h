@@ -302,7 +302,9 @@ gemm_status_t gemm_plan_last_error_bits(gemm_plan_t plan, int64_t* bits);
  * plan to report through and is not checked.  For its own tests the debug
  * build reads GEMM_DEBUG_SHRINK=n once per process: the output's byte
  * range is taken n bytes shorter than it is, so that the checks of the last
- * output elements fail while every access stays inside the buffer. */
+ * output elements fail while every access stays inside the buffer.
+ * GEMM_DEBUG_SHRINK_INPUT=n does that for the groups' starts and counts and for codes that
+ * are copied before a product. */
 int gemm_debug_build(void);
 
 /* Limit, in nanoseconds, of every bounded wait inside this plan's kernels

@@ -38,3 +38,7 @@ def test_operators_pass_their_tests_under_the_checks():
 
 def test_skipped_and_reported():
     assert _run(["-m", "tests.debug_ops"], GEMM_DEBUG_SHRINK="4").strip().startswith("ok")
+
+
+def test_inputs_skipped_and_reported():
+    assert _run(["-m", "tests.debug_inputs"], GEMM_DEBUG_SHRINK_INPUT="4").strip().startswith("ok")
