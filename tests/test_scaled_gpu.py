@@ -327,6 +327,43 @@ def test_operands_at_any_address(plan, by, off):
     assert plan.poll_error() == 0
 
 
+@pytest.mark.parametrize("K", [328, 41, 12, 8, 345])
+@pytest.mark.parametrize("ld,off", [(8, 0), (8, 8), (4, 4), (1, 0), (1, 3)])
+def test_copied_codes(plan, K, ld, off):
+    """Rows `ld` bytes past a multiple of 16 apart, from an address `off` bytes past one: copied first, by words as wide as both
+    allow, the last word of a row in part; and the call says so."""
+    import torch
+    rng = np.random.default_rng(K + ld + off)
+    M, N, E = 50, 70, 3
+    A, SA, a = operand(rng, M, K, "e5m2", spread=1)
+    Bs = [operand(rng, N, K, "e4m3", spread=1) for _ in range(E)]
+    pitch = -(-K // 16) * 16 + ld
+
+    def moved(t, *lead):
+        flat = torch.full((t.numel() // K * pitch + off,), 0x7F, dtype=torch.uint8, device="cuda")[off:]
+        view = flat.view(*lead, pitch)[..., :K]
+        view.copy_(t)
+        assert view.data_ptr() % 16 == off
+        return view.view(torch.float8_e4m3fn if t.dim() == 3 else torch.float8_e5m2)
+
+    A2 = moved(A.view(torch.uint8), M)
+    B2 = moved(torch.stack([b.view(torch.uint8) for b, _, _ in Bs]), E, N)
+    _, D = rows_of(M, N, "f32", fill=0x7F)
+    assert plan.run_scaled(A2, SA, B2[2], Bs[2][1], D) == 0
+    info = plan.last_config()
+    assert info["launches"] == 3 and info["workspace_bytes"] == (M + N) * -(-K // 16) * 16
+    near(D, *expect(a, Bs[2][2]), "f32")
+    rows = 128 * E
+    A3, SA3, a3 = operand(rng, rows, K, "e4m3", spread=1)
+    starts, counts = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 128, 256], [5, 0, 100]))
+    _, D = rows_of(rows, N, "f32", fill=0)
+    assert plan.run_grouped(A3, SA3, B2, torch.stack([s for _, s, _ in Bs]), D, starts, counts) == 0
+    assert plan.last_config()["launches"] == 2
+    for s, n, e in ((0, 5, 0), (256, 100, 2)):
+        near(D[s:s + n], *expect(a3[s:s + n], Bs[e][2]), "f32")
+    assert plan.poll_error() == 0
+
+
 def test_product_many_tiles_and_units(plan, monkeypatch):
     """Every kernel over several tiles a CTA (accumulators and scale columns reused), the slices' rows shared out."""
     import torch
@@ -429,6 +466,38 @@ def test_grouped(plan, g, monkeypatch, kernel, counts):
                 near(D[s:s + m], want, off, out)
         assert torch.equal(buf.view(torch.uint8).view(rows, -1)[none], before.view(torch.uint8).view(rows, -1)[none])
         assert torch.equal(buf[:, N:].contiguous().view(torch.uint8), before[:, N:].contiguous().view(torch.uint8))
+    assert plan.poll_error() == 0
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("fa,fb", [("e5m2", "e4m3"), ("e5m2", "e5m2"), ("e4m3", "e5m2")])
+def test_grouped_types(plan, monkeypatch, kernel, fa, fb):
+    """The input gradient of experts: 8-bit gradients (e5m2) times transposed weights, in every kernel, with an activation or beta."""
+    import torch
+    if kernel:
+        monkeypatch.setenv("GEMM_SCALED_KERNEL", kernel)
+    rng = np.random.default_rng(16)
+    starts, n, rows = segments([33, 0, 130, 64, 300])
+    for N, K, out, beta, act in ((264, 520, "bf16", 0.0, 0), (136, 384, "f32", 0.5, 0), (200, 200, "bf16", 0.0, 4), (96, 130, "f16", 0.0, 3)):
+        A, SA, a = operand(rng, rows, K, fa, spread=2)
+        Bs = [operand(rng, N, K, fb, spread=2) for _ in n]
+        B = torch.stack([v.view(torch.uint8) for v, _, _ in Bs]).view(dtype(fb))
+        buf, D = rows_of(rows, N, out, fill=0x11)
+        c = rng.standard_normal((rows, N))
+        if beta:
+            D.copy_(torch.from_numpy(c))
+        before = buf.clone()
+        c = D.double().cpu().numpy()
+        assert plan.run_grouped(A, SA, B, torch.stack([s for _, s, _ in Bs]), D, torch.from_numpy(starts).cuda(), torch.from_numpy(n).cuda(),
+                                alpha=2.0 ** -6, beta=beta, act=act) == 0
+        none = np.ones(rows, bool)
+        for e, (s, m) in enumerate(zip(starts, n)):
+            none[s:s + m] = False
+            if m:
+                want, off = expect(a[s:s + m], Bs[e][2], 2.0 ** -6, beta, c[s:s + m], act)
+                near(D[s:s + m], want, off, out)
+        none = torch.from_numpy(none).cuda()
+        assert torch.equal(buf.view(torch.uint8).view(rows, -1)[none], before.view(torch.uint8).view(rows, -1)[none])
     assert plan.poll_error() == 0
 
 
