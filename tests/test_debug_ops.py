@@ -42,3 +42,8 @@ def test_skipped_and_reported():
 
 def test_inputs_skipped_and_reported():
     assert _run(["-m", "tests.debug_inputs"], GEMM_DEBUG_SHRINK_INPUT="4").strip().startswith("ok")
+
+
+def test_edges_pass_under_the_checks():
+    _run(["-m", "pytest", "-q", "-x", "-p", "no:cacheprovider", "-m", "gpu", "tests/test_scaled_gpu.py", "tests/test_experts_gpu.py",
+          "-k", "copied or square or meet or share or between or in_place"])
