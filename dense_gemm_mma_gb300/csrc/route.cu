@@ -11,8 +11,8 @@
 // lane in registers, sorted by order-preserving integer keys.  A choice is then one warp
 // maximum over the lanes' first keys: the lowest lane that has it holds the lowest expert that has it, and
 // moves on to its next.  Scores are worked out only where something needs them.
-// Measured, softmax, 16384 tokens, 8 of 128 experts: choice and weights 8.1 us, gradient 8.3 us (519 and 425
-// instructions a token); 16 tokens, sigmoid, 8 of 256 experts in groups: 4.1 us.
+// Measured, softmax, 16384 tokens, 8 of 128 experts: choice and weights 8.2 us, renormalised 9.0 (460 and 519 instructions a
+// token), gradient 8.3 and 8.6 us (370 and 430); 16 tokens, sigmoid, 8 of 256 experts in groups: 4.1 us.
 // Sums and products that make a key are written with the rounding intrinsics, so that no
 // compiler contraction moves it by a bit: the choice depends on it.
 #include <cuda_bf16.h>
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(128) route_backward_kernel(const RouteArgs a) 
   if (!a.sigmoid) {
     // (also where weights are renormalised and `through` is 0: a branch round it took two registers more than
     // the 32 with which 16 CTAs share an SM)
-    const float by = scorer.sum > 0.f ? through / scorer.sum : 0.f;
+    const float by = scorer.sum > 0.f ? 1.f / scorer.sum * through : 0.f;
     if (fabsf(scorer.top) < -kNegInf) {
 #pragma unroll
       for (int i = 0; i < P; ++i) dx[i] -= expf(x[i] - scorer.top) * by;
