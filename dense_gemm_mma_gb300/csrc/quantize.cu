@@ -9,9 +9,9 @@
 // logarithm.  Multiplying by 2^-e is exact, so a code is one rounding (to nearest, ties to even)
 // away from its value.  Infinities and NaN take no part in m and become NaN.
 //
-// What bounds it is memory: each value is read once, and written once per
-// orientation.  Maxima are taken on the magnitudes' bits (ordered like the numbers),
-// one warp reduction per row and block.  8192 x 4096 bf16: one orientation 19.5 us (5.2 TB/s), both 30.0
+// Each value is read once, and written once per orientation; what bounds it is latency and issue more than memory.
+// Maxima are taken on the magnitudes' bits (ordered like the numbers),
+// one warp reduction per row and block.  8192 x 4096 bf16: one orientation 19.5 us (5.2 TB/s), both 29.7
 // us (4.5 TB/s; the columns' scales need the whole tile before the first transposed code).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

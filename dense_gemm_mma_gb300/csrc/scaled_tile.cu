@@ -23,9 +23,9 @@
 // a tile first and only then lets the next tile's MMAs begin.
 //
 // What bounds it: 8192^3 into bf16 330 to 360 us, 3.1 to 3.3 PFLOP/s, at the power limit (287 us, 3.8
-// PFLOP/s, with operands whose bits change little).  Short K: what goes through L2.  16 weight gradients of 2048 x 2048 over
-// 1,024 rows each read 537 MB of tiles and write 268 MB in 76 us, and take 61 if nothing is written; a load
-// takes 4,000 to 5,000 cycles while the tile before is written, of which the ring covers 2,600.
+// PFLOP/s, with operands whose bits change little).  Short K: the turnover of the tiles, with no unit full.  16 weight
+// gradients of 2048 x 2048 over 1,024 rows each (8 k-blocks a tile) read 537 MB of tiles and write 268 MB in 76 us, and take 61 if
+// nothing is written; a load takes 4,000 to 5,000 cycles while the tile before is written, of which the ring covers 2,600.
 #include <type_traits>
 
 #include "scaled.cuh"

@@ -432,7 +432,8 @@ def _operand(t, trans: bool):
 
 
 class Plan:
-    """Owns a gemm_plan_t on one device."""
+    """Owns a gemm_plan_t on one device.  The calls take tensors of that device whose rows (and, in a stack, matrices)
+    each have their own memory, in the order of their indices; others raise ValueError."""
 
     def __init__(self, device: int = 0):
         self.handle = gemm_plan_create(device)
