@@ -39,11 +39,18 @@ SOURCES = [
     "ops.cpp",
     "scaled_tile.cu",
     "scaled_sliced.cu",
+    "mx4_tile.cu",
+    "mx4_sliced.cu",
     "quantize.cu",
+    "quantize_mx4.cu",
     "route.cu",
+    "balance.cu",
     "combine.cu",
+    "norm.cu",
+    "norm_ops.cpp",
 ]
-HEADERS = ["ptx.cuh", "kernels.h", "plan.h", "gemm_tc.cuh", "scaled.cuh"]
+HEADERS = ["ptx.cuh", "kernels.h", "plan.h", "gemm_tc.cuh", "scaled.cuh",
+           "scaled_tile.cuh", "scaled_sliced.cuh", "codes.cuh", "route.cuh", "ops.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

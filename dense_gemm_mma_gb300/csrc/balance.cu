@@ -1,0 +1,270 @@
+// balance.cu -- how evenly a router's choice spreads the tokens, and the gradient of the loss that keeps it even.
+//
+// With p[t, e] token t's share of expert e (softmax of its logits, or its sigmoids over their sum), over the m
+// tokens that have a choice, n choices in all, c[e] of them expert e's:
+//
+//   P[e] = sum over t of p[t, e] / m      loss = scale E sum over e of (c[e] / n) P[e]
+//   factor[e] = d loss / d p[t, e] = scale E c[e] / (n m)
+//   d loss / d x[t, i] = p[t, i] (factor[i] - sum over e of factor[e] p[t, e]), for sigmoids times 1 - s[t, i]
+//
+// What bounds it is reading the logits once, for few tokens latency.  One warp a token, a run of experts a lane, as
+// in the router (route.cuh): lanes keep the sums of their experts' shares from token to token, warps add theirs up
+// in shared memory in a fixed order, CTAs through plan workspace, where the last one to arrive adds them in the
+// order of their indices; counts are whole numbers, which may meet in any order.  The same bits every time.
+#include <algorithm>
+
+#include "route.cuh"
+
+namespace dg {
+namespace {
+
+constexpr int kBuffers = 4;  // warps that add to the CTA's sums at a time
+
+// Warps of a CTA of the sums: with 16 or 32 experts a lane as many as there are registers for.
+template <int P>
+__host__ __device__ constexpr int balance_warps() {
+  return P <= 8 ? 32 : 16;
+}
+
+// Does the token have a choice?  A lane's own is `expert`, -1 for none.
+__device__ __forceinline__ bool has_choice(const BalanceArgs& a, int t, int lane, int* expert) {
+  *expert = -1;
+  if (lane < a.top_k) {
+    const int* const at = a.indices + int64_t(t) * a.top_k + lane;
+    const int e = DG_IN(a.dbg, at, 4, DBG_ROUTE) ? __ldg(at) : -1;
+    if (e >= 0 && e < a.experts) *expert = e;
+  }
+  return __any_sync(kAll, *expert >= 0);
+}
+
+// A lane's experts' shares of a token, from its logits.  One whose scores are all 0 gives none.
+template <int P>
+__device__ __forceinline__ void token_shares(const BalanceArgs& a, const float (&x)[P], float lane_top, float (&p)[P]) {
+  const Scorer scorer(a, x, number_key(lane_top));
+  float sum = scorer.sum;
+  if (a.sigmoid) {
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      p[i] = scorer.score(x[i]);
+      sum += p[i];
+    }
+    sum = warp_sum(sum);
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = scorer.power(x[i]);
+  }
+  const float by = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < P; ++i) p[i] *= by;
+}
+
+__device__ __forceinline__ float block_sum(float v, float* sums) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int i = 0; i < int(blockDim.x >> 5); ++i) v += sums[i];
+  return v;
+}
+
+template <int P>
+__global__ void __launch_bounds__(32 * balance_warps<P>(), 1) balance_kernel(const BalanceArgs a) {
+  constexpr int W = balance_warps<P>(), E = 32 * P;
+  __shared__ float total[kBuffers][E];
+  __shared__ int count[E];
+  __shared__ int tokens;
+  __shared__ float sums[W];
+  __shared__ unsigned ticket;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int run = (a.experts + 31) / 32, first = lane * run;
+  for (int e = threadIdx.x; e < E; e += 32 * W) {
+    count[e] = 0;
+#pragma unroll
+    for (int b = 0; b < kBuffers; ++b) total[b][e] = 0.f;
+  }
+  if (threadIdx.x == 0) tokens = 0;
+  __syncthreads();
+  wait_prior_grid();
+  float acc[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) acc[i] = 0.f;
+  int mine = 0;
+  for (int64_t t64 = int64_t(blockIdx.x) * W + warp; t64 < a.tokens; t64 += int64_t(gridDim.x) * W) {
+    const int t = int(t64);
+    float x[P], p[P];
+    load_logits(a, t, first, run, a.wide, x);
+    int expert;
+    const bool live = has_choice(a, t, lane, &expert);
+    if (expert >= 0) atomicAdd(count + expert, 1);
+    float top = kNegInf;
+#pragma unroll
+    for (int i = 0; i < P; ++i) top = fmaxf(top, x[i]);
+    token_shares(a, x, top, p);
+    if (!live) continue;
+    ++mine;
+#pragma unroll
+    for (int i = 0; i < P; ++i) acc[i] += p[i];
+  }
+  if (lane == 0 && mine) atomicAdd(&tokens, mine);
+  for (int w = 0; w < W; w += kBuffers) {  // expert first + i of lane `lane`
+    if (warp / kBuffers == w / kBuffers)
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (i < run) total[warp % kBuffers][first + i] += acc[i];
+    __syncthreads();
+  }
+  auto cta_sum = [&](int e) { return (total[0][e] + total[1][e]) + (total[2][e] + total[3][e]); };
+  const bool alone = gridDim.x == 1;
+  if (!alone) {
+    float* const part = a.parts + int64_t(blockIdx.x) * a.experts;
+    for (int e = threadIdx.x; e < a.experts; e += 32 * W) {
+      if (DG_IN(a.dbg, part + e, 4, DBG_ROUTE)) part[e] = cta_sum(e);
+      if (count[e] && DG_IN(a.dbg, a.counters + 2 + e, 4, DBG_ROUTE)) atomicAdd(a.counters + 2 + e, unsigned(count[e]));
+    }
+    if (threadIdx.x == 0 && DG_IN(a.dbg, a.counters + 1, 4, DBG_ROUTE)) atomicAdd(a.counters + 1, unsigned(tokens));
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) ticket = DG_IN(a.dbg, a.counters, 4, DBG_ROUTE) ? atomicAdd(a.counters, 1u) : 0u;
+    __syncthreads();
+    if (ticket != gridDim.x - 1) return;
+    __threadfence();
+    // the parts, four experts a thread, every `lots`th CTA's to a lot; the lots in their order
+    for (int e = threadIdx.x; e < E; e += 32 * W)
+#pragma unroll
+      for (int b = 0; b < kBuffers; ++b) total[b][e] = 0.f;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBuffers * a.experts; i += 32 * W) {
+      const int e = i % a.experts, lot = i / a.experts;
+      float s = 0.f;
+#pragma unroll 8
+      for (int c = lot; c < int(gridDim.x); c += kBuffers) {
+        const float* const at = a.parts + int64_t(c) * a.experts + e;
+        s += DG_IN(a.dbg, at, 4, DBG_ROUTE) ? __ldcg(at) : 0.f;
+      }
+      total[lot][e] = s;
+    }
+    for (int e = threadIdx.x; e < a.experts; e += 32 * W) {
+      if (!DG_IN(a.dbg, a.counters + 2 + e, 4, DBG_ROUTE)) continue;
+      count[e] = int(__ldcg(a.counters + 2 + e));
+      a.counters[2 + e] = 0u;
+    }
+    if (threadIdx.x == 0) {
+      tokens = int(__ldcg(a.counters + 1));
+      a.counters[0] = a.counters[1] = 0u;
+    }
+  }
+  __syncthreads();
+  // n: whole numbers below 2^31
+  int n = 0;
+  for (int e = threadIdx.x; e < a.experts; e += 32 * W) n += count[e];
+  n = __reduce_add_sync(kAll, n);
+  __shared__ int ns[W];
+  if (lane == 0) ns[warp] = n;
+  __syncthreads();
+  n = 0;
+  for (int w = 0; w < W; ++w) n += ns[w];
+  const float m = float(max(tokens, 1)), all = float(max(n, 1)), by = a.scale * float(a.experts);
+  float loss = 0.f;
+  for (int e = threadIdx.x; e < a.experts; e += 32 * W) {
+    const float share = cta_sum(e) / m, part = by * (float(count[e]) / all);
+    loss += part * share;
+    if (DG_IN(a.dbg, a.counts + e, 4, DBG_ROUTE)) a.counts[e] = count[e];
+    if (DG_IN(a.dbg, a.shares + e, 4, DBG_ROUTE)) a.shares[e] = share;
+    if (DG_IN(a.dbg, a.factor + e, 4, DBG_ROUTE)) a.factor[e] = part / m;
+  }
+  loss = block_sum(loss, sums);
+  if (threadIdx.x == 0 && DG_IN(a.dbg, a.loss, 4, DBG_ROUTE)) *a.loss = loss;
+}
+
+// The difference factor[i] - sum of factor[e] p[e] is taken from the factor of the token's surest expert on, whose
+// own term is then exactly 0: a nearly sure token keeps the digits of its small gradient.
+template <int P>
+__global__ void __launch_bounds__(128) balance_backward_kernel(const BalanceArgs a) {
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const int t = int(blockIdx.x * 4 + (threadIdx.x >> 5));
+  if (t >= a.tokens) return;
+  const int run = (a.experts + 31) / 32, first = lane * run;
+  float x[P], p[P], f[P], old[P];
+  load_logits(a, t, first, run, a.wide, x);
+  int expert;
+  const bool live = has_choice(a, t, lane, &expert);
+  const float dloss = a.dloss == nullptr ? 1.f : DG_IN(a.dbg, a.dloss, 4, DBG_ROUTE) ? __ldg(a.dloss) : 0.f;
+  const int es = a.kind == OUT_F32 ? 4 : 2;
+  char* const dst = static_cast<char*>(a.dlogits) + (int64_t(t) * a.lddl + first) * es;
+  const bool whole = P >= 4 && a.wide_out && run == P && first + P <= a.experts;
+  auto have = [&](int i) { return i < run && first + i < a.experts; };
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    f[i] = have(i) && DG_IN(a.dbg, a.factor + first + i, 4, DBG_ROUTE) ? __ldg(a.factor + first + i) : 0.f;
+    old[i] = 0.f;
+    if (a.accumulate && have(i) && DG_IN(a.dbg, dst + i * es, es, DBG_ROUTE))
+      old[i] = es == 4 ? *reinterpret_cast<const float*>(dst + 4 * i)
+                       : half_at(*reinterpret_cast<const uint16_t*>(dst + 2 * i), 0, a.kind);
+  }
+  float top = kNegInf, reference = 0.f;
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (x[i] > top) top = x[i], reference = f[i];
+  token_shares(a, x, top, p);
+  const uint32_t key = number_key(top), best = __reduce_max_sync(kAll, key);
+  reference = __shfl_sync(kAll, reference, __ffs(__ballot_sync(kAll, key == best)) - 1);
+  float dot = 0.f;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    f[i] -= reference;
+    dot = fmaf(f[i], p[i], dot);
+  }
+  dot = warp_sum(dot);
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    float d = p[i] * (f[i] - dot);
+    if (a.sigmoid) d = x[i] == kNegInf ? 0.f : __fdiv_rn(d, __fadd_rn(1.f, expf(x[i])));
+    x[i] = live ? fmaf(dloss, d, old[i]) : old[i];
+  }
+  if constexpr (P >= 4) {
+    if (whole) {
+      if (!DG_IN(a.dbg, dst, P * es, DBG_ROUTE)) return;
+#pragma unroll
+      for (int i = 0; i < P; i += 4) {
+        if (a.kind == OUT_F32)
+          *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        else
+          *reinterpret_cast<uint2*>(dst + 2 * i) = make_uint2(half_pair(x[i], x[i + 1], a.kind), half_pair(x[i + 2], x[i + 3], a.kind));
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    if (!have(i) || !DG_IN(a.dbg, dst + i * es, es, DBG_ROUTE)) continue;
+    if (es == 4)
+      *reinterpret_cast<float*>(dst + 4 * i) = x[i];
+    else
+      *reinterpret_cast<uint16_t*>(dst + 2 * i) = uint16_t(half_pair(x[i], 0.f, a.kind));
+  }
+}
+
+}  // namespace
+
+// CTAs of the sums: one warp a token until every SM has a CTA.
+int balance_ctas(int64_t tokens, int64_t experts, int sms) {
+  const int64_t warps = experts <= 256 ? 32 : 16;
+  return int(std::max<int64_t>(1, std::min<int64_t>(sms, (tokens + warps - 1) / warps)));
+}
+
+cudaError_t launch_balance(const BalanceArgs& a, int ctas, cudaStream_t s) {
+  return by_experts(a.experts, [&](auto p) {
+    constexpr int P = decltype(p)::value;
+    return launch_k(balance_kernel<P>, dim3(unsigned(ctas)), dim3(32 * balance_warps<P>()), 0, s, a.pdl, a);
+  });
+}
+
+cudaError_t launch_balance_backward(const BalanceArgs& a, cudaStream_t s) {
+  return by_experts(a.experts, [&](auto p) {
+    return launch_k(balance_backward_kernel<decltype(p)::value>, dim3(unsigned((a.tokens + 3) / 4)), dim3(128), 0, s, a.pdl, a);
+  });
+}
+
+}  // namespace dg

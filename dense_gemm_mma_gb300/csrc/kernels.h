@@ -38,7 +38,8 @@ enum DbgSite : int {
   DBG_SCALED = 8,     // 8-bit products: plain loads and stores of D
   DBG_QUANTIZE = 9,   // the quantiser
   DBG_ROUTE = 10,     // routing, its map and its gradient
-  DBG_COMBINE = 11    // the weighted sum of rows and its gradients
+  DBG_COMBINE = 11,   // the weighted sum of rows and its gradients
+  DBG_NORM = 12       // the norm and its gradients
 };
 constexpr int DBG_SITE_SHIFT = 16;
 constexpr int DBG_FLAG = 1 << 30;
@@ -373,6 +374,15 @@ cudaError_t launch_scaled_sliced(const ScMaps& m, const ScParams& p, int grid, c
 int scaled_sliced_smem(int bn, int stages, int part_rows);
 int scaled_sliced_clusters(int slices);  // clusters of that many CTAs that can be resident at once, a CTA an SM
 
+// The same for 4-bit operands (E2M1, scales of blocks of 32): maps a and b of bytes, two values each; sa and sb
+// with a row block's scale tiles as their second coordinate and the row block as their third (box two tiles).
+cudaError_t launch_mx4_tile(bool pair, const ScMaps& m, const ScParams& p, int grid, cudaStream_t s);
+int mx4_tile_clusters();
+int mx4_tile_stages(bool pair);
+cudaError_t launch_mx4_sliced(const ScMaps& m, const ScParams& p, int grid, cudaStream_t s);
+int mx4_sliced_smem(int bn, int stages, int part_rows);
+int mx4_sliced_clusters(int slices);
+
 // Rows of `cols` bytes (groups x rows of them, `ld` bytes apart, groups `group` bytes apart) copied
 // to rows of `ld_out` bytes, a multiple of 16: makes a code matrix whose rows the TMA cannot address one
 // that it can.  With counts, groups that have none are left out.
@@ -409,6 +419,85 @@ struct QuantArgs {
 };
 cudaError_t launch_quantize(const QuantArgs& a, cudaStream_t s);
 
+// The same into 4 bits (E2M1, a scale for each row and block of 32): cols values are (cols + 1) / 2 bytes;
+// block_rows, e5m2, rows_padded and cols_padded are not used, q_groups and qt_groups count blocks in fours as above.
+cudaError_t launch_quantize_mx4(const QuantArgs& a, cudaStream_t s);
+
+enum CodeKind : int { CODE_E4M3 = 0, CODE_E5M2 = 1, CODE_E2M1 = 2 };
+
+// Values of a block-scaled matrix.
+struct DequantArgs {
+  const uint8_t* q;
+  int64_t ldq;
+  const uint8_t* sq;
+  int code;      // CodeKind
+  int rows, cols;
+  int groups;    // groups of four blocks along a row
+  void* x;
+  int64_t ldx;
+  int x_kind;
+  int wide;      // rows of X on 16-byte boundaries
+  int pdl;
+  DG_DEBUG_FIELD
+};
+cudaError_t launch_dequantize(const DequantArgs& a, cudaStream_t s);
+
+// -------------------------------------------------------------------- norm
+
+constexpr int NORM_MAX_COLS = 32768;  // a row stays in the registers of a CTA
+
+struct NormArgs {
+  int rows, cols;
+  const void* x;
+  int64_t ldx;
+  int x_kind;       // OutKind of x and y
+  const void* r;    // the residual, or null
+  int64_t ldr;
+  int h_kind;       // OutKind of r and h
+  const void* gain; // or null: ones
+  int g_kind;
+  float eps;
+  void* h;          // x + r, or null
+  int64_t ldh;
+  void* y;          // or null
+  int64_t ldy;
+  uint8_t *q, *sq;  // or null
+  int64_t ldq;
+  int e5m2, q_groups, rows_padded;
+  float* rstd;      // or null
+  int wide;         // rows and gain on 16-byte boundaries
+  int warps, per;   // warps of a row, rows of a CTA (set by the launcher)
+  int pdl;
+  DG_DEBUG_FIELD
+};
+cudaError_t launch_norm(NormArgs a, cudaStream_t s);
+
+struct NormBackArgs {
+  int rows, cols;
+  const void* dy;
+  int64_t lddy;
+  int x_kind;       // OutKind of dy
+  const void* h;
+  int64_t ldh;
+  int h_kind;       // OutKind of h, dh and dx
+  const void* gain;
+  int g_kind;
+  const float* rstd;
+  const void* dh;   // gradient that reaches h past the norm, or null
+  int64_t lddh;
+  void* dx;
+  int64_t lddx;
+  float* dgain;     // or null
+  float* parts;     // norm_backward_workspace bytes: rows' partial sums of dgain, part_cols floats each
+  int part_cols;
+  int wide;
+  int warps, per;
+  int pdl;
+  DG_DEBUG_FIELD
+};
+size_t norm_backward_workspace(int64_t rows, int64_t cols, int sms);
+cudaError_t launch_norm_backward(NormBackArgs a, int sms, cudaStream_t s);
+
 // ----------------------------------------------------------------- routing
 
 struct RouteArgs {
@@ -433,6 +522,22 @@ constexpr int ROUTE_MAX_EXPERTS = 1024;
 constexpr int ROUTE_MAX_K = 32;
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t s);
+
+// Balance of a router: tokens, experts, logits, ldl, kind, sigmoid, top_k, scale, indices, wide and pdl as in
+// RouteArgs; for the gradient also dlogits, lddl, wide_out.
+struct BalanceArgs : RouteArgs {
+  int* counts;       // experts
+  float* shares;     // experts
+  float* factor;     // experts
+  float* loss;       // one
+  float* parts;      // several CTAs: balance_workspace bytes, [CTA][experts]
+  unsigned* counters;  // several CTAs: experts + 2 words, zero on entry and left zero
+  const float* dloss;  // gradient: null for 1
+  int accumulate;      // gradient: added to what dlogits holds
+};
+int balance_ctas(int64_t tokens, int64_t experts, int sms);
+cudaError_t launch_balance(const BalanceArgs& a, int ctas, cudaStream_t s);
+cudaError_t launch_balance_backward(const BalanceArgs& a, cudaStream_t s);
 
 struct RouteMapArgs {
   const int* indices;

@@ -1,0 +1,432 @@
+// norm.cu -- root-mean-square norm of a residual stream, and its gradients:
+//
+//   h = x + r      rho = 1 / sqrt(mean(h^2) + eps)      y = h rho gain
+//   g = dy gain    xhat = h rho     dx = rho (g - xhat mean(g xhat)) + dh     dgain = sum over rows of dy xhat
+//
+// y leaves in the input's type and / or as 8-bit codes with one power-of-two scale for each block of 128 (the
+// quantiser's rule, quantize.cu), so that a product's operand needs no pass of its own.  What bounds it is
+// memory: x, r, dy and dh are read once, h, y (or codes) and dx written once.
+//
+// A row stays in registers between its sum of squares and its scaling.  A warp takes 512 columns
+// (four blocks of scales, one word of them) at a time, a lane twice eight neighbouring ones: half a warp holds a
+// block, whose largest magnitude is four exchanges away.  The row's sum meets in shared memory, one barrier a row.
+// Sums, rho and the normalised values are fp32; y and the codes come from the unrounded sum h, one rounding each
+// (the kept h is rounded on its own way out), and the gradients from the kept h, which is what the
+// caller still has.  The gain's gradient is summed row after row in registers, then over the CTAs in the order
+// of their indices by a second launch: the same bits every time, no atomics.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "codes.cuh"
+#include "kernels.h"
+
+namespace dg {
+namespace {
+
+template <typename T>
+__host__ __device__ constexpr int kind_of() {
+  return sizeof(T) == 4 ? OUT_F32 : std::is_same<T, __half>::value ? OUT_F16 : OUT_BF16;
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else if constexpr (std::is_same<T, __half>::value) return __half2float(v);
+  else return __bfloat162float(v);
+}
+template <typename T>
+__device__ __forceinline__ T from_f(float v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else if constexpr (std::is_same<T, __half>::value) return __float2half_rn(v);
+  else return __float2bfloat16_rn(v);
+}
+
+// Eight neighbouring values of a row as they are loaded; what is not there is zero.
+template <typename T>
+struct Eight {
+  static constexpr int WORDS = int(sizeof(T)) * 2;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else if constexpr (std::is_same<T, __half>::value) {
+      const uint16_t h = uint16_t(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+      return __half2float(*reinterpret_cast<const __half*>(&h));
+    } else {
+      return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+  }
+  __device__ __forceinline__ void put(int i, T v) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(v);
+    } else {
+      const uint32_t b = *reinterpret_cast<const uint16_t*>(&v);
+      w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | b << 16 : (w[i / 2] & 0xffff0000u) | b;
+    }
+  }
+  // All eight by 16-byte loads.
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < WORDS / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+};
+
+// `left` columns from p to the end of the row (none: nothing is read).  WIDE: p is on a 16-byte boundary, so that eight
+// columns are loaded whole; the last few of a row one by one.
+template <bool WIDE, typename T, typename A>
+__device__ __forceinline__ void load8(const A& a, Eight<T>& o, const T* p, int left, int site) {
+  o.clear();
+  if (WIDE && left >= 8) {
+    if (DG_IN(a.dbg, p, 8 * int(sizeof(T)), site)) o.load(p);
+  } else if (left > 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left && DG_IN(a.dbg, p + i, int(sizeof(T)), site)) o.put(i, p[i]);
+  }
+}
+
+template <bool WIDE, typename T, typename A>
+__device__ __forceinline__ void store8(const A& a, T* p, const float (&v)[8], int left, int site) {
+  if (WIDE && left >= 8) {
+    Eight<T> o;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o.w[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<T, __half>::value) {
+          const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+          o.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+          o.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+    }
+    if (!DG_IN(a.dbg, p, 8 * int(sizeof(T)), site)) return;
+#pragma unroll
+    for (int i = 0; i < Eight<T>::WORDS / 4; ++i)
+      reinterpret_cast<uint4*>(p)[i] = make_uint4(o.w[4 * i], o.w[4 * i + 1], o.w[4 * i + 2], o.w[4 * i + 3]);
+  } else if (left > 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left && DG_IN(a.dbg, p + i, int(sizeof(T)), site)) p[i] = from_f<T>(v[i]);
+  }
+}
+
+// Eight values of the gain (none: ones), which is of the input's type or fp32.
+template <bool WIDE, typename T, typename A>
+__device__ __forceinline__ void load_gain(const A& a, float (&g)[8], int col, int left) {
+  if (a.gain == nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = 1.f;
+  } else if (a.g_kind == kind_of<T>()) {
+    Eight<T> o;
+    load8<WIDE>(a, o, static_cast<const T*>(a.gain) + col, left, DBG_NORM);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = o.at(i);
+  } else {
+    Eight<float> o;
+    load8<WIDE>(a, o, static_cast<const float*>(a.gain) + col, left, DBG_NORM);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = o.at(i);
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+
+// The sum over a row's warps, [first, first + warps) of the CTA's; every thread of the CTA calls it.
+__device__ __forceinline__ float row_sum(float v, float* sums, int first, int warps) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int i = 0; i < warps; ++i) v += sums[first + i];
+  return v;
+}
+
+// Codes of eight values and the scale byte of the block of 128 that they share with the other lanes of half a warp.
+template <bool E5M2>
+__device__ __forceinline__ uint2 block_codes(const float (&y)[8], uint32_t* byte) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(kAll, m, d));
+  const bool careful = __any_sync(kAll, m >= kInf);
+  if (careful) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, finite_bits(y[i]));
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(kAll, m, d));
+  }
+  *byte = scale_byte<E5M2>(m);
+  const float inv = inverse_scale(*byte);
+  if (careful)
+    return make_uint2(codes4<E5M2, true>(y[0], y[1], y[2], y[3], inv), codes4<E5M2, true>(y[4], y[5], y[6], y[7], inv));
+  return make_uint2(codes4<E5M2, false>(y[0], y[1], y[2], y[3], inv), codes4<E5M2, false>(y[4], y[5], y[6], y[7], inv));
+}
+
+// A CTA takes a.per rows, a.warps warps to a row, G groups of 512 columns to a warp.
+template <typename TX, typename TH, int G, bool WIDE>
+__global__ void __launch_bounds__(512) norm_kernel(const NormArgs a) {
+  __shared__ float sums[16];
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int slot = warp / a.warps, mine = warp - slot * a.warps;
+  const int row = int(blockIdx.x) * a.per + slot;  // past the matrix: only scale bytes, zero
+  const bool live = row < a.rows;
+  const TX* const x = static_cast<const TX*>(a.x) + int64_t(row) * a.ldx;
+  const TH* const r = a.r ? static_cast<const TH*>(a.r) + int64_t(row) * a.ldr : nullptr;
+  Eight<TX> xv[2 * G];
+  Eight<TH> rv[2 * G];
+  float v[2 * G][8], gain[G < 4 ? 2 * G : 1][8];
+#pragma unroll
+  for (int i = 0; i < 2 * G; ++i) {
+    const int col = (mine + i / 2 * a.warps) * 512 + (i & 1) * 256 + lane * 8;
+    const int left = live ? a.cols - col : 0;
+    load8<WIDE>(a, xv[i], x + col, left, DBG_NORM);
+    if (r)
+      load8<WIDE>(a, rv[i], r + col, left, DBG_NORM);
+    else
+      rv[i].clear();
+  }
+  const bool scaled = a.y || a.q;
+  if constexpr (G < 4) {  // (four groups of it leave no registers for the rest)
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) {
+      const int col = (mine + i / 2 * a.warps) * 512 + (i & 1) * 256 + lane * 8;
+      load_gain<WIDE, TX>(a, gain[i], col, live && scaled ? a.cols - col : 0);
+    }
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[i][j] = xv[i].at(j) + rv[i].at(j);
+      sum = fmaf(v[i][j], v[i][j], sum);
+    }
+  sum = row_sum(sum, sums, slot * a.warps, a.warps);
+  const float rho = __frsqrt_rn(__fdiv_rn(sum, float(a.cols)) + a.eps);
+  if (live && a.rstd && mine == 0 && lane == 0 && DG_IN(a.dbg, a.rstd + row, 4, DBG_NORM)) a.rstd[row] = rho;
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 2 * G; ++i) {
+    const int group = mine + i / 2 * a.warps;
+    const int col = group * 512 + (i & 1) * 256 + lane * 8;
+    const int left = live ? a.cols - col : 0;
+    if (a.h) store8<WIDE>(a, static_cast<TH*>(a.h) + int64_t(row) * a.ldh + col, v[i], left, DBG_NORM);
+    if (!scaled) continue;
+    if constexpr (G == 4) load_gain<WIDE, TX>(a, gain[0], col, left);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rho * gain[G < 4 ? i : 0][j];
+    if (a.y) store8<WIDE>(a, static_cast<TX*>(a.y) + int64_t(row) * a.ldy + col, v[i], left, DBG_NORM);
+    if (a.q) {
+      // (a row past the matrix is zero throughout, unless rho is infinite)
+      if (left < 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j >= left) v[i][j] = 0.f;
+      }
+      uint32_t byte;
+      const uint2 c = a.e5m2 ? block_codes<true>(v[i], &byte) : block_codes<false>(v[i], &byte);
+      uint8_t* const dst = a.q + int64_t(row) * a.ldq + col;
+      if (left >= 8) {
+        if (DG_IN(a.dbg, dst, 8, DBG_NORM)) *reinterpret_cast<uint2*>(dst) = c;
+      } else if (left > 0 && DG_IN(a.dbg, dst, left, DBG_NORM)) {
+        for (int j = 0; j < left; ++j) dst[j] = uint8_t((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
+      }
+      // bytes of blocks 2 (i & 1) and 2 (i & 1) + 1 of the group, in lanes 0 and 16
+      const uint32_t other = __shfl_down_sync(kAll, byte, 16);
+      word = (i & 1 ? word : 0u) | (byte | other << 8) << (16 * (i & 1));
+      if ((i & 1) && lane == 0 && group < a.q_groups && row < a.rows_padded) {
+        uint8_t* const s = a.sq + scale_at(row, int64_t(group) * 4, a.q_groups);
+        if (DG_IN(a.dbg, s, 4, DBG_NORM)) *reinterpret_cast<uint32_t*>(s) = word;
+      }
+    }
+  }
+}
+
+template <typename TX, typename TH, int G, bool WIDE>
+__global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a) {
+  __shared__ float sums[2][16];
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int slot = warp / a.warps, mine = warp - slot * a.warps;
+  float gain[2 * G][8], acc[2 * G][8];
+#pragma unroll
+  for (int i = 0; i < 2 * G; ++i) {
+    const int col = (mine + i / 2 * a.warps) * 512 + (i & 1) * 256 + lane * 8;
+    load_gain<WIDE, TX>(a, gain[i], col, a.cols - col);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  }
+  const int step = int(gridDim.x) * a.per;
+  int turn = 0;
+  for (int64_t row0 = int64_t(blockIdx.x) * a.per; row0 < a.rows; row0 += step, turn ^= 1) {
+    const int64_t row = row0 + slot;
+    const bool live = row < a.rows;
+    Eight<TX> dy[2 * G];
+    Eight<TH> h[2 * G], dh[2 * G];
+    float rho = 0.f;
+    if (live && DG_IN(a.dbg, a.rstd + row, 4, DBG_NORM)) rho = __ldg(a.rstd + row);
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) {
+      const int col = (mine + i / 2 * a.warps) * 512 + (i & 1) * 256 + lane * 8;
+      const int left = live ? a.cols - col : 0;
+      load8<WIDE>(a, dy[i], static_cast<const TX*>(a.dy) + row * a.lddy + col, left, DBG_NORM);
+      load8<WIDE>(a, h[i], static_cast<const TH*>(a.h) + row * a.ldh + col, left, DBG_NORM);
+      if (a.dh)
+        load8<WIDE>(a, dh[i], static_cast<const TH*>(a.dh) + row * a.lddh + col, left, DBG_NORM);
+      else
+        dh[i].clear();
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xhat = h[i].at(j) * rho, d = dy[i].at(j);
+        acc[i][j] = fmaf(d, xhat, acc[i][j]);
+        sum = fmaf(d * gain[i][j], xhat, sum);
+      }
+    sum = row_sum(sum, sums[turn], slot * a.warps, a.warps);
+    const float mean = __fdiv_rn(sum, float(a.cols));
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) {
+      const int col = (mine + i / 2 * a.warps) * 512 + (i & 1) * 256 + lane * 8;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = fmaf(rho, fmaf(-h[i].at(j) * rho, mean, dy[i].at(j) * gain[i][j]), dh[i].at(j));
+      store8<WIDE>(a, static_cast<TH*>(a.dx) + row * a.lddx + col, v, live ? a.cols - col : 0, DBG_NORM);
+    }
+  }
+  if (!a.parts) return;
+  float* const part = a.parts + (int64_t(blockIdx.x) * a.per + slot) * a.part_cols;
+#pragma unroll
+  for (int i = 0; i < 2 * G; ++i) {
+    const int col = (mine + i / 2 * a.warps) * 512 + (i & 1) * 256 + lane * 8;
+    if (col < a.part_cols) store8<true>(a, part + col, acc[i], 8, DBG_NORM);
+  }
+}
+
+// dgain[c] = sum over the parts, in their order: a warp's lane takes a column, its CTA's warps every 32nd part each, whose sums
+// are added in the warps' order.
+__global__ void __launch_bounds__(1024) norm_gain_kernel(const NormBackArgs a, int parts) {
+  __shared__ float sums[32][33];
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = int(blockIdx.x) * 32 + lane;
+  float s = 0.f;
+  if (col < a.cols)
+    for (int p = warp; p < parts; p += 32) {
+      const float* const at = a.parts + int64_t(p) * a.part_cols + col;
+      if (DG_IN(a.dbg, at, 4, DBG_NORM)) s += __ldcg(at);
+    }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp > 0 || col >= a.cols) return;
+  s = 0.f;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) s += sums[w][lane];
+  if (DG_IN(a.dbg, a.dgain + col, 4, DBG_NORM)) a.dgain[col] = s;
+}
+
+// Warps to a row and groups to a warp, for `cols` columns; rows to a CTA, so that it has four warps at least.
+struct Shape {
+  int g, warps, per;
+};
+Shape shape_of(int cols, int most_warps, int64_t rows) {
+  const int groups = (cols + 511) / 512;
+  Shape s;
+  s.g = groups <= most_warps ? 1 : groups <= 2 * most_warps ? 2 : 4;
+  s.warps = (groups + s.g - 1) / s.g;
+  s.per = int(std::max<int64_t>(1, std::min<int64_t>(4 / s.warps, rows)));
+  return s;
+}
+
+template <typename F>
+cudaError_t by_types(int x_kind, int h_kind, F f) {
+  if (x_kind == OUT_F32) return f(float{}, float{});
+  if (x_kind == OUT_BF16) return h_kind == OUT_F32 ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
+  return h_kind == OUT_F32 ? f(__half{}, float{}) : f(__half{}, __half{});
+}
+
+template <typename F>
+cudaError_t by_groups(int g, bool wide, F f) {
+  using std::integral_constant;
+  if (wide) {
+    if (g == 1) return f(integral_constant<int, 1>{}, std::true_type{});
+    if (g == 2) return f(integral_constant<int, 2>{}, std::true_type{});
+    return f(integral_constant<int, 4>{}, std::true_type{});
+  }
+  if (g == 1) return f(integral_constant<int, 1>{}, std::false_type{});
+  if (g == 2) return f(integral_constant<int, 2>{}, std::false_type{});
+  return f(integral_constant<int, 4>{}, std::false_type{});
+}
+
+}  // namespace
+
+cudaError_t launch_norm(NormArgs a, cudaStream_t s) {
+  const int64_t rows = a.q ? a.rows_padded : a.rows;
+  const Shape sh = shape_of(a.cols, 16, rows);
+  a.warps = sh.warps;
+  a.per = sh.per;
+  return by_types(a.x_kind, a.h_kind, [&](auto x, auto h) {
+    return by_groups(sh.g, a.wide != 0, [&](auto g, auto w) {
+      return launch_k(norm_kernel<decltype(x), decltype(h), decltype(g)::value, decltype(w)::value>,
+                      dim3(unsigned((rows + sh.per - 1) / sh.per)), dim3(unsigned(32 * sh.warps * sh.per)), 0, s, a.pdl, a);
+    });
+  });
+}
+
+// Rows' partial sums of the gain's gradient that the launch below makes.
+static int norm_parts(int64_t rows, int cols, int sms, int* grid) {
+  const Shape sh = shape_of(cols, 16, rows);
+  *grid = int(std::min<int64_t>((rows + sh.per - 1) / sh.per, int64_t(sms) * std::max(1, 16 / (sh.warps * sh.per))));
+  return *grid * sh.per;
+}
+
+size_t norm_backward_workspace(int64_t rows, int64_t cols, int sms) {
+  int grid;
+  return size_t(norm_parts(rows, int(cols), sms, &grid)) * size_t((cols + 7) / 8 * 8) * 4;
+}
+
+cudaError_t launch_norm_backward(NormBackArgs a, int sms, cudaStream_t s) {
+  int grid = 0;
+  const int parts = norm_parts(a.rows, a.cols, sms, &grid);
+  const Shape sh = shape_of(a.cols, 16, a.rows);
+  a.warps = sh.warps;
+  a.per = sh.per;
+  a.part_cols = (a.cols + 7) / 8 * 8;
+  if (!a.dgain) a.parts = nullptr;
+  if (a.rows > 0) {
+    const cudaError_t err = by_types(a.x_kind, a.h_kind, [&](auto x, auto h) {
+      return by_groups(sh.g, a.wide != 0, [&](auto g, auto w) {
+        return launch_k(norm_backward_kernel<decltype(x), decltype(h), decltype(g)::value, decltype(w)::value>,
+                        dim3(unsigned(grid)), dim3(unsigned(32 * sh.warps * sh.per)), 0, s, a.pdl, a);
+      });
+    });
+    if (err != cudaSuccess || !a.dgain) return err;
+  }
+  return launch_k(norm_gain_kernel, dim3(unsigned((a.cols + 31) / 32)), dim3(1024), 0, s, a.pdl, a, parts);
+}
+
+}  // namespace dg

@@ -1,89 +1,25 @@
-// ops.cpp -- the C ABI of the 8-bit block-scaled products, the quantiser, the routing
-// to experts and the weighted sum of their rows (include/gemm.h): argument checks,
+// ops.cpp -- the C ABI of the block-scaled products of 8 and 4 bits, the quantisers, the routing
+// to experts with its balance, and the weighted sum of their rows (include/gemm.h): argument checks,
 // the choice of kernel, tensor maps and launches.
 #include "gemm.h"
 
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
-#include <cstdarg>
 #include <cstdint>
-#include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <initializer_list>
 #include <utility>
 
-#include "plan.h"
+#include "ops.h"
 
 using namespace dg;
 
 namespace {
 
 constexpr int kSmemMax = 232448;  // shared memory of a CTA; an SM holds 1 KB more for each CTA
-
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
-
-bool is_float_type(gemm_type_t t) { return t == GEMM_TYPE_BF16 || t == GEMM_TYPE_F16 || t == GEMM_TYPE_F32; }
-bool is_code_type(gemm_type_t t) { return t == GEMM_TYPE_E4M3 || t == GEMM_TYPE_E5M2; }
-int64_t type_bytes(gemm_type_t t) { return t == GEMM_TYPE_F32 ? 4 : is_code_type(t) ? 1 : 2; }
-
-bool size_ok(int64_t n) { return n >= 0 && n <= kMaxDim; }
-
-// Scale tiles (512 bytes) of a rows x cols matrix.
-int64_t scale_groups(int64_t cols) { return std::max<int64_t>(1, ceil_div(cols, 512)); }
-int64_t scale_tiles(int64_t rows, int64_t cols) { return std::max<int64_t>(1, ceil_div(rows, 128)) * scale_groups(cols); }
-
-// Every launch of this file goes through here: errors of the launch become a status.
-gemm_status_t launched(cudaError_t e) {
-  if (e == cudaSuccess) return GEMM_OK;
-  cudaGetLastError();
-  return GEMM_ERR_CUDA;
-}
-
-const char* type_name(gemm_type_t t) {
-  static const char* kName[] = {"bf16", "f16", "f32", "tf32", "e4m3", "e5m2"};
-  return int(t) >= 0 && int(t) < 6 ? kName[int(t)] : "?";
-}
-
-// A call under GEMM_NVTX (a range named after it, closed on every return) and GEMM_LOG (one line when it
-// has succeeded).
-class CallScope {
- public:
-  CallScope(const gemm_plan* plan, const char* format, ...) __attribute__((format(printf, 3, 4)))
-      : log_(plan->log), nvtx_(plan->nvtx) {
-    if (!log_ && !nvtx_) return;
-    va_list args;
-    va_start(args, format);
-    std::vsnprintf(text_, sizeof text_, format, args);
-    va_end(args);
-    if (nvtx_) nvtxRangePushA(text_);
-  }
-  CallScope(const CallScope&) = delete;
-  CallScope& operator=(const CallScope&) = delete;
-  ~CallScope() {
-    if (nvtx_) nvtxRangePop();
-  }
-  gemm_status_t done(gemm_status_t st, const gemm_config_info_t* c = nullptr) const {
-    if (!log_ || st != GEMM_OK || (c && c->path == GEMM_PATH_NONE)) return st;
-    if (c)
-      std::fprintf(stderr,
-                   "gemm_log %s -> %s tile %dx%d cta/tile %d split %d stages %d grid %d sms %d tiles %lld launches %d "
-                   "workspace %lld B\n",
-                   text_, c->path == GEMM_PATH_SCALED_SLICED ? "scaled_sliced" : "scaled",
-                   c->tile_m, c->tile_n, c->cta_per_tile, c->splitk, c->stages, c->grid, c->sms, (long long)c->tiles, c->launches,
-                   (long long)c->workspace_bytes);
-    else
-      std::fprintf(stderr, "gemm_log %s\n", text_);
-    return st;
-  }
-
- private:
-  const bool log_, nvtx_;
-  char text_[160];
-};
 
 // 3-D row-major tensor (inner contiguous, ld elements between rows, group elements
 // between groups); boxes of box_inner x box_rows x 1.  Out-of-range reads give zero.
@@ -99,12 +35,10 @@ bool map3(CUtensorMap* m, CUtensorMapDataType t, int64_t esize, const void* ptr,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A run of n bytes.
-Region run_of(const void* p, int64_t n) { return region(p, p ? 1 : 0, n, 0, 1); }
-
 // A product as its callers give it.
 struct Product {
   const char* name = "gemm_run_scaled";
+  bool four = false;  // 4-bit operands (scales of blocks of 32), else 8-bit ones
   int group = SC_DENSE;
   int64_t groups = 1;
   int64_t M = 0, N = 0, K = 0;  // SC_ROWS: M = rows of A and D; SC_K: K = columns of A and B
@@ -124,6 +58,8 @@ struct Product {
   float alpha = 1.f, beta = 0.f;
   gemm_epilogue_t epi{};
   bool nothing() const { return M == 0 || N == 0 || groups == 0; }
+  int64_t k_bytes() const { return four ? ceil_div(K, 2) : K; }  // of a row of codes
+  int64_t tiles_of(int64_t rows) const { return four ? mx4_scale_tiles(rows, K) : scale_tiles(rows, K); }
 };
 
 // Do `groups` matrices, `group` elements from one to the next, share a byte with y?  What lies between
@@ -138,15 +74,16 @@ bool groups_meet(const void* p, int64_t groups, int64_t rows, int64_t cols, int6
 }
 
 gemm_status_t check_product(const Product& x) {
-  if (!is_code_type(x.a_type) || !is_code_type(x.b_type) || !is_float_type(x.d_type)) return GEMM_ERR_INVALID_ARG;
+  if (!x.four && (!is_code_type(x.a_type) || !is_code_type(x.b_type))) return GEMM_ERR_INVALID_ARG;
+  if (!is_float_type(x.d_type)) return GEMM_ERR_INVALID_ARG;
   if (x.epi.act < GEMM_ACT_NONE || x.epi.act > GEMM_ACT_SILU) return GEMM_ERR_INVALID_ARG;
   if (x.M < 0 || x.N < 0 || x.K < 0 || x.groups < 0) return GEMM_ERR_INVALID_ARG;
   if (!size_ok(x.M) || !size_ok(x.N) || !size_ok(x.K) || x.groups > SC_MAX_GROUPS) return GEMM_ERR_UNSUPPORTED;
-  const int64_t one = 1;
-  if (x.lda < std::max(one, x.K) || x.ldb < std::max(one, x.K) || x.ldd < std::max(one, x.N)) return GEMM_ERR_INVALID_ARG;
+  const int64_t one = 1, kb = x.k_bytes();
+  if (x.lda < std::max(one, kb) || x.ldb < std::max(one, kb) || x.ldd < std::max(one, x.N)) return GEMM_ERR_INVALID_ARG;
   if (x.nothing()) return GEMM_OK;
   const bool rows = x.group == SC_ROWS, by_k = x.group == SC_K;
-  if (rows && x.groups > 1 && x.b_group < (x.N - 1) * x.ldb + x.K) return GEMM_ERR_INVALID_ARG;
+  if (rows && x.groups > 1 && x.b_group < (x.N - 1) * x.ldb + kb) return GEMM_ERR_INVALID_ARG;
   if (by_k && x.groups > 1 && x.d_group < (x.M - 1) * x.ldd + x.N) return GEMM_ERR_INVALID_ARG;
   if (x.group != SC_DENSE && (!x.starts || !x.counts)) return GEMM_ERR_INVALID_ARG;
   if (!x.D) return GEMM_ERR_INVALID_ARG;
@@ -159,13 +96,13 @@ gemm_status_t check_product(const Product& x) {
   if (x.K > 0) {
     if (!x.A || !x.B || !x.SA || !x.SB) return GEMM_ERR_INVALID_ARG;
     const int64_t nb = rows ? x.groups : 1;
-    if (d_meets(region(x.A, x.M, x.K, x.lda, 1)) || d_meets(run_of(x.SA, scale_tiles(x.M, x.K) * 512)) ||
-        d_meets(run_of(x.SB, nb * scale_tiles(x.N, x.K) * 512)) ||
-        (rows ? groups_meet(x.B, nb, x.N, x.K, x.ldb, x.b_group, 1, region(x.D, x.M, x.N, x.ldd, es))
-              : d_meets(region(x.B, x.N, x.K, x.ldb, 1))))
+    if (d_meets(region(x.A, x.M, kb, x.lda, 1)) || d_meets(run_of(x.SA, x.tiles_of(x.M) * 512)) ||
+        d_meets(run_of(x.SB, nb * x.tiles_of(x.N) * 512)) ||
+        (rows ? groups_meet(x.B, nb, x.N, kb, x.ldb, x.b_group, 1, region(x.D, x.M, x.N, x.ldd, es))
+              : d_meets(region(x.B, x.N, kb, x.ldb, 1))))
       return GEMM_ERR_INVALID_ARG;
     if (!aligned(x.SA, 16) || !aligned(x.SB, 16)) return GEMM_ERR_ALIGNMENT;
-    if (scale_tiles(x.M, x.K) > kMaxDim || nb * scale_tiles(x.N, x.K) > kMaxDim) return GEMM_ERR_UNSUPPORTED;
+    if (x.tiles_of(x.M) > kMaxDim || nb * x.tiles_of(x.N) > kMaxDim) return GEMM_ERR_UNSUPPORTED;
   }
   if (!aligned(x.D, 16) || (x.ldd * es) % 16 || (by_k && x.groups > 1 && (x.d_group * es) % 16)) return GEMM_ERR_ALIGNMENT;
   if (x.group != SC_DENSE && (!aligned(x.starts, 4) || !aligned(x.counts, 4))) return GEMM_ERR_ALIGNMENT;
@@ -179,13 +116,15 @@ enum ScKernel { SC_TILE, SC_PAIR, SC_SLICED };
 struct ScPick {
   ScKernel kernel = SC_TILE;
   int bn = 128, slices = 1, stages = 0, part_rows = 32;
+  bool four = false;
 };
 
 void set_sliced(ScPick* c, int slices) {
   c->slices = slices;
   c->part_rows = slices > 1 ? c->bn : 32;
   c->stages = 8;
-  while (c->stages > 2 && scaled_sliced_smem(c->bn, c->stages, c->part_rows) > kSmemMax) --c->stages;
+  const auto smem = c->four ? mx4_sliced_smem : scaled_sliced_smem;
+  while (c->stages > 2 && smem(c->bn, c->stages, c->part_rows) > kSmemMax) --c->stages;
 }
 
 // Clusters of 1 .. 8 CTAs that the device holds at once (16 tiles in 8 slices, 128 CTAs,
@@ -203,9 +142,10 @@ struct Residency {
 // every cluster resident at once, a CTA an SM (4096 x 4096, one row: 6.2 us in 4 slices,
 // 128 CTAs, against 7.9 in 5).  A slice may be empty: its CTA still takes its share of the rows that
 // the slices add up (33 x 1024 x 512, four k-blocks: 5.3 us in 8 slices, 6.4 in 2).
-ScPick pick_sliced(int64_t rows, int64_t tiles, int sms) {
+ScPick pick_sliced(bool four, int64_t rows, int64_t tiles, int sms) {
   static const Residency fits(sms);
   ScPick c;
+  c.four = four;
   c.kernel = SC_SLICED;
   c.bn = int(std::min<int64_t>(128, round_up(rows, 32)));
   int s = 8;
@@ -222,13 +162,14 @@ constexpr int64_t kFewRows = 48;
 // the device; its rows are estimated from the capacity, which holds up to 127 empty rows a
 // group).  GEMM_SCALED_KERNEL=tile|pair|sliced and GEMM_SCALED_SLICES=n override it.
 ScPick pick(const Product& x, int sms) {
-  const int64_t kb = ceil_div(x.K, SC_BK), nb = ceil_div(x.N, 128), mb = ceil_div(x.M, 128);
+  const int64_t kb = ceil_div(x.k_bytes(), SC_BK), nb = ceil_div(x.N, 128), mb = ceil_div(x.M, 128);
   ScPick c;
+  c.four = x.four;
   if (x.group == SC_ROWS) {
     const int64_t per = std::max<int64_t>(1, x.M / x.groups - 127);
     const int64_t active = std::max<int64_t>(1, std::min(x.groups, x.M / 128));
     if (per <= kFewRows)
-      c = pick_sliced(128, active * nb, sms);
+      c = pick_sliced(x.four, 128, active * nb, sms);
     else  // (256 rows each: 53.6 us on single CTAs, 48.8 on pairs; 8 experts of 4096 x 1024, 150 rows: 14.9 and 18.3)
       c.kernel = per < 256 ? SC_TILE : SC_PAIR;
   } else if (x.group == SC_K) {
@@ -243,7 +184,7 @@ ScPick pick(const Product& x, int sms) {
     // slices, 19.4 whole; 128 x 6912 x 2048: 11.8 in 2 slices, 10.5 whole.
     c.kernel = mb * nb > sms ? SC_PAIR : SC_TILE;
     if (mb * nb <= sms) {
-      const ScPick sl = pick_sliced(x.M, mb * nb, sms);
+      const ScPick sl = pick_sliced(x.four, x.M, mb * nb, sms);
       const double rows = double(std::min<int64_t>(x.M, 128)), s = sl.slices;
       if (x.M <= 64 || 0.07 * rows / s < 0.22 * double(kb) * (1 - 1 / s)) c = sl;
     }
@@ -252,7 +193,7 @@ ScPick pick(const Product& x, int sms) {
     if (!std::strcmp(f, "tile")) c.kernel = SC_TILE;
     if (!std::strcmp(f, "pair")) c.kernel = SC_PAIR;
     if (!std::strcmp(f, "sliced") && x.group != SC_K && c.kernel != SC_SLICED)
-      c = pick_sliced(x.group == SC_ROWS ? 128 : x.M, mb * nb, sms);
+      c = pick_sliced(x.four, x.group == SC_ROWS ? 128 : x.M, mb * nb, sms);
   }
   if (c.kernel == SC_SLICED) {
     const int s = env_int("GEMM_SCALED_SLICES", 0);
@@ -303,15 +244,15 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
     return GEMM_OK;
   }
   DeviceGuard guard(plan->device);
-  const int64_t b_groups = x.group == SC_ROWS ? x.groups : 1;
-  const size_t a_copy = repack_bytes(x.A, x.lda, 1, 0, x.M, x.K);
-  const size_t b_copy = repack_bytes(x.B, x.ldb, b_groups, x.b_group, x.N, x.K);
+  const int64_t b_groups = x.group == SC_ROWS ? x.groups : 1, kbytes = x.k_bytes();
+  const size_t a_copy = repack_bytes(x.A, x.lda, 1, 0, x.M, kbytes);
+  const size_t b_copy = repack_bytes(x.B, x.ldb, b_groups, x.b_group, x.N, kbytes);
   if (a_copy + b_copy > 0) {
     gemm_status_t st = ensure_tws(plan, a_copy + b_copy, s);
     int64_t none = 0;
-    if (st == GEMM_OK && a_copy) st = repack(plan, &x.A, &x.lda, 1, &none, x.M, x.K, nullptr, plan->tws, s);
+    if (st == GEMM_OK && a_copy) st = repack(plan, &x.A, &x.lda, 1, &none, x.M, kbytes, nullptr, plan->tws, s);
     if (st == GEMM_OK && b_copy)
-      st = repack(plan, &x.B, &x.ldb, b_groups, &x.b_group, x.N, x.K, x.group == SC_ROWS ? x.counts : nullptr,
+      st = repack(plan, &x.B, &x.ldb, b_groups, &x.b_group, x.N, kbytes, x.group == SC_ROWS ? x.counts : nullptr,
                   static_cast<char*>(plan->tws) + a_copy, s);
     if (st != GEMM_OK) return st;
   }
@@ -329,10 +270,10 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   p.cap = int(x.group == SC_K ? x.K : x.M);
   p.m_blocks = int(ceil_div(x.M, tile_m));
   p.n_blocks = int(ceil_div(x.N, tile_n));
-  p.k_blocks = int(ceil_div(x.K, SC_BK));
+  p.k_blocks = int(ceil_div(kbytes, SC_BK));
   p.sa_cols = int(scale_groups(x.K));
   p.sb_cols = p.sa_cols;
-  p.sb_group = int(scale_tiles(x.N, x.K));
+  p.sb_group = int(x.four ? std::max<int64_t>(1, ceil_div(x.N, 128)) : scale_tiles(x.N, x.K));  // (4 bits: in row blocks)
   p.out_kind = type_kind(x.d_type);
   p.n_tma = int((x.N * es) / 16 * 16 / es);
   p.d = x.D;
@@ -353,7 +294,8 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   // tcgen05 instruction descriptor, kind::mxf8f6f4: bits 7-9 A type and 10-12 B type
   // (0 E4M3, 1 E5M2), 17-22 N>>3, 23 scale type (1 = E8M0), 24-28 M>>4; the kernels add the
   // scale ids (4-5 for B, 29-30 for A).  The sliced kernel's MMA takes B's rows as its A, and its N from the tile.
-  const uint32_t ta = x.a_type == GEMM_TYPE_E5M2, tb = x.b_type == GEMM_TYPE_E5M2;
+  // 4 bits, kind::mxf4: the same with 1 for E2M1, bit 31 clear (K = 64), the scale ids the kernels' too.
+  const uint32_t ta = x.four || x.a_type == GEMM_TYPE_E5M2, tb = x.four || x.b_type == GEMM_TYPE_E5M2;
   const uint32_t mma_m = pair ? 256 : 128, mma_n = sliced ? 0u : uint32_t(tile_n);
   p.idesc = ((sliced ? tb : ta) << 7) | ((sliced ? ta : tb) << 10) | (mma_n >> 3 << 17) | (1u << 23) | (mma_m >> 4 << 24);
   // Groups of tile rows walked column by column: tiles that run at the same time share
@@ -367,7 +309,7 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   if (x.group == SC_ROWS) p.raster = 4;
   int grid;
   if (pair) {
-    static const int clusters = scaled_tile_clusters();
+    static const int clusters = std::min(scaled_tile_clusters(), mx4_tile_clusters());
     if (clusters <= 0) return GEMM_ERR_UNSUPPORTED;
     grid = int(2 * std::min<int64_t>(bound, clusters));
   } else if (sliced) {
@@ -385,12 +327,19 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   if (x.K == 0 || p.n_tma == 0 || sliced)
     ok = map3(&m.d, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, plan->err, 32, 32, 1, 32, 1024, 32, 32, sw);
   if (x.K > 0) {
-    ok = ok && map3(&m.a, u8, 1, x.A, x.K, x.M, 1, x.lda, x.lda * x.M, SC_BK, sliced ? 32 : 128, sw);
-    ok = ok && map3(&m.b, u8, 1, x.B, x.K, x.N, nb, x.ldb, nb > 1 ? x.b_group : x.ldb * x.N, SC_BK, 128, sw);
+    ok = ok && map3(&m.a, u8, 1, x.A, kbytes, x.M, 1, x.lda, x.lda * x.M, SC_BK, sliced ? 32 : 128, sw);
+    ok = ok && map3(&m.b, u8, 1, x.B, kbytes, x.N, nb, x.ldb, nb > 1 ? x.b_group : x.ldb * x.N, SC_BK, 128, sw);
     const CUtensorMapDataType u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
-    const int64_t ta_n = scale_tiles(x.M, x.K), tb_n = nb * p.sb_group;
-    ok = ok && map3(&m.sa, u32, 4, x.SA, 128, ta_n, 1, 128, 128 * ta_n, 128, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
-    ok = ok && map3(&m.sb, u32, 4, x.SB, 128, tb_n, 1, 128, 128 * tb_n, 128, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+    const CUtensorMapSwizzle plain = CU_TENSOR_MAP_SWIZZLE_NONE;
+    if (x.four) {  // tiles along K, row blocks; a box holds a stage's two tiles
+      const int64_t tk = mx4_scale_tiles(1, x.K), ma = std::max<int64_t>(1, ceil_div(x.M, 128));
+      ok = ok && map3(&m.sa, u32, 4, x.SA, 128, tk, ma, 128, 128 * tk, 128, 2, plain);
+      ok = ok && map3(&m.sb, u32, 4, x.SB, 128, tk, nb * p.sb_group, 128, 128 * tk, 128, 2, plain);
+    } else {
+      const int64_t ta_n = scale_tiles(x.M, x.K), tb_n = nb * p.sb_group;
+      ok = ok && map3(&m.sa, u32, 4, x.SA, 128, ta_n, 1, 128, 128 * ta_n, 128, 1, plain);
+      ok = ok && map3(&m.sb, u32, 4, x.SB, 128, tb_n, 1, 128, 128 * tb_n, 128, 1, plain);
+    }
   } else {
     m.a = m.b = m.sa = m.sb = m.d;
   }
@@ -410,10 +359,10 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   info.path = sliced ? GEMM_PATH_SCALED_SLICED : GEMM_PATH_SCALED;
   info.tile_m = tile_m;
   info.tile_n = tile_n;
-  info.tile_k = SC_BK;
+  info.tile_k = x.four ? 2 * SC_BK : SC_BK;
   info.cta_per_tile = pair ? 2 : sliced ? c.slices : 1;
   info.splitk = sliced ? c.slices : 1;
-  info.stages = sliced ? c.stages : scaled_tile_stages(pair);
+  info.stages = sliced ? c.stages : x.four ? mx4_tile_stages(pair) : scaled_tile_stages(pair);
   info.raster_group = p.raster;
   info.grid = grid;
   info.tiles = bound;
@@ -421,6 +370,7 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   info.launches = 1 + int(a_copy > 0) + int(b_copy > 0);
   info.workspace_bytes = int64_t(a_copy + b_copy);
   plan->last = info;
+  if (x.four) return launched(sliced ? launch_mx4_sliced(m, p, grid, s) : launch_mx4_tile(pair, m, p, grid, s));
   return launched(sliced ? launch_scaled_sliced(m, p, grid, s) : launch_scaled_tile(pair, m, p, grid, s));
 }
 
@@ -429,12 +379,9 @@ gemm_status_t checked_run(gemm_plan_t plan, const Product& x, void* stream) {
   const gemm_status_t st = check_product(x);
   if (st != GEMM_OK) return st;
   const CallScope call(plan, "%s %lldx%lldx%lld groups %lld %s %s->%s", x.name, (long long)x.M, (long long)x.N, (long long)x.K,
-                       (long long)x.groups, type_name(x.a_type), type_name(x.b_type), type_name(x.d_type));
+                       (long long)x.groups, x.four ? "mx4" : type_name(x.a_type), x.four ? "mx4" : type_name(x.b_type), type_name(x.d_type));
   return call.done(run_product(plan, x, static_cast<cudaStream_t>(stream)), &plan->last);
 }
-
-// Rows of `ld` elements of es bytes from p allow 16-byte accesses where columns do.
-bool rows_wide(const void* p, int64_t ld, int64_t es) { return aligned(p, 16) && (ld * es) % 16 == 0; }
 
 // Bytes of the weighted sum's loads and stores, given each matrix's address and bytes between rows.
 int access_bytes(int64_t cols, std::initializer_list<std::pair<const void*, int64_t>> rows) {
@@ -442,17 +389,6 @@ int access_bytes(int64_t cols, std::initializer_list<std::pair<const void*, int6
   for (const auto& m : rows)
     while (wide && (!aligned(m.first, size_t(wide)) || m.second % wide)) wide = wide == 16 ? 4 : 0;
   return wide;
-}
-
-// Does a result share a byte with an input or with another result?
-bool results_meet(std::initializer_list<Region> results, std::initializer_list<Region> inputs) {
-  for (const Region* r = results.begin(); r != results.end(); ++r) {
-    for (const Region& i : inputs)
-      if (overlaps(*r, i)) return true;
-    for (const Region* o = results.begin(); o != r; ++o)
-      if (overlaps(*r, *o)) return true;
-  }
-  return false;
 }
 
 gemm_status_t check_route(int64_t tokens, int64_t experts, const void* logits, int64_t ldl, gemm_type_t type,
@@ -487,6 +423,27 @@ RouteArgs route_args(gemm_plan_t plan, int64_t tokens, int64_t experts, const vo
   a.scale = r.scale;
   a.wide = rows_wide(logits, ldl, type_bytes(type));
   a.pdl = plan->pdl;
+  return a;
+}
+
+gemm_status_t check_balance(int64_t tokens, int64_t experts, const void* logits, int64_t ldl, gemm_type_t type,
+                            gemm_score_t score, int32_t top_k, const int32_t* indices) {
+  if (top_k < 1) return GEMM_ERR_INVALID_ARG;
+  // (the choice may be of any router's: as many experts as choices are not asked for)
+  gemm_route_t r{score, int32_t(std::min<int64_t>(top_k, std::max<int64_t>(1, experts))), 1, 1, 1, 0, 1.f};
+  const gemm_status_t st = check_route(tokens, experts, logits, ldl, type, r);
+  if (st != GEMM_OK) return st;
+  if (top_k > ROUTE_MAX_K || tokens * top_k > kMaxDim) return GEMM_ERR_UNSUPPORTED;
+  if (tokens > 0 && !indices) return GEMM_ERR_INVALID_ARG;
+  return aligned(indices, 4) ? GEMM_OK : GEMM_ERR_ALIGNMENT;
+}
+
+BalanceArgs balance_args(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
+                         gemm_type_t type, gemm_score_t score, int32_t top_k, const int32_t* indices) {
+  const gemm_route_t r{score, top_k, 1, 1, 1, 0, 1.f};
+  BalanceArgs a{};
+  static_cast<RouteArgs&>(a) = route_args(plan, tokens, experts, logits, ldl, type, r);
+  a.indices = const_cast<int32_t*>(indices);
   return a;
 }
 
@@ -573,6 +530,54 @@ gemm_status_t gemm_run_grouped_k(gemm_plan_t plan, int64_t groups, int64_t M, in
   return checked_run(plan, x, stream);
 }
 
+int64_t gemm_mx4_scale_bytes(int64_t rows, int64_t cols) {
+  return size_ok(rows) && size_ok(cols) ? mx4_scale_tiles(rows, cols) * 512 : -1;
+}
+
+gemm_status_t gemm_check_mx4(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA, const void* B,
+                             int64_t ldb, const void* SB, const void* D, int64_t ldd, gemm_type_t d_type, float alpha,
+                             float beta, gemm_epilogue_t epilogue) {
+  Product x;
+  x.four = true;
+  x.M = M, x.N = N, x.K = K;
+  x.A = A, x.lda = lda, x.SA = SA;
+  x.B = B, x.ldb = ldb, x.SB = SB;
+  x.D = const_cast<void*>(D), x.ldd = ldd, x.d_type = d_type;
+  x.alpha = alpha, x.beta = beta, x.epi = epilogue;
+  return check_product(x);
+}
+
+gemm_status_t gemm_run_mx4(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA,
+                           const void* B, int64_t ldb, const void* SB, void* D, int64_t ldd, gemm_type_t d_type,
+                           float alpha, float beta, gemm_epilogue_t epilogue, void* stream) {
+  Product x;
+  x.name = "gemm_run_mx4";
+  x.four = true;
+  x.M = M, x.N = N, x.K = K;
+  x.A = A, x.lda = lda, x.SA = SA;
+  x.B = B, x.ldb = ldb, x.SB = SB;
+  x.D = D, x.ldd = ldd, x.d_type = d_type;
+  x.alpha = alpha, x.beta = beta, x.epi = epilogue;
+  return checked_run(plan, x, stream);
+}
+
+gemm_status_t gemm_run_grouped_mx4(gemm_plan_t plan, int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                   const int32_t* starts, const int32_t* counts, const void* A, int64_t lda,
+                                   const void* SA, const void* B, int64_t ldb, int64_t b_group, const void* SB, void* D,
+                                   int64_t ldd, gemm_type_t d_type, float alpha, float beta, gemm_epilogue_t epilogue,
+                                   void* stream) {
+  Product x;
+  x.name = "gemm_run_grouped_mx4";
+  x.four = true;
+  x.group = SC_ROWS, x.groups = groups, x.M = rows, x.N = N, x.K = K;
+  x.starts = starts, x.counts = counts;
+  x.A = A, x.lda = lda, x.SA = SA;
+  x.B = B, x.ldb = ldb, x.b_group = b_group, x.SB = SB;
+  x.D = D, x.ldd = ldd, x.d_type = d_type;
+  x.alpha = alpha, x.beta = beta, x.epi = epilogue;
+  return checked_run(plan, x, stream);
+}
+
 gemm_status_t gemm_quantize(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx, gemm_type_t x_type,
                             const int32_t* rowmap, int64_t map_div, int64_t src_rows, gemm_type_t q_type,
                             int32_t block_rows, void* Q, int64_t ldq, void* SQ, void* QT, int64_t ldqt, void* SQT,
@@ -631,6 +636,93 @@ gemm_status_t gemm_quantize(gemm_plan_t plan, int64_t rows, int64_t cols, const 
               .bytes(SQT, gemm_scale_bytes(cols, rows)).bytes(rowmap, rowmap ? rows * 4 : 0).s;
 #endif
   return call.done(launched(launch_quantize(a, static_cast<cudaStream_t>(stream))));
+}
+
+gemm_status_t gemm_quantize_mx4(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx,
+                                gemm_type_t x_type, const int32_t* rowmap, int64_t map_div, int64_t src_rows, void* Q,
+                                int64_t ldq, void* SQ, void* QT, int64_t ldqt, void* SQT, void* stream) {
+  if (!plan || rows < 0 || cols < 0 || src_rows < 0 || !is_float_type(x_type)) return GEMM_ERR_INVALID_ARG;
+  if (rowmap && map_div < 1) return GEMM_ERR_INVALID_ARG;
+  // (the grid takes 65535 row blocks)
+  if (!size_ok(rows) || !size_ok(cols) || !size_ok(src_rows) || rows > int64_t(65532) * 128 || map_div > kMaxDim)
+    return GEMM_ERR_UNSUPPORTED;
+  if ((Q == nullptr) != (SQ == nullptr) || (QT == nullptr) != (SQT == nullptr) || (!Q && !QT)) return GEMM_ERR_INVALID_ARG;
+  const int64_t one = 1, cb = ceil_div(cols, 2), rb = ceil_div(rows, 2);
+  if (ldx < std::max(one, cols) || (Q && ldq < std::max(one, cb)) || (QT && ldqt < std::max(one, rb)))
+    return GEMM_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return GEMM_OK;
+  const int64_t xr = rowmap ? src_rows : rows, es = type_bytes(x_type);
+  if (!X && xr > 0) return GEMM_ERR_INVALID_ARG;
+  if (!aligned(X, size_t(es)) || !aligned(rowmap, 4) || !aligned(Q, 16) || !aligned(SQ, 16) || !aligned(QT, 16) ||
+      !aligned(SQT, 16) || (Q && ldq % 16) || (QT && ldqt % 16))
+    return GEMM_ERR_ALIGNMENT;
+  const int64_t sq = mx4_scale_tiles(rows, cols) * 512, sqt = mx4_scale_tiles(cols, rows) * 512;
+  // no result may share a byte with X, the map or another result
+  if (results_meet({region(Q, Q ? rows : 0, cb, ldq, 1), run_of(SQ, sq), region(QT, QT ? cols : 0, rb, ldqt, 1), run_of(SQT, sqt)},
+                   {region(X, xr, cols, ldx, es), run_of(rowmap, rows * 4)}))
+    return GEMM_ERR_INVALID_ARG;
+  const CallScope call(plan, "gemm_quantize_mx4 %lldx%lld %s->mx4%s%s%s", (long long)rows, (long long)cols, type_name(x_type),
+                       Q ? " Q" : "", QT ? " QT" : "", rowmap ? " by map" : "");
+  DeviceGuard guard(plan->device);
+  QuantArgs a{};
+  a.x = X;
+  a.ldx = ldx;
+  a.x_kind = type_kind(x_type);
+  a.rows = int(rows);
+  a.cols = int(cols);
+  a.rowmap = rowmap;
+  a.map_div = rowmap ? int(map_div) : 1;
+  a.src_rows = int(xr);
+  a.vec = rows_wide(X, ldx, es);
+  a.q = static_cast<uint8_t*>(Q);
+  a.sq = static_cast<uint8_t*>(SQ);
+  a.qt = static_cast<uint8_t*>(QT);
+  a.sqt = static_cast<uint8_t*>(SQT);
+  a.ldq = ldq;
+  a.ldqt = ldqt;
+  a.q_groups = int(mx4_scale_tiles(1, cols));
+  a.qt_groups = int(mx4_scale_tiles(1, rows));
+  a.pdl = plan->pdl;
+#ifdef DG_DEBUG
+  a.dbg = Spans(plan->err).matrix(X, xr, cols, ldx, es).out_matrix(Q, Q && !QT ? rows : 0, cb, ldq, 1).matrix(Q, Q && QT ? rows : 0, cb, ldq, 1)
+              .bytes(SQ, SQ ? sq : 0).out_matrix(QT, QT ? cols : 0, rb, ldqt, 1).bytes(SQT, SQT ? sqt : 0)
+              .bytes(rowmap, rowmap ? rows * 4 : 0).s;
+#endif
+  return call.done(launched(launch_quantize_mx4(a, static_cast<cudaStream_t>(stream))));
+}
+
+gemm_status_t gemm_dequantize(gemm_plan_t plan, int64_t rows, int64_t cols, const void* Q, int64_t ldq, gemm_type_t q_type,
+                              const void* SQ, void* X, int64_t ldx, gemm_type_t x_type, void* stream) {
+  const bool four = q_type == GEMM_TYPE_E2M1;
+  if (!plan || rows < 0 || cols < 0 || !is_float_type(x_type) || (!four && !is_code_type(q_type))) return GEMM_ERR_INVALID_ARG;
+  if (!size_ok(rows) || !size_ok(cols) || rows * ceil_div(cols, 8) > kMaxDim * 1024) return GEMM_ERR_UNSUPPORTED;
+  const int64_t one = 1, cb = four ? ceil_div(cols, 2) : cols;
+  if (ldq < std::max(one, cb) || ldx < std::max(one, cols)) return GEMM_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return GEMM_OK;
+  if (!Q || !SQ || !X) return GEMM_ERR_INVALID_ARG;
+  const int64_t es = type_bytes(x_type), sq = (four ? mx4_scale_tiles(rows, cols) : scale_tiles(rows, cols)) * 512;
+  if (!aligned(Q, 16) || ldq % 16 || !aligned(SQ, 16) || !aligned(X, size_t(es))) return GEMM_ERR_ALIGNMENT;
+  if (results_meet({region(X, rows, cols, ldx, es)}, {region(Q, rows, cb, ldq, 1), run_of(SQ, sq)})) return GEMM_ERR_INVALID_ARG;
+  const CallScope call(plan, "gemm_dequantize %lldx%lld %s->%s", (long long)rows, (long long)cols, four ? "mx4" : type_name(q_type),
+                       type_name(x_type));
+  DeviceGuard guard(plan->device);
+  DequantArgs a{};
+  a.q = static_cast<const uint8_t*>(Q);
+  a.ldq = ldq;
+  a.sq = static_cast<const uint8_t*>(SQ);
+  a.code = four ? CODE_E2M1 : q_type == GEMM_TYPE_E5M2 ? CODE_E5M2 : CODE_E4M3;
+  a.rows = int(rows);
+  a.cols = int(cols);
+  a.groups = int(four ? mx4_scale_tiles(1, cols) : scale_groups(cols));
+  a.x = X;
+  a.ldx = ldx;
+  a.x_kind = type_kind(x_type);
+  a.wide = rows_wide(X, ldx, es);
+  a.pdl = plan->pdl;
+#ifdef DG_DEBUG
+  a.dbg = Spans(plan->err).matrix(Q, rows, cb, ldq, 1).bytes(SQ, sq).out_matrix(X, rows, cols, ldx, es).s;
+#endif
+  return call.done(launched(launch_dequantize(a, static_cast<cudaStream_t>(stream))));
 }
 
 gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
@@ -694,6 +786,81 @@ gemm_status_t gemm_route_backward(gemm_plan_t plan, int64_t tokens, int64_t expe
               .bytes(dweights, tokens * route.top_k * 4).out_matrix(dlogits, tokens, experts, lddl, type_bytes(l_type)).s;
 #endif
   return call.done(launched(launch_route_backward(a, static_cast<cudaStream_t>(stream))));
+}
+
+gemm_status_t gemm_balance(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
+                           gemm_type_t l_type, gemm_score_t score, int32_t top_k, const int32_t* indices, float scale,
+                           int32_t* counts, float* shares, float* factor, float* loss, void* stream) {
+  if (!plan) return GEMM_ERR_INVALID_ARG;
+  const gemm_status_t st = check_balance(tokens, experts, logits, ldl, l_type, score, top_k, indices);
+  if (st != GEMM_OK) return st;
+  if (!counts || !shares || !factor || !loss) return GEMM_ERR_INVALID_ARG;
+  if (!aligned(counts, 4) || !aligned(shares, 4) || !aligned(factor, 4) || !aligned(loss, 4)) return GEMM_ERR_ALIGNMENT;
+  const int64_t es = type_bytes(l_type);
+  if (results_meet({run_of(counts, experts * 4), run_of(shares, experts * 4), run_of(factor, experts * 4), run_of(loss, 4)},
+                   {region(logits, tokens, experts, ldl, es), run_of(indices, tokens * top_k * 4)}))
+    return GEMM_ERR_INVALID_ARG;
+  const CallScope call(plan, "gemm_balance %lldx%lld %s %s top %d", (long long)tokens, (long long)experts, type_name(l_type),
+                       score == GEMM_SCORE_SIGMOID ? "sigmoid" : "softmax", int(top_k));
+  DeviceGuard guard(plan->device);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int ctas = balance_ctas(tokens, experts, plan->sms);
+  const size_t ws = ctas > 1 ? size_t(ctas) * size_t(experts) * 4 : 0;
+  if (ctas > 1) {
+    gemm_status_t grown = ensure_ws(plan, ws, s);
+    if (grown == GEMM_OK) grown = ensure_counters(plan, size_t(experts) + 2, s);
+    if (grown != GEMM_OK) return grown;
+  }
+  BalanceArgs a = balance_args(plan, tokens, experts, logits, ldl, l_type, score, top_k, indices);
+  a.scale = scale;
+  a.counts = counts;
+  a.shares = shares;
+  a.factor = factor;
+  a.loss = loss;
+  a.parts = static_cast<float*>(plan->ws);
+  a.counters = plan->counters;
+#ifdef DG_DEBUG
+  a.dbg = Spans(plan->err).matrix(logits, tokens, experts, ldl, es).bytes(indices, tokens * top_k * 4).bytes(counts, experts * 4)
+              .bytes(shares, experts * 4).out_matrix(factor, 1, experts, 0, 4).bytes(loss, 4).bytes(plan->ws, int64_t(ws))
+              .bytes(plan->counters, ctas > 1 ? (experts + 2) * 4 : 0).s;
+#endif
+  return call.done(launched(launch_balance(a, ctas, s)));
+}
+
+gemm_status_t gemm_balance_backward(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
+                                    gemm_type_t l_type, gemm_score_t score, int32_t top_k, const int32_t* indices,
+                                    const float* factor, const float* dloss, int32_t accumulate, void* dlogits, int64_t lddl,
+                                    void* stream) {
+  if (!plan) return GEMM_ERR_INVALID_ARG;
+  const gemm_status_t st = check_balance(tokens, experts, logits, ldl, l_type, score, top_k, indices);
+  if (st != GEMM_OK) return st;
+  if (lddl < experts) return GEMM_ERR_INVALID_ARG;
+  if (tokens == 0) return GEMM_OK;
+  if (!factor || !dlogits) return GEMM_ERR_INVALID_ARG;
+  const int64_t es = type_bytes(l_type);
+  if (!aligned(factor, 4) || !aligned(dloss, 4) || !aligned(dlogits, size_t(es))) return GEMM_ERR_ALIGNMENT;
+  // (a token's logits are read before its gradients are written: these may be the logits' own place)
+  const bool in_place = dlogits == logits && lddl == ldl && !accumulate;
+  if (results_meet({region(dlogits, tokens, experts, lddl, es)},
+                   {region(logits, in_place ? 0 : tokens, experts, ldl, es), run_of(indices, tokens * top_k * 4),
+                    run_of(factor, experts * 4), run_of(dloss, 4)}))
+    return GEMM_ERR_INVALID_ARG;
+  const CallScope call(plan, "gemm_balance_backward %lldx%lld %s %s top %d%s", (long long)tokens, (long long)experts,
+                       type_name(l_type), score == GEMM_SCORE_SIGMOID ? "sigmoid" : "softmax", int(top_k),
+                       accumulate ? " accumulated" : "");
+  DeviceGuard guard(plan->device);
+  BalanceArgs a = balance_args(plan, tokens, experts, logits, ldl, l_type, score, top_k, indices);
+  a.factor = const_cast<float*>(factor);
+  a.dloss = dloss;
+  a.accumulate = accumulate != 0;
+  a.dlogits = dlogits;
+  a.lddl = lddl;
+  a.wide_out = rows_wide(dlogits, lddl, es);
+#ifdef DG_DEBUG
+  a.dbg = Spans(plan->err).matrix(logits, tokens, experts, ldl, es).bytes(indices, tokens * top_k * 4).bytes(factor, experts * 4)
+              .bytes(dloss, dloss ? 4 : 0).out_matrix(dlogits, tokens, experts, lddl, es).s;
+#endif
+  return call.done(launched(launch_balance_backward(a, static_cast<cudaStream_t>(stream))));
 }
 
 int64_t gemm_route_rows(int64_t tokens, int64_t top_k, int64_t experts) {

@@ -550,6 +550,28 @@ __device__ __forceinline__ void tc_mma_scaled(uint32_t d_tmem, uint32_t alo, uin
 #undef DG_MMA_SCALED
 }
 
+// The same over K = 64 4-bit values (E2M1, two to a byte), with a scale byte for each 32: the two bytes of each
+// 32-bit word that are meant start at the descriptor's scale ids, 0 or 2 (mx4_ids: of the k-th MMA of a stage).
+__device__ constexpr uint32_t mx4_ids(int k) { return uint32_t(k & 1) << 5 | uint32_t(k & 1) << 30; }
+template <bool PAIR>
+__device__ __forceinline__ void tc_mma_mx4(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t sfa,
+                                           uint32_t sfb, uint32_t accumulate, uint32_t one) {
+#define DG_MMA_MX4(GROUP)                                                                            \
+  asm volatile(                                                                                      \
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"                                                   \
+      "setp.ne.b32 p, %7, 0;\n\tsetp.ne.b32 q, %8, 0;\n\t"                                           \
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"                                             \
+      "@q tcgen05.mma.cta_group::" GROUP                                                             \
+      ".kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, [%5], [%6], p;\n\t}" ::"r"(d_tmem),      \
+      "r"(alo), "r"(blo), "r"(kDescSw128Hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(one) \
+      : "memory")
+  if constexpr (PAIR)
+    DG_MMA_MX4("2");
+  else
+    DG_MMA_MX4("1");
+#undef DG_MMA_MX4
+}
+
 // Arrive on `bar` (a pair: at this offset in both CTAs) once every tcgen05
 // operation that thread has issued so far has completed.
 template <bool PAIR>

@@ -28,11 +28,12 @@ GEMM_ERR_DEBUG_CHECK = 8
 # bits of the plan's error word (gemm_plan_last_error_bits)
 DBG_FLAG = 1 << 30
 DBG_SITES = {0: "tma", 1: "epilogue_store", 2: "epilogue_load", 3: "split_in_kernel", 4: "tile_reduce",
-             5: "gemv", 6: "scale", 7: "transpose", 8: "scaled", 9: "quantize", 10: "route", 11: "combine"}
+             5: "gemv", 6: "scale", 7: "transpose", 8: "scaled", 9: "quantize", 10: "route", 11: "combine",
+             12: "norm"}
 
 GEMM_OP_N, GEMM_OP_T = 0, 1
 GEMM_TYPE_BF16, GEMM_TYPE_F16, GEMM_TYPE_F32, GEMM_TYPE_TF32 = 0, 1, 2, 3
-GEMM_TYPE_E4M3, GEMM_TYPE_E5M2 = 4, 5
+GEMM_TYPE_E4M3, GEMM_TYPE_E5M2, GEMM_TYPE_E2M1 = 4, 5, 6
 GEMM_SCORE_SOFTMAX, GEMM_SCORE_SIGMOID = 0, 1
 GEMM_BF16_F32, GEMM_BF16_BF16, GEMM_F16_F32, GEMM_F16_F16, GEMM_TF32_F32 = 0, 1, 2, 3, 4
 GEMM_ACT_NONE, GEMM_ACT_LEAKY_RELU, GEMM_ACT_RELU, GEMM_ACT_GELU, GEMM_ACT_SILU = 0, 1, 2, 3, 4
@@ -119,6 +120,20 @@ _SIGNATURES = {
                                 _I32, _VP, _I64, _I32, _F, _F, gemm_epilogue_t, _VP]),
     "gemm_run_grouped_k": (_I32, [_VP, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _I64, _VP, _I32, _VP, _I64, _VP, _I32,
                                   _VP, _I64, _I64, _I32, _F, _F, gemm_epilogue_t, _VP]),
+    "gemm_mx4_scale_bytes": (_I64, [_I64, _I64]),
+    "gemm_quantize_mx4": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
+    "gemm_dequantize": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _VP, _I64, _I32, _VP]),
+    "gemm_run_mx4": (_I32, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP, _I64, _I32, _F, _F,
+                            gemm_epilogue_t, _VP]),
+    "gemm_check_mx4": (_I32, [_I64, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP, _I64, _I32, _F, _F, gemm_epilogue_t]),
+    "gemm_run_grouped_mx4": (_I32, [_VP, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _I64, _VP, _VP, _I64, _I64, _VP, _VP, _I64,
+                                    _I32, _F, _F, gemm_epilogue_t, _VP]),
+    "gemm_norm": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _I64, _I32, _VP, _I32, _F, _VP, _I64, _VP, _I64, _I32, _VP,
+                         _I64, _VP, _VP, _VP]),
+    "gemm_norm_backward": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _I64, _I32, _VP, _I32, _VP, _VP, _I64, _VP, _I64,
+                                  _VP, _VP]),
+    "gemm_balance": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _I32, _I32, _VP, _F, _VP, _VP, _VP, _VP, _VP]),
+    "gemm_balance_backward": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _I32, _I32, _VP, _VP, _VP, _I32, _VP, _I64, _VP]),
     "gemm_route": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, gemm_route_t, _VP, _VP, _VP]),
     "gemm_route_backward": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, gemm_route_t, _VP, _VP, _VP, _I64, _VP]),
     "gemm_route_rows": (_I64, [_I64, _I64, _I64]),
@@ -298,6 +313,60 @@ def gemm_run_grouped_k(plan, groups, M, N, rows, starts, counts, A, lda, SA, a_t
                                      D, ldd, d_group, d_type, alpha, beta, gemm_epilogue_t(act, slope), stream)
 
 
+def gemm_mx4_scale_bytes(rows, cols) -> int:
+    return load().gemm_mx4_scale_bytes(rows, cols)
+
+
+def gemm_quantize_mx4(plan, rows, cols, X, ldx, x_type, rowmap, map_div, src_rows, Q, ldq, SQ, QT, ldqt, SQT,
+                      stream=None) -> int:
+    return load().gemm_quantize_mx4(plan, rows, cols, X, ldx, x_type, rowmap, map_div, src_rows, Q, ldq, SQ, QT, ldqt, SQT,
+                                    stream)
+
+
+def gemm_dequantize(plan, rows, cols, Q, ldq, q_type, SQ, X, ldx, x_type, stream=None) -> int:
+    return load().gemm_dequantize(plan, rows, cols, Q, ldq, q_type, SQ, X, ldx, x_type, stream)
+
+
+def gemm_run_mx4(plan, M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta, act=GEMM_ACT_NONE, slope=0.0,
+                 stream=None) -> int:
+    return load().gemm_run_mx4(plan, M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta,
+                               gemm_epilogue_t(act, slope), stream)
+
+
+def gemm_check_mx4(M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta, act=GEMM_ACT_NONE, slope=0.0) -> int:
+    return load().gemm_check_mx4(M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta, gemm_epilogue_t(act, slope))
+
+
+def gemm_run_grouped_mx4(plan, groups, rows, N, K, starts, counts, A, lda, SA, B, ldb, b_group, SB, D, ldd, d_type, alpha,
+                         beta, act=GEMM_ACT_NONE, slope=0.0, stream=None) -> int:
+    return load().gemm_run_grouped_mx4(plan, groups, rows, N, K, starts, counts, A, lda, SA, B, ldb, b_group, SB, D, ldd,
+                                       d_type, alpha, beta, gemm_epilogue_t(act, slope), stream)
+
+
+def gemm_norm(plan, rows, cols, X, ldx, x_type, residual, ldr, h_type, gain, g_type, eps, H, ldh, Y, ldy, q_type, Q, ldq,
+              SQ, rstd, stream=None) -> int:
+    return load().gemm_norm(plan, rows, cols, X, ldx, x_type, residual, ldr, h_type, gain, g_type, eps, H, ldh, Y, ldy,
+                            q_type, Q, ldq, SQ, rstd, stream)
+
+
+def gemm_norm_backward(plan, rows, cols, dY, lddy, x_type, H, ldh, h_type, gain, g_type, rstd, dH, lddh, dX, lddx, dgain,
+                       stream=None) -> int:
+    return load().gemm_norm_backward(plan, rows, cols, dY, lddy, x_type, H, ldh, h_type, gain, g_type, rstd, dH, lddh, dX,
+                                     lddx, dgain, stream)
+
+
+def gemm_balance(plan, tokens, experts, logits, ldl, l_type, score, top_k, indices, scale, counts, shares, factor, loss,
+                 stream=None) -> int:
+    return load().gemm_balance(plan, tokens, experts, logits, ldl, l_type, score, top_k, indices, scale, counts, shares,
+                               factor, loss, stream)
+
+
+def gemm_balance_backward(plan, tokens, experts, logits, ldl, l_type, score, top_k, indices, factor, dloss, accumulate,
+                          dlogits, lddl, stream=None) -> int:
+    return load().gemm_balance_backward(plan, tokens, experts, logits, ldl, l_type, score, top_k, indices, factor, dloss,
+                                        accumulate, dlogits, lddl, stream)
+
+
 def gemm_route(plan, tokens, experts, logits, ldl, l_type, bias, route, weights, indices, stream=None) -> int:
     return load().gemm_route(plan, tokens, experts, logits, ldl, l_type, bias, route, weights, indices, stream)
 
@@ -388,6 +457,38 @@ def _scales(t, rows: int, cols: int, groups: int = 1) -> int:
     return t.data_ptr()
 
 
+def _mx4_scales(t, rows: int, cols: int, groups: int = 1) -> int:
+    """Pointer of the packed scale bytes of `groups` rows x cols matrices of 4-bit values."""
+    need = groups * 512 * (-(-rows // 128) or 1) * (-(-cols // 128) or 1)  # gemm_mx4_scale_bytes
+    if t.element_size() != 1 or t.numel() < need or not t.is_contiguous():
+        raise ValueError(f"scales are {need} contiguous bytes")
+    return t.data_ptr()
+
+
+def _bytes_of(t):
+    """A tensor of 4-bit codes, two to a byte (uint8, or float4_e2m1fn_x2 where torch has it)."""
+    if t.element_size() != 1 or t.is_floating_point() and "float4" not in str(t.dtype) or not t.is_floating_point() and "int8" not in str(t.dtype):
+        raise ValueError("4-bit codes are bytes (uint8) of two")
+    return t
+
+
+def _mx4_columns(K, width: int) -> int:
+    """Columns of a matrix whose rows of 4-bit codes are `width` bytes: twice that unless given."""
+    if K is None:
+        return 2 * width
+    if (K + 1) // 2 != width:
+        raise ValueError("rows of K 4-bit codes are (K + 1) // 2 bytes")
+    return K
+
+
+def _same_shape(t, rows: int, cols: int, name: str):
+    """(pointer, ld) of a matrix that has to be rows x cols."""
+    p, r, c, ld = _matrix(t)
+    if (r, c) != (rows, cols):
+        raise ValueError(f"{name} is {rows} x {cols}")
+    return p, ld
+
+
 def _array(t, n: int, dtype: str) -> int:
     """Pointer of at least n contiguous values ("int32" or "float32")."""
     if t.dtype is not _array_types.get(dtype):
@@ -398,6 +499,13 @@ def _array(t, n: int, dtype: str) -> int:
         raise ValueError(f"expected {dtype}")
     if t.numel() < n or not t.is_contiguous():
         raise ValueError(f"expected {n} contiguous {dtype}")
+    return t.data_ptr()
+
+
+def _vector(t, n: int) -> int:
+    """Pointer of exactly n contiguous values."""
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"expected {n} contiguous values")
     return t.data_ptr()
 
 
@@ -555,7 +663,136 @@ class Plan:
                                          ldb, _scales(SB, N, rows), _type_of(B), d, ldd, d_group, _type_of(D), alpha,
                                          beta, _epilogue(act, slope), self._stream(stream))
 
+    def dequantize(self, Q, SQ, X, *, stream=None) -> int:
+        """X (rows x cols) <- the values of 8-bit Q (float8_e4m3fn, float8_e5m2) or of 4-bit Q (bytes of two) with scales SQ."""
+        x, rows, cols, ldx = _matrix(X)
+        q, r, width, ldq = _matrix(Q)
+        if "float8" in str(Q.dtype):
+            kind, s = _type_of(Q), _scales(SQ, rows, cols)
+        else:
+            kind, s, cols = GEMM_TYPE_E2M1, _mx4_scales(SQ, rows, cols), _mx4_columns(cols, _bytes_of(Q).shape[1])
+        if r != rows or kind != GEMM_TYPE_E2M1 and width != cols:
+            raise ValueError("X has Q's rows and columns")
+        return load().gemm_dequantize(self.handle, rows, cols, q, ldq, kind, s, x, ldx, _type_of(X), self._stream(stream))
+
+    # ------------------------------------------- block-scaled 4-bit products
+
+    def quantize_mx4(self, X, Q=None, SQ=None, QT=None, SQT=None, *, rowmap=None, map_div=1, stream=None) -> int:
+        """X (rows x cols) -> 4-bit Q (rows x (cols + 1) // 2 bytes) and scales SQ (gemm_mx4_scale_bytes uint8), and/or its
+        transpose QT (cols x (rows + 1) // 2 bytes) and SQT.  rowmap as in quantize."""
+        x, src_rows, cols, ldx = _matrix(X)
+        rows = src_rows if rowmap is None else rowmap.numel()
+        q = sq = qt = sqt = None
+        ldq = ldqt = 0
+        if Q is not None:
+            q, ldq = _same_shape(_bytes_of(Q), rows, (cols + 1) // 2, "Q")
+            sq = _mx4_scales(SQ, rows, cols)
+        if QT is not None:
+            qt, ldqt = _same_shape(_bytes_of(QT), cols, (rows + 1) // 2, "QT")
+            sqt = _mx4_scales(SQT, cols, rows)
+        if Q is None and QT is None:
+            raise ValueError("neither Q nor QT")
+        return load().gemm_quantize_mx4(self.handle, rows, cols, x, ldx, _type_of(X),
+                                        None if rowmap is None else _array(rowmap, rows, "int32"), map_div, src_rows, q,
+                                        ldq, sq, qt, ldqt, sqt, self._stream(stream))
+
+    def run_mx4(self, A, SA, B, SB, D, *, K=None, alpha=1.0, beta=0.0, act=GEMM_ACT_NONE, slope=0.0, stream=None) -> int:
+        """D <- act(alpha * A @ B^T + beta * D) on 4-bit A (M x K), B (N x K), bytes of two, with packed scales SA, SB.
+        K: twice the bytes of a row unless given."""
+        a, M, width, lda = _matrix(_bytes_of(A))
+        b, N, width_b, ldb = _matrix(_bytes_of(B))
+        K = _mx4_columns(K, width)
+        if width_b != width:
+            raise ValueError("A and B have the same K")
+        d, ldd = _same_shape(D, M, N, "D")
+        return load().gemm_run_mx4(self.handle, M, N, K, a, lda, _mx4_scales(SA, M, K), b, ldb, _mx4_scales(SB, N, K), d, ldd,
+                                   _type_of(D), alpha, beta, _epilogue(act, slope), self._stream(stream))
+
+    def run_grouped_mx4(self, A, SA, B, SB, D, starts, counts, *, K=None, alpha=1.0, beta=0.0, act=GEMM_ACT_NONE, slope=0.0,
+                        stream=None) -> int:
+        """run_grouped on 4-bit A (rows x K) and B (groups x N x K), bytes of two."""
+        a, rows, width, lda = _matrix(_bytes_of(A))
+        b, groups, N, width_b, ldb, b_group = _matrices(_bytes_of(B))
+        K = _mx4_columns(K, width)
+        if width_b != width:
+            raise ValueError("A and B have the same K")
+        d, ldd = _same_shape(D, rows, N, "D")
+        return load().gemm_run_grouped_mx4(self.handle, groups, rows, N, K, _array(starts, groups, "int32"),
+                                           _array(counts, groups, "int32"), a, lda, _mx4_scales(SA, rows, K), b, ldb, b_group,
+                                           _mx4_scales(SB, N, K, groups), d, ldd, _type_of(D), alpha, beta,
+                                           _epilogue(act, slope), self._stream(stream))
+
+    # -------------------------------------------------------------- norm
+
+    def norm(self, X, gain=None, *, Y=None, Q=None, SQ=None, residual=None, H=None, rstd=None, eps=1e-6, stream=None) -> int:
+        """h = X + residual (rows x cols), rstd = 1 / sqrt(mean(h^2) + eps), Y = h * rstd * gain; also as 8-bit Q with scales SQ,
+        and H = h.  residual and H: X's type or float32; gain (cols): X's type or float32."""
+        x, rows, cols, ldx = _matrix(X)
+        x_type = h_type = g_type = q_type = _type_of(X)
+        r = g = h = y = q = sq = rs = None
+        ldr = ldh = ldy = ldq = 0
+        if residual is not None:
+            r, ldr = _same_shape(residual, rows, cols, "residual")
+            h_type = _type_of(residual)
+        if H is not None:
+            h, ldh = _same_shape(H, rows, cols, "H")
+            h_type = _type_of(H)
+            if residual is not None and residual.dtype != H.dtype:
+                raise ValueError("H is of the residual's type")
+        if gain is not None:
+            g, g_type = _vector(gain, cols), _type_of(gain)
+        if Y is not None:
+            y, ldy = _same_shape(Y, rows, cols, "Y")
+            if Y.dtype != X.dtype:
+                raise ValueError("Y is of X's type")
+        if Q is not None:
+            q, ldq = _same_shape(Q, rows, cols, "Q")
+            sq, q_type = _scales(SQ, rows, cols), _type_of(Q)
+        if rstd is not None:
+            rs = _array(rstd, rows, "float32")
+        return load().gemm_norm(self.handle, rows, cols, x, ldx, x_type, r, ldr, h_type, g, g_type, eps, h, ldh, y, ldy,
+                                q_type, q, ldq, sq, rs, self._stream(stream))
+
+    def norm_backward(self, dY, H, gain, rstd, dX, *, dgain=None, dH=None, stream=None) -> int:
+        """dX (H's type) and dgain (cols float32) from dY, the kept H and rstd; dH: the gradient that reaches h past the norm."""
+        d, rows, cols, lddy = _matrix(dY)
+        h, ldh = _same_shape(H, rows, cols, "H")
+        x, lddx = _same_shape(dX, rows, cols, "dX")
+        p, ldp = (None, 0) if dH is None else _same_shape(dH, rows, cols, "dH")
+        if dX.dtype != H.dtype or dH is not None and dH.dtype != H.dtype:
+            raise ValueError("dX and dH are of H's type")
+        y_type = _type_of(dY)
+        return load().gemm_norm_backward(self.handle, rows, cols, d, lddy, y_type, h, ldh, _type_of(H),
+                                         None if gain is None else _vector(gain, cols), y_type if gain is None else _type_of(gain),
+                                         _array(rstd, rows, "float32"), p, ldp, x, lddx,
+                                         None if dgain is None else _array(dgain, cols, "float32"), self._stream(stream))
+
     # ----------------------------------------------------------- experts
+
+    def balance(self, logits, indices, counts, shares, factor, loss, *, score=GEMM_SCORE_SOFTMAX, scale=1.0, stream=None) -> int:
+        """How evenly the choice (indices, tokens x top_k int32; -1: none) spreads the tokens: counts (experts int32), shares, factor
+        (experts float32) and the balance loss (one float32)."""
+        x, tokens, experts, ldl = _matrix(logits)
+        n, k = indices.shape
+        if n != tokens:
+            raise ValueError("indices is tokens x top_k")
+        return load().gemm_balance(self.handle, tokens, experts, x, ldl, _type_of(logits), score, k,
+                                   _array(indices, tokens * k, "int32"), scale, _array(counts, experts, "int32"),
+                                   _array(shares, experts, "float32"), _array(factor, experts, "float32"),
+                                   _array(loss, 1, "float32"), self._stream(stream))
+
+    def balance_backward(self, logits, indices, factor, dlogits, *, dloss=None, accumulate=False, score=GEMM_SCORE_SOFTMAX,
+                         stream=None) -> int:
+        """The balance loss's gradient of the logits into dlogits (accumulate: added to it); dloss: one float32 on the device."""
+        x, tokens, experts, ldl = _matrix(logits)
+        d, lddl = _same_shape(dlogits, tokens, experts, "dlogits")
+        n, k = indices.shape
+        if n != tokens or dlogits.dtype != logits.dtype:
+            raise ValueError("indices is tokens x top_k, dlogits like logits")
+        return load().gemm_balance_backward(self.handle, tokens, experts, x, ldl, _type_of(logits), score, k,
+                                            _array(indices, tokens * k, "int32"), _array(factor, experts, "float32"),
+                                            None if dloss is None else _array(dloss, 1, "float32"), int(bool(accumulate)), d,
+                                            lddl, self._stream(stream))
 
     def route(self, logits, weights, indices, *, bias=None, score=GEMM_SCORE_SOFTMAX, groups=1, top_groups=1,
               group_top=1, renormalize=False, scale=1.0, stream=None) -> int:

@@ -127,8 +127,8 @@ typedef enum {
   GEMM_PATH_TC_TAIL_SPLIT = 8, /* tcgen05 GEMM: whole tiles for the full waves; only the
                                   tiles of the last, partly filled wave are split along K
                                   (section 3.2's tail wave), + reduction of those tiles  */
-  GEMM_PATH_SCALED = 9,        /* 8-bit block-scaled product, whole output tiles         */
-  GEMM_PATH_SCALED_SLICED = 10 /* 8-bit block-scaled product with few rows or few tiles: */
+  GEMM_PATH_SCALED = 9,        /* block-scaled product (8 or 4 bits), whole output tiles */
+  GEMM_PATH_SCALED_SLICED = 10 /* block-scaled product with few rows or few tiles:       */
                                /* K slices on a cluster of CTAs, added on chip           */
 } gemm_path_t;
 
@@ -238,7 +238,9 @@ const char* gemm_status_string(gemm_status_t status);
 typedef enum { GEMM_TYPE_BF16 = 0, GEMM_TYPE_F16 = 1, GEMM_TYPE_F32 = 2,
                GEMM_TYPE_TF32 = 3, /* operands only (ab_type): fp32 words read as TF32 */
                GEMM_TYPE_E4M3 = 4, /* 8-bit, 4 exponent and 3 fraction bits, no infinity, largest 448   */
-               GEMM_TYPE_E5M2 = 5  /* 8-bit, 5 and 2, largest 57344; both: block-scaled products only */ } gemm_type_t;
+               GEMM_TYPE_E5M2 = 5, /* 8-bit, 5 and 2, largest 57344; both: block-scaled products only */
+               GEMM_TYPE_E2M1 = 6  /* 4-bit, 2 and 1, largest 6, no infinity or NaN, two to a byte: gemm_dequantize only
+                                      (the _mx4 calls imply it) */ } gemm_type_t;
 
 /* D <- act(alpha * op(A) @ op(B) + beta * C) with a separate output D: the
  * gemm_run operation where the C that beta scales is read from one matrix and
@@ -285,8 +287,8 @@ gemm_status_t gemm_plan_poll_error(gemm_plan_t plan, void* stream);
  * starting at a negative coordinate), 1 an epilogue store, 2 an epilogue load
  * of the C that beta scales, 3 the in-kernel split-K reduction, 4 the tile
  * reduction kernel, 5 a GEMV kernel, 6 the K == 0 / alpha == 0 kernel, 7 the
- * TF32 operand transpose, 8 an 8-bit product's load or store of D, 9 the
- * quantiser, 10 routing, 11 the weighted sum.  GEMM_ERR_INVALID_ARG on NULL. */
+ * TF32 operand transpose, 8 a block-scaled product's load or store of D, 9 the
+ * quantisers, 10 routing and its balance, 11 the weighted sum, 12 the norm.  GEMM_ERR_INVALID_ARG on NULL. */
 gemm_status_t gemm_plan_last_error_bits(gemm_plan_t plan, int64_t* bits);
 
 /* 1 in the debug build of the library (libdgemm_gb300_debug.so, compiled
@@ -410,8 +412,8 @@ gemm_status_t gemm_gemv_noalloc(int64_t M, int64_t N, int64_t K,
                                 gemm_epilogue_t epilogue, void* stream);
 
 /* ------------------------------------------------------------------------
- * 8-bit products with a scale for each block of 128, and what goes round them:
- * the quantiser, the experts' products, routing and the weighted sum.
+ * Products of 8 and 4 bits with scales for blocks of values, and what goes round them:
+ * the quantisers, the norm, the experts' products, routing and its balance, and the weighted sum.
  *
  * A block-scaled matrix of R rows and K columns is two buffers:
  *   codes   R x K bytes, row-major, rows `ld` bytes apart: GEMM_TYPE_E4M3 or GEMM_TYPE_E5M2
@@ -427,8 +429,9 @@ gemm_status_t gemm_gemv_noalloc(int64_t M, int64_t N, int64_t K,
  *
  * The calls below are asynchronous on `stream` (a cudaStream_t), ordered like
  * gemm_run's, may be captured into a CUDA graph as gemm_run may, and keep no result
- * between calls.  Two of them use plan workspace, which grows as gemm_run's does: gemm_route_map for more than 2,048
- * slots, and products of codes that have to be copied first.  Row counts that depend on the data (counts, starts, pos, rowmap) are
+ * between calls.  Some of them use plan workspace, which grows as gemm_run's does: gemm_route_map for more than 2,048
+ * slots, products of codes that have to be copied first, gemm_norm_backward with dgain, and gemm_balance for more
+ * than 16 tokens.  Row counts that depend on the data (counts, starts, pos, rowmap) are
  * read on the device: no call waits for them.  Errors are those of gemm_run: argument
  * problems come back before anything is launched.  Results are deterministic.
  * ------------------------------------------------------------------------ */
@@ -516,6 +519,95 @@ gemm_status_t gemm_run_grouped_k(gemm_plan_t plan, int64_t groups, int64_t M, in
                                  gemm_type_t b_type, void* D, int64_t ldd, int64_t d_group, gemm_type_t d_type,
                                  float alpha, float beta, gemm_epilogue_t epilogue, void* stream);
 
+/* ---- 4 bits ----
+ * A matrix of 4-bit values (E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) of R rows and K columns is two buffers:
+ *   codes   (K + 1) / 2 bytes a row, rows `ld` bytes apart: column 2i in the low, 2i + 1 in the high four bits of
+ *           byte i.  With odd K the last byte's high four bits must be 0, as gemm_quantize_mx4 leaves them.
+ *   scales  one E8M0 byte for each row and block of 32 columns, in the same tiles as above: 128 rows and four
+ *           blocks (here 128 columns), tile (r / 128, k / 128) at 512 * ((r / 128) * ceil(K / 128) + k / 128), in it row r,
+ *           block c = k / 32 at byte (r % 32) * 16 + (r % 128) / 32 * 4 + c % 4.  gemm_mx4_scale_bytes(R, K) bytes in all;
+ *           bytes of rows and blocks past the matrix are 0 as gemm_quantize_mx4 writes them and must not be 255.
+ * The scale byte 255 is NaN, and so is every value of its block. */
+
+/* Bytes of the packed scales of a rows x cols matrix of 4-bit values (a multiple of 512, at least 512);
+ * -1 if a size is negative or past 2^31 - 1. */
+int64_t gemm_mx4_scale_bytes(int64_t rows, int64_t cols);
+
+/* Quantise X as gemm_quantize does, to 4-bit codes with a scale for each row and block of 32 columns: Q and SQ the
+ * matrix as it stands (rows of (cols + 1) / 2 bytes), QT and SQT the transposed one (rows of (rows + 1) / 2 bytes, blocks
+ * of 32 rows of X); both or neither of a pair, one pair at least.
+ * A scale is the least power of two, 2^-127 at least, with which the block's largest magnitude stays within 6; a code is
+ * the value over the scale, rounded to nearest, ties to the even code.  A block of zeros has the scale byte 0, one
+ * that holds an infinity or NaN the byte 255 and codes of 0.
+ * rowmap, map_div and src_rows, alignment, aliasing and limits as in gemm_quantize. */
+gemm_status_t gemm_quantize_mx4(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx,
+                                gemm_type_t x_type, const int32_t* rowmap, int64_t map_div, int64_t src_rows, void* Q,
+                                int64_t ldq, void* SQ, void* QT, int64_t ldqt, void* SQT, void* stream);
+
+/* X <- the values that a block-scaled matrix stands for: codes Q of q_type (GEMM_TYPE_E4M3 or E5M2 with scales of
+ * gemm_quantize's tiles, GEMM_TYPE_E2M1 with those of 4 bits) times their scales, to GEMM_TYPE_BF16, F16 or F32.  Products with the
+ * scale are exact in fp32 unless they leave its range; one rounding to X's type, which is exact too for bf16 and fp32 while the values
+ * stay within their normal numbers.  The way back from weights kept in 8 or 4 bits to gemm_run's operands.
+ * Q and SQ 16-byte aligned, ldq (bytes) a multiple of 16, X aligned to its element (rows on 16-byte boundaries are
+ * faster); X may share no byte with Q or SQ. */
+gemm_status_t gemm_dequantize(gemm_plan_t plan, int64_t rows, int64_t cols, const void* Q, int64_t ldq, gemm_type_t q_type,
+                              const void* SQ, void* X, int64_t ldx, gemm_type_t x_type, void* stream);
+
+/* D <- act(alpha * A @ B^T + beta * D) with 4-bit A (M x K) and B (N x K): gemm_run_scaled with codes of 4 bits and
+ * scales of blocks of 32; lda and ldb are bytes, >= (K + 1) / 2.  Everything else as there. */
+gemm_status_t gemm_run_mx4(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA,
+                           const void* B, int64_t ldb, const void* SB, void* D, int64_t ldd, gemm_type_t d_type,
+                           float alpha, float beta, gemm_epilogue_t epilogue, void* stream);
+
+/* The argument checks of gemm_run_mx4 without a plan or a device. */
+gemm_status_t gemm_check_mx4(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA, const void* B,
+                             int64_t ldb, const void* SB, const void* D, int64_t ldd, gemm_type_t d_type, float alpha,
+                             float beta, gemm_epilogue_t epilogue);
+
+/* Experts' products with 4-bit rows and weights: gemm_run_grouped with codes of 4 bits and scales of blocks of 32
+ * (lda, ldb and b_group are bytes; a group's scales gemm_mx4_scale_bytes(N, K) after the last one's).
+ * gemm_quantize_mx4 with gemm_route_map's rowmap orders the tokens by expert. */
+gemm_status_t gemm_run_grouped_mx4(gemm_plan_t plan, int64_t groups, int64_t rows, int64_t N, int64_t K,
+                                   const int32_t* starts, const int32_t* counts, const void* A, int64_t lda,
+                                   const void* SA, const void* B, int64_t ldb, int64_t b_group, const void* SB, void* D,
+                                   int64_t ldd, gemm_type_t d_type, float alpha, float beta, gemm_epilogue_t epilogue,
+                                   void* stream);
+
+/* ---- norm ----
+ * Root-mean-square norm of a residual stream, row by row (rows x cols):
+ *   h = X + residual      rstd = 1 / sqrt(mean(h^2) + eps)      y = h * rstd * gain
+ *   residual, H  of h_type, which is X's type or GEMM_TYPE_F32; residual NULL: h = X; H (the stream for the next layer,
+ *                and what the backward pass reads) NULL: not kept
+ *   gain         cols values of g_type, X's type or GEMM_TYPE_F32; NULL: ones
+ *   Y            the result in X's type, NULL: not wanted
+ *   Q, SQ        the result as codes of q_type (GEMM_TYPE_E4M3 or E5M2) with scales for each row and block of 128
+ *                columns, exactly what gemm_quantize makes of the 32-bit result: an operand for gemm_run_scaled
+ *                and gemm_run_grouped; both or neither
+ *   rstd         rows floats, NULL: not wanted
+ * One of H, Y, Q and rstd at least.  Sums, rstd and products are fp32; Y and the codes are rounded once, from the unrounded h (H is
+ * rounded on its own).  A row whose mean square is infinite has rstd 0.
+ * H may be X or the residual themselves (the same address, stride and type), Y too, not both the same; results
+ * share no byte with inputs or each other otherwise.  cols <= 32768.  Everything needs only its element's
+ * alignment (rows and gain on 16-byte boundaries are faster), Q and SQ 16 bytes with ldq a multiple of 16.
+ * eps is finite and not negative. */
+gemm_status_t gemm_norm(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx, gemm_type_t x_type,
+                        const void* residual, int64_t ldr, gemm_type_t h_type, const void* gain, gemm_type_t g_type,
+                        float eps, void* H, int64_t ldh, void* Y, int64_t ldy, gemm_type_t q_type, void* Q, int64_t ldq,
+                        void* SQ, float* rstd, void* stream);
+
+/* Gradients of gemm_norm from dY (rows x cols, x_type), the kept H (h_type) and rstd:
+ *   dX = rstd * (g - xhat * mean(g * xhat)) + dH,  g = dY * gain,  xhat = H * rstd     dgain = sum over rows of dY * xhat
+ * dX (h_type) is the gradient of X and of the residual alike; dH (h_type, NULL: none) is the gradient that reaches h past the
+ * norm.  dgain: cols floats, overwritten (zeros for no rows), NULL: not wanted.
+ * dX may be dY or dH themselves (the same address, stride and type); otherwise results share no byte with inputs
+ * or each other.  Limits and alignment as in gemm_norm. */
+gemm_status_t gemm_norm_backward(gemm_plan_t plan, int64_t rows, int64_t cols, const void* dY, int64_t lddy,
+                                 gemm_type_t x_type, const void* H, int64_t ldh, gemm_type_t h_type, const void* gain,
+                                 gemm_type_t g_type, const float* rstd, const void* dH, int64_t lddh, void* dX, int64_t lddx,
+                                 float* dgain, void* stream);
+
+/* ---- routing ---- */
+
 typedef enum { GEMM_SCORE_SOFTMAX = 0, GEMM_SCORE_SIGMOID = 1 } gemm_score_t;
 
 /* How tokens choose experts. */
@@ -553,6 +645,28 @@ gemm_status_t gemm_route(gemm_plan_t plan, int64_t tokens, int64_t experts, cons
 gemm_status_t gemm_route_backward(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
                                   gemm_type_t l_type, gemm_route_t route, const int32_t* indices,
                                   const float* dweights, void* dlogits, int64_t lddl, void* stream);
+
+/* How evenly a choice (indices, tokens x top_k, gemm_route's or any other's) spreads the tokens over the experts.  With p[t, e] the
+ * softmax of token t's logits, or each expert's sigmoid over the sum of them all; over the m tokens that have an index in [0,
+ * experts) and the n such indices, counts[e] of them expert e's:
+ *   shares[e] = mean over those tokens of p[t, e]      loss = scale * experts * sum over e of counts[e] / n * shares[e]
+ *   factor[e] = scale * experts * counts[e] / (n * m), the derivative of the loss by p[t, e] (the counts have none)
+ * (each `experts` long; loss one float).  An even router's loss is `scale`.  A token whose indices are all outside (padding,
+ * marked with -1) takes no part, nor does one whose logits are all masked add to the shares; without any tokens all
+ * results are 0.  Masked logits as in gemm_route; a token of sigmoids that are all 0 in fp32 adds nothing.
+ * Results may share no byte with each other, the logits or indices.  experts <= 1024, top_k <= 32. */
+gemm_status_t gemm_balance(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
+                           gemm_type_t l_type, gemm_score_t score, int32_t top_k, const int32_t* indices, float scale,
+                           int32_t* counts, float* shares, float* factor, float* loss, void* stream);
+
+/* Gradient of gemm_balance's loss: dlogits (tokens x experts, of the logits' type) <- (accumulate != 0: dlogits +) dloss *
+ * d loss / d logits, from its factor; every entry is written, 0 (or itself) for tokens that take no part.  dloss: device, one
+ * float, NULL for 1.  accumulate adds in fp32 with one rounding, to gemm_route_backward's result for one.  dlogits may be
+ * the logits themselves (the same address and stride) unless it accumulates, and may share no byte with an input otherwise. */
+gemm_status_t gemm_balance_backward(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
+                                    gemm_type_t l_type, gemm_score_t score, int32_t top_k, const int32_t* indices,
+                                    const float* factor, const float* dloss, int32_t accumulate, void* dlogits, int64_t lddl,
+                                    void* stream);
 
 /* Rows that gemm_route_map's order may take: tokens * top_k, and up to 127 empty rows for each expert
  * that has one, rounded up to 128; -1 if a size is out of range. */
