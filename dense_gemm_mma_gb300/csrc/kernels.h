@@ -375,7 +375,7 @@ int scaled_sliced_smem(int bn, int stages, int part_rows);
 int scaled_sliced_clusters(int slices);  // clusters of that many CTAs that can be resident at once, a CTA an SM
 
 // The same for 4-bit operands (E2M1, scales of blocks of 32): maps a and b of bytes, two values each; sa and sb
-// with a row block's scale tiles as their second coordinate and the row block as their third (box two tiles).
+// with a row block's scale tiles as their second coordinate and the row block as their third (box two tiles; sb for a pair: of two row blocks).
 cudaError_t launch_mx4_tile(bool pair, const ScMaps& m, const ScParams& p, int grid, cudaStream_t s);
 int mx4_tile_clusters();
 int mx4_tile_stages(bool pair);

@@ -22,14 +22,14 @@ namespace {
 constexpr int kSmemMax = 232448;  // shared memory of a CTA; an SM holds 1 KB more for each CTA
 
 // 3-D row-major tensor (inner contiguous, ld elements between rows, group elements
-// between groups); boxes of box_inner x box_rows x 1.  Out-of-range reads give zero.
+// between groups); boxes of box_inner x box_rows x box_groups.  Out-of-range reads give zero.
 bool map3(CUtensorMap* m, CUtensorMapDataType t, int64_t esize, const void* ptr, int64_t inner, int64_t rows, int64_t groups,
-          int64_t ld, int64_t group, int box_inner, int box_rows, CUtensorMapSwizzle swizzle) {
+          int64_t ld, int64_t group, int box_inner, int box_rows, CUtensorMapSwizzle swizzle, int box_groups = 1) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(rows), cuuint64_t(groups)};
   cuuint64_t strides[2] = {cuuint64_t(ld * esize), cuuint64_t(group * esize)};
-  cuuint32_t box[3] = {cuuint32_t(box_inner), cuuint32_t(box_rows), 1};
+  cuuint32_t box[3] = {cuuint32_t(box_inner), cuuint32_t(box_rows), cuuint32_t(box_groups)};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, t, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -331,10 +331,10 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
     ok = ok && map3(&m.b, u8, 1, x.B, kbytes, x.N, nb, x.ldb, nb > 1 ? x.b_group : x.ldb * x.N, SC_BK, 128, sw);
     const CUtensorMapDataType u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
     const CUtensorMapSwizzle plain = CU_TENSOR_MAP_SWIZZLE_NONE;
-    if (x.four) {  // tiles along K, row blocks; a box holds a stage's two tiles
+    if (x.four) {  // tiles along K, row blocks; a box holds a stage's two tiles (B, pairs: of two row blocks)
       const int64_t tk = mx4_scale_tiles(1, x.K), ma = std::max<int64_t>(1, ceil_div(x.M, 128));
       ok = ok && map3(&m.sa, u32, 4, x.SA, 128, tk, ma, 128, 128 * tk, 128, 2, plain);
-      ok = ok && map3(&m.sb, u32, 4, x.SB, 128, tk, nb * p.sb_group, 128, 128 * tk, 128, 2, plain);
+      ok = ok && map3(&m.sb, u32, 4, x.SB, 128, tk, nb * p.sb_group, 128, 128 * tk, 128, 2, plain, pair ? 2 : 1);
     } else {
       const int64_t ta_n = scale_tiles(x.M, x.K), tb_n = nb * p.sb_group;
       ok = ok && map3(&m.sa, u32, 4, x.SA, 128, ta_n, 1, 128, 128 * ta_n, 128, 1, plain);

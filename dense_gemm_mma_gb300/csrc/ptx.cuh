@@ -591,6 +591,20 @@ __device__ __forceinline__ void tc_commit_one(uint32_t bar, uint32_t one) {
         : "memory");
 }
 
+// The same with one arrival, on this CTA's barrier (a pair: the leader's, which is the CTA that calls it).
+template <bool PAIR>
+__device__ __forceinline__ void tc_commit_leader(uint32_t bar, uint32_t one) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\tsetp.ne.b32 q, %1, 0;\n\tmov.b16 m, 1;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+            bar),
+        "r"(one)
+        : "memory");
+  else
+    tc_commit_one<false>(bar, one);
+}
+
 // 3-D tiled load global -> shared (x innermost, z outermost), counted in bytes on `bar`: of
 // this CTA, or for a pair of either CTA (cluster address).
 template <bool PAIR>

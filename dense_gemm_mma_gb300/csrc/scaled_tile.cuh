@@ -24,8 +24,9 @@
 // a tile first and only then lets the next tile's MMAs begin.
 //
 // FOUR (4-bit operands): a ring stage is the same 128 bytes of K, 256 values, and four K = 64 MMAs; with a scale for
-// each 32 values every stage has scale tiles of its own, two for 128 rows.  A set of scale columns is then 24
-// columns for a pair, of which two fit behind the accumulators (16 and four on one CTA).
+// each 32 values every stage has scale tiles of its own, two for 128 rows, and a set of scale columns (24 of a pair): the
+// accumulators overlap by 128 columns.
+//  - warp 10 copies the scales, six copies a k-block.
 //
 // What bounds it: 8192^3 into bf16 330 to 360 us, 3.1 to 3.3 PFLOP/s, at the power limit (287 us, 3.8
 // PFLOP/s, with operands whose bits change little).  Short K: the turnover of the tiles, with no unit full.  16 weight
@@ -41,7 +42,11 @@ namespace dg {
 namespace {
 
 constexpr int kEpiWarps = 8;     // two for each quarter of the accumulator's lanes
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kCopyWarp = 2 + kEpiWarps;  // FOUR: copies the scales
+template <bool FOUR>
+__host__ __device__ constexpr int threads() {
+  return 64 + 32 * kEpiWarps + (FOUR ? 32 : 0);
+}
 constexpr int kBox = 32 * 128;  // one 32-row x 128-byte epilogue box
 
 template <bool PAIR, bool FOUR>
@@ -57,19 +62,19 @@ struct Cfg {
   static constexpr int OFF_STG = OFF_B + STAGES * OPERAND;
   static constexpr int OFF_S = OFF_STG + kEpiWarps * kBox;
   static constexpr int OFF_BAR = OFF_S + STAGES * SCALES;
-  // full[S], empty[S], tmem_full[2], tmem_empty[2], drain
-  static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 5) * 8;
+  // full[S], empty[S], tmem_full[2], tmem_empty[2], drain, set_full[4], copy_drain
+  static constexpr int OFF_MISC = (OFF_BAR + (2 * STAGES + 10) * 8 + 15) / 16 * 16;
   static constexpr int OFF_SEG = OFF_MISC + 16;
   static constexpr int OFF_TABLE = OFF_SEG + SC_MAX_GROUPS * 8;
   static constexpr int SMEM = OFF_TABLE + (SC_MAX_GROUPS + 1) * 4 + 1024;  // + slack for 1024-B alignment
   static_assert(SMEM <= 232448, "shared memory budget");
-  static constexpr int OVERLAP = PAIR ? 64 : 0;  // columns that the two accumulators share
+  static constexpr int OVERLAP = !PAIR ? 0 : FOUR ? 128 : 64;  // columns that the two accumulators share
   static constexpr int ACC1 = BN - OVERLAP;      // first column of the second accumulator
-  static constexpr int SF0 = PAIR ? 448 : 256;   // first scale column
-  static constexpr int SET = FOUR ? 4 * TILES * (1 + BN / 128) : 16;  // columns of a set
-  static constexpr int SETS = FOUR && PAIR ? 2 : 4;
+  static constexpr int SF0 = ACC1 + BN;          // first scale column
+  static constexpr int SET = FOUR ? 8 * (1 + BN / 128) : 16;  // columns of a set
+  static constexpr int SETS = 4;
   static constexpr int TMEM_COLS = 512;
-  static_assert(ACC1 + BN <= SF0 && SF0 + SETS * SET <= TMEM_COLS, "tensor memory budget");
+  static_assert(SF0 + SETS * SET <= TMEM_COLS, "tensor memory budget");
   static_assert(SETS < STAGES, "a set's last MMAs are waited for on a stage that has not been used again");
 };
 
@@ -129,7 +134,7 @@ __device__ __forceinline__ void finish(float (&v)[32], const ScParams& p, const 
 }
 
 template <bool PAIR, bool FOUR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads<FOUR>(), 1)
     scaled_tile_kernel(const __grid_constant__ ScMaps maps, const __grid_constant__ ScParams p) {
   using C = Cfg<PAIR, FOUR>;
   constexpr int S = C::STAGES;
@@ -143,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   const uint32_t full0 = base + C::OFF_BAR, empty0 = full0 + 8 * S;
   const uint32_t tfull0 = empty0 + 8 * S, tempty0 = tfull0 + 16, drain_bar = tempty0 + 16;
+  const uint32_t sfull0 = drain_bar + 8, copy_drain_bar = sfull0 + 8 * C::SETS;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sbase + C::OFF_MISC);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sbase + C::OFF_MISC + 4);
   int2* const seg = reinterpret_cast<int2*>(sbase + C::OFF_SEG);
@@ -158,6 +164,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(tempty0 + 8 * b, PAIR ? 2 * kEpiWarps : kEpiWarps);  // both CTAs' epilogues
     }
     mbar_init(drain_bar, 1);
+    if constexpr (FOUR) {
+      for (int b = 0; b < C::SETS; ++b) mbar_init(sfull0 + 8 * b, 1);
+      mbar_init(copy_drain_bar, 1);
+    }
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&maps.a);
@@ -180,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The groups' segments: a unit's own read from global memory queued behind the operand loads in
   // flight, 2,000 to 5,000 cycles before every tile (K groups of 1,024, 16 x 2048 x 2048: 86 us, with the copy and the release below 78.7).
   if (p.group != SC_DENSE) {
-    for (int e = threadIdx.x; e < p.groups; e += kThreads) {
+    for (int e = threadIdx.x; e < p.groups; e += threads<FOUR>()) {
       int start, count;
       sc_segment(p, e, &start, &count);
       seg[e] = make_int2(start, count);
@@ -234,8 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sf = base + C::OFF_S + stage * C::SCALES;
           if constexpr (FOUR) {  // (two tiles each: past K the box reads zero)
             load(sf, &maps.sa, 0, 2 * kb, sa_row, 4);
-#pragma unroll
-            for (int j = 0; j < C::BN / 128; ++j) load(sf + 1024 * (1 + j), &maps.sb, 0, 2 * kb, sb_row + j, 4);
+            load(sf + 1024, &maps.sb, 0, 2 * kb, sb_row, 4);  // (of all the tile's columns)
           } else {
             load(sf, &maps.sa, 0, sa_row + kb / 4, 0, 4);
 #pragma unroll
@@ -288,22 +297,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t next_phase = phase ^ uint32_t(stage + 1 == S);
           ready = mbar_try_wait(full0 + 8 * next_stage, next_phase);
           if constexpr (FOUR) {
-            // The MMAs that read this set last, SETS k-blocks ago, have completed.
-            const int old = it - C::SETS;
-            if (old >= 0 && !sc_wait<SC_OWN>(empty0 + 8 * (old % S), uint32_t(old / S) & 1u, w, WAIT_MMA_FULL)) {
+            const int set = it % C::SETS;
+            if (!sc_wait<SC_OWN>(sfull0 + 8 * set, uint32_t(it / C::SETS) & 1u, w, WAIT_MMA_FULL)) {
               ok = false;
               break;
             }
-            set_col = tmem_base + C::SF0 + C::SET * uint32_t(it % C::SETS);
-            const uint32_t sf = desc_lo(base + C::OFF_S + stage * C::SCALES);
-            // columns: A's two tiles, then B's first tile of each 128 rows, then their second ones
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              tc_copy_scales<PAIR>(set_col + 4 * t, sf + (512 >> 4) * t, one);
-#pragma unroll
-              for (int j = 0; j < C::BN / 128; ++j)
-                tc_copy_scales<PAIR>(set_col + 8 + 4 * (t * (C::BN / 128) + j), sf + (512 >> 4) * (2 * (1 + j) + t), one);
-            }
+            tc_fence_after();
+            set_col = tmem_base + C::SF0 + C::SET * uint32_t(set);
           } else if (kb == x.kb0 || (kb & 3) == 0) {
             const int old = sets.last_user();
             if (old >= 0 && old > it - S &&
@@ -341,14 +341,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++tiles;
       }
       // Every MMA issued by this warp completes before tensor memory is freed.
-      if (one) {
-        if constexpr (PAIR)
-          tc_commit_pair_multicast(drain_bar, 0x1);
-        else
-          tc_commit(drain_bar);
-      }
-      __syncwarp();
+      tc_commit_leader<PAIR>(drain_bar, one);
       sc_wait<SC_OWN>(drain_bar, 0, w, WAIT_DRAIN);
+    }
+  } else if (FOUR && warp == kCopyWarp) {
+    // ---------------------------------------------------- copy of the scales
+    if (leader) {
+      int stage = 0, it = 0, cursor = 0, old_stage = 0;
+      uint32_t phase = 0, old_phase = 0;
+      bool ok = true;
+      for (int u = unit0; u < units && ok; u += step) {
+        const ScUnit x = sc_unit(p, u, C::TILE_M, C::BN, seg, table, &cursor);
+        for (int kb = x.kb0; kb < x.kb1; ++kb, ++it) {
+          // The stage has landed, and the MMAs that read this set last, SETS k-blocks ago, have completed.
+          if (!sc_wait<SC_OWN>(full0 + 8 * stage, phase, w, WAIT_MMA_FULL) ||
+              (it >= C::SETS && !sc_wait<SC_OWN>(empty0 + 8 * old_stage, old_phase, w, WAIT_MMA_FULL))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t set_col = tmem_base + C::SF0 + C::SET * uint32_t(it % C::SETS);
+          const uint32_t sf = desc_lo(base + C::OFF_S + stage * C::SCALES);
+          // columns: A's two tiles, then B's first tile of each 128 rows, then their second ones
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            tc_copy_scales<PAIR>(set_col + 4 * t, sf + (512 >> 4) * t, one);
+#pragma unroll
+            for (int j = 0; j < C::BN / 128; ++j)
+              tc_copy_scales<PAIR>(set_col + 8 + 4 * (t * (C::BN / 128) + j), sf + (512 >> 4) * (2 * (1 + j) + t), one);
+          }
+          tc_commit_leader<PAIR>(sfull0 + 8 * (it % C::SETS), one);
+          if (it >= C::SETS && ++old_stage == S) {
+            old_stage = 0;
+            old_phase ^= 1u;
+          }
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Every copy completes before tensor memory is freed.
+      tc_commit_leader<PAIR>(copy_drain_bar, one);
+      sc_wait<SC_OWN>(copy_drain_bar, 0, w, WAIT_DRAIN);
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -494,14 +529,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         load(ra, 0);
+        load(rb, 1);
 #pragma unroll
         for (int s = 0; s < kSteps; s += 2) {
           loaded(ra, s);
-          load(rb, s + 1);
-          process(ra, s, true, es == 4);
           loaded(rb, s + 1);
+          process(ra, s, true, es == 4);
           if (s + 2 < kSteps) load(ra, s + 2);
           process(rb, s + 1, es == 4, true);
+          if (s + 2 < kSteps) load(rb, s + 3);
         }
       }
     };
@@ -550,7 +586,7 @@ cudaError_t launch(const ScMaps& m, const ScParams& p, int grid, cudaStream_t s)
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads<FOUR>());
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -579,7 +615,7 @@ int resident_pairs() {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<true, FOUR>::SMEM) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads<FOUR>());
   cfg.dynamicSmemBytes = Cfg<true, FOUR>::SMEM;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
