@@ -26,15 +26,12 @@ __host__ __device__ constexpr int balance_warps() {
   return P <= 8 ? 32 : 16;
 }
 
-// Does the token have a choice?  A lane's own is `expert`, -1 for none.
-__device__ __forceinline__ bool has_choice(const BalanceArgs& a, int t, int lane, int* expert) {
-  *expert = -1;
-  if (lane < a.top_k) {
-    const int* const at = a.indices + int64_t(t) * a.top_k + lane;
-    const int e = DG_IN(a.dbg, at, 4, DBG_ROUTE) ? __ldg(at) : -1;
-    if (e >= 0 && e < a.experts) *expert = e;
-  }
-  return __any_sync(kAll, *expert >= 0);
+// The lane's choice of the token's, -1 for none.
+__device__ __forceinline__ int choice(const BalanceArgs& a, int t, int lane) {
+  if (lane >= a.top_k) return -1;
+  const int* const at = a.indices + int64_t(t) * a.top_k + lane;
+  const int e = DG_IN(a.dbg, at, 4, DBG_ROUTE) ? __ldg(at) : -1;
+  return e >= 0 && e < a.experts ? e : -1;
 }
 
 // A lane's experts' shares of a token, from its logits.  One whose scores are all 0 gives none.
@@ -71,7 +68,9 @@ __device__ __forceinline__ float block_sum(float v, float* sums) {
 template <int P>
 __global__ void __launch_bounds__(32 * balance_warps<P>(), 1) balance_kernel(const BalanceArgs a) {
   constexpr int W = balance_warps<P>(), E = 32 * P;
-  __shared__ float total[kBuffers][E];
+  constexpr int ROOM = E > 1024 / kBuffers ? kBuffers * E : 1024;
+  __shared__ float room[ROOM];
+  float(*const total)[E] = reinterpret_cast<float(*)[E]>(room);
   __shared__ int count[E];
   __shared__ int tokens;
   __shared__ float sums[W];
@@ -86,16 +85,27 @@ __global__ void __launch_bounds__(32 * balance_warps<P>(), 1) balance_kernel(con
   if (threadIdx.x == 0) tokens = 0;
   __syncthreads();
   wait_prior_grid();
-  float acc[P];
+  // the next token's logits and choice are under way while a warp works on one (16 experts a lane and more: no registers)
+  constexpr int AHEAD = P <= 8 ? 1 : 0;
+  const int64_t step = int64_t(gridDim.x) * W;
+  float acc[P], next[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) acc[i] = 0.f;
-  int mine = 0;
-  for (int64_t t64 = int64_t(blockIdx.x) * W + warp; t64 < a.tokens; t64 += int64_t(gridDim.x) * W) {
-    const int t = int(t64);
+  int mine = 0, chosen = -1;
+  auto load = [&](int64_t t) {
+    load_logits(a, int(t), first, run, a.wide, next);
+    chosen = choice(a, int(t), lane);
+  };
+  const int64_t t0 = int64_t(blockIdx.x) * W + warp;
+  if (AHEAD && t0 < a.tokens) load(t0);
+  for (int64_t t = t0; t < a.tokens; t += step) {
     float x[P], p[P];
-    load_logits(a, t, first, run, a.wide, x);
-    int expert;
-    const bool live = has_choice(a, t, lane, &expert);
+    if (!AHEAD) load(t);
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = next[i];
+    const int expert = chosen;
+    if (AHEAD && t + step < a.tokens) load(t + step);
+    const bool live = __any_sync(kAll, expert >= 0);
     if (expert >= 0) atomicAdd(count + expert, 1);
     float top = kNegInf;
 #pragma unroll
@@ -116,6 +126,7 @@ __global__ void __launch_bounds__(32 * balance_warps<P>(), 1) balance_kernel(con
   }
   auto cta_sum = [&](int e) { return (total[0][e] + total[1][e]) + (total[2][e] + total[3][e]); };
   const bool alone = gridDim.x == 1;
+  int sum_lots = kBuffers, lot_stride = E;  // where the sums' lots are
   if (!alone) {
     float* const part = a.parts + int64_t(blockIdx.x) * a.experts;
     for (int e = threadIdx.x; e < a.experts; e += 32 * W) {
@@ -129,21 +140,20 @@ __global__ void __launch_bounds__(32 * balance_warps<P>(), 1) balance_kernel(con
     __syncthreads();
     if (ticket != gridDim.x - 1) return;
     __threadfence();
-    // the parts, four experts a thread, every `lots`th CTA's to a lot; the lots in their order
-    for (int e = threadIdx.x; e < E; e += 32 * W)
-#pragma unroll
-      for (int b = 0; b < kBuffers; ++b) total[b][e] = 0.f;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kBuffers * a.experts; i += 32 * W) {
+    // the parts: `lots` threads an expert, every lots-th CTA's to a lot; then the lots in their order
+    const int lots = max(kBuffers, min(32, ROOM / a.experts));
+    for (int i = threadIdx.x; i < lots * a.experts; i += 32 * W) {
       const int e = i % a.experts, lot = i / a.experts;
       float s = 0.f;
-#pragma unroll 8
-      for (int c = lot; c < int(gridDim.x); c += kBuffers) {
+#pragma unroll 16
+      for (int c = lot; c < int(gridDim.x); c += lots) {
         const float* const at = a.parts + int64_t(c) * a.experts + e;
         s += DG_IN(a.dbg, at, 4, DBG_ROUTE) ? __ldcg(at) : 0.f;
       }
-      total[lot][e] = s;
+      room[i] = s;
     }
+    sum_lots = lots;
+    lot_stride = a.experts;
     for (int e = threadIdx.x; e < a.experts; e += 32 * W) {
       if (!DG_IN(a.dbg, a.counters + 2 + e, 4, DBG_ROUTE)) continue;
       count[e] = int(__ldcg(a.counters + 2 + e));
@@ -167,7 +177,9 @@ __global__ void __launch_bounds__(32 * balance_warps<P>(), 1) balance_kernel(con
   const float m = float(max(tokens, 1)), all = float(max(n, 1)), by = a.scale * float(a.experts);
   float loss = 0.f;
   for (int e = threadIdx.x; e < a.experts; e += 32 * W) {
-    const float share = cta_sum(e) / m, part = by * (float(count[e]) / all);
+    float sum = 0.f;
+    for (int l = 0; l < sum_lots; ++l) sum += room[l * lot_stride + e];
+    const float share = sum / m, part = by * (float(count[e]) / all);
     loss += part * share;
     if (DG_IN(a.dbg, a.counts + e, 4, DBG_ROUTE)) a.counts[e] = count[e];
     if (DG_IN(a.dbg, a.shares + e, 4, DBG_ROUTE)) a.shares[e] = share;
@@ -188,20 +200,36 @@ __global__ void __launch_bounds__(128) balance_backward_kernel(const BalanceArgs
   const int run = (a.experts + 31) / 32, first = lane * run;
   float x[P], p[P], f[P], old[P];
   load_logits(a, t, first, run, a.wide, x);
-  int expert;
-  const bool live = has_choice(a, t, lane, &expert);
+  const bool live = __any_sync(kAll, choice(a, t, lane) >= 0);
   const float dloss = a.dloss == nullptr ? 1.f : DG_IN(a.dbg, a.dloss, 4, DBG_ROUTE) ? __ldg(a.dloss) : 0.f;
   const int es = a.kind == OUT_F32 ? 4 : 2;
   char* const dst = static_cast<char*>(a.dlogits) + (int64_t(t) * a.lddl + first) * es;
   const bool whole = P >= 4 && a.wide_out && run == P && first + P <= a.experts;
   auto have = [&](int i) { return i < run && first + i < a.experts; };
+  bool by_four = false;
+  if constexpr (P >= 4) {
+    by_four = whole && (reinterpret_cast<uintptr_t>(a.factor) & 15) == 0 && DG_IN(a.dbg, a.factor + first, 4 * P, DBG_ROUTE);
+    if (by_four) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    f[i] = have(i) && DG_IN(a.dbg, a.factor + first + i, 4, DBG_ROUTE) ? __ldg(a.factor + first + i) : 0.f;
-    old[i] = 0.f;
-    if (a.accumulate && have(i) && DG_IN(a.dbg, dst + i * es, es, DBG_ROUTE))
-      old[i] = es == 4 ? *reinterpret_cast<const float*>(dst + 4 * i)
-                       : half_at(*reinterpret_cast<const uint16_t*>(dst + 2 * i), 0, a.kind);
+      for (int i = 0; i < P; i += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(a.factor + first + i));
+        f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+      }
+    }
+  }
+  if (!by_four) {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      f[i] = have(i) && DG_IN(a.dbg, a.factor + first + i, 4, DBG_ROUTE) ? __ldg(a.factor + first + i) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) old[i] = 0.f;
+  if (a.accumulate) {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (have(i) && DG_IN(a.dbg, dst + i * es, es, DBG_ROUTE))
+        old[i] = es == 4 ? *reinterpret_cast<const float*>(dst + 4 * i)
+                         : half_at(*reinterpret_cast<const uint16_t*>(dst + 2 * i), 0, a.kind);
   }
   float top = kNegInf, reference = 0.f;
 #pragma unroll

@@ -420,7 +420,7 @@ struct QuantArgs {
 cudaError_t launch_quantize(const QuantArgs& a, cudaStream_t s);
 
 // The same into 4 bits (E2M1, a scale for each row and block of 32): cols values are (cols + 1) / 2 bytes;
-// block_rows, e5m2, rows_padded and cols_padded are not used, q_groups and qt_groups count blocks in fours as above.
+// block_rows, e5m2 and cols_padded are not used, q_groups and qt_groups count blocks in fours as above.
 cudaError_t launch_quantize_mx4(const QuantArgs& a, cudaStream_t s);
 
 enum CodeKind : int { CODE_E4M3 = 0, CODE_E5M2 = 1, CODE_E2M1 = 2 };
@@ -437,10 +437,11 @@ struct DequantArgs {
   int64_t ldx;
   int x_kind;
   int wide;      // rows of X on 16-byte boundaries
+  int step_rows, step_pieces;  // 256 pieces further on (set by the launcher)
   int pdl;
   DG_DEBUG_FIELD
 };
-cudaError_t launch_dequantize(const DequantArgs& a, cudaStream_t s);
+cudaError_t launch_dequantize(DequantArgs a, cudaStream_t s);
 
 // -------------------------------------------------------------------- norm
 
@@ -470,7 +471,7 @@ struct NormArgs {
   int pdl;
   DG_DEBUG_FIELD
 };
-cudaError_t launch_norm(NormArgs a, cudaStream_t s);
+cudaError_t launch_norm(NormArgs a, int sms, cudaStream_t s);
 
 struct NormBackArgs {
   int rows, cols;

@@ -18,6 +18,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "codes.cuh"
@@ -182,82 +183,102 @@ __device__ __forceinline__ uint2 block_codes(const float (&y)[8], uint32_t* byte
   return make_uint2(codes4<E5M2, false>(y[0], y[1], y[2], y[3], inv), codes4<E5M2, false>(y[4], y[5], y[6], y[7], inv));
 }
 
-// A CTA takes a.per rows, a.warps warps to a row, G groups of 512 columns to a warp.
+// A row's values as they are loaded, a lane's part of it: x and r, or dy, h and dh.
+template <typename TA, typename TB, int G, bool THREE>
+struct RowOf {
+  Eight<TA> a[2 * G];
+  Eight<TB> b[2 * G], c[THREE ? 2 * G : 1];
+};
+
+// First column of a lane's i-th eight.
+__device__ __forceinline__ int column_of(int i, int mine, int warps) {
+  return (mine + i / 2 * warps) * 512 + (i & 1) * 256 + int(threadIdx.x & 31) * 8;
+}
+
+// A CTA takes a.per rows at a time, a.warps warps to a row, G groups of 512 columns to a warp; with one group the
+// next rows' loads are under way while it works on one (more leave no registers for that).
 template <typename TX, typename TH, int G, bool WIDE>
-__global__ void __launch_bounds__(512) norm_kernel(const NormArgs a) {
-  __shared__ float sums[16];
+__global__ void __launch_bounds__(512, G == 1 && sizeof(TX) == 2 && sizeof(TH) == 2 ? 2 : 1) norm_kernel(const NormArgs a) {
+  __shared__ float sums[2][16];
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int slot = warp / a.warps, mine = warp - slot * a.warps;
-  const int row = int(blockIdx.x) * a.per + slot;  // past the matrix: only scale bytes, zero
-  const bool live = row < a.rows;
-  const TX* const x = static_cast<const TX*>(a.x) + int64_t(row) * a.ldx;
-  const TH* const r = a.r ? static_cast<const TH*>(a.r) + int64_t(row) * a.ldr : nullptr;
-  Eight<TX> xv[2 * G];
-  Eight<TH> rv[2 * G];
-  float v[2 * G][8], gain[G < 4 ? 2 * G : 1][8];
-#pragma unroll
-  for (int i = 0; i < 2 * G; ++i) {
-    const int col = (mine + i / 2 * a.warps) * 512 + (i & 1) * 256 + lane * 8;
-    const int left = live ? a.cols - col : 0;
-    load8<WIDE>(a, xv[i], x + col, left, DBG_NORM);
-    if (r)
-      load8<WIDE>(a, rv[i], r + col, left, DBG_NORM);
-    else
-      rv[i].clear();
-  }
   const bool scaled = a.y || a.q;
+  const int rows = a.q ? a.rows_padded : a.rows, step = int(gridDim.x) * a.per;
+  auto load = [&](RowOf<TX, TH, G, false>& v, int64_t row) {
+    const bool live = row < a.rows;
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) {
+      const int col = column_of(i, mine, a.warps), left = live ? a.cols - col : 0;
+      load8<WIDE>(a, v.a[i], static_cast<const TX*>(a.x) + row * a.ldx + col, left, DBG_NORM);
+      if (a.r)
+        load8<WIDE>(a, v.b[i], static_cast<const TH*>(a.r) + row * a.ldr + col, left, DBG_NORM);
+      else
+        v.b[i].clear();
+    }
+  };
+  RowOf<TX, TH, G, false> next;
+  if constexpr (G == 1) load(next, int64_t(blockIdx.x) * a.per + slot);
+  float gain[G < 4 ? 2 * G : 1][8];
   if constexpr (G < 4) {  // (four groups of it leave no registers for the rest)
 #pragma unroll
     for (int i = 0; i < 2 * G; ++i) {
-      const int col = (mine + i / 2 * a.warps) * 512 + (i & 1) * 256 + lane * 8;
-      load_gain<WIDE, TX>(a, gain[i], col, live && scaled ? a.cols - col : 0);
+      const int col = column_of(i, mine, a.warps);
+      load_gain<WIDE, TX>(a, gain[i], col, scaled ? a.cols - col : 0);
     }
   }
-  float sum = 0.f;
+  int turn = 0;
+  for (int64_t row0 = int64_t(blockIdx.x) * a.per; row0 < rows; row0 += step, turn ^= 1) {
+    const int64_t row = row0 + slot;  // past the matrix: only scale bytes, zero
+    const bool live = row < a.rows;
+    if constexpr (G > 1) load(next, row);
+    float v[2 * G][8], sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 2 * G; ++i)
+    for (int i = 0; i < 2 * G; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[i][j] = xv[i].at(j) + rv[i].at(j);
-      sum = fmaf(v[i][j], v[i][j], sum);
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] = next.a[i].at(j) + next.b[i].at(j);
+        sum = fmaf(v[i][j], v[i][j], sum);
+      }
+    if constexpr (G == 1) {
+      if (row0 + step < rows) load(next, row + step);
     }
-  sum = row_sum(sum, sums, slot * a.warps, a.warps);
-  const float rho = __frsqrt_rn(__fdiv_rn(sum, float(a.cols)) + a.eps);
-  if (live && a.rstd && mine == 0 && lane == 0 && DG_IN(a.dbg, a.rstd + row, 4, DBG_NORM)) a.rstd[row] = rho;
-  uint32_t word = 0;
+    sum = row_sum(sum, sums[turn], slot * a.warps, a.warps);
+    const float rho = __frsqrt_rn(__fdiv_rn(sum, float(a.cols)) + a.eps);
+    if (live && a.rstd && mine == 0 && lane == 0 && DG_IN(a.dbg, a.rstd + row, 4, DBG_NORM)) a.rstd[row] = rho;
+    uint32_t word = 0;
 #pragma unroll
-  for (int i = 0; i < 2 * G; ++i) {
-    const int group = mine + i / 2 * a.warps;
-    const int col = group * 512 + (i & 1) * 256 + lane * 8;
-    const int left = live ? a.cols - col : 0;
-    if (a.h) store8<WIDE>(a, static_cast<TH*>(a.h) + int64_t(row) * a.ldh + col, v[i], left, DBG_NORM);
-    if (!scaled) continue;
-    if constexpr (G == 4) load_gain<WIDE, TX>(a, gain[0], col, left);
+    for (int i = 0; i < 2 * G; ++i) {
+      const int col = column_of(i, mine, a.warps), group = col >> 9;
+      const int left = live ? a.cols - col : 0;
+      if (a.h) store8<WIDE>(a, static_cast<TH*>(a.h) + row * a.ldh + col, v[i], left, DBG_NORM);
+      if (!scaled) continue;
+      if constexpr (G == 4) load_gain<WIDE, TX>(a, gain[0], col, left);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rho * gain[G < 4 ? i : 0][j];
-    if (a.y) store8<WIDE>(a, static_cast<TX*>(a.y) + int64_t(row) * a.ldy + col, v[i], left, DBG_NORM);
-    if (a.q) {
-      // (a row past the matrix is zero throughout, unless rho is infinite)
-      if (left < 8) {
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rho * gain[G < 4 ? i : 0][j];
+      if (a.y) store8<WIDE>(a, static_cast<TX*>(a.y) + row * a.ldy + col, v[i], left, DBG_NORM);
+      if (a.q) {
+        // (what is not there is zero, unless rho is infinite)
+        if (left < 8) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j >= left) v[i][j] = 0.f;
-      }
-      uint32_t byte;
-      const uint2 c = a.e5m2 ? block_codes<true>(v[i], &byte) : block_codes<false>(v[i], &byte);
-      uint8_t* const dst = a.q + int64_t(row) * a.ldq + col;
-      if (left >= 8) {
-        if (DG_IN(a.dbg, dst, 8, DBG_NORM)) *reinterpret_cast<uint2*>(dst) = c;
-      } else if (left > 0 && DG_IN(a.dbg, dst, left, DBG_NORM)) {
-        for (int j = 0; j < left; ++j) dst[j] = uint8_t((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
-      }
-      // bytes of blocks 2 (i & 1) and 2 (i & 1) + 1 of the group, in lanes 0 and 16
-      const uint32_t other = __shfl_down_sync(kAll, byte, 16);
-      word = (i & 1 ? word : 0u) | (byte | other << 8) << (16 * (i & 1));
-      if ((i & 1) && lane == 0 && group < a.q_groups && row < a.rows_padded) {
-        uint8_t* const s = a.sq + scale_at(row, int64_t(group) * 4, a.q_groups);
-        if (DG_IN(a.dbg, s, 4, DBG_NORM)) *reinterpret_cast<uint32_t*>(s) = word;
+          for (int j = 0; j < 8; ++j)
+            if (j >= left) v[i][j] = 0.f;
+        }
+        uint32_t byte;
+        const uint2 c = a.e5m2 ? block_codes<true>(v[i], &byte) : block_codes<false>(v[i], &byte);
+        uint8_t* const dst = a.q + row * a.ldq + col;
+        if (left >= 8) {
+          if (DG_IN(a.dbg, dst, 8, DBG_NORM)) *reinterpret_cast<uint2*>(dst) = c;
+        } else if (left > 0 && DG_IN(a.dbg, dst, left, DBG_NORM)) {
+          for (int j = 0; j < left; ++j) dst[j] = uint8_t((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
+        }
+        // bytes of blocks 2 (i & 1) and 2 (i & 1) + 1 of the group, in lanes 0 and 16
+        const uint32_t other = __shfl_down_sync(kAll, byte, 16);
+        word = (i & 1 ? word : 0u) | (byte | other << 8) << (16 * (i & 1));
+        if ((i & 1) && lane == 0 && group < a.q_groups && row < a.rows_padded) {
+          uint8_t* const s = a.sq + scale_at(row, int64_t(group) * 4, a.q_groups);
+          if (DG_IN(a.dbg, s, 4, DBG_NORM)) *reinterpret_cast<uint32_t*>(s) = word;
+        }
       }
     }
   }
@@ -269,52 +290,64 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int slot = warp / a.warps, mine = warp - slot * a.warps;
-  float gain[2 * G][8], acc[2 * G][8];
+  const int step = int(gridDim.x) * a.per;
+  auto load = [&](RowOf<TX, TH, G, true>& v, float* rho, int64_t row) {
+    const bool live = row < a.rows;
+    *rho = live && DG_IN(a.dbg, a.rstd + row, 4, DBG_NORM) ? __ldg(a.rstd + row) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) {
+      const int col = column_of(i, mine, a.warps), left = live ? a.cols - col : 0;
+      load8<WIDE>(a, v.a[i], static_cast<const TX*>(a.dy) + row * a.lddy + col, left, DBG_NORM);
+      load8<WIDE>(a, v.b[i], static_cast<const TH*>(a.h) + row * a.ldh + col, left, DBG_NORM);
+      if (a.dh)
+        load8<WIDE>(a, v.c[i], static_cast<const TH*>(a.dh) + row * a.lddh + col, left, DBG_NORM);
+      else
+        v.c[i].clear();
+    }
+  };
+  RowOf<TX, TH, G, true> now, next;
+  float rho = 0.f, rho_next = 0.f;
+  if constexpr (G == 1) load(next, &rho_next, int64_t(blockIdx.x) * a.per + slot);
+  float gain[G < 4 ? 2 * G : 1][8], acc[2 * G][8];
 #pragma unroll
   for (int i = 0; i < 2 * G; ++i) {
-    const int col = (mine + i / 2 * a.warps) * 512 + (i & 1) * 256 + lane * 8;
-    load_gain<WIDE, TX>(a, gain[i], col, a.cols - col);
+    const int col = column_of(i, mine, a.warps);
+    if constexpr (G < 4) load_gain<WIDE, TX>(a, gain[i], col, a.cols - col);
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
   }
-  const int step = int(gridDim.x) * a.per;
   int turn = 0;
   for (int64_t row0 = int64_t(blockIdx.x) * a.per; row0 < a.rows; row0 += step, turn ^= 1) {
     const int64_t row = row0 + slot;
     const bool live = row < a.rows;
-    Eight<TX> dy[2 * G];
-    Eight<TH> h[2 * G], dh[2 * G];
-    float rho = 0.f;
-    if (live && DG_IN(a.dbg, a.rstd + row, 4, DBG_NORM)) rho = __ldg(a.rstd + row);
-#pragma unroll
-    for (int i = 0; i < 2 * G; ++i) {
-      const int col = (mine + i / 2 * a.warps) * 512 + (i & 1) * 256 + lane * 8;
-      const int left = live ? a.cols - col : 0;
-      load8<WIDE>(a, dy[i], static_cast<const TX*>(a.dy) + row * a.lddy + col, left, DBG_NORM);
-      load8<WIDE>(a, h[i], static_cast<const TH*>(a.h) + row * a.ldh + col, left, DBG_NORM);
-      if (a.dh)
-        load8<WIDE>(a, dh[i], static_cast<const TH*>(a.dh) + row * a.lddh + col, left, DBG_NORM);
-      else
-        dh[i].clear();
+    if constexpr (G == 1) {
+      now = next;
+      rho = rho_next;
+      if (row0 + step < a.rows) load(next, &rho_next, row + step);
+    } else {
+      load(now, &rho, row);
     }
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2 * G; ++i)
+    for (int i = 0; i < 2 * G; ++i) {
+      if constexpr (G == 4) load_gain<WIDE, TX>(a, gain[0], column_of(i, mine, a.warps), a.cols - column_of(i, mine, a.warps));
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float xhat = h[i].at(j) * rho, d = dy[i].at(j);
+        const float xhat = now.b[i].at(j) * rho, d = now.a[i].at(j);
         acc[i][j] = fmaf(d, xhat, acc[i][j]);
-        sum = fmaf(d * gain[i][j], xhat, sum);
+        sum = fmaf(d * gain[G < 4 ? i : 0][j], xhat, sum);
       }
+    }
     sum = row_sum(sum, sums[turn], slot * a.warps, a.warps);
     const float mean = __fdiv_rn(sum, float(a.cols));
 #pragma unroll
     for (int i = 0; i < 2 * G; ++i) {
-      const int col = (mine + i / 2 * a.warps) * 512 + (i & 1) * 256 + lane * 8;
+      const int col = column_of(i, mine, a.warps);
+      if constexpr (G == 4) load_gain<WIDE, TX>(a, gain[0], col, a.cols - col);
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        v[j] = fmaf(rho, fmaf(-h[i].at(j) * rho, mean, dy[i].at(j) * gain[i][j]), dh[i].at(j));
+        v[j] = fmaf(rho, fmaf(-now.b[i].at(j) * rho, mean, now.a[i].at(j) * gain[G < 4 ? i : 0][j]), now.c[i].at(j));
       store8<WIDE>(a, static_cast<TH*>(a.dx) + row * a.lddx + col, v, live ? a.cols - col : 0, DBG_NORM);
     }
   }
@@ -322,7 +355,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a
   float* const part = a.parts + (int64_t(blockIdx.x) * a.per + slot) * a.part_cols;
 #pragma unroll
   for (int i = 0; i < 2 * G; ++i) {
-    const int col = (mine + i / 2 * a.warps) * 512 + (i & 1) * 256 + lane * 8;
+    const int col = column_of(i, mine, a.warps);
     if (col < a.part_cols) store8<true>(a, part + col, acc[i], 8, DBG_NORM);
   }
 }
@@ -335,11 +368,13 @@ __global__ void __launch_bounds__(1024) norm_gain_kernel(const NormBackArgs a, i
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = int(blockIdx.x) * 32 + lane;
   float s = 0.f;
-  if (col < a.cols)
+  if (col < a.cols) {
+#pragma unroll 8
     for (int p = warp; p < parts; p += 32) {
       const float* const at = a.parts + int64_t(p) * a.part_cols + col;
-      if (DG_IN(a.dbg, at, 4, DBG_NORM)) s += __ldcg(at);
+      s += DG_IN(a.dbg, at, 4, DBG_NORM) ? __ldcg(at) : 0.f;
     }
+  }
   sums[warp][lane] = s;
   __syncthreads();
   if (warp > 0 || col >= a.cols) return;
@@ -360,6 +395,22 @@ Shape shape_of(int cols, int most_warps, int64_t rows) {
   s.warps = (groups + s.g - 1) / s.g;
   s.per = int(std::max<int64_t>(1, std::min<int64_t>(4 / s.warps, rows)));
   return s;
+}
+
+// CTAs of the forward kernel that an SM holds at once, looked up once for each number of warps.
+template <typename TX, typename TH, int G, bool WIDE>
+int norm_ctas(int threads) {
+  static std::atomic<int> known[17];
+  std::atomic<int>& k = known[threads / 32];
+  int n = k.load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_kernel<TX, TH, G, WIDE>, threads, 0) != cudaSuccess) {
+    cudaGetLastError();
+    n = 1;
+  }
+  n = std::max(1, n);
+  k.store(n, std::memory_order_relaxed);
+  return n;
 }
 
 template <typename F>
@@ -384,15 +435,17 @@ cudaError_t by_groups(int g, bool wide, F f) {
 
 }  // namespace
 
-cudaError_t launch_norm(NormArgs a, cudaStream_t s) {
+cudaError_t launch_norm(NormArgs a, int sms, cudaStream_t s) {
   const int64_t rows = a.q ? a.rows_padded : a.rows;
   const Shape sh = shape_of(a.cols, 16, rows);
   a.warps = sh.warps;
   a.per = sh.per;
   return by_types(a.x_kind, a.h_kind, [&](auto x, auto h) {
     return by_groups(sh.g, a.wide != 0, [&](auto g, auto w) {
-      return launch_k(norm_kernel<decltype(x), decltype(h), decltype(g)::value, decltype(w)::value>,
-                      dim3(unsigned((rows + sh.per - 1) / sh.per)), dim3(unsigned(32 * sh.warps * sh.per)), 0, s, a.pdl, a);
+      const int64_t fit =
+          int64_t(sms) * norm_ctas<decltype(x), decltype(h), decltype(g)::value, decltype(w)::value>(32 * sh.warps * sh.per);
+      return launch_k(norm_kernel<decltype(x), decltype(h), decltype(g)::value, decltype(w)::value>, dim3(unsigned(std::min((rows + sh.per - 1) / sh.per, fit))), dim3(unsigned(32 * sh.warps * sh.per)),
+                      0, s, a.pdl, a);
     });
   });
 }

@@ -91,7 +91,7 @@ gemm_status_t gemm_norm(gemm_plan_t plan, int64_t rows, int64_t cols, const void
               .bytes(gain, gain ? cols * ge : 0).matrix(H, H ? rows : 0, cols, ldh, he).out_matrix(Y, Y ? rows : 0, cols, ldy, xe)
               .matrix(Q, Q ? rows : 0, cols, ldq, 1).bytes(SQ, sq).bytes(rstd, rstd ? rows * 4 : 0).s;
 #endif
-  return call.done(launched(launch_norm(a, static_cast<cudaStream_t>(stream))));
+  return call.done(launched(launch_norm(a, plan->sms, static_cast<cudaStream_t>(stream))));
 }
 
 gemm_status_t gemm_norm_backward(gemm_plan_t plan, int64_t rows, int64_t cols, const void* dY, int64_t lddy,

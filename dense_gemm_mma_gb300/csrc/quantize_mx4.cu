@@ -6,9 +6,9 @@
 // Multiplying by 2^-e is exact, so a code is one rounding (to nearest, ties to the even code) away from its value.
 // E2M1 has neither infinities nor NaN: a block that holds any has the scale byte 255, which is NaN, and codes of 0.
 //
-// A CTA takes 128 x 128 values, which is one scale tile (128 rows x 4 blocks) in either orientation.  A half warp
-// holds 128 columns of a row, a lane eight neighbouring columns of four neighbouring rows: a row's block is four
-// lanes (two exchanges), a column's block 32 rows of four warps (through shared memory).
+// One orientation: warps take rows, no barrier.  Both: a CTA takes 128 x 128 values, which is one scale tile (128 rows x
+// 4 blocks) in either orientation; half a warp holds 128 columns of a row, a lane eight neighbouring columns of four
+// neighbouring rows.  A row's block is four lanes (two exchanges), a column's block 32 rows of four warps (through shared memory).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
@@ -23,13 +23,6 @@ namespace {
 
 constexpr int kWarps = 16;   // 8 rows each
 constexpr int kLaneRows = 4;  // rows of a lane
-
-template <typename T>
-__device__ __forceinline__ float to_f(T v) {
-  if constexpr (sizeof(T) == 4) return v;
-  else if constexpr (std::is_same<T, __half>::value) return __half2float(v);
-  else return __bfloat162float(v);
-}
 
 // Scale byte (e + 127) of a block whose largest magnitude has the bits m (infinities and NaN: kInf and more).
 __device__ __forceinline__ uint32_t mx4_byte(uint32_t m) {
@@ -46,87 +39,180 @@ __device__ __forceinline__ uint32_t mx4_codes2(float a, float b, float inv) {
   return __nv_cvt_float2_to_fp4x2(make_float2(a * inv, b * inv), __NV_E2M1, cudaRoundNearest);
 }
 
-// Eight neighbouring values, as fp32.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_row(const QuantArgs& a, int src, int col, float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = 0.f;
-  if (src < 0 || col >= a.cols) return;
-  const T* const p = static_cast<const T*>(a.x) + int64_t(src) * a.ldx + col;
-  if (VEC && col + 8 <= a.cols) {
-    if (!DG_IN(a.dbg, p, 8 * int(sizeof(T)), DBG_QUANTIZE)) return;
-    alignas(16) T t[8];
-#pragma unroll
-    for (int i = 0; i < int(sizeof(T)) / 2; ++i) reinterpret_cast<uint4*>(t)[i] = reinterpret_cast<const uint4*>(p)[i];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = to_f(t[j]);
-    return;
+// Eight neighbouring values as they are loaded: 16-bit types two to a word, whose magnitudes' bits are ordered like
+// the numbers, so that maxima are taken on words.
+template <typename T>
+struct Row8 {
+  static constexpr int WORDS = int(sizeof(T)) * 2;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else if constexpr (std::is_same<T, __half>::value) {
+      const uint16_t h = uint16_t(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+      return __half2float(*reinterpret_cast<const __half*>(&h));
+    } else {
+      return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
   }
+  __device__ __forceinline__ void load(const QuantArgs& a, int src, int col, bool vec) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (col + j < a.cols && DG_IN(a.dbg, p + j, int(sizeof(T)), DBG_QUANTIZE)) v[j] = to_f(p[j]);
+    for (int j = 0; j < WORDS; ++j) w[j] = 0u;
+    if (src < 0 || col >= a.cols) return;
+    const T* const p = static_cast<const T*>(a.x) + int64_t(src) * a.ldx + col;
+    if (vec && col + 8 <= a.cols) {
+      if (!DG_IN(a.dbg, p, 8 * int(sizeof(T)), DBG_QUANTIZE)) return;
+#pragma unroll
+      for (int i = 0; i < WORDS / 4; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (col + j >= a.cols || !DG_IN(a.dbg, p + j, int(sizeof(T)), DBG_QUANTIZE)) continue;
+      if constexpr (sizeof(T) == 4)
+        w[j] = __float_as_uint(p[j]);
+      else
+        w[j / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[j]) << (16 * (j & 1));
+    }
+  }
+};
+
+// The larger magnitude, of two 16-bit values each or of one 32-bit one (NaN wins: its bits are the largest).
+template <typename T>
+__device__ __forceinline__ uint32_t most(uint32_t x, uint32_t y) {
+  if constexpr (sizeof(T) == 4) return max(x & 0x7fffffffu, y & 0x7fffffffu);
+  else return __vmaxu2(x & 0x7fff7fffu, y & 0x7fff7fffu);
 }
 
-template <typename T, bool VEC, bool TURN>
-__global__ void __launch_bounds__(32 * kWarps) quantize_mx4_kernel(const QuantArgs a) {
+// Scale byte of a magnitude's bits in the input's type.
+template <typename T>
+__device__ __forceinline__ uint32_t byte_of(uint32_t bits) {
+  if constexpr (sizeof(T) == 4) return mx4_byte(bits);
+  else if constexpr (std::is_same<T, __half>::value) {
+    const uint16_t h = uint16_t(bits);
+    return mx4_byte(__float_as_uint(__half2float(*reinterpret_cast<const __half*>(&h))));
+  } else {
+    return mx4_byte(bits << 16);
+  }
+}
+
+// Scale byte of a row's block of 32: the magnitudes of four lanes' eight values.
+template <typename T>
+__device__ __forceinline__ uint32_t row_byte(const Row8<T>& v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < Row8<T>::WORDS; ++j) m = most<T>(m, v.w[j]);
+  m = most<T>(m, __shfl_xor_sync(kAll, m, 1));
+  m = most<T>(m, __shfl_xor_sync(kAll, m, 2));
+  if constexpr (sizeof(T) == 2) m = max(m >> 16, m & 0xffffu);
+  return byte_of<T>(m);
+}
+
+// Codes of eight values; a block without a number has codes of 0.
+__device__ __forceinline__ uint32_t row_codes(uint32_t byte, float a, float b, float c, float d, float e, float f, float g,
+                                              float h) {
+  const float inv = mx4_inverse(byte);
+  const uint32_t codes = mx4_codes2(a, b, inv) | mx4_codes2(c, d, inv) << 8 | mx4_codes2(e, f, inv) << 16 | mx4_codes2(g, h, inv) << 24;
+  return byte == 255u ? 0u : codes;
+}
+
+// `n` bytes of a word, or all four.
+__device__ __forceinline__ void store_codes(const QuantArgs& a, uint8_t* dst, uint32_t c, int n) {
+  if (n >= 4) {
+    if (DG_IN(a.dbg, dst, 4, DBG_QUANTIZE)) *reinterpret_cast<uint32_t*>(dst) = c;
+  } else if (n > 0 && DG_IN(a.dbg, dst, n, DBG_QUANTIZE)) {
+    for (int j = 0; j < n; ++j) dst[j] = uint8_t(c >> (8 * j));
+  }
+}
+
+// One orientation: a warp takes kRowRows rows of 512 columns, all its loads in flight together; a word of four
+// scale bytes is half a warp's.
+constexpr int kRowRows = 2;
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) quantize_mx4_rows_kernel(const QuantArgs a, uint32_t chunks) {
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31, piece = lane & 15;
+  const uint32_t warp = uint32_t((uint64_t(blockIdx.x) * 256 + threadIdx.x) >> 5);
+  const int r0 = int(warp / chunks) * kRowRows, c0 = int(warp % chunks) * 512 + 8 * lane;
+  if (r0 >= a.rows_padded) return;
+  Row8<T> v[kRowRows][2];
+  int src[kRowRows];
+  source_rows(a, r0, src);
+#pragma unroll
+  for (int i = 0; i < kRowRows; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) v[i][h].load(a, src[i], c0 + 256 * h, VEC);
+#pragma unroll
+  for (int i = 0; i < kRowRows; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = c0 + 256 * h;
+      const Row8<T>& x = v[i][h];
+      const uint32_t byte = row_byte<T>(x);
+      const uint32_t c = row_codes(byte, x.at(0), x.at(1), x.at(2), x.at(3), x.at(4), x.at(5), x.at(6), x.at(7));
+      uint32_t word = byte | __shfl_down_sync(kAll, byte, 4) << 8;
+      word |= __shfl_down_sync(kAll, word, 8) << 16;
+      if (src[i] >= 0) store_codes(a, a.q + int64_t(r0 + i) * a.ldq + col / 2, c, (a.cols - col + 1) / 2);
+      if (piece == 0 && col / 128 < a.q_groups) {
+        uint8_t* const s = a.sq + scale_at(r0 + i, col / 32, a.q_groups);
+        if (DG_IN(a.dbg, s, 4, DBG_QUANTIZE)) *reinterpret_cast<uint32_t*>(s) = word;
+      }
+    }
+}
+
+// Both orientations, or the transposed one.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(32 * kWarps, 2) quantize_mx4_kernel(const QuantArgs a) {
+  constexpr int COLS = 8 / (sizeof(T) == 4 ? 1 : 2);  // words of maxima of a lane's eight columns
   __shared__ uint32_t row_bytes[128];          // the scale tile of Q, word by row
-  __shared__ uint32_t col_max[TURN ? kWarps : 1][128];
-  __shared__ uint8_t col_byte[TURN ? 4 : 1][128];  // [block of 32 rows][column]
-  __shared__ uint16_t turn[TURN ? 128 * 32 : 1];   // [column][4 rows ^ swizzle]
+  alignas(16) __shared__ uint32_t col_max[kWarps][16 * COLS];
+  __shared__ uint8_t col_byte[4][128];         // [block of 32 rows][column]
+  __shared__ uint16_t turn[128 * 32];          // [column][4 rows ^ swizzle]
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cb = blockIdx.x, rb = blockIdx.y;
   const int row0 = warp * 8 + (lane >> 4) * kLaneRows;  // of the tile
   const int piece = lane & 15, col = cb * 128 + piece * 8;
-  float v[kLaneRows][8];
+  Row8<T> v[kLaneRows];
   uint32_t live = 0;
+  {
+    int all[8];
+    source_rows(a, rb * 128 + warp * 8, all);
 #pragma unroll
-  for (int i = 0; i < kLaneRows; ++i) {
-    const int src = source_row(a, rb * 128 + row0 + i);
-    live |= uint32_t(src >= 0) << i;
-    load_row<T, VEC>(a, src, col, v[i]);
+    for (int i = 0; i < kLaneRows; ++i) {
+      const int src = lane < 16 ? all[i] : all[i + kLaneRows];
+      live |= uint32_t(src >= 0) << i;
+      v[i].load(a, src, col, VEC);
+    }
   }
-  if constexpr (TURN) {
-    uint32_t m[8];
+  {
+    uint32_t m[COLS];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < COLS; ++j) {
       m[j] = 0;
 #pragma unroll
-      for (int i = 0; i < kLaneRows; ++i) m[j] = max(m[j], __float_as_uint(v[i][j]) & 0x7fffffffu);
-      m[j] = max(m[j], __shfl_xor_sync(kAll, m[j], 16));
+      for (int i = 0; i < kLaneRows; ++i) m[j] = most<T>(m[j], v[i].w[j]);
+      m[j] = most<T>(m[j], __shfl_xor_sync(kAll, m[j], 16));
     }
     if (lane < 16) {
-      *reinterpret_cast<uint4*>(&col_max[warp][piece * 8]) = make_uint4(m[0], m[1], m[2], m[3]);
-      *reinterpret_cast<uint4*>(&col_max[warp][piece * 8 + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
+#pragma unroll
+      for (int j = 0; j < COLS; j += 4)
+        *reinterpret_cast<uint4*>(&col_max[warp][piece * COLS + j]) = make_uint4(m[j], m[j + 1], m[j + 2], m[j + 3]);
     }
   }
   if (a.q) {
 #pragma unroll
     for (int i = 0; i < kLaneRows; ++i) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7fffffffu);
-      m = max(m, __shfl_xor_sync(kAll, m, 1));
-      m = max(m, __shfl_xor_sync(kAll, m, 2));
-      const uint32_t byte = mx4_byte(m);
-      const float inv = mx4_inverse(byte);
-      uint32_t c = 0;
-      if (byte != 255u)
-        c = mx4_codes2(v[i][0], v[i][1], inv) | mx4_codes2(v[i][2], v[i][3], inv) << 8 | mx4_codes2(v[i][4], v[i][5], inv) << 16 |
-            mx4_codes2(v[i][6], v[i][7], inv) << 24;
+      const uint32_t byte = row_byte<T>(v[i]);
+      const uint32_t c = row_codes(byte, v[i].at(0), v[i].at(1), v[i].at(2), v[i].at(3), v[i].at(4), v[i].at(5), v[i].at(6), v[i].at(7));
       // the word of four blocks, in lanes 0 and 16
       uint32_t word = byte | __shfl_down_sync(kAll, byte, 4) << 8;
       word |= __shfl_down_sync(kAll, word, 8) << 16;
       if (piece == 0) row_bytes[row0 + i] = word;
-      if ((live >> i) & 1u) {
-        const int n = min(4, (a.cols - col + 1) / 2);  // bytes of the row that exist
-        uint8_t* const dst = a.q + int64_t(rb * 128 + row0 + i) * a.ldq + col / 2;
-        if (n == 4) {
-          if (DG_IN(a.dbg, dst, 4, DBG_QUANTIZE)) *reinterpret_cast<uint32_t*>(dst) = c;
-        } else if (n > 0 && DG_IN(a.dbg, dst, n, DBG_QUANTIZE)) {
-          for (int j = 0; j < n; ++j) dst[j] = uint8_t(c >> (8 * j));
-        }
-      }
+      if ((live >> i) & 1u) store_codes(a, a.q + int64_t(rb * 128 + row0 + i) * a.ldq + col / 2, c, (a.cols - col + 1) / 2);
     }
   }
   __syncthreads();
@@ -135,60 +221,67 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_mx4_kernel(const QuantAr
     if (DG_IN(a.dbg, s, 16, DBG_QUANTIZE))
       *reinterpret_cast<uint4*>(s) = make_uint4(row_bytes[lane], row_bytes[lane + 32], row_bytes[lane + 64], row_bytes[lane + 96]);
   }
-  if constexpr (TURN) {
-    {  // one thread a column and block of 32 rows
-      const int c = threadIdx.x & 127, b = threadIdx.x >> 7;
-      const uint32_t m = max(max(col_max[4 * b][c], col_max[4 * b + 1][c]), max(col_max[4 * b + 2][c], col_max[4 * b + 3][c]));
-      col_byte[b][c] = uint8_t(mx4_byte(m));
-    }
-    __syncthreads();
+  if (threadIdx.x < 64 * COLS) {  // one thread a word of columns and block of 32 rows
+    const int c = threadIdx.x % (16 * COLS), b = threadIdx.x / (16 * COLS);
+    const uint32_t m = most<T>(most<T>(col_max[4 * b][c], col_max[4 * b + 1][c]), most<T>(col_max[4 * b + 2][c], col_max[4 * b + 3][c]));
+    if constexpr (sizeof(T) == 4)
+      col_byte[b][c] = uint8_t(byte_of<T>(m));
+    else
+      *reinterpret_cast<uint16_t*>(&col_byte[b][2 * c]) = uint16_t(byte_of<T>(m & 0xffffu) | byte_of<T>(m >> 16) << 8);
+  }
+  __syncthreads();
+  {
+    const uint2 bytes = *reinterpret_cast<const uint2*>(&col_byte[warp / 4][piece * 8]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t byte = col_byte[warp / 4][piece * 8 + j];
+      const uint32_t byte = ((j < 4 ? bytes.x : bytes.y) >> (8 * (j & 3))) & 0xffu;
       const float inv = mx4_inverse(byte);
-      uint32_t c = 0;
-      if (byte != 255u) c = mx4_codes2(v[0][j], v[1][j], inv) | mx4_codes2(v[2][j], v[3][j], inv) << 8;
-      turn[(piece * 8 + j) * 32 + ((warp * 2 + (lane >> 4)) ^ (piece * 2))] = uint16_t(c);
+      const uint32_t c = mx4_codes2(v[0].at(j), v[1].at(j), inv) | mx4_codes2(v[2].at(j), v[3].at(j), inv) << 8;
+      turn[(piece * 8 + j) * 32 + ((warp * 2 + (lane >> 4)) ^ (piece * 2))] = uint16_t(byte == 255u ? 0u : c);
     }
-    __syncthreads();
-    {  // 16 bytes of a column: 32 rows
-      const int c = threadIdx.x >> 2, part = threadIdx.x & 3, x = (c >> 3) * 2;
-      const int out_row = cb * 128 + c, r = rb * 128 + part * 32;
-      if (out_row < a.cols && r < a.rows) {
-        uint32_t w[4];
+  }
+  __syncthreads();
+  {  // 16 bytes of a column: 32 rows
+    const int c = threadIdx.x >> 2, part = threadIdx.x & 3, x = (c >> 3) * 2;
+    const int out_row = cb * 128 + c, r = rb * 128 + part * 32;
+    if (out_row < a.cols && r < a.rows) {
+      uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const uint32_t*>(&turn[c * 32 + ((part * 8 + 2 * k) ^ x)]);
-        uint8_t* const dst = a.qt + int64_t(out_row) * a.ldqt + r / 2;
-        const int n = min(16, (a.rows - r + 1) / 2);
-        if (DG_IN(a.dbg, dst, n, DBG_QUANTIZE)) {
-          if (n == 16) {
-            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-          } else {
+      for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const uint32_t*>(&turn[c * 32 + ((part * 8 + 2 * k) ^ x)]);
+      uint8_t* const dst = a.qt + int64_t(out_row) * a.ldqt + r / 2;
+      const int n = min(16, (a.rows - r + 1) / 2);
+      if (DG_IN(a.dbg, dst, n, DBG_QUANTIZE)) {
+        if (n == 16) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (k < n) dst[k] = uint8_t(w[k / 4] >> (8 * (k & 3)));
-          }
+          for (int k = 0; k < 16; ++k)
+            if (k < n) dst[k] = uint8_t(w[k / 4] >> (8 * (k & 3)));
         }
       }
     }
-    if (threadIdx.x < 32) {
-      uint32_t w[4];
+  }
+  if (threadIdx.x < 32) {
+    uint32_t w[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = lane + 32 * k;
-        w[k] = uint32_t(col_byte[0][c]) | uint32_t(col_byte[1][c]) << 8 | uint32_t(col_byte[2][c]) << 16 | uint32_t(col_byte[3][c]) << 24;
-      }
-      uint8_t* const s = a.sqt + (int64_t(cb) * a.qt_groups + rb) * 512 + lane * 16;
-      if (DG_IN(a.dbg, s, 16, DBG_QUANTIZE)) *reinterpret_cast<uint4*>(s) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int k = 0; k < 4; ++k) {
+      const int c = lane + 32 * k;
+      w[k] = uint32_t(col_byte[0][c]) | uint32_t(col_byte[1][c]) << 8 | uint32_t(col_byte[2][c]) << 16 | uint32_t(col_byte[3][c]) << 24;
     }
+    uint8_t* const s = a.sqt + (int64_t(cb) * a.qt_groups + rb) * 512 + lane * 16;
+    if (DG_IN(a.dbg, s, 16, DBG_QUANTIZE)) *reinterpret_cast<uint4*>(s) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
 template <typename T, bool VEC>
 cudaError_t launch_mx4(const QuantArgs& a, cudaStream_t s) {
-  const dim3 grid(unsigned((a.cols + 127) / 128), unsigned((a.rows + 127) / 128));
-  if (a.qt) return launch_k(quantize_mx4_kernel<T, VEC, true>, grid, dim3(32 * kWarps), 0, s, a.pdl, a);
-  return launch_k(quantize_mx4_kernel<T, VEC, false>, grid, dim3(32 * kWarps), 0, s, a.pdl, a);
+  if (!a.qt) {
+    const uint32_t chunks = uint32_t((a.cols + 511) / 512);
+    const int64_t warps = int64_t(a.rows_padded / kRowRows) * chunks;
+    return launch_k(quantize_mx4_rows_kernel<T, VEC>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0, s, a.pdl, a, chunks);
+  }
+  return launch_k(quantize_mx4_kernel<T, VEC>, dim3(unsigned((a.cols + 127) / 128), unsigned((a.rows + 127) / 128)),
+                  dim3(32 * kWarps), 0, s, a.pdl, a);
 }
 
 template <typename T>
@@ -212,12 +305,17 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const DequantArgs a, ui
   wait_prior_grid();
   uint32_t w[kPieces][2], byte[kPieces];
   int row[kPieces], col[kPieces];
+  // (one division a thread: a 64-bit one for each piece took as long as the loads)
+  const uint64_t item = uint64_t(blockIdx.x) * kPieces * 256 + threadIdx.x;
+  uint64_t r = item >> 32 ? item / pieces : uint64_t(uint32_t(item) / pieces);
+  uint32_t c = uint32_t(item - r * pieces);
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
-    const uint64_t item = (uint64_t(blockIdx.x) * kPieces + i) * 256 + threadIdx.x;
-    const uint64_t r = item / pieces;
     row[i] = r < uint64_t(a.rows) ? int(r) : -1;
-    col[i] = int(item - r * pieces) * 8;
+    col[i] = int(c) * 8;
+    c += uint32_t(a.step_pieces);
+    r += uint32_t(a.step_rows);
+    if (c >= pieces) c -= pieces, ++r;
     w[i][0] = w[i][1] = byte[i] = 0u;
     if (row[i] < 0) continue;
     const uint8_t* const q = a.q + int64_t(row[i]) * a.ldq + int64_t(col[i]) * BYTES / 8;
@@ -275,8 +373,10 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const DequantArgs a, ui
 }
 
 template <typename T>
-cudaError_t launch_values(const DequantArgs& a, cudaStream_t s) {
+cudaError_t launch_values(DequantArgs a, cudaStream_t s) {
   const uint32_t pieces = uint32_t((a.cols + 7) / 8);
+  a.step_rows = int(256 / pieces);
+  a.step_pieces = int(256 % pieces);
   const uint64_t items = uint64_t(a.rows) * pieces;
   const dim3 grid(unsigned((items + 256 * kPieces - 1) / (256 * kPieces)));
   switch (a.code) {
@@ -296,7 +396,7 @@ cudaError_t launch_quantize_mx4(const QuantArgs& a, cudaStream_t s) {
   }
 }
 
-cudaError_t launch_dequantize(const DequantArgs& a, cudaStream_t s) {
+cudaError_t launch_dequantize(DequantArgs a, cudaStream_t s) {
   switch (a.x_kind) {
     case OUT_F32: return launch_values<float>(a, s);
     case OUT_BF16: return launch_values<__nv_bfloat16>(a, s);

@@ -515,16 +515,24 @@ __global__ void __launch_bounds__(threads<FOUR>(), 1)
           __syncwarp();  // whole again before the next tcgen05.ld
         };
         if (BETA || A != ACT_SIMPLE || empty) {
+          // (the next MMAs wait for two steps' columns: both are read before the first one's arithmetic, of which there is one copy)
 #pragma unroll 1
-          for (int s = 0; s < kSteps; ++s) {
+          for (int s = 0; s < kSteps; s += 2) {
             if (!empty) {
               load(ra, s);
+              load(rb, s + 1);
               loaded(ra, s);
+              loaded(rb, s + 1);
             } else {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) ra[k] = 0u;
+              for (int k = 0; k < 32; ++k) ra[k] = rb[k] = 0u;
             }
-            process(ra, s, s % per == 0, s % per == per - 1);
+#pragma unroll 1
+            for (int t = s; t < s + 2; ++t) {
+              process(ra, t, t % per == 0, t % per == per - 1);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) ra[k] = rb[k];
+            }
           }
           continue;
         }
