@@ -34,23 +34,24 @@ __device__ __forceinline__ int choice(const BalanceArgs& a, int t, int lane) {
   return e >= 0 && e < a.experts ? e : -1;
 }
 
-// A lane's experts' shares of a token, from its logits.  One whose scores are all 0 gives none.
+// A lane's experts' shares of a token, from its logits, the largest of which (of the token's) is `top`.  One whose
+// scores are all 0 gives none; of logits of plus infinity each takes an equal share.
 template <int P>
-__device__ __forceinline__ void token_shares(const BalanceArgs& a, const float (&x)[P], float lane_top, float (&p)[P]) {
-  const Scorer scorer(a, x, number_key(lane_top));
-  float sum = scorer.sum;
+__device__ __forceinline__ void token_shares(const BalanceArgs& a, const float (&x)[P], float top, float (&p)[P]) {
+  float sum = 0.f;
   if (a.sigmoid) {
-    sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      p[i] = scorer.score(x[i]);
-      sum += p[i];
-    }
-    sum = warp_sum(sum);
+    for (int i = 0; i < P; ++i) p[i] = __fdividef(1.f, 1.f + expf(-x[i]));  // (0 where exp(-x) is past 2^126)
+  } else if (fabsf(top) < -kNegInf) {  // exp(-inf) is 0: nothing to look out for
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = expf(x[i] - top);
   } else {
 #pragma unroll
-    for (int i = 0; i < P; ++i) p[i] = scorer.power(x[i]);
+    for (int i = 0; i < P; ++i) p[i] = x[i] == top && top > 0.f ? 1.f : 0.f;
   }
+#pragma unroll
+  for (int i = 0; i < P; ++i) sum += p[i];
+  sum = warp_sum(sum);
   const float by = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int i = 0; i < P; ++i) p[i] *= by;
@@ -107,11 +108,12 @@ __global__ void __launch_bounds__(32 * balance_warps<P>(), 1) balance_kernel(con
     if (AHEAD && t + step < a.tokens) load(t + step);
     const bool live = __any_sync(kAll, expert >= 0);
     if (expert >= 0) atomicAdd(count + expert, 1);
+    if (!live) continue;
     float top = kNegInf;
 #pragma unroll
     for (int i = 0; i < P; ++i) top = fmaxf(top, x[i]);
+    if (!a.sigmoid) top = key_value(__reduce_max_sync(kAll, number_key(top)));
     token_shares(a, x, top, p);
-    if (!live) continue;
     ++mine;
 #pragma unroll
     for (int i = 0; i < P; ++i) acc[i] += p[i];
@@ -235,8 +237,8 @@ __global__ void __launch_bounds__(128) balance_backward_kernel(const BalanceArgs
 #pragma unroll
   for (int i = 0; i < P; ++i)
     if (x[i] > top) top = x[i], reference = f[i];
-  token_shares(a, x, top, p);
   const uint32_t key = number_key(top), best = __reduce_max_sync(kAll, key);
+  token_shares(a, x, key_value(best), p);
   reference = __shfl_sync(kAll, reference, __ffs(__ballot_sync(kAll, key == best)) - 1);
   float dot = 0.f;
 #pragma unroll

@@ -437,11 +437,10 @@ struct DequantArgs {
   int64_t ldx;
   int x_kind;
   int wide;      // rows of X on 16-byte boundaries
-  int step_rows, step_pieces;  // 256 pieces further on (set by the launcher)
   int pdl;
   DG_DEBUG_FIELD
 };
-cudaError_t launch_dequantize(DequantArgs a, cudaStream_t s);
+cudaError_t launch_dequantize(const DequantArgs& a, cudaStream_t s);
 
 // -------------------------------------------------------------------- norm
 

@@ -81,23 +81,23 @@ struct Eight {
   }
 };
 
-// `left` columns from p to the end of the row (none: nothing is read).  WIDE: p is on a 16-byte boundary, so that eight
+// `left` columns from p to the end of the row (none: nothing is read).  a.wide: p is on a 16-byte boundary, so that eight
 // columns are loaded whole; the last few of a row one by one.
-template <bool WIDE, typename T, typename A>
+template <typename T, typename A>
 __device__ __forceinline__ void load8(const A& a, Eight<T>& o, const T* p, int left, int site) {
   o.clear();
-  if (WIDE && left >= 8) {
+  if (a.wide && left >= 8) {
     if (DG_IN(a.dbg, p, 8 * int(sizeof(T)), site)) o.load(p);
-  } else if (left > 0) {
+  } else if (left > 0 && DG_IN(a.dbg, p, min(left, 8) * int(sizeof(T)), site)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left && DG_IN(a.dbg, p + i, int(sizeof(T)), site)) o.put(i, p[i]);
+      if (i < left) o.put(i, p[i]);
   }
 }
 
-template <bool WIDE, typename T, typename A>
+template <typename T, typename A>
 __device__ __forceinline__ void store8(const A& a, T* p, const float (&v)[8], int left, int site) {
-  if (WIDE && left >= 8) {
+  if (a.wide && left >= 8) {
     Eight<T> o;
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -118,27 +118,27 @@ __device__ __forceinline__ void store8(const A& a, T* p, const float (&v)[8], in
 #pragma unroll
     for (int i = 0; i < Eight<T>::WORDS / 4; ++i)
       reinterpret_cast<uint4*>(p)[i] = make_uint4(o.w[4 * i], o.w[4 * i + 1], o.w[4 * i + 2], o.w[4 * i + 3]);
-  } else if (left > 0) {
+  } else if (left > 0 && DG_IN(a.dbg, p, min(left, 8) * int(sizeof(T)), site)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left && DG_IN(a.dbg, p + i, int(sizeof(T)), site)) p[i] = from_f<T>(v[i]);
+      if (i < left) p[i] = from_f<T>(v[i]);
   }
 }
 
 // Eight values of the gain (none: ones), which is of the input's type or fp32.
-template <bool WIDE, typename T, typename A>
+template <typename T, typename A>
 __device__ __forceinline__ void load_gain(const A& a, float (&g)[8], int col, int left) {
   if (a.gain == nullptr) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = 1.f;
   } else if (a.g_kind == kind_of<T>()) {
     Eight<T> o;
-    load8<WIDE>(a, o, static_cast<const T*>(a.gain) + col, left, DBG_NORM);
+    load8(a, o, static_cast<const T*>(a.gain) + col, left, DBG_NORM);
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = o.at(i);
   } else {
     Eight<float> o;
-    load8<WIDE>(a, o, static_cast<const float*>(a.gain) + col, left, DBG_NORM);
+    load8(a, o, static_cast<const float*>(a.gain) + col, left, DBG_NORM);
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = o.at(i);
   }
@@ -150,14 +150,19 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The sum over a row's warps, [first, first + warps) of the CTA's; every thread of the CTA calls it.
+// The sum over a row's warps, [first, first + warps) of the CTA's; every thread of the CTA calls it.  (All lanes get
+// lane 0's order of additions, whatever their own would be.)
 __device__ __forceinline__ float row_sum(float v, float* sums, int first, int warps) {
+  if (warps == 1) return warp_sum(v);
+  const int lane = threadIdx.x & 31;
   v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+  if (lane == 0) sums[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0.f;
-  for (int i = 0; i < warps; ++i) v += sums[first + i];
-  return v;
+  v = lane < warps ? sums[first + lane] : 0.f;
+  // (16 warps at most)
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return __shfl_sync(kAll, v, 0);
 }
 
 // Codes of eight values and the scale byte of the block of 128 that they share with the other lanes of half a warp.
@@ -183,6 +188,13 @@ __device__ __forceinline__ uint2 block_codes(const float (&y)[8], uint32_t* byte
   return make_uint2(codes4<E5M2, false>(y[0], y[1], y[2], y[3], inv), codes4<E5M2, false>(y[4], y[5], y[6], y[7], inv));
 }
 
+// Eight of a part's sums; parts are on 16-byte boundaries.
+__device__ __forceinline__ void store_part(const NormBackArgs& a, float* p, const float (&v)[8]) {
+  if (!DG_IN(a.dbg, p, 32, DBG_NORM)) return;
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
 // A row's values as they are loaded, a lane's part of it: x and r, or dy, h and dh.
 template <typename TA, typename TB, int G, bool THREE>
 struct RowOf {
@@ -197,7 +209,7 @@ __device__ __forceinline__ int column_of(int i, int mine, int warps) {
 
 // A CTA takes a.per rows at a time, a.warps warps to a row, G groups of 512 columns to a warp; with one group the
 // next rows' loads are under way while it works on one (more leave no registers for that).
-template <typename TX, typename TH, int G, bool WIDE>
+template <typename TX, typename TH, int G>
 __global__ void __launch_bounds__(512, G == 1 && sizeof(TX) == 2 && sizeof(TH) == 2 ? 2 : 1) norm_kernel(const NormArgs a) {
   __shared__ float sums[2][16];
   wait_prior_grid();
@@ -210,9 +222,9 @@ __global__ void __launch_bounds__(512, G == 1 && sizeof(TX) == 2 && sizeof(TH) =
 #pragma unroll
     for (int i = 0; i < 2 * G; ++i) {
       const int col = column_of(i, mine, a.warps), left = live ? a.cols - col : 0;
-      load8<WIDE>(a, v.a[i], static_cast<const TX*>(a.x) + row * a.ldx + col, left, DBG_NORM);
+      load8(a, v.a[i], static_cast<const TX*>(a.x) + row * a.ldx + col, left, DBG_NORM);
       if (a.r)
-        load8<WIDE>(a, v.b[i], static_cast<const TH*>(a.r) + row * a.ldr + col, left, DBG_NORM);
+        load8(a, v.b[i], static_cast<const TH*>(a.r) + row * a.ldr + col, left, DBG_NORM);
       else
         v.b[i].clear();
     }
@@ -224,7 +236,7 @@ __global__ void __launch_bounds__(512, G == 1 && sizeof(TX) == 2 && sizeof(TH) =
 #pragma unroll
     for (int i = 0; i < 2 * G; ++i) {
       const int col = column_of(i, mine, a.warps);
-      load_gain<WIDE, TX>(a, gain[i], col, scaled ? a.cols - col : 0);
+      load_gain<TX>(a, gain[i], col, scaled ? a.cols - col : 0);
     }
   }
   int turn = 0;
@@ -251,12 +263,12 @@ __global__ void __launch_bounds__(512, G == 1 && sizeof(TX) == 2 && sizeof(TH) =
     for (int i = 0; i < 2 * G; ++i) {
       const int col = column_of(i, mine, a.warps), group = col >> 9;
       const int left = live ? a.cols - col : 0;
-      if (a.h) store8<WIDE>(a, static_cast<TH*>(a.h) + row * a.ldh + col, v[i], left, DBG_NORM);
+      if (a.h) store8(a, static_cast<TH*>(a.h) + row * a.ldh + col, v[i], left, DBG_NORM);
       if (!scaled) continue;
-      if constexpr (G == 4) load_gain<WIDE, TX>(a, gain[0], col, left);
+      if constexpr (G == 4) load_gain<TX>(a, gain[0], col, left);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rho * gain[G < 4 ? i : 0][j];
-      if (a.y) store8<WIDE>(a, static_cast<TX*>(a.y) + row * a.ldy + col, v[i], left, DBG_NORM);
+      if (a.y) store8(a, static_cast<TX*>(a.y) + row * a.ldy + col, v[i], left, DBG_NORM);
       if (a.q) {
         // (what is not there is zero, unless rho is infinite)
         if (left < 8) {
@@ -284,35 +296,38 @@ __global__ void __launch_bounds__(512, G == 1 && sizeof(TX) == 2 && sizeof(TH) =
   }
 }
 
-template <typename TX, typename TH, int G, bool WIDE>
+// Rows of up to kBackCols columns: a lane's sixteen stay in registers, the next row's loads under way.
+constexpr int kBackCols = 16 * 512;
+
+template <typename TX, typename TH>
 __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a) {
   __shared__ float sums[2][16];
   wait_prior_grid();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5;
   const int slot = warp / a.warps, mine = warp - slot * a.warps;
   const int step = int(gridDim.x) * a.per;
-  auto load = [&](RowOf<TX, TH, G, true>& v, float* rho, int64_t row) {
+  auto load = [&](RowOf<TX, TH, 1, true>& v, float* rho, int64_t row) {
     const bool live = row < a.rows;
     *rho = live && DG_IN(a.dbg, a.rstd + row, 4, DBG_NORM) ? __ldg(a.rstd + row) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 2 * G; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const int col = column_of(i, mine, a.warps), left = live ? a.cols - col : 0;
-      load8<WIDE>(a, v.a[i], static_cast<const TX*>(a.dy) + row * a.lddy + col, left, DBG_NORM);
-      load8<WIDE>(a, v.b[i], static_cast<const TH*>(a.h) + row * a.ldh + col, left, DBG_NORM);
+      load8(a, v.a[i], static_cast<const TX*>(a.dy) + row * a.lddy + col, left, DBG_NORM);
+      load8(a, v.b[i], static_cast<const TH*>(a.h) + row * a.ldh + col, left, DBG_NORM);
       if (a.dh)
-        load8<WIDE>(a, v.c[i], static_cast<const TH*>(a.dh) + row * a.lddh + col, left, DBG_NORM);
+        load8(a, v.c[i], static_cast<const TH*>(a.dh) + row * a.lddh + col, left, DBG_NORM);
       else
         v.c[i].clear();
     }
   };
-  RowOf<TX, TH, G, true> now, next;
-  float rho = 0.f, rho_next = 0.f;
-  if constexpr (G == 1) load(next, &rho_next, int64_t(blockIdx.x) * a.per + slot);
-  float gain[G < 4 ? 2 * G : 1][8], acc[2 * G][8];
+  RowOf<TX, TH, 1, true> now, next;
+  float rho_next;
+  load(next, &rho_next, int64_t(blockIdx.x) * a.per + slot);
+  float gain[2][8], acc[2][8];
 #pragma unroll
-  for (int i = 0; i < 2 * G; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const int col = column_of(i, mine, a.warps);
-    if constexpr (G < 4) load_gain<WIDE, TX>(a, gain[i], col, a.cols - col);
+    load_gain<TX>(a, gain[i], col, a.cols - col);
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
   }
@@ -320,67 +335,119 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a
   for (int64_t row0 = int64_t(blockIdx.x) * a.per; row0 < a.rows; row0 += step, turn ^= 1) {
     const int64_t row = row0 + slot;
     const bool live = row < a.rows;
-    if constexpr (G == 1) {
-      now = next;
-      rho = rho_next;
-      if (row0 + step < a.rows) load(next, &rho_next, row + step);
-    } else {
-      load(now, &rho, row);
-    }
+    now = next;
+    const float rho = rho_next;
+    if (row0 + step < a.rows) load(next, &rho_next, row + step);
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2 * G; ++i) {
-      if constexpr (G == 4) load_gain<WIDE, TX>(a, gain[0], column_of(i, mine, a.warps), a.cols - column_of(i, mine, a.warps));
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float xhat = now.b[i].at(j) * rho, d = now.a[i].at(j);
         acc[i][j] = fmaf(d, xhat, acc[i][j]);
-        sum = fmaf(d * gain[G < 4 ? i : 0][j], xhat, sum);
+        sum = fmaf(d * gain[i][j], xhat, sum);
       }
-    }
     sum = row_sum(sum, sums[turn], slot * a.warps, a.warps);
     const float mean = __fdiv_rn(sum, float(a.cols));
 #pragma unroll
-    for (int i = 0; i < 2 * G; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const int col = column_of(i, mine, a.warps);
-      if constexpr (G == 4) load_gain<WIDE, TX>(a, gain[0], col, a.cols - col);
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        v[j] = fmaf(rho, fmaf(-now.b[i].at(j) * rho, mean, now.a[i].at(j) * gain[G < 4 ? i : 0][j]), now.c[i].at(j));
-      store8<WIDE>(a, static_cast<TH*>(a.dx) + row * a.lddx + col, v, live ? a.cols - col : 0, DBG_NORM);
+        v[j] = fmaf(rho, fmaf(-now.b[i].at(j) * rho, mean, now.a[i].at(j) * gain[i][j]), now.c[i].at(j));
+      store8(a, static_cast<TH*>(a.dx) + row * a.lddx + col, v, live ? a.cols - col : 0, DBG_NORM);
     }
   }
   if (!a.parts) return;
   float* const part = a.parts + (int64_t(blockIdx.x) * a.per + slot) * a.part_cols;
 #pragma unroll
-  for (int i = 0; i < 2 * G; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const int col = column_of(i, mine, a.warps);
-    if (col < a.part_cols) store8<true>(a, part + col, acc[i], 8, DBG_NORM);
+    if (col < a.part_cols) store_part(a, part + col, acc[i]);
   }
 }
 
-// dgain[c] = sum over the parts, in their order: a warp's lane takes a column, its CTA's warps every 32nd part each, whose sums
-// are added in the warps' order.
+// Longer rows: read twice, the second time from a cache; the gain's gradient is summed in shared memory, each column
+// by the one thread that has it.  A CTA a row, a.warps = 16.
+template <typename TX, typename TH>
+__global__ void __launch_bounds__(512) norm_backward_long_kernel(const NormBackArgs a) {
+  extern __shared__ float4 acc_room[];
+  __shared__ float sums[2][16];
+  wait_prior_grid();
+  float* const acc = reinterpret_cast<float*>(acc_room);
+  const int first = int(threadIdx.x) * 8, stride = 512 * 8;
+  for (int col = first; col < a.part_cols; col += stride)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[col + j] = 0.f;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    const float rho = DG_IN(a.dbg, a.rstd + row, 4, DBG_NORM) ? __ldg(a.rstd + row) : 0.f;
+    const TX* const dy = static_cast<const TX*>(a.dy) + row * a.lddy;
+    const TH* const h = static_cast<const TH*>(a.h) + row * a.ldh;
+    Eight<TX> d8;
+    Eight<TH> h8, p8;
+    float gain[8], sum = 0.f;
+    for (int col = first; col < a.cols; col += stride) {
+      load8(a, d8, dy + col, a.cols - col, DBG_NORM);
+      load8(a, h8, h + col, a.cols - col, DBG_NORM);
+      load_gain<TX>(a, gain, col, a.cols - col);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xhat = h8.at(j) * rho, d = d8.at(j);
+        acc[col + j] = fmaf(d, xhat, acc[col + j]);
+        sum = fmaf(d * gain[j], xhat, sum);
+      }
+    }
+    sum = row_sum(sum, sums[turn], 0, 16);
+    const float mean = __fdiv_rn(sum, float(a.cols));
+    for (int col = first; col < a.cols; col += stride) {
+      load8(a, d8, dy + col, a.cols - col, DBG_NORM);
+      load8(a, h8, h + col, a.cols - col, DBG_NORM);
+      load_gain<TX>(a, gain, col, a.cols - col);
+      if (a.dh)
+        load8(a, p8, static_cast<const TH*>(a.dh) + row * a.lddh + col, a.cols - col, DBG_NORM);
+      else
+        p8.clear();
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = fmaf(rho, fmaf(-h8.at(j) * rho, mean, d8.at(j) * gain[j]), p8.at(j));
+      store8(a, static_cast<TH*>(a.dx) + row * a.lddx + col, v, a.cols - col, DBG_NORM);
+    }
+  }
+  if (!a.parts) return;
+  float* const part = a.parts + int64_t(blockIdx.x) * a.part_cols;
+  for (int col = first; col < a.part_cols; col += stride) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = acc[col + j];
+    store_part(a, part + col, v);
+  }
+}
+
+// dgain[c] = sum over the parts: eight columns a CTA, every 128th part to a thread of a column; the threads' sums are
+// added in a fixed order.  (32 columns a CTA, every 32nd part: 1 us more for 456 parts of 2050.)
 __global__ void __launch_bounds__(1024) norm_gain_kernel(const NormBackArgs a, int parts) {
-  __shared__ float sums[32][33];
+  __shared__ float sums[32][8];
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = int(blockIdx.x) * 32 + lane;
+  const int col = int(blockIdx.x) * 8 + (lane & 7);
   float s = 0.f;
   if (col < a.cols) {
-#pragma unroll 8
-    for (int p = warp; p < parts; p += 32) {
+#pragma unroll 4
+    for (int p = warp * 4 + (lane >> 3); p < parts; p += 128) {
       const float* const at = a.parts + int64_t(p) * a.part_cols + col;
       s += DG_IN(a.dbg, at, 4, DBG_NORM) ? __ldcg(at) : 0.f;
     }
   }
-  sums[warp][lane] = s;
+  s += __shfl_xor_sync(kAll, s, 8);
+  s += __shfl_xor_sync(kAll, s, 16);
+  if (lane < 8) sums[warp][lane] = s;
   __syncthreads();
-  if (warp > 0 || col >= a.cols) return;
+  if (threadIdx.x >= 8 || col >= a.cols) return;
   s = 0.f;
 #pragma unroll
-  for (int w = 0; w < 32; ++w) s += sums[w][lane];
+  for (int w = 0; w < 32; ++w) s += sums[w][threadIdx.x];
   if (DG_IN(a.dbg, a.dgain + col, 4, DBG_NORM)) a.dgain[col] = s;
 }
 
@@ -398,13 +465,13 @@ Shape shape_of(int cols, int most_warps, int64_t rows) {
 }
 
 // CTAs of the forward kernel that an SM holds at once, looked up once for each number of warps.
-template <typename TX, typename TH, int G, bool WIDE>
+template <typename TX, typename TH, int G>
 int norm_ctas(int threads) {
   static std::atomic<int> known[17];
   std::atomic<int>& k = known[threads / 32];
   int n = k.load(std::memory_order_relaxed);
   if (n > 0) return n;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_kernel<TX, TH, G, WIDE>, threads, 0) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_kernel<TX, TH, G>, threads, 0) != cudaSuccess) {
     cudaGetLastError();
     n = 1;
   }
@@ -421,16 +488,10 @@ cudaError_t by_types(int x_kind, int h_kind, F f) {
 }
 
 template <typename F>
-cudaError_t by_groups(int g, bool wide, F f) {
-  using std::integral_constant;
-  if (wide) {
-    if (g == 1) return f(integral_constant<int, 1>{}, std::true_type{});
-    if (g == 2) return f(integral_constant<int, 2>{}, std::true_type{});
-    return f(integral_constant<int, 4>{}, std::true_type{});
-  }
-  if (g == 1) return f(integral_constant<int, 1>{}, std::false_type{});
-  if (g == 2) return f(integral_constant<int, 2>{}, std::false_type{});
-  return f(integral_constant<int, 4>{}, std::false_type{});
+cudaError_t by_groups(int g, F f) {
+  if (g == 1) return f(std::integral_constant<int, 1>{});
+  if (g == 2) return f(std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 4>{});
 }
 
 }  // namespace
@@ -441,16 +502,16 @@ cudaError_t launch_norm(NormArgs a, int sms, cudaStream_t s) {
   a.warps = sh.warps;
   a.per = sh.per;
   return by_types(a.x_kind, a.h_kind, [&](auto x, auto h) {
-    return by_groups(sh.g, a.wide != 0, [&](auto g, auto w) {
+    return by_groups(sh.g, [&](auto g) {
       const int64_t fit =
-          int64_t(sms) * norm_ctas<decltype(x), decltype(h), decltype(g)::value, decltype(w)::value>(32 * sh.warps * sh.per);
-      return launch_k(norm_kernel<decltype(x), decltype(h), decltype(g)::value, decltype(w)::value>, dim3(unsigned(std::min((rows + sh.per - 1) / sh.per, fit))), dim3(unsigned(32 * sh.warps * sh.per)),
+          int64_t(sms) * norm_ctas<decltype(x), decltype(h), decltype(g)::value>(32 * sh.warps * sh.per);
+      return launch_k(norm_kernel<decltype(x), decltype(h), decltype(g)::value>, dim3(unsigned(std::min((rows + sh.per - 1) / sh.per, fit))), dim3(unsigned(32 * sh.warps * sh.per)),
                       0, s, a.pdl, a);
     });
   });
 }
 
-// Rows' partial sums of the gain's gradient that the launch below makes.
+// Rows' partial sums of the gain's gradient that the launch below makes, and its CTAs.  (16 warps an SM: 128 registers a thread.)
 static int norm_parts(int64_t rows, int cols, int sms, int* grid) {
   const Shape sh = shape_of(cols, 16, rows);
   *grid = int(std::min<int64_t>((rows + sh.per - 1) / sh.per, int64_t(sms) * std::max(1, 16 / (sh.warps * sh.per))));
@@ -462,6 +523,26 @@ size_t norm_backward_workspace(int64_t rows, int64_t cols, int sms) {
   return size_t(norm_parts(rows, int(cols), sms, &grid)) * size_t((cols + 7) / 8 * 8) * 4;
 }
 
+namespace {
+
+// The shared memory of the sums has to be asked for, once on each device.
+template <typename TX, typename TH>
+cudaError_t launch_long(const NormBackArgs& a, int grid, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (bit == 0 || (ready.load(std::memory_order_acquire) & bit) == 0) {
+    const cudaError_t err =
+        cudaFuncSetAttribute(norm_backward_long_kernel<TX, TH>, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_MAX_COLS * 4);
+    if (err != cudaSuccess) return err;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  return launch_k(norm_backward_long_kernel<TX, TH>, dim3(unsigned(grid)), dim3(512), size_t(a.part_cols) * 4, s, a.pdl, a);
+}
+
+}  // namespace
+
 cudaError_t launch_norm_backward(NormBackArgs a, int sms, cudaStream_t s) {
   int grid = 0;
   const int parts = norm_parts(a.rows, a.cols, sms, &grid);
@@ -472,14 +553,14 @@ cudaError_t launch_norm_backward(NormBackArgs a, int sms, cudaStream_t s) {
   if (!a.dgain) a.parts = nullptr;
   if (a.rows > 0) {
     const cudaError_t err = by_types(a.x_kind, a.h_kind, [&](auto x, auto h) {
-      return by_groups(sh.g, a.wide != 0, [&](auto g, auto w) {
-        return launch_k(norm_backward_kernel<decltype(x), decltype(h), decltype(g)::value, decltype(w)::value>,
-                        dim3(unsigned(grid)), dim3(unsigned(32 * sh.warps * sh.per)), 0, s, a.pdl, a);
-      });
+      using TX = decltype(x);
+      using TH = decltype(h);
+      if (a.cols > kBackCols) return launch_long<TX, TH>(a, grid, s);
+      return launch_k(norm_backward_kernel<TX, TH>, dim3(unsigned(grid)), dim3(unsigned(32 * sh.warps * sh.per)), 0, s, a.pdl, a);
     });
     if (err != cudaSuccess || !a.dgain) return err;
   }
-  return launch_k(norm_gain_kernel, dim3(unsigned((a.cols + 31) / 32)), dim3(1024), 0, s, a.pdl, a, parts);
+  return launch_k(norm_gain_kernel, dim3(unsigned((a.cols + 7) / 8)), dim3(1024), 0, s, a.pdl, a, parts);
 }
 
 }  // namespace dg

@@ -697,7 +697,8 @@ gemm_status_t gemm_dequantize(gemm_plan_t plan, int64_t rows, int64_t cols, cons
                               const void* SQ, void* X, int64_t ldx, gemm_type_t x_type, void* stream) {
   const bool four = q_type == GEMM_TYPE_E2M1;
   if (!plan || rows < 0 || cols < 0 || !is_float_type(x_type) || (!four && !is_code_type(q_type))) return GEMM_ERR_INVALID_ARG;
-  if (!size_ok(rows) || !size_ok(cols) || rows * ceil_div(cols, 8) > kMaxDim * 1024) return GEMM_ERR_UNSUPPORTED;
+  if (!size_ok(rows) || !size_ok(cols) || rows * ceil_div(cols, 512) > kMaxDim * 16)  // (its grid)
+    return GEMM_ERR_UNSUPPORTED;
   const int64_t one = 1, cb = four ? ceil_div(cols, 2) : cols;
   if (ldq < std::max(one, cb) || ldx < std::max(one, cols)) return GEMM_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return GEMM_OK;

@@ -11,7 +11,6 @@
 // neighbouring rows.  A row's block is four lanes (two exchanges), a column's block 32 rows of four warps (through shared memory).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
 
 #include <type_traits>
 
@@ -33,10 +32,31 @@ __device__ __forceinline__ uint32_t mx4_byte(uint32_t m) {
 // 2^-e; 0 for a block without a number, whose codes are 0.
 __device__ __forceinline__ float mx4_inverse(uint32_t byte) { return byte == 255u ? 0.f : inverse_scale(byte); }
 
-// The codes of two values times inv, the first one's in the low four bits.  (NaN would become the largest code: a
-// block that holds any has inv = 0, and NaN * 0 is NaN.)
-__device__ __forceinline__ uint32_t mx4_codes2(float a, float b, float inv) {
-  return __nv_cvt_float2_to_fp4x2(make_float2(a * inv, b * inv), __NV_E2M1, cudaRoundNearest);
+// The codes of eight values, the first one's in the low four bits.  (cvt rounds to nearest, ties to the even code, and
+// takes its second value for the low half.)
+__device__ __forceinline__ uint32_t mx4_codes8(float a, float b, float c, float d, float e, float f, float g, float h) {
+  uint32_t out;
+  asm("{\n\t.reg .b8 p, q, r, s;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 r, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n\t"
+      "mov.b32 %0, {p, q, r, s};\n\t}"
+      : "=r"(out)
+      : "f"(a), "f"(b), "f"(c), "f"(d), "f"(e), "f"(f), "f"(g), "f"(h));
+  return out;
+}
+
+// The values of eight codes, two to a word of fp16.
+__device__ __forceinline__ void mx4_values8(uint32_t codes, uint32_t (&v)[4]) {
+  asm("{\n\t.reg .b8 p, q, r, s;\n\t"
+      "mov.b32 {p, q, r, s}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, p;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, q;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, r;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, s;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(codes));
 }
 
 // Eight neighbouring values as they are loaded: 16-bit types two to a word, whose magnitudes' bits are ordered like
@@ -68,9 +88,10 @@ struct Row8 {
       }
       return;
     }
+    if (!DG_IN(a.dbg, p, min(8, a.cols - col) * int(sizeof(T)), DBG_QUANTIZE)) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (col + j >= a.cols || !DG_IN(a.dbg, p + j, int(sizeof(T)), DBG_QUANTIZE)) continue;
+      if (col + j >= a.cols) continue;
       if constexpr (sizeof(T) == 4)
         w[j] = __float_as_uint(p[j]);
       else
@@ -110,11 +131,12 @@ __device__ __forceinline__ uint32_t row_byte(const Row8<T>& v) {
   return byte_of<T>(m);
 }
 
-// Codes of eight values; a block without a number has codes of 0.
-__device__ __forceinline__ uint32_t row_codes(uint32_t byte, float a, float b, float c, float d, float e, float f, float g,
-                                              float h) {
+// Codes of a row's eight values; a block without a number has codes of 0.
+template <typename T>
+__device__ __forceinline__ uint32_t row_codes(uint32_t byte, const Row8<T>& v) {
   const float inv = mx4_inverse(byte);
-  const uint32_t codes = mx4_codes2(a, b, inv) | mx4_codes2(c, d, inv) << 8 | mx4_codes2(e, f, inv) << 16 | mx4_codes2(g, h, inv) << 24;
+  const uint32_t codes = mx4_codes8(v.at(0) * inv, v.at(1) * inv, v.at(2) * inv, v.at(3) * inv, v.at(4) * inv, v.at(5) * inv,
+                                    v.at(6) * inv, v.at(7) * inv);
   return byte == 255u ? 0u : codes;
 }
 
@@ -152,7 +174,7 @@ __global__ void __launch_bounds__(256) quantize_mx4_rows_kernel(const QuantArgs 
       const int col = c0 + 256 * h;
       const Row8<T>& x = v[i][h];
       const uint32_t byte = row_byte<T>(x);
-      const uint32_t c = row_codes(byte, x.at(0), x.at(1), x.at(2), x.at(3), x.at(4), x.at(5), x.at(6), x.at(7));
+      const uint32_t c = row_codes(byte, x);
       uint32_t word = byte | __shfl_down_sync(kAll, byte, 4) << 8;
       word |= __shfl_down_sync(kAll, word, 8) << 16;
       if (src[i] >= 0) store_codes(a, a.q + int64_t(r0 + i) * a.ldq + col / 2, c, (a.cols - col + 1) / 2);
@@ -207,7 +229,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) quantize_mx4_kernel(const Quan
 #pragma unroll
     for (int i = 0; i < kLaneRows; ++i) {
       const uint32_t byte = row_byte<T>(v[i]);
-      const uint32_t c = row_codes(byte, v[i].at(0), v[i].at(1), v[i].at(2), v[i].at(3), v[i].at(4), v[i].at(5), v[i].at(6), v[i].at(7));
+      const uint32_t c = row_codes(byte, v[i]);
       // the word of four blocks, in lanes 0 and 16
       uint32_t word = byte | __shfl_down_sync(kAll, byte, 4) << 8;
       word |= __shfl_down_sync(kAll, word, 8) << 16;
@@ -232,12 +254,15 @@ __global__ void __launch_bounds__(32 * kWarps, 2) quantize_mx4_kernel(const Quan
   __syncthreads();
   {
     const uint2 bytes = *reinterpret_cast<const uint2*>(&col_byte[warp / 4][piece * 8]);
+    uint16_t* const to = turn + piece * 8 * 32 + ((warp * 2 + (lane >> 4)) ^ (piece * 2));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t byte = ((j < 4 ? bytes.x : bytes.y) >> (8 * (j & 3))) & 0xffu;
-      const float inv = mx4_inverse(byte);
-      const uint32_t c = mx4_codes2(v[0].at(j), v[1].at(j), inv) | mx4_codes2(v[2].at(j), v[3].at(j), inv) << 8;
-      turn[(piece * 8 + j) * 32 + ((warp * 2 + (lane >> 4)) ^ (piece * 2))] = uint16_t(byte == 255u ? 0u : c);
+    for (int j = 0; j < 8; j += 2) {  // two columns at a time
+      const uint32_t b0 = ((j < 4 ? bytes.x : bytes.y) >> (8 * (j & 3))) & 0xffu, b1 = ((j < 4 ? bytes.x : bytes.y) >> (8 * (j & 3) + 8)) & 0xffu;
+      const float i0 = mx4_inverse(b0), i1 = mx4_inverse(b1);
+      const uint32_t c = mx4_codes8(v[0].at(j) * i0, v[1].at(j) * i0, v[2].at(j) * i0, v[3].at(j) * i0, v[0].at(j + 1) * i1,
+                                    v[1].at(j + 1) * i1, v[2].at(j + 1) * i1, v[3].at(j + 1) * i1);
+      to[j * 32] = uint16_t(b0 == 255u ? 0u : c);
+      to[(j + 1) * 32] = uint16_t(b1 == 255u ? 0u : c >> 16);
     }
   }
   __syncthreads();
@@ -296,93 +321,114 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7fc00000u : byte << 23);
 }
 
-// A thread takes kPieces pieces of eight values, a warp's width of pieces apart; T: the result's type.
-constexpr int kPieces = 4;
-
-template <typename T, int CODE>
-__global__ void __launch_bounds__(256) dequantize_kernel(const DequantArgs a, uint32_t pieces) {
-  constexpr int BLOCK = CODE == CODE_E2M1 ? 32 : 128, BYTES = CODE == CODE_E2M1 ? 4 : 8;
-  wait_prior_grid();
-  uint32_t w[kPieces][2], byte[kPieces];
-  int row[kPieces], col[kPieces];
-  // (one division a thread: a 64-bit one for each piece took as long as the loads)
-  const uint64_t item = uint64_t(blockIdx.x) * kPieces * 256 + threadIdx.x;
-  uint64_t r = item >> 32 ? item / pieces : uint64_t(uint32_t(item) / pieces);
-  uint32_t c = uint32_t(item - r * pieces);
+// Eight values from their codes (one word of 4-bit ones, two of 8-bit ones) and their scale.
+template <int CODE>
+__device__ __forceinline__ void code_values(uint32_t w0, uint32_t w1, float by, float (&v)[8]) {
+  uint32_t pairs[4];  // fp16, which holds every code's value
+  if constexpr (CODE == CODE_E2M1) {
+    mx4_values8(w0, pairs);
+  } else {
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    row[i] = r < uint64_t(a.rows) ? int(r) : -1;
-    col[i] = int(c) * 8;
-    c += uint32_t(a.step_pieces);
-    r += uint32_t(a.step_rows);
-    if (c >= pieces) c -= pieces, ++r;
-    w[i][0] = w[i][1] = byte[i] = 0u;
-    if (row[i] < 0) continue;
-    const uint8_t* const q = a.q + int64_t(row[i]) * a.ldq + int64_t(col[i]) * BYTES / 8;
-    const int n = CODE == CODE_E2M1 ? min(4, (a.cols - col[i] + 1) / 2) : min(8, a.cols - col[i]);
-    if (DG_IN(a.dbg, q, n, DBG_QUANTIZE)) {
-      if (n == BYTES) {
-        if constexpr (BYTES == 4) {
-          w[i][0] = *reinterpret_cast<const uint32_t*>(q);
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(q);
-          w[i][0] = u.x, w[i][1] = u.y;
-        }
-      } else {
-        for (int j = 0; j < n; ++j) w[i][j / 4] |= uint32_t(q[j]) << (8 * (j & 3));
-      }
+    for (int j = 0; j < 4; ++j) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t((j < 2 ? w0 : w1) >> (16 * (j & 1))),
+                                                       CODE == CODE_E5M2 ? __NV_E5M2 : __NV_E4M3);
+      pairs[j] = uint32_t(h.x) | uint32_t(h.y) << 16;
     }
-    const uint8_t* const s = a.sq + scale_at(row[i], col[i] / BLOCK, a.groups);
-    if (DG_IN(a.dbg, s, 1, DBG_QUANTIZE)) byte[i] = *s;
   }
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    if (row[i] < 0) continue;
-    const float by = scale_value(byte[i]);
-    float v[8];
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&pairs[j]));
+    v[2 * j] = f.x * by, v[2 * j + 1] = f.y * by;
+  }
+}
+
+// A warp takes kValueRows rows of 512 columns, a lane twice eight neighbouring ones: rows' addresses are worked out once, and
+// the second eight's codes, scale and result are a constant further on.  T: the result's type.  (Pieces of eight wherever
+// they fell, each with its own addresses: 8192 x 4096 to bf16 from 4 bits 17.2 us.)
+constexpr int kValueRows = 2;
+
+template <typename T, int CODE>
+__global__ void __launch_bounds__(256) dequantize_kernel(const DequantArgs a, uint32_t chunks) {
+  constexpr int BLOCK = CODE == CODE_E2M1 ? 32 : 128, BYTES = CODE == CODE_E2M1 ? 4 : 8;
+  constexpr int NEXT_SCALE = CODE == CODE_E2M1 ? 1024 : 2;  // bytes from a block's scale to that of the block 256 columns on
+  wait_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const uint64_t warp = uint64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const uint64_t pair = warp >> 32 ? warp / chunks : uint64_t(uint32_t(warp) / chunks);
+  const int r0 = int(pair) * kValueRows, c0 = int(warp - pair * chunks) * 512 + 8 * lane;
+  if (pair * kValueRows >= uint64_t(a.rows)) return;
+  uint32_t w[kValueRows][2][2], byte[kValueRows][2];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      __half2_raw h;
-      if constexpr (CODE == CODE_E2M1) {
-        h = __nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t(w[i][0] >> (4 * j)), __NV_E2M1);
-      } else {
-        h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[i][j / 4] >> (8 * (j & 3))), CODE == CODE_E5M2 ? __NV_E5M2 : __NV_E4M3);
+  for (int i = 0; i < kValueRows; ++i) {
+    const uint8_t* const q = a.q + int64_t(r0 + i) * a.ldq + int64_t(c0) * BYTES / 8;
+    const uint8_t* const s = a.sq + scale_at(r0 + i, c0 / BLOCK, a.groups);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      w[i][h][0] = w[i][h][1] = byte[i][h] = 0u;
+      const int left = r0 + i < a.rows ? a.cols - c0 - 256 * h : 0;
+      const uint8_t* const p = q + 256 * h * BYTES / 8;
+      if (left >= 8) {
+        if (DG_IN(a.dbg, p, BYTES, DBG_QUANTIZE)) {
+          if constexpr (BYTES == 8) {
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
+            w[i][h][0] = u.x, w[i][h][1] = u.y;
+          } else {
+            w[i][h][0] = *reinterpret_cast<const uint32_t*>(p);
+          }
+        }
+      } else if (left > 0) {
+        const int n = CODE == CODE_E2M1 ? (left + 1) / 2 : left;
+        if (DG_IN(a.dbg, p, n, DBG_QUANTIZE)) {
+#pragma unroll
+          for (int j = 0; j < BYTES; ++j)
+            if (j < n) w[i][h][j / 4] |= uint32_t(p[j]) << (8 * (j & 3));
+        }
       }
-      const float2 f = __half22float2(__half2(h));
-      v[j] = f.x * by, v[j + 1] = f.y * by;
+      if (left > 0 && DG_IN(a.dbg, s + NEXT_SCALE * h, 1, DBG_QUANTIZE)) byte[i][h] = s[NEXT_SCALE * h];
     }
-    T* const dst = static_cast<T*>(a.x) + int64_t(row[i]) * a.ldx + col[i];
-    const int n = min(8, a.cols - col[i]);
-    alignas(16) T t[8];
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if constexpr (sizeof(T) == 4) t[j] = v[j];
-      else if constexpr (std::is_same<T, __half>::value) t[j] = __float2half_rn(v[j]);
-      else t[j] = __float2bfloat16_rn(v[j]);
-    }
-    if (!DG_IN(a.dbg, dst, n * int(sizeof(T)), DBG_QUANTIZE)) continue;
-    if (n == 8 && a.wide) {
+  for (int i = 0; i < kValueRows; ++i) {
+    T* const x = static_cast<T*>(a.x) + int64_t(r0 + i) * a.ldx + c0;
 #pragma unroll
-      for (int k = 0; k < int(sizeof(T)) / 2; ++k) reinterpret_cast<uint4*>(dst)[k] = reinterpret_cast<const uint4*>(t)[k];
-    } else {
+    for (int h = 0; h < 2; ++h) {
+      const int left = r0 + i < a.rows ? a.cols - c0 - 256 * h : 0;
+      if (left <= 0) continue;
+      T* const dst = x + 256 * h;
+      float v[8];
+      code_values<CODE>(w[i][h][0], w[i][h][1], scale_value(byte[i][h]), v);
+      alignas(16) T t[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) dst[j] = t[j];
+      for (int j = 0; j < 8; j += 2) {
+        if constexpr (sizeof(T) == 4)
+          t[j] = v[j], t[j + 1] = v[j + 1];
+        else if constexpr (std::is_same<T, __half>::value)
+          *reinterpret_cast<__half2*>(t + j) = __floats2half2_rn(v[j], v[j + 1]);
+        else
+          *reinterpret_cast<__nv_bfloat162*>(t + j) = __floats2bfloat162_rn(v[j], v[j + 1]);
+      }
+      if (!DG_IN(a.dbg, dst, min(8, left) * int(sizeof(T)), DBG_QUANTIZE)) continue;
+      if (left >= 8 && a.wide) {
+#pragma unroll
+        for (int k = 0; k < int(sizeof(T)) / 2; ++k) reinterpret_cast<uint4*>(dst)[k] = reinterpret_cast<const uint4*>(t)[k];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < left) dst[j] = t[j];
+      }
     }
   }
 }
 
 template <typename T>
-cudaError_t launch_values(DequantArgs a, cudaStream_t s) {
-  const uint32_t pieces = uint32_t((a.cols + 7) / 8);
-  a.step_rows = int(256 / pieces);
-  a.step_pieces = int(256 % pieces);
-  const uint64_t items = uint64_t(a.rows) * pieces;
-  const dim3 grid(unsigned((items + 256 * kPieces - 1) / (256 * kPieces)));
+cudaError_t launch_values(const DequantArgs& a, cudaStream_t s) {
+  const uint32_t chunks = uint32_t((a.cols + 511) / 512);
+  const uint64_t warps = uint64_t((a.rows + kValueRows - 1) / kValueRows) * chunks;
+  const dim3 grid(unsigned((warps + 7) / 8));
   switch (a.code) {
-    case CODE_E4M3: return launch_k(dequantize_kernel<T, CODE_E4M3>, grid, dim3(256), 0, s, a.pdl, a, pieces);
-    case CODE_E5M2: return launch_k(dequantize_kernel<T, CODE_E5M2>, grid, dim3(256), 0, s, a.pdl, a, pieces);
-    default: return launch_k(dequantize_kernel<T, CODE_E2M1>, grid, dim3(256), 0, s, a.pdl, a, pieces);
+    case CODE_E4M3: return launch_k(dequantize_kernel<T, CODE_E4M3>, grid, dim3(256), 0, s, a.pdl, a, chunks);
+    case CODE_E5M2: return launch_k(dequantize_kernel<T, CODE_E5M2>, grid, dim3(256), 0, s, a.pdl, a, chunks);
+    default: return launch_k(dequantize_kernel<T, CODE_E2M1>, grid, dim3(256), 0, s, a.pdl, a, chunks);
   }
 }
 
@@ -396,7 +442,7 @@ cudaError_t launch_quantize_mx4(const QuantArgs& a, cudaStream_t s) {
   }
 }
 
-cudaError_t launch_dequantize(DequantArgs a, cudaStream_t s) {
+cudaError_t launch_dequantize(const DequantArgs& a, cudaStream_t s) {
   switch (a.x_kind) {
     case OUT_F32: return launch_values<float>(a, s);
     case OUT_BF16: return launch_values<__nv_bfloat16>(a, s);

@@ -460,14 +460,20 @@ def _scales(t, rows: int, cols: int, groups: int = 1) -> int:
 def _mx4_scales(t, rows: int, cols: int, groups: int = 1) -> int:
     """Pointer of the packed scale bytes of `groups` rows x cols matrices of 4-bit values."""
     need = groups * 512 * (-(-rows // 128) or 1) * (-(-cols // 128) or 1)  # gemm_mx4_scale_bytes
-    if t.element_size() != 1 or t.numel() < need or not t.is_contiguous():
+    if t.numel() < need or t.element_size() != 1 or not t.is_contiguous():
         raise ValueError(f"scales are {need} contiguous bytes")
     return t.data_ptr()
 
 
+_byte_types: list = []
+
+
 def _bytes_of(t):
     """A tensor of 4-bit codes, two to a byte (uint8, or float4_e2m1fn_x2 where torch has it)."""
-    if t.element_size() != 1 or t.is_floating_point() and "float4" not in str(t.dtype) or not t.is_floating_point() and "int8" not in str(t.dtype):
+    if not _byte_types:
+        import torch
+        _byte_types.extend(d for d in (torch.uint8, getattr(torch, "float4_e2m1fn_x2", None)) if d is not None)
+    if t.dtype not in _byte_types:
         raise ValueError("4-bit codes are bytes (uint8) of two")
     return t
 
@@ -487,6 +493,13 @@ def _same_shape(t, rows: int, cols: int, name: str):
     if (r, c) != (rows, cols):
         raise ValueError(f"{name} is {rows} x {cols}")
     return p, ld
+
+
+def _like(t, other, rows: int, cols: int, ld: int, name: str):
+    """_same_shape for a matrix that is laid out like `other` (rows x cols, ld) more often than not: one look at it then."""
+    if t.shape == other.shape and t.stride() == other.stride():
+        return t.data_ptr(), ld
+    return _same_shape(t, rows, cols, name)
 
 
 def _array(t, n: int, dtype: str) -> int:
@@ -667,13 +680,15 @@ class Plan:
         """X (rows x cols) <- the values of 8-bit Q (float8_e4m3fn, float8_e5m2) or of 4-bit Q (bytes of two) with scales SQ."""
         x, rows, cols, ldx = _matrix(X)
         q, r, width, ldq = _matrix(Q)
-        if "float8" in str(Q.dtype):
-            kind, s = _type_of(Q), _scales(SQ, rows, cols)
+        x_type = _type_of(X)
+        kind = _types.get(Q.dtype)
+        if kind == GEMM_TYPE_E4M3 or kind == GEMM_TYPE_E5M2:
+            s = _scales(SQ, rows, cols)
         else:
-            kind, s, cols = GEMM_TYPE_E2M1, _mx4_scales(SQ, rows, cols), _mx4_columns(cols, _bytes_of(Q).shape[1])
-        if r != rows or kind != GEMM_TYPE_E2M1 and width != cols:
+            kind, s, width = GEMM_TYPE_E2M1, _mx4_scales(SQ, rows, cols), _mx4_columns(cols, _bytes_of(Q).shape[1])
+        if r != rows or width != cols:
             raise ValueError("X has Q's rows and columns")
-        return load().gemm_dequantize(self.handle, rows, cols, q, ldq, kind, s, x, ldx, _type_of(X), self._stream(stream))
+        return load().gemm_dequantize(self.handle, rows, cols, q, ldq, kind, s, x, ldx, x_type, self._stream(stream))
 
     # ------------------------------------------- block-scaled 4-bit products
 
@@ -732,22 +747,23 @@ class Plan:
         r = g = h = y = q = sq = rs = None
         ldr = ldh = ldy = ldq = 0
         if residual is not None:
-            r, ldr = _same_shape(residual, rows, cols, "residual")
-            h_type = _type_of(residual)
+            r, ldr = _like(residual, X, rows, cols, ldx, "residual")
+            h_type = _types.get(residual.dtype, -1)
         if H is not None:
-            h, ldh = _same_shape(H, rows, cols, "H")
-            h_type = _type_of(H)
-            if residual is not None and residual.dtype != H.dtype:
+            h, ldh = _like(H, X, rows, cols, ldx, "H")
+            if residual is None:
+                h_type = _types.get(H.dtype, -1)
+            elif residual.dtype is not H.dtype:
                 raise ValueError("H is of the residual's type")
         if gain is not None:
-            g, g_type = _vector(gain, cols), _type_of(gain)
+            g, g_type = _vector(gain, cols), _types.get(gain.dtype, -1)
         if Y is not None:
-            y, ldy = _same_shape(Y, rows, cols, "Y")
-            if Y.dtype != X.dtype:
+            y, ldy = _like(Y, X, rows, cols, ldx, "Y")
+            if Y.dtype is not X.dtype:
                 raise ValueError("Y is of X's type")
         if Q is not None:
             q, ldq = _same_shape(Q, rows, cols, "Q")
-            sq, q_type = _scales(SQ, rows, cols), _type_of(Q)
+            sq, q_type = _scales(SQ, rows, cols), _types.get(Q.dtype, -1)
         if rstd is not None:
             rs = _array(rstd, rows, "float32")
         return load().gemm_norm(self.handle, rows, cols, x, ldx, x_type, r, ldr, h_type, g, g_type, eps, h, ldh, y, ldy,
@@ -756,9 +772,9 @@ class Plan:
     def norm_backward(self, dY, H, gain, rstd, dX, *, dgain=None, dH=None, stream=None) -> int:
         """dX (H's type) and dgain (cols float32) from dY, the kept H and rstd; dH: the gradient that reaches h past the norm."""
         d, rows, cols, lddy = _matrix(dY)
-        h, ldh = _same_shape(H, rows, cols, "H")
-        x, lddx = _same_shape(dX, rows, cols, "dX")
-        p, ldp = (None, 0) if dH is None else _same_shape(dH, rows, cols, "dH")
+        h, ldh = _like(H, dY, rows, cols, lddy, "H")
+        x, lddx = _like(dX, dY, rows, cols, lddy, "dX")
+        p, ldp = (None, 0) if dH is None else _like(dH, dY, rows, cols, lddy, "dH")
         if dX.dtype != H.dtype or dH is not None and dH.dtype != H.dtype:
             raise ValueError("dX and dH are of H's type")
         y_type = _type_of(dY)
