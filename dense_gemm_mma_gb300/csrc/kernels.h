@@ -465,7 +465,7 @@ struct NormArgs {
   int64_t ldq;
   int e5m2, q_groups, rows_padded;
   float* rstd;      // or null
-  int wide;         // rows and gain on 16-byte boundaries
+  int wide;         // bytes of a load that rows' and the gain's alignment allows: 16, 4 or 0 (by value)
   int warps, per;   // warps of a row, rows of a CTA (set by the launcher)
   int pdl;
   DG_DEBUG_FIELD
@@ -495,7 +495,7 @@ struct NormBackArgs {
   int pdl;
   DG_DEBUG_FIELD
 };
-size_t norm_backward_workspace(int64_t rows, int64_t cols, int sms);
+size_t norm_backward_workspace(int x_kind, int h_kind, int64_t rows, int64_t cols, int sms);
 cudaError_t launch_norm_backward(NormBackArgs a, int sms, cudaStream_t s);
 
 // ----------------------------------------------------------------- routing

@@ -7,8 +7,8 @@
 // quantiser's rule, quantize.cu), so that a product's operand needs no pass of its own.  What bounds it is
 // memory: x, r, dy and dh are read once, h, y (or codes) and dx written once.
 //
-// A row stays in registers between its sum of squares and its scaling.  A warp takes 512 columns
-// (four blocks of scales, one word of them) at a time, a lane twice eight neighbouring ones: half a warp holds a
+// A row stays in registers between its sum of squares and its scaling.  A warp takes 256 columns
+// (two blocks of scales) at a time, a lane eight neighbouring ones: half a warp holds a
 // block, whose largest magnitude is four exchanges away.  The row's sum meets in shared memory, one barrier a row.
 // Sums, rho and the normalised values are fp32; y and the codes come from the unrounded sum h, one rounding each
 // (the kept h is rounded on its own way out), and the gradients from the kept h, which is what the
@@ -30,19 +30,6 @@ namespace {
 template <typename T>
 __host__ __device__ constexpr int kind_of() {
   return sizeof(T) == 4 ? OUT_F32 : std::is_same<T, __half>::value ? OUT_F16 : OUT_BF16;
-}
-
-template <typename T>
-__device__ __forceinline__ float to_f(T v) {
-  if constexpr (sizeof(T) == 4) return v;
-  else if constexpr (std::is_same<T, __half>::value) return __half2float(v);
-  else return __bfloat162float(v);
-}
-template <typename T>
-__device__ __forceinline__ T from_f(float v) {
-  if constexpr (sizeof(T) == 4) return v;
-  else if constexpr (std::is_same<T, __half>::value) return __float2half_rn(v);
-  else return __float2bfloat16_rn(v);
 }
 
 // Eight neighbouring values of a row as they are loaded; what is not there is zero.
@@ -81,47 +68,73 @@ struct Eight {
   }
 };
 
-// `left` columns from p to the end of the row (none: nothing is read).  a.wide: p is on a 16-byte boundary, so that eight
-// columns are loaded whole; the last few of a row one by one.
+// `left` columns from p to the end of the row (none: nothing is read).  a.wide: what p's alignment allows, 16 bytes (eight
+// columns are loaded whole), 4 (words, as the last columns of a row always are then) or 0 (value by value).  Words go
+// straight to their registers: a value that has to be put together is waited for at once, which made the
+// loads for the next row no loads ahead (6912 x 2050, gradients: 36.6 us for 113 MB, 8192 x 2048 26.9 for 134).
 template <typename T, typename A>
 __device__ __forceinline__ void load8(const A& a, Eight<T>& o, const T* p, int left, int site) {
   o.clear();
-  if (a.wide && left >= 8) {
+  if (a.wide == 16 && left >= 8) {
     if (DG_IN(a.dbg, p, 8 * int(sizeof(T)), site)) o.load(p);
   } else if (left > 0 && DG_IN(a.dbg, p, min(left, 8) * int(sizeof(T)), site)) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) o.put(i, p[i]);
+      for (int i = 0; i < 8; ++i)
+        if (i < left) o.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    } else if (a.wide) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (2 * i + 1 < left)
+          o.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        else if (2 * i < left)
+          o.w[i] = reinterpret_cast<const uint16_t*>(p)[2 * i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) o.put(i, p[i]);
+    }
   }
 }
 
 template <typename T, typename A>
 __device__ __forceinline__ void store8(const A& a, T* p, const float (&v)[8], int left, int site) {
-  if (a.wide && left >= 8) {
-    Eight<T> o;
-    if constexpr (sizeof(T) == 4) {
+  if (left <= 0 || !DG_IN(a.dbg, p, min(left, 8) * int(sizeof(T)), site)) return;
+  if constexpr (sizeof(T) == 4) {
+    if (a.wide == 16 && left >= 8) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o.w[i] = __float_as_uint(v[i]);
+      for (int i = 0; i < 8; ++i)
+        if (i < left) p[i] = v[i];
+    }
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    if (a.wide == 16 && left >= 8) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if constexpr (std::is_same<T, __half>::value) {
-          const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-          o.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        if (a.wide && 2 * i + 1 < left) {
+          reinterpret_cast<uint32_t*>(p)[i] = w[i];
         } else {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-          o.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+          if (2 * i < left) reinterpret_cast<uint16_t*>(p)[2 * i] = uint16_t(w[i]);
+          if (2 * i + 1 < left) reinterpret_cast<uint16_t*>(p)[2 * i + 1] = uint16_t(w[i] >> 16);
         }
       }
     }
-    if (!DG_IN(a.dbg, p, 8 * int(sizeof(T)), site)) return;
-#pragma unroll
-    for (int i = 0; i < Eight<T>::WORDS / 4; ++i)
-      reinterpret_cast<uint4*>(p)[i] = make_uint4(o.w[4 * i], o.w[4 * i + 1], o.w[4 * i + 2], o.w[4 * i + 3]);
-  } else if (left > 0 && DG_IN(a.dbg, p, min(left, 8) * int(sizeof(T)), site)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = from_f<T>(v[i]);
   }
 }
 
@@ -196,32 +209,34 @@ __device__ __forceinline__ void store_part(const NormBackArgs& a, float* p, cons
 }
 
 // A row's values as they are loaded, a lane's part of it: x and r, or dy, h and dh.
-template <typename TA, typename TB, int G, bool THREE>
+template <typename TA, typename TB, int NE, bool THREE>
 struct RowOf {
-  Eight<TA> a[2 * G];
-  Eight<TB> b[2 * G], c[THREE ? 2 * G : 1];
+  Eight<TA> a[NE];
+  Eight<TB> b[NE], c[THREE ? NE : 1];
 };
 
-// First column of a lane's i-th eight.
+// First column of a lane's i-th eight: two neighbouring 256s of a warp are a word of scales.
+template <int NE>
 __device__ __forceinline__ int column_of(int i, int mine, int warps) {
-  return (mine + i / 2 * warps) * 512 + (i & 1) * 256 + int(threadIdx.x & 31) * 8;
+  const int piece = NE == 1 ? mine : (mine + i / 2 * warps) * 2 + (i & 1);
+  return piece * 256 + int(threadIdx.x & 31) * 8;
 }
 
-// A CTA takes a.per rows at a time, a.warps warps to a row, G groups of 512 columns to a warp; with one group the
+// A CTA takes a.per rows at a time, a.warps warps to a row, NE times 256 columns to a warp; up to two the
 // next rows' loads are under way while it works on one (more leave no registers for that).
-template <typename TX, typename TH, int G>
-__global__ void __launch_bounds__(512, G == 1 && sizeof(TX) == 2 && sizeof(TH) == 2 ? 2 : 1) norm_kernel(const NormArgs a) {
+template <typename TX, typename TH, int NE>
+__global__ void __launch_bounds__(512, NE <= 2 && sizeof(TX) == 2 && sizeof(TH) == 2 ? 2 : 1) norm_kernel(const NormArgs a) {
   __shared__ float sums[2][16];
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int slot = warp / a.warps, mine = warp - slot * a.warps;
   const bool scaled = a.y || a.q;
   const int rows = a.q ? a.rows_padded : a.rows, step = int(gridDim.x) * a.per;
-  auto load = [&](RowOf<TX, TH, G, false>& v, int64_t row) {
+  auto load = [&](RowOf<TX, TH, NE, false>& v, int64_t row) {
     const bool live = row < a.rows;
 #pragma unroll
-    for (int i = 0; i < 2 * G; ++i) {
-      const int col = column_of(i, mine, a.warps), left = live ? a.cols - col : 0;
+    for (int i = 0; i < NE; ++i) {
+      const int col = column_of<NE>(i, mine, a.warps), left = live ? a.cols - col : 0;
       load8(a, v.a[i], static_cast<const TX*>(a.x) + row * a.ldx + col, left, DBG_NORM);
       if (a.r)
         load8(a, v.b[i], static_cast<const TH*>(a.r) + row * a.ldr + col, left, DBG_NORM);
@@ -229,13 +244,13 @@ __global__ void __launch_bounds__(512, G == 1 && sizeof(TX) == 2 && sizeof(TH) =
         v.b[i].clear();
     }
   };
-  RowOf<TX, TH, G, false> next;
-  if constexpr (G == 1) load(next, int64_t(blockIdx.x) * a.per + slot);
-  float gain[G < 4 ? 2 * G : 1][8];
-  if constexpr (G < 4) {  // (four groups of it leave no registers for the rest)
+  RowOf<TX, TH, NE, false> next;
+  if constexpr (NE <= 2) load(next, int64_t(blockIdx.x) * a.per + slot);
+  float gain[NE < 8 ? NE : 1][8];
+  if constexpr (NE < 8) {  // (eight of them leave no registers for the rest)
 #pragma unroll
-    for (int i = 0; i < 2 * G; ++i) {
-      const int col = column_of(i, mine, a.warps);
+    for (int i = 0; i < NE; ++i) {
+      const int col = column_of<NE>(i, mine, a.warps);
       load_gain<TX>(a, gain[i], col, scaled ? a.cols - col : 0);
     }
   }
@@ -243,16 +258,16 @@ __global__ void __launch_bounds__(512, G == 1 && sizeof(TX) == 2 && sizeof(TH) =
   for (int64_t row0 = int64_t(blockIdx.x) * a.per; row0 < rows; row0 += step, turn ^= 1) {
     const int64_t row = row0 + slot;  // past the matrix: only scale bytes, zero
     const bool live = row < a.rows;
-    if constexpr (G > 1) load(next, row);
-    float v[2 * G][8], sum = 0.f;
+    if constexpr (NE > 2) load(next, row);
+    float v[NE][8], sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2 * G; ++i)
+    for (int i = 0; i < NE; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v[i][j] = next.a[i].at(j) + next.b[i].at(j);
         sum = fmaf(v[i][j], v[i][j], sum);
       }
-    if constexpr (G == 1) {
+    if constexpr (NE <= 2) {
       if (row0 + step < rows) load(next, row + step);
     }
     sum = row_sum(sum, sums[turn], slot * a.warps, a.warps);
@@ -260,14 +275,14 @@ __global__ void __launch_bounds__(512, G == 1 && sizeof(TX) == 2 && sizeof(TH) =
     if (live && a.rstd && mine == 0 && lane == 0 && DG_IN(a.dbg, a.rstd + row, 4, DBG_NORM)) a.rstd[row] = rho;
     uint32_t word = 0;
 #pragma unroll
-    for (int i = 0; i < 2 * G; ++i) {
-      const int col = column_of(i, mine, a.warps), group = col >> 9;
+    for (int i = 0; i < NE; ++i) {
+      const int col = column_of<NE>(i, mine, a.warps);
       const int left = live ? a.cols - col : 0;
       if (a.h) store8(a, static_cast<TH*>(a.h) + row * a.ldh + col, v[i], left, DBG_NORM);
       if (!scaled) continue;
-      if constexpr (G == 4) load_gain<TX>(a, gain[0], col, left);
+      if constexpr (NE == 8) load_gain<TX>(a, gain[0], col, left);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rho * gain[G < 4 ? i : 0][j];
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rho * gain[NE < 8 ? i : 0][j];
       if (a.y) store8(a, static_cast<TX*>(a.y) + row * a.ldy + col, v[i], left, DBG_NORM);
       if (a.q) {
         // (what is not there is zero, unless rho is infinite)
@@ -284,34 +299,38 @@ __global__ void __launch_bounds__(512, G == 1 && sizeof(TX) == 2 && sizeof(TH) =
         } else if (left > 0 && DG_IN(a.dbg, dst, left, DBG_NORM)) {
           for (int j = 0; j < left; ++j) dst[j] = uint8_t((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
         }
-        // bytes of blocks 2 (i & 1) and 2 (i & 1) + 1 of the group, in lanes 0 and 16
-        const uint32_t other = __shfl_down_sync(kAll, byte, 16);
-        word = (i & 1 ? word : 0u) | (byte | other << 8) << (16 * (i & 1));
-        if ((i & 1) && lane == 0 && group < a.q_groups && row < a.rows_padded) {
-          uint8_t* const s = a.sq + scale_at(row, int64_t(group) * 4, a.q_groups);
-          if (DG_IN(a.dbg, s, 4, DBG_NORM)) *reinterpret_cast<uint32_t*>(s) = word;
+        // the bytes of both blocks, in lane 0
+        const uint32_t two = byte | __shfl_down_sync(kAll, byte, 16) << 8;
+        word = i & 1 ? word | two << 16 : two;
+        if (lane == 0 && (NE == 1 || (i & 1)) && (col >> 9) < a.q_groups && row < a.rows_padded) {
+          uint8_t* const s = a.sq + scale_at(row, NE == 1 ? col >> 7 : col >> 9 << 2, a.q_groups);
+          if constexpr (NE == 1) {
+            if (DG_IN(a.dbg, s, 2, DBG_NORM)) *reinterpret_cast<uint16_t*>(s) = uint16_t(word);
+          } else {
+            if (DG_IN(a.dbg, s, 4, DBG_NORM)) *reinterpret_cast<uint32_t*>(s) = word;
+          }
         }
       }
     }
   }
 }
 
-// Rows of up to kBackCols columns: a lane's sixteen stay in registers, the next row's loads under way.
+// Rows of up to kBackCols columns: a lane's eight or sixteen stay in registers, the next row's loads under way.
 constexpr int kBackCols = 16 * 512;
 
-template <typename TX, typename TH>
+template <typename TX, typename TH, int NE>
 __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a) {
   __shared__ float sums[2][16];
   wait_prior_grid();
   const int warp = threadIdx.x >> 5;
   const int slot = warp / a.warps, mine = warp - slot * a.warps;
   const int step = int(gridDim.x) * a.per;
-  auto load = [&](RowOf<TX, TH, 1, true>& v, float* rho, int64_t row) {
+  auto load = [&](RowOf<TX, TH, NE, true>& v, float* rho, int64_t row) {
     const bool live = row < a.rows;
     *rho = live && DG_IN(a.dbg, a.rstd + row, 4, DBG_NORM) ? __ldg(a.rstd + row) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int col = column_of(i, mine, a.warps), left = live ? a.cols - col : 0;
+    for (int i = 0; i < NE; ++i) {
+      const int col = column_of<NE>(i, mine, a.warps), left = live ? a.cols - col : 0;
       load8(a, v.a[i], static_cast<const TX*>(a.dy) + row * a.lddy + col, left, DBG_NORM);
       load8(a, v.b[i], static_cast<const TH*>(a.h) + row * a.ldh + col, left, DBG_NORM);
       if (a.dh)
@@ -320,13 +339,13 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a
         v.c[i].clear();
     }
   };
-  RowOf<TX, TH, 1, true> now, next;
+  RowOf<TX, TH, NE, true> now, next;
   float rho_next;
   load(next, &rho_next, int64_t(blockIdx.x) * a.per + slot);
-  float gain[2][8], acc[2][8];
+  float gain[NE][8], acc[NE][8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int col = column_of(i, mine, a.warps);
+  for (int i = 0; i < NE; ++i) {
+    const int col = column_of<NE>(i, mine, a.warps);
     load_gain<TX>(a, gain[i], col, a.cols - col);
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
@@ -340,7 +359,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a
     if (row0 + step < a.rows) load(next, &rho_next, row + step);
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NE; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float xhat = now.b[i].at(j) * rho, d = now.a[i].at(j);
@@ -350,8 +369,8 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a
     sum = row_sum(sum, sums[turn], slot * a.warps, a.warps);
     const float mean = __fdiv_rn(sum, float(a.cols));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int col = column_of(i, mine, a.warps);
+    for (int i = 0; i < NE; ++i) {
+      const int col = column_of<NE>(i, mine, a.warps);
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -360,10 +379,31 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackArgs a
     }
   }
   if (!a.parts) return;
-  float* const part = a.parts + (int64_t(blockIdx.x) * a.per + slot) * a.part_cols;
+  // the CTA's rows together, in the order of their slots (several only where four warps have a row each or two rows)
+  __shared__ float room[4 * 2 * 256];
+  for (int k = 1; k < a.per; ++k) {
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int col = column_of(i, mine, a.warps);
+    for (int i = 0; i < NE; ++i) {
+      float* const at = room + column_of<NE>(i, mine, a.warps);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (slot == k) at[j] = acc[i][j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const float* const at = room + column_of<NE>(i, mine, a.warps);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (slot == 0) acc[i][j] += at[j];
+    }
+  }
+  if (slot > 0) return;
+  float* const part = a.parts + int64_t(blockIdx.x) * a.part_cols;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int col = column_of<NE>(i, mine, a.warps);
     if (col < a.part_cols) store_part(a, part + col, acc[i]);
   }
 }
@@ -451,33 +491,53 @@ __global__ void __launch_bounds__(1024) norm_gain_kernel(const NormBackArgs a, i
   if (DG_IN(a.dbg, a.dgain + col, 4, DBG_NORM)) a.dgain[col] = s;
 }
 
-// Warps to a row and groups to a warp, for `cols` columns; rows to a CTA, so that it has four warps at least.
+// Warps to a row, each with `ne` times 256 columns (codes: whole words of scales, 512 columns), and rows to a CTA, so that it
+// has four warps at least.  256 columns a warp up to 16 warps, which is latency's best (1 x 4096: 2.1 us, with 512 a warp 2.4;
+// 8192 x 4096 bf16 44.4 and 47.9), except where more warps cost more than they hide: codes of many rows
+// (8192 x 4096: 50.3, with 512 a warp 48.8) and the gradients of 16-bit rows (8192 x 4096: 60.1 and 49.3; 32-bit 87.6 and 101).
+enum Form : int { FORM_PLAIN, FORM_CODES, FORM_BACK16, FORM_BACK32 };
 struct Shape {
-  int g, warps, per;
+  int ne, warps, per;
 };
-Shape shape_of(int cols, int most_warps, int64_t rows) {
-  const int groups = (cols + 511) / 512;
+Shape shape_of(int cols, Form form, int64_t rows) {
+  const int pieces = form == FORM_CODES ? (cols + 511) / 512 * 2 : (cols + 255) / 256;
+  const int most = form == FORM_BACK16 || (form == FORM_CODES && rows > 1024) ? 4 : 16;
   Shape s;
-  s.g = groups <= most_warps ? 1 : groups <= 2 * most_warps ? 2 : 4;
-  s.warps = (groups + s.g - 1) / s.g;
+  s.ne = pieces <= most ? 1 : pieces <= 32 ? 2 : pieces <= 64 ? 4 : 8;
+  s.warps = (pieces + s.ne - 1) / s.ne;
   s.per = int(std::max<int64_t>(1, std::min<int64_t>(4 / s.warps, rows)));
   return s;
 }
 
-// CTAs of the forward kernel that an SM holds at once, looked up once for each number of warps.
-template <typename TX, typename TH, int G>
-int norm_ctas(int threads) {
-  static std::atomic<int> known[17];
+Shape back_shape(int x_kind, int64_t cols, int64_t rows) {
+  return shape_of(int(cols), x_kind == OUT_F32 ? FORM_BACK32 : FORM_BACK16, rows);
+}
+
+// CTAs of a kernel that an SM holds at once; `known`: the kernel's, by warps, looked up once each.
+template <typename K>
+int resident(K kern, int threads, size_t smem, std::atomic<int>* known) {
   std::atomic<int>& k = known[threads / 32];
   int n = k.load(std::memory_order_relaxed);
   if (n > 0) return n;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_kernel<TX, TH, G>, threads, 0) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess) {
     cudaGetLastError();
     n = 1;
   }
   n = std::max(1, n);
   k.store(n, std::memory_order_relaxed);
   return n;
+}
+
+template <typename TX, typename TH, int NE>
+int norm_ctas(int threads) {
+  static std::atomic<int> known[17];
+  return resident(norm_kernel<TX, TH, NE>, threads, 0, known);
+}
+
+template <typename TX, typename TH, int NE>
+int norm_backward_ctas(int threads) {
+  static std::atomic<int> known[17];
+  return resident(norm_backward_kernel<TX, TH, NE>, threads, 0, known);
 }
 
 template <typename F>
@@ -488,21 +548,22 @@ cudaError_t by_types(int x_kind, int h_kind, F f) {
 }
 
 template <typename F>
-cudaError_t by_groups(int g, F f) {
-  if (g == 1) return f(std::integral_constant<int, 1>{});
-  if (g == 2) return f(std::integral_constant<int, 2>{});
-  return f(std::integral_constant<int, 4>{});
+cudaError_t by_eights(int ne, F f) {
+  if (ne == 1) return f(std::integral_constant<int, 1>{});
+  if (ne == 2) return f(std::integral_constant<int, 2>{});
+  if (ne == 4) return f(std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, 8>{});
 }
 
 }  // namespace
 
 cudaError_t launch_norm(NormArgs a, int sms, cudaStream_t s) {
   const int64_t rows = a.q ? a.rows_padded : a.rows;
-  const Shape sh = shape_of(a.cols, 16, rows);
+  const Shape sh = shape_of(a.cols, a.q ? FORM_CODES : FORM_PLAIN, rows);
   a.warps = sh.warps;
   a.per = sh.per;
   return by_types(a.x_kind, a.h_kind, [&](auto x, auto h) {
-    return by_groups(sh.g, [&](auto g) {
+    return by_eights(sh.ne, [&](auto g) {
       const int64_t fit =
           int64_t(sms) * norm_ctas<decltype(x), decltype(h), decltype(g)::value>(32 * sh.warps * sh.per);
       return launch_k(norm_kernel<decltype(x), decltype(h), decltype(g)::value>, dim3(unsigned(std::min((rows + sh.per - 1) / sh.per, fit))), dim3(unsigned(32 * sh.warps * sh.per)),
@@ -511,16 +572,24 @@ cudaError_t launch_norm(NormArgs a, int sms, cudaStream_t s) {
   });
 }
 
-// Rows' partial sums of the gain's gradient that the launch below makes, and its CTAs.  (16 warps an SM: 128 registers a thread.)
-static int norm_parts(int64_t rows, int cols, int sms, int* grid) {
-  const Shape sh = shape_of(cols, 16, rows);
-  *grid = int(std::min<int64_t>((rows + sh.per - 1) / sh.per, int64_t(sms) * std::max(1, 16 / (sh.warps * sh.per))));
-  return *grid * sh.per;
+// CTAs of the gradients' first launch, each of which leaves one part of the gain's: those that are resident at once (long
+// rows: as many as an SM's shared memory holds the sums of).
+static int norm_backward_grid(int x_kind, int h_kind, int64_t rows, int64_t cols, int sms) {
+  const Shape sh = back_shape(x_kind, cols, rows);
+  int fit = int(std::max<int64_t>(1, 200 * 1024 / (cols * 4)));
+  if (cols <= kBackCols)
+    by_types(x_kind, h_kind, [&](auto x, auto h) {
+      using TX = decltype(x);
+      using TH = decltype(h);
+      const int threads = 32 * sh.warps * sh.per;
+      fit = sh.ne == 1 ? norm_backward_ctas<TX, TH, 1>(threads) : norm_backward_ctas<TX, TH, 2>(threads);
+      return cudaSuccess;
+    });
+  return int(std::min<int64_t>((rows + sh.per - 1) / sh.per, int64_t(sms) * fit));
 }
 
-size_t norm_backward_workspace(int64_t rows, int64_t cols, int sms) {
-  int grid;
-  return size_t(norm_parts(rows, int(cols), sms, &grid)) * size_t((cols + 7) / 8 * 8) * 4;
+size_t norm_backward_workspace(int x_kind, int h_kind, int64_t rows, int64_t cols, int sms) {
+  return size_t(norm_backward_grid(x_kind, h_kind, rows, cols, sms)) * size_t((cols + 7) / 8 * 8) * 4;
 }
 
 namespace {
@@ -544,9 +613,8 @@ cudaError_t launch_long(const NormBackArgs& a, int grid, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_norm_backward(NormBackArgs a, int sms, cudaStream_t s) {
-  int grid = 0;
-  const int parts = norm_parts(a.rows, a.cols, sms, &grid);
-  const Shape sh = shape_of(a.cols, 16, a.rows);
+  const int grid = norm_backward_grid(a.x_kind, a.h_kind, a.rows, a.cols, sms);
+  const Shape sh = back_shape(a.x_kind, a.cols, a.rows);
   a.warps = sh.warps;
   a.per = sh.per;
   a.part_cols = (a.cols + 7) / 8 * 8;
@@ -556,11 +624,11 @@ cudaError_t launch_norm_backward(NormBackArgs a, int sms, cudaStream_t s) {
       using TX = decltype(x);
       using TH = decltype(h);
       if (a.cols > kBackCols) return launch_long<TX, TH>(a, grid, s);
-      return launch_k(norm_backward_kernel<TX, TH>, dim3(unsigned(grid)), dim3(unsigned(32 * sh.warps * sh.per)), 0, s, a.pdl, a);
+      return launch_k(sh.ne == 1 ? norm_backward_kernel<TX, TH, 1> : norm_backward_kernel<TX, TH, 2>, dim3(unsigned(grid)), dim3(unsigned(32 * sh.warps * sh.per)), 0, s, a.pdl, a);
     });
     if (err != cudaSuccess || !a.dgain) return err;
   }
-  return launch_k(norm_gain_kernel, dim3(unsigned((a.cols + 7) / 8)), dim3(1024), 0, s, a.pdl, a, parts);
+  return launch_k(norm_gain_kernel, dim3(unsigned((a.cols + 7) / 8)), dim3(1024), 0, s, a.pdl, a, grid);
 }
 
 }  // namespace dg

@@ -6,6 +6,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
+#include <utility>
 
 #include "ops.h"
 
@@ -16,6 +18,14 @@ namespace {
 // A result that takes an input's own place: a lane reads its columns of a row before it writes them.
 bool in_place(const void* out, int64_t ldo, gemm_type_t to, const void* in, int64_t ldi, gemm_type_t ti) {
   return out && out == in && ldo == ldi && to == ti;
+}
+
+// Bytes of loads and stores that each matrix's address (none: anything) and bytes between rows allow: 16, 4 or 0.
+int access_of(std::initializer_list<std::pair<const void*, int64_t>> rows) {
+  int wide = 16;
+  for (const auto& m : rows)
+    while (m.first && wide && (!aligned(m.first, size_t(wide)) || m.second % wide)) wide = wide == 16 ? 4 : 0;
+  return wide;
 }
 
 // x_type and h_type, the sizes and the gain.
@@ -83,8 +93,7 @@ gemm_status_t gemm_norm(gemm_plan_t plan, int64_t rows, int64_t cols, const void
   a.q_groups = int(scale_groups(cols));
   a.rows_padded = int(std::min<int64_t>(round_up(rows, 128), kMaxDim));
   a.rstd = rstd;
-  a.wide = rows_wide(X, ldx, xe) && (!residual || rows_wide(residual, ldr, he)) && (!H || rows_wide(H, ldh, he)) &&
-           (!Y || rows_wide(Y, ldy, xe)) && aligned(gain, 16);
+  a.wide = access_of({{X, ldx * xe}, {residual, ldr * he}, {H, ldh * he}, {Y, ldy * xe}, {gain, 0}});
   a.pdl = plan->pdl;
 #ifdef DG_DEBUG
   a.dbg = Spans(plan->err).matrix(X, rows, cols, ldx, xe).matrix(residual, residual ? rows : 0, cols, ldr, he)
@@ -121,7 +130,7 @@ gemm_status_t gemm_norm_backward(gemm_plan_t plan, int64_t rows, int64_t cols, c
                        dH ? " dH" : "", dgain ? " dgain" : "");
   DeviceGuard guard(plan->device);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const size_t ws = dgain && rows > 0 ? norm_backward_workspace(rows, cols, plan->sms) : 0;
+  const size_t ws = dgain && rows > 0 ? norm_backward_workspace(type_kind(x_type), type_kind(h_type), rows, cols, plan->sms) : 0;
   if (ws > 0) {
     const gemm_status_t grown = ensure_ws(plan, ws, s);
     if (grown != GEMM_OK) return grown;
@@ -144,8 +153,7 @@ gemm_status_t gemm_norm_backward(gemm_plan_t plan, int64_t rows, int64_t cols, c
   a.lddx = lddx;
   a.dgain = dgain;
   a.parts = static_cast<float*>(plan->ws);
-  a.wide = rows_wide(dY, lddy, xe) && rows_wide(H, ldh, he) && (!dH || rows_wide(dH, lddh, he)) && rows_wide(dX, lddx, he) &&
-           aligned(gain, 16);
+  a.wide = access_of({{dY, lddy * xe}, {H, ldh * he}, {dH, lddh * he}, {dX, lddx * he}, {gain, 0}});
   a.pdl = plan->pdl;
 #ifdef DG_DEBUG
   a.dbg = Spans(plan->err).matrix(dY, rows, cols, lddy, xe).matrix(H, rows, cols, ldh, he).bytes(gain, gain ? cols * ge : 0)
