@@ -437,6 +437,7 @@ struct DequantArgs {
   int64_t ldx;
   int x_kind;
   int wide;      // rows of X on 16-byte boundaries
+  int q_wide;    // eight codes of a row on a boundary of their size
   int pdl;
   DG_DEBUG_FIELD
 };

@@ -704,7 +704,7 @@ gemm_status_t gemm_dequantize(gemm_plan_t plan, int64_t rows, int64_t cols, cons
   if (rows == 0 || cols == 0) return GEMM_OK;
   if (!Q || !SQ || !X) return GEMM_ERR_INVALID_ARG;
   const int64_t es = type_bytes(x_type), sq = (four ? mx4_scale_tiles(rows, cols) : scale_tiles(rows, cols)) * 512;
-  if (!aligned(Q, 16) || ldq % 16 || !aligned(SQ, 16) || !aligned(X, size_t(es))) return GEMM_ERR_ALIGNMENT;
+  if (!aligned(SQ, 16) || !aligned(X, size_t(es))) return GEMM_ERR_ALIGNMENT;
   if (results_meet({region(X, rows, cols, ldx, es)}, {region(Q, rows, cb, ldq, 1), run_of(SQ, sq)})) return GEMM_ERR_INVALID_ARG;
   const CallScope call(plan, "gemm_dequantize %lldx%lld %s->%s", (long long)rows, (long long)cols, four ? "mx4" : type_name(q_type),
                        type_name(x_type));
@@ -713,6 +713,7 @@ gemm_status_t gemm_dequantize(gemm_plan_t plan, int64_t rows, int64_t cols, cons
   a.q = static_cast<const uint8_t*>(Q);
   a.ldq = ldq;
   a.sq = static_cast<const uint8_t*>(SQ);
+  a.q_wide = aligned(Q, four ? 4 : 8) && ldq % (four ? 4 : 8) == 0;
   a.code = four ? CODE_E2M1 : q_type == GEMM_TYPE_E5M2 ? CODE_E5M2 : CODE_E4M3;
   a.rows = int(rows);
   a.cols = int(cols);

@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const DequantArgs a, ui
       w[i][h][0] = w[i][h][1] = byte[i][h] = 0u;
       const int left = r0 + i < a.rows ? a.cols - c0 - 256 * h : 0;
       const uint8_t* const p = q + 256 * h * BYTES / 8;
-      if (left >= 8) {
+      if (left >= 8 && a.q_wide) {
         if (DG_IN(a.dbg, p, BYTES, DBG_QUANTIZE)) {
           if constexpr (BYTES == 8) {
             const uint2 u = *reinterpret_cast<const uint2*>(p);
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const DequantArgs a, ui
           }
         }
       } else if (left > 0) {
-        const int n = CODE == CODE_E2M1 ? (left + 1) / 2 : left;
+        const int n = min(BYTES, CODE == CODE_E2M1 ? (left + 1) / 2 : left);
         if (DG_IN(a.dbg, p, n, DBG_QUANTIZE)) {
 #pragma unroll
           for (int j = 0; j < BYTES; ++j)

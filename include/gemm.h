@@ -548,8 +548,8 @@ gemm_status_t gemm_quantize_mx4(gemm_plan_t plan, int64_t rows, int64_t cols, co
  * gemm_quantize's tiles, GEMM_TYPE_E2M1 with those of 4 bits) times their scales, to GEMM_TYPE_BF16, F16 or F32.  Products with the
  * scale are exact in fp32 unless they leave its range; one rounding to X's type, which is exact too for bf16 and fp32 while the values
  * stay within their normal numbers.  The way back from weights kept in 8 or 4 bits to gemm_run's operands.
- * Q and SQ 16-byte aligned, ldq (bytes) a multiple of 16, X aligned to its element (rows on 16-byte boundaries are
- * faster); X may share no byte with Q or SQ. */
+ * Q at any address, rows ldq bytes apart (8 codes on a boundary of their size are read fastest), SQ 16-byte aligned, X
+ * aligned to its element (rows on 16-byte boundaries are faster); X may share no byte with Q or SQ. */
 gemm_status_t gemm_dequantize(gemm_plan_t plan, int64_t rows, int64_t cols, const void* Q, int64_t ldq, gemm_type_t q_type,
                               const void* SQ, void* X, int64_t ldx, gemm_type_t x_type, void* stream);
 
