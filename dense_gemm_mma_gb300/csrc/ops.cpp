@@ -654,9 +654,7 @@ gemm_status_t gemm_quantize_mx4(gemm_plan_t plan, int64_t rows, int64_t cols, co
   if (rows == 0 || cols == 0) return GEMM_OK;
   const int64_t xr = rowmap ? src_rows : rows, es = type_bytes(x_type);
   if (!X && xr > 0) return GEMM_ERR_INVALID_ARG;
-  if (!aligned(X, size_t(es)) || !aligned(rowmap, 4) || !aligned(Q, 16) || !aligned(SQ, 16) || !aligned(QT, 16) ||
-      !aligned(SQT, 16) || (Q && ldq % 16) || (QT && ldqt % 16))
-    return GEMM_ERR_ALIGNMENT;
+  if (!aligned(X, size_t(es)) || !aligned(rowmap, 4) || !aligned(SQ, 16) || !aligned(SQT, 16)) return GEMM_ERR_ALIGNMENT;
   const int64_t sq = mx4_scale_tiles(rows, cols) * 512, sqt = mx4_scale_tiles(cols, rows) * 512;
   // no result may share a byte with X, the map or another result
   if (results_meet({region(Q, Q ? rows : 0, cb, ldq, 1), run_of(SQ, sq), region(QT, QT ? cols : 0, rb, ldqt, 1), run_of(SQT, sqt)},
@@ -682,6 +680,8 @@ gemm_status_t gemm_quantize_mx4(gemm_plan_t plan, int64_t rows, int64_t cols, co
   a.sqt = static_cast<uint8_t*>(SQT);
   a.ldq = ldq;
   a.ldqt = ldqt;
+  a.q_wide = aligned(Q, 4) && ldq % 4 == 0;
+  a.qt_wide = rows_wide(QT, ldqt, 1);
   a.q_groups = int(mx4_scale_tiles(1, cols));
   a.qt_groups = int(mx4_scale_tiles(1, rows));
   a.pdl = plan->pdl;

@@ -140,12 +140,12 @@ __device__ __forceinline__ uint32_t row_codes(uint32_t byte, const Row8<T>& v) {
   return byte == 255u ? 0u : codes;
 }
 
-// `n` bytes of a word, or all four.
+// `n` bytes of a word, or all four: as a word where rows allow it.
 __device__ __forceinline__ void store_codes(const QuantArgs& a, uint8_t* dst, uint32_t c, int n) {
-  if (n >= 4) {
+  if (n >= 4 && a.q_wide) {
     if (DG_IN(a.dbg, dst, 4, DBG_QUANTIZE)) *reinterpret_cast<uint32_t*>(dst) = c;
-  } else if (n > 0 && DG_IN(a.dbg, dst, n, DBG_QUANTIZE)) {
-    for (int j = 0; j < n; ++j) dst[j] = uint8_t(c >> (8 * j));
+  } else if (n > 0 && DG_IN(a.dbg, dst, min(n, 4), DBG_QUANTIZE)) {
+    for (int j = 0; j < min(n, 4); ++j) dst[j] = uint8_t(c >> (8 * j));
   }
 }
 
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) quantize_mx4_kernel(const Quan
       uint8_t* const dst = a.qt + int64_t(out_row) * a.ldqt + r / 2;
       const int n = min(16, (a.rows - r + 1) / 2);
       if (DG_IN(a.dbg, dst, n, DBG_QUANTIZE)) {
-        if (n == 16) {
+        if (n == 16 && a.qt_wide) {
           *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
 #pragma unroll

@@ -539,7 +539,8 @@ int64_t gemm_mx4_scale_bytes(int64_t rows, int64_t cols);
  * A scale is the least power of two, 2^-127 at least, with which the block's largest magnitude stays within 6; a code is
  * the value over the scale, rounded to nearest, ties to the even code.  A block of zeros has the scale byte 0, one
  * that holds an infinity or NaN the byte 255 and codes of 0.
- * rowmap, map_div and src_rows, alignment, aliasing and limits as in gemm_quantize. */
+ * Q and QT at any address, rows any number of bytes apart (16-byte boundaries are fastest, and spare the products a
+ * copy); otherwise alignment, rowmap, map_div, src_rows, aliasing and limits as in gemm_quantize. */
 gemm_status_t gemm_quantize_mx4(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx,
                                 gemm_type_t x_type, const int32_t* rowmap, int64_t map_div, int64_t src_rows, void* Q,
                                 int64_t ldq, void* SQ, void* QT, int64_t ldqt, void* SQT, void* stream);
