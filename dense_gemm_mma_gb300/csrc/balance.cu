@@ -18,9 +18,7 @@
 namespace dg {
 namespace {
 
-constexpr int kBuffers = 4;  // warps that add to the CTA's sums at a time
-
-// Warps of a CTA of the sums: with 16 or 32 experts a lane as many as there are registers for.
+// Warps of a CTA of the sums at most: with 16 or 32 experts a lane as many as there are registers for.
 template <int P>
 __host__ __device__ constexpr int balance_warps() {
   return P <= 8 ? 32 : 16;
@@ -57,58 +55,36 @@ __device__ __forceinline__ void token_shares(const BalanceArgs& a, const float (
   for (int i = 0; i < P; ++i) p[i] *= by;
 }
 
-__device__ __forceinline__ float block_sum(float v, float* sums) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.f;
-  for (int i = 0; i < int(blockDim.x >> 5); ++i) v += sums[i];
-  return v;
-}
-
+// What bounds few tokens, and half of the time of many, is the chain behind the last token, so it has few barriers: the
+// warps' sums side by side in shared memory, a thread an expert adds them up; the choices' number and the loss's sum in one
+// reduction.
 template <int P>
 __global__ void __launch_bounds__(32 * balance_warps<P>(), 1) balance_kernel(const BalanceArgs a) {
   constexpr int W = balance_warps<P>(), E = 32 * P;
-  constexpr int ROOM = E > 1024 / kBuffers ? kBuffers * E : 1024;
-  __shared__ float room[ROOM];
-  float(*const total)[E] = reinterpret_cast<float(*)[E]>(room);
+  constexpr int ROWS = W * E <= 8192 ? W : 8192 / E;  // warps whose sums shared memory takes at once: all, or half
+  __shared__ float room[ROWS * E];
   __shared__ int count[E];
   __shared__ int tokens;
-  __shared__ float sums[W];
+  __shared__ float loss_sums[W];
+  __shared__ int n_sums[W];
   __shared__ unsigned ticket;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int threads = int(blockDim.x), warps = threads >> 5;
   const int run = (a.experts + 31) / 32, first = lane * run;
-  for (int e = threadIdx.x; e < E; e += 32 * W) {
-    count[e] = 0;
-#pragma unroll
-    for (int b = 0; b < kBuffers; ++b) total[b][e] = 0.f;
-  }
+  for (int e = threadIdx.x; e < E; e += threads) count[e] = 0;
   if (threadIdx.x == 0) tokens = 0;
   __syncthreads();
   wait_prior_grid();
-  // the next token's logits and choice are under way while a warp works on one (16 experts a lane and more: no registers)
-  constexpr int AHEAD = P <= 8 ? 1 : 0;
-  const int64_t step = int64_t(gridDim.x) * W;
-  float acc[P], next[P];
+  float acc[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) acc[i] = 0.f;
-  int mine = 0, chosen = -1;
-  auto load = [&](int64_t t) {
-    load_logits(a, int(t), first, run, a.wide, next);
-    chosen = choice(a, int(t), lane);
-  };
-  const int64_t t0 = int64_t(blockIdx.x) * W + warp;
-  if (AHEAD && t0 < a.tokens) load(t0);
-  for (int64_t t = t0; t < a.tokens; t += step) {
+  int mine = 0;
+  for (int64_t t = int64_t(blockIdx.x) * warps + warp; t < a.tokens; t += int64_t(gridDim.x) * warps) {
     float x[P], p[P];
-    if (!AHEAD) load(t);
-#pragma unroll
-    for (int i = 0; i < P; ++i) x[i] = next[i];
-    const int expert = chosen;
-    if (AHEAD && t + step < a.tokens) load(t + step);
-    const bool live = __any_sync(kAll, expert >= 0);
+    load_logits(a, int(t), first, run, a.wide, x);
+    const int expert = choice(a, int(t), lane);
+    if (!__any_sync(kAll, expert >= 0)) continue;
     if (expert >= 0) atomicAdd(count + expert, 1);
-    if (!live) continue;
     float top = kNegInf;
 #pragma unroll
     for (int i = 0; i < P; ++i) top = fmaxf(top, x[i]);
@@ -119,20 +95,37 @@ __global__ void __launch_bounds__(32 * balance_warps<P>(), 1) balance_kernel(con
     for (int i = 0; i < P; ++i) acc[i] += p[i];
   }
   if (lane == 0 && mine) atomicAdd(&tokens, mine);
-  for (int w = 0; w < W; w += kBuffers) {  // expert first + i of lane `lane`
-    if (warp / kBuffers == w / kBuffers)
+  auto put = [&](int row) {  // expert first + i of lane `lane`
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (i < run) room[row * E + first + i] = acc[i];
+  };
+  if constexpr (ROWS < W) {  // the upper half's sums to the lower half
+    if (warp >= ROWS) put(warp - ROWS);
+    __syncthreads();
+    if (warp < ROWS && warp + ROWS < warps) {
 #pragma unroll
       for (int i = 0; i < P; ++i)
-        if (i < run) total[warp % kBuffers][first + i] += acc[i];
+        if (i < run) acc[i] += room[warp * E + first + i];
+    }
     __syncthreads();
   }
-  auto cta_sum = [&](int e) { return (total[0][e] + total[1][e]) + (total[2][e] + total[3][e]); };
-  const bool alone = gridDim.x == 1;
-  int sum_lots = kBuffers, lot_stride = E;  // where the sums' lots are
-  if (!alone) {
+  if (warp < ROWS) put(warp);
+  __syncthreads();
+  int lots = min(ROWS, warps), stride = E;  // where the sums lie
+  auto sum_of = [&](int e) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // (in eight chains: an order that depends on the sizes alone)
+    int l = 0;
+    for (; l + 8 <= lots; l += 8)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += room[(l + j) * stride + e];
+    for (int j = 0; l < lots; ++l, ++j) v[0] += room[l * stride + e];
+    return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+  };
+  if (gridDim.x > 1) {
     float* const part = a.parts + int64_t(blockIdx.x) * a.experts;
-    for (int e = threadIdx.x; e < a.experts; e += 32 * W) {
-      if (DG_IN(a.dbg, part + e, 4, DBG_ROUTE)) part[e] = cta_sum(e);
+    for (int e = threadIdx.x; e < a.experts; e += threads) {
+      if (DG_IN(a.dbg, part + e, 4, DBG_ROUTE)) part[e] = sum_of(e);
       if (count[e] && DG_IN(a.dbg, a.counters + 2 + e, 4, DBG_ROUTE)) atomicAdd(a.counters + 2 + e, unsigned(count[e]));
     }
     if (threadIdx.x == 0 && DG_IN(a.dbg, a.counters + 1, 4, DBG_ROUTE)) atomicAdd(a.counters + 1, unsigned(tokens));
@@ -142,21 +135,7 @@ __global__ void __launch_bounds__(32 * balance_warps<P>(), 1) balance_kernel(con
     __syncthreads();
     if (ticket != gridDim.x - 1) return;
     __threadfence();
-    // the parts: `lots` threads an expert, every lots-th CTA's to a lot; then the lots in their order
-    const int lots = max(kBuffers, min(32, ROOM / a.experts));
-    for (int i = threadIdx.x; i < lots * a.experts; i += 32 * W) {
-      const int e = i % a.experts, lot = i / a.experts;
-      float s = 0.f;
-#pragma unroll 16
-      for (int c = lot; c < int(gridDim.x); c += lots) {
-        const float* const at = a.parts + int64_t(c) * a.experts + e;
-        s += DG_IN(a.dbg, at, 4, DBG_ROUTE) ? __ldcg(at) : 0.f;
-      }
-      room[i] = s;
-    }
-    sum_lots = lots;
-    lot_stride = a.experts;
-    for (int e = threadIdx.x; e < a.experts; e += 32 * W) {
+    for (int e = threadIdx.x; e < a.experts; e += threads) {
       if (!DG_IN(a.dbg, a.counters + 2 + e, 4, DBG_ROUTE)) continue;
       count[e] = int(__ldcg(a.counters + 2 + e));
       a.counters[2 + e] = 0u;
@@ -165,30 +144,55 @@ __global__ void __launch_bounds__(32 * balance_warps<P>(), 1) balance_kernel(con
       tokens = int(__ldcg(a.counters + 1));
       a.counters[0] = a.counters[1] = 0u;
     }
+    // the parts: every lots-th CTA's to a lot, a thread a lot of an expert; then the lots in their order
+    lots = max(1, min(32, threads / a.experts));
+    stride = a.experts;
+    for (int i = threadIdx.x; i < lots * a.experts; i += threads) {
+      const int e = i % a.experts, lot = i / a.experts;
+      float s = 0.f;
+      for (int c0 = lot; c0 < int(gridDim.x); c0 += 10 * lots) {  // (ten loads together, whatever is left)
+        float v[10];
+#pragma unroll
+        for (int j = 0; j < 10; ++j) {
+          const int c = c0 + j * lots;
+          const float* const at = a.parts + int64_t(c) * a.experts + e;
+          v[j] = c < int(gridDim.x) && DG_IN(a.dbg, at, 4, DBG_ROUTE) ? __ldcg(at) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 10; ++j) s += v[j];
+      }
+      room[i] = s;
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  // n: whole numbers below 2^31
+  // shares; n (whole numbers below 2^31) and the sum of counts times shares
+  const float m = float(max(tokens, 1));
   int n = 0;
-  for (int e = threadIdx.x; e < a.experts; e += 32 * W) n += count[e];
-  n = __reduce_add_sync(kAll, n);
-  __shared__ int ns[W];
-  if (lane == 0) ns[warp] = n;
-  __syncthreads();
-  n = 0;
-  for (int w = 0; w < W; ++w) n += ns[w];
-  const float m = float(max(tokens, 1)), all = float(max(n, 1)), by = a.scale * float(a.experts);
-  float loss = 0.f;
-  for (int e = threadIdx.x; e < a.experts; e += 32 * W) {
-    float sum = 0.f;
-    for (int l = 0; l < sum_lots; ++l) sum += room[l * lot_stride + e];
-    const float share = sum / m, part = by * (float(count[e]) / all);
-    loss += part * share;
+  float dot = 0.f;
+  for (int e = threadIdx.x; e < a.experts; e += threads) {
+    const float share = __fdiv_rn(sum_of(e), m);
+    n += count[e];
+    dot = fmaf(float(count[e]), share, dot);
     if (DG_IN(a.dbg, a.counts + e, 4, DBG_ROUTE)) a.counts[e] = count[e];
     if (DG_IN(a.dbg, a.shares + e, 4, DBG_ROUTE)) a.shares[e] = share;
-    if (DG_IN(a.dbg, a.factor + e, 4, DBG_ROUTE)) a.factor[e] = part / m;
   }
-  loss = block_sum(loss, sums);
-  if (threadIdx.x == 0 && DG_IN(a.dbg, a.loss, 4, DBG_ROUTE)) *a.loss = loss;
+  const int active = min(warps, (a.experts + 31) / 32);  // warps that have experts
+  if (warp < active) {
+    n = __reduce_add_sync(kAll, n);
+    dot = warp_sum(dot);
+    if (lane == 0) n_sums[warp] = n, loss_sums[warp] = dot;
+  }
+  __syncthreads();
+  n = 0;
+  for (int w = 0; w < active; ++w) n += n_sums[w];
+  const float by = __fdiv_rn(a.scale * float(a.experts), float(max(n, 1)));
+  for (int e = threadIdx.x; e < a.experts; e += threads)
+    if (DG_IN(a.dbg, a.factor + e, 4, DBG_ROUTE)) a.factor[e] = __fdiv_rn(by * float(count[e]), m);
+  if (threadIdx.x == 0 && DG_IN(a.dbg, a.loss, 4, DBG_ROUTE)) {
+    dot = 0.f;
+    for (int w = 0; w < active; ++w) dot += loss_sums[w];
+    *a.loss = by * dot;
+  }
 }
 
 // The difference factor[i] - sum of factor[e] p[e] is taken from the factor of the token's surest expert on, whose
@@ -278,16 +282,21 @@ __global__ void __launch_bounds__(128) balance_backward_kernel(const BalanceArgs
 
 }  // namespace
 
-// CTAs of the sums: one warp a token until every SM has a CTA.
+static int warps_for(int64_t experts) { return experts <= 256 ? 32 : 16; }
+
+// CTAs of the sums: one warp a token until every SM has a CTA.  (Two an SM, half the tokens a warp: 13.1 instead of 11.0 us for 16384
+// tokens of 128 experts, twice the parts.)
 int balance_ctas(int64_t tokens, int64_t experts, int sms) {
-  const int64_t warps = experts <= 256 ? 32 : 16;
+  const int64_t warps = warps_for(experts);
   return int(std::max<int64_t>(1, std::min<int64_t>(sms, (tokens + warps - 1) / warps)));
 }
 
 cudaError_t launch_balance(const BalanceArgs& a, int ctas, cudaStream_t s) {
+  // (no more warps than tokens, but four)
+  const int warps = std::max(4, std::min(warps_for(a.experts), a.tokens));
   return by_experts(a.experts, [&](auto p) {
     constexpr int P = decltype(p)::value;
-    return launch_k(balance_kernel<P>, dim3(unsigned(ctas)), dim3(32 * balance_warps<P>()), 0, s, a.pdl, a);
+    return launch_k(balance_kernel<P>, dim3(unsigned(ctas)), dim3(unsigned(32 * warps)), 0, s, a.pdl, a);
   });
 }
 

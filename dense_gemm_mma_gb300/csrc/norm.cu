@@ -474,10 +474,15 @@ __global__ void __launch_bounds__(1024) norm_gain_kernel(const NormBackArgs a, i
   const int col = int(blockIdx.x) * 8 + (lane & 7);
   float s = 0.f;
   if (col < a.cols) {
-#pragma unroll 4
-    for (int p = warp * 4 + (lane >> 3); p < parts; p += 128) {
-      const float* const at = a.parts + int64_t(p) * a.part_cols + col;
-      s += DG_IN(a.dbg, at, 4, DBG_NORM) ? __ldcg(at) : 0.f;
+    for (int p0 = warp * 4 + (lane >> 3); p0 < parts; p0 += 4 * 128) {  // (four loads together, whatever is left)
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int p = p0 + j * 128;
+        const float* const at = a.parts + int64_t(p) * a.part_cols + col;
+        v[j] = p < parts && DG_IN(a.dbg, at, 4, DBG_NORM) ? __ldcg(at) : 0.f;
+      }
+      s += (v[0] + v[1]) + (v[2] + v[3]);
     }
   }
   s += __shfl_xor_sync(kAll, s, 8);

@@ -100,11 +100,15 @@ struct Row8 {
   }
 };
 
-// The larger magnitude, of two 16-bit values each or of one 32-bit one (NaN wins: its bits are the largest).
+// A word's magnitudes, and the larger ones of two words' (16-bit types two each; NaN wins: its bits are the largest).
+template <typename T>
+__device__ __forceinline__ uint32_t magnitude(uint32_t x) {
+  return x & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu);
+}
 template <typename T>
 __device__ __forceinline__ uint32_t most(uint32_t x, uint32_t y) {
-  if constexpr (sizeof(T) == 4) return max(x & 0x7fffffffu, y & 0x7fffffffu);
-  else return __vmaxu2(x & 0x7fff7fffu, y & 0x7fff7fffu);
+  if constexpr (sizeof(T) == 4) return max(x, y);
+  else return __vmaxu2(x, y);
 }
 
 // Scale byte of a magnitude's bits in the input's type.
@@ -122,21 +126,37 @@ __device__ __forceinline__ uint32_t byte_of(uint32_t bits) {
 // Scale byte of a row's block of 32: the magnitudes of four lanes' eight values.
 template <typename T>
 __device__ __forceinline__ uint32_t row_byte(const Row8<T>& v) {
-  uint32_t m = 0;
+  uint32_t m = magnitude<T>(v.w[0]);
 #pragma unroll
-  for (int j = 0; j < Row8<T>::WORDS; ++j) m = most<T>(m, v.w[j]);
+  for (int j = 1; j < Row8<T>::WORDS; ++j) m = most<T>(m, magnitude<T>(v.w[j]));
   m = most<T>(m, __shfl_xor_sync(kAll, m, 1));
   m = most<T>(m, __shfl_xor_sync(kAll, m, 2));
   if constexpr (sizeof(T) == 2) m = max(m >> 16, m & 0xffffu);
   return byte_of<T>(m);
 }
 
+// A word's two bf16 values times those of another word.  By a power of two that is exact, but for results below bf16's
+// least normal number, which are codes of 0 either way; and bf16 has fp32's exponents, so that every 2^-e is one.
+__device__ __forceinline__ uint32_t times2(uint32_t w, uint32_t by) {
+  const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&by));
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
 // Codes of a row's eight values; a block without a number has codes of 0.
 template <typename T>
 __device__ __forceinline__ uint32_t row_codes(uint32_t byte, const Row8<T>& v) {
   const float inv = mx4_inverse(byte);
-  const uint32_t codes = mx4_codes8(v.at(0) * inv, v.at(1) * inv, v.at(2) * inv, v.at(3) * inv, v.at(4) * inv, v.at(5) * inv,
-                                    v.at(6) * inv, v.at(7) * inv);
+  uint32_t codes;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const uint32_t by = __byte_perm(__float_as_uint(inv), 0u, 0x3232);
+    const uint32_t a = times2(v.w[0], by), b = times2(v.w[1], by), c = times2(v.w[2], by), d = times2(v.w[3], by);
+    codes = mx4_codes8(low(a), high(a), low(b), high(b), low(c), high(c), low(d), high(d));
+  } else {
+    codes = mx4_codes8(v.at(0) * inv, v.at(1) * inv, v.at(2) * inv, v.at(3) * inv, v.at(4) * inv, v.at(5) * inv, v.at(6) * inv,
+                       v.at(7) * inv);
+  }
   return byte == 255u ? 0u : codes;
 }
 
@@ -214,9 +234,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) quantize_mx4_kernel(const Quan
     uint32_t m[COLS];
 #pragma unroll
     for (int j = 0; j < COLS; ++j) {
-      m[j] = 0;
+      m[j] = magnitude<T>(v[0].w[j]);
 #pragma unroll
-      for (int i = 0; i < kLaneRows; ++i) m[j] = most<T>(m[j], v[i].w[j]);
+      for (int i = 1; i < kLaneRows; ++i) m[j] = most<T>(m[j], magnitude<T>(v[i].w[j]));
       m[j] = most<T>(m[j], __shfl_xor_sync(kAll, m[j], 16));
     }
     if (lane < 16) {
@@ -259,8 +279,16 @@ __global__ void __launch_bounds__(32 * kWarps, 2) quantize_mx4_kernel(const Quan
     for (int j = 0; j < 8; j += 2) {  // two columns at a time
       const uint32_t b0 = ((j < 4 ? bytes.x : bytes.y) >> (8 * (j & 3))) & 0xffu, b1 = ((j < 4 ? bytes.x : bytes.y) >> (8 * (j & 3) + 8)) & 0xffu;
       const float i0 = mx4_inverse(b0), i1 = mx4_inverse(b1);
-      const uint32_t c = mx4_codes8(v[0].at(j) * i0, v[1].at(j) * i0, v[2].at(j) * i0, v[3].at(j) * i0, v[0].at(j + 1) * i1,
-                                    v[1].at(j + 1) * i1, v[2].at(j + 1) * i1, v[3].at(j + 1) * i1);
+      uint32_t c;
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const uint32_t by = __byte_perm(__float_as_uint(i0), __float_as_uint(i1), 0x7632);
+        const uint32_t p = times2(v[0].w[j / 2], by), q = times2(v[1].w[j / 2], by), r = times2(v[2].w[j / 2], by),
+                       s = times2(v[3].w[j / 2], by);
+        c = mx4_codes8(low(p), low(q), low(r), low(s), high(p), high(q), high(r), high(s));
+      } else {
+        c = mx4_codes8(v[0].at(j) * i0, v[1].at(j) * i0, v[2].at(j) * i0, v[3].at(j) * i0, v[0].at(j + 1) * i1,
+                       v[1].at(j + 1) * i1, v[2].at(j + 1) * i1, v[3].at(j + 1) * i1);
+      }
       to[j * 32] = uint16_t(b0 == 255u ? 0u : c);
       to[(j + 1) * 32] = uint16_t(b1 == 255u ? 0u : c >> 16);
     }
