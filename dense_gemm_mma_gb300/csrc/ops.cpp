@@ -156,7 +156,8 @@ ScPick pick_sliced(bool four, int64_t rows, int64_t tiles, int sms) {
 
 // Rows of a group up to which the sliced kernel is faster than 128 x 128 tiles (32 experts of 2048 x 2048:
 // 32 rows each 30.2 against 33.3 us, 64 rows 35.4 against 33.2).
-constexpr int64_t kFewRows = 48;
+// 4 bits, the same experts: 16 rows 20.4 and 20.2 us, 32 rows 21.5 and 20.1, 64 rows 24.3 and 20.9.
+constexpr int64_t kFewRows = 48, kFewRowsMx4 = 16;
 
 // Which kernel a product takes, by sizes alone (the counts of a grouped call are on
 // the device; its rows are estimated from the capacity, which holds up to 127 empty rows a
@@ -168,10 +169,11 @@ ScPick pick(const Product& x, int sms) {
   if (x.group == SC_ROWS) {
     const int64_t per = std::max<int64_t>(1, x.M / x.groups - 127);
     const int64_t active = std::max<int64_t>(1, std::min(x.groups, x.M / 128));
-    if (per <= kFewRows)
+    if (per <= (x.four ? kFewRowsMx4 : kFewRows))
       c = pick_sliced(x.four, 128, active * nb, sms);
-    else  // (256 rows each: 53.6 us on single CTAs, 48.8 on pairs; 8 experts of 4096 x 1024, 150 rows: 14.9 and 18.3)
-      c.kernel = per < 256 ? SC_TILE : SC_PAIR;
+    else  // (256 rows each: 53.6 us on single CTAs, 48.8 on pairs; 8 experts of 4096 x 1024, 150 rows: 14.9 and 18.3.
+          // 4 bits, 32 experts of 2048 x 2048: 128 rows 22.4 and 26.3, 160 rows 31.2 and 27.7)
+      c.kernel = per < (x.four ? 129 : 256) ? SC_TILE : SC_PAIR;
   } else if (x.group == SC_K) {
     // (16 gradients of 2048 x 2048: 192 rows each, 319 with the padding, 49.8 us on single CTAs, 52.3 on pairs; 384 rows
     // 60.3 and 54.6)
@@ -181,12 +183,17 @@ ScPick pick(const Product& x, int sms) {
     // us, pairs 12.3), 256 x 256 on pairs beyond (400 x 8192 x 8192: 27 us, 37 on single CTAs).
     // Fewer tiles: K slices, if what they save of the K loop (0.22 us a k-block) pays for adding up
     // the slices' rows (0.07 us a row and CTA).  735 x 6489: 800 rows 14.1 us in 3
-    // slices, 19.4 whole; 128 x 6912 x 2048: 11.8 in 2 slices, 10.5 whole.
-    c.kernel = mb * nb > sms ? SC_PAIR : SC_TILE;
+    // slices, 19.4 whole; 128 x 6912 x 2048: 11.8 in 2 slices, 10.5 whole.  4 bits: a k-block saves more beside the
+    // whole tile's longer start (0.9 us for the same choices: 128 x 4096 x 2048 8.4 in 4 slices, 9.7 whole; 128 x 8192 x 2048 10.1 in
+    // 2, 9.9 whole; 256 x 4096 x 8192 14.0 in 2, 15.3 whole).
+    // Up to four k-blocks of 4 bits, two and a half waves on single CTAs (1200 x 2048 x 512: 9.2 us, pairs 10.5; 512 x 6912 x 1024 10.5 and
+    // 11.2).
+    const int64_t whole = x.four && kb <= 4 ? sms * 5 / 2 : sms;
+    c.kernel = mb * nb > whole ? SC_PAIR : SC_TILE;
     if (mb * nb <= sms) {
       const ScPick sl = pick_sliced(x.four, x.M, mb * nb, sms);
       const double rows = double(std::min<int64_t>(x.M, 128)), s = sl.slices;
-      if (x.M <= 64 || 0.07 * rows / s < 0.22 * double(kb) * (1 - 1 / s)) c = sl;
+      if (x.M <= 64 || 0.07 * rows / s < (x.four ? 0.9 : 0.22) * double(kb) * (1 - 1 / s)) c = sl;
     }
   }
   if (const char* f = std::getenv("GEMM_SCALED_KERNEL")) {
