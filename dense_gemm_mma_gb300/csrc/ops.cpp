@@ -307,8 +307,9 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   p.idesc = ((sliced ? tb : ta) << 7) | ((sliced ? ta : tb) << 10) | (mma_n >> 3 << 17) | (1u << 23) | (mma_m >> 4 << 24);
   // Groups of tile rows walked column by column: tiles that run at the same time share
   // rows of A and of B in L2.
-  // (4 bits: 8192 x 8192 x 2048 in groups of 4 59.1 us, of 8 60.8, of 16 63.6; 8192^3 172, 172 and 169)
-  p.raster = sliced ? std::max(1, p.m_blocks) : x.four ? 4 : 8;
+  // (4 bits, up to eight k-blocks: 8192 x 8192 x 2048 in groups of 4 59.1 us, of 8 60.8, of 16 63.6; more: 4096 x 4096 x 8192 61.2, 54.4
+  // and 56.4, 8192 x 8192 x 16384 370, 345 and 344)
+  p.raster = sliced ? std::max(1, p.m_blocks) : x.four && p.k_blocks <= 8 ? 4 : 8;
   const int64_t bound = x.group == SC_ROWS  // SC_ROWS: whole tiles and one partial tile for each group at most
                             ? (ceil_div(x.M, tile_m) + std::min<int64_t>(x.groups, ceil_div(x.M, 128))) * p.n_blocks
                             : int64_t(p.m_blocks) * p.n_blocks * (x.group == SC_K ? x.groups : 1);
