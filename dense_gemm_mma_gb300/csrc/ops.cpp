@@ -539,11 +539,11 @@ gemm_status_t gemm_run_grouped_k(gemm_plan_t plan, int64_t groups, int64_t M, in
   return checked_run(plan, x, stream);
 }
 
-int64_t gemm_mx4_scale_bytes(int64_t rows, int64_t cols) {
+int64_t gemm_mx_scale_bytes(int64_t rows, int64_t cols) {
   return size_ok(rows) && size_ok(cols) ? mx4_scale_tiles(rows, cols) * 512 : -1;
 }
 
-gemm_status_t gemm_check_mx4(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA, const void* B,
+gemm_status_t gemm_check_mx(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA, const void* B,
                              int64_t ldb, const void* SB, const void* D, int64_t ldd, gemm_type_t d_type, float alpha,
                              float beta, gemm_epilogue_t epilogue) {
   Product x;
@@ -556,11 +556,11 @@ gemm_status_t gemm_check_mx4(int64_t M, int64_t N, int64_t K, const void* A, int
   return check_product(x);
 }
 
-gemm_status_t gemm_run_mx4(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA,
+gemm_status_t gemm_run_mx(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA,
                            const void* B, int64_t ldb, const void* SB, void* D, int64_t ldd, gemm_type_t d_type,
                            float alpha, float beta, gemm_epilogue_t epilogue, void* stream) {
   Product x;
-  x.name = "gemm_run_mx4";
+  x.name = "gemm_run_mx";
   x.four = true;
   x.M = M, x.N = N, x.K = K;
   x.A = A, x.lda = lda, x.SA = SA;
@@ -570,13 +570,13 @@ gemm_status_t gemm_run_mx4(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, co
   return checked_run(plan, x, stream);
 }
 
-gemm_status_t gemm_run_grouped_mx4(gemm_plan_t plan, int64_t groups, int64_t rows, int64_t N, int64_t K,
+gemm_status_t gemm_run_grouped_mx(gemm_plan_t plan, int64_t groups, int64_t rows, int64_t N, int64_t K,
                                    const int32_t* starts, const int32_t* counts, const void* A, int64_t lda,
                                    const void* SA, const void* B, int64_t ldb, int64_t b_group, const void* SB, void* D,
                                    int64_t ldd, gemm_type_t d_type, float alpha, float beta, gemm_epilogue_t epilogue,
                                    void* stream) {
   Product x;
-  x.name = "gemm_run_grouped_mx4";
+  x.name = "gemm_run_grouped_mx";
   x.four = true;
   x.group = SC_ROWS, x.groups = groups, x.M = rows, x.N = N, x.K = K;
   x.starts = starts, x.counts = counts;
@@ -647,7 +647,7 @@ gemm_status_t gemm_quantize(gemm_plan_t plan, int64_t rows, int64_t cols, const 
   return call.done(launched(launch_quantize(a, static_cast<cudaStream_t>(stream))));
 }
 
-gemm_status_t gemm_quantize_mx4(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx,
+gemm_status_t gemm_quantize_mx(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx,
                                 gemm_type_t x_type, const int32_t* rowmap, int64_t map_div, int64_t src_rows, void* Q,
                                 int64_t ldq, void* SQ, void* QT, int64_t ldqt, void* SQT, void* stream) {
   if (!plan || rows < 0 || cols < 0 || src_rows < 0 || !is_float_type(x_type)) return GEMM_ERR_INVALID_ARG;
@@ -668,7 +668,7 @@ gemm_status_t gemm_quantize_mx4(gemm_plan_t plan, int64_t rows, int64_t cols, co
   if (results_meet({region(Q, Q ? rows : 0, cb, ldq, 1), run_of(SQ, sq), region(QT, QT ? cols : 0, rb, ldqt, 1), run_of(SQT, sqt)},
                    {region(X, xr, cols, ldx, es), run_of(rowmap, rows * 4)}))
     return GEMM_ERR_INVALID_ARG;
-  const CallScope call(plan, "gemm_quantize_mx4 %lldx%lld %s->mx4%s%s%s", (long long)rows, (long long)cols, type_name(x_type),
+  const CallScope call(plan, "gemm_quantize_mx %lldx%lld %s->mx4%s%s%s", (long long)rows, (long long)cols, type_name(x_type),
                        Q ? " Q" : "", QT ? " QT" : "", rowmap ? " by map" : "");
   DeviceGuard guard(plan->device);
   QuantArgs a{};

@@ -120,13 +120,13 @@ _SIGNATURES = {
                                 _I32, _VP, _I64, _I32, _F, _F, gemm_epilogue_t, _VP]),
     "gemm_run_grouped_k": (_I32, [_VP, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _I64, _VP, _I32, _VP, _I64, _VP, _I32,
                                   _VP, _I64, _I64, _I32, _F, _F, gemm_epilogue_t, _VP]),
-    "gemm_mx4_scale_bytes": (_I64, [_I64, _I64]),
-    "gemm_quantize_mx4": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
+    "gemm_mx_scale_bytes": (_I64, [_I64, _I64]),
+    "gemm_quantize_mx": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
     "gemm_dequantize": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _VP, _I64, _I32, _VP]),
-    "gemm_run_mx4": (_I32, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP, _I64, _I32, _F, _F,
+    "gemm_run_mx": (_I32, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP, _I64, _I32, _F, _F,
                             gemm_epilogue_t, _VP]),
-    "gemm_check_mx4": (_I32, [_I64, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP, _I64, _I32, _F, _F, gemm_epilogue_t]),
-    "gemm_run_grouped_mx4": (_I32, [_VP, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _I64, _VP, _VP, _I64, _I64, _VP, _VP, _I64,
+    "gemm_check_mx": (_I32, [_I64, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP, _I64, _I32, _F, _F, gemm_epilogue_t]),
+    "gemm_run_grouped_mx": (_I32, [_VP, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _I64, _VP, _VP, _I64, _I64, _VP, _VP, _I64,
                                     _I32, _F, _F, gemm_epilogue_t, _VP]),
     "gemm_norm": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _I64, _I32, _VP, _I32, _F, _VP, _I64, _VP, _I64, _I32, _VP,
                          _I64, _VP, _VP, _VP]),
@@ -313,13 +313,13 @@ def gemm_run_grouped_k(plan, groups, M, N, rows, starts, counts, A, lda, SA, a_t
                                      D, ldd, d_group, d_type, alpha, beta, gemm_epilogue_t(act, slope), stream)
 
 
-def gemm_mx4_scale_bytes(rows, cols) -> int:
-    return load().gemm_mx4_scale_bytes(rows, cols)
+def gemm_mx_scale_bytes(rows, cols) -> int:
+    return load().gemm_mx_scale_bytes(rows, cols)
 
 
-def gemm_quantize_mx4(plan, rows, cols, X, ldx, x_type, rowmap, map_div, src_rows, Q, ldq, SQ, QT, ldqt, SQT,
+def gemm_quantize_mx(plan, rows, cols, X, ldx, x_type, rowmap, map_div, src_rows, Q, ldq, SQ, QT, ldqt, SQT,
                       stream=None) -> int:
-    return load().gemm_quantize_mx4(plan, rows, cols, X, ldx, x_type, rowmap, map_div, src_rows, Q, ldq, SQ, QT, ldqt, SQT,
+    return load().gemm_quantize_mx(plan, rows, cols, X, ldx, x_type, rowmap, map_div, src_rows, Q, ldq, SQ, QT, ldqt, SQT,
                                     stream)
 
 
@@ -327,19 +327,19 @@ def gemm_dequantize(plan, rows, cols, Q, ldq, q_type, SQ, X, ldx, x_type, stream
     return load().gemm_dequantize(plan, rows, cols, Q, ldq, q_type, SQ, X, ldx, x_type, stream)
 
 
-def gemm_run_mx4(plan, M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta, act=GEMM_ACT_NONE, slope=0.0,
+def gemm_run_mx(plan, M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta, act=GEMM_ACT_NONE, slope=0.0,
                  stream=None) -> int:
-    return load().gemm_run_mx4(plan, M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta,
+    return load().gemm_run_mx(plan, M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta,
                                gemm_epilogue_t(act, slope), stream)
 
 
-def gemm_check_mx4(M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta, act=GEMM_ACT_NONE, slope=0.0) -> int:
-    return load().gemm_check_mx4(M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta, gemm_epilogue_t(act, slope))
+def gemm_check_mx(M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta, act=GEMM_ACT_NONE, slope=0.0) -> int:
+    return load().gemm_check_mx(M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta, gemm_epilogue_t(act, slope))
 
 
-def gemm_run_grouped_mx4(plan, groups, rows, N, K, starts, counts, A, lda, SA, B, ldb, b_group, SB, D, ldd, d_type, alpha,
+def gemm_run_grouped_mx(plan, groups, rows, N, K, starts, counts, A, lda, SA, B, ldb, b_group, SB, D, ldd, d_type, alpha,
                          beta, act=GEMM_ACT_NONE, slope=0.0, stream=None) -> int:
-    return load().gemm_run_grouped_mx4(plan, groups, rows, N, K, starts, counts, A, lda, SA, B, ldb, b_group, SB, D, ldd,
+    return load().gemm_run_grouped_mx(plan, groups, rows, N, K, starts, counts, A, lda, SA, B, ldb, b_group, SB, D, ldd,
                                        d_type, alpha, beta, gemm_epilogue_t(act, slope), stream)
 
 
@@ -459,7 +459,7 @@ def _scales(t, rows: int, cols: int, groups: int = 1) -> int:
 
 def _mx4_scales(t, rows: int, cols: int, groups: int = 1) -> int:
     """Pointer of the packed scale bytes of `groups` rows x cols matrices of 4-bit values."""
-    need = groups * 512 * (-(-rows // 128) or 1) * (-(-cols // 128) or 1)  # gemm_mx4_scale_bytes
+    need = groups * 512 * (-(-rows // 128) or 1) * (-(-cols // 128) or 1)  # gemm_mx_scale_bytes
     if t.numel() < need or t.element_size() != 1 or not t.is_contiguous():
         raise ValueError(f"scales are {need} contiguous bytes")
     return t.data_ptr()
@@ -693,7 +693,7 @@ class Plan:
     # ------------------------------------------- block-scaled 4-bit products
 
     def quantize_mx4(self, X, Q=None, SQ=None, QT=None, SQT=None, *, rowmap=None, map_div=1, stream=None) -> int:
-        """X (rows x cols) -> 4-bit Q (rows x (cols + 1) // 2 bytes) and scales SQ (gemm_mx4_scale_bytes uint8), and/or its
+        """X (rows x cols) -> 4-bit Q (rows x (cols + 1) // 2 bytes) and scales SQ (gemm_mx_scale_bytes uint8), and/or its
         transpose QT (cols x (rows + 1) // 2 bytes) and SQT.  rowmap as in quantize."""
         x, src_rows, cols, ldx = _matrix(X)
         rows = src_rows if rowmap is None else rowmap.numel()
@@ -707,7 +707,7 @@ class Plan:
             sqt = _mx4_scales(SQT, cols, rows)
         if Q is None and QT is None:
             raise ValueError("neither Q nor QT")
-        return load().gemm_quantize_mx4(self.handle, rows, cols, x, ldx, _type_of(X),
+        return load().gemm_quantize_mx(self.handle, rows, cols, x, ldx, _type_of(X),
                                         None if rowmap is None else _array(rowmap, rows, "int32"), map_div, src_rows, q,
                                         ldq, sq, qt, ldqt, sqt, self._stream(stream))
 
@@ -720,7 +720,7 @@ class Plan:
         if width_b != width:
             raise ValueError("A and B have the same K")
         d, ldd = _same_shape(D, M, N, "D")
-        return load().gemm_run_mx4(self.handle, M, N, K, a, lda, _mx4_scales(SA, M, K), b, ldb, _mx4_scales(SB, N, K), d, ldd,
+        return load().gemm_run_mx(self.handle, M, N, K, a, lda, _mx4_scales(SA, M, K), b, ldb, _mx4_scales(SB, N, K), d, ldd,
                                    _type_of(D), alpha, beta, _epilogue(act, slope), self._stream(stream))
 
     def run_grouped_mx4(self, A, SA, B, SB, D, starts, counts, *, K=None, alpha=1.0, beta=0.0, act=GEMM_ACT_NONE, slope=0.0,
@@ -732,7 +732,7 @@ class Plan:
         if width_b != width:
             raise ValueError("A and B have the same K")
         d, ldd = _same_shape(D, rows, N, "D")
-        return load().gemm_run_grouped_mx4(self.handle, groups, rows, N, K, _array(starts, groups, "int32"),
+        return load().gemm_run_grouped_mx(self.handle, groups, rows, N, K, _array(starts, groups, "int32"),
                                            _array(counts, groups, "int32"), a, lda, _mx4_scales(SA, rows, K), b, ldb, b_group,
                                            _mx4_scales(SB, N, K, groups), d, ldd, _type_of(D), alpha, beta,
                                            _epilogue(act, slope), self._stream(stream))

@@ -7,8 +7,8 @@
     balance loss of the choice        gemm_balance
 
 and back: gemm_balance_backward adds the loss's part to the logits' gradient, gemm_norm_backward takes the experts' gradient and
-the one that reaches h past the norm.  Serving: the experts' weights in 4 bits (gemm_quantize_mx4), the tokens quantised
-through the router's map, gemm_run_grouped_mx4 twice; a projection behind it reads the norm's own 8-bit codes.
+the one that reaches h past the norm.  Serving: the experts' weights in 4 bits (gemm_quantize_mx), the tokens quantised
+through the router's map, gemm_run_grouped_mx twice; a projection behind it reads the norm's own 8-bit codes.
 
 Prints how far each result is from the same layer in 32 bits (serving: from one with the same 4-bit weights), and times.
 """
@@ -38,7 +38,7 @@ class Codes4:
     def __init__(self, plan, x, *, rowmap=None, map_div=1):
         rows, cols = (x.shape[0] if rowmap is None else rowmap.numel()), x.shape[1]
         self.q = padded(rows, (cols + 1) // 2, torch.uint8)
-        self.s = torch.empty(gemm.gemm_mx4_scale_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+        self.s = torch.empty(gemm.gemm_mx_scale_bytes(rows, cols), dtype=torch.uint8, device="cuda")
         ok(plan.quantize_mx4(x, self.q, self.s, rowmap=rowmap, map_div=map_div))
 
 

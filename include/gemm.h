@@ -240,7 +240,7 @@ typedef enum { GEMM_TYPE_BF16 = 0, GEMM_TYPE_F16 = 1, GEMM_TYPE_F32 = 2,
                GEMM_TYPE_E4M3 = 4, /* 8-bit, 4 exponent and 3 fraction bits, no infinity, largest 448   */
                GEMM_TYPE_E5M2 = 5, /* 8-bit, 5 and 2, largest 57344; both: block-scaled products only */
                GEMM_TYPE_E2M1 = 6  /* 4-bit, 2 and 1, largest 6, no infinity or NaN, two to a byte: gemm_dequantize only
-                                      (the _mx4 calls imply it) */ } gemm_type_t;
+                                      (the _mx calls imply it) */ } gemm_type_t;
 
 /* D <- act(alpha * op(A) @ op(B) + beta * C) with a separate output D: the
  * gemm_run operation where the C that beta scales is read from one matrix and
@@ -522,16 +522,16 @@ gemm_status_t gemm_run_grouped_k(gemm_plan_t plan, int64_t groups, int64_t M, in
 /* ---- 4 bits ----
  * A matrix of 4-bit values (E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) of R rows and K columns is two buffers:
  *   codes   (K + 1) / 2 bytes a row, rows `ld` bytes apart: column 2i in the low, 2i + 1 in the high four bits of
- *           byte i.  With odd K the last byte's high four bits must be 0, as gemm_quantize_mx4 leaves them.
+ *           byte i.  With odd K the last byte's high four bits must be 0, as gemm_quantize_mx leaves them.
  *   scales  one E8M0 byte for each row and block of 32 columns, in the same tiles as above: 128 rows and four
  *           blocks (here 128 columns), tile (r / 128, k / 128) at 512 * ((r / 128) * ceil(K / 128) + k / 128), in it row r,
- *           block c = k / 32 at byte (r % 32) * 16 + (r % 128) / 32 * 4 + c % 4.  gemm_mx4_scale_bytes(R, K) bytes in all;
- *           bytes of rows and blocks past the matrix are 0 as gemm_quantize_mx4 writes them and must not be 255.
+ *           block c = k / 32 at byte (r % 32) * 16 + (r % 128) / 32 * 4 + c % 4.  gemm_mx_scale_bytes(R, K) bytes in all;
+ *           bytes of rows and blocks past the matrix are 0 as gemm_quantize_mx writes them and must not be 255.
  * The scale byte 255 is NaN, and so is every value of its block. */
 
 /* Bytes of the packed scales of a rows x cols matrix of 4-bit values (a multiple of 512, at least 512);
  * -1 if a size is negative or past 2^31 - 1. */
-int64_t gemm_mx4_scale_bytes(int64_t rows, int64_t cols);
+int64_t gemm_mx_scale_bytes(int64_t rows, int64_t cols);
 
 /* Quantise X as gemm_quantize does, to 4-bit codes with a scale for each row and block of 32 columns: Q and SQ the
  * matrix as it stands (rows of (cols + 1) / 2 bytes), QT and SQT the transposed one (rows of (rows + 1) / 2 bytes, blocks
@@ -541,7 +541,7 @@ int64_t gemm_mx4_scale_bytes(int64_t rows, int64_t cols);
  * that holds an infinity or NaN the byte 255 and codes of 0.
  * Q and QT at any address, rows any number of bytes apart (16-byte boundaries are fastest, and spare the products a
  * copy); otherwise alignment, rowmap, map_div, src_rows, aliasing and limits as in gemm_quantize. */
-gemm_status_t gemm_quantize_mx4(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx,
+gemm_status_t gemm_quantize_mx(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx,
                                 gemm_type_t x_type, const int32_t* rowmap, int64_t map_div, int64_t src_rows, void* Q,
                                 int64_t ldq, void* SQ, void* QT, int64_t ldqt, void* SQT, void* stream);
 
@@ -556,19 +556,19 @@ gemm_status_t gemm_dequantize(gemm_plan_t plan, int64_t rows, int64_t cols, cons
 
 /* D <- act(alpha * A @ B^T + beta * D) with 4-bit A (M x K) and B (N x K): gemm_run_scaled with codes of 4 bits and
  * scales of blocks of 32; lda and ldb are bytes, >= (K + 1) / 2.  Everything else as there. */
-gemm_status_t gemm_run_mx4(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA,
+gemm_status_t gemm_run_mx(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA,
                            const void* B, int64_t ldb, const void* SB, void* D, int64_t ldd, gemm_type_t d_type,
                            float alpha, float beta, gemm_epilogue_t epilogue, void* stream);
 
-/* The argument checks of gemm_run_mx4 without a plan or a device. */
-gemm_status_t gemm_check_mx4(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA, const void* B,
+/* The argument checks of gemm_run_mx without a plan or a device. */
+gemm_status_t gemm_check_mx(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA, const void* B,
                              int64_t ldb, const void* SB, const void* D, int64_t ldd, gemm_type_t d_type, float alpha,
                              float beta, gemm_epilogue_t epilogue);
 
 /* Experts' products with 4-bit rows and weights: gemm_run_grouped with codes of 4 bits and scales of blocks of 32
- * (lda, ldb and b_group are bytes; a group's scales gemm_mx4_scale_bytes(N, K) after the last one's).
- * gemm_quantize_mx4 with gemm_route_map's rowmap orders the tokens by expert. */
-gemm_status_t gemm_run_grouped_mx4(gemm_plan_t plan, int64_t groups, int64_t rows, int64_t N, int64_t K,
+ * (lda, ldb and b_group are bytes; a group's scales gemm_mx_scale_bytes(N, K) after the last one's).
+ * gemm_quantize_mx with gemm_route_map's rowmap orders the tokens by expert. */
+gemm_status_t gemm_run_grouped_mx(gemm_plan_t plan, int64_t groups, int64_t rows, int64_t N, int64_t K,
                                    const int32_t* starts, const int32_t* counts, const void* A, int64_t lda,
                                    const void* SA, const void* B, int64_t ldb, int64_t b_group, const void* SB, void* D,
                                    int64_t ldd, gemm_type_t d_type, float alpha, float beta, gemm_epilogue_t epilogue,

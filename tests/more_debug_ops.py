@@ -14,7 +14,7 @@ def main():
     assert gemm.gemm_debug_build() == 1 and os.environ.get("GEMM_DEBUG_SHRINK") == "4"
     plan = gemm.Plan(0)
     new = lambda *n: torch.zeros(n, dtype=torch.uint8, device="cuda")  # noqa: E731
-    scales = lambda r, k: new(gemm.gemm_mx4_scale_bytes(r, k))  # noqa: E731
+    scales = lambda r, k: new(gemm.gemm_mx_scale_bytes(r, k))  # noqa: E731
 
     for kernel in ("sliced", "tile", "pair"):  # N = 130: the last columns go through plain stores
         os.environ["GEMM_SCALED_KERNEL"] = kernel

@@ -24,9 +24,9 @@ def calls(gm, plan, stream=None):
     rowmap = ints(gm.gemm_route_rows(T, k, E))
     rows = rowmap.numel()
     load, shares, factor, loss, dl = ints(E), *(torch.zeros(n, device="cuda") for n in (E, E, 1)), torch.zeros_like(logits)
-    q, sq, qt, st = new(rows, N // 2), new(gm.gemm_mx4_scale_bytes(rows, N)), new(N, rows // 2), new(gm.gemm_mx4_scale_bytes(N, rows))
+    q, sq, qt, st = new(rows, N // 2), new(gm.gemm_mx_scale_bytes(rows, N)), new(N, rows // 2), new(gm.gemm_mx_scale_bytes(N, rows))
     W = torch.randint(0, 256, (E, N, N // 2), generator=gen, device="cuda").to(torch.uint8)
-    SW = torch.full((E * gm.gemm_mx4_scale_bytes(N, N),), 125, dtype=torch.uint8, device="cuda")
+    SW = torch.full((E * gm.gemm_mx_scale_bytes(N, N),), 125, dtype=torch.uint8, device="cuda")
     D, Y = torch.zeros((rows, N), device="cuda"), torch.zeros((rows, N), device="cuda")
     torch.cuda.synchronize()
     on = {"stream": stream}
@@ -56,8 +56,8 @@ def test_a_line_for_each_call(g, monkeypatch, capfd):
     lines = [line for line in capfd.readouterr().err.splitlines() if line.startswith("gemm_log")]
     rows = quiet[-1].numel()
     want = ["gemm_norm 40x64 bf16 residual H Y Q e4m3", "gemm_route 40x8", "gemm_route_map 40x2", "gemm_balance 40x8 f32 softmax top 2",
-            "gemm_balance_backward 40x8 f32 softmax top 2 accumulated", "gemm_quantize_mx4 %dx64 bf16->mx4 Q QT by map" % rows,
-            "gemm_run_mx4 %dx64x64 groups 1 mx4 mx4->f32 -> scaled" % rows, "gemm_run_grouped_mx4 %dx64x64 groups 8 mx4 mx4->f32 -> scaled" % rows,
+            "gemm_balance_backward 40x8 f32 softmax top 2 accumulated", "gemm_quantize_mx %dx64 bf16->mx4 Q QT by map" % rows,
+            "gemm_run_mx %dx64x64 groups 1 mx4 mx4->f32 -> scaled" % rows, "gemm_run_grouped_mx %dx64x64 groups 8 mx4 mx4->f32 -> scaled" % rows,
             "gemm_dequantize 40x64 e4m3->bf16", "gemm_norm_backward 40x64 bf16 dgain"]
     assert len(lines) == len(want) and all(line.startswith("gemm_log " + w) for line, w in zip(lines, want)), lines
     assert all(torch.equal(a, b) for a, b in zip(quiet, loud))

@@ -42,7 +42,7 @@ def test_far_rows(g):
     assert torch.equal(yf, dx) and torch.equal(dgain2, dgain)
 
     new = lambda *n: torch.zeros(n, dtype=torch.uint8, device="cuda")  # noqa: E731
-    size = g.gemm_mx4_scale_bytes(R, N)
+    size = g.gemm_mx_scale_bytes(R, N)
     q, s, q2, s2 = new(R, 144)[:, :132], new(size), new(R, 144)[:, :132], new(size)
     assert plan.quantize_mx4(x, q, s) == g.GEMM_OK and plan.quantize_mx4(xf, q2, s2) == g.GEMM_OK
     assert torch.equal(q, q2) and torch.equal(s, s2)

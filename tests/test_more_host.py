@@ -1,4 +1,4 @@
-"""Host side of the 4-bit products, the norm and the balance loss: sizes, every refusal of gemm_check_mx4, calls without a
+"""Host side of the 4-bit products, the norm and the balance loss: sizes, every refusal of gemm_check_mx, calls without a
 plan, and the references' own pins, without a device."""
 import numpy as np
 import pytest
@@ -16,14 +16,14 @@ def built_library():
 
 @pytest.mark.parametrize("rows,cols", [(1, 1), (0, 0), (128, 128), (129, 129), (1, 4096), (1000, 127)])
 def test_scale_bytes(rows, cols):
-    n = g.gemm_mx4_scale_bytes(rows, cols)
+    n = g.gemm_mx_scale_bytes(rows, cols)
     assert n == max(1, -(-rows // 128)) * max(1, -(-cols // 128)) * 512
     if cols:
         assert ref.pack_scales4(np.zeros((rows, -(-cols // 32)), np.int64), cols).size == n
 
 
 def test_sizes_out_of_range():
-    assert g.gemm_mx4_scale_bytes(-1, 5) == -1 and g.gemm_mx4_scale_bytes(5, 2 ** 31) == -1
+    assert g.gemm_mx_scale_bytes(-1, 5) == -1 and g.gemm_mx_scale_bytes(5, 2 ** 31) == -1
 
 
 OK = dict(M=64, N=96, K=201, A=0x100000, lda=112, SA=0x200000, B=0x300000, ldb=112, SB=0x400000, D=0x500000, ldd=96, d_type=0,
@@ -31,7 +31,7 @@ OK = dict(M=64, N=96, K=201, A=0x100000, lda=112, SA=0x200000, B=0x300000, ldb=1
 
 
 def check(**change):
-    return g.gemm_check_mx4(**{**OK, **change})
+    return g.gemm_check_mx(**{**OK, **change})
 
 
 def test_accepts():
@@ -68,9 +68,9 @@ def test_the_8_bit_product_takes_no_4_bit_type():
 
 def test_calls_without_a_plan_are_refused():
     bad = g.GEMM_ERR_INVALID_ARG
-    assert g.gemm_run_mx4(None, *[OK[n] for n in ("M", "N", "K", "A", "lda", "SA", "B", "ldb", "SB", "D", "ldd", "d_type")], 1.0, 0.0) == bad
-    assert g.gemm_run_grouped_mx4(None, 1, 128, 8, 32, 16, 16, 16, 16, 16, 16, 16, 128, 16, 16, 8, 2, 1.0, 0.0) == bad
-    assert g.gemm_quantize_mx4(None, 1, 32, 16, 32, 2, None, 1, 1, 16, 16, 16, None, 0, None) == bad
+    assert g.gemm_run_mx(None, *[OK[n] for n in ("M", "N", "K", "A", "lda", "SA", "B", "ldb", "SB", "D", "ldd", "d_type")], 1.0, 0.0) == bad
+    assert g.gemm_run_grouped_mx(None, 1, 128, 8, 32, 16, 16, 16, 16, 16, 16, 16, 128, 16, 16, 8, 2, 1.0, 0.0) == bad
+    assert g.gemm_quantize_mx(None, 1, 32, 16, 32, 2, None, 1, 1, 16, 16, 16, None, 0, None) == bad
     assert g.gemm_dequantize(None, 1, 32, 16, 16, 6, 16, 16, 32, 2) == bad
     assert g.gemm_norm(None, 1, 8, 16, 8, 2, None, 0, 2, None, 2, 1e-6, None, 0, 64, 8, 4, None, 0, None, None) == bad
     assert g.gemm_norm_backward(None, 1, 8, 16, 8, 2, 16, 8, 2, None, 2, 16, None, 0, 64, 8, None) == bad

@@ -60,7 +60,7 @@ def float_rows(n, width, name, extra=0, fill=float("nan")):
 
 def scale_room(g, rows, cols, fill=0xEE):
     import torch
-    return torch.full((g.gemm_mx4_scale_bytes(rows, cols),), fill, dtype=torch.uint8, device="cuda")
+    return torch.full((g.gemm_mx_scale_bytes(rows, cols),), fill, dtype=torch.uint8, device="cuda")
 
 
 # ------------------------------------------------------------------ quantiser
@@ -455,7 +455,7 @@ def test_refusals(plan, g):
     import torch
     x = torch.zeros((8, 64), device="cuda", dtype=torch.bfloat16)
     q, s = torch.zeros((8, 32), device="cuda", dtype=torch.uint8), torch.zeros(512, device="cuda", dtype=torch.uint8)
-    call = lambda **c: g.gemm_quantize_mx4(*{**dict(  # noqa: E731
+    call = lambda **c: g.gemm_quantize_mx(*{**dict(  # noqa: E731
         plan=plan.handle, rows=8, cols=64, X=x.data_ptr(), ldx=64, x_type=0, rowmap=None, map_div=1, src_rows=8, Q=q.data_ptr(), ldq=32,
         SQ=s.data_ptr(), QT=None, ldqt=0, SQT=None), **c}.values())
     assert call() == g.GEMM_OK and call(rows=0) == g.GEMM_OK and call(cols=0) == g.GEMM_OK
