@@ -414,7 +414,7 @@ struct QuantArgs {
   uint8_t *q, *sq, *qt, *sqt;  // q / sq or qt / sqt may be null
   int64_t ldq, ldqt;
   int q_groups, qt_groups;  // groups of four blocks along the rows of q / of qt
-  int q_wide, qt_wide;      // 4 bits: rows of q allow words, of qt 16 bytes
+  int x_words, q_wide, qt_wide;  // 4 bits: rows of X allow words, of q too, of qt 16 bytes
   int pdl;
   DG_DEBUG_FIELD
 };

@@ -688,6 +688,7 @@ gemm_status_t gemm_quantize_mx(gemm_plan_t plan, int64_t rows, int64_t cols, con
   a.sqt = static_cast<uint8_t*>(SQT);
   a.ldq = ldq;
   a.ldqt = ldqt;
+  a.x_words = aligned(X, 4) && (ldx * es) % 4 == 0;
   a.q_wide = aligned(Q, 4) && ldq % 4 == 0;
   a.qt_wide = rows_wide(QT, ldqt, 1);
   a.q_groups = int(mx4_scale_tiles(1, cols));

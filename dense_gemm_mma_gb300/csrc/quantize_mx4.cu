@@ -9,6 +9,8 @@
 // One orientation: warps take rows, no barrier.  Both: a CTA takes 128 x 128 values, which is one scale tile (128 rows x
 // 4 blocks) in either orientation; half a warp holds 128 columns of a row, a lane eight neighbouring columns of four
 // neighbouring rows.  A row's block is four lanes (two exchanges), a column's block 32 rows of four warps (through shared memory).
+// What bounds it is issuing instructions: 8192 x 4096 bf16 19 us one way (85 MB, 4.4 TB/s), 30 both (103 MB), where a thread spends ~22
+// instructions a value; back to bf16 14.6 us (85 MB, 5.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -88,14 +90,24 @@ struct Row8 {
       }
       return;
     }
-    if (!DG_IN(a.dbg, p, min(8, a.cols - col) * int(sizeof(T)), DBG_QUANTIZE)) return;
+    const int n = min(8, a.cols - col);
+    if (!DG_IN(a.dbg, p, n * int(sizeof(T)), DBG_QUANTIZE)) return;
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (col + j >= a.cols) continue;
-      if constexpr (sizeof(T) == 4)
-        w[j] = __float_as_uint(p[j]);
-      else
-        w[j / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[j]) << (16 * (j & 1));
+      for (int j = 0; j < 8; ++j)
+        if (j < n) w[j] = reinterpret_cast<const uint32_t*>(p)[j];
+    } else if (a.x_words) {  // words, and the last value of an odd number
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (2 * j + 1 < n)
+          w[j] = reinterpret_cast<const uint32_t*>(p)[j];
+        else if (2 * j < n)
+          w[j] = reinterpret_cast<const uint16_t*>(p)[2 * j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) w[j / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[j]) << (16 * (j & 1));
     }
   }
 };

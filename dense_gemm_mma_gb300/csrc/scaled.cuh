@@ -1,4 +1,4 @@
-// scaled.cuh -- what the two 8-bit block-scaled product kernels share.
+// scaled.cuh -- what the two block-scaled product kernels share.
 //
 // D[m, n] = act(alpha * sum_k a[m,k] b[n,k] 2^(ea[m,k/128] + eb[n,k/128]) + beta * D[m, n])
 //
@@ -13,6 +13,10 @@
 // The scales come as 512-byte tiles (128 rows x 4 blocks; include/gemm.h), which is
 // the image tcgen05.cp lays into tensor memory: one copy per 128 rows serves four
 // k-blocks, whose MMAs pick byte (k-block mod 4) of each 32-bit word.
+//
+// 4-bit operands (E2M1, two to a byte): tcgen05.mma.kind::mxf4 multiplies each 32 products by two E8M0 scales, so a
+// scale covers 32 values: an MMA (K = 64) takes two bytes of each word, a word serves two of them, and a k-block of 128 bytes,
+// 256 values, has two scale tiles for 128 rows.
 #pragma once
 
 #include <atomic>

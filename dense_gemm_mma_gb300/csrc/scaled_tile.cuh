@@ -24,11 +24,16 @@
 // a tile first and only then lets the next tile's MMAs begin.
 //
 // FOUR (4-bit operands): a ring stage is the same 128 bytes of K, 256 values, and four K = 64 MMAs; with a scale for
-// each 32 values every stage has scale tiles of its own, two for 128 rows, and a set of scale columns (24 of a pair): the
-// accumulators overlap by 128 columns.
-//  - warp 10 copies the scales, six copies a k-block.
+// each 32 values every stage has scale tiles of its own, two for 128 rows, and a set of scale columns (24 of a pair), so that four sets
+// need the accumulators to overlap by 128 columns.  A set is written again when the MMAs that read it have completed.
+//  - warp 10 copies the scales, six copies a k-block, and signals the MMA warp.  In the MMA warp itself the copies and the
+//    wait for their set made a k-block's eleven instructions longer to issue than its MMAs take (8192^3 187 us; 214 with a copy
+//    group before every second MMA).
+// 8192^3 into bf16 168 to 178 us, 6.2 to 6.5 PFLOP/s.  The MMAs of a k-block take 512 cycles, a k-block 550 while the ring is
+// full and 640 to 1,100 behind it: without the copies (wrong results) 154 us, without the stores 150, without the loads 139; the
+// MMAs of the next tile begin ~900 cycles after the last of this one (their completion, 500 for 128 columns to be read, the signal).
 //
-// What bounds it: 8192^3 into bf16 330 to 360 us, 3.1 to 3.3 PFLOP/s, at the power limit (287 us, 3.8
+// What bounds it (8 bits): 8192^3 into bf16 330 to 360 us, 3.1 to 3.3 PFLOP/s, at the power limit (287 us, 3.8
 // PFLOP/s, with operands whose bits change little).  Short K: the turnover of the tiles, with no unit full.  16 weight
 // gradients of 2048 x 2048 over 1,024 rows each (8 k-blocks a tile) read 537 MB of tiles and write 268 MB in 76 us, and take 61 if
 // nothing is written; a load takes 4,000 to 5,000 cycles while the tile before is written, of which the ring covers 2,600.

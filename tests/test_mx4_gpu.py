@@ -91,12 +91,12 @@ SHAPES = [(1, 1), (1, 32), (7, 31), (33, 2050), (127, 129), (128, 512), (129, 64
 
 @pytest.mark.parametrize("R,K", SHAPES)
 @pytest.mark.parametrize("name", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("odd", [0, 1, 2])
 def test_quantize(plan, g, R, K, name, odd):
     import torch
     rng = np.random.default_rng(R * 1000 + K)
     x = values(rng, R, K, name)
-    _, xd = float_rows(R, K, name, extra=1 if odd else 0)  # odd rows: no wide loads
+    _, xd = float_rows(R, K, name, extra=odd)  # rows 1 value further apart: no wide loads; 2: words
     xd.copy_(x)
     x64 = x.double().numpy()
     want, byte = ref.quantize4(x64)
