@@ -378,7 +378,8 @@ int scaled_sliced_clusters(int slices);  // clusters of that many CTAs that can 
 // with a row block's scale tiles as their second coordinate and the row block as their third (box two tiles; sb for a pair: of two row blocks).
 cudaError_t launch_mx4_tile(bool pair, const ScMaps& m, const ScParams& p, int grid, cudaStream_t s);
 int mx4_tile_clusters();
-int mx4_tile_stages(bool pair);
+int mx4_tile_stages(bool pair, const ScParams& p);
+int mx4_tile_box_row(bool pair, const ScParams& p);  // bytes of a row of the boxes that results are stored in, and of their swizzle
 cudaError_t launch_mx4_sliced(const ScMaps& m, const ScParams& p, int grid, cudaStream_t s);
 int mx4_sliced_smem(int bn, int stages, int part_rows);
 int mx4_sliced_clusters(int slices);

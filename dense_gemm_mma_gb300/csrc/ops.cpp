@@ -357,7 +357,9 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
                                    : x.d_type == GEMM_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int64_t nd = x.group == SC_K ? x.groups : 1;
-    ok = ok && map3(&m.d, dt, es, x.D, p.n_tma, x.M, nd, x.ldd, nd > 1 ? x.d_group : x.ldd * x.M, int(128 / es), 32, sw);
+    const int row = x.four ? mx4_tile_box_row(pair, p) : 128;
+    ok = ok && map3(&m.d, dt, es, x.D, p.n_tma, x.M, nd, x.ldd, nd > 1 ? x.d_group : x.ldd * x.M, int(row / es), 32,
+                    row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : sw);
   }
   if (!ok) return GEMM_ERR_CUDA;
 #ifdef DG_DEBUG
@@ -371,7 +373,7 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   info.tile_k = x.four ? 2 * SC_BK : SC_BK;
   info.cta_per_tile = pair ? 2 : sliced ? c.slices : 1;
   info.splitk = sliced ? c.slices : 1;
-  info.stages = sliced ? c.stages : x.four ? mx4_tile_stages(pair) : scaled_tile_stages(pair);
+  info.stages = sliced ? c.stages : x.four ? mx4_tile_stages(pair, p) : scaled_tile_stages(pair);
   info.raster_group = p.raster;
   info.grid = grid;
   info.tiles = bound;

@@ -7,7 +7,7 @@ cudaError_t launch_scaled_tile(bool pair, const ScMaps& m, const ScParams& p, in
   return pair ? launch<true, false>(m, p, grid, s) : launch<false, false>(m, p, grid, s);
 }
 
-int scaled_tile_stages(bool pair) { return pair ? Cfg<true, false>::STAGES : Cfg<false, false>::STAGES; }
+int scaled_tile_stages(bool pair) { return pair ? Cfg<true, false, false>::STAGES : Cfg<false, false, false>::STAGES; }
 
 int scaled_tile_clusters() { return resident_pairs<false>(); }
 

@@ -29,6 +29,8 @@
 //  - warp 10 copies the scales, six copies a k-block, and signals the MMA warp.  In the MMA warp itself the copies and the
 //    wait for their set made a k-block's eleven instructions longer to issue than its MMAs take (8192^3 187 us; 214 with a copy
 //    group before every second MMA).
+// SIX: a sixth stage where the results are 16-bit and the groups few.  An epilogue warp's box is then 32 columns of 64
+// bytes, and the tables of the groups are short: 8192^3 172 -> 159 us, 2304 x 6912 x 8192 54.6 -> 51.1.
 // 8192^3 into bf16 168 to 178 us, 6.2 to 6.5 PFLOP/s.  The MMAs of a k-block take 512 cycles, a k-block 550 while the ring is
 // full and 640 to 1,100 behind it: without the copies (wrong results) 154 us, without the stores 150, without the loads 139; the
 // MMAs of the next tile begin ~900 cycles after the last of this one (their completion, 500 for 128 columns to be read, the signal).
@@ -52,26 +54,33 @@ template <bool FOUR>
 __host__ __device__ constexpr int threads() {
   return 64 + 32 * kEpiWarps + (FOUR ? 32 : 0);
 }
-constexpr int kBox = 32 * 128;  // one 32-row x 128-byte epilogue box
 
-template <bool PAIR, bool FOUR>
+// Groups whose segments and tile counts the six-stage kernel has room for.
+constexpr int kSixGroups = 64;
+
+template <bool PAIR, bool FOUR, bool SIX>
 struct Cfg {
+  static_assert(!SIX || (PAIR && FOUR), "six stages: pairs, 4-bit operands");
   static constexpr int TILE_M = PAIR ? 256 : 128;
   static constexpr int BN = PAIR ? 256 : 128;
   static constexpr int OPERAND = 128 * SC_BK;         // bytes of A, and of B, per stage and CTA
   static constexpr int TILES = FOUR ? 2 : 1;           // scale tiles along K of a stage
   static constexpr int SCALES = 512 * TILES * (1 + BN / 128);  // scale tiles of a stage: A's rows, all of the tile's columns
-  static constexpr int STAGES = 5;
+  static constexpr int STAGES = SIX ? 6 : 5;
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + STAGES * OPERAND;
   static constexpr int OFF_STG = OFF_B + STAGES * OPERAND;
-  static constexpr int OFF_S = OFF_STG + kEpiWarps * kBox;
+  static constexpr int ROW = SIX ? 64 : 128;   // bytes to a row of an epilogue warp's box, its swizzle the same
+  static constexpr int BOX = 32 * ROW;
+  static constexpr int OFF_S = OFF_STG + kEpiWarps * BOX;
   static constexpr int OFF_BAR = OFF_S + STAGES * SCALES;
   // full[S], empty[S], tmem_full[2], tmem_empty[2], drain, set_full[4], copy_drain
-  static constexpr int OFF_MISC = (OFF_BAR + (2 * STAGES + 10) * 8 + 15) / 16 * 16;
-  static constexpr int OFF_SEG = OFF_MISC + 16;
-  static constexpr int OFF_TABLE = OFF_SEG + SC_MAX_GROUPS * 8;
-  static constexpr int SMEM = OFF_TABLE + (SC_MAX_GROUPS + 1) * 4 + 1024;  // + slack for 1024-B alignment
+  static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 10) * 8;
+  static constexpr int OFF_SEG = OFF_MISC + 8;
+  static constexpr int GROUPS = SIX ? kSixGroups : SC_MAX_GROUPS;
+  static constexpr int OFF_TABLE = OFF_SEG + GROUPS * 8;
+  // + slack for 1024-byte alignment (SIX: the declaration's)
+  static constexpr int SMEM = OFF_TABLE + (GROUPS + 1) * 4 + (SIX ? 0 : 1024);
   static_assert(SMEM <= 232448, "shared memory budget");
   static constexpr int OVERLAP = !PAIR ? 0 : FOUR ? 128 : 64;  // columns that the two accumulators share
   static constexpr int ACC1 = BN - OVERLAP;      // first column of the second accumulator
@@ -124,7 +133,7 @@ __device__ __forceinline__ void blend(float (&v)[32], const ScParams& p, const u
 
 // The epilogue's arithmetic, compiled for what a call needs: BETA (with every activation), or
 // one of ACT_SIMPLE, ACT_GELU and ACT_SILU without it.
-template <bool BETA, int A>
+template <bool BETA, int A, bool SHORT>
 __device__ __forceinline__ void finish(float (&v)[32], const ScParams& p, const uint8_t* row, int col, bool live) {
   if constexpr (BETA) {
     if (p.out_kind == OUT_F32)
@@ -135,20 +144,24 @@ __device__ __forceinline__ void finish(float (&v)[32], const ScParams& p, const 
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= p.alpha;
   }
-  sc_act<A>(v, p.act, p.slope);
+  sc_act<A, SHORT>(v, p.act, p.slope);
 }
 
-template <bool PAIR, bool FOUR>
+template <bool PAIR, bool FOUR, bool SIX>
 __global__ void __launch_bounds__(threads<FOUR>(), 1)
     scaled_tile_kernel(const __grid_constant__ ScMaps maps, const __grid_constant__ ScParams p) {
-  using C = Cfg<PAIR, FOUR>;
+  using C = Cfg<PAIR, FOUR, SIX>;
   constexpr int S = C::STAGES;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const sbase = smem_raw + (base - raw);
+  if (SIX && base != raw) {  // (there is no room for another alignment than the declared one)
+    if (threadIdx.x == 0) atomicOr(p.err, WAIT_DRAIN);
+    return;
+  }
   const int warp = sc_warp();
   const int lane = threadIdx.x & 31;
   const uint32_t full0 = base + C::OFF_BAR, empty0 = full0 + 8 * S;
@@ -396,16 +409,17 @@ __global__ void __launch_bounds__(threads<FOUR>(), 1)
     const int q = warp & 3;       // tensor-memory lane quarter this warp may read
     const int half = e >> 2;      // which of the quarter's warps: chunks half, half + 2, ...
     constexpr int kHalves = kEpiWarps / 4;
-    const uint32_t stg0 = base + C::OFF_STG + e * kBox;
-    uint8_t* const stg_p0 = sbase + C::OFF_STG + e * kBox;
-    const int es = p.out_kind == OUT_F32 ? 4 : 2;
-    const int cw = 128 / es;  // columns per 128-byte box row
+    const uint32_t stg0 = base + C::OFF_STG + e * C::BOX;
+    uint8_t* const stg_p0 = sbase + C::OFF_STG + e * C::BOX;
+    const int es = !SIX && p.out_kind == OUT_F32 ? 4 : 2;
+    const int cw = C::ROW / es;  // columns of a box
     const int chunks = C::BN / cw;
     const int shared_chunks = C::OVERLAP / cw;
     constexpr int kSteps = C::BN / 32 / kHalves;  // 32-column steps of a warp
     static_assert(kSteps % 2 == 0, "steps go in pairs");
     const int per = cw / 32;  // steps to a chunk
-    const int sw = lane & 7;  // 128-byte swizzle: 16-byte chunk j of row r lives at j ^ (r % 8)
+    // 128-byte swizzle: 16-byte piece j of row r lives at j ^ (r % 8); 64-byte: at j ^ (r / 2 % 4)
+    const int sw = SIX ? lane >> 1 & 3 : lane & 7;
     int cursor = 0, tiles = 0;
     auto tiles_loop = [&](auto beta_c, auto act_c) {
       constexpr bool BETA = decltype(beta_c)::value;
@@ -446,7 +460,7 @@ __global__ void __launch_bounds__(threads<FOUR>(), 1)
         uint8_t* const d_row = static_cast<uint8_t*>(p.d) + (int64_t(x.zd) * p.d_group + int64_t(y0 + lane) * p.ldd) * es;
         // the shared columns first: the last ones of accumulator 0, the first ones of accumulator 1
         const int first = acc == 0 ? chunks - shared_chunks : 0;
-        // Steps of 32 columns, two to a chunk of 16-bit results: step s is columns 32 * (s % per) of
+        // Steps of 32 columns, two to a chunk of 16-bit results (SIX: one): step s is columns 32 * (s % per) of
         // this warp's chunk s / per.  After step last_shared it has read what the next MMAs wait for (-1: it
         // has none of it).
         auto chunk_of = [&](int s) { return (half + s / per * kHalves + first) & (chunks - 1); };
@@ -456,6 +470,7 @@ __global__ void __launch_bounds__(threads<FOUR>(), 1)
         // prompt through 32 experts 215 -> 208 us, weight gradients of 16 experts 78.6 -> 76.2).  Those steps are unrolled,
         // so that no copy of registers that a load still writes is needed on the way; GELU or SiLU four times over no longer
         // fits the instruction cache (2711 x 3104 x 5376, GELU: 44 us, 56 unrolled; 8192 x 8192 x 1024, SiLU: 71 and 84).
+        // Nor do their short forms gain (SIX, 8192 x 8192 x 512: SiLU 57 us, 61 unrolled; GELU 76 and 100).
         uint32_t ra[32], rb[32];
         auto load = [&](uint32_t (&r)[32], int s) { tmem_ld_32x32b_x32(t_row + chunk_of(s) * cw + 32 * (s % per), r); };
         auto loaded = [&](uint32_t (&r)[32], int s) {
@@ -466,16 +481,16 @@ __global__ void __launch_bounds__(threads<FOUR>(), 1)
           const int h = s % per;
           const int x0 = x.n0 + chunk_of(s) * cw;
           if (x0 >= p.N) return;
-          uint8_t* const row_p = stg_p0 + lane * 128;
+          uint8_t* const row_p = stg_p0 + lane * C::ROW;
           float v[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
-          finish<BETA, A>(v, p, d_row, x0 + 32 * h, mine);
+          finish<BETA, A, SIX>(v, p, d_row, x0 + 32 * h, mine);
           if (opens) {
             if (lane == 0) bulk_wait_read<0>();  // the store that last used this box has read it
             __syncwarp();
           }
-          if (es == 4) {
+          if (!SIX && es == 4) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               *reinterpret_cast<float4*>(row_p + ((j ^ sw) << 4)) =
@@ -494,7 +509,7 @@ __global__ void __launch_bounds__(threads<FOUR>(), 1)
             if (!by_tma) {
               const int piece = 16 / es;
 #pragma unroll 1
-              for (int j = 0; j < 8 && x0 + (j + 1) * piece <= p.n_tma; ++j) {
+              for (int j = 0; j < C::ROW / 16 && x0 + (j + 1) * piece <= p.n_tma; ++j) {
                 uint8_t* const dst = d_row + int64_t(x0 + j * piece) * es;
                 if (DG_IN(p.dbg, dst, 16, DBG_SCALED))
                   *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(row_p + ((j ^ sw) << 4));
@@ -547,9 +562,9 @@ __global__ void __launch_bounds__(threads<FOUR>(), 1)
         for (int s = 0; s < kSteps; s += 2) {
           loaded(ra, s);
           loaded(rb, s + 1);
-          process(ra, s, true, es == 4);
+          process(ra, s, true, SIX || es == 4);
           if (s + 2 < kSteps) load(ra, s + 2);
-          process(rb, s + 1, es == 4, true);
+          process(rb, s + 1, SIX || es == 4, true);
           if (s + 2 < kSteps) load(rb, s + 3);
         }
       }
@@ -584,10 +599,10 @@ __global__ void __launch_bounds__(threads<FOUR>(), 1)
   }
 }
 
-template <bool PAIR, bool FOUR>
+template <bool PAIR, bool FOUR, bool SIX = false>
 cudaError_t launch(const ScMaps& m, const ScParams& p, int grid, cudaStream_t s) {
-  constexpr int smem = Cfg<PAIR, FOUR>::SMEM;
-  auto kern = scaled_tile_kernel<PAIR, FOUR>;
+  constexpr int smem = Cfg<PAIR, FOUR, SIX>::SMEM;
+  auto kern = scaled_tile_kernel<PAIR, FOUR, SIX>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
@@ -622,14 +637,14 @@ cudaError_t launch(const ScMaps& m, const ScParams& p, int grid, cudaStream_t s)
 }
 
 // Pairs that can be resident at once.
-template <bool FOUR>
+template <bool FOUR, bool SIX = false>
 int resident_pairs() {
-  auto kern = scaled_tile_kernel<true, FOUR>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<true, FOUR>::SMEM) != cudaSuccess) return 0;
+  auto kern = scaled_tile_kernel<true, FOUR, SIX>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<true, FOUR, SIX>::SMEM) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(threads<FOUR>());
-  cfg.dynamicSmemBytes = Cfg<true, FOUR>::SMEM;
+  cfg.dynamicSmemBytes = Cfg<true, FOUR, SIX>::SMEM;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;

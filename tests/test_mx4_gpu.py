@@ -306,6 +306,90 @@ def test_product(plan, g, monkeypatch, kernel, M, N, K):
     assert cfg["tile_k"] == 256
 
 
+@pytest.mark.parametrize("M,N,K", [(300, 1030, 1300), (257, 33, 1537), (1, 257, 2048), (2100, 2090, 1281)])
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+def test_six_stages(plan, g, monkeypatch, M, N, K, out):
+    """Pairs into 16 bits with more than four k-blocks: a ring of six stages, boxes of 32 columns."""
+    monkeypatch.setenv("GEMM_SCALED_KERNEL", "pair")
+    rng = np.random.default_rng(M + N + K)
+    A, SA, a = operand(rng, M, K, spread=2)
+    B, SB, b = operand(rng, N, K, spread=2)
+    a, b = a / 64, b / 64  # (alpha)
+    for beta, act in ((0.0, 0), (0.0, 1), (0.0, 3), (0.0, 4), (0.5, 0), (-0.75, 3)):
+        buf, D = float_rows(M, N, out, extra=8, fill=2.0)
+        assert plan.run_mx4(A, SA, B, SB, D, K=K, alpha=2.0 ** -12, beta=beta, act=act, slope=0.1) == g.GEMM_OK
+        assert plan.last_config()["stages"] == 6
+        near(D, *expect(a, b, 1.0, beta, np.full((M, N), 2.0), act, 0.1), out)
+        assert (buf[:, N:] == 2.0).all()
+    _, D = float_rows(M, N, "f32")
+    assert plan.run_mx4(A, SA, B, SB, D, K=K) == g.GEMM_OK and plan.last_config()["stages"] == 5
+    assert plan.poll_error() == g.GEMM_OK
+
+
+@pytest.mark.parametrize("E", [64, 65])
+def test_groups_of_six_and_five_stages(plan, g, monkeypatch, E):
+    import torch
+    monkeypatch.setenv("GEMM_SCALED_KERNEL", "pair")
+    rng = np.random.default_rng(E)
+    N, K = 136, 1300
+    counts = [int(c) for c in np.where(rng.random(E) < 0.2, 0, rng.integers(1, 200, E))]
+    starts, at = [], 0
+    for c in counts:
+        starts.append(at)
+        at += -(-c // 128) * 128
+    A, SA, a = operand(rng, at + 128, K)
+    B = [operand(rng, N, K) for _ in range(E)]
+    Bq, SB = torch.stack([b[0] for b in B]), torch.cat([b[1] for b in B])
+    _, D = float_rows(at + 128, N, "bf16", fill=7.0)
+    dev = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    assert plan.run_grouped_mx4(A, SA, Bq, SB, D, dev(starts), dev(counts), K=K) == g.GEMM_OK
+    assert plan.last_config()["stages"] == (6 if E == 64 else 5)
+    inside = np.zeros(at + 128, bool)
+    for e, (s, c) in enumerate(zip(starts, counts)):
+        if c:
+            inside[s:s + c] = True
+            near(D[s:s + c], *expect(a[s:s + c], B[e][2]), "bf16")
+    assert (D[torch.from_numpy(~inside).cuda()] == 7.0).all()
+    assert plan.poll_error() == g.GEMM_OK
+
+
+@pytest.mark.parametrize("act", [3, 4])
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+def test_activations_of_exact_products(plan, g, monkeypatch, act, out):
+    """One product to each result, exact: the activation by itself, from small values to beyond where it ends, and NaN.
+
+    Tolerance: the exponent's rounding -- SiLU's is one product by a constant that is 2^-26 off, 1.25 |x| 2^-24; GELU's two, of
+    x^2 / 2, 1.125 x^2 2^-24; both below 2^-16 where the result is not 0 -- and 2^-20 for the rest, relative, and half a step."""
+    import torch
+    monkeypatch.setenv("GEMM_SCALED_KERNEL", "pair")
+    K = 1312
+    code, byte = np.zeros((256, K), int), np.full((256, K // 32), 127)
+    code[:, 0] = np.arange(256) % 16  # x = value * value * 2^e, e = -14 to 1
+    byte[:, 0] = 127 - 14 + np.arange(256) // 16
+    w = np.zeros((24, K), int)
+    w[:, 0] = 1 + np.arange(24) % 7
+    wb = np.full((24, K // 32), 127)
+    wb[8:, 0], wb[16:, 0] = 130, 127 + 120  # times 8; far out
+    a, b = (ref.scaled4(ref.decode4(ref.pack4(c), K), s) for c, s in ((code, byte), (w, wb)))
+    byte[255, 0] = 255
+    dev = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
+    buf, D = float_rows(256, 24, out)
+    A, B = (dev(np.ascontiguousarray(ref.pack4(c))) for c in (code, w))
+    assert A.stride(0) % 16 == 0
+    assert plan.run_mx4(A, dev(ref.pack_scales4(byte, K)), B, dev(ref.pack_scales4(wb, K)), D, K=K, act=act) == g.GEMM_OK
+    assert plan.last_config()["stages"] == 6 and plan.poll_error() == g.GEMM_OK
+    assert torch.isnan(D[255]).all()
+    x = (a @ b.T)[:255]
+    want = scaled_ref.act(x, act)
+    most = 65520 if out == "f16" else 3.4e38
+    got, want = (np.where(np.abs(v) >= most, np.sign(v) * most, v) for v in (D[:255].double().cpu().numpy(), want))
+    part = np.minimum(1.25 * np.abs(x) * 2.0 ** -24 if act == 4 else 1.125 * x * x * 2.0 ** -24, 2.0 ** -16)
+    # (1 / (1 + exp(-x)) and exp(-x^2 / 2) below the smallest normal number, 2^-126, may be 0)
+    tol = np.abs(want) * (part + 2.0 ** -20 + ROUND[out]) + (2.0 ** -25 if out == "f16" else 2.0 ** -119)
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (x[bad][:4], got[bad][:4], want[bad][:4])
+
+
 @pytest.mark.parametrize("slices", [1, 2, 3, 5, 8])
 def test_product_slices(plan, g, monkeypatch, slices):
     monkeypatch.setenv("GEMM_SCALED_KERNEL", "sliced")
