@@ -172,7 +172,7 @@ ScPick pick(const Product& x, int sms) {
     if (per <= (x.four ? kFewRowsMx4 : kFewRows))
       c = pick_sliced(x.four, 128, active * nb, sms);
     else  // (256 rows each: 53.6 us on single CTAs, 48.8 on pairs; 8 experts of 4096 x 1024, 150 rows: 14.9 and 18.3.
-          // 4 bits, 32 experts of 2048 x 2048: 128 rows 22.4 and 26.3, 160 rows 31.2 and 27.7)
+          // 4 bits, 32 experts of 2048 x 2048: 128 rows 22.4 and 25.3, 160 rows 31.2 and 26.7)
       c.kernel = per < (x.four ? 129 : 256) ? SC_TILE : SC_PAIR;
   } else if (x.group == SC_K) {
     // (16 gradients of 2048 x 2048: 192 rows each, 319 with the padding, 49.8 us on single CTAs, 52.3 on pairs; 384 rows
@@ -307,8 +307,8 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   p.idesc = ((sliced ? tb : ta) << 7) | ((sliced ? ta : tb) << 10) | (mma_n >> 3 << 17) | (1u << 23) | (mma_m >> 4 << 24);
   // Groups of tile rows walked column by column: tiles that run at the same time share
   // rows of A and of B in L2.
-  // (4 bits, up to eight k-blocks: 8192 x 8192 x 2048 in groups of 4 59.1 us, of 8 60.8, of 16 63.6; more: 4096 x 4096 x 8192 61.2, 54.4
-  // and 56.4, 8192 x 8192 x 16384 370, 345 and 344)
+  // (4 bits, up to eight k-blocks: 8192 x 8192 x 2048 in groups of 4 53.6 us, of 8 54.9; more: 4096 x 4096 x 8192 52.5 and 51.8,
+  // 8192 x 8192 x 16384 335 and 320)
   p.raster = sliced ? std::max(1, p.m_blocks) : x.four && p.k_blocks <= 8 ? 4 : 8;
   const int64_t bound = x.group == SC_ROWS  // SC_ROWS: whole tiles and one partial tile for each group at most
                             ? (ceil_div(x.M, tile_m) + std::min<int64_t>(x.groups, ceil_div(x.M, 128))) * p.n_blocks

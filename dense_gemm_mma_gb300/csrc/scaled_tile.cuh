@@ -31,9 +31,9 @@
 //    group before every second MMA).
 // SIX: a sixth stage where the results are 16-bit and the groups few.  An epilogue warp's box is then 32 columns of 64
 // bytes, and the tables of the groups are short: 8192^3 172 -> 159 us, 2304 x 6912 x 8192 54.6 -> 51.1.
-// 8192^3 into bf16 168 to 178 us, 6.2 to 6.5 PFLOP/s.  The MMAs of a k-block take 512 cycles, a k-block 550 while the ring is
-// full and 640 to 1,100 behind it: without the copies (wrong results) 154 us, without the stores 150, without the loads 139; the
-// MMAs of the next tile begin ~900 cycles after the last of this one (their completion, 500 for 128 columns to be read, the signal).
+// 8192^3 into bf16 157 to 160 us, 6.9 to 7.0 PFLOP/s.  The MMAs of a k-block take 512 cycles; of five stages a k-block took 550 while the
+// ring was full and 640 to 1,100 behind it: 168 to 178 us, without the copies (wrong results) 154, without the stores 150, without the
+// loads 139.  The MMAs of the next tile begin ~900 cycles after the last of this one (their completion, 500 for 128 columns to be read, the signal).
 //
 // What bounds it (8 bits): 8192^3 into bf16 330 to 360 us, 3.1 to 3.3 PFLOP/s, at the power limit (287 us, 3.8
 // PFLOP/s, with operands whose bits change little).  Short K: the turnover of the tiles, with no unit full.  16 weight
