@@ -423,7 +423,7 @@ cudaError_t launch_quantize(const QuantArgs& a, cudaStream_t s);
 
 // The same into 4 bits (E2M1, a scale for each row and block of 32): cols values are (cols + 1) / 2 bytes;
 // block_rows, e5m2 and cols_padded are not used, q_groups and qt_groups count blocks in fours as above.
-cudaError_t launch_quantize_mx4(const QuantArgs& a, cudaStream_t s);
+cudaError_t launch_quantize_mx4(const QuantArgs& a, int sms, cudaStream_t s);
 
 enum CodeKind : int { CODE_E4M3 = 0, CODE_E5M2 = 1, CODE_E2M1 = 2 };
 

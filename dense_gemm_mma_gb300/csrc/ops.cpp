@@ -654,8 +654,8 @@ gemm_status_t gemm_quantize_mx(gemm_plan_t plan, int64_t rows, int64_t cols, con
                                 int64_t ldq, void* SQ, void* QT, int64_t ldqt, void* SQT, void* stream) {
   if (!plan || rows < 0 || cols < 0 || src_rows < 0 || !is_float_type(x_type)) return GEMM_ERR_INVALID_ARG;
   if (rowmap && map_div < 1) return GEMM_ERR_INVALID_ARG;
-  // (the grid takes 65535 row blocks)
-  if (!size_ok(rows) || !size_ok(cols) || !size_ok(src_rows) || rows > int64_t(65532) * 128 || map_div > kMaxDim)
+  // (indices behind the last tile have to fit 32 bits too)
+  if (!size_ok(rows) || !size_ok(cols + 1024) || !size_ok(src_rows) || rows > int64_t(65532) * 128 || map_div > kMaxDim)
     return GEMM_ERR_UNSUPPORTED;
   if ((Q == nullptr) != (SQ == nullptr) || (QT == nullptr) != (SQT == nullptr) || (!Q && !QT)) return GEMM_ERR_INVALID_ARG;
   const int64_t one = 1, cb = ceil_div(cols, 2), rb = ceil_div(rows, 2);
@@ -701,14 +701,14 @@ gemm_status_t gemm_quantize_mx(gemm_plan_t plan, int64_t rows, int64_t cols, con
               .bytes(SQ, SQ ? sq : 0).out_matrix(QT, QT ? cols : 0, rb, ldqt, 1).bytes(SQT, SQT ? sqt : 0)
               .bytes(rowmap, rowmap ? rows * 4 : 0).s;
 #endif
-  return call.done(launched(launch_quantize_mx4(a, static_cast<cudaStream_t>(stream))));
+  return call.done(launched(launch_quantize_mx4(a, plan->sms, static_cast<cudaStream_t>(stream))));
 }
 
 gemm_status_t gemm_dequantize(gemm_plan_t plan, int64_t rows, int64_t cols, const void* Q, int64_t ldq, gemm_type_t q_type,
                               const void* SQ, void* X, int64_t ldx, gemm_type_t x_type, void* stream) {
   const bool four = q_type == GEMM_TYPE_E2M1;
   if (!plan || rows < 0 || cols < 0 || !is_float_type(x_type) || (!four && !is_code_type(q_type))) return GEMM_ERR_INVALID_ARG;
-  if (!size_ok(rows) || !size_ok(cols) || rows * ceil_div(cols, 512) > kMaxDim * 16)  // (its grid)
+  if (!size_ok(rows + 1024) || !size_ok(cols + 1024) || rows * ceil_div(cols, 512) > kMaxDim * 16)  // (its grid)
     return GEMM_ERR_UNSUPPORTED;
   const int64_t one = 1, cb = four ? ceil_div(cols, 2) : cols;
   if (ldq < std::max(one, cb) || ldx < std::max(one, cols)) return GEMM_ERR_INVALID_ARG;

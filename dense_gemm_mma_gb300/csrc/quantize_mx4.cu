@@ -9,7 +9,7 @@
 // One orientation: warps take rows, no barrier.  Both: a CTA takes 128 x 128 values, which is one scale tile (128 rows x
 // 4 blocks) in either orientation; half a warp holds 128 columns of a row, a lane eight neighbouring columns of four
 // neighbouring rows.  A row's block is four lanes (two exchanges), a column's block 32 rows of four warps (through shared memory).
-// What bounds it is issuing instructions: 8192 x 4096 bf16 19 us one way (85 MB, 4.4 TB/s), 30 both (103 MB), where a thread spends ~22
+// What bounds it is issuing instructions: 8192 x 4096 bf16 19 us one way (85 MB, 4.4 TB/s), 29 both (103 MB), where a thread spends ~22
 // instructions a value; back to bf16 14.6 us (85 MB, 5.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -217,141 +217,196 @@ __global__ void __launch_bounds__(256) quantize_mx4_rows_kernel(const QuantArgs 
     }
 }
 
-// Both orientations, or the transposed one.
-template <typename T, bool VEC>
+// 16 bytes from global to shared memory, complete for the thread that asked after copies_wait().
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(to))), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Both orientations, or the transposed one.  AHEAD (16-bit types by 16 bytes): a CTA takes one tile after another, and the next tile's
+// values are copied to shared memory, where each thread reads its own again, while it works on one.
+template <typename T, bool VEC, bool AHEAD>
 __global__ void __launch_bounds__(32 * kWarps, 2) quantize_mx4_kernel(const QuantArgs a) {
   constexpr int COLS = 8 / (sizeof(T) == 4 ? 1 : 2);  // words of maxima of a lane's eight columns
+  static_assert(!AHEAD || (VEC && sizeof(T) == 2), "copies of eight values are 16 bytes");
   __shared__ uint32_t row_bytes[128];          // the scale tile of Q, word by row
   alignas(16) __shared__ uint32_t col_max[kWarps][16 * COLS];
   __shared__ uint8_t col_byte[4][128];         // [block of 32 rows][column]
   __shared__ uint16_t turn[128 * 32];          // [column][4 rows ^ swizzle]
+  __shared__ uint4 ahead[AHEAD ? kLaneRows * 32 * kWarps : 1];  // [row of a lane][thread]
   wait_prior_grid();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int cb = blockIdx.x, rb = blockIdx.y;
   const int row0 = warp * 8 + (lane >> 4) * kLaneRows;  // of the tile
-  const int piece = lane & 15, col = cb * 128 + piece * 8;
-  Row8<T> v[kLaneRows];
-  uint32_t live = 0;
-  {
+  const int piece = lane & 15;
+  const int col_blocks = (a.cols + 127) / 128, row_blocks = (a.rows + 127) / 128;
+  int cb = blockIdx.x, rb = blockIdx.y, step_c = 0, step_r = 0;
+  if constexpr (AHEAD) {  // (one row of CTAs, no more than there are tiles)
+    rb = int(blockIdx.x / unsigned(col_blocks)), cb = int(blockIdx.x % unsigned(col_blocks));
+    step_r = int(gridDim.x / unsigned(col_blocks)), step_c = int(gridDim.x % unsigned(col_blocks));
+  }
+  // The tile's rows of this lane that exist, whose values are on their way (of whole eights; the others are loaded when it
+  // is the tile's turn).
+  auto fetch = [&](int c, int r) {
     int all[8];
-    source_rows(a, rb * 128 + warp * 8, all);
+    source_rows(a, r * 128 + warp * 8, all);
+    uint32_t rows = 0;
+    const int at = c * 128 + piece * 8;
 #pragma unroll
     for (int i = 0; i < kLaneRows; ++i) {
       const int src = lane < 16 ? all[i] : all[i + kLaneRows];
-      live |= uint32_t(src >= 0) << i;
-      v[i].load(a, src, col, VEC);
+      rows |= uint32_t(src >= 0) << i;
+      const T* const p = static_cast<const T*>(a.x) + int64_t(src) * a.ldx + at;
+      if (src >= 0 && at + 8 <= a.cols && DG_IN(a.dbg, p, 16, DBG_QUANTIZE)) copy16(&ahead[i * 32 * kWarps + threadIdx.x], p);
     }
-  }
-  {
-    uint32_t m[COLS];
+    return rows;
+  };
+  uint32_t live = 0;
+  if constexpr (AHEAD) live = fetch(cb, rb);
+  do {
+    const int col = cb * 128 + piece * 8;
+    Row8<T> v[kLaneRows];
+    if constexpr (AHEAD) {
+      copies_wait();
 #pragma unroll
-    for (int j = 0; j < COLS; ++j) {
-      m[j] = magnitude<T>(v[0].w[j]);
-#pragma unroll
-      for (int i = 1; i < kLaneRows; ++i) m[j] = most<T>(m[j], magnitude<T>(v[i].w[j]));
-      m[j] = most<T>(m[j], __shfl_xor_sync(kAll, m[j], 16));
-    }
-    if (lane < 16) {
-#pragma unroll
-      for (int j = 0; j < COLS; j += 4)
-        *reinterpret_cast<uint4*>(&col_max[warp][piece * COLS + j]) = make_uint4(m[j], m[j + 1], m[j + 2], m[j + 3]);
-    }
-  }
-  if (a.q) {
-#pragma unroll
-    for (int i = 0; i < kLaneRows; ++i) {
-      const uint32_t byte = row_byte<T>(v[i]);
-      const uint32_t c = row_codes(byte, v[i]);
-      // the word of four blocks, in lanes 0 and 16
-      uint32_t word = byte | __shfl_down_sync(kAll, byte, 4) << 8;
-      word |= __shfl_down_sync(kAll, word, 8) << 16;
-      if (piece == 0) row_bytes[row0 + i] = word;
-      if ((live >> i) & 1u) store_codes(a, a.q + int64_t(rb * 128 + row0 + i) * a.ldq + col / 2, c, (a.cols - col + 1) / 2);
-    }
-  }
-  __syncthreads();
-  if (a.q && threadIdx.x < 32) {  // line `lane` of the tile: rows lane, lane + 32, lane + 64, lane + 96
-    uint8_t* const s = a.sq + (int64_t(rb) * a.q_groups + cb) * 512 + lane * 16;
-    if (DG_IN(a.dbg, s, 16, DBG_QUANTIZE))
-      *reinterpret_cast<uint4*>(s) = make_uint4(row_bytes[lane], row_bytes[lane + 32], row_bytes[lane + 64], row_bytes[lane + 96]);
-  }
-  if (threadIdx.x < 64 * COLS) {  // one thread a word of columns and block of 32 rows
-    const int c = threadIdx.x % (16 * COLS), b = threadIdx.x / (16 * COLS);
-    const uint32_t m = most<T>(most<T>(col_max[4 * b][c], col_max[4 * b + 1][c]), most<T>(col_max[4 * b + 2][c], col_max[4 * b + 3][c]));
-    if constexpr (sizeof(T) == 4)
-      col_byte[b][c] = uint8_t(byte_of<T>(m));
-    else
-      *reinterpret_cast<uint16_t*>(&col_byte[b][2 * c]) = uint16_t(byte_of<T>(m & 0xffffu) | byte_of<T>(m >> 16) << 8);
-  }
-  __syncthreads();
-  {
-    const uint2 bytes = *reinterpret_cast<const uint2*>(&col_byte[warp / 4][piece * 8]);
-    uint16_t* const to = turn + piece * 8 * 32 + ((warp * 2 + (lane >> 4)) ^ (piece * 2));
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {  // two columns at a time
-      const uint32_t b0 = ((j < 4 ? bytes.x : bytes.y) >> (8 * (j & 3))) & 0xffu, b1 = ((j < 4 ? bytes.x : bytes.y) >> (8 * (j & 3) + 8)) & 0xffu;
-      const float i0 = mx4_inverse(b0), i1 = mx4_inverse(b1);
-      uint32_t c;
-      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        const uint32_t by = __byte_perm(__float_as_uint(i0), __float_as_uint(i1), 0x7632);
-        const uint32_t p = times2(v[0].w[j / 2], by), q = times2(v[1].w[j / 2], by), r = times2(v[2].w[j / 2], by),
-                       s = times2(v[3].w[j / 2], by);
-        c = mx4_codes8(low(p), low(q), low(r), low(s), high(p), high(q), high(r), high(s));
-      } else {
-        c = mx4_codes8(v[0].at(j) * i0, v[1].at(j) * i0, v[2].at(j) * i0, v[3].at(j) * i0, v[0].at(j + 1) * i1,
-                       v[1].at(j + 1) * i1, v[2].at(j + 1) * i1, v[3].at(j + 1) * i1);
+      for (int i = 0; i < kLaneRows; ++i) {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (((live >> i) & 1u) && col + 8 <= a.cols) w = ahead[i * 32 * kWarps + threadIdx.x];
+        v[i].w[0] = w.x, v[i].w[1] = w.y, v[i].w[2] = w.z, v[i].w[3] = w.w;
       }
-      to[j * 32] = uint16_t(b0 == 255u ? 0u : c);
-      to[(j + 1) * 32] = uint16_t(b1 == 255u ? 0u : c >> 16);
     }
-  }
-  __syncthreads();
-  {  // 16 bytes of a column: 32 rows
-    const int c = threadIdx.x >> 2, part = threadIdx.x & 3, x = (c >> 3) * 2;
-    const int out_row = cb * 128 + c, r = rb * 128 + part * 32;
-    if (out_row < a.cols && r < a.rows) {
-      uint32_t w[4];
+    if (!AHEAD || __any_sync(kAll, col < a.cols && col + 8 > a.cols)) {
+      int all[8];
+      source_rows(a, rb * 128 + warp * 8, all);
+      if (!AHEAD) live = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const uint32_t*>(&turn[c * 32 + ((part * 8 + 2 * k) ^ x)]);
-      uint8_t* const dst = a.qt + int64_t(out_row) * a.ldqt + r / 2;
-      const int n = min(16, (a.rows - r + 1) / 2);
-      if (DG_IN(a.dbg, dst, n, DBG_QUANTIZE)) {
-        if (n == 16 && a.qt_wide) {
-          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int i = 0; i < kLaneRows; ++i) {
+        const int src = lane < 16 ? all[i] : all[i + kLaneRows];
+        if (!AHEAD) live |= uint32_t(src >= 0) << i;
+        if (!AHEAD || col + 8 > a.cols) v[i].load(a, src, col, VEC && !AHEAD);
+      }
+    }
+    {
+      uint32_t m[COLS];
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) {
+        m[j] = magnitude<T>(v[0].w[j]);
+#pragma unroll
+        for (int i = 1; i < kLaneRows; ++i) m[j] = most<T>(m[j], magnitude<T>(v[i].w[j]));
+        m[j] = most<T>(m[j], __shfl_xor_sync(kAll, m[j], 16));
+      }
+      if (lane < 16) {
+#pragma unroll
+        for (int j = 0; j < COLS; j += 4)
+          *reinterpret_cast<uint4*>(&col_max[warp][piece * COLS + j]) = make_uint4(m[j], m[j + 1], m[j + 2], m[j + 3]);
+      }
+    }
+    if (a.q) {
+#pragma unroll
+      for (int i = 0; i < kLaneRows; ++i) {
+        const uint32_t byte = row_byte<T>(v[i]);
+        const uint32_t c = row_codes(byte, v[i]);
+        // the word of four blocks, in lanes 0 and 16
+        uint32_t word = byte | __shfl_down_sync(kAll, byte, 4) << 8;
+        word |= __shfl_down_sync(kAll, word, 8) << 16;
+        if (piece == 0) row_bytes[row0 + i] = word;
+        if ((live >> i) & 1u) store_codes(a, a.q + int64_t(rb * 128 + row0 + i) * a.ldq + col / 2, c, (a.cols - col + 1) / 2);
+      }
+    }
+    __syncthreads();
+    int next_c = cb + step_c, next_r = rb + step_r;
+    if constexpr (AHEAD) {
+      if (next_c >= col_blocks) next_c -= col_blocks, ++next_r;
+      if (next_r < row_blocks) live = fetch(next_c, next_r);
+    }
+    if (a.q && threadIdx.x < 32) {  // line `lane` of the tile: rows lane, lane + 32, lane + 64, lane + 96
+      uint8_t* const s = a.sq + (int64_t(rb) * a.q_groups + cb) * 512 + lane * 16;
+      if (DG_IN(a.dbg, s, 16, DBG_QUANTIZE))
+        *reinterpret_cast<uint4*>(s) = make_uint4(row_bytes[lane], row_bytes[lane + 32], row_bytes[lane + 64], row_bytes[lane + 96]);
+    }
+    if (threadIdx.x < 64 * COLS) {  // one thread a word of columns and block of 32 rows
+      const int c = threadIdx.x % (16 * COLS), b = threadIdx.x / (16 * COLS);
+      const uint32_t m = most<T>(most<T>(col_max[4 * b][c], col_max[4 * b + 1][c]), most<T>(col_max[4 * b + 2][c], col_max[4 * b + 3][c]));
+      if constexpr (sizeof(T) == 4)
+        col_byte[b][c] = uint8_t(byte_of<T>(m));
+      else
+        *reinterpret_cast<uint16_t*>(&col_byte[b][2 * c]) = uint16_t(byte_of<T>(m & 0xffffu) | byte_of<T>(m >> 16) << 8);
+    }
+    __syncthreads();
+    {
+      const uint2 bytes = *reinterpret_cast<const uint2*>(&col_byte[warp / 4][piece * 8]);
+      uint16_t* const to = turn + piece * 8 * 32 + ((warp * 2 + (lane >> 4)) ^ (piece * 2));
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {  // two columns at a time
+        const uint32_t b0 = ((j < 4 ? bytes.x : bytes.y) >> (8 * (j & 3))) & 0xffu, b1 = ((j < 4 ? bytes.x : bytes.y) >> (8 * (j & 3) + 8)) & 0xffu;
+        const float i0 = mx4_inverse(b0), i1 = mx4_inverse(b1);
+        uint32_t c;
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+          const uint32_t by = __byte_perm(__float_as_uint(i0), __float_as_uint(i1), 0x7632);
+          const uint32_t p = times2(v[0].w[j / 2], by), q = times2(v[1].w[j / 2], by), r = times2(v[2].w[j / 2], by),
+                         s = times2(v[3].w[j / 2], by);
+          c = mx4_codes8(low(p), low(q), low(r), low(s), high(p), high(q), high(r), high(s));
         } else {
+          c = mx4_codes8(v[0].at(j) * i0, v[1].at(j) * i0, v[2].at(j) * i0, v[3].at(j) * i0, v[0].at(j + 1) * i1,
+                         v[1].at(j + 1) * i1, v[2].at(j + 1) * i1, v[3].at(j + 1) * i1);
+        }
+        to[j * 32] = uint16_t(b0 == 255u ? 0u : c);
+        to[(j + 1) * 32] = uint16_t(b1 == 255u ? 0u : c >> 16);
+      }
+    }
+    __syncthreads();
+    {  // 16 bytes of a column: 32 rows
+      const int c = threadIdx.x >> 2, part = threadIdx.x & 3, x = (c >> 3) * 2;
+      const int out_row = cb * 128 + c, r = rb * 128 + part * 32;
+      if (out_row < a.cols && r < a.rows) {
+        uint32_t w[4];
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (k < n) dst[k] = uint8_t(w[k / 4] >> (8 * (k & 3)));
+        for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const uint32_t*>(&turn[c * 32 + ((part * 8 + 2 * k) ^ x)]);
+        uint8_t* const dst = a.qt + int64_t(out_row) * a.ldqt + r / 2;
+        const int n = min(16, (a.rows - r + 1) / 2);
+        if (DG_IN(a.dbg, dst, n, DBG_QUANTIZE)) {
+          if (n == 16 && a.qt_wide) {
+            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (k < n) dst[k] = uint8_t(w[k / 4] >> (8 * (k & 3)));
+          }
         }
       }
     }
-  }
-  if (threadIdx.x < 32) {
-    uint32_t w[4];
+    if (threadIdx.x < 32) {
+      uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = lane + 32 * k;
-      w[k] = uint32_t(col_byte[0][c]) | uint32_t(col_byte[1][c]) << 8 | uint32_t(col_byte[2][c]) << 16 | uint32_t(col_byte[3][c]) << 24;
+      for (int k = 0; k < 4; ++k) {
+        const int c = lane + 32 * k;
+        w[k] = uint32_t(col_byte[0][c]) | uint32_t(col_byte[1][c]) << 8 | uint32_t(col_byte[2][c]) << 16 | uint32_t(col_byte[3][c]) << 24;
+      }
+      uint8_t* const s = a.sqt + (int64_t(cb) * a.qt_groups + rb) * 512 + lane * 16;
+      if (DG_IN(a.dbg, s, 16, DBG_QUANTIZE)) *reinterpret_cast<uint4*>(s) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    uint8_t* const s = a.sqt + (int64_t(cb) * a.qt_groups + rb) * 512 + lane * 16;
-    if (DG_IN(a.dbg, s, 16, DBG_QUANTIZE)) *reinterpret_cast<uint4*>(s) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+    cb = next_c, rb = next_r;
+  } while (AHEAD && rb < row_blocks);
 }
 
 template <typename T, bool VEC>
-cudaError_t launch_mx4(const QuantArgs& a, cudaStream_t s) {
+cudaError_t launch_mx4(const QuantArgs& a, int sms, cudaStream_t s) {
   if (!a.qt) {
     const uint32_t chunks = uint32_t((a.cols + 511) / 512);
     const int64_t warps = int64_t(a.rows_padded / kRowRows) * chunks;
     return launch_k(quantize_mx4_rows_kernel<T, VEC>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0, s, a.pdl, a, chunks);
   }
-  return launch_k(quantize_mx4_kernel<T, VEC>, dim3(unsigned((a.cols + 127) / 128), unsigned((a.rows + 127) / 128)),
-                  dim3(32 * kWarps), 0, s, a.pdl, a);
+  const dim3 tiles(unsigned((a.cols + 127) / 128), unsigned((a.rows + 127) / 128));
+  // Tiles one after another once there are more than run at the same time (8192 x 4096 bf16, both orientations: 29.3 us, each tile a CTA of its
+  // own 30.9; transposed alone 20.1 and 24.6; fewer tiles 0.3 us longer; fp32, without the copies ahead, 38.2 and 34.5).
+  if constexpr (VEC && sizeof(T) == 2) {
+    if (int64_t(tiles.x) * tiles.y > 2 * sms) return launch_k(quantize_mx4_kernel<T, true, true>, dim3(unsigned(2 * sms)), dim3(32 * kWarps), 0, s, a.pdl, a);
+  }
+  return launch_k(quantize_mx4_kernel<T, VEC, false>, tiles, dim3(32 * kWarps), 0, s, a.pdl, a);
 }
 
 template <typename T>
-cudaError_t launch_mx4_type(const QuantArgs& a, cudaStream_t s) {
-  return a.vec ? launch_mx4<T, true>(a, s) : launch_mx4<T, false>(a, s);
+cudaError_t launch_mx4_type(const QuantArgs& a, int sms, cudaStream_t s) {
+  return a.vec ? launch_mx4<T, true>(a, sms, s) : launch_mx4<T, false>(a, sms, s);
 }
 
 // ------------------------------------------------------------------ values
@@ -474,11 +529,11 @@ cudaError_t launch_values(const DequantArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_quantize_mx4(const QuantArgs& a, cudaStream_t s) {
+cudaError_t launch_quantize_mx4(const QuantArgs& a, int sms, cudaStream_t s) {
   switch (a.x_kind) {
-    case OUT_F32: return launch_mx4_type<float>(a, s);
-    case OUT_BF16: return launch_mx4_type<__nv_bfloat16>(a, s);
-    default: return launch_mx4_type<__half>(a, s);
+    case OUT_F32: return launch_mx4_type<float>(a, sms, s);
+    case OUT_BF16: return launch_mx4_type<__nv_bfloat16>(a, sms, s);
+    default: return launch_mx4_type<__half>(a, sms, s);
   }
 }
 

@@ -540,7 +540,7 @@ int64_t gemm_mx_scale_bytes(int64_t rows, int64_t cols);
  * the value over the scale, rounded to nearest, ties to the even code.  A block of zeros has the scale byte 0, one
  * that holds an infinity or NaN the byte 255 and codes of 0.
  * Q and QT at any address, rows any number of bytes apart (16-byte boundaries are fastest, and spare the products a
- * copy); otherwise alignment, rowmap, map_div, src_rows, aliasing and limits as in gemm_quantize. */
+ * copy); otherwise alignment, rowmap, map_div, src_rows, aliasing and limits as in gemm_quantize, but 2^31 - 1025 columns at most. */
 gemm_status_t gemm_quantize_mx(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx,
                                 gemm_type_t x_type, const int32_t* rowmap, int64_t map_div, int64_t src_rows, void* Q,
                                 int64_t ldq, void* SQ, void* QT, int64_t ldqt, void* SQT, void* stream);
@@ -550,7 +550,8 @@ gemm_status_t gemm_quantize_mx(gemm_plan_t plan, int64_t rows, int64_t cols, con
  * scale are exact in fp32 unless they leave its range; one rounding to X's type, which is exact too for bf16 and fp32 while the values
  * stay within their normal numbers.  The way back from weights kept in 8 or 4 bits to gemm_run's operands.
  * Q at any address, rows ldq bytes apart (8 codes on a boundary of their size are read fastest), SQ 16-byte aligned, X
- * aligned to its element (rows on 16-byte boundaries are faster); X may share no byte with Q or SQ. */
+ * aligned to its element (rows on 16-byte boundaries are faster); X may share no byte with Q or SQ.  2^31 - 1025 rows or
+ * columns at most. */
 gemm_status_t gemm_dequantize(gemm_plan_t plan, int64_t rows, int64_t cols, const void* Q, int64_t ldq, gemm_type_t q_type,
                               const void* SQ, void* X, int64_t ldx, gemm_type_t x_type, void* stream);
 

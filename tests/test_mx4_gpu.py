@@ -158,6 +158,52 @@ def test_quantize_through_a_row_map(plan, g, name):
     assert np.array_equal(sqt.cpu().numpy(), ref.pack_scales4(byte_t, rows))
 
 
+@pytest.mark.parametrize("R,K,gathered", [(2500, 2699, False), (2688, 2688, False), (2500, 2704, True), (130, 40100, False)])
+@pytest.mark.parametrize("name", ["bf16", "f16", "f32"])
+def test_quantize_more_tiles_than_ctas(plan, g, R, K, gathered, name):
+    """Both orientations of more 128 x 128 tiles than CTAs run at once; a part of the rows and columns against 64 bits."""
+    import torch
+    rng = np.random.default_rng(R + K)
+    x = torch.from_numpy(rng.standard_normal((R, K)) * 10.0 ** rng.integers(-3, 3, (R, 1))).to(dtype(name))
+    _, xd = float_rows(R, K, name)
+    xd.copy_(x)
+    rowmap, source = None, np.arange(R)
+    if gathered:
+        source = np.where(rng.random(R) < 0.1, -1, rng.integers(0, R, R))
+        rowmap = torch.from_numpy(source.astype(np.int32)).cuda()
+    x64 = np.where(source[:, None] >= 0, x.double().numpy()[np.maximum(source, 0)], 0.0)
+    _, q = byte_rows(R, -(-K // 2), 0xA5)
+    _, qt = byte_rows(K, -(-R // 2), 0xA5)
+    sq, sqt, one, tone = scale_room(g, R, K), scale_room(g, K, R), scale_room(g, R, K), scale_room(g, K, R)
+    for _ in range(2):
+        assert plan.quantize_mx4(xd, q, sq, qt, sqt, rowmap=rowmap) == g.GEMM_OK
+    assert plan.quantize_mx4(xd, None, None, qt[:, :], tone, rowmap=rowmap) == g.GEMM_OK and torch.equal(tone, sqt)
+    _, q1 = byte_rows(R, -(-K // 2), 0xA5)
+    assert plan.quantize_mx4(xd, q1, one, rowmap=rowmap) == g.GEMM_OK
+    assert torch.equal(one, sq) and torch.equal(q1, q)  # the rows' kernel says the same
+    rows = np.unique(np.concatenate([rng.integers(0, R, 12), [0, R - 1]]))
+    cols = np.unique(np.concatenate([rng.integers(0, K, 25), [0, K - 1]]))
+    want, byte = ref.quantize4(x64[rows])
+    live = source[rows] >= 0
+    same(ref.decode4(q.cpu().numpy()[rows], K)[live], want[live])
+    want_t, byte_t = ref.quantize4(x64.T[cols])
+    same(ref.decode4(qt.cpu().numpy()[cols], R), want_t)
+    for packed, at, want_b, width in ((sq, rows, byte, K), (sqt, cols, byte_t, R)):
+        tiles, nb = -(-width // 128), np.arange(want_b.shape[1])
+        where = ((at[:, None] // 128) * tiles + nb // 4) * 512 + at[:, None] % 32 * 16 + at[:, None] % 128 // 32 * 4 + nb % 4
+        assert np.array_equal(packed.cpu().numpy()[where], want_b)
+
+
+def test_sizes_past_the_indices(plan, g):
+    import torch
+    x = torch.zeros(64, device="cuda", dtype=torch.bfloat16)
+    n, p = 2 ** 31 - 1, x.data_ptr()
+    # (refused by its size before anything is read)
+    assert g.gemm_quantize_mx(plan.handle, 1, n, p, n, 0, None, 1, 1, p + 32, n, p + 64, None, 0, None) == g.GEMM_ERR_UNSUPPORTED
+    assert g.gemm_dequantize(plan.handle, 1, n, p, n, 6, p + 64, p + 32, n, 0) == g.GEMM_ERR_UNSUPPORTED
+    assert g.gemm_dequantize(plan.handle, n, 1, p, n, 6, p + 64, p + 32, n, 0) == g.GEMM_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("R,K", [(1, 1), (3, 33), (130, 515), (64, 1024)])
 @pytest.mark.parametrize("out", ["bf16", "f32", "f16"])
 def test_dequantize(plan, g, R, K, out):
