@@ -223,6 +223,24 @@ __device__ __forceinline__ void copy16(void* to, const void* from) {
 }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Rows of X that this lane's rows of a tile come from: half a warp's kLaneRows of the warp's eight from r0 on.  (Without a map there is
+// nothing to exchange.)
+__device__ __forceinline__ void lane_rows(const QuantArgs& a, int r0, int (&src)[kLaneRows]) {
+  const bool lower = (threadIdx.x & 31) < 16;
+  if (a.rowmap) {
+    int all[2 * kLaneRows];
+    source_rows(a, r0, all);
+#pragma unroll
+    for (int i = 0; i < kLaneRows; ++i) src[i] = lower ? all[i] : all[i + kLaneRows];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kLaneRows; ++i) {
+      const int r = r0 + (lower ? i : i + kLaneRows);
+      src[i] = r < a.rows ? r : -1;
+    }
+  }
+}
+
 // Both orientations, or the transposed one.  AHEAD (16-bit types by 16 bytes): a CTA takes one tile after another, and the next tile's
 // values are copied to shared memory, where each thread reads its own again, while it works on one.
 template <typename T, bool VEC, bool AHEAD>
@@ -247,16 +265,15 @@ __global__ void __launch_bounds__(32 * kWarps, 2) quantize_mx4_kernel(const Quan
   // The tile's rows of this lane that exist, whose values are on their way (of whole eights; the others are loaded when it
   // is the tile's turn).
   auto fetch = [&](int c, int r) {
-    int all[8];
-    source_rows(a, r * 128 + warp * 8, all);
+    int src[kLaneRows];
+    lane_rows(a, r * 128 + warp * 8, src);
     uint32_t rows = 0;
     const int at = c * 128 + piece * 8;
 #pragma unroll
     for (int i = 0; i < kLaneRows; ++i) {
-      const int src = lane < 16 ? all[i] : all[i + kLaneRows];
-      rows |= uint32_t(src >= 0) << i;
-      const T* const p = static_cast<const T*>(a.x) + int64_t(src) * a.ldx + at;
-      if (src >= 0 && at + 8 <= a.cols && DG_IN(a.dbg, p, 16, DBG_QUANTIZE)) copy16(&ahead[i * 32 * kWarps + threadIdx.x], p);
+      rows |= uint32_t(src[i] >= 0) << i;
+      const T* const p = static_cast<const T*>(a.x) + int64_t(src[i]) * a.ldx + at;
+      if (src[i] >= 0 && at + 8 <= a.cols && DG_IN(a.dbg, p, 16, DBG_QUANTIZE)) copy16(&ahead[i * 32 * kWarps + threadIdx.x], p);
     }
     return rows;
   };
@@ -275,14 +292,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) quantize_mx4_kernel(const Quan
       }
     }
     if (!AHEAD || __any_sync(kAll, col < a.cols && col + 8 > a.cols)) {
-      int all[8];
-      source_rows(a, rb * 128 + warp * 8, all);
+      int src[kLaneRows];
+      lane_rows(a, rb * 128 + warp * 8, src);
       if (!AHEAD) live = 0;
 #pragma unroll
       for (int i = 0; i < kLaneRows; ++i) {
-        const int src = lane < 16 ? all[i] : all[i + kLaneRows];
-        if (!AHEAD) live |= uint32_t(src >= 0) << i;
-        if (!AHEAD || col + 8 > a.cols) v[i].load(a, src, col, VEC && !AHEAD);
+        if (!AHEAD) live |= uint32_t(src[i] >= 0) << i;
+        if (!AHEAD || col + 8 > a.cols) v[i].load(a, src[i], col, VEC && !AHEAD);
       }
     }
     {
@@ -305,10 +321,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) quantize_mx4_kernel(const Quan
       for (int i = 0; i < kLaneRows; ++i) {
         const uint32_t byte = row_byte<T>(v[i]);
         const uint32_t c = row_codes(byte, v[i]);
-        // the word of four blocks, in lanes 0 and 16
-        uint32_t word = byte | __shfl_down_sync(kAll, byte, 4) << 8;
-        word |= __shfl_down_sync(kAll, word, 8) << 16;
-        if (piece == 0) row_bytes[row0 + i] = word;
+        if ((piece & 3) == 0) reinterpret_cast<uint8_t*>(row_bytes + row0 + i)[piece >> 2] = uint8_t(byte);
         if ((live >> i) & 1u) store_codes(a, a.q + int64_t(rb * 128 + row0 + i) * a.ldq + col / 2, c, (a.cols - col + 1) / 2);
       }
     }
