@@ -9,7 +9,7 @@
 // One orientation: warps take rows, no barrier.  Both: a CTA takes 128 x 128 values, which is one scale tile (128 rows x
 // 4 blocks) in either orientation; half a warp holds 128 columns of a row, a lane eight neighbouring columns of four
 // neighbouring rows.  A row's block is four lanes (two exchanges), a column's block 32 rows of four warps (through shared memory).
-// What bounds it is issuing instructions: 8192 x 4096 bf16 19 us one way (85 MB, 4.4 TB/s), 29 both (103 MB), where a thread spends ~22
+// What bounds it is issuing instructions: 8192 x 4096 bf16 19 us one way (85 MB, 4.4 TB/s), 28 both (103 MB), where a thread spends ~22
 // instructions a value; back to bf16 14.6 us (85 MB, 5.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -410,7 +410,7 @@ cudaError_t launch_mx4(const QuantArgs& a, int sms, cudaStream_t s) {
   }
   const dim3 tiles(unsigned((a.cols + 127) / 128), unsigned((a.rows + 127) / 128));
   // Tiles one after another once there are more than run at the same time (8192 x 4096 bf16, both orientations: 29.3 us, each tile a CTA of its
-  // own 30.9; transposed alone 20.1 and 24.6; fewer tiles 0.3 us longer; fp32, without the copies ahead, 38.2 and 34.5).
+  // own 30.9; transposed alone 20.1 and 24.6; 1024 x 4096 5.2 and 4.9; fp32, without the copies ahead, 37.6 and 34.6).
   if constexpr (VEC && sizeof(T) == 2) {
     if (int64_t(tiles.x) * tiles.y > 2 * sms) return launch_k(quantize_mx4_kernel<T, true, true>, dim3(unsigned(2 * sms)), dim3(32 * kWarps), 0, s, a.pdl, a);
   }
