@@ -34,14 +34,17 @@ __device__ __forceinline__ int choice(const BalanceArgs& a, int t, int lane) {
   return e >= 0 && e < a.experts ? e : -1;
 }
 
-// A lane's experts' shares of a token, from its logits, the largest of which (of the token's) is `top`.  One whose
-// scores are all 0 gives none; of logits of plus infinity each takes an equal share.
+// A lane's experts' shares of a token, from its logits, the largest of which (of the token's) is `top`.  Masked experts
+// (minus infinity) have none, a token of nothing else none at all; of logits of plus infinity (softmax) each takes an equal share.
+// Sigmoids are taken times exp(-c), c = min(top, 0): 1 / (exp(c) + exp(c - x)), whose largest is 1/2 at least, so that a token
+// whose sigmoids are all tiny, or 0 in fp32, has the shares that their ratio gives.
 template <int P>
 __device__ __forceinline__ void token_shares(const BalanceArgs& a, const float (&x)[P], float top, float (&p)[P]) {
   float sum = 0.f;
   if (a.sigmoid) {
+    const float c = top == kNegInf ? 0.f : fminf(top, 0.f), ec = expf(c);
 #pragma unroll
-    for (int i = 0; i < P; ++i) p[i] = __fdividef(1.f, 1.f + expf(-x[i]));  // (0 where exp(-x) is past 2^126)
+    for (int i = 0; i < P; ++i) p[i] = __fdividef(1.f, ec + expf(c - x[i]));  // (0 where exp(c - x) is past 2^126)
   } else if (fabsf(top) < -kNegInf) {  // exp(-inf) is 0: nothing to look out for
 #pragma unroll
     for (int i = 0; i < P; ++i) p[i] = expf(x[i] - top);
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__(32 * balance_warps<P>(), 1) balance_kernel(con
     float top = kNegInf;
 #pragma unroll
     for (int i = 0; i < P; ++i) top = fmaxf(top, x[i]);
-    if (!a.sigmoid) top = key_value(__reduce_max_sync(kAll, number_key(top)));
+    top = key_value(__reduce_max_sync(kAll, number_key(top)));
     token_shares(a, x, top, p);
     ++mine;
 #pragma unroll

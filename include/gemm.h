@@ -655,7 +655,7 @@ gemm_status_t gemm_route_backward(gemm_plan_t plan, int64_t tokens, int64_t expe
  *   factor[e] = scale * experts * counts[e] / (n * m), the derivative of the loss by p[t, e] (the counts have none)
  * (each `experts` long; loss one float).  An even router's loss is `scale`.  A token whose indices are all outside (padding,
  * marked with -1) takes no part, nor does one whose logits are all masked add to the shares; without any tokens all
- * results are 0.  Masked logits as in gemm_route; a token of sigmoids that are all 0 in fp32 adds nothing.
+ * results are 0.  Masked logits as in gemm_route.  Shares are ratios: sigmoids too small for fp32 have the shares of their ratio.
  * Results may share no byte with each other, the logits or indices.  experts <= 1024, top_k <= 32. */
 gemm_status_t gemm_balance(gemm_plan_t plan, int64_t tokens, int64_t experts, const void* logits, int64_t ldl,
                            gemm_type_t l_type, gemm_score_t score, int32_t top_k, const int32_t* indices, float scale,
