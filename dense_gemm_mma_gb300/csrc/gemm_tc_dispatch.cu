@@ -24,31 +24,29 @@ extern template int max_clusters<256, TC_KPAIR>();
 
 namespace {
 template <int MODE>
-int cfg_value(int bn, bool stages) {
-  if (bn == 128) return stages ? TcCfg<128, MODE>::STAGES : TcCfg<128, MODE>::SMEM_BYTES;
-  if (bn == 256) return stages ? TcCfg<256, MODE>::STAGES : TcCfg<256, MODE>::SMEM_BYTES;
-  if (bn == 64 && MODE == TC_SOLO) return stages ? TcCfg<64>::STAGES : TcCfg<64>::SMEM_BYTES;
+int stages_of(int bn) {
+  if (bn == 128) return TcCfg<128, MODE>::STAGES;
+  if (bn == 256) return TcCfg<256, MODE>::STAGES;
+  if (bn == 64 && MODE == TC_SOLO) return TcCfg<64>::STAGES;
   return -1;
-}
-
-int cfg_of(int bn, int mode, bool stages) {
-  switch (mode) {
-    case TC_SOLO: return cfg_value<TC_SOLO>(bn, stages);
-    case TC_PAIR: return cfg_value<TC_PAIR>(bn, stages);
-    case TC_KPAIR: return cfg_value<TC_KPAIR>(bn, stages);
-    default: return -1;
-  }
 }
 }  // namespace
 
-int tc_smem_bytes(int bn, int mode) { return cfg_of(bn, mode, false); }
+int tc_stages(int bn, int mode) {
+  switch (mode) {
+    case TC_SOLO: return stages_of<TC_SOLO>(bn);
+    case TC_PAIR: return stages_of<TC_PAIR>(bn);
+    case TC_KPAIR: return stages_of<TC_KPAIR>(bn);
+    default: return -1;
+  }
+}
+
 int tc_ring_bytes(int bn, int mode) {
-  const int st = cfg_of(bn, mode, true);
+  const int st = tc_stages(bn, mode);
   if (st <= 0) return -1;
   const int b_cols = mode == TC_PAIR ? bn / 2 : bn;
   return st * (TC_BM + b_cols) * TC_BK * 2;
 }
-int tc_stages(int bn, int mode) { return cfg_of(bn, mode, true); }
 
 int tc_max_clusters(int bn, int mode) {
   if (mode == TC_PAIR) return bn == 256 ? max_clusters<256, TC_PAIR>() : (bn == 128 ? max_clusters<128, TC_PAIR>() : 0);

@@ -147,9 +147,8 @@ struct TcParams {
   DG_DEBUG_FIELD     // (debug build) the byte ranges this launch may touch
 };
 
-// Shared-memory footprint and ring depth of the tensor-core kernel for a tile
-// width and TcMode (TC_PAIR and TC_KPAIR exist for bn 128 and 256); -1 if none.
-int tc_smem_bytes(int bn, int mode);
+// Ring depth of the tensor-core kernel for a tile width and TcMode (TC_PAIR and
+// TC_KPAIR exist for bn 128 and 256); -1 if none.
 int tc_stages(int bn, int mode);
 // Bytes of the operand ring (A and B stages) of one CTA.
 int tc_ring_bytes(int bn, int mode);
