@@ -131,19 +131,39 @@ void set_sliced(ScPick* c, int slices) {
 // took two waves: a cluster lies within one group of SMs).
 struct Residency {
   int clusters[9];
-  explicit Residency(int sms) {
+  Residency(bool four, int sms) {
     clusters[0] = 0;
     clusters[1] = sms;
-    for (int s = 2; s <= 8; ++s) clusters[s] = scaled_sliced_clusters(s);
+    for (int s = 2; s <= 8; ++s) clusters[s] = four ? mx4_sliced_clusters(s) : scaled_sliced_clusters(s);
   }
 };
+
+// Those of the 8-bit or of the 4-bit kernel, which is asked for them at the first product that may take it.
+const Residency& residency(bool four, int sms) {
+  if (four) {
+    static const Residency fits(true, sms);
+    return fits;
+  }
+  static const Residency fits(false, sms);
+  return fits;
+}
+
+// CTA pairs that the device holds at once, of either too.
+int resident_pairs(bool four) {
+  if (four) {
+    static const int pairs = mx4_tile_clusters();
+    return pairs;
+  }
+  static const int pairs = scaled_tile_clusters();
+  return pairs;
+}
 
 // `rows` rows of A at most in a tile, `tiles` tiles.  K is cut into as many slices as leave
 // every cluster resident at once, a CTA an SM (4096 x 4096, one row: 6.2 us in 4 slices,
 // 128 CTAs, against 7.9 in 5).  A slice may be empty: its CTA still takes its share of the rows that
 // the slices add up (33 x 1024 x 512, four k-blocks: 5.3 us in 8 slices, 6.4 in 2).
 ScPick pick_sliced(bool four, int64_t rows, int64_t tiles, int sms) {
-  static const Residency fits(sms);
+  const Residency& fits = residency(four, sms);
   ScPick c;
   c.four = four;
   c.kernel = SC_SLICED;
@@ -318,7 +338,7 @@ gemm_status_t run_product(gemm_plan* plan, Product x, cudaStream_t s) {
   if (x.group == SC_ROWS) p.raster = 4;
   int grid;
   if (pair) {
-    static const int clusters = std::min(scaled_tile_clusters(), mx4_tile_clusters());
+    const int clusters = resident_pairs(x.four);
     if (clusters <= 0) return GEMM_ERR_UNSUPPORTED;
     grid = int(2 * std::min<int64_t>(bound, clusters));
   } else if (sliced) {
