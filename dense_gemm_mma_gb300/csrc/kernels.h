@@ -490,15 +490,18 @@ struct NormBackArgs {
   void* dx;
   int64_t lddx;
   float* dgain;     // or null
-  float* parts;     // norm_backward_workspace bytes: rows' partial sums of dgain, part_cols floats each
-  int part_cols;
+  float* parts;     // with dgain: a CTA's rows' sums of it, part_cols floats each
+  int part_cols;    // (set by the launcher)
   int wide;
   int warps, per;
   int pdl;
   DG_DEBUG_FIELD
 };
-size_t norm_backward_workspace(int x_kind, int h_kind, int64_t rows, int64_t cols, int sms);
-cudaError_t launch_norm_backward(NormBackArgs a, int sms, cudaStream_t s);
+// Floats of a part: cols, rounded up to whole 32-byte pieces.
+constexpr int norm_part_cols(int64_t cols) { return int((cols + 7) / 8 * 8); }
+// CTAs of the gradients' first launch, each of which leaves one part of the gain's: those that are resident at once.
+int norm_backward_grid(int x_kind, int h_kind, int64_t rows, int64_t cols, int sms);
+cudaError_t launch_norm_backward(NormBackArgs a, int grid, cudaStream_t s);
 
 // ----------------------------------------------------------------- routing
 

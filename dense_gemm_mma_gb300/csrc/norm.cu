@@ -579,31 +579,11 @@ cudaError_t launch_norm(NormArgs a, int sms, cudaStream_t s) {
   });
 }
 
-// CTAs of the gradients' first launch, each of which leaves one part of the gain's: those that are resident at once (long
-// rows: as many as an SM's shared memory holds the sums of).
-static int norm_backward_grid(int x_kind, int h_kind, int64_t rows, int64_t cols, int sms) {
-  const Shape sh = back_shape(x_kind, cols, rows);
-  int fit = int(std::max<int64_t>(1, 200 * 1024 / (cols * 4)));
-  if (cols <= kBackCols)
-    by_types(x_kind, h_kind, [&](auto x, auto h) {
-      using TX = decltype(x);
-      using TH = decltype(h);
-      const int threads = 32 * sh.warps * sh.per;
-      fit = sh.ne == 1 ? norm_backward_ctas<TX, TH, 1>(threads) : norm_backward_ctas<TX, TH, 2>(threads);
-      return cudaSuccess;
-    });
-  return int(std::min<int64_t>((rows + sh.per - 1) / sh.per, int64_t(sms) * fit));
-}
-
-size_t norm_backward_workspace(int x_kind, int h_kind, int64_t rows, int64_t cols, int sms) {
-  return size_t(norm_backward_grid(x_kind, h_kind, rows, cols, sms)) * size_t((cols + 7) / 8 * 8) * 4;
-}
-
 namespace {
 
 // The shared memory of the sums has to be asked for, once on each device.
 template <typename TX, typename TH>
-cudaError_t launch_long(const NormBackArgs& a, int grid, cudaStream_t s) {
+cudaError_t allow_long() {
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
@@ -614,17 +594,54 @@ cudaError_t launch_long(const NormBackArgs& a, int grid, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     ready.fetch_or(bit, std::memory_order_release);
   }
+  return cudaSuccess;
+}
+
+// CTAs of the long rows' kernel that an SM holds at once: registers allow two or three, the rows' sums one to six.  As many as the
+// sums allow, waves of which the last was half empty and up to three times the parts: 4096 x 10240 bf16 97.6 us, so 79.7; x 16384 fp32 248
+// and 199.  (Asked at every call: it goes by the columns.)
+template <typename TX, typename TH>
+int norm_long_ctas(size_t smem) {
+  int n = 0;
+  if (allow_long<TX, TH>() != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_backward_long_kernel<TX, TH>, 512, smem) != cudaSuccess)
+    cudaGetLastError();
+  return std::max(1, n);
+}
+
+}  // namespace
+
+int norm_backward_grid(int x_kind, int h_kind, int64_t rows, int64_t cols, int sms) {
+  const Shape sh = back_shape(x_kind, cols, rows);
+  int fit = 1;
+  by_types(x_kind, h_kind, [&](auto x, auto h) {
+    using TX = decltype(x);
+    using TH = decltype(h);
+    const int threads = 32 * sh.warps * sh.per;
+    fit = cols > kBackCols ? norm_long_ctas<TX, TH>(size_t(norm_part_cols(cols)) * 4)
+          : sh.ne == 1     ? norm_backward_ctas<TX, TH, 1>(threads)
+                           : norm_backward_ctas<TX, TH, 2>(threads);
+    return cudaSuccess;
+  });
+  return int(std::min<int64_t>((rows + sh.per - 1) / sh.per, int64_t(sms) * fit));
+}
+
+namespace {
+
+template <typename TX, typename TH>
+cudaError_t launch_long(const NormBackArgs& a, int grid, cudaStream_t s) {
+  const cudaError_t err = allow_long<TX, TH>();
+  if (err != cudaSuccess) return err;
   return launch_k(norm_backward_long_kernel<TX, TH>, dim3(unsigned(grid)), dim3(512), size_t(a.part_cols) * 4, s, a.pdl, a);
 }
 
 }  // namespace
 
-cudaError_t launch_norm_backward(NormBackArgs a, int sms, cudaStream_t s) {
-  const int grid = norm_backward_grid(a.x_kind, a.h_kind, a.rows, a.cols, sms);
+cudaError_t launch_norm_backward(NormBackArgs a, int grid, cudaStream_t s) {
   const Shape sh = back_shape(a.x_kind, a.cols, a.rows);
   a.warps = sh.warps;
   a.per = sh.per;
-  a.part_cols = (a.cols + 7) / 8 * 8;
+  a.part_cols = norm_part_cols(a.cols);
   if (!a.dgain) a.parts = nullptr;
   if (a.rows > 0) {
     const cudaError_t err = by_types(a.x_kind, a.h_kind, [&](auto x, auto h) {

@@ -130,7 +130,8 @@ gemm_status_t gemm_norm_backward(gemm_plan_t plan, int64_t rows, int64_t cols, c
                        dH ? " dH" : "", dgain ? " dgain" : "");
   DeviceGuard guard(plan->device);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const size_t ws = dgain && rows > 0 ? norm_backward_workspace(type_kind(x_type), type_kind(h_type), rows, cols, plan->sms) : 0;
+  const int grid = norm_backward_grid(type_kind(x_type), type_kind(h_type), rows, cols, plan->sms);
+  const size_t ws = dgain ? size_t(grid) * size_t(norm_part_cols(cols)) * 4 : 0;
   if (ws > 0) {
     const gemm_status_t grown = ensure_ws(plan, ws, s);
     if (grown != GEMM_OK) return grown;
@@ -160,7 +161,7 @@ gemm_status_t gemm_norm_backward(gemm_plan_t plan, int64_t rows, int64_t cols, c
               .bytes(rstd, rows * 4).matrix(dH, dH ? rows : 0, cols, lddh, he).out_matrix(dX, rows, cols, lddx, he)
               .bytes(dgain, dgain ? cols * 4 : 0).bytes(plan->ws, int64_t(ws)).s;
 #endif
-  return call.done(launched(launch_norm_backward(a, plan->sms, s)));
+  return call.done(launched(launch_norm_backward(a, grid, s)));
 }
 
 }  // extern "C"
