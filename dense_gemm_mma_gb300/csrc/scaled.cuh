@@ -222,8 +222,9 @@ __device__ __forceinline__ float sc_silu(float x) { return __fdividef(x, 1.f + e
 
 // The two for results that are rounded to 16 bits, from the hardware's 2^x and 1 / x (2^-22 each): the rounding
 // of the exponent adds 1.25 |x| 2^-24 to SiLU and 1.125 x^2 2^-24 to GELU, so that they are 2^-18 off at most where an fp16 result
-// is not subnormal, beside half a step of 2^-11, and 2^-16 anywhere, beside bf16's 2^-8.  4-bit 8192 x 8192 x 2048 into fp16, expf and the division
-// above in place of these: SiLU 80.6 us, now 65.2; erfcf: GELU 152, now 83.5; without an activation 53.4.
+// is not subnormal, beside half a step of 2^-11, and 2^-16 where a bf16 result is not, beside 2^-8; but below -87.3 SiLU is 0
+// (the reciprocal is no normal number), as sc_silu is, where the exact one is below 2^-119.  4-bit 8192 x 8192 x 2048 into fp16, expf and the
+// division above in place of these: SiLU 80.6 us, now 65.2; erfcf: GELU 152, now 83.5; without an activation 53.4.
 __device__ __forceinline__ float sc_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -556,7 +556,10 @@ gemm_status_t gemm_dequantize(gemm_plan_t plan, int64_t rows, int64_t cols, cons
                               const void* SQ, void* X, int64_t ldx, gemm_type_t x_type, void* stream);
 
 /* D <- act(alpha * A @ B^T + beta * D) with 4-bit A (M x K) and B (N x K): gemm_run_scaled with codes of 4 bits and
- * scales of blocks of 32; lda and ldb are bytes, >= (K + 1) / 2.  Everything else as there. */
+ * scales of blocks of 32; lda and ldb are bytes, >= (K + 1) / 2.  Everything else as there, but that GELU and SiLU of larger calls
+ * with 16-bit results are computed to 2^-18 (GEMM_TYPE_F16) or 2^-16 (GEMM_TYPE_BF16) of the result before it is rounded: one
+ * next to a rounding border may fall to either side with M, N, K and groups.  SiLU is 0 below -87.3, where it is less than 2^-119
+ * in size. */
 gemm_status_t gemm_run_mx(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA,
                            const void* B, int64_t ldb, const void* SB, void* D, int64_t ldd, gemm_type_t d_type,
                            float alpha, float beta, gemm_epilogue_t epilogue, void* stream);
