@@ -590,7 +590,8 @@ gemm_status_t gemm_run_grouped_mx(gemm_plan_t plan, int64_t groups, int64_t rows
  *                and gemm_run_grouped; both or neither
  *   rstd         rows floats, NULL: not wanted
  * One of H, Y, Q and rstd at least.  Sums, rstd and products are fp32; Y and the codes are rounded once, from the unrounded h (H is
- * rounded on its own).  A row whose mean square is infinite has rstd 0.
+ * rounded on its own).  A row whose sum of squares is past fp32's largest number (4096 values of 3e17) has rstd 0; squares below 2^-149
+ * add nothing, which shows where eps is 0 or next to it: a row of values below 2^-75 has the rstd of zeros.
  * H may be X or the residual themselves (the same address, stride and type), Y too, not both the same; results
  * share no byte with inputs or each other otherwise.  cols <= 32768.  Everything needs only its element's
  * alignment (rows and gain on 16-byte boundaries are faster), Q and SQ 16 bytes with ldq a multiple of 16.
