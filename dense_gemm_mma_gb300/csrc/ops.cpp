@@ -566,8 +566,8 @@ int64_t gemm_mx_scale_bytes(int64_t rows, int64_t cols) {
 }
 
 gemm_status_t gemm_check_mx(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA, const void* B,
-                             int64_t ldb, const void* SB, const void* D, int64_t ldd, gemm_type_t d_type, float alpha,
-                             float beta, gemm_epilogue_t epilogue) {
+                            int64_t ldb, const void* SB, const void* D, int64_t ldd, gemm_type_t d_type, float alpha,
+                            float beta, gemm_epilogue_t epilogue) {
   Product x;
   x.four = true;
   x.M = M, x.N = N, x.K = K;
@@ -579,8 +579,8 @@ gemm_status_t gemm_check_mx(int64_t M, int64_t N, int64_t K, const void* A, int6
 }
 
 gemm_status_t gemm_run_mx(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA,
-                           const void* B, int64_t ldb, const void* SB, void* D, int64_t ldd, gemm_type_t d_type,
-                           float alpha, float beta, gemm_epilogue_t epilogue, void* stream) {
+                          const void* B, int64_t ldb, const void* SB, void* D, int64_t ldd, gemm_type_t d_type,
+                          float alpha, float beta, gemm_epilogue_t epilogue, void* stream) {
   Product x;
   x.name = "gemm_run_mx";
   x.four = true;
@@ -593,10 +593,10 @@ gemm_status_t gemm_run_mx(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, con
 }
 
 gemm_status_t gemm_run_grouped_mx(gemm_plan_t plan, int64_t groups, int64_t rows, int64_t N, int64_t K,
-                                   const int32_t* starts, const int32_t* counts, const void* A, int64_t lda,
-                                   const void* SA, const void* B, int64_t ldb, int64_t b_group, const void* SB, void* D,
-                                   int64_t ldd, gemm_type_t d_type, float alpha, float beta, gemm_epilogue_t epilogue,
-                                   void* stream) {
+                                  const int32_t* starts, const int32_t* counts, const void* A, int64_t lda,
+                                  const void* SA, const void* B, int64_t ldb, int64_t b_group, const void* SB, void* D,
+                                  int64_t ldd, gemm_type_t d_type, float alpha, float beta, gemm_epilogue_t epilogue,
+                                  void* stream) {
   Product x;
   x.name = "gemm_run_grouped_mx";
   x.four = true;
@@ -670,8 +670,8 @@ gemm_status_t gemm_quantize(gemm_plan_t plan, int64_t rows, int64_t cols, const 
 }
 
 gemm_status_t gemm_quantize_mx(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx,
-                                gemm_type_t x_type, const int32_t* rowmap, int64_t map_div, int64_t src_rows, void* Q,
-                                int64_t ldq, void* SQ, void* QT, int64_t ldqt, void* SQT, void* stream) {
+                               gemm_type_t x_type, const int32_t* rowmap, int64_t map_div, int64_t src_rows, void* Q,
+                               int64_t ldq, void* SQ, void* QT, int64_t ldqt, void* SQT, void* stream) {
   if (!plan || rows < 0 || cols < 0 || src_rows < 0 || !is_float_type(x_type)) return GEMM_ERR_INVALID_ARG;
   if (rowmap && map_div < 1) return GEMM_ERR_INVALID_ARG;
   // (indices behind the last tile have to fit 32 bits too)

@@ -124,10 +124,10 @@ _SIGNATURES = {
     "gemm_quantize_mx": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
     "gemm_dequantize": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _VP, _I64, _I32, _VP]),
     "gemm_run_mx": (_I32, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP, _I64, _I32, _F, _F,
-                            gemm_epilogue_t, _VP]),
+                           gemm_epilogue_t, _VP]),
     "gemm_check_mx": (_I32, [_I64, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP, _I64, _I32, _F, _F, gemm_epilogue_t]),
     "gemm_run_grouped_mx": (_I32, [_VP, _I64, _I64, _I64, _I64, _VP, _VP, _VP, _I64, _VP, _VP, _I64, _I64, _VP, _VP, _I64,
-                                    _I32, _F, _F, gemm_epilogue_t, _VP]),
+                                   _I32, _F, _F, gemm_epilogue_t, _VP]),
     "gemm_norm": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _I64, _I32, _VP, _I32, _F, _VP, _I64, _VP, _I64, _I32, _VP,
                          _I64, _VP, _VP, _VP]),
     "gemm_norm_backward": (_I32, [_VP, _I64, _I64, _VP, _I64, _I32, _VP, _I64, _I32, _VP, _I32, _VP, _VP, _I64, _VP, _I64,
@@ -318,9 +318,9 @@ def gemm_mx_scale_bytes(rows, cols) -> int:
 
 
 def gemm_quantize_mx(plan, rows, cols, X, ldx, x_type, rowmap, map_div, src_rows, Q, ldq, SQ, QT, ldqt, SQT,
-                      stream=None) -> int:
+                     stream=None) -> int:
     return load().gemm_quantize_mx(plan, rows, cols, X, ldx, x_type, rowmap, map_div, src_rows, Q, ldq, SQ, QT, ldqt, SQT,
-                                    stream)
+                                   stream)
 
 
 def gemm_dequantize(plan, rows, cols, Q, ldq, q_type, SQ, X, ldx, x_type, stream=None) -> int:
@@ -328,9 +328,9 @@ def gemm_dequantize(plan, rows, cols, Q, ldq, q_type, SQ, X, ldx, x_type, stream
 
 
 def gemm_run_mx(plan, M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta, act=GEMM_ACT_NONE, slope=0.0,
-                 stream=None) -> int:
+                stream=None) -> int:
     return load().gemm_run_mx(plan, M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta,
-                               gemm_epilogue_t(act, slope), stream)
+                              gemm_epilogue_t(act, slope), stream)
 
 
 def gemm_check_mx(M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta, act=GEMM_ACT_NONE, slope=0.0) -> int:
@@ -338,9 +338,9 @@ def gemm_check_mx(M, N, K, A, lda, SA, B, ldb, SB, D, ldd, d_type, alpha, beta, 
 
 
 def gemm_run_grouped_mx(plan, groups, rows, N, K, starts, counts, A, lda, SA, B, ldb, b_group, SB, D, ldd, d_type, alpha,
-                         beta, act=GEMM_ACT_NONE, slope=0.0, stream=None) -> int:
+                        beta, act=GEMM_ACT_NONE, slope=0.0, stream=None) -> int:
     return load().gemm_run_grouped_mx(plan, groups, rows, N, K, starts, counts, A, lda, SA, B, ldb, b_group, SB, D, ldd,
-                                       d_type, alpha, beta, gemm_epilogue_t(act, slope), stream)
+                                      d_type, alpha, beta, gemm_epilogue_t(act, slope), stream)
 
 
 def gemm_norm(plan, rows, cols, X, ldx, x_type, residual, ldr, h_type, gain, g_type, eps, H, ldh, Y, ldy, q_type, Q, ldq,
@@ -708,8 +708,8 @@ class Plan:
         if Q is None and QT is None:
             raise ValueError("neither Q nor QT")
         return load().gemm_quantize_mx(self.handle, rows, cols, x, ldx, _type_of(X),
-                                        None if rowmap is None else _array(rowmap, rows, "int32"), map_div, src_rows, q,
-                                        ldq, sq, qt, ldqt, sqt, self._stream(stream))
+                                       None if rowmap is None else _array(rowmap, rows, "int32"), map_div, src_rows, q,
+                                       ldq, sq, qt, ldqt, sqt, self._stream(stream))
 
     def run_mx4(self, A, SA, B, SB, D, *, K=None, alpha=1.0, beta=0.0, act=GEMM_ACT_NONE, slope=0.0, stream=None) -> int:
         """D <- act(alpha * A @ B^T + beta * D) on 4-bit A (M x K), B (N x K), bytes of two, with packed scales SA, SB.
@@ -721,7 +721,7 @@ class Plan:
             raise ValueError("A and B have the same K")
         d, ldd = _same_shape(D, M, N, "D")
         return load().gemm_run_mx(self.handle, M, N, K, a, lda, _mx4_scales(SA, M, K), b, ldb, _mx4_scales(SB, N, K), d, ldd,
-                                   _type_of(D), alpha, beta, _epilogue(act, slope), self._stream(stream))
+                                  _type_of(D), alpha, beta, _epilogue(act, slope), self._stream(stream))
 
     def run_grouped_mx4(self, A, SA, B, SB, D, starts, counts, *, K=None, alpha=1.0, beta=0.0, act=GEMM_ACT_NONE, slope=0.0,
                         stream=None) -> int:
@@ -733,9 +733,9 @@ class Plan:
             raise ValueError("A and B have the same K")
         d, ldd = _same_shape(D, rows, N, "D")
         return load().gemm_run_grouped_mx(self.handle, groups, rows, N, K, _array(starts, groups, "int32"),
-                                           _array(counts, groups, "int32"), a, lda, _mx4_scales(SA, rows, K), b, ldb, b_group,
-                                           _mx4_scales(SB, N, K, groups), d, ldd, _type_of(D), alpha, beta,
-                                           _epilogue(act, slope), self._stream(stream))
+                                          _array(counts, groups, "int32"), a, lda, _mx4_scales(SA, rows, K), b, ldb, b_group,
+                                          _mx4_scales(SB, N, K, groups), d, ldd, _type_of(D), alpha, beta,
+                                          _epilogue(act, slope), self._stream(stream))
 
     # -------------------------------------------------------------- norm
 

@@ -542,8 +542,8 @@ int64_t gemm_mx_scale_bytes(int64_t rows, int64_t cols);
  * Q and QT at any address, rows any number of bytes apart (16-byte boundaries are fastest, and spare the products a
  * copy); otherwise alignment, rowmap, map_div, src_rows, aliasing and limits as in gemm_quantize, but 2^31 - 1025 columns at most. */
 gemm_status_t gemm_quantize_mx(gemm_plan_t plan, int64_t rows, int64_t cols, const void* X, int64_t ldx,
-                                gemm_type_t x_type, const int32_t* rowmap, int64_t map_div, int64_t src_rows, void* Q,
-                                int64_t ldq, void* SQ, void* QT, int64_t ldqt, void* SQT, void* stream);
+                               gemm_type_t x_type, const int32_t* rowmap, int64_t map_div, int64_t src_rows, void* Q,
+                               int64_t ldq, void* SQ, void* QT, int64_t ldqt, void* SQT, void* stream);
 
 /* X <- the values that a block-scaled matrix stands for: codes Q of q_type (GEMM_TYPE_E4M3 or E5M2 with scales of
  * gemm_quantize's tiles, GEMM_TYPE_E2M1 with those of 4 bits) times their scales, to GEMM_TYPE_BF16, F16 or F32.  Products with the
@@ -561,22 +561,22 @@ gemm_status_t gemm_dequantize(gemm_plan_t plan, int64_t rows, int64_t cols, cons
  * next to a rounding border may fall to either side with M, N, K and groups.  SiLU is 0 below -87.3, where it is less than 2^-119
  * in size. */
 gemm_status_t gemm_run_mx(gemm_plan_t plan, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA,
-                           const void* B, int64_t ldb, const void* SB, void* D, int64_t ldd, gemm_type_t d_type,
-                           float alpha, float beta, gemm_epilogue_t epilogue, void* stream);
+                          const void* B, int64_t ldb, const void* SB, void* D, int64_t ldd, gemm_type_t d_type,
+                          float alpha, float beta, gemm_epilogue_t epilogue, void* stream);
 
 /* The argument checks of gemm_run_mx without a plan or a device. */
 gemm_status_t gemm_check_mx(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA, const void* B,
-                             int64_t ldb, const void* SB, const void* D, int64_t ldd, gemm_type_t d_type, float alpha,
-                             float beta, gemm_epilogue_t epilogue);
+                            int64_t ldb, const void* SB, const void* D, int64_t ldd, gemm_type_t d_type, float alpha,
+                            float beta, gemm_epilogue_t epilogue);
 
 /* Experts' products with 4-bit rows and weights: gemm_run_grouped with codes of 4 bits and scales of blocks of 32
  * (lda, ldb and b_group are bytes; a group's scales gemm_mx_scale_bytes(N, K) after the last one's).
  * gemm_quantize_mx with gemm_route_map's rowmap orders the tokens by expert. */
 gemm_status_t gemm_run_grouped_mx(gemm_plan_t plan, int64_t groups, int64_t rows, int64_t N, int64_t K,
-                                   const int32_t* starts, const int32_t* counts, const void* A, int64_t lda,
-                                   const void* SA, const void* B, int64_t ldb, int64_t b_group, const void* SB, void* D,
-                                   int64_t ldd, gemm_type_t d_type, float alpha, float beta, gemm_epilogue_t epilogue,
-                                   void* stream);
+                                  const int32_t* starts, const int32_t* counts, const void* A, int64_t lda,
+                                  const void* SA, const void* B, int64_t ldb, int64_t b_group, const void* SB, void* D,
+                                  int64_t ldd, gemm_type_t d_type, float alpha, float beta, gemm_epilogue_t epilogue,
+                                  void* stream);
 
 /* ---- norm ----
  * Root-mean-square norm of a residual stream, row by row (rows x cols):
