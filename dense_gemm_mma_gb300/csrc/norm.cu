@@ -15,7 +15,7 @@
 // caller still has.  The gain's gradient is summed row after row in registers, then over the CTAs in the order
 // of their indices by a second launch: the same bits every time, no atomics.
 // Measured, bf16: 1 x 4096 2.1 us; 8192 x 4096 with the residual 44 us (6.1 TB/s), into codes 43 (5.5); 6912 x 2050 21.5 us, its
-// gradients 27.8 with the gain's, 24.7 without; 4096 x 16384 gradients 123 us (4.4).
+// gradients 27.1 with the gain's, 24.7 without; 4096 x 10240 gradients 79.7 us (4.2), x 16384 124 (4.3), fp32 199 (5.4).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
